@@ -379,6 +379,103 @@ int dmuon_adamw_status(void);
 int dmuon_step_noalloc(void* param, const void* grad, void* momentum, int64_t rows, int64_t cols,
                        int32_t dtype, float lr, float beta, float wd, int32_t ns_steps, void* stream);
 
+/* ---- layer norm ----------------------------------------------------------
+ *
+ * No counterpart in the paper: the operators from here on produce the
+ * gradients that the optimizer steps above consume.  They share these
+ * conventions: row-major contiguous tensors on 16-byte boundaries (else
+ * DMUON_ERR_ALIGN); one dtype (DMUON_BF16 | DMUON_FP32) for activations,
+ * weights and their gradients, with row statistics and losses in fp32; all
+ * arithmetic, sums and softmax statistics in fp32 or better; asynchronous on
+ * `stream`; no allocation and no host synchronisation (so a call can be
+ * captured in a CUDA graph); results do not depend on the order in which thread
+ * blocks finish.  The caller owns every buffer; a workspace (256-byte aligned)
+ * holds nothing from one call to the next and must not be used by two calls
+ * that may overlap on the GPU.
+ *
+ * x: rows x cols.  mu = mean(x), r = 1/sqrt(mean((x - mu)^2) + eps),
+ *   y = (x - mu) r weight + bias.
+ * weight, bias: cols elements or NULL (1 and 0).  mean, rstd: rows floats each,
+ * or NULL (not stored); the backward pass needs both.  rows in [0, 2^30], cols
+ * in [1, 2^20], eps >= 0.  Returns DMUON_OK, DMUON_ERR_INVALID_ARG,
+ * DMUON_ERR_UNSUPPORTED_DTYPE, DMUON_ERR_ALIGN or DMUON_ERR_CUDA. */
+int dmuon_layer_norm_forward(const void* x, const void* weight, const void* bias, void* y, float* mean, float* rstd,
+                             int64_t rows, int64_t cols, int32_t dtype, float eps, void* stream);
+/* Workspace of the backward pass (0 for sizes it refuses). */
+size_t dmuon_layer_norm_workspace_bytes(int64_t rows, int64_t cols, int32_t dtype);
+/* With n = (x - mu) r and g = dy weight:
+ *   dx = r (g - mean(g) - n mean(g n)),  dweight = sum_rows dy n,  dbias = sum_rows dy.
+ * dweight and dbias may each be NULL (not computed; both NULL: no workspace
+ * needed); with no rows they are zero.  Also returns DMUON_ERR_NO_WORKSPACE and
+ * DMUON_ERR_WORKSPACE_TOO_SMALL. */
+int dmuon_layer_norm_backward(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+                              void* dx, void* dweight, void* dbias, int64_t rows, int64_t cols, int32_t dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- gated feed-forward block ---------------------------------------------
+ *
+ * x, y: tokens x dim.  w_gate, w_up: hidden x dim.  w_down: dim x hidden (the
+ * matrices the Muon step updates).
+ *   a = x w_gate^T,  u = x w_up^T,  h = act(a) u,  y = h w_down^T
+ * with act = a sigmoid(a) (SILU) or a Phi(a), Phi the normal distribution
+ * function (GELU).  Both projections, the activation and the product are one
+ * kernel on the tensor cores.  gate, up: tokens x hidden, receive a and u for
+ * the backward pass, or both NULL.  bf16: h (and a, u, and in the backward
+ * pass da, du) are rounded to bf16, the operand type of the next product.
+ * fp32: every product runs as six products of bf16 parts (x = hi + mid + lo),
+ * which keeps fp32 accuracy.  tokens in [0, 2^24], dim and hidden in
+ * [1, 2^20].  Widths that are a multiple of 8 are read in place; bf16 matrices
+ * of other widths, and fp32 ones, are first copied into the workspace. */
+#define DMUON_ACT_SILU 0
+#define DMUON_ACT_GELU 1
+/* Workspace of the forward or the backward pass (0 for sizes it refuses, and for no tokens). */
+size_t dmuon_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype, int32_t backward);
+int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const void* w_up, const void* w_down, void* y,
+                            void* gate, void* up, int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype,
+                            int32_t activation, void* workspace, size_t workspace_bytes, void* stream);
+/* With dh = dy w_down, da = dh u act'(a), du = dh act(a):
+ *   dx = da w_gate + du w_up,  dw_gate = da^T x,  dw_up = du^T x,  dw_down = dy^T h
+ * from the stored gate and up.  With no tokens the weights' gradients are zero.
+ * Returns DMUON_OK, DMUON_ERR_INVALID_ARG, DMUON_ERR_UNSUPPORTED_DTYPE,
+ * DMUON_ERR_ALIGN, DMUON_ERR_NO_WORKSPACE, DMUON_ERR_WORKSPACE_TOO_SMALL,
+ * DMUON_ERR_UNSUPPORTED_DEVICE (not sm_103) or DMUON_ERR_CUDA, like the
+ * forward pass. */
+int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                             const void* gate, const void* up, void* dx, void* dw_gate, void* dw_up, void* dw_down,
+                             int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype, int32_t activation,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- vocabulary loss --------------------------------------------------------
+ *
+ * Softmax cross entropy straight from the hidden states, without keeping the
+ * logits.  x: tokens x dim, weight: vocab x dim, targets: tokens int64.
+ *   z = x weight^T,  lse = log sum_v exp(z_v),  loss = lse - z_target
+ * per token (loss and lse: tokens floats).  A token whose target is
+ * ignore_index has loss 0 and no gradient; any other target outside
+ * [0, vocab) gives a NaN loss and no gradient.
+ * With dx and dweight (both or neither) also the gradients of
+ * sum_i coef[i] loss[i] (coef NULL: 1):
+ *   dz = coef (softmax(z) - onehot(target)),  dx = dz weight,  dweight = dz^T x.
+ * The vocabulary is visited in pieces of 128 columns whose maximum and sum of
+ * exponentials are kept; for the gradient the exponentials of a piece of the
+ * tokens are held in the workspace (bf16, or fp32 for fp32 tensors) and turned
+ * into dz there, so the logits are computed once.  Tokens are taken in pieces
+ * whose logits fit `budget` bytes (0: 2 GiB; at least 256 tokens), and dweight
+ * is summed over the pieces in fp32.  tokens in [0, 2^24], dim in [1, 2^20],
+ * vocab in [1, 2^22].  Status codes as for the gated block. */
+size_t dmuon_vocab_loss_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab, int32_t dtype, int32_t grad,
+                                        uint64_t budget);
+int dmuon_vocab_loss(const void* x, const void* weight, const int64_t* targets, const float* coef,
+                     int64_t ignore_index, float* loss, float* lse, void* dx, void* dweight, int64_t tokens,
+                     int64_t dim, int64_t vocab, int32_t dtype, uint64_t budget, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Synchronous: DMUON_ERR_DEVICE_TIMEOUT if a wait inside a gated block's or
+ * vocabulary loss's kernel on the current device gave up (about 2 s; its
+ * outputs are then not complete) since the last call, else DMUON_OK; clears
+ * the flag. */
+int dmuon_ops_status(void);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,7 +19,10 @@ from ._lib import (  # noqa: F401
     ENGINE_TC_BF16, ENGINE_SIMT_FP32, ENGINE_TC_SPLIT, TILE_AUTO, TILE_PACKED, TILE_SINGLE, SCALE_ASPECT, SCALE_RMS, TIMER_NAMES, ASSIGN_GREEDY, ASSIGN_EXACT, DmuonError,
 )
 
-__all__ = ["Muon", "dmuon_plan", "dmuon_step", "assign_owners", "adamw_step", "load"]
+_OPS = ("layer_norm", "layer_norm_backward", "layer_norm_workspace", "gated_ffn", "gated_ffn_backward",
+        "gated_ffn_workspace", "vocab_loss", "vocab_loss_grad", "vocab_loss_workspace", "ops_status")
+
+__all__ = ["Muon", "dmuon_plan", "dmuon_step", "assign_owners", "adamw_step", "load", *_OPS]
 
 _DTYPES = {"bf16": BF16, "fp32": FP32}
 _PREC = {"bf16": PREC_BF16, "fp32": PREC_FP32}
@@ -30,6 +33,16 @@ _TILES = {"auto": TILE_AUTO, "packed": TILE_PACKED, "single": TILE_SINGLE}
 
 def load():
     return _lib.load()
+
+
+def __getattr__(name):
+    # the operators allocate their outputs, so their module imports torch; it is
+    # loaded with the first use of one
+    if name in _OPS:
+        from . import ops
+        globals()[name] = getattr(ops, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _stream_handle(stream):

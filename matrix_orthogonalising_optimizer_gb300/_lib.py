@@ -23,6 +23,7 @@ MAX_NS_STEPS = 16
 TIMER_NAMES = ("momentum", "norm", "syrk", "ns", "final", "tc", "simt")
 BUF_X, BUF_RF, BUF_R_OPERAND = 0, 1, 2
 ASSIGN_GREEDY, ASSIGN_EXACT = 0, 1
+ACT_SILU, ACT_GELU = 0, 1
 
 
 class Shape(ctypes.Structure):
@@ -76,6 +77,19 @@ SIGNATURES = {
     "dmuon_adamw_status": (c_int, []),
     "dmuon_step_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32, c_float, c_float,
                                    c_float, c_int32, c_void_p]),
+    "dmuon_layer_norm_forward": (c_int, [c_void_p] * 6 + [c_int64, c_int64, c_int32, c_float, c_void_p]),
+    "dmuon_layer_norm_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int32]),
+    "dmuon_layer_norm_backward": (c_int, [c_void_p] * 8 + [c_int64, c_int64, c_int32, c_void_p, c_size_t, c_void_p]),
+    "dmuon_gated_ffn_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int32]),
+    "dmuon_gated_ffn_forward": (c_int, [c_void_p] * 7 + [c_int64, c_int64, c_int64, c_int32, c_int32, c_void_p,
+                                                         c_size_t, c_void_p]),
+    "dmuon_gated_ffn_backward": (c_int, [c_void_p] * 11 + [c_int64, c_int64, c_int64, c_int32, c_int32, c_void_p,
+                                                           c_size_t, c_void_p]),
+    "dmuon_vocab_loss_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int32, c_uint64]),
+    "dmuon_vocab_loss": (c_int, [c_void_p] * 4 + [c_int64] + [c_void_p] * 4 + [c_int64, c_int64, c_int64, c_int32,
+                                                                               c_uint64, c_void_p, c_size_t,
+                                                                               c_void_p]),
+    "dmuon_ops_status": (c_int, []),
 }
 
 _lib = None

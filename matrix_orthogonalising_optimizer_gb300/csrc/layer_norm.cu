@@ -1,0 +1,670 @@
+// Layer norm, forward and backward, with the reduction of the weight's and the
+// bias's gradient over the rows.
+//
+//   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps), n = (x - mu) r
+//   y  = n w + b
+//   g  = dy w;  dx = r (g - mean(g) - n mean(g n));  dw = sum dy n, db = sum dy
+//
+// HBM-bound: forward 4 bytes per bf16 element (read x, write y), backward 6
+// (read x and dy, write dx), twice that in fp32.  Each row is read once and
+// held in registers by the threads of its group (WPR warps, VPT 16-byte vectors
+// per thread), so the variance is the mean of squared deviations from the
+// finished mean -- no difference of large sums -- and the next row's loads are
+// issued before the current row's reductions.  All arithmetic is fp32, one
+// rounding per stored value.  In the backward pass a thread meets the same
+// columns in every row and keeps their dw and db sums in registers; a block's
+// groups add theirs up in shared memory, each block writes one partial row, and
+// a second kernel adds the partial rows in a fixed order, so the result does
+// not depend on scheduling.  Rows wider than a group holds take three plain
+// passes (wide kernels).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "dmuon.h"
+#include "internal.h"
+
+namespace dmuon {
+void set_last_error(const std::string& msg);
+}
+
+namespace {
+
+using dmuon::ELEM_BF16;
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int kBwdThreads = 512;
+constexpr int kMaxPartials = 1024;  // partial rows of the backward pass
+
+struct NormArgs {
+    const void* x;
+    const void* dy;
+    const void* w;
+    const void* b;
+    void* out;          // y or dx
+    float* mean;
+    float* rstd;
+    float* partial;     // backward: [blocks][2][cols]
+    int64_t rows;
+    int32_t cols;
+    int32_t aligned;    // rows start on 16-byte boundaries
+    float eps;
+};
+
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) {
+    return static_cast<float>(v);
+}
+
+template <typename T>
+__device__ __forceinline__ T from_f(float v) {
+    if constexpr (sizeof(T) == 2) return __float2bfloat16_rn(v);
+    else return v;
+}
+
+// 16 bytes from column c of a row; columns >= cols read as zero.
+template <typename T>
+__device__ __forceinline__ uint4 ld_raw(const T* row, int c, int cols, bool aligned) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (c >= cols) return q;
+    if (aligned) return *reinterpret_cast<const uint4*>(row + c);
+    T t[kVec<T>];
+#pragma unroll
+    for (int j = 0; j < kVec<T>; ++j) t[j] = c + j < cols ? row[c + j] : from_f<T>(0.0f);
+    if constexpr (sizeof(T) == 4) {
+        q = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
+    } else {
+        const unsigned short* h = reinterpret_cast<const unsigned short*>(t);
+        q = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+    return q;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[kVec<T>]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(w[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = __uint_as_float(w[k] << 16);
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void st_vec(T* row, int c, int cols, bool aligned, const float (&v)[kVec<T>]) {
+    if (c >= cols) return;
+    if (aligned) {
+        uint4 q;
+        if constexpr (sizeof(T) == 4) {
+            q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        } else {
+            __nv_bfloat162 h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+            q = *reinterpret_cast<const uint4*>(h);
+        }
+        *reinterpret_cast<uint4*>(row + c) = q;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kVec<T>; ++j)
+        if (c + j < cols) row[c + j] = from_f<T>(v[j]);
+}
+
+template <int N>
+__device__ __forceinline__ void warp_sum(float (&s)[N]) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(kFull, s[k], o);
+}
+
+// Sum over the WPR warps of a row group, in a fixed order.  `buf` alternates
+// between two halves of shared memory from call to call, so one barrier per
+// reduction is enough: a half is written again only after the barrier of the
+// reduction in between.
+template <int WPR, int N>
+__device__ __forceinline__ void group_sum(float (&s)[N], float (*red)[N], int bar) {
+    warp_sum(s);
+    if constexpr (WPR > 1) {
+        const int w = (threadIdx.x / 32) % WPR;
+        if (threadIdx.x % 32 == 0)
+#pragma unroll
+            for (int k = 0; k < N; ++k) red[w][k] = s[k];
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(WPR * 32) : "memory");
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i)
+#pragma unroll
+            for (int k = 0; k < N; ++k) s[k] += red[i][k];
+    }
+}
+
+template <typename T, int VPT, int WPR>
+__global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int V = kVec<T>, TPR = WPR * 32, G = WPR == 1 ? 4 : 1;
+    __shared__ float red[2][WPR][1];
+    const int g = threadIdx.x / TPR, tr = threadIdx.x % TPR;
+    const bool al = a.aligned != 0;
+    uint4 w[VPT], b[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = (k * TPR + tr) * V;
+        w[k] = a.w ? ld_raw(static_cast<const T*>(a.w), c, a.cols, al) : make_uint4(0, 0, 0, 0);
+        b[k] = a.b ? ld_raw(static_cast<const T*>(a.b), c, a.cols, al) : make_uint4(0, 0, 0, 0);
+    }
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * G + g;
+    uint4 next[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+        if (row < a.rows)
+            next[k] = ld_raw(static_cast<const T*>(a.x) + row * a.cols, (k * TPR + tr) * V, a.cols, al);
+    for (; row < a.rows; row += stride) {
+        float x[VPT][V];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) unpack<T>(next[k], x[k]);
+        if (row + stride < a.rows) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                next[k] = ld_raw(static_cast<const T*>(a.x) + (row + stride) * a.cols, (k * TPR + tr) * V, a.cols, al);
+        }
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[0] += x[k][j];
+        group_sum<WPR>(s, red[0], 1 + g);
+        const float mean = s[0] * inv;
+        s[0] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + tr) * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                x[k][j] -= mean;
+                if (c + j < a.cols) s[0] = fmaf(x[k][j], x[k][j], s[0]);
+            }
+        }
+        group_sum<WPR>(s, red[1], 1 + g);
+        const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+        if (tr == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            float wv[V], bv[V];
+            unpack<T>(w[k], wv);
+            unpack<T>(b[k], bv);
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[k][j] = fmaf(x[k][j] * rstd, a.w ? wv[j] : 1.0f, bv[j]);
+            st_vec(static_cast<T*>(a.out) + row * a.cols, (k * TPR + tr) * V, a.cols, al, x[k]);
+        }
+    }
+}
+
+template <typename T, int VPT, int WPR>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int V = kVec<T>, TPR = WPR * 32, G = kBwdThreads / TPR;
+    __shared__ float red[G][2][WPR][2];
+    extern __shared__ float sums[];  // [2][TPR * VPT * V], groups > 1 only
+    const int g = threadIdx.x / TPR, tr = threadIdx.x % TPR;
+    const bool al = a.aligned != 0;
+    uint4 w[VPT];
+    float dw[VPT][V], db[VPT][V];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        w[k] = a.w ? ld_raw(static_cast<const T*>(a.w), (k * TPR + tr) * V, a.cols, al) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < V; ++j) dw[k][j] = db[k][j] = 0.0f;
+    }
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * G + g;
+    uint4 nx[VPT], nd[VPT];
+    float nm = 0.0f, nr = 0.0f;
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + tr) * V;
+            nx[k] = ld_raw(static_cast<const T*>(a.x) + r * a.cols, c, a.cols, al);
+            nd[k] = ld_raw(static_cast<const T*>(a.dy) + r * a.cols, c, a.cols, al);
+        }
+        nm = a.mean[r];
+        nr = a.rstd[r];
+    };
+    if (row < a.rows) fetch(row);
+    int flip = 0;
+    for (; row < a.rows; row += stride, flip ^= 1) {
+        uint4 cx[VPT], cd[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            cx[k] = nx[k];
+            cd[k] = nd[k];
+        }
+        const float mean = nm, rstd = nr;
+        if (row + stride < a.rows) fetch(row + stride);
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + tr) * V;
+            float x[V], d[V], wv[V];
+            unpack<T>(cx[k], x);
+            unpack<T>(cd[k], d);
+            unpack<T>(w[k], wv);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float n = (x[j] - mean) * rstd;
+                const float gr = a.w ? d[j] * wv[j] : d[j];
+                // beyond the row d is zero, x - mean is not
+                s[0] += gr;
+                s[1] = c + j < a.cols ? fmaf(gr, n, s[1]) : s[1];
+                dw[k][j] = c + j < a.cols ? fmaf(d[j], n, dw[k][j]) : 0.0f;
+                db[k][j] += d[j];
+            }
+        }
+        group_sum<WPR>(s, red[g][flip], 1 + g);
+        const float m1 = s[0] * inv, m2 = s[1] * inv;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            float x[V], d[V], wv[V];
+            unpack<T>(cx[k], x);
+            unpack<T>(cd[k], d);
+            unpack<T>(w[k], wv);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float n = (x[j] - mean) * rstd;
+                const float gr = a.w ? d[j] * wv[j] : d[j];
+                x[j] = rstd * (gr - m1 - n * m2);
+            }
+            st_vec(static_cast<T*>(a.out) + row * a.cols, (k * TPR + tr) * V, a.cols, al, x);
+        }
+    }
+    if (!a.partial) return;
+    float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    if constexpr (G > 1) {
+        // the groups' sums, one group after the other
+        for (int i = 0; i < G; ++i) {
+            if (g == i) {
+#pragma unroll
+                for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int c = j * (TPR * VPT) + k * TPR + tr;  // conflict-free order
+                        sums[c] = i ? sums[c] + dw[k][j] : dw[k][j];
+                        sums[TPR * VPT * V + c] = i ? sums[TPR * VPT * V + c] + db[k][j] : db[k][j];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.cols; c += kBwdThreads) {
+            const int i = (c % V) * (TPR * VPT) + c / V;
+            p[c] = sums[i];
+            p[a.cols + c] = sums[TPR * VPT * V + i];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = (k * TPR + tr) * V + j;
+                if (c < a.cols) {
+                    p[c] = dw[k][j];
+                    p[a.cols + c] = db[k][j];
+                }
+            }
+    }
+}
+
+// dw and db: column sums of the partial rows [n][2][cols], 32 columns per block,
+// 32 slices of the rows, in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial, int n, int cols, T* dw, T* db) {
+    __shared__ float red[32][33];
+    const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // column of the 2 x cols pair
+    float s = 0.0f;
+    if (i < 2 * static_cast<int64_t>(cols)) {
+        const float* p = partial + i;
+#pragma unroll 4
+        for (int r = slice; r < n; r += 32) s += p[static_cast<int64_t>(r) * 2 * cols];
+    }
+    red[slice][lane] = s;
+    __syncthreads();
+    if (slice == 0 && i < 2 * static_cast<int64_t>(cols)) {
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s += red[k][lane];
+        T* out = i < cols ? dw : db;
+        if (out) out[i < cols ? i : i - cols] = from_f<T>(s);
+    }
+}
+
+// ------------------------------------------------ rows wider than a group
+
+__device__ __forceinline__ float block_sum(float s, float* red) {
+    float v[1] = {s};
+    warp_sum(v);
+    __syncthreads();  // the previous sum has been read
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v[0];
+    __syncthreads();
+    s = 0.0f;
+    for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += red[i];
+    return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float red[32];
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + row * a.cols;
+        T* y = static_cast<T*>(a.out) + row * a.cols;
+        float s = 0.0f;
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) s += to_f(x[c]);
+        const float mean = block_sum(s, red) * inv;
+        s = 0.0f;
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float d = to_f(x[c]) - mean;
+            s = fmaf(d, d, s);
+        }
+        const float rstd = 1.0f / sqrtf(block_sum(s, red) * inv + a.eps);
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float n = (to_f(x[c]) - mean) * rstd;
+            y[c] = from_f<T>(fmaf(n, a.w ? to_f(static_cast<const T*>(a.w)[c]) : 1.0f,
+                                  a.b ? to_f(static_cast<const T*>(a.b)[c]) : 0.0f));
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float red[32];
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + row * a.cols;
+        const T* dy = static_cast<const T*>(a.dy) + row * a.cols;
+        T* dx = static_cast<T*>(a.out) + row * a.cols;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float g = to_f(dy[c]) * (a.w ? to_f(static_cast<const T*>(a.w)[c]) : 1.0f);
+            s1 += g;
+            s2 = fmaf(g, (to_f(x[c]) - mean) * rstd, s2);
+        }
+        const float m1 = block_sum(s1, red) * inv, m2 = block_sum(s2, red) * inv;
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float g = to_f(dy[c]) * (a.w ? to_f(static_cast<const T*>(a.w)[c]) : 1.0f);
+            dx[c] = from_f<T>(rstd * (g - m1 - (to_f(x[c]) - mean) * rstd * m2));
+        }
+    }
+}
+
+// Partial row blockIdx.y of dw and db: its share of the rows, one column per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_cols_wide_kernel(const __grid_constant__ NormArgs a, int64_t per) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.cols) return;
+    const int64_t r0 = blockIdx.y * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
+    float dw = 0.0f, db = 0.0f;
+    for (int64_t r = r0; r < r1; ++r) {
+        const float d = to_f(static_cast<const T*>(a.dy)[r * a.cols + c]);
+        dw = fmaf(d, (to_f(static_cast<const T*>(a.x)[r * a.cols + c]) - a.mean[r]) * a.rstd[r], dw);
+        db += d;
+    }
+    float* p = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.cols;
+    p[c] = dw;
+    p[a.cols + c] = db;
+}
+
+// ------------------------------------------------ host
+
+int fail(int code, const std::string& msg) {
+    dmuon::set_last_error(msg);
+    return code;
+}
+
+// Row group of `vecs` 16-byte vectors: warps per row and vectors per thread.
+// Forward with many rows: a thread holds up to four vectors and a narrow row
+// belongs to one warp (no barrier); with fewer rows than the machine has room
+// for, a row is spread over more warps to shorten its chain of loads and sums.
+// Backward: the column sums take 16 registers per vector, so a thread holds
+// one vector and a second or fourth only in rows wider than 16 warps.
+struct Shape {
+    int vpt = 0, wpr = 0;  // 0: wide kernels
+};
+
+Shape choose(int64_t rows, int64_t vecs, int sms, bool bwd) {
+    const bool spread = bwd || rows < 4 * static_cast<int64_t>(sms);
+    static const int vpts[3] = {1, 2, 4};
+    static const int wprs[5] = {1, 2, 4, 8, 16};
+    if (spread) {
+        for (int v : vpts)
+            for (int w : wprs)
+                if (static_cast<int64_t>(v) * w * 32 >= vecs) return {v, w};
+    } else {
+        for (int w : wprs)
+            for (int v : vpts)
+                if (static_cast<int64_t>(v) * w * 32 >= vecs) return {v, w};
+    }
+    return {};
+}
+
+template <typename T, int VPT, int WPR>
+cudaError_t run_fwd(const NormArgs& a, int grid, cudaStream_t s) {
+    norm_fwd_kernel<T, VPT, WPR><<<grid, WPR == 1 ? 128 : WPR * 32, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int VPT, int WPR>
+cudaError_t run_bwd(const NormArgs& a, int grid, cudaStream_t s) {
+    // the groups' column sums: at most 32 KB
+    constexpr size_t smem = WPR < 16 ? static_cast<size_t>(2) * WPR * 32 * VPT * kVec<T> * 4 : 0;
+    norm_bwd_kernel<T, VPT, WPR><<<grid, kBwdThreads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int VPT>
+cudaError_t run_fwd_vpt(int wpr, const NormArgs& a, int grid, cudaStream_t s) {
+    switch (wpr) {
+        case 1: return run_fwd<T, VPT, 1>(a, grid, s);
+        case 2: return run_fwd<T, VPT, 2>(a, grid, s);
+        case 4: return run_fwd<T, VPT, 4>(a, grid, s);
+        case 8: return run_fwd<T, VPT, 8>(a, grid, s);
+        default: return run_fwd<T, VPT, 16>(a, grid, s);
+    }
+}
+
+template <typename T>
+cudaError_t run_shape(const Shape& sh, const NormArgs& a, bool bwd, int grid, cudaStream_t s) {
+    if (!bwd) {
+        if (sh.vpt == 1) return run_fwd_vpt<T, 1>(sh.wpr, a, grid, s);
+        if (sh.vpt == 2) return run_fwd_vpt<T, 2>(sh.wpr, a, grid, s);
+        return run_fwd_vpt<T, 4>(sh.wpr, a, grid, s);
+    }
+    if (sh.vpt == 2) return run_bwd<T, 2, 16>(a, grid, s);
+    if (sh.vpt == 4) return run_bwd<T, 4, 16>(a, grid, s);
+    switch (sh.wpr) {
+        case 1: return run_bwd<T, 1, 1>(a, grid, s);
+        case 2: return run_bwd<T, 1, 2>(a, grid, s);
+        case 4: return run_bwd<T, 1, 4>(a, grid, s);
+        case 8: return run_bwd<T, 1, 8>(a, grid, s);
+        default: return run_bwd<T, 1, 16>(a, grid, s);
+    }
+}
+
+int check(int64_t rows, int64_t cols, int32_t dtype, const char* where) {
+    if (rows < 0 || rows > kMaxRows || cols < 1 || cols > DMUON_MAX_DIM)
+        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": rows must be in [0, 2^30], cols in [1, 2^20]");
+    if (dtype != DMUON_BF16 && dtype != DMUON_FP32)
+        return fail(DMUON_ERR_UNSUPPORTED_DTYPE, std::string(where) + ": dtype must be DMUON_BF16 or DMUON_FP32");
+    return DMUON_OK;
+}
+
+int check_ptr(const void* p, const char* name, const char* where, bool required, size_t align = 16) {
+    if (!p) return required ? fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": " + name + " is NULL") : DMUON_OK;
+    if (reinterpret_cast<uintptr_t>(p) % align)
+        return fail(DMUON_ERR_ALIGN,
+                    std::string(where) + ": " + name + " is not " + std::to_string(align) + "-byte aligned");
+    return DMUON_OK;
+}
+
+int device_sms(int* sms, const char* where) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    return e == cudaSuccess ? DMUON_OK : fail(DMUON_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
+}
+
+int cuda_result(cudaError_t e, const char* where) {
+    return e == cudaSuccess ? DMUON_OK : fail(DMUON_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
+}
+
+// Partial rows of the backward pass: the blocks of a persistent grid, at most
+// kMaxPartials and no more than rows (a block with no row would write zeros).
+int64_t partial_rows(int64_t rows) { return std::min<int64_t>(rows, kMaxPartials); }
+
+}  // namespace
+
+extern "C" int dmuon_layer_norm_forward(const void* x, const void* weight, const void* bias, void* y, float* mean,
+                                        float* rstd, int64_t rows, int64_t cols, int32_t dtype, float eps,
+                                        void* stream) {
+    const char* where = "dmuon_layer_norm_forward";
+    int r = check(rows, cols, dtype, where);
+    if (r != DMUON_OK) return r;
+    if (!(eps >= 0.0f) || !std::isfinite(eps))
+        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": eps must be finite and >= 0");
+    if (rows == 0) return DMUON_OK;
+    if ((r = check_ptr(x, "x", where, true)) || (r = check_ptr(y, "y", where, true)) ||
+        (r = check_ptr(weight, "weight", where, false)) || (r = check_ptr(bias, "bias", where, false)) ||
+        (r = check_ptr(mean, "mean", where, false, 4)) || (r = check_ptr(rstd, "rstd", where, false, 4)))
+        return r;
+    int sms = 0;
+    if ((r = device_sms(&sms, where))) return r;
+    const bool bf = dtype == DMUON_BF16;
+    const int vec = bf ? 8 : 4;
+    NormArgs a = {};
+    a.x = x;
+    a.w = weight;
+    a.b = bias;
+    a.out = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.cols = static_cast<int32_t>(cols);
+    a.aligned = cols % vec == 0;
+    a.eps = eps;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Shape sh = choose(rows, (cols + vec - 1) / vec, sms, false);
+    if (sh.wpr == 0) {
+        const int grid = static_cast<int>(std::min<int64_t>(rows, 2 * sms));
+        if (bf) norm_fwd_wide_kernel<__nv_bfloat16><<<grid, 1024, 0, s>>>(a);
+        else norm_fwd_wide_kernel<float><<<grid, 1024, 0, s>>>(a);
+        return cuda_result(cudaGetLastError(), where);
+    }
+    const int64_t groups = sh.wpr == 1 ? 4 : 1, threads = sh.wpr == 1 ? 128 : 32 * sh.wpr;
+    const int grid = static_cast<int>(std::min<int64_t>((rows + groups - 1) / groups, sms * (1536 / threads)));
+    return cuda_result(bf ? run_shape<__nv_bfloat16>(sh, a, false, grid, s) : run_shape<float>(sh, a, false, grid, s),
+                       where);
+}
+
+extern "C" size_t dmuon_layer_norm_workspace_bytes(int64_t rows, int64_t cols, int32_t dtype) {
+    if (check(rows, cols, dtype, "dmuon_layer_norm_workspace_bytes") != DMUON_OK) return 0;
+    return static_cast<size_t>(partial_rows(rows)) * 2 * static_cast<size_t>(cols) * sizeof(float);
+}
+
+extern "C" int dmuon_layer_norm_backward(const void* dy, const void* x, const void* weight, const float* mean,
+                                         const float* rstd, void* dx, void* dweight, void* dbias, int64_t rows,
+                                         int64_t cols, int32_t dtype, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+    const char* where = "dmuon_layer_norm_backward";
+    int r = check(rows, cols, dtype, where);
+    if (r != DMUON_OK) return r;
+    if ((r = check_ptr(dweight, "dweight", where, false)) || (r = check_ptr(dbias, "dbias", where, false)) ||
+        (r = check_ptr(weight, "weight", where, false)))
+        return r;
+    const bool sums = dweight || dbias;
+    if (rows > 0) {
+        if ((r = check_ptr(dy, "dy", where, true)) || (r = check_ptr(x, "x", where, true)) ||
+            (r = check_ptr(mean, "mean", where, true, 4)) || (r = check_ptr(rstd, "rstd", where, true, 4)) ||
+            (r = check_ptr(dx, "dx", where, true)))
+            return r;
+        const size_t need = sums ? dmuon_layer_norm_workspace_bytes(rows, cols, dtype) : 0;
+        if (need && !workspace) return fail(DMUON_ERR_NO_WORKSPACE, std::string(where) + ": workspace is NULL");
+        if (need && reinterpret_cast<uintptr_t>(workspace) % 256)
+            return fail(DMUON_ERR_ALIGN, std::string(where) + ": workspace is not 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(DMUON_ERR_WORKSPACE_TOO_SMALL, std::string(where) + ": workspace of " +
+                                                           std::to_string(workspace_bytes) + " bytes, " +
+                                                           std::to_string(need) + " needed");
+    }
+    int sms = 0;
+    if ((r = device_sms(&sms, where))) return r;
+    const bool bf = dtype == DMUON_BF16;
+    const int vec = bf ? 8 : 4;
+    NormArgs a = {};
+    a.x = x;
+    a.dy = dy;
+    a.w = weight;
+    a.out = dx;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.partial = sums ? static_cast<float*>(workspace) : nullptr;
+    a.rows = rows;
+    a.cols = static_cast<int32_t>(cols);
+    a.aligned = cols % vec == 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int partials = 0;
+    if (rows > 0) {
+        const Shape sh = choose(rows, (cols + vec - 1) / vec, sms, true);
+        cudaError_t e;
+        if (sh.wpr == 0) {
+            const int grid = static_cast<int>(std::min<int64_t>(rows, 2 * sms));
+            if (bf) norm_bwd_wide_kernel<__nv_bfloat16><<<grid, 1024, 0, s>>>(a);
+            else norm_bwd_wide_kernel<float><<<grid, 1024, 0, s>>>(a);
+            e = cudaGetLastError();
+            if (e == cudaSuccess && sums) {
+                const int64_t want = std::min<int64_t>(partial_rows(rows), 64);
+                const int64_t per = (rows + want - 1) / want;
+                partials = static_cast<int>((rows + per - 1) / per);
+                const dim3 g2(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(partials));
+                if (bf) norm_cols_wide_kernel<__nv_bfloat16><<<g2, 256, 0, s>>>(a, per);
+                else norm_cols_wide_kernel<float><<<g2, 256, 0, s>>>(a, per);
+                e = cudaGetLastError();
+            }
+        } else {
+            const int64_t groups = kBwdThreads / (32 * sh.wpr);
+            partials = static_cast<int>(std::min<int64_t>({(rows + groups - 1) / groups, int64_t(2) * sms,
+                                                           partial_rows(rows)}));
+            e = bf ? run_shape<__nv_bfloat16>(sh, a, true, partials, s) : run_shape<float>(sh, a, true, partials, s);
+        }
+        if (e != cudaSuccess) return cuda_result(e, where);
+    }
+    if (!sums) return DMUON_OK;
+    const int grid = static_cast<int>((2 * cols + 31) / 32);
+    if (bf)
+        norm_reduce_kernel<<<grid, 1024, 0, s>>>(a.partial, partials, a.cols, static_cast<__nv_bfloat16*>(dweight),
+                                                 static_cast<__nv_bfloat16*>(dbias));
+    else
+        norm_reduce_kernel<<<grid, 1024, 0, s>>>(a.partial, partials, a.cols, static_cast<float*>(dweight),
+                                                 static_cast<float*>(dbias));
+    return cuda_result(cudaGetLastError(), where);
+}

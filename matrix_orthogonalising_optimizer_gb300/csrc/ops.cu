@@ -1,0 +1,716 @@
+// Host side of the gated feed-forward block and the vocabulary loss: argument
+// checks, workspace layout, tensor maps and launches, and the two small
+// kernels around the shared tensor-core GEMM (ops_gemm.cu) -- the operand
+// pack (fp32 into bf16 parts, rows whose stride TMA cannot take into padded
+// ones) and the loss's row pass.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "dmuon.h"
+#include "ops.h"
+#include "tc.cuh"
+
+namespace dmuon {
+namespace {
+
+int fail(int code, const std::string& msg) {
+    set_last_error(msg);
+    return code;
+}
+
+#define OPS_CUDA(call)                                                                                       \
+    do {                                                                                                     \
+        const cudaError_t e_ = (call);                                                                       \
+        if (e_ != cudaSuccess) return fail(DMUON_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e_)); \
+    } while (0)
+#define OPS_TRY(call)                       \
+    do {                                    \
+        const int r_ = (call);              \
+        if (r_ != DMUON_OK) return r_;      \
+    } while (0)
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int64_t kMaxWidth = int64_t(1) << 20;
+constexpr int64_t kMaxVocab = int64_t(1) << 22;
+constexpr int kMaxLaunches = 4;   // GEMM launches of one call (of one piece)
+constexpr int kSlots = 192;       // partial-sum slots: 48 MiB
+constexpr int kTails = 192;       // split tiles per launch
+constexpr uint64_t kDefaultBudget = uint64_t(2) << 30;
+
+int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+int64_t ceil_div(int64_t v, int64_t a) { return (v + a - 1) / a; }
+
+// ------------------------------------------------------------ workspace
+
+struct Arena {
+    char* base;
+    size_t off = 0;
+    template <typename T>
+    T* take(int64_t count) {
+        T* p = reinterpret_cast<T*>(base + off);  // only offsets are used when base is null
+        off += static_cast<size_t>(up(count * static_cast<int64_t>(sizeof(T)), 256));
+        return p;
+    }
+};
+
+// Counters and partial sums of a call's GEMM launches.
+struct Common {
+    int32_t* counters;  // [kMaxLaunches] unit counters, 64 ints apart, then the tail counts
+    float* partials;
+    static constexpr int64_t kTailInts = int64_t(kTails) * kOpsTailCounts;
+    static constexpr int64_t kInts = kMaxLaunches * (64 + kTailInts);
+    void lay(Arena& a) {
+        counters = a.take<int32_t>(kInts);
+        partials = a.take<float>(kSlots * kOpsSlotFloats);
+    }
+    void bind(OpsLaunch& l, int launch) const {
+        l.counter = counters + launch * 64;
+        l.tail_count = counters + kMaxLaunches * 64 + launch * kTailInts;
+        l.partials = partials;
+    }
+    cudaError_t clear(int launches, cudaStream_t s) const {
+        const int64_t ints = launches <= 0 ? 0 : kMaxLaunches * 64 + launches * kTailInts;
+        return cudaMemsetAsync(counters, 0, ints * sizeof(int32_t), s);
+    }
+};
+
+// An operand as the tensor cores read it: bf16 rows of 16-byte stride, `parts`
+// of them; either the caller's matrix itself or a packed copy.
+struct Operand {
+    const void* p = nullptr;
+    int64_t rows = 0, cols = 0, ld = 0, part = 0;
+    int parts = 1;
+};
+
+// ------------------------------------------------------------ operand pack
+
+constexpr int kMaxPacks = 6;
+
+struct PackItem {
+    const void* src;
+    __nv_bfloat16* dst;
+    int64_t rows, cols, ld, part, first;  // first: running count of 8-column groups
+};
+
+struct PackArgs {
+    PackItem item[kMaxPacks];
+    int32_t n;
+    int32_t f32;
+    int64_t groups;
+};
+
+// One thread per 8 destination columns: fp32 values split into three bf16
+// parts, x = hi + mid + lo, or bf16 values copied.  Memory-bound; only fp32
+// operands and row strides that are not a multiple of 16 bytes come here.
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
+    for (int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; g < a.groups;
+         g += static_cast<int64_t>(gridDim.x) * 256) {
+        int k = 0;
+        while (k + 1 < a.n && a.item[k + 1].first <= g) ++k;
+        const PackItem& it = a.item[k];
+        const int64_t gr = it.ld / 8, r = (g - it.first) / gr, c0 = (g - it.first - r * gr) * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t i = r * it.cols + c0 + j;
+            v[j] = c0 + j >= it.cols ? 0.0f
+                   : a.f32           ? static_cast<const float*>(it.src)[i]
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(it.src)[i]);
+        }
+        __nv_bfloat16* d = it.dst + r * it.ld + c0;
+        const int parts = a.f32 ? kF32Parts : 1;
+        for (int p = 0; p < parts; ++p) {
+            *reinterpret_cast<uint4*>(d + p * it.part) =
+                make_uint4(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]), tc::pack_bf16x2(v[4], v[5]),
+                           tc::pack_bf16x2(v[6], v[7]));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = tc::bf16_rest(v[j]);
+        }
+    }
+}
+
+struct Packer {
+    PackArgs args = {};
+    explicit Packer(bool f32) { args.f32 = f32 ? 1 : 0; }
+
+    // The operand of the row-major contiguous matrix src (rows x cols); a copy
+    // in the workspace where the tensor cores cannot read it in place.
+    Operand add(Arena& a, const void* src, int64_t rows, int64_t cols) {
+        Operand o;
+        o.rows = rows;
+        o.cols = cols;
+        o.ld = up(cols, 8);
+        o.parts = args.f32 ? kF32Parts : 1;
+        o.part = rows * o.ld;
+        if (!args.f32 && cols % 8 == 0) {
+            o.p = src;
+            return o;
+        }
+        __nv_bfloat16* d = a.take<__nv_bfloat16>(o.part * o.parts);
+        o.p = d;
+        PackItem& it = args.item[args.n++];
+        it = PackItem{src, d, rows, cols, o.ld, o.part, args.groups};
+        args.groups += rows * o.ld / 8;
+        return o;
+    }
+    cudaError_t run(cudaStream_t s) const {
+        if (args.groups == 0) return cudaSuccess;
+        const int64_t blocks = std::min<int64_t>(ceil_div(args.groups, 256), 4096);
+        pack_kernel<<<static_cast<int>(blocks), 256, 0, s>>>(args);
+        return cudaGetLastError();
+    }
+};
+
+// A bf16 (parts) buffer written by one product's epilogue and read by others.
+Operand scratch(Arena& a, int64_t rows, int64_t cols, int parts) {
+    Operand o;
+    o.rows = rows;
+    o.cols = cols;
+    o.ld = up(cols, 8);
+    o.parts = parts;
+    o.part = rows * o.ld;
+    o.p = a.take<__nv_bfloat16>(o.part * parts);
+    return o;
+}
+
+OpsMat out_of(const Operand& o) {
+    return OpsMat{const_cast<void*>(o.p), o.ld, ELEM_BF16, 1, o.parts > 1 ? o.part : 0};
+}
+
+OpsMat user_mat(const void* p, int64_t ld, bool f32) {
+    return OpsMat{const_cast<void*>(p), ld, f32 ? ELEM_F32 : ELEM_BF16, ld % (f32 ? 4 : 8) == 0 ? 1 : 0, 0};
+}
+
+// ------------------------------------------------------------ products
+
+int encode(CUtensorMap* map, const Operand& o, bool mn) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)
+                   : nullptr;
+    }();
+    if (!enc) return fail(DMUON_ERR_CUDA, "cuTensorMapEncodeTiled entry point not found");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
+                                static_cast<cuuint64_t>(o.parts)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld * 2), static_cast<cuuint64_t>(o.part * 2)};
+    // K-major: 64 deep x 128 rows; MN-major: 64 columns x 64 deep
+    const cuuint32_t box[3] = {64, mn ? 64u : 128u, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(DMUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
+    return DMUON_OK;
+}
+
+// D (M x N) = sum over sources of A_s B_s, K deep each.  `dual`: B's two
+// sources are two matrices of N rows against one A.
+int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a, bool a_mn, const Operand* b,
+                bool b_mn, int sources, bool dual) {
+    const int na = dual ? 1 : sources;
+    for (int s = 0; s < na; ++s) OPS_TRY(encode(&P.a[s], a[s], a_mn));
+    for (int s = 0; s < sources; ++s) OPS_TRY(encode(&P.b[s], b[s], b_mn));
+    P.M = static_cast<int32_t>(M);
+    P.N = static_cast<int32_t>(N);
+    P.slabs = static_cast<int32_t>(ceil_div(K, 64));
+    P.a_mn = a_mn;
+    P.b_mn = b_mn;
+    P.dual = dual;
+    P.tiles_m = static_cast<int32_t>(ceil_div(M, 256));
+    P.tiles_n = static_cast<int32_t>(ceil_div(N, dual ? 128 : 256));
+    // part products above 2^-24 of the whole, the smallest first
+    static const int kPairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
+    const bool f32 = a[0].parts > 1;
+    P.nseg = 0;
+    for (int i = f32 ? 0 : 5; i < 6; ++i)
+        for (int s = 0; s < na; ++s)
+            P.seg[P.nseg++] = static_cast<uint16_t>(s | kPairs[i][0] << 4 | kPairs[i][1] << 8);
+    return DMUON_OK;
+}
+
+int run_gemm(OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s, const char* where) {
+    int pairs = 0;
+    OPS_CUDA(ops_pairs(&pairs));
+    ops_schedule(l, pairs, kSlots, kTails);
+    OPS_CUDA(launch_ops_gemm(l, kind, f32, s));
+    return DMUON_OK;
+}
+
+// ------------------------------------------------------------ checks
+
+int check_dtype(int32_t dtype, const char* where) {
+    if (dtype != DMUON_BF16 && dtype != DMUON_FP32)
+        return fail(DMUON_ERR_UNSUPPORTED_DTYPE, std::string(where) + ": dtype must be DMUON_BF16 or DMUON_FP32");
+    return DMUON_OK;
+}
+
+int check_ptr(const void* p, const char* name, const char* where, size_t align = 16) {
+    if (!p) return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": " + name + " is NULL");
+    if (reinterpret_cast<uintptr_t>(p) % align)
+        return fail(DMUON_ERR_ALIGN,
+                    std::string(where) + ": " + name + " is not " + std::to_string(align) + "-byte aligned");
+    return DMUON_OK;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need, const char* where) {
+    if (need == 0) return DMUON_OK;
+    if (!ws) return fail(DMUON_ERR_NO_WORKSPACE, std::string(where) + ": workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(ws) % 256)
+        return fail(DMUON_ERR_ALIGN, std::string(where) + ": workspace is not 256-byte aligned");
+    if (have < need)
+        return fail(DMUON_ERR_WORKSPACE_TOO_SMALL, std::string(where) + ": workspace of " + std::to_string(have) +
+                                                       " bytes, " + std::to_string(need) + " needed");
+    return DMUON_OK;
+}
+
+bool in_range(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+
+int check_device(const char* where) {
+    int dev = 0, major = 0, minor = 0;
+    OPS_CUDA(cudaGetDevice(&dev));
+    OPS_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+    OPS_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
+    if (major != 10 || minor != 3)
+        return fail(DMUON_ERR_UNSUPPORTED_DEVICE, std::string(where) + ": needs an sm_103 GPU");
+    return DMUON_OK;
+}
+
+// ------------------------------------------------------------ gated block
+
+struct FfnLayout {
+    Common common;
+    Packer pack;
+    Operand x, wg, wu, wd, dy, h, da, du;
+    size_t bytes = 0;
+
+    FfnLayout(char* base, const void* px, const void* pg, const void* pu, const void* pd, const void* pdy, int64_t n,
+              int64_t d, int64_t f, bool f32, bool backward)
+        : pack(f32) {
+        Arena a{base};
+        common.lay(a);
+        x = pack.add(a, px, n, d);
+        wg = pack.add(a, pg, f, d);
+        wu = pack.add(a, pu, f, d);
+        wd = pack.add(a, pd, d, f);
+        const int parts = f32 ? kF32Parts : 1;
+        h = scratch(a, n, f, parts);
+        if (backward) {
+            dy = pack.add(a, pdy, n, d);
+            da = scratch(a, n, f, parts);
+            du = scratch(a, n, f, parts);
+        }
+        bytes = a.off;
+    }
+};
+
+bool ffn_sizes_ok(int64_t n, int64_t d, int64_t f) {
+    return in_range(n, 0, kMaxTokens) && in_range(d, 1, kMaxWidth) && in_range(f, 1, kMaxWidth);
+}
+
+int check_ffn(int64_t n, int64_t d, int64_t f, int32_t dtype, int32_t act, const char* where) {
+    if (!ffn_sizes_ok(n, d, f))
+        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": tokens must be in [0, 2^24], dim and hidden in [1, 2^20]");
+    OPS_TRY(check_dtype(dtype, where));
+    if (act != DMUON_ACT_SILU && act != DMUON_ACT_GELU)
+        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": unknown activation");
+    return DMUON_OK;
+}
+
+// ------------------------------------------------------------ vocabulary loss
+
+struct LossRowArgs {
+    const float2* stats;        // [rows][nblk]
+    const float* target_logit;  // [rows]
+    const int64_t* targets;
+    const float* coef;          // NULL: 1
+    float* loss;
+    float* lse;
+    const void* e;              // exponentials (bf16 or fp32), NULL: losses only
+    __nv_bfloat16* dz;          // logit gradients, kF32Parts parts for fp32
+    int64_t ld, part, ignore;
+    int64_t vocab;
+    int32_t nblk, groups;       // 8-column groups of a row
+    int32_t seg_groups;         // groups per blockIdx.y
+};
+
+constexpr int kRowThreads = 256;
+
+// Row pass of the loss.  Each block reduces its row's (max, sum) blocks to
+// lse = M + log sum_b s_b exp(m_b - M) in a fixed order; the first writes the
+// loss, and each turns its share of the row's exponentials e = exp(z - m_b)
+// into logit gradients dz = c e exp(m_b - lse), the target's as c expm1(z_t -
+// lse), which keeps the digits of p - 1 where p is near 1.  Memory-bound: 4
+// bytes per bf16 logit, in place.
+template <bool kF32>
+__global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_constant__ LossRowArgs a) {
+    __shared__ float red[kRowThreads / 32];
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float2* st = a.stats + row * a.nblk;
+    float m = __int_as_float(0xff800000);
+    for (int b = tid; b < a.nblk; b += kRowThreads) m = fmaxf(m, st[b].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(tc::kFullMask, m, o));
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int w = 1; w < kRowThreads / 32; ++w) m = fmaxf(m, red[w]);
+    __syncthreads();
+    float s = 0.0f;
+    for (int b = tid; b < a.nblk; b += kRowThreads) {
+        const float2 v = st[b];
+        s += v.y * expf(v.x - m);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(tc::kFullMask, s, o);
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowThreads / 32; ++w) s += red[w];
+    const float lse = m + logf(s);
+    const int64_t t = a.targets[row];
+    const bool ignored = t == a.ignore;
+    const bool valid = !ignored && t >= 0 && t < a.vocab;
+    const float nll = valid ? lse - a.target_logit[row] : 0.0f;
+    if (blockIdx.y == 0 && tid == 0) {
+        a.lse[row] = lse;
+        a.loss[row] = valid || ignored ? nll : __int_as_float(0x7fc00000);
+    }
+    if (!a.e) return;
+    const float c = valid ? (a.coef ? a.coef[row] : 1.0f) : 0.0f;
+    const int g0 = blockIdx.y * a.seg_groups, g1 = min(a.groups, g0 + a.seg_groups);
+    for (int g = g0 + tid; g < g1; g += kRowThreads) {
+        const int64_t c0 = static_cast<int64_t>(g) * 8;
+        const int64_t off = row * a.ld + c0;
+        float v[8];
+        if (kF32) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.e) + off);
+            const float4 x = p[0], y = p[1];
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+            v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.e) + off);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = tc::unpack_bf16x2(w[k]);
+                v[2 * k] = f.x;
+                v[2 * k + 1] = f.y;
+            }
+        }
+        const float scale = c * expf(st[c0 / 128].x - lse);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = valid ? v[k] * scale : 0.0f;
+            if (valid && c0 + k == t) v[k] = c * expm1f(-nll);
+        }
+        __nv_bfloat16* d = a.dz + off;
+#pragma unroll
+        for (int p = 0; p < (kF32 ? kF32Parts : 1); ++p) {
+            *reinterpret_cast<uint4*>(d + p * a.part) =
+                make_uint4(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]), tc::pack_bf16x2(v[4], v[5]),
+                           tc::pack_bf16x2(v[6], v[7]));
+            if (kF32) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = tc::bf16_rest(v[k]);
+            }
+        }
+    }
+}
+
+struct LossLayout {
+    Common common;
+    Packer pack;
+    Operand x, w, dz;
+    void* e = nullptr;         // exponentials (bf16: in dz's buffer)
+    float2* stats = nullptr;
+    float* target_logit = nullptr;
+    float* dw_sum = nullptr;   // fp32 sum of dW over pieces (bf16, more than one piece)
+    int64_t piece = 0, pieces = 0;  // tokens per piece
+    int nblk = 0;
+    size_t bytes = 0;
+
+    LossLayout(char* base, const void* px, const void* pw, int64_t n, int64_t d, int64_t v, bool f32, bool grad,
+               uint64_t budget)
+        : pack(f32) {
+        Arena a{base};
+        common.lay(a);
+        x = pack.add(a, px, n, d);
+        w = pack.add(a, pw, v, d);
+        nblk = static_cast<int>(ceil_div(v, 128));
+        const int64_t ld = up(v, 8);
+        // bytes of one token's logits: statistics, exponentials, gradients
+        const int64_t row = 8 * nblk + (grad ? (f32 ? 10 : 2) * ld : 0);
+        const int64_t limit = static_cast<int64_t>(std::min<uint64_t>(budget ? budget : kDefaultBudget, 1ull << 46));
+        // whole 256-row tiles per piece, at least one; pieces of equal size
+        piece = std::max<int64_t>(limit / row / 256 * 256, 256);
+        pieces = std::max<int64_t>(ceil_div(n, piece), 1);
+        piece = std::min(n, up(ceil_div(n, pieces), 256));
+        pieces = n > 0 ? ceil_div(n, piece) : 0;
+        stats = a.take<float2>(piece * nblk);
+        target_logit = a.take<float>(piece);
+        if (grad) {
+            dz = scratch(a, piece, v, f32 ? kF32Parts : 1);
+            e = f32 ? static_cast<void*>(a.take<float>(piece * ld)) : const_cast<void*>(dz.p);
+            if (!f32 && pieces > 1) dw_sum = a.take<float>(v * up(d, 4));
+        }
+        bytes = a.off;
+    }
+};
+
+bool loss_sizes_ok(int64_t n, int64_t d, int64_t v) {
+    return in_range(n, 0, kMaxTokens) && in_range(d, 1, kMaxWidth) && in_range(v, 1, kMaxVocab);
+}
+
+// Rows [r0, r0 + n) of an operand.
+Operand rows_of(const Operand& o, int64_t r0, int64_t n) {
+    Operand s = o;
+    s.p = static_cast<const __nv_bfloat16*>(o.p) + r0 * o.ld;
+    s.rows = n;
+    return s;
+}
+
+}  // namespace
+}  // namespace dmuon
+
+using namespace dmuon;
+
+extern "C" int dmuon_ops_status(void) {
+    int32_t v = 0;
+    if (ops_read_status(&v) != cudaSuccess)
+        return fail(DMUON_ERR_CUDA, "dmuon_ops_status: cannot read the status flag");
+    return v ? DMUON_ERR_DEVICE_TIMEOUT : DMUON_OK;
+}
+
+extern "C" size_t dmuon_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype,
+                                                  int32_t backward) {
+    if (!ffn_sizes_ok(tokens, dim, hidden) || check_dtype(dtype, "dmuon_gated_ffn_workspace_bytes") != DMUON_OK)
+        return 0;
+    if (tokens == 0) return 0;
+    return FfnLayout(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, tokens, dim, hidden, dtype == DMUON_FP32,
+                     backward != 0)
+        .bytes;
+}
+
+extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                                       void* y, void* gate, void* up_proj, int64_t tokens, int64_t dim, int64_t hidden,
+                                       int32_t dtype, int32_t activation, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+    const char* where = "dmuon_gated_ffn_forward";
+    OPS_TRY(check_ffn(tokens, dim, hidden, dtype, activation, where));
+    if ((gate == nullptr) != (up_proj == nullptr))
+        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": gate and up are stored together or not at all");
+    if (tokens == 0) return DMUON_OK;
+    OPS_TRY(check_ptr(x, "x", where));
+    OPS_TRY(check_ptr(w_gate, "w_gate", where));
+    OPS_TRY(check_ptr(w_up, "w_up", where));
+    OPS_TRY(check_ptr(w_down, "w_down", where));
+    OPS_TRY(check_ptr(y, "y", where));
+    if (gate) {
+        OPS_TRY(check_ptr(gate, "gate", where));
+        OPS_TRY(check_ptr(up_proj, "up", where));
+    }
+    const bool f32 = dtype == DMUON_FP32;
+    FfnLayout L(static_cast<char*>(workspace), x, w_gate, w_up, w_down, nullptr, tokens, dim, hidden, f32, false);
+    OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
+    OPS_TRY(check_device(where));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    OPS_CUDA(L.common.clear(2, s));
+    OPS_CUDA(L.pack.run(s));
+    {
+        OpsLaunch l = {};
+        l.n = 1;
+        L.common.bind(l, 0);
+        OpsProblem& P = l.p[0];
+        const Operand b[2] = {L.wg, L.wu};
+        OPS_TRY(set_problem(P, tokens, hidden, dim, &L.x, false, b, false, 2, true));
+        P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
+        P.out0 = out_of(L.h);
+        if (gate) {
+            P.out1 = user_mat(gate, hidden, f32);
+            P.out2 = user_mat(up_proj, hidden, f32);
+        }
+        OPS_TRY(run_gemm(l, OPS_GATE, f32, s, where));
+    }
+    OpsLaunch l = {};
+    l.n = 1;
+    L.common.bind(l, 1);
+    OPS_TRY(set_problem(l.p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false));
+    l.p[0].out0 = user_mat(y, dim, f32);
+    return run_gemm(l, OPS_STORE, f32, s, where);
+}
+
+extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up,
+                                        const void* w_down, const void* gate, const void* up_proj, void* dx,
+                                        void* dw_gate, void* dw_up, void* dw_down, int64_t tokens, int64_t dim,
+                                        int64_t hidden, int32_t dtype, int32_t activation, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+    const char* where = "dmuon_gated_ffn_backward";
+    OPS_TRY(check_ffn(tokens, dim, hidden, dtype, activation, where));
+    OPS_TRY(check_ptr(dw_gate, "dw_gate", where));
+    OPS_TRY(check_ptr(dw_up, "dw_up", where));
+    OPS_TRY(check_ptr(dw_down, "dw_down", where));
+    const bool f32 = dtype == DMUON_FP32;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tokens == 0) {  // no rows: the weights' gradients are sums over none
+        const size_t bytes = static_cast<size_t>(dim) * hidden * (f32 ? 4 : 2);
+        OPS_CUDA(cudaMemsetAsync(dw_gate, 0, bytes, s));
+        OPS_CUDA(cudaMemsetAsync(dw_up, 0, bytes, s));
+        OPS_CUDA(cudaMemsetAsync(dw_down, 0, bytes, s));
+        return DMUON_OK;
+    }
+    OPS_TRY(check_ptr(dy, "dy", where));
+    OPS_TRY(check_ptr(x, "x", where));
+    OPS_TRY(check_ptr(w_gate, "w_gate", where));
+    OPS_TRY(check_ptr(w_up, "w_up", where));
+    OPS_TRY(check_ptr(w_down, "w_down", where));
+    OPS_TRY(check_ptr(gate, "gate", where));
+    OPS_TRY(check_ptr(up_proj, "up", where));
+    OPS_TRY(check_ptr(dx, "dx", where));
+    FfnLayout L(static_cast<char*>(workspace), x, w_gate, w_up, w_down, dy, tokens, dim, hidden, f32, true);
+    OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
+    OPS_TRY(check_device(where));
+    OPS_CUDA(L.common.clear(2, s));
+    OPS_CUDA(L.pack.run(s));
+    {
+        // dh = dy Wd; the epilogue turns it into da, du and h
+        OpsLaunch l = {};
+        l.n = 1;
+        L.common.bind(l, 0);
+        OpsProblem& P = l.p[0];
+        OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false));
+        P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
+        P.in0 = user_mat(gate, hidden, f32);
+        P.in1 = user_mat(up_proj, hidden, f32);
+        P.out0 = out_of(L.da);
+        P.out1 = out_of(L.du);
+        P.out2 = out_of(L.h);
+        OPS_TRY(run_gemm(l, OPS_DGATE, f32, s, where));
+    }
+    // dx and the three weight gradients in one launch, the longest K first
+    OpsLaunch l = {};
+    l.n = 4;
+    L.common.bind(l, 1);
+    const bool dx_first = 2 * hidden >= tokens;
+    int k = dx_first ? 1 : 0;
+    OPS_TRY(set_problem(l.p[k], hidden, dim, tokens, &L.da, true, &L.x, true, 1, false));
+    l.p[k++].out0 = user_mat(dw_gate, dim, f32);
+    OPS_TRY(set_problem(l.p[k], hidden, dim, tokens, &L.du, true, &L.x, true, 1, false));
+    l.p[k++].out0 = user_mat(dw_up, dim, f32);
+    OPS_TRY(set_problem(l.p[k], dim, hidden, tokens, &L.dy, true, &L.h, true, 1, false));
+    l.p[k++].out0 = user_mat(dw_down, hidden, f32);
+    k = dx_first ? 0 : 3;
+    const Operand a[2] = {L.da, L.du}, b[2] = {L.wg, L.wu};
+    OPS_TRY(set_problem(l.p[k], tokens, dim, hidden, a, false, b, true, 2, false));
+    l.p[k].out0 = user_mat(dx, dim, f32);
+    return run_gemm(l, OPS_STORE, f32, s, where);
+}
+
+extern "C" size_t dmuon_vocab_loss_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab, int32_t dtype,
+                                                   int32_t grad, uint64_t budget) {
+    if (!loss_sizes_ok(tokens, dim, vocab) || check_dtype(dtype, "dmuon_vocab_loss_workspace_bytes") != DMUON_OK)
+        return 0;
+    if (tokens == 0) return 0;
+    return LossLayout(nullptr, nullptr, nullptr, tokens, dim, vocab, dtype == DMUON_FP32, grad != 0, budget).bytes;
+}
+
+extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t* targets, const float* coef,
+                                int64_t ignore_index, float* loss, float* lse, void* dx, void* dweight, int64_t tokens,
+                                int64_t dim, int64_t vocab, int32_t dtype, uint64_t budget, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    const char* where = "dmuon_vocab_loss";
+    if (!loss_sizes_ok(tokens, dim, vocab))
+        return fail(DMUON_ERR_INVALID_ARG,
+                    std::string(where) + ": tokens must be in [0, 2^24], dim in [1, 2^20], vocab in [1, 2^22]");
+    OPS_TRY(check_dtype(dtype, where));
+    if (tokens > 0 && (dx == nullptr) != (dweight == nullptr))
+        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": dx and dweight come together or not at all");
+    const bool f32 = dtype == DMUON_FP32, grad = dweight != nullptr;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (grad) OPS_TRY(check_ptr(dweight, "dweight", where));
+    if (tokens == 0) {
+        if (grad) OPS_CUDA(cudaMemsetAsync(dweight, 0, static_cast<size_t>(vocab) * dim * (f32 ? 4 : 2), s));
+        return DMUON_OK;
+    }
+    OPS_TRY(check_ptr(x, "x", where));
+    OPS_TRY(check_ptr(weight, "weight", where));
+    OPS_TRY(check_ptr(targets, "targets", where, 8));
+    OPS_TRY(check_ptr(loss, "loss", where, 4));
+    OPS_TRY(check_ptr(lse, "lse", where, 4));
+    if (grad) OPS_TRY(check_ptr(dx, "dx", where));
+    if (coef) OPS_TRY(check_ptr(coef, "coef", where, 4));
+    LossLayout L(static_cast<char*>(workspace), x, weight, tokens, dim, vocab, f32, grad, budget);
+    OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
+    OPS_TRY(check_device(where));
+    OPS_CUDA(L.pack.run(s));
+    const int64_t es = f32 ? 4 : 2;
+    for (int64_t i = 0; i < L.pieces; ++i) {
+        const int64_t r0 = i * L.piece, n = std::min(L.piece, tokens - r0);
+        OPS_CUDA(L.common.clear(grad ? 2 : 1, s));
+        const Operand xp = rows_of(L.x, r0, n);
+        {
+            OpsLaunch l = {};
+            l.n = 1;
+            L.common.bind(l, 0);
+            OpsProblem& P = l.p[0];
+            OPS_TRY(set_problem(P, n, vocab, dim, &xp, false, &L.w, false, 1, false));
+            P.stats = L.stats;
+            P.nblk = L.nblk;
+            P.target_logit = L.target_logit;
+            P.targets = targets + r0;
+            if (grad) P.out0 = OpsMat{L.e, L.dz.ld, f32 ? ELEM_F32 : ELEM_BF16, 1, 0};
+            OPS_TRY(run_gemm(l, OPS_LOGITS, f32, s, where));
+        }
+        LossRowArgs a = {};
+        a.stats = L.stats;
+        a.target_logit = L.target_logit;
+        a.targets = targets + r0;
+        a.coef = coef ? coef + r0 : nullptr;
+        a.loss = loss + r0;
+        a.lse = lse + r0;
+        a.ignore = ignore_index;
+        a.vocab = vocab;
+        a.nblk = L.nblk;
+        int segs = 1;
+        if (grad) {
+            a.e = L.e;
+            a.dz = static_cast<__nv_bfloat16*>(const_cast<void*>(L.dz.p));
+            a.ld = L.dz.ld;
+            a.part = L.dz.part;
+            a.groups = static_cast<int32_t>(ceil_div(vocab, 8));
+            // a few rows: share each row among blocks, so that about 1200 run
+            segs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.groups, 1024), 1200 / n)));
+            a.seg_groups = static_cast<int32_t>(ceil_div(a.groups, segs));
+        }
+        const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(segs));
+        if (f32) loss_row_kernel<true><<<grid, kRowThreads, 0, s>>>(a);
+        else loss_row_kernel<false><<<grid, kRowThreads, 0, s>>>(a);
+        OPS_CUDA(cudaGetLastError());
+        if (!grad) continue;
+        // dx (K = vocab) and dW (K = the piece's tokens) in one launch
+        const Operand dz = rows_of(L.dz, 0, n);
+        OpsLaunch l = {};
+        l.n = 2;
+        L.common.bind(l, 1);
+        const int kx = vocab >= n ? 0 : 1;
+        OPS_TRY(set_problem(l.p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false));
+        l.p[kx].out0 = user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
+        OpsProblem& W = l.p[1 - kx];
+        OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false));
+        // the sum over pieces stays in fp32: rounded once, with the last piece
+        const OpsMat sum = L.dw_sum ? user_mat(L.dw_sum, up(dim, 4), true) : user_mat(dweight, dim, f32);
+        const bool last = i + 1 == L.pieces;
+        W.out0 = last ? user_mat(dweight, dim, f32) : sum;
+        if (i > 0) W.in0 = sum;
+        OPS_TRY(run_gemm(l, OPS_STORE, f32, s, where));
+    }
+    return DMUON_OK;
+}

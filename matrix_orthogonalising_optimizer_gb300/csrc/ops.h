@@ -1,0 +1,85 @@
+// Internal structures of the training operators (layer norm, gated
+// feed-forward block, vocabulary loss): the grouped tcgen05 GEMM they share
+// and its host-side builder.  Not part of the C ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+#include <string>
+
+#include "internal.h"
+
+namespace dmuon {
+
+void set_last_error(const std::string& msg);
+
+constexpr int kOpsMaxProblems = 4;
+constexpr int kOpsMaxSegs = 12;
+
+// An fp32 matrix enters the tensor cores as three bf16 parts, x = hi + mid +
+// lo (8 + 8 + 8 significant bits), and a product of two such matrices as the
+// six part products above 2^-24 of the whole, the smallest first.
+constexpr int kF32Parts = 3;
+
+enum OpsEpi : int32_t { OPS_STORE = 0, OPS_GATE = 1, OPS_DGATE = 2, OPS_LOGITS = 3 };
+enum OpsAct : int32_t { OPS_SILU = 0, OPS_GELU = 1 };
+
+// A row-major matrix an epilogue reads or writes.
+struct OpsMat {
+    void* p;
+    int64_t ld;      // elements
+    int32_t type;    // ElemType
+    int32_t vec;     // rows start on 16-byte boundaries: 16-byte accesses
+    int64_t part;    // > 0: kF32Parts bf16 parts, `part` elements apart
+};
+
+// D (M x N) = sum over K segments of A-part (M x K) * B-part (K x N).  Segment s
+// reads source, A part and B part from seg[s]; every segment is `slabs` 64-deep
+// K slabs long (a ragged end is zero-filled by TMA).  A is K-major (stored
+// M x K) or MN-major (stored K x M), B likewise (N x K or K x N).  `dual`: B is
+// two matrices of N rows, source maps b[0] and b[1], and a pair tile is 128
+// columns of each (CTA rank r loads those of matrix r), so accumulator columns
+// 0..127 belong to the first and 128..255 to the second.
+struct OpsProblem {
+    CUtensorMap a[2], b[2];
+    int32_t M, N;
+    int32_t slabs, nseg;
+    uint16_t seg[kOpsMaxSegs];  // source | A part << 4 | B part << 8
+    int32_t a_mn, b_mn, dual;
+    int32_t tiles_m, tiles_n;
+    // work units: `whole` tiles of all K, then the other tiles in `split` K ranges each
+    int32_t whole, split;
+    int32_t unit_begin;  // first unit of this problem in the launch
+    int32_t tail_begin;  // first split tile (counter index)
+    int32_t slot_begin;  // first partial-sum slot
+    // epilogue
+    int32_t act;
+    OpsMat out0, out1, out2;  // STORE: D | GATE: h, a, u | DGATE: da, du, h | LOGITS: exponentials
+    OpsMat in0, in1;          // STORE: in0 = addend (fp32) | DGATE: a, u
+    float2* stats;            // LOGITS: [M][nblk] (max, sum of exp) of 128-column blocks
+    int32_t nblk;
+    float* target_logit;      // LOGITS: [M]
+    const int64_t* targets;   // LOGITS: [M]
+};
+
+struct OpsLaunch {
+    OpsProblem p[kOpsMaxProblems];
+    int32_t n, total_units;
+    int32_t* counter;      // unit counter, zero at launch
+    int32_t* tail_count;   // arrivals per (split tile, CTA rank, epilogue warp), zero at launch
+    float* partials;       // split tiles' partial sums
+};
+
+constexpr int64_t kOpsSlotFloats = 256 * 256;  // one partial accumulator of a pair tile
+constexpr int kOpsTailCounts = 16;             // counters per split tile
+
+// Splits the launch's problems into work units (see OpsProblem) for `pairs`
+// resident CTA pairs; `slots` partial-sum slots are available.  Host only.
+void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails);
+cudaError_t ops_pairs(int* pairs);  // resident CTA pairs of the GEMM kernel on the current device
+cudaError_t ops_read_status(int32_t* v);  // reads and clears the GEMM's time-out flag
+cudaError_t launch_ops_gemm(const OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s);
+
+}  // namespace dmuon

@@ -1,0 +1,834 @@
+// Grouped GEMM of the training operators on the 5th-generation tensor cores
+// (sm_103a), with the operators' element-wise parts fused into its epilogue.
+//
+// One launch holds up to four products D = A B of any sizes, each with A and B
+// K-major or MN-major, so every product of a forward and a backward pass reads
+// its operands where they lie (no transposed copies):
+//   gated block  h = act(x Wg^T) * (x Wu^T)   one pass, dual B tile   OPS_GATE
+//                y = h Wd^T                                           OPS_STORE
+//                dh = dy Wd -> da, du, h                              OPS_DGATE
+//                dx = da Wg + du Wu (two K sources), dW = . ^T .      OPS_STORE
+//   vocab loss   z = x W^T -> exp(z - block max), block max and sum   OPS_LOGITS
+//                dx = dz W, dW = dz^T x                               OPS_STORE
+//
+// What bounds it: the tensor cores for more than a few hundred rows, else the
+// read of the weights.  A 256 x 256 tile of a CTA pair
+// (tcgen05.mma.cta_group::2, CTA rank r holds rows 128 r .. of A and columns
+// 128 r .. of B in its own shared memory) takes 32 KB of operands per CTA and
+// 64-deep K slab from L2 for 8.4 MFLOP, and six such stages are in flight.
+// Two 256-column TMEM accumulators let the eight epilogue warps work on one
+// tile while the next one's MMAs run.
+//
+// Schedule: units are taken in order from a counter (neighbouring tiles stay
+// together in L2).  Tiles that would leave most pairs idle at the end of a
+// launch are split along K (ops_schedule): each unit of a split tile stores its
+// partial sum, and the warp that arrives last at a tile's counter adds the
+// partial sums in K order -- a fixed order, so results do not depend on which
+// unit was last -- and runs the epilogue.  No unit waits for another.
+//
+// Warp roles and the bounded waits are those of the optimizer's GEMM
+// (gemm_tc.cu): warp 0 TMA, warp 1 MMA (leader CTA), warps 4..11 epilogue.
+#include <type_traits>
+
+#include "ops.h"
+#include "tc.cuh"
+
+namespace dmuon {
+namespace {
+
+using namespace tc;
+
+// set by a wait that gave up; read and cleared by dmuon_ops_status
+__device__ int32_t g_ops_status = 0;
+
+constexpr int BM = 128, BN = 256;               // per-CTA accumulator
+constexpr int STAGES = 6;
+constexpr int SLAB_K = 64;                      // bf16 per 128-byte swizzled row
+constexpr int UMMA_K = 16;
+constexpr int kPair = 2;
+constexpr int kThreads = 384;
+constexpr int OP_BYTES = 128 * 128;             // one CTA's share of an operand slab
+constexpr int MN_BOX_BYTES = SLAB_K * 128;      // one MN-major box: 64 K-rows x 128 B
+constexpr uint32_t STAGE_TX = kPair * 2 * OP_BYTES;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int kTileRing = 4;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kRegsLow = 56, kRegsEpi = 224;    // 56 + 2 x 224 = 3 x 168: the launch's registers
+constexpr uint32_t kTileReaders = kPair * kEpiWarps + 2;
+constexpr int CH = 16;
+constexpr uint16_t kPairMask = 3;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct __align__(1024) Smem {
+    uint8_t a[STAGES][OP_BYTES];
+    uint8_t b[STAGES][OP_BYTES];
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t tile_full[kTileRing];
+    uint64_t tile_empty[kTileRing];
+    int32_t tile_slot[kTileRing];
+    uint32_t tmem_base;
+};
+
+__host__ __device__ constexpr uint32_t make_idesc(bool a_mn, bool b_mn) {
+    // kind::f16: bf16 A and B, fp32 D, M = 256 (the pair), N = 256
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>((kPair * BM) >> 4) << 24);
+}
+
+struct Unit {
+    int p, tm, tn, kb0, kb1, part, split, slot, tail;
+};
+
+__device__ __forceinline__ Unit decode_unit(const OpsLaunch& L, int t) {
+    Unit u;
+    u.p = 0;
+    while (u.p + 1 < L.n && L.p[u.p + 1].unit_begin <= t) ++u.p;
+    const OpsProblem& P = L.p[u.p];
+    const int local = t - P.unit_begin;
+    const int total = P.slabs * P.nseg;
+    int tile = local;
+    u.split = 1;
+    u.part = u.slot = u.tail = 0;
+    u.kb0 = 0;
+    u.kb1 = total;
+    if (local >= P.whole) {
+        const int r = local - P.whole, tt = r / P.split;
+        tile = P.whole + tt;
+        u.split = P.split;
+        u.part = r - tt * P.split;
+        u.kb0 = static_cast<int>(static_cast<int64_t>(total) * u.part / P.split);
+        u.kb1 = static_cast<int>(static_cast<int64_t>(total) * (u.part + 1) / P.split);
+        u.slot = P.slot_begin + tt * P.split;
+        u.tail = P.tail_begin + tt;
+    }
+    // panels of 8 column tiles, row tiles inside a panel: the pairs in flight
+    // then cover about 10 x 8 tiles, whose rows and columns stay in L2
+    constexpr int kPanel = 8;
+    const int panel_tiles = P.tiles_m * kPanel;
+    const int panel = tile / panel_tiles;
+    const int within = tile - panel * panel_tiles;
+    const int width = min(kPanel, P.tiles_n - panel * kPanel);
+    u.tm = within / width;
+    u.tn = panel * kPanel + within % width;
+    return u;
+}
+
+__device__ __forceinline__ int wait_tile(uint64_t* full, const int32_t* slots, int k, int32_t* status, int total) {
+    const int slot = k % kTileRing;
+    const uint32_t ph = static_cast<uint32_t>(k / kTileRing) & 1u;
+    if (!mbar_wait<true>(&full[slot], ph, status)) return total;
+    int32_t t;
+    asm volatile("ld.acquire.cluster.shared::cta.b32 %0, [%1];" : "=r"(t) : "r"(saddr(&slots[slot])) : "memory");
+    return t;
+}
+
+__device__ __forceinline__ void release_tile(uint64_t* empty, int k) {
+    mbar_arrive_cluster(mapa(saddr(&empty[k % kTileRing]), 0));
+}
+
+// ------------------------------------------------------- matrix accesses
+// After tcgen05.ld lane i of a warp holds row r0 + i, columns c0 .. c0 + 15.
+// Whole chunks of 16-byte-aligned rows are regrouped between lanes so that one
+// instruction covers whole 32-byte sectors; others go element by element.  All
+// 32 lanes call these; rows >= M and columns >= N are not touched.
+
+__device__ __forceinline__ void st_bf16(__nv_bfloat16* base, int64_t ld, bool vec, int r0, int c0, int lane,
+                                        const float (&v)[CH], int M, int N) {
+    if (vec && c0 + CH <= N) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+        const bool odd = lane & 1;
+        uint32_t d0[4], d1[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t keep = odd ? w[4 + k] : w[k];
+            const uint32_t recv = __shfl_xor_sync(kFullMask, odd ? w[k] : w[4 + k], 1);
+            d0[k] = odd ? recv : keep;  // row (lane & ~1), half `odd`
+            d1[k] = odd ? keep : recv;  // row (lane | 1),  half `odd`
+        }
+        const int ra = r0 + (lane & ~1);
+        __nv_bfloat16* p = base + static_cast<int64_t>(ra) * ld + c0 + 8 * odd;
+        if (ra < M) *reinterpret_cast<uint4*>(p) = make_uint4(d0[0], d0[1], d0[2], d0[3]);
+        if (ra + 1 < M) *reinterpret_cast<uint4*>(p + ld) = make_uint4(d1[0], d1[1], d1[2], d1[3]);
+        return;
+    }
+    const int r = r0 + lane;
+    if (r < M) {
+        __nv_bfloat16* p = base + static_cast<int64_t>(r) * ld + c0;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            if (c0 + j < N) p[j] = __float2bfloat16_rn(v[j]);
+    }
+}
+
+__device__ __forceinline__ void st_f32(float* base, int64_t ld, bool vec, int r0, int c0, int lane,
+                                       const float (&v)[CH], int M, int N) {
+    if (vec && c0 + CH <= N) {
+        float w[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) w[j] = v[j];
+        quad_transpose(w, lane);
+        const int rq = r0 + (lane & ~3);
+        float* p = base + static_cast<int64_t>(rq) * ld + c0 + 4 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (rq + j < M)
+                *reinterpret_cast<float4*>(p + j * ld) = make_float4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        return;
+    }
+    const int r = r0 + lane;
+    if (r < M) {
+        float* p = base + static_cast<int64_t>(r) * ld + c0;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            if (c0 + j < N) p[j] = v[j];
+    }
+}
+
+// A matrix of the given element type, or of bf16 parts (part > 0).
+__device__ __forceinline__ void st_mat(const OpsMat& m, int r0, int c0, int lane, const float (&v)[CH], int M, int N) {
+    if (m.type == ELEM_F32) {
+        st_f32(static_cast<float*>(m.p), m.ld, m.vec, r0, c0, lane, v, M, N);
+        return;
+    }
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(m.p);
+    st_bf16(p, m.ld, m.vec, r0, c0, lane, v, M, N);
+    if (m.part > 0) {
+        float w[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) w[j] = bf16_rest(v[j]);
+        st_bf16(p + m.part, m.ld, m.vec, r0, c0, lane, w, M, N);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) w[j] = bf16_rest(w[j]);
+        st_bf16(p + 2 * m.part, m.ld, m.vec, r0, c0, lane, w, M, N);
+    }
+}
+
+__device__ __forceinline__ void ld_mat(const OpsMat& m, int r0, int c0, int lane, float (&x)[CH], int M, int N) {
+    if (m.vec && c0 + CH <= N) {
+        if (m.type == ELEM_BF16) {
+            const bool odd = lane & 1;
+            const int ra = r0 + (lane & ~1);
+            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(m.p) + static_cast<int64_t>(ra) * m.ld + c0 +
+                                     8 * odd;
+            uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
+            if (ra < M) a = *reinterpret_cast<const uint4*>(p);
+            if (ra + 1 < M) b = *reinterpret_cast<const uint4*>(p + m.ld);
+            const uint32_t d0[4] = {a.x, a.y, a.z, a.w}, d1[4] = {b.x, b.y, b.z, b.w};
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t recv = __shfl_xor_sync(kFullMask, odd ? d0[k] : d1[k], 1);
+                w[k] = odd ? recv : d0[k];
+                w[4 + k] = odd ? d1[k] : recv;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 f = unpack_bf16x2(w[k]);
+                x[2 * k] = f.x;
+                x[2 * k + 1] = f.y;
+            }
+        } else {
+            const int rq = r0 + (lane & ~3);
+            const float* p = static_cast<const float*>(m.p) + static_cast<int64_t>(rq) * m.ld + c0 + 4 * (lane & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (rq + j < M) q = *reinterpret_cast<const float4*>(p + j * m.ld);
+                x[4 * j] = q.x;
+                x[4 * j + 1] = q.y;
+                x[4 * j + 2] = q.z;
+                x[4 * j + 3] = q.w;
+            }
+            quad_transpose(x, lane);
+        }
+        return;
+    }
+    const int r = r0 + lane;
+    const int64_t i0 = static_cast<int64_t>(r) * m.ld + c0;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        x[j] = 0.0f;
+        if (r < M && c0 + j < N)
+            x[j] = m.type == ELEM_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(m.p)[i0 + j])
+                                       : static_cast<const float*>(m.p)[i0 + j];
+    }
+}
+
+// ------------------------------------------------------- element formulas
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// act(a) and, for the backward pass, act'(a).  bf16 results take the
+// approximate exponential and reciprocal (relative error about 2^-22, far
+// below the storage rounding).
+template <bool kF32>
+__device__ __forceinline__ float act_gate(int act, float a) {
+    if (act == OPS_SILU) {
+        if (kF32) return 1.0f / (1.0f + expf(-a));
+        return rcp_approx(1.0f + ex2(-a * kLog2e));
+    }
+    return 0.5f * erfcf(-a * 0.70710678118654752f);
+}
+
+template <bool kF32>
+__device__ __forceinline__ float act_slope(int act, float a, float gate) {
+    // act(a) = a gate(a): act' = gate + a gate'
+    if (act == OPS_SILU) return gate * (1.0f + a * (1.0f - gate));
+    const float pdf = 0.3989422804014327f * (kF32 ? expf(-0.5f * a * a) : ex2(-0.5f * kLog2e * a * a));
+    return gate + a * pdf;
+}
+
+// ------------------------------------------------------- accumulator source
+
+// The finished accumulator of a warp's 32 rows: TMEM for a whole tile, TMEM
+// plus the other units' stored partial sums, in K order, for a split one.
+struct Acc {
+    uint32_t taddr;
+    const float* parts;  // slot of part 0, this warp's first row
+    int split, mine;
+
+    __device__ __forceinline__ void load(int tcol, float (&v)[CH], int lane) const {
+        __syncwarp();
+        tmem_ld16(taddr + static_cast<uint32_t>(tcol), v);
+        if (split > 1) {
+            float s[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) s[j] = 0.0f;
+            for (int i = 0; i < split; ++i) {
+                if (i == mine) {
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) s[j] += v[j];
+                } else {
+                    const float* p = parts + i * kOpsSlotFloats + static_cast<int64_t>(tcol) * BM + lane;
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) s[j] += __ldcg(p + j * BM);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < CH; ++j) v[j] = s[j];
+        }
+    }
+};
+
+// ------------------------------------------------------- epilogues
+// h: column half of this warp's group; r0: its first row.
+
+template <bool kF32>
+__device__ __forceinline__ void epi_store(const OpsProblem& P, const Acc& acc, const Unit& u, int half, int r0,
+                                          int lane) {
+#pragma unroll 1
+    for (int kc = 0; kc < BN / 2 / CH; ++kc) {
+        const int tcol = half * (BN / 2) + kc * CH, c0 = u.tn * BN + tcol;
+        if (c0 >= P.N) break;
+        float add[CH];
+        if (P.in0.p) ld_mat(P.in0, r0, c0, lane, add, P.M, P.N);
+        float v[CH];
+        acc.load(tcol, v, lane);
+        if (P.in0.p) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) v[j] += add[j];
+        }
+        st_mat(P.out0, r0, c0, lane, v, P.M, P.N);
+    }
+}
+
+template <bool kF32>
+__device__ __forceinline__ void epi_gate(const OpsProblem& P, const Acc& acc, const Unit& u, int half, int r0,
+                                         int lane) {
+#pragma unroll 1
+    for (int kc = 0; kc < BN / 4 / CH; ++kc) {
+        const int tcol = half * (BN / 4) + kc * CH, c0 = u.tn * (BN / 2) + tcol;
+        if (c0 >= P.N) break;
+        float a[CH], w[CH];
+        acc.load(tcol, a, lane);
+        acc.load(BN / 2 + tcol, w, lane);
+        if (P.out1.p) {
+            st_mat(P.out1, r0, c0, lane, a, P.M, P.N);
+            st_mat(P.out2, r0, c0, lane, w, P.M, P.N);
+        }
+#pragma unroll
+        for (int j = 0; j < CH; ++j) w[j] *= a[j] * act_gate<kF32>(P.act, a[j]);
+        st_mat(P.out0, r0, c0, lane, w, P.M, P.N);
+    }
+}
+
+template <bool kF32>
+__device__ __forceinline__ void epi_dgate(const OpsProblem& P, const Acc& acc, const Unit& u, int half, int r0,
+                                          int lane) {
+#pragma unroll 1
+    for (int kc = 0; kc < BN / 2 / CH; ++kc) {
+        const int tcol = half * (BN / 2) + kc * CH, c0 = u.tn * BN + tcol;
+        if (c0 >= P.N) break;
+        float a[CH], w[CH], v[CH];
+        ld_mat(P.in0, r0, c0, lane, a, P.M, P.N);
+        ld_mat(P.in1, r0, c0, lane, w, P.M, P.N);
+        acc.load(tcol, v, lane);
+        float h[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const float g = act_gate<kF32>(P.act, a[j]);
+            const float s = act_slope<kF32>(P.act, a[j], g);
+            const float f = a[j] * g;
+            h[j] = f * w[j];             // the forward pass's h, from the stored a and u
+            w[j] = v[j] * w[j] * s;      // da
+            a[j] = v[j] * f;             // du
+        }
+        st_mat(P.out0, r0, c0, lane, w, P.M, P.N);
+        st_mat(P.out1, r0, c0, lane, a, P.M, P.N);
+        st_mat(P.out2, r0, c0, lane, h, P.M, P.N);
+    }
+}
+
+template <bool kF32>
+__device__ __forceinline__ void epi_logits(const OpsProblem& P, const Acc& acc, const Unit& u, int half, int r0,
+                                           int lane) {
+    const int cb = u.tn * BN + half * (BN / 2);
+    const int r = r0 + lane;
+    const float ninf = __int_as_float(0xff800000);
+    float m = ninf;
+#pragma unroll 1
+    for (int kc = 0; kc < BN / 2 / CH; ++kc) {
+        const int c0 = cb + kc * CH;
+        if (c0 >= P.N) break;
+        float v[CH];
+        acc.load(half * (BN / 2) + kc * CH, v, lane);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) m = fmaxf(m, c0 + j < P.N ? v[j] : ninf);
+    }
+    int64_t t = -1;
+    if (r < P.M) t = P.targets[r] - cb;
+    const int tl = t >= 0 && t < BN / 2 ? static_cast<int>(t) : -1;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int kc = 0; kc < BN / 2 / CH; ++kc) {
+        const int c0 = cb + kc * CH;
+        if (c0 >= P.N) break;
+        float v[CH];
+        acc.load(half * (BN / 2) + kc * CH, v, lane);
+        if (tl >= 0 && tl / CH == kc) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                if (tl % CH == j && c0 + j < P.N) P.target_logit[r] = v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            v[j] = kF32 ? expf(v[j] - m) : ex2((v[j] - m) * kLog2e);
+            if (c0 + j < P.N) s += v[j];
+        }
+        if (P.out0.p) st_mat(P.out0, r0, c0, lane, v, P.M, P.N);
+    }
+    if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] = make_float2(m, s);
+}
+
+template <int kKind, bool kF32>
+__global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_constant__ OpsLaunch L) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&S.full[s], 1);
+            mbar_init(&S.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&S.acc_full[b], 1);
+            mbar_init(&S.acc_empty[b], kPair * kEpiWarps);
+        }
+        for (int i = 0; i < kTileRing; ++i) {
+            mbar_init(&S.tile_full[i], 1);
+            mbar_init(&S.tile_empty[i], kTileReaders);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem_base)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = S.tmem_base;
+    const int rank = static_cast<int>(cluster_rank());
+    const int total = L.total_units;
+    // programmatic dependent launch: global memory only after the previous
+    // kernel has completed
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp < kEpiWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------ TMA producer
+            uint32_t stage = 0, phase = 0, n_issued = 0;
+            bool ok = true;
+            const uint32_t full0 = mapa(saddr(&S.full[0]), 0);
+            int t_next = rank == 0 ? atomicAdd(L.counter, 1) : 0;
+            for (int k = 0; ok; ++k) {
+                int t;
+                if (rank == 0) {
+                    const int slot = k % kTileRing;
+                    const uint32_t ph = static_cast<uint32_t>(k / kTileRing) & 1u;
+                    if (!mbar_wait<true>(&S.tile_empty[slot], ph ^ 1u, &g_ops_status)) {
+                        ok = false;
+                        break;
+                    }
+                    t = t_next < total ? t_next : total;
+                    if (t < total) t_next = atomicAdd(L.counter, 1);
+                    S.tile_slot[slot] = t;
+                    st_cluster_u32(mapa(saddr(&S.tile_slot[slot]), 1), t);
+                    mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 0));
+                    mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 1));
+                } else {
+                    t = wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
+                    release_tile(S.tile_empty, k);
+                }
+                if (t >= total) {
+                    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+                    break;
+                }
+                const Unit u = decode_unit(L, t);
+                const OpsProblem& P = L.p[u.p];
+                const int slabs = P.slabs;
+                const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
+                const int a_row = (2 * u.tm + rank) * BM;
+                const int b_col = P.dual ? u.tn * (BN / 2) : u.tn * BN + rank * (BN / kPair);
+                int seg = u.kb0 / slabs, within = (u.kb0 - seg * slabs) * SLAB_K;
+                const int seg_end = slabs * SLAB_K;
+                const CUtensorMap *ma = nullptr, *mb = nullptr;
+                int pa = 0, pb = 0;
+                bool fresh = true;
+                for (int kb = u.kb0; kb < u.kb1; ++kb) {
+                    if (fresh) {
+                        const uint32_t sg = P.seg[seg];
+                        const int src = sg & 15;
+                        ma = &P.a[src];
+                        mb = &P.b[P.dual ? rank : src];
+                        pa = (sg >> 4) & 15;
+                        pb = sg >> 8;
+                        fresh = false;
+                    }
+                    if (!mbar_wait<false>(&S.empty[stage], phase ^ 1, &g_ops_status)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_expect_tx(&S.full[stage], STAGE_TX);
+                    ++n_issued;
+                    const uint32_t fb = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
+                    if (!a_mn) {
+                        tma_load_3d_pair(S.a[stage], ma, fb, within, a_row, pa);
+                    } else {
+                        tma_load_3d_pair(S.a[stage], ma, fb, a_row, within, pa);
+                        tma_load_3d_pair(S.a[stage] + MN_BOX_BYTES, ma, fb, a_row + 64, within, pa);
+                    }
+                    if (!b_mn) {
+                        tma_load_3d_pair(S.b[stage], mb, fb, within, b_col, pb);
+                    } else {
+                        tma_load_3d_pair(S.b[stage], mb, fb, b_col, within, pb);
+                        tma_load_3d_pair(S.b[stage] + MN_BOX_BYTES, mb, fb, b_col + 64, within, pb);
+                    }
+                    within += SLAB_K;
+                    if (within == seg_end) {
+                        within = 0;
+                        ++seg;
+                        fresh = true;
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                // let copies already issued land before the CTA can exit
+                if (rank == 0)
+                    for (uint32_t j = 1; j <= STAGES && j <= n_issued; ++j) {
+                        const uint32_t q = n_issued - j;
+                        mbar_wait<false>(&S.full[q % STAGES], (q / STAGES) & 1u, &g_ops_status);
+                    }
+            } else {
+                // the MMA's releases of the last ring round: no commit is still
+                // in flight towards this CTA when the pair leaves
+                for (int i = 0; i < STAGES && ok; ++i) {
+                    ok = mbar_wait<true>(&S.empty[stage], phase ^ 1, &g_ops_status);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ------------------------------------------------ MMA issuer (leader)
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            const uint64_t a_k = smem_desc(saddr(S.a[0]), 0, 1024), a_m = smem_desc(saddr(S.a[0]), MN_BOX_BYTES, 1024);
+            const uint64_t b_k = smem_desc(saddr(S.b[0]), 0, 1024), b_m = smem_desc(saddr(S.b[0]), MN_BOX_BYTES, 1024);
+            constexpr uint64_t step_k = (UMMA_K * 2) >> 4, step_mn = (UMMA_K * 128) >> 4;
+            for (int k = 0; ok; ++k) {
+                const int t = wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
+                release_tile(S.tile_empty, k);
+                if (t >= total) break;
+                const Unit u = decode_unit(L, t);
+                const bool a_mn = L.p[u.p].a_mn != 0, b_mn = L.p[u.p].b_mn != 0;
+                const int buf = k & 1;
+                const uint32_t use = static_cast<uint32_t>(k >> 1);
+                if (!mbar_wait<true>(&S.acc_empty[buf], (use & 1) ^ 1, &g_ops_status)) break;
+                fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
+                const uint32_t idesc = make_idesc(a_mn, b_mn);
+                const uint64_t a0 = a_mn ? a_m : a_k, b0 = b_mn ? b_m : b_k;
+                const uint64_t a_step = a_mn ? step_mn : step_k, b_step = b_mn ? step_mn : step_k;
+                for (int kb = u.kb0; kb < u.kb1; ++kb) {
+                    if (!mbar_wait<false>(&S.full[stage], phase, &g_ops_status)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint64_t ad = a0 + static_cast<uint64_t>(stage) * (OP_BYTES >> 4);
+                    const uint64_t bd = b0 + static_cast<uint64_t>(stage) * (OP_BYTES >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < SLAB_K / UMMA_K; ++kk)
+                        umma_bf16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb != u.kb0 || kk) ? 1u : 0u);
+                    umma_commit_pair(&S.empty[stage], kPairMask);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                // also on failure: covers every MMA issued so far
+                umma_commit_pair(&S.acc_full[buf], kPairMask);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        // ------------------------------------------------ epilogue
+        const int q = warp & 3;                   // TMEM lane quarter this warp may access
+        const int half = (warp - kEpiWarp0) / 4;  // column half
+        for (int k = 0;; ++k) {
+            const int t = wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa(saddr(&S.tile_empty[k % kTileRing]), 0));
+            if (t >= total) break;
+            const Unit u = decode_unit(L, t);
+            const OpsProblem& P = L.p[u.p];
+            const int buf = k & 1;
+            const uint32_t use = static_cast<uint32_t>(k >> 1);
+            const int r0 = (2 * u.tm + rank) * BM + q * 32;
+            // rows, or this group's columns (of every pair of matrices, for
+            // the dual tile), lie outside the matrix
+            const int c_first = kKind == OPS_GATE ? u.tn * (BN / 2) + half * (BN / 4) : u.tn * BN + half * (BN / 2);
+            bool active = r0 < P.M && c_first < P.N;
+            const bool ready = mbar_wait<true>(&S.acc_full[buf], use & 1, &g_ops_status);
+            fence_after();
+            active = active && ready;
+            Acc acc{tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN), nullptr, 1, 0};
+            if (active && u.split > 1) {
+                // store this unit's partial sum [column][row]; the last unit of
+                // the tile adds them up
+                float* slot = L.partials + static_cast<int64_t>(u.slot) * kOpsSlotFloats +
+                              static_cast<int64_t>(rank) * BN * BM + q * 32;
+                constexpr int kBlocks = kKind == OPS_GATE ? 2 : 1;
+#pragma unroll 1
+                for (int b = 0; b < kBlocks; ++b)
+#pragma unroll 1
+                    for (int kc = 0; kc < BN / 2 / CH / kBlocks; ++kc) {
+                        const int cc = half * (BN / 2 / kBlocks) + kc * CH;  // column inside its block
+                        if (u.tn * (BN / kBlocks) + cc >= P.N) break;
+                        const int tcol = b * (BN / 2) + cc;
+                        float v[CH];
+                        acc.load(tcol, v, lane);
+                        float* p = slot + static_cast<int64_t>(u.part) * kOpsSlotFloats +
+                                   static_cast<int64_t>(tcol) * BM + lane;
+#pragma unroll
+                        for (int j = 0; j < CH; ++j) __stcg(p + j * BM, v[j]);
+                    }
+                __threadfence();
+                __syncwarp();
+                int before = 0;
+                if (lane == 0)
+                    before = atomicAdd(&L.tail_count[u.tail * kOpsTailCounts + rank * kEpiWarps + (warp - kEpiWarp0)],
+                                       1);
+                before = __shfl_sync(kFullMask, before, 0);
+                active = before == u.split - 1;
+                __threadfence();
+                acc.parts = slot;
+                acc.split = u.split;
+                acc.mine = u.part;
+            }
+            if (active) {
+                if constexpr (kKind == OPS_STORE) epi_store<kF32>(P, acc, u, half, r0, lane);
+                else if constexpr (kKind == OPS_GATE) epi_gate<kF32>(P, acc, u, half, r0, lane);
+                else if constexpr (kKind == OPS_DGATE) epi_dgate<kF32>(P, acc, u, half, r0, lane);
+                else epi_logits<kF32>(P, acc, u, half, r0, lane);
+            }
+            // every tcgen05.ld of the accumulator has completed (wait::ld): the
+            // release is relaxed, so it does not wait for this warp's stores
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa(saddr(&S.acc_empty[buf]), 0));
+        }
+    }
+
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+using Kernel = void (*)(OpsLaunch);
+
+Kernel kernel_of(int32_t kind, bool f32) {
+    switch (kind) {
+        case OPS_STORE: return ops_gemm_kernel<OPS_STORE, false>;
+        case OPS_GATE: return f32 ? ops_gemm_kernel<OPS_GATE, true> : ops_gemm_kernel<OPS_GATE, false>;
+        case OPS_DGATE: return f32 ? ops_gemm_kernel<OPS_DGATE, true> : ops_gemm_kernel<OPS_DGATE, false>;
+        default: return f32 ? ops_gemm_kernel<OPS_LOGITS, true> : ops_gemm_kernel<OPS_LOGITS, false>;
+    }
+}
+
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+
+}  // namespace
+
+cudaError_t ops_pairs(int* pairs) {
+    static PerDevice cache;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    // shared-memory attribute of every instance and the resident pairs, once
+    // per device with that device current
+    return cache.get(dev, pairs, [&](int* out) {
+        cudaError_t r = cudaSuccess;
+        for (int kind = 0; kind < 4 && r == cudaSuccess; ++kind)
+            for (int f = 0; f < 2 && r == cudaSuccess; ++f)
+                r = cudaFuncSetAttribute(kernel_of(kind, f != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kSmemBytes));
+        if (r != cudaSuccess) return r;
+        int sms = 0;
+        r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (r != cudaSuccess) return r;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kPair;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(sms / kPair * kPair);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        r = cudaOccupancyMaxActiveClusters(&n, kernel_of(OPS_STORE, false), &cfg);
+        if (r != cudaSuccess) return r;
+        *out = n > 0 ? n : sms / kPair;
+        return cudaSuccess;
+    });
+}
+
+// Work units.  A launch ends when its last unit does: with T equal tiles on P
+// pairs the last round leaves P - T mod P pairs idle.  The tiles of that round
+// are split into S K ranges, S minimising ceil(rem S / P) / S (the time of the
+// round in tiles) plus the cost of storing and adding the partial sums, about
+// kSplitCost slabs per range.  In a launch of several products the longest
+// tiles come first (the caller's order), a product whose tiles are long
+// against the launch's share per pair is split throughout, and only the last
+// product's last round is split as above.
+void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
+    constexpr double kSplitCost = 10.0;  // slabs
+    constexpr int kMinSlabs = 8;         // per range
+    double work = 0.0;
+    for (int i = 0; i < l.n; ++i)
+        work += static_cast<double>(l.p[i].tiles_m) * l.p[i].tiles_n * l.p[i].slabs * l.p[i].nseg;
+    const double share = work / pairs;  // slabs per pair
+    int unit = 0, tail = 0, slot = 0;
+    for (int i = 0; i < l.n; ++i) {
+        OpsProblem& p = l.p[i];
+        const int tiles = p.tiles_m * p.tiles_n, total = p.slabs * p.nseg;
+        int rem = 0, best = 1;
+        if (l.n == 1) {
+            rem = tiles % pairs;
+            double cost = total;
+            for (int s = 2; s <= 32 && rem > 0 && total / s >= kMinSlabs; ++s) {
+                const double c = static_cast<double>((static_cast<int64_t>(rem) * s + pairs - 1) / pairs) *
+                                 (static_cast<double>(total) / s + kSplitCost);
+                if (c < cost) {
+                    cost = c;
+                    best = s;
+                }
+            }
+        } else if (total > 0.25 * share) {
+            rem = tiles;
+            best = static_cast<int>(4.0 * total / share) + 1;
+            if (best > 32) best = 32;
+            if (best > total / kMinSlabs) best = total / kMinSlabs;
+        }
+        while (best > 1 && (static_cast<int64_t>(rem) * best > slots - slot || rem > tails - tail)) --best;
+        if (best <= 1 || rem > tails - tail) {
+            rem = 0;
+            best = 1;
+        }
+        p.whole = tiles - rem;
+        p.split = best;
+        p.unit_begin = unit;
+        p.tail_begin = tail;
+        p.slot_begin = slot;
+        unit += p.whole + rem * best;
+        tail += rem;
+        slot += rem * best;
+    }
+    l.total_units = unit;
+}
+
+cudaError_t ops_read_status(int32_t* v) {
+    const int32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(v, g_ops_status, sizeof(*v));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_ops_status, &zero, sizeof(zero));
+    return e;
+}
+
+cudaError_t launch_ops_gemm(const OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s) {
+    if (l.total_units <= 0) return cudaSuccess;
+    int pairs = 0;
+    const cudaError_t e = ops_pairs(&pairs);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((l.total_units < pairs ? l.total_units : pairs) * kPair);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel_of(kind, f32), l);
+}
+
+}  // namespace dmuon

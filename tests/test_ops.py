@@ -1,0 +1,572 @@
+"""Layer norm, gated feed-forward block and vocabulary loss.
+
+CPU: argument refusals, workspace queries.  GPU: every output against a plain
+fp64 implementation, element by element, within bounds that follow from the
+stated roundings:
+
+- a stored bf16 value is off by at most U = 2^-8 of itself (fp32: 2^-24);
+- a product that reads operands rounded to bf16 on the way (h, da, du, dz) is
+  off by at most U per rounded operand of sum |a| |b|;
+- fp32 accumulation of K terms adds at most (K + 64) 2^-23 of sum |a| |b|
+  (2^-23, not 2^-24, per addition: the tensor cores may truncate), six times
+  the terms where fp32 matrices run as bf16 parts, whose dropped products stay
+  below 2^-22 of sum |a| |b|;
+- exponentials, logarithms and activations are good to 2^-18 of themselves.
+"""
+import math
+
+import pytest
+import torch
+
+import matrix_orthogonalising_optimizer_gb300 as pkg
+from matrix_orthogonalising_optimizer_gb300 import _lib
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+FN = 2.0 ** -18
+TINY = 1e-30
+
+
+def acc(K, dt):
+    """Relative accumulation bound of a K-deep product."""
+    return (K + 64) * 2.0 ** -23 if dt == torch.bfloat16 else (6 * K + 64) * 2.0 ** -23 + 2.0 ** -22
+
+
+def within(got, want, bound, what):
+    assert got.shape == want.shape, what
+    d = (got.double() - want).abs()
+    bad = ~(d <= bound + TINY)
+    if bad.any():
+        i = int(bad.flatten().nonzero()[0])
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off; first {i}: got "
+                             f"{float(got.flatten()[i])}, want {float(want.flatten()[i])}, bound "
+                             f"{float((bound + 0 * want).flatten()[i])}")
+
+
+def randn(g, *shape, std=1.0, dt=torch.bfloat16):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dt)
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ---------------------------------------------------------------- refusals (no GPU)
+
+P16 = 1 << 20  # an aligned address that no refused call touches
+
+
+def err(lib):
+    return lib.dmuon_last_error().decode()
+
+
+def test_layer_norm_refusals(lib):
+    def fwd(x=P16, w=P16, y=P16, mean=P16, rows=4, cols=8, dtype=_lib.BF16, eps=1e-5):
+        return lib.dmuon_layer_norm_forward(x, w, None, y, mean, mean, rows, cols, dtype, eps, None)
+
+    assert fwd(rows=-1) == _lib.ERR_INVALID_ARG and "rows" in err(lib)
+    assert fwd(cols=0) == _lib.ERR_INVALID_ARG
+    assert fwd(cols=(1 << 20) + 1) == _lib.ERR_INVALID_ARG
+    assert fwd(dtype=2) == _lib.ERR_UNSUPPORTED_DTYPE
+    assert fwd(eps=-1.0) == _lib.ERR_INVALID_ARG and "eps" in err(lib)
+    assert fwd(eps=float("nan")) == _lib.ERR_INVALID_ARG
+    assert fwd(x=None) == _lib.ERR_INVALID_ARG and "x is NULL" in err(lib)
+    assert fwd(y=P16 + 8) == _lib.ERR_ALIGN
+    assert fwd(w=P16 + 2) == _lib.ERR_ALIGN
+    assert fwd(mean=P16 + 2) == _lib.ERR_ALIGN
+    assert fwd(rows=0, x=None) == _lib.OK
+
+    need = lib.dmuon_layer_norm_workspace_bytes(4, 8, _lib.BF16)
+    assert need >= 4 * 8 * 2
+
+    def bwd(ws=P16, n=need, dx=P16, rstd=P16):
+        return lib.dmuon_layer_norm_backward(P16, P16, None, P16, rstd, dx, P16, P16, 4, 8, _lib.BF16, ws, n, None)
+
+    assert bwd(ws=None) == _lib.ERR_NO_WORKSPACE
+    assert bwd(ws=P16 + 16) == _lib.ERR_ALIGN
+    assert bwd(n=need - 1) == _lib.ERR_WORKSPACE_TOO_SMALL
+    assert bwd(dx=None) == _lib.ERR_INVALID_ARG
+    assert bwd(rstd=None) == _lib.ERR_INVALID_ARG
+    assert lib.dmuon_layer_norm_workspace_bytes(-1, 8, _lib.BF16) == 0
+
+
+def test_gated_ffn_refusals(lib):
+    need = lib.dmuon_gated_ffn_workspace_bytes(4, 64, 128, _lib.BF16, 0)
+    back = lib.dmuon_gated_ffn_workspace_bytes(4, 64, 128, _lib.BF16, 1)
+    assert 0 < need < back
+    # fp32 operands are packed into bf16 parts
+    assert lib.dmuon_gated_ffn_workspace_bytes(4, 64, 128, _lib.FP32, 0) > need + 6 * 3 * 64 * 128
+
+    def fwd(x=P16, y=P16, gate=P16, up=P16, tokens=4, dim=64, hidden=128, dtype=_lib.BF16, act=0, ws=P16, n=need):
+        return lib.dmuon_gated_ffn_forward(x, P16, P16, P16, y, gate, up, tokens, dim, hidden, dtype, act, ws, n, None)
+
+    for bad in (dict(tokens=-1), dict(tokens=(1 << 24) + 1), dict(dim=0), dict(hidden=0), dict(hidden=1 << 21)):
+        assert fwd(**bad) == _lib.ERR_INVALID_ARG
+    assert fwd(dtype=7) == _lib.ERR_UNSUPPORTED_DTYPE
+    assert fwd(act=2) == _lib.ERR_INVALID_ARG and "activation" in err(lib)
+    assert fwd(up=None) == _lib.ERR_INVALID_ARG and "together" in err(lib)
+    assert fwd(x=None) == _lib.ERR_INVALID_ARG
+    assert fwd(y=P16 + 4) == _lib.ERR_ALIGN
+    assert fwd(ws=None) == _lib.ERR_NO_WORKSPACE
+    assert fwd(ws=P16 + 128) == _lib.ERR_ALIGN
+    assert fwd(n=need - 1) == _lib.ERR_WORKSPACE_TOO_SMALL
+    assert fwd(tokens=0, ws=None) == _lib.OK
+
+    def bwd(dy=P16, dwd=P16, ws=P16, n=back):
+        return lib.dmuon_gated_ffn_backward(dy, P16, P16, P16, P16, P16, P16, P16, P16, P16, dwd, 4, 64, 128,
+                                            _lib.BF16, 0, ws, n, None)
+
+    assert bwd(dy=None) == _lib.ERR_INVALID_ARG
+    assert bwd(dwd=P16 + 2) == _lib.ERR_ALIGN
+    assert bwd(n=need) == _lib.ERR_WORKSPACE_TOO_SMALL
+
+
+def test_vocab_loss_refusals(lib):
+    def need(tokens=300, dim=64, vocab=1000, dtype=_lib.BF16, grad=1, budget=0):
+        return lib.dmuon_vocab_loss_workspace_bytes(tokens, dim, vocab, dtype, grad, budget)
+
+    assert need(grad=0) < need()
+    # a budget bounds the logits held at once; one piece of 256 tokens is the least
+    assert need(tokens=100000, budget=1) < need(tokens=100000)
+    assert need(tokens=200000, budget=1) == need(tokens=100000, budget=1)
+
+    def call(x=P16, targets=P16, coef=None, loss=P16, dx=P16, dw=P16, tokens=300, dim=64, vocab=1000, dtype=_lib.BF16,
+             ws=P16, n=None):
+        return lib.dmuon_vocab_loss(x, P16, targets, coef, -100, loss, P16, dx, dw, tokens, dim, vocab, dtype, 0, ws,
+                                    need() if n is None else n, None)
+
+    for bad in (dict(tokens=-1), dict(dim=0), dict(vocab=0), dict(vocab=(1 << 22) + 1), dict(dw=None), dict(dx=None),
+                dict(x=None), dict(targets=None), dict(loss=None)):
+        assert call(**bad) == _lib.ERR_INVALID_ARG, bad
+    assert call(dtype=-1) == _lib.ERR_UNSUPPORTED_DTYPE
+    assert call(targets=P16 + 4) == _lib.ERR_ALIGN
+    assert call(dw=P16 + 8) == _lib.ERR_ALIGN
+    assert call(coef=P16 + 2) == _lib.ERR_ALIGN
+    assert call(ws=None) == _lib.ERR_NO_WORKSPACE
+    assert call(n=need() - 1) == _lib.ERR_WORKSPACE_TOO_SMALL
+
+
+def test_bindings_refuse_host_tensors():
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.layer_norm(x)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.gated_ffn(x, x, x, x)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.vocab_loss(x, x, torch.zeros(4, dtype=torch.int64))
+
+
+@pytest.mark.gpu
+def test_bindings_refuse_mismatches():
+    x = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(32, 16, dtype=torch.bfloat16, device="cuda")
+    d = torch.zeros(16, 32, dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError, match="shape"):
+        pkg.layer_norm(x, torch.zeros(8, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        pkg.layer_norm(x.t())
+    with pytest.raises(_lib_error(), match="dtype"):
+        pkg.layer_norm(x.half())
+    with pytest.raises(ValueError, match="torch.bfloat16"):
+        pkg.gated_ffn(x, w.float(), w, d)
+    with pytest.raises(ValueError, match="w_down"):
+        pkg.gated_ffn(x, w, w, w)
+    with pytest.raises(ValueError, match="activation"):
+        pkg.gated_ffn(x, w, w, d, activation="relu")
+    with pytest.raises(ValueError, match="int64"):
+        pkg.vocab_loss(x, w, t.int())
+    with pytest.raises(_lib_error(), match="needed"):
+        pkg.vocab_loss(x, w, t, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def _lib_error():
+    return _lib.DmuonError
+
+
+# ---------------------------------------------------------------- layer norm
+
+def norm_reference(x, w, b, eps):
+    x = x.double()
+    mean = x.mean(-1)
+    c = x - mean[..., None]
+    rstd = ((c * c).mean(-1) + eps) ** -0.5
+    n = c * rstd[..., None]
+    y = n * (w.double() if w is not None else 1.0) + (b.double() if b is not None else 0.0)
+    return y, mean, rstd, n
+
+
+NORM_SHAPES = [(1, 1), (1, 768), (3, 7), (5, 64), (2, 1000), (37, 1001), (700, 96), (1300, 2048), (3, 4096),
+               (640, 4100), (20, 8192), (9, 12000), (33, 16384), (5, 16400), (3, 40001)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES)
+def test_layer_norm(rows, cols, dtype):
+    dt = DT[dtype]
+    g = gen(rows * 100003 + cols)
+    x = (torch.randn(rows, cols, generator=g, device="cuda") * 2 + 3 * torch.randn(rows, 1, generator=g, device="cuda"))
+    x = x.to(dt)
+    w, b = randn(g, cols, dt=dt), randn(g, cols, dt=dt)
+    dy = randn(g, rows, cols, dt=dt)
+    eps = 1e-5
+    y, mean, rstd = pkg.layer_norm(x, w, b, eps=eps)
+    ey, em, er, n = norm_reference(x, w, b, eps)
+    # statistics in fp32: a sum of `cols` terms, tree-wise (at most cols/32 + 64 deep)
+    k = (cols / 32 + 64) * 2.0 ** -24
+    xabs = x.double().abs().mean(-1)
+    within(mean, em, k * xabs + 2.0 ** -23 * em.abs(), "mean")
+    # rstd: relative error of the sum of squares, and of the mean's error squared
+    within(rstd, er, er * (k + 4 * 2.0 ** -23 + (k * xabs * er) ** 2), "rstd")
+    wd = w.double().abs()
+    within(y, ey, U[dt] * ey.abs() + 2 * (k + 2.0 ** -21) * (n.abs() + (xabs * er)[:, None]) * wd + 2.0 ** -22
+           * b.double().abs(), "y")
+
+    dx, dw, db = pkg.layer_norm_backward(dy, x, w, mean, rstd)
+    # the backward pass's own formula from the fp32 statistics it is given
+    n = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    gr = dy.double() * w.double()
+    m1, m2 = gr.mean(1, keepdim=True), (gr * n).mean(1, keepdim=True)
+    r = rstd.double()[:, None]
+    edx = r * (gr - m1 - n * m2)
+    nerr = (x.double().abs() + mean.double().abs()[:, None]) * r * 2.0 ** -23  # error of n from x - mean
+    scale = r * (gr.abs() + gr.abs().mean(1, keepdim=True) + n.abs() * (gr * n).abs().mean(1, keepdim=True))
+    within(dx, edx, U[dt] * edx.abs() + 2 * (k + 2.0 ** -21) * scale + 2 * r * nerr * (gr * n).abs().mean(1, True)
+           + 2 * r * n.abs() * (gr.abs() * nerr).mean(1, True), "dx")
+    kr = (rows + 64) * 2.0 ** -24
+    edw, edb = (dy.double() * n).sum(0), dy.double().sum(0)
+    within(dw, edw, U[dt] * edw.abs() + ((kr + 2.0 ** -21) * (dy.double() * n).abs()
+                                         + dy.double().abs() * nerr).sum(0), "dweight")
+    within(db, edb, U[dt] * edb.abs() + kr * dy.double().abs().sum(0), "dbias")
+
+
+@pytest.mark.gpu
+def test_layer_norm_without_weight_and_constant_rows():
+    x = torch.full((3, 50), 7.25, device="cuda")
+    x[1] = 0
+    y, mean, rstd = pkg.layer_norm(x, eps=1e-5)
+    assert (y == 0).all() and (mean == x[:, 0]).all()
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
+    dy = torch.randn(3, 50, device="cuda")
+    dx, dw, db = pkg.layer_norm_backward(dy, x, None, mean, rstd)
+    want = rstd[:, None] * (dy - dy.mean(1, keepdim=True))
+    assert torch.allclose(dx, want, atol=1e-3) and (dw == 0).all()
+    # a large common offset leaves the variance exact to the rounding of x
+    x = 4096.0 + torch.arange(64, device="cuda").float().repeat(2, 1)
+    _, mean, rstd = pkg.layer_norm(x, eps=0.0)
+    assert torch.allclose(rstd, torch.full_like(rstd, (64 * 64 - 1) / 12.0) ** -0.5, rtol=1e-6)
+    # no rows: nothing forward, zero sums backward
+    e = torch.empty(0, 24, device="cuda")
+    y, mean, rstd = pkg.layer_norm(e)
+    dx, dw, db = pkg.layer_norm_backward(e, e, None, mean, rstd)
+    assert y.shape == (0, 24) and dx.shape == (0, 24) and not dw.any() and not db.any()
+    # one column: the deviation is zero
+    y, _, _ = pkg.layer_norm(torch.randn(4, 1, device="cuda"), torch.ones(1, device="cuda"),
+                             torch.full((1,), 0.5, device="cuda"))
+    assert (y == 0.5).all()
+
+
+# ---------------------------------------------------------------- gated block
+
+def act64(a, name):
+    """act(a), act'(a) and a bound on the terms act' is made of."""
+    if name == "silu":
+        s = torch.sigmoid(a)
+        return a * s, s * (1 + a * (1 - s)), s * (1 + a.abs())
+    p = torch.special.ndtr(a)
+    pdf = torch.exp(-a * a / 2) / math.sqrt(2 * math.pi)
+    return a * p, p + a * pdf, p + a.abs() * pdf
+
+
+def ffn_inputs(n, d, f, dt, seed):
+    g = gen(seed)
+    return (randn(g, n, d, dt=dt), randn(g, f, d, std=d ** -0.5, dt=dt), randn(g, f, d, std=d ** -0.5, dt=dt),
+            randn(g, d, f, std=f ** -0.5, dt=dt), randn(g, n, d, dt=dt))
+
+
+FFN_SHAPES = [(1, 64, 128), (1, 1, 1), (2, 72, 200), (17, 128, 96), (129, 64, 257), (257, 200, 384), (300, 101, 333),
+              (512, 256, 768), (31, 2048, 512), (5, 64, 5000), (1000, 520, 264), (64, 4096, 64)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,d,f", FFN_SHAPES)
+def test_gated_ffn(n, d, f, dtype):
+    dt = DT[dtype]
+    act = "gelu" if (n + d + f) % 2 else "silu"
+    x, wg, wu, wd, dy = ffn_inputs(n, d, f, dt, n * 7 + d * 3 + f)
+    y, gate, up = pkg.gated_ffn(x, wg, wu, wd, activation=act, save=True)
+    assert torch.equal(y, pkg.gated_ffn(x, wg, wu, wd, activation=act))
+    X, G, UP, D, DY = (t.double() for t in (x, wg, wu, wd, dy))
+    u = U[dt]
+    ea, eu = X @ G.T, X @ UP.T
+    da_, du_ = acc(d, dt) * (X.abs() @ G.abs().T), acc(d, dt) * (X.abs() @ UP.abs().T)
+    within(gate, ea, u * ea.abs() + da_, "gate")
+    within(up, eu, u * eu.abs() + du_, "up")
+    p, dp, dpb = act64(ea, act)
+    h = p * eu
+    # |act'| <= 1.13; the operand h is rounded once for bf16
+    op = u if dt == torch.bfloat16 else 0.0
+    herr = op * h.abs() + FN * h.abs() + 1.2 * (da_ * eu.abs() + du_ * p.abs() + da_ * du_)
+    ey = h @ D.T
+    within(y, ey, u * ey.abs() + (1 + u) * (herr @ D.abs().T + acc(f, dt) * (h.abs() @ D.abs().T)), "y")
+
+    dx, dwg, dwu, dwd = pkg.gated_ffn_backward(dy, x, wg, wu, wd, gate, up, activation=act)
+    a, uu = gate.double(), up.double()
+    p, dp, dpb = act64(a, act)
+    h = p * uu
+    dh = DY @ D
+    eh = acc(d, dt) * (DY.abs() @ D.abs())
+    da, du = dh * uu * dp, dh * p
+    hb = (op + FN) * h.abs() + TINY
+    dab = (1 + op) * eh * uu.abs() * dpb + (op + FN) * dh.abs() * uu.abs() * dpb
+    dub = (1 + op) * eh * p.abs() + (op + FN) * dh.abs() * p.abs()
+    for name, got, want, bound in (
+            ("dx", dx, da @ G + du @ UP, dab @ G.abs() + dub @ UP.abs()
+             + acc(2 * f, dt) * (da.abs() @ G.abs() + du.abs() @ UP.abs())),
+            ("dw_gate", dwg, da.T @ X, dab.T @ X.abs() + acc(n, dt) * (da.abs().T @ X.abs())),
+            ("dw_up", dwu, du.T @ X, dub.T @ X.abs() + acc(n, dt) * (du.abs().T @ X.abs())),
+            ("dw_down", dwd, DY.T @ h, DY.abs().T @ hb + acc(n, dt) * (DY.abs().T @ h.abs()))):
+        within(got, want, u * want.abs() + (1 + u) * bound, name)
+    assert pkg.ops_status() == 0
+
+
+@pytest.mark.gpu
+def test_gated_ffn_repeats_bitwise_and_leading_dimensions():
+    # shapes whose launches split tiles along K: the sums' order is fixed
+    x, wg, wu, wd, dy = ffn_inputs(96, 1024, 1536, torch.bfloat16, 5)
+    ws = torch.empty(pkg.gated_ffn_workspace(96, 1024, 1536, backward=True), dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(5):
+        ws.random_(0, 255)  # nothing is kept between calls
+        y, gate, up = pkg.gated_ffn(x, wg, wu, wd, save=True, workspace=ws)
+        out = (y, gate, up, *pkg.gated_ffn_backward(dy, x, wg, wu, wd, gate, up, workspace=ws))
+        if first is None:
+            first = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(out, first))
+    y3, gate3, _ = pkg.gated_ffn(x.view(4, 24, 1024), wg, wu, wd, save=True)
+    assert y3.shape == (4, 24, 1024) and gate3.shape == (4, 24, 1536) and torch.equal(y3.view(96, 1024), first[0])
+
+
+@pytest.mark.gpu
+def test_gated_ffn_saturated_and_empty():
+    # gates far on both sides: sigmoid reaches 0 and 1 without NaN
+    for act in ("silu", "gelu"):
+        x = torch.tensor([[300.0, 0, 0, 0, 0, 0, 0, 0], [-300.0, 0, 0, 0, 0, 0, 0, 0]], device="cuda",
+                         dtype=torch.bfloat16)
+        w = torch.zeros(8, 8, device="cuda", dtype=torch.bfloat16)
+        w[:, 0] = 1
+        eye = torch.eye(8, device="cuda", dtype=torch.bfloat16)
+        y, gate, up = pkg.gated_ffn(x, w, w, eye, activation=act, save=True)
+        assert (y[0] == torch.tensor(90000.0, device="cuda").bfloat16()).all() and (y[1] == 0).all()
+        dx, dwg, dwu, dwd = pkg.gated_ffn_backward(torch.ones_like(y), x, w, w, eye, gate, up, activation=act)
+        assert torch.isfinite(dx).all() and torch.isfinite(dwg).all()
+        assert (dx[0, 0] == 4800.0) and (dx[1] == 0).all()  # 8 (u act' + act) = 8 (300 + 300)
+    e = torch.empty(0, 8, device="cuda", dtype=torch.bfloat16)
+    y, gate, up = pkg.gated_ffn(e, w, w, eye, save=True)
+    dx, dwg, dwu, dwd = pkg.gated_ffn_backward(e, e, w, w, eye, gate, up)
+    assert y.shape == (0, 8) and not dwg.any() and not dwu.any() and not dwd.any()
+
+
+# ---------------------------------------------------------------- vocabulary loss
+
+def loss_inputs(n, d, v, dt, seed, ignore=-100, scale=1.0):
+    g = gen(seed)
+    w = randn(g, v, d, std=0.1, dt=dt)
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    x = (torch.randn(n, d, generator=g, device="cuda") * scale
+         + 8 * torch.rand(n, 1, generator=g, device="cuda") / (0.01 * d) * w[t].float()).to(dt)
+    if n > 2:
+        t[torch.rand(n, generator=g, device="cuda") < 0.2] = ignore
+        t[0], t[1] = 0, v - 1  # first and last column
+    coef = torch.rand(n, generator=g, device="cuda") / n
+    return x, w, t, coef
+
+
+def check_loss(x, w, t, coef, out, ignore=-100):
+    """Losses and, when given, gradients of a call against the fp64 formula."""
+    dt = x.dtype
+    d = x.shape[1]
+    loss, lse = out[:2]
+    X, W = x.double(), w.double()
+    z = X @ W.T
+    ez = acc(d, dt) * (X.abs() @ W.abs().T).amax(1)
+    want = torch.logsumexp(z, 1)
+    keep = t != ignore
+    idx = t.clamp(min=0)[:, None]
+    zt = z.gather(1, idx)[:, 0]
+    fl = FN * (1 + z.abs().amax(1))
+    within(lse, want, ez + fl, "lse")
+    within(loss, torch.where(keep, want - zt, torch.zeros_like(zt)), 2 * (ez + fl) * keep, "loss")
+    if len(out) == 2:
+        return
+    dx, dw = out[2:]
+    c = torch.where(keep, coef.double() if coef is not None else torch.ones_like(zt), torch.zeros_like(zt))[:, None]
+    p = torch.softmax(z, 1)
+    hot = torch.zeros_like(p).scatter_(1, idx, 1.0)
+    dz = c * (p - hot)
+    # exponentials and dz are each rounded to bf16; the logits' errors shift p by twice as much
+    op = 2 * U[dt] if dt == torch.bfloat16 else 2.0 ** -22
+    dzb = (op + U[dt] ** 2 + FN) * dz.abs() + c * p * (2 * (ez + fl)[:, None])
+    edx, edw = dz @ W, dz.T @ X
+    u = U[dt]
+    within(dx, edx, u * edx.abs() + (1 + u) * (dzb @ W.abs() + acc(w.shape[0], dt) * (dz.abs() @ W.abs())), "dx")
+    within(dw, edw, u * edw.abs() + (1 + u) * (dzb.T @ X.abs() + acc(len(t), dt) * (dz.abs().T @ X.abs())), "dweight")
+
+
+LOSS_SHAPES = [(1, 64, 1), (1, 64, 1000), (3, 1, 5), (2, 8, 129), (17, 100, 255), (130, 64, 1003), (257, 136, 640),
+               (300, 512, 10007), (5, 2048, 700), (600, 72, 128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,d,v", LOSS_SHAPES)
+def test_vocab_loss(n, d, v, dtype):
+    dt = DT[dtype]
+    x, w, t, coef = loss_inputs(n, d, v, dt, n + d + v)
+    check_loss(x, w, t, None, pkg.vocab_loss(x, w, t))
+    check_loss(x, w, t, coef, pkg.vocab_loss_grad(x, w, t, coef=coef))
+    assert pkg.ops_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_vocab_loss_in_pieces(dtype):
+    # a budget of one 256-token piece: four pieces, dW summed in fp32 across them
+    dt = DT[dtype]
+    x, w, t, coef = loss_inputs(900, 96, 777, dt, 3)
+    out = pkg.vocab_loss_grad(x, w, t, coef=coef, budget=1)
+    check_loss(x, w, t, coef, out)
+    whole = pkg.vocab_loss_grad(x, w, t, coef=coef)
+    for a, b in zip(out[:3], whole[:3]):  # rows do not depend on the piece they are in
+        assert torch.equal(a, b)
+    check_loss(x, w, t, None, pkg.vocab_loss(x, w, t, budget=1))
+
+
+@pytest.mark.gpu
+def test_vocab_loss_targets():
+    x, w, t, coef = loss_inputs(40, 64, 500, torch.bfloat16, 9)
+    # nothing counted: no loss, no gradient
+    none = torch.full_like(t, -100)
+    loss, lse, dx, dw = pkg.vocab_loss_grad(x, w, none)
+    assert not loss.any() and not dx.any() and not dw.any() and torch.isfinite(lse).all()
+    # another ignore index, and a target it shadows
+    t7 = torch.where(t == -100, torch.full_like(t, 7), t)
+    check_loss(x, w, t7, coef, pkg.vocab_loss_grad(x, w, t7, coef=coef, ignore_index=7), ignore=7)
+    # targets outside the vocabulary: NaN loss, no gradient, other rows untouched
+    bad = t.clone()
+    bad[3], bad[4] = 500, -1
+    loss, lse, dx, dw = pkg.vocab_loss_grad(x, w, bad, coef=coef)
+    assert loss[3:5].isnan().all() and not dx[3:5].any()
+    good = t.clone()
+    good[3:5] = -100
+    rest = torch.arange(40, device="cuda")
+    rest = rest[(rest != 3) & (rest != 4)]
+    ref = pkg.vocab_loss_grad(x, w, good, coef=coef)
+    assert torch.equal(loss[rest], ref[0][rest]) and torch.equal(dx, ref[2]) and torch.equal(dw, ref[3])
+    # no tokens
+    loss, lse, dx, dw = pkg.vocab_loss_grad(x[:0], w, t[:0])
+    assert loss.shape == (0,) and dx.shape == (0, 64) and not dw.any()
+
+
+@pytest.mark.gpu
+def test_vocab_loss_large_logits():
+    # logits of +-1e4: the blocks' maxima are far apart, probabilities are 0 or 1
+    x = torch.zeros(3, 64, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(1000, 64, device="cuda", dtype=torch.bfloat16)
+    x[:, 0] = 100.0
+    w[700, 0] = 100.0
+    w[13, 0] = -100.0
+    t = torch.tensor([700, 13, 5], device="cuda")
+    loss, lse, dx, dw = pkg.vocab_loss_grad(x, w, t)
+    assert torch.equal(lse, torch.full((3,), 1e4, device="cuda"))
+    assert torch.equal(loss, torch.tensor([0.0, 2e4, 1e4], device="cuda"))
+    assert not dx[0].any() and dx[1, 0] == 200.0 and dx[2, 0] == 100.0
+    assert dw[700, 0] == 200.0 and dw[13, 0] == -100.0 and dw[5, 0] == -100.0 and not dw[6].any()
+
+
+@pytest.mark.gpu
+def test_vocab_loss_repeats_bitwise():
+    x, w, t, coef = loss_inputs(70, 1024, 2049, torch.bfloat16, 21)
+    ws = torch.empty(pkg.vocab_loss_workspace(70, 1024, 2049, grad=True), dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(4):
+        ws.random_(0, 255)
+        out = pkg.vocab_loss_grad(x, w, t, coef=coef, workspace=ws)
+        if first is None:
+            first = [o.clone() for o in out]
+        assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
+# ---------------------------------------------------------------- differences, streams, graphs
+
+@pytest.mark.gpu
+def test_gradients_against_differences():
+    """fp32 chain norm -> block -> norm -> loss: the directional derivative along each
+    gradient against central differences of the loss.  Step e along a unit
+    direction: truncation O(e^2), rounding about 2^-22 |L| / e; e = 2^-6 keeps both
+    below 2^-9 of a derivative of order one."""
+    g = gen(77)
+    n, d, f, v = 48, 40, 56, 90
+    dt = torch.float32
+    p = {"x": randn(g, n, d, dt=dt), "w1": 1 + randn(g, d, std=0.1, dt=dt), "b1": randn(g, d, std=0.1, dt=dt),
+         "wg": randn(g, f, d, std=d ** -0.5, dt=dt), "wu": randn(g, f, d, std=d ** -0.5, dt=dt),
+         "wd": randn(g, d, f, std=f ** -0.5, dt=dt), "w2": 1 + randn(g, d, std=0.1, dt=dt),
+         "b2": randn(g, d, std=0.1, dt=dt), "wv": randn(g, v, d, std=0.3, dt=dt)}
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    t[5] = -100
+    coef = torch.rand(n, generator=g, device="cuda")
+
+    def forward(q, grads=False):
+        y1, m1, r1 = pkg.layer_norm(q["x"], q["w1"], q["b1"])
+        h, gate, up = pkg.gated_ffn(y1, q["wg"], q["wu"], q["wd"], save=True)
+        z = q["x"] + h
+        y2, m2, r2 = pkg.layer_norm(z, q["w2"], q["b2"])
+        if not grads:
+            return float((pkg.vocab_loss(y2, q["wv"], t)[0].double() * coef.double()).sum())
+        _, _, dy2, dwv = pkg.vocab_loss_grad(y2, q["wv"], t, coef=coef)
+        dz, dw2, db2 = pkg.layer_norm_backward(dy2, z, q["w2"], m2, r2)
+        dy1, dwg, dwu, dwd = pkg.gated_ffn_backward(dz, y1, q["wg"], q["wu"], q["wd"], gate, up)
+        dx, dw1, db1 = pkg.layer_norm_backward(dy1, q["x"], q["w1"], m1, r1)
+        return {"x": dx + dz, "w1": dw1, "b1": db1, "wg": dwg, "wu": dwu, "wd": dwd, "w2": dw2, "b2": db2, "wv": dwv}
+
+    grads = forward(p, grads=True)
+    e = 2.0 ** -6
+    for name, gr in grads.items():
+        norm = gr.double().norm()
+        direction = (gr.double() / norm).float()
+        diff = [forward({**p, name: p[name] + s * e * direction}) for s in (1, -1)]
+        slope = (diff[0] - diff[1]) / (2 * e)
+        assert abs(slope - float(norm)) <= 2.0 ** -7 * max(float(norm), 1.0), name
+
+
+@pytest.mark.gpu
+def test_operators_on_another_stream_and_in_a_graph():
+    x, wg, wu, wd, dy = ffn_inputs(130, 128, 256, torch.bfloat16, 2)
+    t = torch.randint(0, 256, (130,), device="cuda")
+    ws = torch.empty(max(pkg.gated_ffn_workspace(130, 128, 256, backward=True),
+                         pkg.vocab_loss_workspace(130, 128, 256, grad=True)), dtype=torch.uint8, device="cuda")
+
+    def work(stream=None):
+        y, m, r = pkg.layer_norm(x, stream=stream)
+        z, gate, up = pkg.gated_ffn(y, wg, wu, wd, save=True, workspace=ws, stream=stream)
+        loss, _, dz, _ = pkg.vocab_loss_grad(z, wg, t, workspace=ws, stream=stream)
+        dyy, *dws = pkg.gated_ffn_backward(dz, y, wg, wu, wd, gate, up, workspace=ws, stream=stream)
+        return (loss, pkg.layer_norm_backward(dyy, x, None, m, r, stream=stream)[0], *dws)
+
+    want = [o.clone() for o in work()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = work(stream)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for o in got:
+        o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
