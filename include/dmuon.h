@@ -419,9 +419,11 @@ int dmuon_layer_norm_backward(const void* dy, const void* x, const void* weight,
  *   a = x w_gate^T,  u = x w_up^T,  h = act(a) u,  y = h w_down^T
  * with act = a sigmoid(a) (SILU) or a Phi(a), Phi the normal distribution
  * function (GELU).  Both projections, the activation and the product are one
- * kernel on the tensor cores.  gate, up: tokens x hidden, receive a and u for
- * the backward pass, or both NULL.  bf16: h (and a, u, and in the backward
- * pass da, du) are rounded to bf16, the operand type of the next product.
+ * kernel on the tensor cores.  saved_act, saved_slope, saved_h: tokens x hidden
+ * each, receive act(a), u act'(a) and h for the backward pass, or all NULL.
+ * bf16: these, h as the next product's operand, and da and du below are the
+ * only values rounded to bf16 on the way, once each from fp32 (keeping a and u
+ * instead would save one array and cost a second rounding in every gradient).
  * fp32: every product runs as six products of bf16 parts (x = hi + mid + lo),
  * which keeps fp32 accuracy.  tokens in [0, 2^24], dim and hidden in
  * [1, 2^20].  Widths that are a multiple of 8 are read in place; bf16 matrices
@@ -431,19 +433,20 @@ int dmuon_layer_norm_backward(const void* dy, const void* x, const void* weight,
 /* Workspace of the forward or the backward pass (0 for sizes it refuses, and for no tokens). */
 size_t dmuon_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype, int32_t backward);
 int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const void* w_up, const void* w_down, void* y,
-                            void* gate, void* up, int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype,
-                            int32_t activation, void* workspace, size_t workspace_bytes, void* stream);
-/* With dh = dy w_down, da = dh u act'(a), du = dh act(a):
- *   dx = da w_gate + du w_up,  dw_gate = da^T x,  dw_up = du^T x,  dw_down = dy^T h
- * from the stored gate and up.  With no tokens the weights' gradients are zero.
+                            void* saved_act, void* saved_slope, void* saved_h, int64_t tokens, int64_t dim,
+                            int64_t hidden, int32_t dtype, int32_t activation, void* workspace,
+                            size_t workspace_bytes, void* stream);
+/* With dh = dy w_down, da = dh saved_slope, du = dh saved_act:
+ *   dx = da w_gate + du w_up,  dw_gate = da^T x,  dw_up = du^T x,  dw_down = dy^T saved_h.
+ * With no tokens the weights' gradients are zero.
  * Returns DMUON_OK, DMUON_ERR_INVALID_ARG, DMUON_ERR_UNSUPPORTED_DTYPE,
  * DMUON_ERR_ALIGN, DMUON_ERR_NO_WORKSPACE, DMUON_ERR_WORKSPACE_TOO_SMALL,
  * DMUON_ERR_UNSUPPORTED_DEVICE (not sm_103) or DMUON_ERR_CUDA, like the
  * forward pass. */
 int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up, const void* w_down,
-                             const void* gate, const void* up, void* dx, void* dw_gate, void* dw_up, void* dw_down,
-                             int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype, int32_t activation,
-                             void* workspace, size_t workspace_bytes, void* stream);
+                             const void* saved_act, const void* saved_slope, const void* saved_h, void* dx,
+                             void* dw_gate, void* dw_up, void* dw_down, int64_t tokens, int64_t dim, int64_t hidden,
+                             int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- vocabulary loss --------------------------------------------------------
  *

@@ -1,0 +1,45 @@
+// Element formulas shared by the operators' kernels: the activations of the
+// gated block and the exponential of the vocabulary loss.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "ops.h"
+
+namespace dmuon {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// act(a) = a gate(a), act'(a) = gate + a gate'.  bf16 results take the
+// approximate exponential and reciprocal (relative error about 2^-22, far
+// below the storage rounding).
+template <bool kF32>
+__device__ __forceinline__ float act_gate(int act, float a) {
+    if (act == OPS_SILU) {
+        if (kF32) return 1.0f / (1.0f + expf(-a));
+        return rcp_approx(1.0f + ex2(-a * kLog2e));
+    }
+    return 0.5f * erfcf(-a * 0.70710678118654752f);
+}
+
+template <bool kF32>
+__device__ __forceinline__ float act_slope(int act, float a, float gate) {
+    if (act == OPS_SILU) return gate * (1.0f + a * (1.0f - gate));
+    const float pdf = 0.3989422804014327f * (kF32 ? expf(-0.5f * a * a) : ex2(-0.5f * kLog2e * a * a));
+    return gate + a * pdf;
+}
+
+}  // namespace dmuon

@@ -34,6 +34,7 @@ int fail(int code, const std::string& msg) {
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 constexpr int64_t kMaxVocab = int64_t(1) << 22;
+constexpr int kChain = 8;         // K = 512 per chain of MMAs under register sums
 constexpr int kMaxLaunches = 4;   // GEMM launches of one call (of one piece)
 constexpr int kSlots = 192;       // partial-sum slots: 48 MiB
 constexpr int kTails = 192;       // split tiles per launch
@@ -237,6 +238,7 @@ int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a
 int run_gemm(OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s, const char* where) {
     int pairs = 0;
     OPS_CUDA(ops_pairs(&pairs));
+    l.chain = kChain;
     ops_schedule(l, pairs, kSlots, kTails);
     OPS_CUDA(launch_ops_gemm(l, kind, f32, s));
     return DMUON_OK;
@@ -272,13 +274,36 @@ int check_workspace(const void* ws, size_t have, size_t need, const char* where)
 bool in_range(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 
 int check_device(const char* where) {
-    int dev = 0, major = 0, minor = 0;
+    static PerDevice cache;  // compute capability, 10 major + minor
+    int dev = 0, cc = 0;
     OPS_CUDA(cudaGetDevice(&dev));
-    OPS_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
-    OPS_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
-    if (major != 10 || minor != 3)
-        return fail(DMUON_ERR_UNSUPPORTED_DEVICE, std::string(where) + ": needs an sm_103 GPU");
+    OPS_CUDA(cache.get(dev, &cc, [&](int* out) {
+        int major = 0, minor = 0;
+        cudaError_t e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+        *out = 10 * major + minor;
+        return e;
+    }));
+    if (cc != 103) return fail(DMUON_ERR_UNSUPPORTED_DEVICE, std::string(where) + ": needs an sm_103 GPU");
     return DMUON_OK;
+}
+
+// The streaming kernel takes bf16 products of a few rows whose K it can read in
+// whole 16-byte pieces.
+bool use_stream(int64_t tokens, int64_t k0, int64_t k1, bool f32) {
+    return !f32 && tokens <= kStreamTokens && k0 % 8 == 0 && k1 % 8 == 0;
+}
+
+OpsStream stream_args(const Operand& x, const Operand& w, int64_t N, int64_t K) {
+    OpsStream a = {};
+    a.x = static_cast<const __nv_bfloat16*>(x.p);
+    a.w[0] = static_cast<const __nv_bfloat16*>(w.p);
+    a.ldx = x.ld;
+    a.ldw = w.ld;
+    a.tokens = static_cast<int32_t>(x.rows);
+    a.N = static_cast<int32_t>(N);
+    a.K = static_cast<int32_t>(K);
+    return a;
 }
 
 // ------------------------------------------------------------ gated block
@@ -289,8 +314,10 @@ struct FfnLayout {
     Operand x, wg, wu, wd, dy, h, da, du;
     size_t bytes = 0;
 
-    FfnLayout(char* base, const void* px, const void* pg, const void* pu, const void* pd, const void* pdy, int64_t n,
-              int64_t d, int64_t f, bool f32, bool backward)
+    // forward: h is written (in the caller's saved h where the next product can
+    // read it there); backward: h is read
+    FfnLayout(char* base, const void* px, const void* pg, const void* pu, const void* pd, const void* pdy,
+              const void* ph, int64_t n, int64_t d, int64_t f, bool f32, bool backward)
         : pack(f32) {
         Arena a{base};
         common.lay(a);
@@ -299,11 +326,14 @@ struct FfnLayout {
         wu = pack.add(a, pu, f, d);
         wd = pack.add(a, pd, d, f);
         const int parts = f32 ? kF32Parts : 1;
-        h = scratch(a, n, f, parts);
         if (backward) {
             dy = pack.add(a, pdy, n, d);
+            h = pack.add(a, ph, n, f);
             da = scratch(a, n, f, parts);
             du = scratch(a, n, f, parts);
+        } else {
+            h = scratch(a, n, f, parts);
+            if (ph && !f32 && f % 8 == 0) h.p = ph;
         }
         bytes = a.off;
     }
@@ -313,13 +343,10 @@ bool ffn_sizes_ok(int64_t n, int64_t d, int64_t f) {
     return in_range(n, 0, kMaxTokens) && in_range(d, 1, kMaxWidth) && in_range(f, 1, kMaxWidth);
 }
 
-int check_ffn(int64_t n, int64_t d, int64_t f, int32_t dtype, int32_t act, const char* where) {
+int check_ffn(int64_t n, int64_t d, int64_t f, int32_t dtype, const char* where) {
     if (!ffn_sizes_ok(n, d, f))
         return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": tokens must be in [0, 2^24], dim and hidden in [1, 2^20]");
-    OPS_TRY(check_dtype(dtype, where));
-    if (act != DMUON_ACT_SILU && act != DMUON_ACT_GELU)
-        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": unknown activation");
-    return DMUON_OK;
+    return check_dtype(dtype, where);
 }
 
 // ------------------------------------------------------------ vocabulary loss
@@ -335,7 +362,8 @@ struct LossRowArgs {
     __nv_bfloat16* dz;          // logit gradients, kF32Parts parts for fp32
     int64_t ld, part, ignore;
     int64_t vocab;
-    int32_t nblk, groups;       // 8-column groups of a row
+    int32_t nblk, block;        // statistics blocks of a row, columns per block
+    int32_t groups;             // 8-column groups of a row
     int32_t seg_groups;         // groups per blockIdx.y
 };
 
@@ -406,7 +434,7 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
                 v[2 * k + 1] = f.y;
             }
         }
-        const float scale = c * expf(st[c0 / 128].x - lse);
+        const float scale = c * expf(st[c0 / a.block].x - lse);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             v[k] = valid ? v[k] * scale : 0.0f;
@@ -435,7 +463,8 @@ struct LossLayout {
     float* target_logit = nullptr;
     float* dw_sum = nullptr;   // fp32 sum of dW over pieces (bf16, more than one piece)
     int64_t piece = 0, pieces = 0;  // tokens per piece
-    int nblk = 0;
+    bool stream;               // a few rows: the streaming kernel
+    int block = 128, nblk = 0;  // columns per statistics block, blocks
     size_t bytes = 0;
 
     LossLayout(char* base, const void* px, const void* pw, int64_t n, int64_t d, int64_t v, bool f32, bool grad,
@@ -445,7 +474,9 @@ struct LossLayout {
         common.lay(a);
         x = pack.add(a, px, n, d);
         w = pack.add(a, pw, v, d);
-        nblk = static_cast<int>(ceil_div(v, 128));
+        stream = use_stream(n, d, 8, f32);
+        if (stream) block = ops_stream_block(n);
+        nblk = static_cast<int>(ceil_div(v, block));
         const int64_t ld = up(v, 8);
         // bytes of one token's logits: statistics, exponentials, gradients
         const int64_t row = 8 * nblk + (grad ? (f32 ? 10 : 2) * ld : 0);
@@ -495,34 +526,55 @@ extern "C" size_t dmuon_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, i
     if (!ffn_sizes_ok(tokens, dim, hidden) || check_dtype(dtype, "dmuon_gated_ffn_workspace_bytes") != DMUON_OK)
         return 0;
     if (tokens == 0) return 0;
-    return FfnLayout(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, tokens, dim, hidden, dtype == DMUON_FP32,
-                     backward != 0)
+    return FfnLayout(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, tokens, dim, hidden,
+                     dtype == DMUON_FP32, backward != 0)
         .bytes;
 }
 
 extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const void* w_up, const void* w_down,
-                                       void* y, void* gate, void* up_proj, int64_t tokens, int64_t dim, int64_t hidden,
-                                       int32_t dtype, int32_t activation, void* workspace, size_t workspace_bytes,
-                                       void* stream) {
+                                       void* y, void* saved_act, void* saved_slope, void* saved_h, int64_t tokens,
+                                       int64_t dim, int64_t hidden, int32_t dtype, int32_t activation, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
     const char* where = "dmuon_gated_ffn_forward";
-    OPS_TRY(check_ffn(tokens, dim, hidden, dtype, activation, where));
-    if ((gate == nullptr) != (up_proj == nullptr))
-        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": gate and up are stored together or not at all");
+    OPS_TRY(check_ffn(tokens, dim, hidden, dtype, where));
+    if (activation != DMUON_ACT_SILU && activation != DMUON_ACT_GELU)
+        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": unknown activation");
+    if ((saved_act == nullptr) != (saved_slope == nullptr) || (saved_act == nullptr) != (saved_h == nullptr))
+        return fail(DMUON_ERR_INVALID_ARG,
+                    std::string(where) + ": saved_act, saved_slope and saved_h are stored together or not at all");
     if (tokens == 0) return DMUON_OK;
     OPS_TRY(check_ptr(x, "x", where));
     OPS_TRY(check_ptr(w_gate, "w_gate", where));
     OPS_TRY(check_ptr(w_up, "w_up", where));
     OPS_TRY(check_ptr(w_down, "w_down", where));
     OPS_TRY(check_ptr(y, "y", where));
-    if (gate) {
-        OPS_TRY(check_ptr(gate, "gate", where));
-        OPS_TRY(check_ptr(up_proj, "up", where));
+    if (saved_act) {
+        OPS_TRY(check_ptr(saved_act, "saved_act", where));
+        OPS_TRY(check_ptr(saved_slope, "saved_slope", where));
+        OPS_TRY(check_ptr(saved_h, "saved_h", where));
     }
     const bool f32 = dtype == DMUON_FP32;
-    FfnLayout L(static_cast<char*>(workspace), x, w_gate, w_up, w_down, nullptr, tokens, dim, hidden, f32, false);
+    FfnLayout L(static_cast<char*>(workspace), x, w_gate, w_up, w_down, nullptr, saved_h, tokens, dim, hidden, f32,
+                false);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (use_stream(tokens, dim, hidden, f32)) {
+        OpsStream a = stream_args(L.x, L.wg, hidden, dim);
+        a.w[1] = static_cast<const __nv_bfloat16*>(L.wu.p);
+        a.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
+        a.out0 = out_of(L.h);
+        if (saved_act) {
+            a.out1 = user_mat(saved_act, hidden, f32);
+            a.out2 = user_mat(saved_slope, hidden, f32);
+        }
+        OPS_CUDA(launch_ops_stream(a, OPS_GATE, s));
+        a = stream_args(L.h, L.wd, dim, hidden);
+        a.after = 1;
+        a.out0 = user_mat(y, dim, f32);
+        OPS_CUDA(launch_ops_stream(a, OPS_STORE, s));
+        return DMUON_OK;
+    }
     OPS_CUDA(L.common.clear(2, s));
     OPS_CUDA(L.pack.run(s));
     {
@@ -534,9 +586,10 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
         OPS_TRY(set_problem(P, tokens, hidden, dim, &L.x, false, b, false, 2, true));
         P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
         P.out0 = out_of(L.h);
-        if (gate) {
-            P.out1 = user_mat(gate, hidden, f32);
-            P.out2 = user_mat(up_proj, hidden, f32);
+        if (saved_act) {
+            P.out1 = user_mat(saved_act, hidden, f32);
+            P.out2 = user_mat(saved_slope, hidden, f32);
+            if (L.h.p != saved_h) P.out3 = user_mat(saved_h, hidden, f32);
         }
         OPS_TRY(run_gemm(l, OPS_GATE, f32, s, where));
     }
@@ -549,12 +602,12 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
 }
 
 extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up,
-                                        const void* w_down, const void* gate, const void* up_proj, void* dx,
-                                        void* dw_gate, void* dw_up, void* dw_down, int64_t tokens, int64_t dim,
-                                        int64_t hidden, int32_t dtype, int32_t activation, void* workspace,
+                                        const void* w_down, const void* saved_act, const void* saved_slope,
+                                        const void* saved_h, void* dx, void* dw_gate, void* dw_up, void* dw_down,
+                                        int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype, void* workspace,
                                         size_t workspace_bytes, void* stream) {
     const char* where = "dmuon_gated_ffn_backward";
-    OPS_TRY(check_ffn(tokens, dim, hidden, dtype, activation, where));
+    OPS_TRY(check_ffn(tokens, dim, hidden, dtype, where));
     OPS_TRY(check_ptr(dw_gate, "dw_gate", where));
     OPS_TRY(check_ptr(dw_up, "dw_up", where));
     OPS_TRY(check_ptr(dw_down, "dw_down", where));
@@ -572,27 +625,26 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     OPS_TRY(check_ptr(w_gate, "w_gate", where));
     OPS_TRY(check_ptr(w_up, "w_up", where));
     OPS_TRY(check_ptr(w_down, "w_down", where));
-    OPS_TRY(check_ptr(gate, "gate", where));
-    OPS_TRY(check_ptr(up_proj, "up", where));
+    OPS_TRY(check_ptr(saved_act, "saved_act", where));
+    OPS_TRY(check_ptr(saved_slope, "saved_slope", where));
+    OPS_TRY(check_ptr(saved_h, "saved_h", where));
     OPS_TRY(check_ptr(dx, "dx", where));
-    FfnLayout L(static_cast<char*>(workspace), x, w_gate, w_up, w_down, dy, tokens, dim, hidden, f32, true);
+    FfnLayout L(static_cast<char*>(workspace), x, w_gate, w_up, w_down, dy, saved_h, tokens, dim, hidden, f32, true);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
     OPS_CUDA(L.common.clear(2, s));
     OPS_CUDA(L.pack.run(s));
     {
-        // dh = dy Wd; the epilogue turns it into da, du and h
+        // dh = dy Wd; the epilogue turns it into da and du
         OpsLaunch l = {};
         l.n = 1;
         L.common.bind(l, 0);
         OpsProblem& P = l.p[0];
         OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false));
-        P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
-        P.in0 = user_mat(gate, hidden, f32);
-        P.in1 = user_mat(up_proj, hidden, f32);
+        P.in0 = user_mat(saved_act, hidden, f32);
+        P.in1 = user_mat(saved_slope, hidden, f32);
         P.out0 = out_of(L.da);
         P.out1 = out_of(L.du);
-        P.out2 = out_of(L.h);
         OPS_TRY(run_gemm(l, OPS_DGATE, f32, s, where));
     }
     // dx and the three weight gradients in one launch, the longest K first
@@ -654,9 +706,17 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
     const int64_t es = f32 ? 4 : 2;
     for (int64_t i = 0; i < L.pieces; ++i) {
         const int64_t r0 = i * L.piece, n = std::min(L.piece, tokens - r0);
-        OPS_CUDA(L.common.clear(grad ? 2 : 1, s));
+        if (grad || !L.stream) OPS_CUDA(L.common.clear(grad ? 2 : 1, s));
         const Operand xp = rows_of(L.x, r0, n);
-        {
+        if (L.stream) {
+            OpsStream a = stream_args(xp, L.w, vocab, dim);
+            a.stats = L.stats;
+            a.nblk = L.nblk;
+            a.target_logit = L.target_logit;
+            a.targets = targets + r0;
+            if (grad) a.out0 = out_of(L.dz);
+            OPS_CUDA(launch_ops_stream(a, OPS_LOGITS, s));
+        } else {
             OpsLaunch l = {};
             l.n = 1;
             L.common.bind(l, 0);
@@ -679,6 +739,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         a.ignore = ignore_index;
         a.vocab = vocab;
         a.nblk = L.nblk;
+        a.block = L.block;
         int segs = 1;
         if (grad) {
             a.e = L.e;

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
@@ -56,8 +57,8 @@ struct OpsProblem {
     int32_t slot_begin;  // first partial-sum slot
     // epilogue
     int32_t act;
-    OpsMat out0, out1, out2;  // STORE: D | GATE: h, a, u | DGATE: da, du, h | LOGITS: exponentials
-    OpsMat in0, in1;          // STORE: in0 = addend (fp32) | DGATE: a, u
+    OpsMat out0, out1, out2, out3;  // STORE: D | GATE: h, act, u act', h again | DGATE: da, du | LOGITS: exponentials
+    OpsMat in0, in1;          // STORE: in0 = addend (fp32) | DGATE: act, u act'
     float2* stats;            // LOGITS: [M][nblk] (max, sum of exp) of 128-column blocks
     int32_t nblk;
     float* target_logit;      // LOGITS: [M]
@@ -67,10 +68,32 @@ struct OpsProblem {
 struct OpsLaunch {
     OpsProblem p[kOpsMaxProblems];
     int32_t n, total_units;
+    int32_t chain;         // K slabs per chain of MMAs where sums are added up in registers
     int32_t* counter;      // unit counter, zero at launch
     int32_t* tail_count;   // arrivals per (split tile, CTA rank, epilogue warp), zero at launch
     float* partials;       // split tiles' partial sums
 };
+
+// Product of a few rows x (tokens x K) with weight rows (N x K, twice for the
+// gated block), bf16, K a multiple of 8: the weights are streamed once through
+// registers (ops_stream.cu).
+struct OpsStream {
+    const __nv_bfloat16* x;
+    const __nv_bfloat16* w[2];  // [0]; GATE: gate and up
+    int64_t ldx, ldw;           // elements, multiples of 8
+    int32_t tokens, N, K;
+    int32_t act;
+    int32_t after;              // the launch directly follows the library's own kernel, which did not write w
+    OpsMat out0, out1, out2, out3;  // as OpsProblem
+    float2* stats;              // LOGITS: [tokens][nblk] of ops_stream_block() columns
+    int32_t nblk;
+    float* target_logit;
+    const int64_t* targets;
+};
+
+constexpr int kStreamTokens = 32;  // most rows ops_stream takes
+int ops_stream_block(int64_t tokens);  // LOGITS: columns per statistics block
+cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s);
 
 constexpr int64_t kOpsSlotFloats = 256 * 256;  // one partial accumulator of a pair tile
 constexpr int kOpsTailCounts = 16;             // counters per split tile

@@ -30,6 +30,7 @@
 // (gemm_tc.cu): warp 0 TMA, warp 1 MMA (leader CTA), warps 4..11 epilogue.
 #include <type_traits>
 
+#include "act.cuh"
 #include "ops.h"
 #include "tc.cuh"
 
@@ -57,7 +58,6 @@ constexpr int kRegsLow = 56, kRegsEpi = 224;    // 56 + 2 x 224 = 3 x 168: the l
 constexpr uint32_t kTileReaders = kPair * kEpiWarps + 2;
 constexpr int CH = 16;
 constexpr uint16_t kPairMask = 3;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct __align__(1024) Smem {
     uint8_t a[STAGES][OP_BYTES];
@@ -259,87 +259,73 @@ __device__ __forceinline__ void ld_mat(const OpsMat& m, int r0, int c0, int lane
     }
 }
 
-// ------------------------------------------------------- element formulas
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// act(a) and, for the backward pass, act'(a).  bf16 results take the
-// approximate exponential and reciprocal (relative error about 2^-22, far
-// below the storage rounding).
-template <bool kF32>
-__device__ __forceinline__ float act_gate(int act, float a) {
-    if (act == OPS_SILU) {
-        if (kF32) return 1.0f / (1.0f + expf(-a));
-        return rcp_approx(1.0f + ex2(-a * kLog2e));
-    }
-    return 0.5f * erfcf(-a * 0.70710678118654752f);
-}
-
-template <bool kF32>
-__device__ __forceinline__ float act_slope(int act, float a, float gate) {
-    // act(a) = a gate(a): act' = gate + a gate'
-    if (act == OPS_SILU) return gate * (1.0f + a * (1.0f - gate));
-    const float pdf = 0.3989422804014327f * (kF32 ? expf(-0.5f * a * a) : ex2(-0.5f * kLog2e * a * a));
-    return gate + a * pdf;
-}
-
 // ------------------------------------------------------- accumulator source
+// A warp's share of an accumulator is 128 columns of 32 rows, in eight chunks of
+// 16: columns 128 half .. of the tile, or for the dual tile columns 64 half ..
+// of each of its two matrices (chunks 0..3 and 4..7).
 
-// The finished accumulator of a warp's 32 rows: TMEM for a whole tile, TMEM
-// plus the other units' stored partial sums, in K order, for a split one.
-struct Acc {
+template <int kKind>
+__device__ __forceinline__ int chunk_col(int half, int ci) {
+    if (kKind == OPS_GATE) return (ci >> 2) * (BN / 2) + half * (BN / 4) + (ci & 3) * CH;
+    return half * (BN / 2) + ci * CH;
+}
+
+// Sums left in TMEM (one chain of MMAs over the tile's whole K range).
+template <int kKind>
+struct TmemSrc {
     uint32_t taddr;
-    const float* parts;  // slot of part 0, this warp's first row
-    int split, mine;
-
-    __device__ __forceinline__ void load(int tcol, float (&v)[CH], int lane) const {
+    int half;
+    __device__ __forceinline__ void load(int ci, float (&v)[CH]) {
         __syncwarp();
-        tmem_ld16(taddr + static_cast<uint32_t>(tcol), v);
-        if (split > 1) {
-            float s[CH];
+        tmem_ld16(taddr + static_cast<uint32_t>(chunk_col<kKind>(half, ci)), v);
+    }
+    __device__ __forceinline__ void load_pair(int ci, float (&a)[CH], float (&b)[CH]) {
+        load(ci, a);
+        load(ci + 4, b);
+    }
+};
+
+// Sums in registers, added up there from several shorter chains of MMAs or, for
+// a split tile, from all units' stored partial sums.  Chunks are taken in order:
+// each load hands out the first 16 values and moves the others down, so that
+// the chunk loop stays a loop (unrolled eight times it tripled the code).
+struct RegSrc {
+    float (&r)[BN / 2];
+    __device__ __forceinline__ void load(int, float (&v)[CH]) {
 #pragma unroll
-            for (int j = 0; j < CH; ++j) s[j] = 0.0f;
-            for (int i = 0; i < split; ++i) {
-                if (i == mine) {
+        for (int j = 0; j < CH; ++j) v[j] = r[j];
 #pragma unroll
-                    for (int j = 0; j < CH; ++j) s[j] += v[j];
-                } else {
-                    const float* p = parts + i * kOpsSlotFloats + static_cast<int64_t>(tcol) * BM + lane;
+        for (int j = 0; j < BN / 2 - CH; ++j) r[j] = r[j + CH];
+    }
+    __device__ __forceinline__ void load_pair(int, float (&a)[CH], float (&b)[CH]) {
 #pragma unroll
-                    for (int j = 0; j < CH; ++j) s[j] += __ldcg(p + j * BM);
-                }
-            }
+        for (int j = 0; j < CH; ++j) {
+            a[j] = r[j];
+            b[j] = r[BN / 4 + j];
+        }
 #pragma unroll
-            for (int j = 0; j < CH; ++j) v[j] = s[j];
+        for (int j = 0; j < BN / 4 - CH; ++j) {
+            r[j] = r[j + CH];
+            r[BN / 4 + j] = r[BN / 4 + j + CH];
         }
     }
 };
 
 // ------------------------------------------------------- epilogues
-// h: column half of this warp's group; r0: its first row.
+// u: the unit; half: this warp's column half; r0: its first row.
 
-template <bool kF32>
-__device__ __forceinline__ void epi_store(const OpsProblem& P, const Acc& acc, const Unit& u, int half, int r0,
+template <bool kF32, typename Src>
+__device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
                                           int lane) {
 #pragma unroll 1
-    for (int kc = 0; kc < BN / 2 / CH; ++kc) {
-        const int tcol = half * (BN / 2) + kc * CH, c0 = u.tn * BN + tcol;
+    for (int kc = 0; kc < 8; ++kc) {
+        const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
         if (c0 >= P.N) break;
-        float add[CH];
-        if (P.in0.p) ld_mat(P.in0, r0, c0, lane, add, P.M, P.N);
         float v[CH];
-        acc.load(tcol, v, lane);
+        acc.load(kc, v);
         if (P.in0.p) {
+            float add[CH];
+            ld_mat(P.in0, r0, c0, lane, add, P.M, P.N);
 #pragma unroll
             for (int j = 0; j < CH; ++j) v[j] += add[j];
         }
@@ -347,96 +333,102 @@ __device__ __forceinline__ void epi_store(const OpsProblem& P, const Acc& acc, c
     }
 }
 
-template <bool kF32>
-__device__ __forceinline__ void epi_gate(const OpsProblem& P, const Acc& acc, const Unit& u, int half, int r0,
+template <bool kF32, typename Src>
+__device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
                                          int lane) {
 #pragma unroll 1
-    for (int kc = 0; kc < BN / 4 / CH; ++kc) {
-        const int tcol = half * (BN / 4) + kc * CH, c0 = u.tn * (BN / 2) + tcol;
+    for (int kc = 0; kc < 4; ++kc) {
+        const int c0 = u.tn * (BN / 2) + half * (BN / 4) + kc * CH;
         if (c0 >= P.N) break;
         float a[CH], w[CH];
-        acc.load(tcol, a, lane);
-        acc.load(BN / 2 + tcol, w, lane);
+        acc.load_pair(kc, a, w);
         if (P.out1.p) {
-            st_mat(P.out1, r0, c0, lane, a, P.M, P.N);
-            st_mat(P.out2, r0, c0, lane, w, P.M, P.N);
-        }
+            float f[CH], s[CH];
 #pragma unroll
-        for (int j = 0; j < CH; ++j) w[j] *= a[j] * act_gate<kF32>(P.act, a[j]);
+            for (int j = 0; j < CH; ++j) {
+                const float g = act_gate<kF32>(P.act, a[j]);
+                f[j] = a[j] * g;
+                s[j] = w[j] * act_slope<kF32>(P.act, a[j], g);
+                w[j] *= f[j];
+            }
+            st_mat(P.out1, r0, c0, lane, f, P.M, P.N);
+            st_mat(P.out2, r0, c0, lane, s, P.M, P.N);
+            if (P.out3.p) st_mat(P.out3, r0, c0, lane, w, P.M, P.N);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) w[j] *= a[j] * act_gate<kF32>(P.act, a[j]);
+        }
         st_mat(P.out0, r0, c0, lane, w, P.M, P.N);
     }
 }
 
-template <bool kF32>
-__device__ __forceinline__ void epi_dgate(const OpsProblem& P, const Acc& acc, const Unit& u, int half, int r0,
+template <bool kF32, typename Src>
+__device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
                                           int lane) {
 #pragma unroll 1
-    for (int kc = 0; kc < BN / 2 / CH; ++kc) {
-        const int tcol = half * (BN / 2) + kc * CH, c0 = u.tn * BN + tcol;
+    for (int kc = 0; kc < 8; ++kc) {
+        const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
         if (c0 >= P.N) break;
-        float a[CH], w[CH], v[CH];
-        ld_mat(P.in0, r0, c0, lane, a, P.M, P.N);
-        ld_mat(P.in1, r0, c0, lane, w, P.M, P.N);
-        acc.load(tcol, v, lane);
-        float h[CH];
+        float f[CH], s[CH], v[CH];
+        ld_mat(P.in0, r0, c0, lane, f, P.M, P.N);
+        ld_mat(P.in1, r0, c0, lane, s, P.M, P.N);
+        acc.load(kc, v);
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const float g = act_gate<kF32>(P.act, a[j]);
-            const float s = act_slope<kF32>(P.act, a[j], g);
-            const float f = a[j] * g;
-            h[j] = f * w[j];             // the forward pass's h, from the stored a and u
-            w[j] = v[j] * w[j] * s;      // da
-            a[j] = v[j] * f;             // du
+            s[j] *= v[j];  // da = dh u act'(a)
+            f[j] *= v[j];  // du = dh act(a)
         }
-        st_mat(P.out0, r0, c0, lane, w, P.M, P.N);
-        st_mat(P.out1, r0, c0, lane, a, P.M, P.N);
-        st_mat(P.out2, r0, c0, lane, h, P.M, P.N);
+        st_mat(P.out0, r0, c0, lane, s, P.M, P.N);
+        st_mat(P.out1, r0, c0, lane, f, P.M, P.N);
     }
 }
 
 template <bool kF32>
-__device__ __forceinline__ void epi_logits(const OpsProblem& P, const Acc& acc, const Unit& u, int half, int r0,
-                                           int lane) {
+__device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, int half, int r0, int lane,
+                                           float (&z)[BN / 2]) {
     const int cb = u.tn * BN + half * (BN / 2);
     const int r = r0 + lane;
     const float ninf = __int_as_float(0xff800000);
-    float m = ninf;
-#pragma unroll 1
-    for (int kc = 0; kc < BN / 2 / CH; ++kc) {
-        const int c0 = cb + kc * CH;
-        if (c0 >= P.N) break;
-        float v[CH];
-        acc.load(half * (BN / 2) + kc * CH, v, lane);
+    const bool whole = cb + BN / 2 <= P.N;
+    if (!whole) {  // columns past the vocabulary: exp gives 0
 #pragma unroll
-        for (int j = 0; j < CH; ++j) m = fmaxf(m, c0 + j < P.N ? v[j] : ninf);
+        for (int j = 0; j < BN / 2; ++j) z[j] = cb + j < P.N ? z[j] : ninf;
     }
-    int64_t t = -1;
-    if (r < P.M) t = P.targets[r] - cb;
-    const int tl = t >= 0 && t < BN / 2 ? static_cast<int>(t) : -1;
-    float s = 0.0f;
-#pragma unroll 1
-    for (int kc = 0; kc < BN / 2 / CH; ++kc) {
-        const int c0 = cb + kc * CH;
-        if (c0 >= P.N) break;
-        float v[CH];
-        acc.load(half * (BN / 2) + kc * CH, v, lane);
-        if (tl >= 0 && tl / CH == kc) {
+    float m = z[0];
 #pragma unroll
-            for (int j = 0; j < CH; ++j)
-                if (tl % CH == j && c0 + j < P.N) P.target_logit[r] = v[j];
-        }
+    for (int j = 1; j < BN / 2; ++j) m = fmaxf(m, z[j]);
+    const int64_t t = r < P.M ? P.targets[r] - cb : -1;
+    if (t >= 0 && t < BN / 2 && cb + t < P.N) {
+        float zt = 0.0f;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            v[j] = kF32 ? expf(v[j] - m) : ex2((v[j] - m) * kLog2e);
-            if (c0 + j < P.N) s += v[j];
-        }
-        if (P.out0.p) st_mat(P.out0, r0, c0, lane, v, P.M, P.N);
+        for (int j = 0; j < BN / 2; ++j) zt = t == j ? z[j] : zt;
+        P.target_logit[r] = zt;
     }
-    if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] = make_float2(m, s);
+    float s0 = 0.0f, s1 = 0.0f;
+    const float ms = m * kLog2e;
+#pragma unroll
+    for (int kc = 0; kc < 8; ++kc) {
+        float v[CH];
+#pragma unroll
+        for (int j = 0; j < CH; j += 2) {
+            v[j] = kF32 ? expf(z[kc * CH + j] - m) : ex2(fmaf(z[kc * CH + j], kLog2e, -ms));
+            v[j + 1] = kF32 ? expf(z[kc * CH + j + 1] - m) : ex2(fmaf(z[kc * CH + j + 1], kLog2e, -ms));
+            s0 += v[j];
+            s1 += v[j + 1];
+        }
+        if (P.out0.p) st_mat(P.out0, r0, cb + kc * CH, lane, v, P.M, P.N);
+    }
+    if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] = make_float2(m, s0 + s1);
 }
 
 template <int kKind, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_constant__ OpsLaunch L) {
+    // Sums that must keep fp32 accuracy (fp32 matrices, logits) are added up in
+    // registers from chains of L.chain slabs: the tensor cores truncate each
+    // addition to the accumulator, and over a 4096-deep chain that bias reached
+    // 2.6e-6 of a logit, five times the error of fp32 FMAs.  Sums that a bf16
+    // store rounds anyway stay in TMEM.
+    constexpr bool kRegs = kF32 || kKind == OPS_LOGITS;
     extern __shared__ uint8_t smem_raw[];
     Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x / 32;
@@ -582,39 +574,49 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
             const uint64_t a_k = smem_desc(saddr(S.a[0]), 0, 1024), a_m = smem_desc(saddr(S.a[0]), MN_BOX_BYTES, 1024);
             const uint64_t b_k = smem_desc(saddr(S.b[0]), 0, 1024), b_m = smem_desc(saddr(S.b[0]), MN_BOX_BYTES, 1024);
             constexpr uint64_t step_k = (UMMA_K * 2) >> 4, step_mn = (UMMA_K * 128) >> 4;
+            int it = 0;
             for (int k = 0; ok; ++k) {
                 const int t = wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
                 release_tile(S.tile_empty, k);
                 if (t >= total) break;
                 const Unit u = decode_unit(L, t);
                 const bool a_mn = L.p[u.p].a_mn != 0, b_mn = L.p[u.p].b_mn != 0;
-                const int buf = k & 1;
-                const uint32_t use = static_cast<uint32_t>(k >> 1);
-                if (!mbar_wait<true>(&S.acc_empty[buf], (use & 1) ^ 1, &g_ops_status)) break;
-                fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
                 const uint32_t idesc = make_idesc(a_mn, b_mn);
                 const uint64_t a0 = a_mn ? a_m : a_k, b0 = b_mn ? b_m : b_k;
                 const uint64_t a_step = a_mn ? step_mn : step_k, b_step = b_mn ? step_mn : step_k;
-                for (int kb = u.kb0; kb < u.kb1; ++kb) {
-                    if (!mbar_wait<false>(&S.full[stage], phase, &g_ops_status)) {
+                // one accumulator per chain of MMAs: the unit's whole K range, or
+                // (register sums) L.chain slabs of it
+                for (int c0 = u.kb0; ok && c0 < u.kb1; ++it) {
+                    const int c1 = kRegs && c0 + L.chain < u.kb1 ? c0 + L.chain : u.kb1;
+                    const int buf = it & 1;
+                    const uint32_t use = static_cast<uint32_t>(it >> 1);
+                    if (!mbar_wait<true>(&S.acc_empty[buf], (use & 1) ^ 1, &g_ops_status)) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t ad = a0 + static_cast<uint64_t>(stage) * (OP_BYTES >> 4);
-                    const uint64_t bd = b0 + static_cast<uint64_t>(stage) * (OP_BYTES >> 4);
+                    const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
+                    for (int kb = c0; kb < c1; ++kb) {
+                        if (!mbar_wait<false>(&S.full[stage], phase, &g_ops_status)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
+                        const uint64_t ad = a0 + static_cast<uint64_t>(stage) * (OP_BYTES >> 4);
+                        const uint64_t bd = b0 + static_cast<uint64_t>(stage) * (OP_BYTES >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < SLAB_K / UMMA_K; ++kk)
-                        umma_bf16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb != u.kb0 || kk) ? 1u : 0u);
-                    umma_commit_pair(&S.empty[stage], kPairMask);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
+                        for (int kk = 0; kk < SLAB_K / UMMA_K; ++kk)
+                            umma_bf16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb != c0 || kk) ? 1u : 0u);
+                        umma_commit_pair(&S.empty[stage], kPairMask);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
+                    // also on failure: covers every MMA issued so far
+                    umma_commit_pair(&S.acc_full[buf], kPairMask);
+                    c0 = c1;
                 }
-                // also on failure: covers every MMA issued so far
-                umma_commit_pair(&S.acc_full[buf], kPairMask);
             }
         }
     } else {
@@ -622,6 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
         // ------------------------------------------------ epilogue
         const int q = warp & 3;                   // TMEM lane quarter this warp may access
         const int half = (warp - kEpiWarp0) / 4;  // column half
+        int it = 0;
+        float r[kRegs ? BN / 2 : 1];
         for (int k = 0;; ++k) {
             const int t = wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
             __syncwarp();
@@ -629,37 +633,77 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
             if (t >= total) break;
             const Unit u = decode_unit(L, t);
             const OpsProblem& P = L.p[u.p];
-            const int buf = k & 1;
-            const uint32_t use = static_cast<uint32_t>(k >> 1);
             const int r0 = (2 * u.tm + rank) * BM + q * 32;
-            // rows, or this group's columns (of every pair of matrices, for
-            // the dual tile), lie outside the matrix
+            // false: this warp's rows or columns lie outside the matrix
             const int c_first = kKind == OPS_GATE ? u.tn * (BN / 2) + half * (BN / 4) : u.tn * BN + half * (BN / 2);
             bool active = r0 < P.M && c_first < P.N;
-            const bool ready = mbar_wait<true>(&S.acc_full[buf], use & 1, &g_ops_status);
-            fence_after();
-            active = active && ready;
-            Acc acc{tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN), nullptr, 1, 0};
-            if (active && u.split > 1) {
+            uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+            const int buf = it & 1;
+            if constexpr (kRegs) {
+                // add the chains up; each accumulator goes back to the MMAs
+                // before anything is done with the sum
+#pragma unroll
+                for (int j = 0; j < BN / 2; ++j) r[j] = 0.0f;
+                for (int c0 = u.kb0; c0 < u.kb1; c0 += L.chain, ++it) {
+                    const bool ready = mbar_wait<true>(&S.acc_full[it & 1], (it >> 1) & 1, &g_ops_status);
+                    fence_after();
+                    active = active && ready;
+                    if (active) {
+                        const uint32_t base = taddr + static_cast<uint32_t>((it & 1) * BN);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            float v[32];
+                            __syncwarp();
+                            tmem_ld32(base + static_cast<uint32_t>(chunk_col<kKind>(half, 2 * b)), v);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) r[b * 32 + j] += v[j];
+                        }
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(mapa(saddr(&S.acc_empty[it & 1]), 0));
+                }
+            } else {
+                const bool ready = mbar_wait<true>(&S.acc_full[buf], (it >> 1) & 1, &g_ops_status);
+                fence_after();
+                active = active && ready;
+                taddr += static_cast<uint32_t>(buf * BN);
+                ++it;
+            }
+            const auto finish = [&](auto acc) {
+                if constexpr (kKind == OPS_STORE) epi_store<kF32>(P, acc, u, half, r0, lane);
+                else if constexpr (kKind == OPS_GATE) epi_gate<kF32>(P, acc, u, half, r0, lane);
+                else if constexpr (kKind == OPS_DGATE) epi_dgate<kF32>(P, acc, u, half, r0, lane);
+                else epi_logits<kF32>(P, u, half, r0, lane, acc.r);
+            };
+            if (active && u.split == 1) {
+                if constexpr (kRegs) finish(RegSrc{r});
+                else finish(TmemSrc<kKind>{taddr, half});
+            } else if (active) {
                 // store this unit's partial sum [column][row]; the last unit of
-                // the tile adds them up
+                // the tile adds them all up, in K order
                 float* slot = L.partials + static_cast<int64_t>(u.slot) * kOpsSlotFloats +
                               static_cast<int64_t>(rank) * BN * BM + q * 32;
-                constexpr int kBlocks = kKind == OPS_GATE ? 2 : 1;
-#pragma unroll 1
-                for (int b = 0; b < kBlocks; ++b)
-#pragma unroll 1
-                    for (int kc = 0; kc < BN / 2 / CH / kBlocks; ++kc) {
-                        const int cc = half * (BN / 2 / kBlocks) + kc * CH;  // column inside its block
-                        if (u.tn * (BN / kBlocks) + cc >= P.N) break;
-                        const int tcol = b * (BN / 2) + cc;
-                        float v[CH];
-                        acc.load(tcol, v, lane);
-                        float* p = slot + static_cast<int64_t>(u.part) * kOpsSlotFloats +
-                                   static_cast<int64_t>(tcol) * BM + lane;
+                const auto inside = [&](int tcol) {
+                    return (kKind == OPS_GATE ? u.tn * (BN / 2) + tcol % (BN / 2) : u.tn * BN + tcol) < P.N;
+                };
+                constexpr int kUnroll = kRegs ? 8 : 1;
+#pragma unroll kUnroll
+                for (int ci = 0; ci < 8; ++ci) {
+                    const int tcol = chunk_col<kKind>(half, ci);
+                    if (!inside(tcol)) continue;
+                    float v[CH];
+                    if constexpr (kRegs) {
 #pragma unroll
-                        for (int j = 0; j < CH; ++j) __stcg(p + j * BM, v[j]);
+                        for (int j = 0; j < CH; ++j) v[j] = r[ci * CH + j];
+                    } else {
+                        TmemSrc<kKind>{taddr, half}.load(ci, v);
                     }
+                    float* p = slot + static_cast<int64_t>(u.part) * kOpsSlotFloats + static_cast<int64_t>(tcol) * BM +
+                               lane;
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) __stcg(p + j * BM, v[j]);
+                }
                 __threadfence();
                 __syncwarp();
                 int before = 0;
@@ -667,23 +711,34 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                     before = atomicAdd(&L.tail_count[u.tail * kOpsTailCounts + rank * kEpiWarps + (warp - kEpiWarp0)],
                                        1);
                 before = __shfl_sync(kFullMask, before, 0);
-                active = before == u.split - 1;
-                __threadfence();
-                acc.parts = slot;
-                acc.split = u.split;
-                acc.mine = u.part;
+                if (before == u.split - 1) {
+                    __threadfence();
+                    float sum[BN / 2];
+#pragma unroll
+                    for (int j = 0; j < BN / 2; ++j) sum[j] = 0.0f;
+#pragma unroll 1
+                    for (int i = 0; i < u.split; ++i) {
+                        const float* p = slot + i * kOpsSlotFloats + lane;
+#pragma unroll
+                        for (int ci = 0; ci < 8; ++ci) {
+                            const int tcol = chunk_col<kKind>(half, ci);
+                            if (inside(tcol)) {
+#pragma unroll
+                                for (int j = 0; j < CH; ++j) sum[ci * CH + j] += __ldcg(p + (tcol + j) * BM);
+                            }
+                        }
+                    }
+                    finish(RegSrc{sum});
+                }
             }
-            if (active) {
-                if constexpr (kKind == OPS_STORE) epi_store<kF32>(P, acc, u, half, r0, lane);
-                else if constexpr (kKind == OPS_GATE) epi_gate<kF32>(P, acc, u, half, r0, lane);
-                else if constexpr (kKind == OPS_DGATE) epi_dgate<kF32>(P, acc, u, half, r0, lane);
-                else epi_logits<kF32>(P, acc, u, half, r0, lane);
+            if constexpr (!kRegs) {
+                // every tcgen05.ld of the accumulator has completed (wait::ld):
+                // the release is relaxed, so it does not wait for this warp's
+                // stores
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa(saddr(&S.acc_empty[buf]), 0));
             }
-            // every tcgen05.ld of the accumulator has completed (wait::ld): the
-            // release is relaxed, so it does not wait for this warp's stores
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa(saddr(&S.acc_empty[buf]), 0));
         }
     }
 
@@ -701,7 +756,7 @@ using Kernel = void (*)(OpsLaunch);
 
 Kernel kernel_of(int32_t kind, bool f32) {
     switch (kind) {
-        case OPS_STORE: return ops_gemm_kernel<OPS_STORE, false>;
+        case OPS_STORE: return f32 ? ops_gemm_kernel<OPS_STORE, true> : ops_gemm_kernel<OPS_STORE, false>;
         case OPS_GATE: return f32 ? ops_gemm_kernel<OPS_GATE, true> : ops_gemm_kernel<OPS_GATE, false>;
         case OPS_DGATE: return f32 ? ops_gemm_kernel<OPS_DGATE, true> : ops_gemm_kernel<OPS_DGATE, false>;
         default: return f32 ? ops_gemm_kernel<OPS_LOGITS, true> : ops_gemm_kernel<OPS_LOGITS, false>;
@@ -750,14 +805,14 @@ cudaError_t ops_pairs(int* pairs) {
 
 // Work units.  A launch ends when its last unit does: with T equal tiles on P
 // pairs the last round leaves P - T mod P pairs idle.  The tiles of that round
-// are split into S K ranges, S minimising ceil(rem S / P) / S (the time of the
-// round in tiles) plus the cost of storing and adding the partial sums, about
-// kSplitCost slabs per range.  In a launch of several products the longest
-// tiles come first (the caller's order), a product whose tiles are long
-// against the launch's share per pair is split throughout, and only the last
-// product's last round is split as above.
+// are split into S K ranges, S minimising the round's time: ceil(rem S / P)
+// units of total / S slabs plus what a unit costs beside its slabs, and the
+// partial sums that the last unit of a tile loads one after the other (all in
+// slabs, about 0.35 us).  In a launch of several products the longest tiles come
+// first (the caller's order), and a product whose tiles are long against the
+// launch's share per pair is split throughout.
 void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
-    constexpr double kSplitCost = 10.0;  // slabs
+    constexpr double kUnitCost = 4.0, kStoreCost = 4.0, kPartCost = 3.0;  // slabs
     constexpr int kMinSlabs = 8;         // per range
     double work = 0.0;
     for (int i = 0; i < l.n; ++i)
@@ -770,10 +825,11 @@ void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
         int rem = 0, best = 1;
         if (l.n == 1) {
             rem = tiles % pairs;
-            double cost = total;
+            double cost = total + kUnitCost;
             for (int s = 2; s <= 32 && rem > 0 && total / s >= kMinSlabs; ++s) {
                 const double c = static_cast<double>((static_cast<int64_t>(rem) * s + pairs - 1) / pairs) *
-                                 (static_cast<double>(total) / s + kSplitCost);
+                                     (static_cast<double>(total) / s + kUnitCost) +
+                                 kStoreCost + kPartCost * s;
                 if (c < cost) {
                     cost = c;
                     best = s;
@@ -782,7 +838,7 @@ void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
         } else if (total > 0.25 * share) {
             rem = tiles;
             best = static_cast<int>(4.0 * total / share) + 1;
-            if (best > 32) best = 32;
+            if (best > 12) best = 12;
             if (best > total / kMinSlabs) best = total / kMinSlabs;
         }
         while (best > 1 && (static_cast<int64_t>(rem) * best > slots - slot || rem > tails - tail)) --best;

@@ -1,0 +1,253 @@
+// Products of a few rows with a weight matrix: generated tokens through the
+// gated block, a handful of positions against the vocabulary.
+//
+// Bound by the read of the weights (2 bytes per weight, 2 FLOP per weight and
+// row), so the kernel is built around loads in flight: a weight goes from HBM
+// straight to the registers that feed the tensor cores, without shared memory,
+// and is read once for all rows.  A block holds 16 MT weight rows (for the gated
+// block 8 MT of each projection, so a gate and its up value meet in one
+// thread); its eight warps take 32-column pieces of K in turn -- 512 contiguous
+// bytes per row and round -- and add up their sums in shared memory.  When there
+// are few weight rows, K is also shared by a cluster of up to 8 blocks, whose
+// leader adds their sums through distributed shared memory; the order is fixed.
+//
+// mma.sync.m16n8k16 with K permuted: a thread's 16-byte load holds 8 consecutive
+// k of its row, of which elements (0,1), (2,3) serve one MMA and (4,5), (6,7)
+// the next as the fragment's two column pairs.  The sum over k does not depend
+// on which k sits in which slot as long as weights and x agree, and both are
+// loaded alike.  The tcgen05 kernel needs the weights in shared memory and 256
+// rows of x per tile: at one row it read them at 2.4 TB/s.
+#include <cuda_bf16.h>
+
+#include "act.cuh"
+#include "ops.h"
+#include "tc.cuh"
+
+namespace dmuon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ uint4 ld_stream(const __nv_bfloat16* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(reinterpret_cast<uint64_t>(p)));
+    return v;
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void st1(const OpsMat& m, int64_t r, int64_t c, float v) {
+    static_cast<__nv_bfloat16*>(m.p)[r * m.ld + c] = __float2bfloat16_rn(v);
+}
+
+template <int kKind, int NT, int MT>
+__global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) ops_stream_kernel(const __grid_constant__ OpsStream P) {
+    constexpr int R = 16 * MT, T = 8 * NT;     // weight rows, x rows of the block's result
+    constexpr int U = MT == 1 ? 4 : 2;         // K pieces loaded at a time
+    __shared__ float part[kWarps][R * T];      // [warp][token][row]
+    __shared__ float sum[R * T];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    uint32_t rank, cluster;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(cluster));
+    const int tile = blockIdx.x / cluster;
+    const int n0 = tile * (kKind == OPS_GATE ? R / 2 : R);  // first output column
+
+    // this thread's weight rows: g and g + 8 of every 16-row tile (rows past the
+    // matrix read its last row and are dropped at the end)
+    const __nv_bfloat16* wp[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = kKind == OPS_GATE ? n0 + 8 * m + g : n0 + 16 * m + 8 * h + g;
+            wp[m][h] = P.w[kKind == OPS_GATE ? h : 0] + static_cast<int64_t>(min(n, P.N - 1)) * P.ldw + 8 * t;
+        }
+    const __nv_bfloat16* xp[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xp[n] = P.x + static_cast<int64_t>(min(8 * n + g, P.tokens - 1)) * P.ldx + 8 * t;
+
+    // K pieces of 32: the cluster's blocks take contiguous shares, a block's
+    // warps every eighth piece of its share
+    const int pieces = (P.K + 31) / 32;
+    const int p0 = static_cast<int>(static_cast<int64_t>(pieces) * rank / cluster);
+    const int p1 = static_cast<int>(static_cast<int64_t>(pieces) * (rank + 1) / cluster);
+    float c[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[m][n][i] = 0.0f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 w[U][MT][2];
+    const auto load_w = [&](int p) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (p + u * kWarps) * 32;
+            const bool in = p + u * kWarps < p1 && k + 8 * t < P.K;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) w[u][m][h] = in ? ld_stream(wp[m][h] + k) : zero;
+        }
+    };
+    // programmatic dependent launch: after the library's own kernel the weights
+    // may be read before that kernel has finished (it waited for everything
+    // before it, and writes no weights); x and all outputs wait
+    if (P.after) load_w(p0 + warp);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!P.after) load_w(p0 + warp);
+    for (int p = p0 + warp; p < p1; p += U * kWarps) {
+        uint4 x[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (p + u * kWarps) * 32;
+            const bool in = p + u * kWarps < p1 && k + 8 * t < P.K;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[u][n] = in ? *reinterpret_cast<const uint4*>(xp[n] + k) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma(c[m][n], w[u][m][0].x, w[u][m][1].x, w[u][m][0].y, w[u][m][1].y, x[u][n].x, x[u][n].y);
+                    mma(c[m][n], w[u][m][0].z, w[u][m][1].z, w[u][m][0].w, w[u][m][1].w, x[u][n].z, x[u][n].w);
+                }
+        if (p + U * kWarps < p1) load_w(p + U * kWarps);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                part[warp][(8 * n + 2 * t + (i & 1)) * R + 16 * m + 8 * (i >> 1) + g] = c[m][n][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < R * T; i += kThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) s += part[k][i];
+        sum[i] = s;
+    }
+    if (cluster > 1) {
+        tc::cluster_sync();
+        if (rank == 0) {
+            for (int i = threadIdx.x; i < R * T; i += kThreads) {
+                float s = sum[i];
+                for (uint32_t k = 1; k < cluster; ++k) {
+                    float v;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(v)
+                                 : "r"(tc::mapa(tc::saddr(&sum[i]), k))
+                                 : "memory");
+                    s += v;
+                }
+                part[0][i] = s;
+            }
+        }
+        tc::cluster_sync();  // the leader has read the others' shared memory
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
+    const float* v = cluster > 1 ? part[0] : sum;
+    if constexpr (kKind == OPS_STORE) {
+        for (int i = threadIdx.x; i < R * T; i += kThreads) {
+            const int tok = i / R, n = n0 + i % R;
+            if (tok < P.tokens && n < P.N) st1(P.out0, tok, n, v[i]);
+        }
+    } else if constexpr (kKind == OPS_GATE) {
+        for (int i = threadIdx.x; i < R * T / 2; i += kThreads) {
+            const int tok = i / (R / 2), j = i % (R / 2), n = n0 + j;
+            const int at = tok * R + 16 * (j / 8) + j % 8;
+            if (tok >= P.tokens || n >= P.N) continue;
+            const float a = v[at], u = v[at + 8];
+            const float gate = act_gate<false>(P.act, a), f = a * gate;
+            if (P.out1.p) {
+                st1(P.out1, tok, n, f);
+                st1(P.out2, tok, n, u * act_slope<false>(P.act, a, gate));
+                if (P.out3.p) st1(P.out3, tok, n, f * u);
+            }
+            st1(P.out0, tok, n, f * u);
+        }
+    } else {
+        // R lanes per token: maximum and sum of exponentials of the block's columns
+        const float ninf = __int_as_float(0xff800000);
+        for (int i = threadIdx.x; i < R * T; i += kThreads) {
+            const int tok = i / R, n = n0 + i % R;
+            const float z = n < P.N ? v[i] : ninf;
+            float m = z;
+#pragma unroll
+            for (int o = R / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(tc::kFullMask, m, o));
+            const float e = ex2((z - m) * kLog2e);
+            float s = e;
+#pragma unroll
+            for (int o = R / 2; o; o >>= 1) s += __shfl_xor_sync(tc::kFullMask, s, o);
+            if (tok >= P.tokens || n >= P.N) continue;
+            if (P.targets[tok] == n) P.target_logit[tok] = z;
+            if (P.out0.p) st1(P.out0, tok, n, e);
+            if (i % R == 0) P.stats[static_cast<int64_t>(tok) * P.nblk + tile] = make_float2(m, s);
+        }
+    }
+}
+
+using Kernel = void (*)(OpsStream);
+
+template <int kKind>
+Kernel pick(int tokens) {
+    if (tokens <= 8) return ops_stream_kernel<kKind, 1, 1>;
+    if (tokens <= 16) return ops_stream_kernel<kKind, 2, 2>;
+    return ops_stream_kernel<kKind, 4, 2>;
+}
+
+}  // namespace
+
+int ops_stream_block(int64_t tokens) { return tokens <= 8 ? 16 : 32; }
+
+cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static PerDevice count;
+    e = count.get(dev, &sms, [&](int* out) { return cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev); });
+    if (e != cudaSuccess) return e;
+    const int rows = (a.tokens <= 8 ? 16 : 32) / (kind == OPS_GATE ? 2 : 1);
+    const int tiles = (a.N + rows - 1) / rows;
+    // at least about six blocks per SM, so the last round is short; a block keeps
+    // at least two rounds of its eight warps
+    int cluster = 1;
+    while (cluster < 8 && tiles * cluster < 6 * sms && a.K / (cluster * 2) >= 2 * 32 * kWarps) cluster *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(tiles * cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const Kernel k = kind == OPS_GATE ? pick<OPS_GATE>(a.tokens)
+                     : kind == OPS_LOGITS ? pick<OPS_LOGITS>(a.tokens)
+                                          : pick<OPS_STORE>(a.tokens);
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+}  // namespace dmuon

@@ -15,8 +15,6 @@ reused from call to call on one stream.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib
@@ -39,52 +37,59 @@ def _act(name):
     return _ACTS[name]
 
 
-def _check(where, like, **tensors):
-    """Every given tensor: CUDA, contiguous, on like's device, of the given dtype and shape."""
-    dev = like.device
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda or t.device != dev:
-            raise ValueError(f"{where}: {name} must be a CUDA tensor on the device of the first argument")
-        if t.dtype != dtype:
-            raise ValueError(f"{where}: {name} must be {dtype}, not {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous")
+def _refuse(where, name, t, dtype, shape, dev):
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{where}: {name} must be a CUDA tensor on the device of the first argument")
+    if t.dtype is not dtype:
+        raise ValueError(f"{where}: {name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{where}: {name} must be contiguous")
 
 
-@contextlib.contextmanager
-def _launch(stream, tensors):
-    """The raw stream handle of a call, with its device and stream current (outputs are
-    allocated there) and the inputs kept alive for it."""
+def _check(where, dev, dt, *tensors):
+    """Every (name, tensor, shape): on CUDA device dev, of dtype dt, of that shape, contiguous."""
+    for name, t, shape in tensors:
+        if t is not None and not (t.is_cuda and t.dtype is dt and t.shape == shape and t.is_contiguous()
+                                  and t.device == dev):
+            _refuse(where, name, t, dt, shape, dev)
+
+
+def _elsewhere(stream, dev):
+    """The call has to run under another device or stream than the current one."""
+    return stream is not None or torch.cuda.current_device() != dev.index
+
+
+def _run_elsewhere(stream, tensors, call):
+    """call() with the tensors' device and the given stream current, so that outputs are
+    allocated there; the inputs are kept alive for that stream."""
     dev = tensors[0].device
     with torch.cuda.device(dev):
-        cur = torch.cuda.current_stream()
-        if stream is None:
-            yield cur.cuda_stream
-            return
-        st = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+        cur = torch.cuda.current_stream(dev)
+        st = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream or cur
         with torch.cuda.stream(st):
-            yield st.cuda_stream
+            out = call()
         if st.cuda_stream != cur.cuda_stream:
             for t in tensors:
                 if t is not None:
                     t.record_stream(st)
+        return out
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream without building an object
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _space(workspace, nbytes, device):
-    """(pointer, bytes, tensor) of the caller's workspace, or of a new one."""
+def _space(workspace, need, device):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one of need() bytes."""
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need(), dtype=torch.uint8, device=device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace.data_ptr() if nbytes else None, workspace.numel() * workspace.element_size(), workspace
+    return workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), workspace
 
 
 def ops_status() -> int:
@@ -96,16 +101,21 @@ def ops_status() -> int:
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, stream=None):
     """``(y, mean, rstd)`` of a layer norm over the last dimension (weight, bias optional)."""
-    cols = x.shape[-1]
-    _check("layer_norm", x, x=(x, x.dtype, x.shape), weight=(weight, x.dtype, (cols,)), bias=(bias, x.dtype, (cols,)))
+    dt, dev, shape = x.dtype, x.device, x.shape
+    cols = shape[-1]
+    _check("layer_norm", dev, dt, ("x", x, shape), ("weight", weight, (cols,)), ("bias", bias, (cols,)))
     rows = x.numel() // cols if cols else 0
-    with _launch(stream, (x, weight, bias)) as s:
-        y = torch.empty_like(x)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-        _lib.check(_lib.load().dmuon_layer_norm_forward(x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(),
-                                                        mean.data_ptr(), rstd.data_ptr(), rows, cols, _dtype(x.dtype),
-                                                        eps, s), "dmuon_layer_norm_forward")
+
+    if _elsewhere(stream, dev):
+        return _run_elsewhere(stream, (x, weight, bias),
+                              lambda: layer_norm(x, weight, bias, eps))
+    s = _raw_stream(dev.index)
+    y = torch.empty_like(x)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
+    st = _lib.load().dmuon_layer_norm_forward(x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(),
+                                              mean.data_ptr(), rstd.data_ptr(), rows, cols, _dtype(dt), eps, s)
+    _lib.check(st, "dmuon_layer_norm_forward")
     return y, mean, rstd
 
 
@@ -116,21 +126,24 @@ def layer_norm_workspace(rows, cols, dtype="bf16") -> int:
 
 def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None, stream=None):
     """``(dx, dweight, dbias)`` from the forward pass's input and statistics."""
-    cols = x.shape[-1]
-    _check("layer_norm_backward", x, x=(x, x.dtype, x.shape), dy=(dy, x.dtype, x.shape),
-           weight=(weight, x.dtype, (cols,)), mean=(mean, torch.float32, x.shape[:-1]),
-           rstd=(rstd, torch.float32, x.shape[:-1]))
+    dt, dev, shape = x.dtype, x.device, x.shape
+    cols = shape[-1]
+    _check("layer_norm_backward", dev, dt, ("x", x, shape), ("dy", dy, shape), ("weight", weight, (cols,)))
+    _check("layer_norm_backward", dev, torch.float32, ("mean", mean, shape[:-1]), ("rstd", rstd, shape[:-1]))
     rows = x.numel() // cols if cols else 0
-    nbytes = layer_norm_workspace(rows, cols, x.dtype)
-    with _launch(stream, (x, dy, weight, mean, rstd, workspace)) as s:
-        dx = torch.empty_like(x)
-        dw = torch.empty(cols, dtype=x.dtype, device=x.device)
-        db = torch.empty_like(dw)
-        wp, wb, _keep = _space(workspace, nbytes, x.device)
-        _lib.check(_lib.load().dmuon_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
-                                                         rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr(),
-                                                         rows, cols, _dtype(x.dtype), wp, wb, s),
-                   "dmuon_layer_norm_backward")
+
+    if _elsewhere(stream, dev):
+        return _run_elsewhere(stream, (x, dy, weight, mean, rstd, workspace),
+                              lambda: layer_norm_backward(dy, x, weight, mean, rstd, workspace))
+    s = _raw_stream(dev.index)
+    dx = torch.empty_like(x)
+    dw = torch.empty(cols, dtype=dt, device=dev)
+    db = torch.empty_like(dw)
+    wp, wb, _keep = _space(workspace, lambda: layer_norm_workspace(rows, cols, dt), dev)
+    st = _lib.load().dmuon_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
+                                               rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows,
+                                               cols, _dtype(dt), wp, wb, s)
+    _lib.check(st, "dmuon_layer_norm_backward")
     return dx, dw, db
 
 
@@ -143,47 +156,59 @@ def gated_ffn_workspace(tokens, dim, hidden, dtype="bf16", backward=False) -> in
 
 
 def gated_ffn(x, w_gate, w_up, w_down, activation="silu", save=False, workspace=None, stream=None):
-    """``y = (act(x w_gate^T) * (x w_up^T)) w_down^T``; with ``save`` ``(y, gate, up)``, the
-    projections that the backward pass reads."""
-    dim, hidden = x.shape[-1], w_gate.shape[0]
+    """``y = h w_down^T`` with ``h = act(a) * u``, ``a = x w_gate^T``, ``u = x w_up^T``; with
+    ``save`` ``(y, saved, h)``, what the backward pass reads: ``saved`` is the pair
+    ``(act(a), u act'(a))``."""
+    dt, dev, shape = x.dtype, x.device, x.shape
+    dim, hidden = shape[-1], w_gate.shape[0]
     tokens = x.numel() // dim if dim else 0
-    _check("gated_ffn", x, x=(x, x.dtype, x.shape), w_gate=(w_gate, x.dtype, (hidden, dim)),
-           w_up=(w_up, x.dtype, (hidden, dim)), w_down=(w_down, x.dtype, (dim, hidden)))
+    _check("gated_ffn", dev, dt, ("x", x, shape), ("w_gate", w_gate, (hidden, dim)), ("w_up", w_up, (hidden, dim)),
+           ("w_down", w_down, (dim, hidden)))
     act = _act(activation)
-    nbytes = gated_ffn_workspace(tokens, dim, hidden, x.dtype)
-    with _launch(stream, (x, w_gate, w_up, w_down, workspace)) as s:
-        y = torch.empty_like(x)
-        gate = up = None
-        if save:
-            gate = torch.empty(*x.shape[:-1], hidden, dtype=x.dtype, device=x.device)
-            up = torch.empty_like(gate)
-        wp, wb, _keep = _space(workspace, nbytes, x.device)
-        _lib.check(_lib.load().dmuon_gated_ffn_forward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-                                                       w_down.data_ptr(), y.data_ptr(), _ptr(gate), _ptr(up), tokens,
-                                                       dim, hidden, _dtype(x.dtype), act, wp, wb, s),
-                   "dmuon_gated_ffn_forward")
-    return (y, gate, up) if save else y
+
+    if _elsewhere(stream, dev):
+        return _run_elsewhere(stream, (x, w_gate, w_up, w_down, workspace),
+                              lambda: gated_ffn(x, w_gate, w_up, w_down, activation, save, workspace))
+    s = _raw_stream(dev.index)
+    y = torch.empty_like(x)
+    saved, h = (None, None), None
+    if save:
+        h = torch.empty(*shape[:-1], hidden, dtype=dt, device=dev)
+        saved = (torch.empty_like(h), torch.empty_like(h))
+    wp, wb, _keep = _space(workspace, lambda: gated_ffn_workspace(tokens, dim, hidden, dt), dev)
+    st = _lib.load().dmuon_gated_ffn_forward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+                                             y.data_ptr(), _ptr(saved[0]), _ptr(saved[1]), _ptr(h), tokens, dim,
+                                             hidden, _dtype(dt), act, wp, wb, s)
+    _lib.check(st, "dmuon_gated_ffn_forward")
+    return (y, saved, h) if save else y
 
 
-def gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, activation="silu", workspace=None, stream=None):
-    """``(dx, dw_gate, dw_up, dw_down)``, the weights' gradients ready for the Muon step."""
-    dim, hidden = x.shape[-1], w_gate.shape[0]
+def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, h, activation="silu", workspace=None, stream=None):
+    """``(dx, dw_gate, dw_up, dw_down)``, the weights' gradients ready for the Muon step.
+
+    ``saved`` already holds the activation and its slope; ``activation`` is only checked, so
+    that both passes take the same keywords."""
+    dt, dev, shape = x.dtype, x.device, x.shape
+    dim, hidden = shape[-1], w_gate.shape[0]
     tokens = x.numel() // dim if dim else 0
-    inner = (*x.shape[:-1], hidden)
-    _check("gated_ffn_backward", x, x=(x, x.dtype, x.shape), dy=(dy, x.dtype, x.shape),
-           w_gate=(w_gate, x.dtype, (hidden, dim)), w_up=(w_up, x.dtype, (hidden, dim)),
-           w_down=(w_down, x.dtype, (dim, hidden)), gate=(gate, x.dtype, inner), up=(up, x.dtype, inner))
-    act = _act(activation)
-    nbytes = gated_ffn_workspace(tokens, dim, hidden, x.dtype, backward=True)
-    with _launch(stream, (x, dy, w_gate, w_up, w_down, gate, up, workspace)) as s:
-        dx = torch.empty_like(x)
-        dwg, dwu, dwd = torch.empty_like(w_gate), torch.empty_like(w_up), torch.empty_like(w_down)
-        wp, wb, _keep = _space(workspace, nbytes, x.device)
-        _lib.check(_lib.load().dmuon_gated_ffn_backward(dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
-                                                        w_up.data_ptr(), w_down.data_ptr(), gate.data_ptr(),
-                                                        up.data_ptr(), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
-                                                        dwd.data_ptr(), tokens, dim, hidden, _dtype(x.dtype), act, wp,
-                                                        wb, s), "dmuon_gated_ffn_backward")
+    inner = (*shape[:-1], hidden)
+    _check("gated_ffn_backward", dev, dt, ("x", x, shape), ("dy", dy, shape), ("w_gate", w_gate, (hidden, dim)),
+           ("w_up", w_up, (hidden, dim)), ("w_down", w_down, (dim, hidden)), ("saved[0]", saved[0], inner),
+           ("saved[1]", saved[1], inner), ("h", h, inner))
+    _act(activation)
+
+    if _elsewhere(stream, dev):
+        return _run_elsewhere(stream, (x, dy, w_gate, w_up, w_down, *saved, h, workspace),
+                              lambda: gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, h, activation, workspace))
+    s = _raw_stream(dev.index)
+    dx = torch.empty_like(x)
+    dwg, dwu, dwd = torch.empty_like(w_gate), torch.empty_like(w_up), torch.empty_like(w_down)
+    wp, wb, _keep = _space(workspace, lambda: gated_ffn_workspace(tokens, dim, hidden, dt, backward=True), dev)
+    st = _lib.load().dmuon_gated_ffn_backward(dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                                              w_down.data_ptr(), saved[0].data_ptr(), saved[1].data_ptr(),
+                                              h.data_ptr(), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
+                                              dwd.data_ptr(), tokens, dim, hidden, _dtype(dt), wp, wb, s)
+    _lib.check(st, "dmuon_gated_ffn_backward")
     return dx, dwg, dwu, dwd
 
 
@@ -195,22 +220,27 @@ def vocab_loss_workspace(tokens, dim, vocab, dtype="bf16", grad=False, budget=0)
 
 
 def _vocab_loss(where, x, weight, targets, coef, ignore_index, workspace, budget, stream, grad):
+    dt, dev, rows = x.dtype, x.device, x.shape[:-1]
     dim, vocab = x.shape[-1], weight.shape[0]
     tokens = x.numel() // dim if dim else 0
-    rows = x.shape[:-1]
-    _check(where, x, x=(x, x.dtype, x.shape), weight=(weight, x.dtype, (vocab, dim)),
-           targets=(targets, torch.int64, rows), coef=(coef, torch.float32, rows))
-    nbytes = vocab_loss_workspace(tokens, dim, vocab, x.dtype, grad, budget)
-    with _launch(stream, (x, weight, targets, coef, workspace)) as s:
-        loss = torch.empty(rows, dtype=torch.float32, device=x.device)
-        lse = torch.empty_like(loss)
-        dx = torch.empty_like(x) if grad else None
-        dw = torch.empty_like(weight) if grad else None
-        wp, wb, _keep = _space(workspace, nbytes, x.device)
-        _lib.check(_lib.load().dmuon_vocab_loss(x.data_ptr(), weight.data_ptr(), targets.data_ptr(), _ptr(coef),
-                                                ignore_index, loss.data_ptr(), lse.data_ptr(), _ptr(dx), _ptr(dw),
-                                                tokens, dim, vocab, _dtype(x.dtype), budget, wp, wb, s),
-                   "dmuon_vocab_loss")
+    _check(where, dev, dt, ("x", x, x.shape), ("weight", weight, (vocab, dim)))
+    _check(where, dev, torch.int64, ("targets", targets, rows))
+    _check(where, dev, torch.float32, ("coef", coef, rows))
+
+    if _elsewhere(stream, dev):
+        return _run_elsewhere(stream, (x, weight, targets, coef, workspace),
+                              lambda: _vocab_loss(where, x, weight, targets, coef, ignore_index, workspace, budget, None,
+                                                  grad))
+    s = _raw_stream(dev.index)
+    loss = torch.empty(rows, dtype=torch.float32, device=dev)
+    lse = torch.empty_like(loss)
+    dx = torch.empty_like(x) if grad else None
+    dw = torch.empty_like(weight) if grad else None
+    wp, wb, _keep = _space(workspace, lambda: vocab_loss_workspace(tokens, dim, vocab, dt, grad, budget), dev)
+    st = _lib.load().dmuon_vocab_loss(x.data_ptr(), weight.data_ptr(), targets.data_ptr(), _ptr(coef),
+                                      ignore_index, loss.data_ptr(), lse.data_ptr(), _ptr(dx), _ptr(dw), tokens,
+                                      dim, vocab, _dtype(dt), budget, wp, wb, s)
+    _lib.check(st, "dmuon_vocab_loss")
     return loss, lse, dx, dw
 
 

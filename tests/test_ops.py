@@ -97,14 +97,16 @@ def test_gated_ffn_refusals(lib):
     # fp32 operands are packed into bf16 parts
     assert lib.dmuon_gated_ffn_workspace_bytes(4, 64, 128, _lib.FP32, 0) > need + 6 * 3 * 64 * 128
 
-    def fwd(x=P16, y=P16, gate=P16, up=P16, tokens=4, dim=64, hidden=128, dtype=_lib.BF16, act=0, ws=P16, n=need):
-        return lib.dmuon_gated_ffn_forward(x, P16, P16, P16, y, gate, up, tokens, dim, hidden, dtype, act, ws, n, None)
+    def fwd(x=P16, y=P16, slope=P16, h=P16, tokens=4, dim=64, hidden=128, dtype=_lib.BF16, act=0, ws=P16, n=need):
+        return lib.dmuon_gated_ffn_forward(x, P16, P16, P16, y, P16, slope, h, tokens, dim, hidden, dtype, act, ws, n,
+                                           None)
 
     for bad in (dict(tokens=-1), dict(tokens=(1 << 24) + 1), dict(dim=0), dict(hidden=0), dict(hidden=1 << 21)):
         assert fwd(**bad) == _lib.ERR_INVALID_ARG
     assert fwd(dtype=7) == _lib.ERR_UNSUPPORTED_DTYPE
     assert fwd(act=2) == _lib.ERR_INVALID_ARG and "activation" in err(lib)
-    assert fwd(up=None) == _lib.ERR_INVALID_ARG and "together" in err(lib)
+    assert fwd(slope=None) == _lib.ERR_INVALID_ARG and "together" in err(lib)
+    assert fwd(h=None) == _lib.ERR_INVALID_ARG
     assert fwd(x=None) == _lib.ERR_INVALID_ARG
     assert fwd(y=P16 + 4) == _lib.ERR_ALIGN
     assert fwd(ws=None) == _lib.ERR_NO_WORKSPACE
@@ -113,8 +115,8 @@ def test_gated_ffn_refusals(lib):
     assert fwd(tokens=0, ws=None) == _lib.OK
 
     def bwd(dy=P16, dwd=P16, ws=P16, n=back):
-        return lib.dmuon_gated_ffn_backward(dy, P16, P16, P16, P16, P16, P16, P16, P16, P16, dwd, 4, 64, 128,
-                                            _lib.BF16, 0, ws, n, None)
+        return lib.dmuon_gated_ffn_backward(dy, P16, P16, P16, P16, P16, P16, P16, P16, P16, P16, dwd, 4, 64, 128,
+                                            _lib.BF16, ws, n, None)
 
     assert bwd(dy=None) == _lib.ERR_INVALID_ARG
     assert bwd(dwd=P16 + 2) == _lib.ERR_ALIGN
@@ -286,7 +288,8 @@ def ffn_inputs(n, d, f, dt, seed):
 
 
 FFN_SHAPES = [(1, 64, 128), (1, 1, 1), (2, 72, 200), (17, 128, 96), (129, 64, 257), (257, 200, 384), (300, 101, 333),
-              (512, 256, 768), (31, 2048, 512), (5, 64, 5000), (1000, 520, 264), (64, 4096, 64)]
+              (512, 256, 768), (31, 2048, 512), (5, 64, 5000), (1000, 520, 264), (64, 4096, 64),
+              (8, 2056, 104), (16, 40, 1032), (23, 1032, 2000), (32, 8, 8), (9, 520, 7)]
 
 
 @pytest.mark.gpu
@@ -296,32 +299,36 @@ def test_gated_ffn(n, d, f, dtype):
     dt = DT[dtype]
     act = "gelu" if (n + d + f) % 2 else "silu"
     x, wg, wu, wd, dy = ffn_inputs(n, d, f, dt, n * 7 + d * 3 + f)
-    y, gate, up = pkg.gated_ffn(x, wg, wu, wd, activation=act, save=True)
+    y, (f_act, f_slope), h_out = pkg.gated_ffn(x, wg, wu, wd, activation=act, save=True)
     assert torch.equal(y, pkg.gated_ffn(x, wg, wu, wd, activation=act))
     X, G, UP, D, DY = (t.double() for t in (x, wg, wu, wd, dy))
     u = U[dt]
     ea, eu = X @ G.T, X @ UP.T
     da_, du_ = acc(d, dt) * (X.abs() @ G.abs().T), acc(d, dt) * (X.abs() @ UP.abs().T)
-    within(gate, ea, u * ea.abs() + da_, "gate")
-    within(up, eu, u * eu.abs() + du_, "up")
     p, dp, dpb = act64(ea, act)
     h = p * eu
-    # |act'| <= 1.13; the operand h is rounded once for bf16
+    # |act'| <= 1.13 and |act''| <= 0.8
+    perr = FN * p.abs() + 1.2 * da_
+    within(f_act, p, u * p.abs() + (1 + u) * perr, "act")
+    serr = FN * dpb + 0.8 * da_
+    within(f_slope, dp * eu, u * (dp * eu).abs() + (1 + u) * (serr * (eu.abs() + du_) + dpb * du_), "slope")
+    herr = FN * h.abs() + 1.2 * (da_ * eu.abs() + du_ * p.abs() + da_ * du_)
+    within(h_out, h, u * h.abs() + (1 + u) * herr, "h")
+    # the operand h is rounded once for bf16
     op = u if dt == torch.bfloat16 else 0.0
-    herr = op * h.abs() + FN * h.abs() + 1.2 * (da_ * eu.abs() + du_ * p.abs() + da_ * du_)
+    herr = op * h.abs() + (1 + op) * herr
     ey = h @ D.T
     within(y, ey, u * ey.abs() + (1 + u) * (herr @ D.abs().T + acc(f, dt) * (h.abs() @ D.abs().T)), "y")
 
-    dx, dwg, dwu, dwd = pkg.gated_ffn_backward(dy, x, wg, wu, wd, gate, up, activation=act)
-    a, uu = gate.double(), up.double()
-    p, dp, dpb = act64(a, act)
-    h = p * uu
+    dx, dwg, dwu, dwd = pkg.gated_ffn_backward(dy, x, wg, wu, wd, (f_act, f_slope), h_out, activation=act)
+    # the backward pass's own formula from the tensors it is given
+    h = h_out.double()
     dh = DY @ D
     eh = acc(d, dt) * (DY.abs() @ D.abs())
-    da, du = dh * uu * dp, dh * p
-    hb = (op + FN) * h.abs() + TINY
-    dab = (1 + op) * eh * uu.abs() * dpb + (op + FN) * dh.abs() * uu.abs() * dpb
-    dub = (1 + op) * eh * p.abs() + (op + FN) * dh.abs() * p.abs()
+    da, du = dh * f_slope.double(), dh * f_act.double()
+    hb = 0 * h
+    dab = (1 + op) * eh * f_slope.double().abs() + (op + FN) * da.abs()
+    dub = (1 + op) * eh * f_act.double().abs() + (op + FN) * du.abs()
     for name, got, want, bound in (
             ("dx", dx, da @ G + du @ UP, dab @ G.abs() + dub @ UP.abs()
              + acc(2 * f, dt) * (da.abs() @ G.abs() + du.abs() @ UP.abs())),
@@ -340,13 +347,13 @@ def test_gated_ffn_repeats_bitwise_and_leading_dimensions():
     first = None
     for _ in range(5):
         ws.random_(0, 255)  # nothing is kept between calls
-        y, gate, up = pkg.gated_ffn(x, wg, wu, wd, save=True, workspace=ws)
-        out = (y, gate, up, *pkg.gated_ffn_backward(dy, x, wg, wu, wd, gate, up, workspace=ws))
+        y, saved, h = pkg.gated_ffn(x, wg, wu, wd, save=True, workspace=ws)
+        out = (y, *saved, h, *pkg.gated_ffn_backward(dy, x, wg, wu, wd, saved, h, workspace=ws))
         if first is None:
             first = [t.clone() for t in out]
         assert all(torch.equal(a, b) for a, b in zip(out, first))
-    y3, gate3, _ = pkg.gated_ffn(x.view(4, 24, 1024), wg, wu, wd, save=True)
-    assert y3.shape == (4, 24, 1024) and gate3.shape == (4, 24, 1536) and torch.equal(y3.view(96, 1024), first[0])
+    y3, saved3, h3 = pkg.gated_ffn(x.view(4, 24, 1024), wg, wu, wd, save=True)
+    assert y3.shape == (4, 24, 1024) and h3.shape == (4, 24, 1536) and torch.equal(y3.view(96, 1024), first[0])
 
 
 @pytest.mark.gpu
@@ -358,14 +365,14 @@ def test_gated_ffn_saturated_and_empty():
         w = torch.zeros(8, 8, device="cuda", dtype=torch.bfloat16)
         w[:, 0] = 1
         eye = torch.eye(8, device="cuda", dtype=torch.bfloat16)
-        y, gate, up = pkg.gated_ffn(x, w, w, eye, activation=act, save=True)
+        y, saved, h = pkg.gated_ffn(x, w, w, eye, activation=act, save=True)
         assert (y[0] == torch.tensor(90000.0, device="cuda").bfloat16()).all() and (y[1] == 0).all()
-        dx, dwg, dwu, dwd = pkg.gated_ffn_backward(torch.ones_like(y), x, w, w, eye, gate, up, activation=act)
+        dx, dwg, dwu, dwd = pkg.gated_ffn_backward(torch.ones_like(y), x, w, w, eye, saved, h, activation=act)
         assert torch.isfinite(dx).all() and torch.isfinite(dwg).all()
         assert (dx[0, 0] == 4800.0) and (dx[1] == 0).all()  # 8 (u act' + act) = 8 (300 + 300)
     e = torch.empty(0, 8, device="cuda", dtype=torch.bfloat16)
-    y, gate, up = pkg.gated_ffn(e, w, w, eye, save=True)
-    dx, dwg, dwu, dwd = pkg.gated_ffn_backward(e, e, w, w, eye, gate, up)
+    y, saved, h = pkg.gated_ffn(e, w, w, eye, save=True)
+    dx, dwg, dwu, dwd = pkg.gated_ffn_backward(e, e, w, w, eye, saved, h)
     assert y.shape == (0, 8) and not dwg.any() and not dwu.any() and not dwd.any()
 
 
@@ -416,7 +423,7 @@ def check_loss(x, w, t, coef, out, ignore=-100):
 
 
 LOSS_SHAPES = [(1, 64, 1), (1, 64, 1000), (3, 1, 5), (2, 8, 129), (17, 100, 255), (130, 64, 1003), (257, 136, 640),
-               (300, 512, 10007), (5, 2048, 700), (600, 72, 128)]
+               (300, 512, 10007), (5, 2048, 700), (600, 72, 128), (8, 40, 33), (16, 1032, 4099), (32, 264, 1000)]
 
 
 @pytest.mark.gpu
@@ -520,14 +527,14 @@ def test_gradients_against_differences():
 
     def forward(q, grads=False):
         y1, m1, r1 = pkg.layer_norm(q["x"], q["w1"], q["b1"])
-        h, gate, up = pkg.gated_ffn(y1, q["wg"], q["wu"], q["wd"], save=True)
-        z = q["x"] + h
+        f1, saved, h = pkg.gated_ffn(y1, q["wg"], q["wu"], q["wd"], save=True)
+        z = q["x"] + f1
         y2, m2, r2 = pkg.layer_norm(z, q["w2"], q["b2"])
         if not grads:
             return float((pkg.vocab_loss(y2, q["wv"], t)[0].double() * coef.double()).sum())
         _, _, dy2, dwv = pkg.vocab_loss_grad(y2, q["wv"], t, coef=coef)
         dz, dw2, db2 = pkg.layer_norm_backward(dy2, z, q["w2"], m2, r2)
-        dy1, dwg, dwu, dwd = pkg.gated_ffn_backward(dz, y1, q["wg"], q["wu"], q["wd"], gate, up)
+        dy1, dwg, dwu, dwd = pkg.gated_ffn_backward(dz, y1, q["wg"], q["wu"], q["wd"], saved, h)
         dx, dw1, db1 = pkg.layer_norm_backward(dy1, q["x"], q["w1"], m1, r1)
         return {"x": dx + dz, "w1": dw1, "b1": db1, "wg": dwg, "wu": dwu, "wd": dwd, "w2": dw2, "b2": db2, "wv": dwv}
 
@@ -550,9 +557,9 @@ def test_operators_on_another_stream_and_in_a_graph():
 
     def work(stream=None):
         y, m, r = pkg.layer_norm(x, stream=stream)
-        z, gate, up = pkg.gated_ffn(y, wg, wu, wd, save=True, workspace=ws, stream=stream)
+        z, saved, h = pkg.gated_ffn(y, wg, wu, wd, save=True, workspace=ws, stream=stream)
         loss, _, dz, _ = pkg.vocab_loss_grad(z, wg, t, workspace=ws, stream=stream)
-        dyy, *dws = pkg.gated_ffn_backward(dz, y, wg, wu, wd, gate, up, workspace=ws, stream=stream)
+        dyy, *dws = pkg.gated_ffn_backward(dz, y, wg, wu, wd, saved, h, workspace=ws, stream=stream)
         return (loss, pkg.layer_norm_backward(dyy, x, None, m, r, stream=stream)[0], *dws)
 
     want = [o.clone() for o in work()]
