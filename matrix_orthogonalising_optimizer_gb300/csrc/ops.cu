@@ -71,9 +71,17 @@ struct Common {
         l.tail_count = counters + kMaxLaunches * 64 + launch * kTailInts;
         l.partials = partials;
     }
-    cudaError_t clear(int launches, cudaStream_t s) const {
-        const int64_t ints = launches <= 0 ? 0 : kMaxLaunches * 64 + launches * kTailInts;
-        return cudaMemsetAsync(counters, 0, ints * sizeof(int32_t), s);
+    // Zeroes the counters that the scheduled launches use (none where every
+    // unit is some pair's first and no tile is split).
+    cudaError_t clear(const OpsLaunch* l, int launches, int pairs, cudaStream_t s) const {
+        int64_t ints = 0;
+        for (int i = 0; i < launches; ++i) {
+            bool split = false;
+            for (int k = 0; k < l[i].n; ++k) split = split || l[i].p[k].split > 1;
+            if (split) ints = kMaxLaunches * 64 + (i + 1) * kTailInts;
+            else if (l[i].total_units > pairs) ints = std::max<int64_t>(ints, (i + 1) * 64);
+        }
+        return ints ? cudaMemsetAsync(counters, 0, ints * sizeof(int32_t), s) : cudaSuccess;
     }
 };
 
@@ -217,6 +225,8 @@ int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a
     const int na = dual ? 1 : sources;
     for (int s = 0; s < na; ++s) OPS_TRY(encode(&P.a[s], a[s], a_mn));
     for (int s = 0; s < sources; ++s) OPS_TRY(encode(&P.b[s], b[s], b_mn));
+    P.maps_a = na;
+    P.maps_b = sources;
     P.M = static_cast<int32_t>(M);
     P.N = static_cast<int32_t>(N);
     P.slabs = static_cast<int32_t>(ceil_div(K, 64));
@@ -235,12 +245,16 @@ int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a
     return DMUON_OK;
 }
 
-int run_gemm(OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s, const char* where) {
+// Schedules a call's launches and zeroes the counters they need.
+int schedule(OpsLaunch* l, int launches, const Common& common, cudaStream_t s, const char* where) {
     int pairs = 0;
     OPS_CUDA(ops_pairs(&pairs));
-    l.chain = kChain;
-    ops_schedule(l, pairs, kSlots, kTails);
-    OPS_CUDA(launch_ops_gemm(l, kind, f32, s));
+    for (int i = 0; i < launches; ++i) {
+        l[i].chain = kChain;
+        common.bind(l[i], i);
+        ops_schedule(l[i], pairs, kSlots, kTails);
+    }
+    OPS_CUDA(common.clear(l, launches, pairs, s));
     return DMUON_OK;
 }
 
@@ -362,7 +376,7 @@ struct LossRowArgs {
     __nv_bfloat16* dz;          // logit gradients, kF32Parts parts for fp32
     int64_t ld, part, ignore;
     int64_t vocab;
-    int32_t nblk, block;        // statistics blocks of a row, columns per block
+    int32_t nblk, shift;        // statistics blocks of a row, log2 of their columns
     int32_t groups;             // 8-column groups of a row
     int32_t seg_groups;         // groups per blockIdx.y
 };
@@ -434,7 +448,7 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
                 v[2 * k + 1] = f.y;
             }
         }
-        const float scale = c * expf(st[c0 / a.block].x - lse);
+        const float scale = c * expf(st[c0 >> a.shift].x - lse);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             v[k] = valid ? v[k] * scale : 0.0f;
@@ -575,30 +589,25 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
         OPS_CUDA(launch_ops_stream(a, OPS_STORE, s));
         return DMUON_OK;
     }
-    OPS_CUDA(L.common.clear(2, s));
-    OPS_CUDA(L.pack.run(s));
-    {
-        OpsLaunch l = {};
-        l.n = 1;
-        L.common.bind(l, 0);
-        OpsProblem& P = l.p[0];
-        const Operand b[2] = {L.wg, L.wu};
-        OPS_TRY(set_problem(P, tokens, hidden, dim, &L.x, false, b, false, 2, true));
-        P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
-        P.out0 = out_of(L.h);
-        if (saved_act) {
-            P.out1 = user_mat(saved_act, hidden, f32);
-            P.out2 = user_mat(saved_slope, hidden, f32);
-            if (L.h.p != saved_h) P.out3 = user_mat(saved_h, hidden, f32);
-        }
-        OPS_TRY(run_gemm(l, OPS_GATE, f32, s, where));
+    OpsLaunch l[2] = {};
+    l[0].n = l[1].n = 1;
+    OpsProblem& P = l[0].p[0];
+    const Operand b[2] = {L.wg, L.wu};
+    OPS_TRY(set_problem(P, tokens, hidden, dim, &L.x, false, b, false, 2, true));
+    P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
+    P.out0 = out_of(L.h);
+    if (saved_act) {
+        P.out1 = user_mat(saved_act, hidden, f32);
+        P.out2 = user_mat(saved_slope, hidden, f32);
+        if (L.h.p != saved_h) P.out3 = user_mat(saved_h, hidden, f32);
     }
-    OpsLaunch l = {};
-    l.n = 1;
-    L.common.bind(l, 1);
-    OPS_TRY(set_problem(l.p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false));
-    l.p[0].out0 = user_mat(y, dim, f32);
-    return run_gemm(l, OPS_STORE, f32, s, where);
+    OPS_TRY(set_problem(l[1].p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false));
+    l[1].p[0].out0 = user_mat(y, dim, f32);
+    OPS_TRY(schedule(l, 2, L.common, s, where));
+    OPS_CUDA(L.pack.run(s));
+    OPS_CUDA(launch_ops_gemm(l[0], OPS_GATE, f32, s));
+    OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
+    return DMUON_OK;
 }
 
 extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up,
@@ -632,38 +641,35 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     FfnLayout L(static_cast<char*>(workspace), x, w_gate, w_up, w_down, dy, saved_h, tokens, dim, hidden, f32, true);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
-    OPS_CUDA(L.common.clear(2, s));
-    OPS_CUDA(L.pack.run(s));
-    {
-        // dh = dy Wd; the epilogue turns it into da and du
-        OpsLaunch l = {};
-        l.n = 1;
-        L.common.bind(l, 0);
-        OpsProblem& P = l.p[0];
-        OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false));
-        P.in0 = user_mat(saved_act, hidden, f32);
-        P.in1 = user_mat(saved_slope, hidden, f32);
-        P.out0 = out_of(L.da);
-        P.out1 = out_of(L.du);
-        OPS_TRY(run_gemm(l, OPS_DGATE, f32, s, where));
-    }
+    OpsLaunch l[2] = {};
+    // dh = dy Wd; the epilogue turns it into da and du
+    l[0].n = 1;
+    OpsProblem& P = l[0].p[0];
+    OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false));
+    P.in0 = user_mat(saved_act, hidden, f32);
+    P.in1 = user_mat(saved_slope, hidden, f32);
+    P.out0 = out_of(L.da);
+    P.out1 = out_of(L.du);
     // dx and the three weight gradients in one launch, the longest K first
-    OpsLaunch l = {};
-    l.n = 4;
-    L.common.bind(l, 1);
+    l[1].n = 4;
+    OpsProblem* p = l[1].p;
     const bool dx_first = 2 * hidden >= tokens;
     int k = dx_first ? 1 : 0;
-    OPS_TRY(set_problem(l.p[k], hidden, dim, tokens, &L.da, true, &L.x, true, 1, false));
-    l.p[k++].out0 = user_mat(dw_gate, dim, f32);
-    OPS_TRY(set_problem(l.p[k], hidden, dim, tokens, &L.du, true, &L.x, true, 1, false));
-    l.p[k++].out0 = user_mat(dw_up, dim, f32);
-    OPS_TRY(set_problem(l.p[k], dim, hidden, tokens, &L.dy, true, &L.h, true, 1, false));
-    l.p[k++].out0 = user_mat(dw_down, hidden, f32);
+    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.da, true, &L.x, true, 1, false));
+    p[k++].out0 = user_mat(dw_gate, dim, f32);
+    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.du, true, &L.x, true, 1, false));
+    p[k++].out0 = user_mat(dw_up, dim, f32);
+    OPS_TRY(set_problem(p[k], dim, hidden, tokens, &L.dy, true, &L.h, true, 1, false));
+    p[k++].out0 = user_mat(dw_down, hidden, f32);
     k = dx_first ? 0 : 3;
     const Operand a[2] = {L.da, L.du}, b[2] = {L.wg, L.wu};
-    OPS_TRY(set_problem(l.p[k], tokens, dim, hidden, a, false, b, true, 2, false));
-    l.p[k].out0 = user_mat(dx, dim, f32);
-    return run_gemm(l, OPS_STORE, f32, s, where);
+    OPS_TRY(set_problem(p[k], tokens, dim, hidden, a, false, b, true, 2, false));
+    p[k].out0 = user_mat(dx, dim, f32);
+    OPS_TRY(schedule(l, 2, L.common, s, where));
+    OPS_CUDA(L.pack.run(s));
+    OPS_CUDA(launch_ops_gemm(l[0], OPS_DGATE, f32, s));
+    OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
+    return DMUON_OK;
 }
 
 extern "C" size_t dmuon_vocab_loss_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab, int32_t dtype,
@@ -702,12 +708,38 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
     LossLayout L(static_cast<char*>(workspace), x, weight, tokens, dim, vocab, f32, grad, budget);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
-    OPS_CUDA(L.pack.run(s));
     const int64_t es = f32 ? 4 : 2;
     for (int64_t i = 0; i < L.pieces; ++i) {
         const int64_t r0 = i * L.piece, n = std::min(L.piece, tokens - r0);
-        if (grad || !L.stream) OPS_CUDA(L.common.clear(grad ? 2 : 1, s));
-        const Operand xp = rows_of(L.x, r0, n);
+        const Operand xp = rows_of(L.x, r0, n), dz = rows_of(L.dz, 0, n);
+        // logits; then, from dz, dx (K = vocab) and dW (K = the piece's tokens)
+        // in one launch
+        OpsLaunch l[2] = {};
+        if (!L.stream) {
+            l[0].n = 1;
+            OpsProblem& P = l[0].p[0];
+            OPS_TRY(set_problem(P, n, vocab, dim, &xp, false, &L.w, false, 1, false));
+            P.stats = L.stats;
+            P.nblk = L.nblk;
+            P.target_logit = L.target_logit;
+            P.targets = targets + r0;
+            if (grad) P.out0 = OpsMat{L.e, L.dz.ld, f32 ? ELEM_F32 : ELEM_BF16, 1, 0};
+        }
+        if (grad) {
+            l[1].n = 2;
+            const int kx = vocab >= n ? 0 : 1;
+            OPS_TRY(set_problem(l[1].p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false));
+            l[1].p[kx].out0 = user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
+            OpsProblem& W = l[1].p[1 - kx];
+            OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false));
+            // the sum over pieces stays in fp32: rounded once, with the last piece
+            const OpsMat sum = L.dw_sum ? user_mat(L.dw_sum, up(dim, 4), true) : user_mat(dweight, dim, f32);
+            const bool last = i + 1 == L.pieces;
+            W.out0 = last ? user_mat(dweight, dim, f32) : sum;
+            if (i > 0) W.in0 = sum;
+        }
+        OPS_TRY(schedule(l, 2, L.common, s, where));
+        if (i == 0) OPS_CUDA(L.pack.run(s));
         if (L.stream) {
             OpsStream a = stream_args(xp, L.w, vocab, dim);
             a.stats = L.stats;
@@ -717,17 +749,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             if (grad) a.out0 = out_of(L.dz);
             OPS_CUDA(launch_ops_stream(a, OPS_LOGITS, s));
         } else {
-            OpsLaunch l = {};
-            l.n = 1;
-            L.common.bind(l, 0);
-            OpsProblem& P = l.p[0];
-            OPS_TRY(set_problem(P, n, vocab, dim, &xp, false, &L.w, false, 1, false));
-            P.stats = L.stats;
-            P.nblk = L.nblk;
-            P.target_logit = L.target_logit;
-            P.targets = targets + r0;
-            if (grad) P.out0 = OpsMat{L.e, L.dz.ld, f32 ? ELEM_F32 : ELEM_BF16, 1, 0};
-            OPS_TRY(run_gemm(l, OPS_LOGITS, f32, s, where));
+            OPS_CUDA(launch_ops_gemm(l[0], OPS_LOGITS, f32, s));
         }
         LossRowArgs a = {};
         a.stats = L.stats;
@@ -739,7 +761,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         a.ignore = ignore_index;
         a.vocab = vocab;
         a.nblk = L.nblk;
-        a.block = L.block;
+        a.shift = L.block == 128 ? 7 : L.block == 32 ? 5 : 4;
         int segs = 1;
         if (grad) {
             a.e = L.e;
@@ -755,23 +777,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         if (f32) loss_row_kernel<true><<<grid, kRowThreads, 0, s>>>(a);
         else loss_row_kernel<false><<<grid, kRowThreads, 0, s>>>(a);
         OPS_CUDA(cudaGetLastError());
-        if (!grad) continue;
-        // dx (K = vocab) and dW (K = the piece's tokens) in one launch
-        const Operand dz = rows_of(L.dz, 0, n);
-        OpsLaunch l = {};
-        l.n = 2;
-        L.common.bind(l, 1);
-        const int kx = vocab >= n ? 0 : 1;
-        OPS_TRY(set_problem(l.p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false));
-        l.p[kx].out0 = user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
-        OpsProblem& W = l.p[1 - kx];
-        OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false));
-        // the sum over pieces stays in fp32: rounded once, with the last piece
-        const OpsMat sum = L.dw_sum ? user_mat(L.dw_sum, up(dim, 4), true) : user_mat(dweight, dim, f32);
-        const bool last = i + 1 == L.pieces;
-        W.out0 = last ? user_mat(dweight, dim, f32) : sum;
-        if (i > 0) W.in0 = sum;
-        OPS_TRY(run_gemm(l, OPS_STORE, f32, s, where));
+        if (grad) OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
     }
     return DMUON_OK;
 }

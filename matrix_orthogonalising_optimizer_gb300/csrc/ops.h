@@ -45,6 +45,7 @@ struct OpsMat {
 // 0..127 belong to the first and 128..255 to the second.
 struct OpsProblem {
     CUtensorMap a[2], b[2];
+    int32_t maps_a, maps_b;     // tensor maps in use
     int32_t M, N;
     int32_t slabs, nseg;
     uint16_t seg[kOpsMaxSegs];  // source | A part << 4 | B part << 8

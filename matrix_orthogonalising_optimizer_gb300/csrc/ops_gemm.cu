@@ -58,6 +58,7 @@ constexpr int kRegsLow = 56, kRegsEpi = 224;    // 56 + 2 x 224 = 3 x 168: the l
 constexpr uint32_t kTileReaders = kPair * kEpiWarps + 2;
 constexpr int CH = 16;
 constexpr uint16_t kPairMask = 3;
+constexpr int kStageLd = CH + 1;                // odd: rows and columns are both free of bank conflicts
 
 struct __align__(1024) Smem {
     uint8_t a[STAGES][OP_BYTES];
@@ -70,6 +71,7 @@ struct __align__(1024) Smem {
     uint64_t tile_empty[kTileRing];
     int32_t tile_slot[kTileRing];
     uint32_t tmem_base;
+    float stage[kEpiWarps][32 * kStageLd];  // a 32 x 16 chunk per epilogue warp (rows of unaligned matrices)
 };
 
 __host__ __device__ constexpr uint32_t make_idesc(bool a_mn, bool b_mn) {
@@ -132,130 +134,154 @@ __device__ __forceinline__ void release_tile(uint64_t* empty, int k) {
 // ------------------------------------------------------- matrix accesses
 // After tcgen05.ld lane i of a warp holds row r0 + i, columns c0 .. c0 + 15.
 // Whole chunks of 16-byte-aligned rows are regrouped between lanes so that one
-// instruction covers whole 32-byte sectors; others go element by element.  All
-// 32 lanes call these; rows >= M and columns >= N are not touched.
+// instruction covers whole 32-byte sectors; other chunks go through the warp's
+// slice of shared memory and move as two 16-element row segments per
+// instruction (element by element from each lane's own row, an instruction
+// touches 32 rows: six times the sectors).  All 32 lanes call these; rows >= M
+// and columns >= N are not touched.
+
+template <typename T>
+__device__ __forceinline__ void st_staged(T* base, int64_t ld, int r0, int c0, int lane, const float (&v)[CH], int M,
+                                          int N, float* stg) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) stg[lane * kStageLd + j] = v[j];
+    __syncwarp();
+    const int c = lane % CH;
+    T* p = base + static_cast<int64_t>(r0) * ld + c0 + c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + lane / CH;
+        const float x = stg[r * kStageLd + c];
+        if (r0 + r < M && c0 + c < N) {
+            if constexpr (sizeof(T) == 2) p[r * ld] = __float2bfloat16_rn(x);
+            else p[r * ld] = x;
+        }
+    }
+    __syncwarp();
+}
+
+template <typename T>
+__device__ __forceinline__ void ld_staged(const T* base, int64_t ld, int r0, int c0, int lane, float (&v)[CH], int M,
+                                          int N, float* stg) {
+    const int c = lane % CH;
+    const T* p = base + static_cast<int64_t>(r0) * ld + c0 + c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + lane / CH;
+        stg[r * kStageLd + c] = r0 + r < M && c0 + c < N ? static_cast<float>(p[r * ld]) : 0.0f;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < CH; ++j) v[j] = stg[lane * kStageLd + j];
+    __syncwarp();
+}
 
 __device__ __forceinline__ void st_bf16(__nv_bfloat16* base, int64_t ld, bool vec, int r0, int c0, int lane,
-                                        const float (&v)[CH], int M, int N) {
-    if (vec && c0 + CH <= N) {
-        uint32_t w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-        const bool odd = lane & 1;
-        uint32_t d0[4], d1[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t keep = odd ? w[4 + k] : w[k];
-            const uint32_t recv = __shfl_xor_sync(kFullMask, odd ? w[k] : w[4 + k], 1);
-            d0[k] = odd ? recv : keep;  // row (lane & ~1), half `odd`
-            d1[k] = odd ? keep : recv;  // row (lane | 1),  half `odd`
-        }
-        const int ra = r0 + (lane & ~1);
-        __nv_bfloat16* p = base + static_cast<int64_t>(ra) * ld + c0 + 8 * odd;
-        if (ra < M) *reinterpret_cast<uint4*>(p) = make_uint4(d0[0], d0[1], d0[2], d0[3]);
-        if (ra + 1 < M) *reinterpret_cast<uint4*>(p + ld) = make_uint4(d1[0], d1[1], d1[2], d1[3]);
+                                        const float (&v)[CH], int M, int N, float* stg) {
+    if (!vec || c0 + CH > N) {
+        st_staged(base, ld, r0, c0, lane, v, M, N, stg);
         return;
     }
-    const int r = r0 + lane;
-    if (r < M) {
-        __nv_bfloat16* p = base + static_cast<int64_t>(r) * ld + c0;
+    uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-            if (c0 + j < N) p[j] = __float2bfloat16_rn(v[j]);
+    for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    const bool odd = lane & 1;
+    uint32_t d0[4], d1[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t keep = odd ? w[4 + k] : w[k];
+        const uint32_t recv = __shfl_xor_sync(kFullMask, odd ? w[k] : w[4 + k], 1);
+        d0[k] = odd ? recv : keep;  // row (lane & ~1), half `odd`
+        d1[k] = odd ? keep : recv;  // row (lane | 1),  half `odd`
     }
+    const int ra = r0 + (lane & ~1);
+    __nv_bfloat16* p = base + static_cast<int64_t>(ra) * ld + c0 + 8 * odd;
+    if (ra < M) *reinterpret_cast<uint4*>(p) = make_uint4(d0[0], d0[1], d0[2], d0[3]);
+    if (ra + 1 < M) *reinterpret_cast<uint4*>(p + ld) = make_uint4(d1[0], d1[1], d1[2], d1[3]);
 }
 
 __device__ __forceinline__ void st_f32(float* base, int64_t ld, bool vec, int r0, int c0, int lane,
-                                       const float (&v)[CH], int M, int N) {
-    if (vec && c0 + CH <= N) {
-        float w[CH];
-#pragma unroll
-        for (int j = 0; j < CH; ++j) w[j] = v[j];
-        quad_transpose(w, lane);
-        const int rq = r0 + (lane & ~3);
-        float* p = base + static_cast<int64_t>(rq) * ld + c0 + 4 * (lane & 3);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (rq + j < M)
-                *reinterpret_cast<float4*>(p + j * ld) = make_float4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                                       const float (&v)[CH], int M, int N, float* stg) {
+    if (!vec || c0 + CH > N) {
+        st_staged(base, ld, r0, c0, lane, v, M, N, stg);
         return;
     }
-    const int r = r0 + lane;
-    if (r < M) {
-        float* p = base + static_cast<int64_t>(r) * ld + c0;
+    float w[CH];
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-            if (c0 + j < N) p[j] = v[j];
-    }
+    for (int j = 0; j < CH; ++j) w[j] = v[j];
+    quad_transpose(w, lane);
+    const int rq = r0 + (lane & ~3);
+    float* p = base + static_cast<int64_t>(rq) * ld + c0 + 4 * (lane & 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (rq + j < M)
+            *reinterpret_cast<float4*>(p + j * ld) = make_float4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
 // A matrix of the given element type, or of bf16 parts (part > 0).
-__device__ __forceinline__ void st_mat(const OpsMat& m, int r0, int c0, int lane, const float (&v)[CH], int M, int N) {
+__device__ __forceinline__ void st_mat(const OpsMat& m, int r0, int c0, int lane, const float (&v)[CH], int M, int N,
+                                       float* stg) {
     if (m.type == ELEM_F32) {
-        st_f32(static_cast<float*>(m.p), m.ld, m.vec, r0, c0, lane, v, M, N);
+        st_f32(static_cast<float*>(m.p), m.ld, m.vec, r0, c0, lane, v, M, N, stg);
         return;
     }
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(m.p);
-    st_bf16(p, m.ld, m.vec, r0, c0, lane, v, M, N);
+    st_bf16(p, m.ld, m.vec, r0, c0, lane, v, M, N, stg);
     if (m.part > 0) {
         float w[CH];
 #pragma unroll
         for (int j = 0; j < CH; ++j) w[j] = bf16_rest(v[j]);
-        st_bf16(p + m.part, m.ld, m.vec, r0, c0, lane, w, M, N);
+        st_bf16(p + m.part, m.ld, m.vec, r0, c0, lane, w, M, N, stg);
 #pragma unroll
         for (int j = 0; j < CH; ++j) w[j] = bf16_rest(w[j]);
-        st_bf16(p + 2 * m.part, m.ld, m.vec, r0, c0, lane, w, M, N);
+        st_bf16(p + 2 * m.part, m.ld, m.vec, r0, c0, lane, w, M, N, stg);
     }
 }
 
-__device__ __forceinline__ void ld_mat(const OpsMat& m, int r0, int c0, int lane, float (&x)[CH], int M, int N) {
-    if (m.vec && c0 + CH <= N) {
-        if (m.type == ELEM_BF16) {
-            const bool odd = lane & 1;
-            const int ra = r0 + (lane & ~1);
-            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(m.p) + static_cast<int64_t>(ra) * m.ld + c0 +
-                                     8 * odd;
-            uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
-            if (ra < M) a = *reinterpret_cast<const uint4*>(p);
-            if (ra + 1 < M) b = *reinterpret_cast<const uint4*>(p + m.ld);
-            const uint32_t d0[4] = {a.x, a.y, a.z, a.w}, d1[4] = {b.x, b.y, b.z, b.w};
-            uint32_t w[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t recv = __shfl_xor_sync(kFullMask, odd ? d0[k] : d1[k], 1);
-                w[k] = odd ? recv : d0[k];
-                w[4 + k] = odd ? d1[k] : recv;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 f = unpack_bf16x2(w[k]);
-                x[2 * k] = f.x;
-                x[2 * k + 1] = f.y;
-            }
-        } else {
-            const int rq = r0 + (lane & ~3);
-            const float* p = static_cast<const float*>(m.p) + static_cast<int64_t>(rq) * m.ld + c0 + 4 * (lane & 3);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (rq + j < M) q = *reinterpret_cast<const float4*>(p + j * m.ld);
-                x[4 * j] = q.x;
-                x[4 * j + 1] = q.y;
-                x[4 * j + 2] = q.z;
-                x[4 * j + 3] = q.w;
-            }
-            quad_transpose(x, lane);
-        }
+__device__ __forceinline__ void ld_mat(const OpsMat& m, int r0, int c0, int lane, float (&x)[CH], int M, int N,
+                                       float* stg) {
+    if (!m.vec || c0 + CH > N) {
+        if (m.type == ELEM_BF16)
+            ld_staged(static_cast<const __nv_bfloat16*>(m.p), m.ld, r0, c0, lane, x, M, N, stg);
+        else
+            ld_staged(static_cast<const float*>(m.p), m.ld, r0, c0, lane, x, M, N, stg);
         return;
     }
-    const int r = r0 + lane;
-    const int64_t i0 = static_cast<int64_t>(r) * m.ld + c0;
+    if (m.type == ELEM_BF16) {
+        const bool odd = lane & 1;
+        const int ra = r0 + (lane & ~1);
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(m.p) + static_cast<int64_t>(ra) * m.ld + c0 +
+                                 8 * odd;
+        uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
+        if (ra < M) a = *reinterpret_cast<const uint4*>(p);
+        if (ra + 1 < M) b = *reinterpret_cast<const uint4*>(p + m.ld);
+        const uint32_t d0[4] = {a.x, a.y, a.z, a.w}, d1[4] = {b.x, b.y, b.z, b.w};
+        uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        x[j] = 0.0f;
-        if (r < M && c0 + j < N)
-            x[j] = m.type == ELEM_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(m.p)[i0 + j])
-                                       : static_cast<const float*>(m.p)[i0 + j];
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t recv = __shfl_xor_sync(kFullMask, odd ? d0[k] : d1[k], 1);
+            w[k] = odd ? recv : d0[k];
+            w[4 + k] = odd ? d1[k] : recv;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 f = unpack_bf16x2(w[k]);
+            x[2 * k] = f.x;
+            x[2 * k + 1] = f.y;
+        }
+    } else {
+        const int rq = r0 + (lane & ~3);
+        const float* p = static_cast<const float*>(m.p) + static_cast<int64_t>(rq) * m.ld + c0 + 4 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (rq + j < M) q = *reinterpret_cast<const float4*>(p + j * m.ld);
+            x[4 * j] = q.x;
+            x[4 * j + 1] = q.y;
+            x[4 * j + 2] = q.z;
+            x[4 * j + 3] = q.w;
+        }
+        quad_transpose(x, lane);
     }
 }
 
@@ -316,7 +342,7 @@ struct RegSrc {
 
 template <bool kF32, typename Src>
 __device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
-                                          int lane) {
+                                          int lane, float* stg) {
 #pragma unroll 1
     for (int kc = 0; kc < 8; ++kc) {
         const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
@@ -325,17 +351,17 @@ __device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Un
         acc.load(kc, v);
         if (P.in0.p) {
             float add[CH];
-            ld_mat(P.in0, r0, c0, lane, add, P.M, P.N);
+            ld_mat(P.in0, r0, c0, lane, add, P.M, P.N, stg);
 #pragma unroll
             for (int j = 0; j < CH; ++j) v[j] += add[j];
         }
-        st_mat(P.out0, r0, c0, lane, v, P.M, P.N);
+        st_mat(P.out0, r0, c0, lane, v, P.M, P.N, stg);
     }
 }
 
 template <bool kF32, typename Src>
 __device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
-                                         int lane) {
+                                         int lane, float* stg) {
 #pragma unroll 1
     for (int kc = 0; kc < 4; ++kc) {
         const int c0 = u.tn * (BN / 2) + half * (BN / 4) + kc * CH;
@@ -351,41 +377,41 @@ __device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Uni
                 s[j] = w[j] * act_slope<kF32>(P.act, a[j], g);
                 w[j] *= f[j];
             }
-            st_mat(P.out1, r0, c0, lane, f, P.M, P.N);
-            st_mat(P.out2, r0, c0, lane, s, P.M, P.N);
-            if (P.out3.p) st_mat(P.out3, r0, c0, lane, w, P.M, P.N);
+            st_mat(P.out1, r0, c0, lane, f, P.M, P.N, stg);
+            st_mat(P.out2, r0, c0, lane, s, P.M, P.N, stg);
+            if (P.out3.p) st_mat(P.out3, r0, c0, lane, w, P.M, P.N, stg);
         } else {
 #pragma unroll
             for (int j = 0; j < CH; ++j) w[j] *= a[j] * act_gate<kF32>(P.act, a[j]);
         }
-        st_mat(P.out0, r0, c0, lane, w, P.M, P.N);
+        st_mat(P.out0, r0, c0, lane, w, P.M, P.N, stg);
     }
 }
 
 template <bool kF32, typename Src>
 __device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
-                                          int lane) {
+                                          int lane, float* stg) {
 #pragma unroll 1
     for (int kc = 0; kc < 8; ++kc) {
         const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
         if (c0 >= P.N) break;
         float f[CH], s[CH], v[CH];
-        ld_mat(P.in0, r0, c0, lane, f, P.M, P.N);
-        ld_mat(P.in1, r0, c0, lane, s, P.M, P.N);
+        ld_mat(P.in0, r0, c0, lane, f, P.M, P.N, stg);
+        ld_mat(P.in1, r0, c0, lane, s, P.M, P.N, stg);
         acc.load(kc, v);
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             s[j] *= v[j];  // da = dh u act'(a)
             f[j] *= v[j];  // du = dh act(a)
         }
-        st_mat(P.out0, r0, c0, lane, s, P.M, P.N);
-        st_mat(P.out1, r0, c0, lane, f, P.M, P.N);
+        st_mat(P.out0, r0, c0, lane, s, P.M, P.N, stg);
+        st_mat(P.out1, r0, c0, lane, f, P.M, P.N, stg);
     }
 }
 
 template <bool kF32>
 __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, int half, int r0, int lane,
-                                           float (&z)[BN / 2]) {
+                                           float (&z)[BN / 2], float* stg) {
     const int cb = u.tn * BN + half * (BN / 2);
     const int r = r0 + lane;
     const float ninf = __int_as_float(0xff800000);
@@ -394,9 +420,13 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
 #pragma unroll
         for (int j = 0; j < BN / 2; ++j) z[j] = cb + j < P.N ? z[j] : ninf;
     }
-    float m = z[0];
+    float mx[8];  // several chains: two warps per scheduler do not hide one
 #pragma unroll
-    for (int j = 1; j < BN / 2; ++j) m = fmaxf(m, z[j]);
+    for (int j = 0; j < 8; ++j) mx[j] = z[j];
+#pragma unroll
+    for (int j = 8; j < BN / 2; ++j) mx[j % 8] = fmaxf(mx[j % 8], z[j]);
+    const float m = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                          fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
     const int64_t t = r < P.M ? P.targets[r] - cb : -1;
     if (t >= 0 && t < BN / 2 && cb + t < P.N) {
         float zt = 0.0f;
@@ -404,21 +434,19 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
         for (int j = 0; j < BN / 2; ++j) zt = t == j ? z[j] : zt;
         P.target_logit[r] = zt;
     }
-    float s0 = 0.0f, s1 = 0.0f;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const float ms = m * kLog2e;
 #pragma unroll
     for (int kc = 0; kc < 8; ++kc) {
         float v[CH];
 #pragma unroll
-        for (int j = 0; j < CH; j += 2) {
+        for (int j = 0; j < CH; ++j) {
             v[j] = kF32 ? expf(z[kc * CH + j] - m) : ex2(fmaf(z[kc * CH + j], kLog2e, -ms));
-            v[j + 1] = kF32 ? expf(z[kc * CH + j + 1] - m) : ex2(fmaf(z[kc * CH + j + 1], kLog2e, -ms));
-            s0 += v[j];
-            s1 += v[j + 1];
+            sum[j % 4] += v[j];
         }
-        if (P.out0.p) st_mat(P.out0, r0, cb + kc * CH, lane, v, P.M, P.N);
+        if (P.out0.p) st_mat(P.out0, r0, cb + kc * CH, lane, v, P.M, P.N, stg);
     }
-    if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] = make_float2(m, s0 + s1);
+    if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
 template <int kKind, bool kF32>
@@ -462,6 +490,14 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
     const uint32_t tmem = S.tmem_base;
     const int rank = static_cast<int>(cluster_rank());
     const int total = L.total_units;
+    if (warp == 2 && lane < 4 * L.n) {
+        // the used tensor maps into the descriptor cache before their first use
+        const OpsProblem& P = L.p[lane / 4];
+        const bool of_b = lane & 2, second = lane & 1;
+        if (!second || (of_b ? P.maps_b : P.maps_a) > 1)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(of_b ? &P.b[second] : &P.a[second]))
+                         : "memory");
+    }
     // programmatic dependent launch: global memory only after the previous
     // kernel has completed
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -473,7 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
             uint32_t stage = 0, phase = 0, n_issued = 0;
             bool ok = true;
             const uint32_t full0 = mapa(saddr(&S.full[0]), 0);
-            int t_next = rank == 0 ? atomicAdd(L.counter, 1) : 0;
+            // the first unit is the pair's own index; a launch with more units
+            // than pairs hands out the others from the counter
+            const int pairs = static_cast<int>(gridDim.x) / kPair;
+            int t_next = static_cast<int>(blockIdx.x) / kPair;
+            const bool more = total > pairs;
             for (int k = 0; ok; ++k) {
                 int t;
                 if (rank == 0) {
@@ -484,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                         break;
                     }
                     t = t_next < total ? t_next : total;
-                    if (t < total) t_next = atomicAdd(L.counter, 1);
+                    if (t < total) t_next = more ? pairs + atomicAdd(L.counter, 1) : total;
                     S.tile_slot[slot] = t;
                     st_cluster_u32(mapa(saddr(&S.tile_slot[slot]), 1), t);
                     mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 0));
@@ -624,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
         // ------------------------------------------------ epilogue
         const int q = warp & 3;                   // TMEM lane quarter this warp may access
         const int half = (warp - kEpiWarp0) / 4;  // column half
+        float* stg = S.stage[warp - kEpiWarp0];
         int it = 0;
         float r[kRegs ? BN / 2 : 1];
         for (int k = 0;; ++k) {
@@ -671,10 +712,10 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                 ++it;
             }
             const auto finish = [&](auto acc) {
-                if constexpr (kKind == OPS_STORE) epi_store<kF32>(P, acc, u, half, r0, lane);
-                else if constexpr (kKind == OPS_GATE) epi_gate<kF32>(P, acc, u, half, r0, lane);
-                else if constexpr (kKind == OPS_DGATE) epi_dgate<kF32>(P, acc, u, half, r0, lane);
-                else epi_logits<kF32>(P, u, half, r0, lane, acc.r);
+                if constexpr (kKind == OPS_STORE) epi_store<kF32>(P, acc, u, half, r0, lane, stg);
+                else if constexpr (kKind == OPS_GATE) epi_gate<kF32>(P, acc, u, half, r0, lane, stg);
+                else if constexpr (kKind == OPS_DGATE) epi_dgate<kF32>(P, acc, u, half, r0, lane, stg);
+                else epi_logits<kF32>(P, u, half, r0, lane, acc.r, stg);
             };
             if (active && u.split == 1) {
                 if constexpr (kRegs) finish(RegSrc{r});
@@ -812,7 +853,7 @@ cudaError_t ops_pairs(int* pairs) {
 // first (the caller's order), and a product whose tiles are long against the
 // launch's share per pair is split throughout.
 void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
-    constexpr double kUnitCost = 4.0, kStoreCost = 4.0, kPartCost = 3.0;  // slabs
+    constexpr double kUnitCost = 4.0, kStoreCost = 12.0, kPartCost = 3.0;  // slabs
     constexpr int kMinSlabs = 8;         // per range
     double work = 0.0;
     for (int i = 0; i < l.n; ++i)
