@@ -9,14 +9,21 @@
 // (read x and dy, write dx), twice that in fp32.  Each row is read once and
 // held in registers by the threads of its group (WPR warps, VPT 16-byte vectors
 // per thread), so the variance is the mean of squared deviations from the
-// finished mean -- no difference of large sums -- and the next row's loads are
-// issued before the current row's reductions.  All arithmetic is fp32, one
-// rounding per stored value.  In the backward pass a thread meets the same
-// columns in every row and keeps their dw and db sums in registers; a block's
-// groups add theirs up in shared memory, each block writes one partial row, and
-// a second kernel adds the partial rows in a fixed order, so the result does
-// not depend on scheduling.  Rows wider than a group holds take three plain
-// passes (wide kernels).
+// finished mean -- no difference of large sums.  All arithmetic is fp32, one
+// rounding per stored value.
+//
+// Many aligned rows (ring kernels): persistent groups; bulk asynchronous copies
+// bring each group's next rows into a shared-memory ring while it works on the
+// current one, so the loads in flight do not cost registers, and the arithmetic
+// runs on packed pairs (fma.rn.f32x2).  Fewer rows, or rows that do not start on
+// 16 bytes (register kernels): a row is spread over as many threads as hold it
+// and the next row is loaded into registers ahead.
+//
+// In the backward pass a thread meets the same columns in every row and keeps
+// their dw and db sums in registers; a block's groups add theirs up in shared
+// memory, each block writes one partial row, and a second kernel adds the
+// partial rows in a fixed order, so the result does not depend on scheduling.
+// Rows wider than a group holds take three plain passes (wide kernels).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -25,6 +32,7 @@
 
 #include "dmuon.h"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace dmuon {
 void set_last_error(const std::string& msg);
@@ -32,12 +40,14 @@ void set_last_error(const std::string& msg);
 
 namespace {
 
-using dmuon::ELEM_BF16;
+// set by a wait that gave up; read and cleared by dmuon_ops_status
+__device__ int32_t g_norm_status = 0;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int kBwdThreads = 512;
 constexpr int kMaxPartials = 1024;  // partial rows of the backward pass
+__host__ __device__ constexpr int bwd_groups(int wpr) { return kBwdThreads / (32 * wpr); }
 
 struct NormArgs {
     const void* x;
@@ -52,6 +62,7 @@ struct NormArgs {
     int32_t cols;
     int32_t aligned;    // rows start on 16-byte boundaries
     float eps;
+    int32_t stages;     // ring kernels: rows in a group's ring
 };
 
 template <typename T>
@@ -130,32 +141,44 @@ __device__ __forceinline__ void warp_sum(float (&s)[N]) {
         for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(kFull, s[k], o);
 }
 
-// Sum over the WPR warps of a row group, in a fixed order.  `buf` alternates
-// between two halves of shared memory from call to call, so one barrier per
-// reduction is enough: a half is written again only after the barrier of the
-// reduction in between.
+// Sum over the WPR warps of a row group, in a fixed order.  `red` alternates
+// between two buffers from call to call, so one barrier per reduction is enough:
+// a buffer is written again only after the barrier of the reduction in between.
+// Every thread reads all warps' sums, 16 bytes at a time.
 template <int WPR, int N>
-__device__ __forceinline__ void group_sum(float (&s)[N], float (*red)[N], int bar) {
+struct alignas(16) GroupRed {
+    float v[N][WPR < 4 ? 4 : WPR];
+};
+
+template <int WPR, int N>
+__device__ __forceinline__ void group_sum(float (&s)[N], GroupRed<WPR, N>& red, int bar) {
     warp_sum(s);
     if constexpr (WPR > 1) {
         const int w = (threadIdx.x / 32) % WPR;
         if (threadIdx.x % 32 == 0)
 #pragma unroll
-            for (int k = 0; k < N; ++k) red[w][k] = s[k];
+            for (int k = 0; k < N; ++k) red.v[k][w] = s[k];
         asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(WPR * 32) : "memory");
 #pragma unroll
-        for (int k = 0; k < N; ++k) s[k] = 0.0f;
+        for (int k = 0; k < N; ++k) {
+            if constexpr (WPR == 2) {
+                s[k] = red.v[k][0] + red.v[k][1];
+            } else {
+                s[k] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < WPR; ++i)
-#pragma unroll
-            for (int k = 0; k < N; ++k) s[k] += red[i][k];
+                for (int i = 0; i < WPR; i += 4) {
+                    const float4 q = *reinterpret_cast<const float4*>(&red.v[k][i]);
+                    s[k] += (q.x + q.y) + (q.z + q.w);
+                }
+            }
+        }
     }
 }
 
 template <typename T, int VPT, int WPR>
 __global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>, TPR = WPR * 32, G = WPR == 1 ? 4 : 1;
-    __shared__ float red[2][WPR][1];
+    __shared__ GroupRed<WPR, 1> red[2];
     const int g = threadIdx.x / TPR, tr = threadIdx.x % TPR;
     const bool al = a.aligned != 0;
     uint4 w[VPT], b[VPT];
@@ -220,7 +243,7 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32) norm_fwd_kernel(con
 template <typename T, int VPT, int WPR>
 __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>, TPR = WPR * 32, G = kBwdThreads / TPR;
-    __shared__ float red[G][2][WPR][2];
+    __shared__ GroupRed<WPR, 2> red[G][2];
     extern __shared__ float sums[];  // [2][TPR * VPT * V], groups > 1 only
     const int g = threadIdx.x / TPR, tr = threadIdx.x % TPR;
     const bool al = a.aligned != 0;
@@ -327,6 +350,313 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const __grid_cons
                     p[a.cols + c] = db[k][j];
                 }
             }
+    }
+}
+
+// ------------------------------------------------ ring kernels
+
+using dmuon::tc::mbar_expect_tx;
+using dmuon::tc::mbar_init;
+using dmuon::tc::mbar_wait;
+using dmuon::tc::saddr;
+
+constexpr int kMaxStages = 3;
+constexpr size_t kRingBytes = 196608;  // most ring memory of a block
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     saddr(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(saddr(bar))
+                 : "memory");
+}
+
+// Pairs of fp32 values in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <typename T>
+__device__ __forceinline__ void unpack2(const uint4& q, float2 (&v)[kVec<T> / 2]) {
+    float t[kVec<T>];
+    unpack<T>(q, t);
+#pragma unroll
+    for (int k = 0; k < kVec<T> / 2; ++k) v[k] = make_float2(t[2 * k], t[2 * k + 1]);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack2(const float2 (&v)[kVec<T> / 2]) {
+    if constexpr (sizeof(T) == 4) {
+        return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                          __float_as_uint(v[1].y));
+    } else {
+        return make_uint4(dmuon::tc::pack_bf16x2(v[0].x, v[0].y), dmuon::tc::pack_bf16x2(v[1].x, v[1].y),
+                          dmuon::tc::pack_bf16x2(v[2].x, v[2].y), dmuon::tc::pack_bf16x2(v[3].x, v[3].y));
+    }
+}
+
+// A group's ring of rows in shared memory, `arrays` rows per stage.  Thread 0 of
+// the group issues; a stage is refilled once the whole group has passed a
+// barrier after reading it.
+struct Ring {
+    uint8_t* rows;
+    uint64_t* full;
+    uint32_t bytes;  // of one row
+    int arrays;
+    bool dead;       // a wait gave up: the results are lost (status), the loop goes on
+    __device__ __forceinline__ uint8_t* at(int stage, int k) const { return rows + (stage * arrays + k) * bytes; }
+    __device__ __forceinline__ void issue(int stage, const void* a, const void* b) {
+        mbar_expect_tx(&full[stage], bytes * arrays);
+        bulk_load(at(stage, 0), a, bytes, &full[stage]);
+        if (arrays > 1) bulk_load(at(stage, 1), b, bytes, &full[stage]);
+    }
+    __device__ __forceinline__ void wait(int stage, uint32_t phase) {
+        if (!dead) dead = !mbar_wait<false>(&full[stage], phase, &g_norm_status);
+    }
+};
+
+__device__ __forceinline__ Ring make_ring(uint8_t* smem, uint32_t bytes, int arrays, int stages, int groups, int g, int tr) {
+    // barriers first, then the groups' rows
+    Ring r;
+    r.full = reinterpret_cast<uint64_t*>(smem) + g * kMaxStages;
+    r.rows = smem + (groups * kMaxStages * 8 + 15) / 16 * 16 + static_cast<size_t>(g) * stages * arrays * bytes;
+    r.bytes = bytes;
+    r.arrays = arrays;
+    r.dead = false;
+    if (tr == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&r.full[s], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    return r;
+}
+
+__host__ __device__ constexpr int ring_bwd_threads(int wpr) { return wpr > 8 ? wpr * 32 : 256; }
+__host__ __device__ constexpr int ring_groups(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }
+
+template <typename T, int VPT, int WPR>
+__global__ void __launch_bounds__(ring_groups(WPR) * WPR * 32, 512 / (ring_groups(WPR) * WPR * 32)) norm_fwd_ring_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int V = kVec<T>, TPR = WPR * 32, G = ring_groups(WPR);
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ GroupRed<WPR, 1> red[G][2];
+    const int g = threadIdx.x / TPR, tr = threadIdx.x % TPR;
+    Ring ring = make_ring(smem, a.cols * static_cast<uint32_t>(sizeof(T)), 1, a.stages, G, g, tr);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * G + g;
+    const T* x0 = static_cast<const T*>(a.x);
+    if (tr == 0)
+        for (int s = 0; s < a.stages; ++s)
+            if (first + s * stride < a.rows) ring.issue(s, x0 + (first + s * stride) * a.cols, nullptr);
+    uint4 w[VPT], b[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = (k * TPR + tr) * V;
+        w[k] = a.w ? ld_raw(static_cast<const T*>(a.w), c, a.cols, true) : make_uint4(0, 0, 0, 0);
+        b[k] = a.b ? ld_raw(static_cast<const T*>(a.b), c, a.cols, true) : make_uint4(0, 0, 0, 0);
+    }
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int64_t row = first; row < a.rows; row += stride) {
+        ring.wait(stage, phase);
+        float2 x[VPT][V / 2];
+        float2 s2 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + tr) * V;
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (c < a.cols) q = *reinterpret_cast<const uint4*>(ring.at(stage, 0) + c * sizeof(T));
+            unpack2<T>(q, x[k]);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) s2 = add2(s2, x[k][j]);
+        }
+        float s[1] = {s2.x + s2.y};
+        group_sum<WPR>(s, red[g][0], 1 + g);
+        // the whole group has its part of the row in registers (WPR = 1: the
+        // warp's shuffles ordered its reads): refill the stage
+        if (tr == 0 && row + a.stages * stride < a.rows) ring.issue(stage, x0 + (row + a.stages * stride) * a.cols, nullptr);
+        const float mean = s[0] * inv;
+        s2 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const bool in = (k * TPR + tr) * V < a.cols;  // a vector lies inside the row or past it
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                x[k][j] = add2(x[k][j], both(in ? -mean : 0.0f));
+                s2 = fma2(x[k][j], x[k][j], s2);
+            }
+        }
+        s[0] = s2.x + s2.y;
+        group_sum<WPR>(s, red[g][1], 1 + g);
+        const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+        if (tr == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + tr) * V;
+            float2 wv[V / 2], bv[V / 2];
+            unpack2<T>(w[k], wv);
+            unpack2<T>(b[k], bv);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j)
+                x[k][j] = fma2(mul2(x[k][j], both(rstd)), a.w ? wv[j] : both(1.0f), bv[j]);
+            if (c < a.cols)
+                *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.cols + c) = pack2<T>(x[k]);
+        }
+        if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+}
+
+template <typename T, int VPT, int WPR>
+__global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(WPR)) norm_bwd_ring_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int V = kVec<T>, TPR = WPR * 32, G = ring_bwd_threads(WPR) / TPR;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ GroupRed<WPR, 2> red[G][2];
+    const int g = threadIdx.x / TPR, tr = threadIdx.x % TPR;
+    Ring ring = make_ring(smem, a.cols * static_cast<uint32_t>(sizeof(T)), 2, a.stages, G, g, tr);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * G + g;
+    const T *x0 = static_cast<const T*>(a.x), *d0 = static_cast<const T*>(a.dy);
+    if (tr == 0)
+        for (int s = 0; s < a.stages; ++s) {
+            const int64_t r = first + s * stride;
+            if (r < a.rows) ring.issue(s, x0 + r * a.cols, d0 + r * a.cols);
+        }
+    float2 w[VPT][V / 2], dw[VPT][V / 2], db[VPT][V / 2];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        unpack2<T>(a.w ? ld_raw(static_cast<const T*>(a.w), (k * TPR + tr) * V, a.cols, true) : make_uint4(0, 0, 0, 0),
+                   w[k]);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            if (!a.w) w[k][j] = both(1.0f);
+            dw[k][j] = db[k][j] = both(0.0f);
+        }
+    }
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    int stage = 0, flip = 0;
+    uint32_t phase = 0;
+    float nm = first < a.rows ? a.mean[first] : 0.0f, nr = first < a.rows ? a.rstd[first] : 0.0f;
+    for (int64_t row = first; row < a.rows; row += stride, flip ^= 1) {
+        const float mean = nm, rstd = nr;
+        if (row + stride < a.rows) {
+            nm = a.mean[row + stride];
+            nr = a.rstd[row + stride];
+        }
+        ring.wait(stage, phase);
+        float2 n[VPT][V / 2], gr[VPT][V / 2], s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + tr) * V;
+            uint4 qx = make_uint4(0, 0, 0, 0), qd = qx;
+            if (c < a.cols) {
+                qx = *reinterpret_cast<const uint4*>(ring.at(stage, 0) + c * sizeof(T));
+                qd = *reinterpret_cast<const uint4*>(ring.at(stage, 1) + c * sizeof(T));
+            }
+            float2 d[V / 2];
+            unpack2<T>(qx, n[k]);
+            unpack2<T>(qd, d);
+            // a vector past the row is never stored, and its d = 0 adds nothing
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                n[k][j] = mul2(add2(n[k][j], both(-mean)), both(rstd));
+                gr[k][j] = mul2(d[j], w[k][j]);
+                s1 = add2(s1, gr[k][j]);
+                s2 = fma2(gr[k][j], n[k][j], s2);
+                dw[k][j] = fma2(d[j], n[k][j], dw[k][j]);
+                db[k][j] = add2(db[k][j], d[j]);
+            }
+        }
+        float s[2] = {s1.x + s1.y, s2.x + s2.y};
+        group_sum<WPR>(s, red[g][flip], 1 + g);
+        if (tr == 0) {
+            const int64_t r = row + a.stages * stride;
+            if (r < a.rows) ring.issue(stage, x0 + r * a.cols, d0 + r * a.cols);
+        }
+        const float2 m1 = both(-s[0] * inv), m2 = both(-s[1] * inv);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + tr) * V;
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j)
+                n[k][j] = mul2(fma2(n[k][j], m2, add2(gr[k][j], m1)), both(rstd));
+            if (c < a.cols)
+                *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.cols + c) = pack2<T>(n[k]);
+        }
+        if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+    if (!a.partial) return;
+    float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    if constexpr (G > 1) {
+        // the groups' sums, one group after the other, in the ring's memory
+        // (every copy has been waited for)
+        float* sums = reinterpret_cast<float*>(smem);
+        constexpr int kCols = TPR * VPT * V;
+        __syncthreads();
+        for (int i = 0; i < G; ++i) {
+            if (g == i) {
+#pragma unroll
+                for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) {
+                        const int c = 2 * j * (TPR * VPT) + k * TPR + tr;  // conflict-free order
+                        const float2 u = dw[k][j], v = db[k][j];
+                        sums[c] = i ? sums[c] + u.x : u.x;
+                        sums[c + TPR * VPT] = i ? sums[c + TPR * VPT] + u.y : u.y;
+                        sums[kCols + c] = i ? sums[kCols + c] + v.x : v.x;
+                        sums[kCols + c + TPR * VPT] = i ? sums[kCols + c + TPR * VPT] + v.y : v.y;
+                    }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.cols; c += G * TPR) {
+            const int i = (c % V) * (TPR * VPT) + c / V;
+            p[c] = sums[i];
+            p[a.cols + c] = sums[kCols + i];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + tr) * V;
+            if (c < a.cols)
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    *reinterpret_cast<float2*>(p + c + 2 * j) = dw[k][j];
+                    *reinterpret_cast<float2*>(p + a.cols + c + 2 * j) = db[k][j];
+                }
+        }
     }
 }
 
@@ -443,71 +773,132 @@ int fail(int code, const std::string& msg) {
 }
 
 // Row group of `vecs` 16-byte vectors: warps per row and vectors per thread.
-// Forward with many rows: a thread holds up to four vectors and a narrow row
-// belongs to one warp (no barrier); with fewer rows than the machine has room
-// for, a row is spread over more warps to shorten its chain of loads and sums.
-// Backward: the column sums take 16 registers per vector, so a thread holds
-// one vector and a second or fourth only in rows wider than 16 warps.
 struct Shape {
     int vpt = 0, wpr = 0;  // 0: wide kernels
 };
 
-Shape choose(int64_t rows, int64_t vecs, int sms, bool bwd) {
-    const bool spread = bwd || rows < 4 * static_cast<int64_t>(sms);
-    static const int vpts[3] = {1, 2, 4};
-    static const int wprs[5] = {1, 2, 4, 8, 16};
-    if (spread) {
-        for (int v : vpts)
-            for (int w : wprs)
-                if (static_cast<int64_t>(v) * w * 32 >= vecs) return {v, w};
-    } else {
-        for (int w : wprs)
-            for (int v : vpts)
-                if (static_cast<int64_t>(v) * w * 32 >= vecs) return {v, w};
-    }
+// Smallest group with at most `vpt` vectors per thread; rows wider than 16 warps
+// take more vectors.
+Shape choose(int64_t vecs, int vpt) {
+    for (int w = 1; w <= 16; w *= 2)
+        if (static_cast<int64_t>(vpt) * w * 32 >= vecs) return {vpt, w};
+    for (int v = 2 * vpt; v <= 4; v *= 2)
+        if (static_cast<int64_t>(v) * 512 >= vecs) return {v, 16};
     return {};
 }
 
-template <typename T, int VPT, int WPR>
-cudaError_t run_fwd(const NormArgs& a, int grid, cudaStream_t s) {
-    norm_fwd_kernel<T, VPT, WPR><<<grid, WPR == 1 ? 128 : WPR * 32, 0, s>>>(a);
+// Ring kernels: enough rows that every group passes over several.
+bool use_ring(int64_t rows, const NormArgs& a, int sms) { return a.aligned && rows >= 8 * static_cast<int64_t>(sms); }
+
+size_t ring_bytes(int groups, int arrays, int stages, int64_t cols, int es) {
+    return (static_cast<size_t>(groups) * kMaxStages * 8 + 15) / 16 * 16 +
+           static_cast<size_t>(groups) * stages * arrays * cols * es;
+}
+
+// Rows per ring: up to four, as many as kRingBytes holds (at least two do: the
+// widest group's row is 32 KB).
+int ring_stages(int groups, int arrays, int64_t cols, int es) {
+    const size_t row = static_cast<size_t>(groups) * arrays * cols * es;
+    return static_cast<int>(std::min<size_t>(kMaxStages, kRingBytes / row));
+}
+
+// Launches a ring kernel on as many blocks as fit the device, at most `rows`
+// groups of them; *grid receives the block count.
+template <typename K>
+cudaError_t run_ring(K kernel, dmuon::PerDevice& cfg, const NormArgs& a, int threads, int groups, size_t smem,
+                     int max_grid, int* grid, cudaStream_t s) {
+    int dev = 0, unused = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cfg.get(dev, &unused, [&](int*) {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(kRingBytes) + 1024);
+        });
+    int per_sm = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    *grid = static_cast<int>(std::min<int64_t>({(a.rows + groups - 1) / groups,
+                                                static_cast<int64_t>(std::max(per_sm, 1)) * sms, max_grid}));
+    kernel<<<*grid, threads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T, int VPT, int WPR>
-cudaError_t run_bwd(const NormArgs& a, int grid, cudaStream_t s) {
-    // the groups' column sums: at most 32 KB
-    constexpr size_t smem = WPR < 16 ? static_cast<size_t>(2) * WPR * 32 * VPT * kVec<T> * 4 : 0;
-    norm_bwd_kernel<T, VPT, WPR><<<grid, kBwdThreads, smem, s>>>(a);
-    return cudaGetLastError();
+cudaError_t run_fwd_ring(const NormArgs& a, int max_grid, int* grid, cudaStream_t s) {
+    static dmuon::PerDevice cfg;
+    constexpr int groups = ring_groups(WPR), es = sizeof(T);
+    NormArgs r = a;
+    r.stages = ring_stages(groups, 1, a.cols, es);
+    return run_ring(norm_fwd_ring_kernel<T, VPT, WPR>, cfg, r, groups * WPR * 32, groups,
+                    ring_bytes(groups, 1, r.stages, a.cols, es), max_grid, grid, s);
 }
 
-template <typename T, int VPT>
-cudaError_t run_fwd_vpt(int wpr, const NormArgs& a, int grid, cudaStream_t s) {
-    switch (wpr) {
-        case 1: return run_fwd<T, VPT, 1>(a, grid, s);
-        case 2: return run_fwd<T, VPT, 2>(a, grid, s);
-        case 4: return run_fwd<T, VPT, 4>(a, grid, s);
-        case 8: return run_fwd<T, VPT, 8>(a, grid, s);
-        default: return run_fwd<T, VPT, 16>(a, grid, s);
+template <typename T, int VPT, int WPR>
+cudaError_t run_bwd_ring(const NormArgs& a, int max_grid, int* grid, cudaStream_t s) {
+    static dmuon::PerDevice cfg;
+    constexpr int G = ring_bwd_threads(WPR) / (32 * WPR), es = sizeof(T);
+    NormArgs r = a;
+    r.stages = ring_stages(G, 2, a.cols, es);
+    // the groups' column sums reuse the ring
+    const size_t sums = G > 1 ? static_cast<size_t>(2) * WPR * 32 * VPT * kVec<T> * 4 : 0;
+    return run_ring(norm_bwd_ring_kernel<T, VPT, WPR>, cfg, r, ring_bwd_threads(WPR), G,
+                    std::max(sums, ring_bytes(G, 2, r.stages, a.cols, es)), max_grid, grid, s);
+}
+
+template <typename T, int VPT, int WPR>
+cudaError_t run_registers(const NormArgs& a, bool bwd, int max_grid, int* grid, cudaStream_t s) {
+    if (bwd) {
+        constexpr int G = bwd_groups(WPR);
+        // the groups' column sums: at most 32 KB
+        constexpr size_t smem = G > 1 ? static_cast<size_t>(2) * WPR * 32 * VPT * kVec<T> * 4 : 0;
+        *grid = static_cast<int>(std::min<int64_t>((a.rows + G - 1) / G, max_grid));
+        norm_bwd_kernel<T, VPT, WPR><<<*grid, kBwdThreads, smem, s>>>(a);
+    } else {
+        constexpr int threads = WPR == 1 ? 128 : WPR * 32, groups = WPR == 1 ? 4 : 1;
+        *grid = static_cast<int>(std::min<int64_t>((a.rows + groups - 1) / groups, max_grid));
+        norm_fwd_kernel<T, VPT, WPR><<<*grid, threads, 0, s>>>(a);
     }
+    return cudaGetLastError();
 }
 
+// Forward ring: four vectors per thread, so a 4096-column bf16 row belongs to
+// four warps (one vector per thread and sixteen warps: 65 us instead of 47 for
+// 16384 x 4096, the two block-wide reductions bound it).  Backward: the column
+// sums take 16 registers per vector, so a thread holds one vector and more only
+// in rows wider than 16 warps.
 template <typename T>
-cudaError_t run_shape(const Shape& sh, const NormArgs& a, bool bwd, int grid, cudaStream_t s) {
-    if (!bwd) {
-        if (sh.vpt == 1) return run_fwd_vpt<T, 1>(sh.wpr, a, grid, s);
-        if (sh.vpt == 2) return run_fwd_vpt<T, 2>(sh.wpr, a, grid, s);
-        return run_fwd_vpt<T, 4>(sh.wpr, a, grid, s);
+cudaError_t run_shape(int64_t vecs, const NormArgs& a, bool bwd, bool ring, int max_grid, int* grid, cudaStream_t s) {
+    if (ring && !bwd) {
+        switch (choose(vecs, 4).wpr) {
+            case 1: return vecs <= 32 ? run_fwd_ring<T, 1, 1>(a, max_grid, grid, s)
+                                      : run_fwd_ring<T, 4, 1>(a, max_grid, grid, s);
+            case 2: return run_fwd_ring<T, 4, 2>(a, max_grid, grid, s);
+            case 4: return run_fwd_ring<T, 4, 4>(a, max_grid, grid, s);
+            case 8: return run_fwd_ring<T, 4, 8>(a, max_grid, grid, s);
+            default: return run_fwd_ring<T, 4, 16>(a, max_grid, grid, s);
+        }
     }
-    if (sh.vpt == 2) return run_bwd<T, 2, 16>(a, grid, s);
-    if (sh.vpt == 4) return run_bwd<T, 4, 16>(a, grid, s);
+    if (ring) {
+        const Shape sh = choose(vecs, 2);
+        if (sh.vpt == 4) return run_bwd_ring<T, 4, 16>(a, max_grid, grid, s);
+        switch (sh.wpr) {
+            case 1: return run_bwd_ring<T, 2, 1>(a, max_grid, grid, s);
+            case 2: return run_bwd_ring<T, 2, 2>(a, max_grid, grid, s);
+            case 4: return run_bwd_ring<T, 2, 4>(a, max_grid, grid, s);
+            case 8: return run_bwd_ring<T, 2, 8>(a, max_grid, grid, s);
+            default: return run_bwd_ring<T, 2, 16>(a, max_grid, grid, s);
+        }
+    }
+    const Shape sh = choose(vecs, 1);
+    if (sh.vpt == 2) return run_registers<T, 2, 16>(a, bwd, max_grid, grid, s);
+    if (sh.vpt == 4) return run_registers<T, 4, 16>(a, bwd, max_grid, grid, s);
     switch (sh.wpr) {
-        case 1: return run_bwd<T, 1, 1>(a, grid, s);
-        case 2: return run_bwd<T, 1, 2>(a, grid, s);
-        case 4: return run_bwd<T, 1, 4>(a, grid, s);
-        case 8: return run_bwd<T, 1, 8>(a, grid, s);
-        default: return run_bwd<T, 1, 16>(a, grid, s);
+        case 1: return run_registers<T, 1, 1>(a, bwd, max_grid, grid, s);
+        case 2: return run_registers<T, 1, 2>(a, bwd, max_grid, grid, s);
+        case 4: return run_registers<T, 1, 4>(a, bwd, max_grid, grid, s);
+        case 8: return run_registers<T, 1, 8>(a, bwd, max_grid, grid, s);
+        default: return run_registers<T, 1, 16>(a, bwd, max_grid, grid, s);
     }
 }
 
@@ -544,6 +935,17 @@ int64_t partial_rows(int64_t rows) { return std::min<int64_t>(rows, kMaxPartials
 
 }  // namespace
 
+namespace dmuon {
+
+cudaError_t norm_read_status(int32_t* v) {
+    const int32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(v, g_norm_status, sizeof(*v));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_norm_status, &zero, sizeof(zero));
+    return e;
+}
+
+}  // namespace dmuon
+
 extern "C" int dmuon_layer_norm_forward(const void* x, const void* weight, const void* bias, void* y, float* mean,
                                         float* rstd, int64_t rows, int64_t cols, int32_t dtype, float eps,
                                         void* stream) {
@@ -573,16 +975,18 @@ extern "C" int dmuon_layer_norm_forward(const void* x, const void* weight, const
     a.aligned = cols % vec == 0;
     a.eps = eps;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Shape sh = choose(rows, (cols + vec - 1) / vec, sms, false);
-    if (sh.wpr == 0) {
+    const int64_t vecs = (cols + vec - 1) / vec;
+    if (choose(vecs, 1).wpr == 0) {
         const int grid = static_cast<int>(std::min<int64_t>(rows, 2 * sms));
         if (bf) norm_fwd_wide_kernel<__nv_bfloat16><<<grid, 1024, 0, s>>>(a);
         else norm_fwd_wide_kernel<float><<<grid, 1024, 0, s>>>(a);
         return cuda_result(cudaGetLastError(), where);
     }
-    const int64_t groups = sh.wpr == 1 ? 4 : 1, threads = sh.wpr == 1 ? 128 : 32 * sh.wpr;
-    const int grid = static_cast<int>(std::min<int64_t>((rows + groups - 1) / groups, sms * (1536 / threads)));
-    return cuda_result(bf ? run_shape<__nv_bfloat16>(sh, a, false, grid, s) : run_shape<float>(sh, a, false, grid, s),
+    const bool ring = use_ring(rows, a, sms);
+    const int most = ring ? 64 * sms : 4 * sms;
+    int grid = 0;
+    return cuda_result(bf ? run_shape<__nv_bfloat16>(vecs, a, false, ring, most, &grid, s)
+                          : run_shape<float>(vecs, a, false, ring, most, &grid, s),
                        where);
 }
 
@@ -634,9 +1038,9 @@ extern "C" int dmuon_layer_norm_backward(const void* dy, const void* x, const vo
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     int partials = 0;
     if (rows > 0) {
-        const Shape sh = choose(rows, (cols + vec - 1) / vec, sms, true);
+        const int64_t vecs = (cols + vec - 1) / vec;
         cudaError_t e;
-        if (sh.wpr == 0) {
+        if (choose(vecs, 1).wpr == 0) {
             const int grid = static_cast<int>(std::min<int64_t>(rows, 2 * sms));
             if (bf) norm_bwd_wide_kernel<__nv_bfloat16><<<grid, 1024, 0, s>>>(a);
             else norm_bwd_wide_kernel<float><<<grid, 1024, 0, s>>>(a);
@@ -651,10 +1055,10 @@ extern "C" int dmuon_layer_norm_backward(const void* dy, const void* x, const vo
                 e = cudaGetLastError();
             }
         } else {
-            const int64_t groups = kBwdThreads / (32 * sh.wpr);
-            partials = static_cast<int>(std::min<int64_t>({(rows + groups - 1) / groups, int64_t(2) * sms,
-                                                           partial_rows(rows)}));
-            e = bf ? run_shape<__nv_bfloat16>(sh, a, true, partials, s) : run_shape<float>(sh, a, true, partials, s);
+            const int most = static_cast<int>(std::min<int64_t>(4 * sms, partial_rows(rows)));
+            const bool ring = use_ring(rows, a, sms);
+            e = bf ? run_shape<__nv_bfloat16>(vecs, a, true, ring, most, &partials, s)
+                   : run_shape<float>(vecs, a, true, ring, most, &partials, s);
         }
         if (e != cudaSuccess) return cuda_result(e, where);
     }

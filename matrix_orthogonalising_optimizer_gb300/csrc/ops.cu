@@ -529,10 +529,10 @@ Operand rows_of(const Operand& o, int64_t r0, int64_t n) {
 using namespace dmuon;
 
 extern "C" int dmuon_ops_status(void) {
-    int32_t v = 0;
-    if (ops_read_status(&v) != cudaSuccess)
-        return fail(DMUON_ERR_CUDA, "dmuon_ops_status: cannot read the status flag");
-    return v ? DMUON_ERR_DEVICE_TIMEOUT : DMUON_OK;
+    int32_t v = 0, w = 0;
+    if (ops_read_status(&v) != cudaSuccess || norm_read_status(&w) != cudaSuccess)
+        return fail(DMUON_ERR_CUDA, "dmuon_ops_status: cannot read the status flags");
+    return v || w ? DMUON_ERR_DEVICE_TIMEOUT : DMUON_OK;
 }
 
 extern "C" size_t dmuon_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype,
@@ -577,15 +577,15 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
         OpsStream a = stream_args(L.x, L.wg, hidden, dim);
         a.w[1] = static_cast<const __nv_bfloat16*>(L.wu.p);
         a.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
-        a.out0 = out_of(L.h);
+        a.out[0] = out_of(L.h);
         if (saved_act) {
-            a.out1 = user_mat(saved_act, hidden, f32);
-            a.out2 = user_mat(saved_slope, hidden, f32);
+            a.out[1] = user_mat(saved_act, hidden, f32);
+            a.out[2] = user_mat(saved_slope, hidden, f32);
         }
         OPS_CUDA(launch_ops_stream(a, OPS_GATE, s));
         a = stream_args(L.h, L.wd, dim, hidden);
         a.after = 1;
-        a.out0 = user_mat(y, dim, f32);
+        a.out[0] = user_mat(y, dim, f32);
         OPS_CUDA(launch_ops_stream(a, OPS_STORE, s));
         return DMUON_OK;
     }
@@ -595,14 +595,14 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
     const Operand b[2] = {L.wg, L.wu};
     OPS_TRY(set_problem(P, tokens, hidden, dim, &L.x, false, b, false, 2, true));
     P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
-    P.out0 = out_of(L.h);
+    P.out[0] = out_of(L.h);
     if (saved_act) {
-        P.out1 = user_mat(saved_act, hidden, f32);
-        P.out2 = user_mat(saved_slope, hidden, f32);
-        if (L.h.p != saved_h) P.out3 = user_mat(saved_h, hidden, f32);
+        P.out[1] = user_mat(saved_act, hidden, f32);
+        P.out[2] = user_mat(saved_slope, hidden, f32);
+        if (L.h.p != saved_h) P.out[3] = user_mat(saved_h, hidden, f32);
     }
     OPS_TRY(set_problem(l[1].p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false));
-    l[1].p[0].out0 = user_mat(y, dim, f32);
+    l[1].p[0].out[0] = user_mat(y, dim, f32);
     OPS_TRY(schedule(l, 2, L.common, s, where));
     OPS_CUDA(L.pack.run(s));
     OPS_CUDA(launch_ops_gemm(l[0], OPS_GATE, f32, s));
@@ -646,25 +646,25 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     l[0].n = 1;
     OpsProblem& P = l[0].p[0];
     OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false));
-    P.in0 = user_mat(saved_act, hidden, f32);
-    P.in1 = user_mat(saved_slope, hidden, f32);
-    P.out0 = out_of(L.da);
-    P.out1 = out_of(L.du);
+    P.in[0] = user_mat(saved_slope, hidden, f32);
+    P.in[1] = user_mat(saved_act, hidden, f32);
+    P.out[0] = out_of(L.da);
+    P.out[1] = out_of(L.du);
     // dx and the three weight gradients in one launch, the longest K first
     l[1].n = 4;
     OpsProblem* p = l[1].p;
     const bool dx_first = 2 * hidden >= tokens;
     int k = dx_first ? 1 : 0;
     OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.da, true, &L.x, true, 1, false));
-    p[k++].out0 = user_mat(dw_gate, dim, f32);
+    p[k++].out[0] = user_mat(dw_gate, dim, f32);
     OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.du, true, &L.x, true, 1, false));
-    p[k++].out0 = user_mat(dw_up, dim, f32);
+    p[k++].out[0] = user_mat(dw_up, dim, f32);
     OPS_TRY(set_problem(p[k], dim, hidden, tokens, &L.dy, true, &L.h, true, 1, false));
-    p[k++].out0 = user_mat(dw_down, hidden, f32);
+    p[k++].out[0] = user_mat(dw_down, hidden, f32);
     k = dx_first ? 0 : 3;
     const Operand a[2] = {L.da, L.du}, b[2] = {L.wg, L.wu};
     OPS_TRY(set_problem(p[k], tokens, dim, hidden, a, false, b, true, 2, false));
-    p[k].out0 = user_mat(dx, dim, f32);
+    p[k].out[0] = user_mat(dx, dim, f32);
     OPS_TRY(schedule(l, 2, L.common, s, where));
     OPS_CUDA(L.pack.run(s));
     OPS_CUDA(launch_ops_gemm(l[0], OPS_DGATE, f32, s));
@@ -723,20 +723,20 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             P.nblk = L.nblk;
             P.target_logit = L.target_logit;
             P.targets = targets + r0;
-            if (grad) P.out0 = OpsMat{L.e, L.dz.ld, f32 ? ELEM_F32 : ELEM_BF16, 1, 0};
+            if (grad) P.out[0] = OpsMat{L.e, L.dz.ld, f32 ? ELEM_F32 : ELEM_BF16, 1, 0};
         }
         if (grad) {
             l[1].n = 2;
             const int kx = vocab >= n ? 0 : 1;
             OPS_TRY(set_problem(l[1].p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false));
-            l[1].p[kx].out0 = user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
+            l[1].p[kx].out[0] = user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
             OpsProblem& W = l[1].p[1 - kx];
             OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false));
             // the sum over pieces stays in fp32: rounded once, with the last piece
             const OpsMat sum = L.dw_sum ? user_mat(L.dw_sum, up(dim, 4), true) : user_mat(dweight, dim, f32);
             const bool last = i + 1 == L.pieces;
-            W.out0 = last ? user_mat(dweight, dim, f32) : sum;
-            if (i > 0) W.in0 = sum;
+            W.out[0] = last ? user_mat(dweight, dim, f32) : sum;
+            if (i > 0) W.in[0] = sum;
         }
         OPS_TRY(schedule(l, 2, L.common, s, where));
         if (i == 0) OPS_CUDA(L.pack.run(s));
@@ -746,7 +746,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             a.nblk = L.nblk;
             a.target_logit = L.target_logit;
             a.targets = targets + r0;
-            if (grad) a.out0 = out_of(L.dz);
+            if (grad) a.out[0] = out_of(L.dz);
             OPS_CUDA(launch_ops_stream(a, OPS_LOGITS, s));
         } else {
             OPS_CUDA(launch_ops_gemm(l[0], OPS_LOGITS, f32, s));

@@ -58,8 +58,8 @@ struct OpsProblem {
     int32_t slot_begin;  // first partial-sum slot
     // epilogue
     int32_t act;
-    OpsMat out0, out1, out2, out3;  // STORE: D | GATE: h, act, u act', h again | DGATE: da, du | LOGITS: exponentials
-    OpsMat in0, in1;          // STORE: in0 = addend (fp32) | DGATE: act, u act'
+    OpsMat out[4];  // STORE: D | GATE: h, act, u act', h again | DGATE: da, du | LOGITS: exponentials
+    OpsMat in[2];   // STORE: in[0] = addend (fp32) | DGATE: u act', act
     float2* stats;            // LOGITS: [M][nblk] (max, sum of exp) of 128-column blocks
     int32_t nblk;
     float* target_logit;      // LOGITS: [M]
@@ -85,7 +85,7 @@ struct OpsStream {
     int32_t tokens, N, K;
     int32_t act;
     int32_t after;              // the launch directly follows the library's own kernel, which did not write w
-    OpsMat out0, out1, out2, out3;  // as OpsProblem
+    OpsMat out[4];              // as OpsProblem
     float2* stats;              // LOGITS: [tokens][nblk] of ops_stream_block() columns
     int32_t nblk;
     float* target_logit;
@@ -104,6 +104,7 @@ constexpr int kOpsTailCounts = 16;             // counters per split tile
 void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails);
 cudaError_t ops_pairs(int* pairs);  // resident CTA pairs of the GEMM kernel on the current device
 cudaError_t ops_read_status(int32_t* v);  // reads and clears the GEMM's time-out flag
+cudaError_t norm_read_status(int32_t* v);  // the same of the layer norm's ring kernels
 cudaError_t launch_ops_gemm(const OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s);
 
 }  // namespace dmuon

@@ -148,7 +148,7 @@ __device__ __forceinline__ void st_staged(T* base, int64_t ld, int r0, int c0, i
     __syncwarp();
     const int c = lane % CH;
     T* p = base + static_cast<int64_t>(r0) * ld + c0 + c;
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < 16; ++i) {
         const int r = 2 * i + lane / CH;
         const float x = stg[r * kStageLd + c];
@@ -165,7 +165,7 @@ __device__ __forceinline__ void ld_staged(const T* base, int64_t ld, int r0, int
                                           int N, float* stg) {
     const int c = lane % CH;
     const T* p = base + static_cast<int64_t>(r0) * ld + c0 + c;
-#pragma unroll
+#pragma unroll 8
     for (int i = 0; i < 16; ++i) {
         const int r = 2 * i + lane / CH;
         stg[r * kStageLd + c] = r0 + r < M && c0 + c < N ? static_cast<float>(p[r * ld]) : 0.0f;
@@ -219,22 +219,20 @@ __device__ __forceinline__ void st_f32(float* base, int64_t ld, bool vec, int r0
 }
 
 // A matrix of the given element type, or of bf16 parts (part > 0).
-__device__ __forceinline__ void st_mat(const OpsMat& m, int r0, int c0, int lane, const float (&v)[CH], int M, int N,
+__device__ __forceinline__ void st_mat(const OpsMat& m, int r0, int c0, int lane, float (&v)[CH], int M, int N,
                                        float* stg) {
     if (m.type == ELEM_F32) {
         st_f32(static_cast<float*>(m.p), m.ld, m.vec, r0, c0, lane, v, M, N, stg);
         return;
     }
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(m.p);
-    st_bf16(p, m.ld, m.vec, r0, c0, lane, v, M, N, stg);
-    if (m.part > 0) {
-        float w[CH];
+#pragma unroll 1
+    for (int k = 0; k < kF32Parts; ++k) {
+        st_bf16(p, m.ld, m.vec, r0, c0, lane, v, M, N, stg);
+        if (m.part == 0) break;
+        p += m.part;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) w[j] = bf16_rest(v[j]);
-        st_bf16(p + m.part, m.ld, m.vec, r0, c0, lane, w, M, N, stg);
-#pragma unroll
-        for (int j = 0; j < CH; ++j) w[j] = bf16_rest(w[j]);
-        st_bf16(p + 2 * m.part, m.ld, m.vec, r0, c0, lane, w, M, N, stg);
+        for (int j = 0; j < CH; ++j) v[j] = bf16_rest(v[j]);
     }
 }
 
@@ -339,74 +337,82 @@ struct RegSrc {
 
 // ------------------------------------------------------- epilogues
 // u: the unit; half: this warp's column half; r0: its first row.
+//
+// The loops over chunks, outputs and parts stay loops: an epilogue runs once or
+// a few times per launch, so its instructions come from L2, and the first form,
+// inlined per output and unrolled, spent 6 to 11 us per fp32 chunk on
+// instruction fetches.
 
 template <bool kF32, typename Src>
-__device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
-                                          int lane, float* stg) {
+__device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
+                                          float* stg) {
 #pragma unroll 1
     for (int kc = 0; kc < 8; ++kc) {
         const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
         if (c0 >= P.N) break;
         float v[CH];
         acc.load(kc, v);
-        if (P.in0.p) {
+        if (P.in[0].p) {
             float add[CH];
-            ld_mat(P.in0, r0, c0, lane, add, P.M, P.N, stg);
+            ld_mat(P.in[0], r0, c0, lane, add, P.M, P.N, stg);
 #pragma unroll
             for (int j = 0; j < CH; ++j) v[j] += add[j];
         }
-        st_mat(P.out0, r0, c0, lane, v, P.M, P.N, stg);
+        st_mat(P.out[0], r0, c0, lane, v, P.M, P.N, stg);
     }
 }
 
 template <bool kF32, typename Src>
-__device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
-                                         int lane, float* stg) {
+__device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
+                                         float* stg) {
 #pragma unroll 1
     for (int kc = 0; kc < 4; ++kc) {
         const int c0 = u.tn * (BN / 2) + half * (BN / 4) + kc * CH;
         if (c0 >= P.N) break;
-        float a[CH], w[CH];
-        acc.load_pair(kc, a, w);
-        if (P.out1.p) {
-            float f[CH], s[CH];
+        float f[CH], s[CH], h[CH];
+        acc.load_pair(kc, f, h);
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                const float g = act_gate<kF32>(P.act, a[j]);
-                f[j] = a[j] * g;
-                s[j] = w[j] * act_slope<kF32>(P.act, a[j], g);
-                w[j] *= f[j];
-            }
-            st_mat(P.out1, r0, c0, lane, f, P.M, P.N, stg);
-            st_mat(P.out2, r0, c0, lane, s, P.M, P.N, stg);
-            if (P.out3.p) st_mat(P.out3, r0, c0, lane, w, P.M, P.N, stg);
-        } else {
-#pragma unroll
-            for (int j = 0; j < CH; ++j) w[j] *= a[j] * act_gate<kF32>(P.act, a[j]);
+        for (int j = 0; j < CH; ++j) {
+            const float a = f[j], w = h[j], g = act_gate<kF32>(P.act, a);
+            f[j] = a * g;
+            h[j] = f[j] * w;
+            if (P.out[1].p) s[j] = w * act_slope<kF32>(P.act, a, g);
         }
-        st_mat(P.out0, r0, c0, lane, w, P.M, P.N, stg);
+#pragma unroll 1
+        for (int o = 0; o < 4; ++o) {
+            if (!P.out[o].p) continue;
+            float v[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) v[j] = o == 1 ? f[j] : o == 2 ? s[j] : h[j];
+            st_mat(P.out[o], r0, c0, lane, v, P.M, P.N, stg);
+        }
     }
 }
 
 template <bool kF32, typename Src>
-__device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0,
-                                          int lane, float* stg) {
+__device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
+                                          float* stg) {
 #pragma unroll 1
     for (int kc = 0; kc < 8; ++kc) {
         const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
         if (c0 >= P.N) break;
-        float f[CH], s[CH], v[CH];
-        ld_mat(P.in0, r0, c0, lane, f, P.M, P.N, stg);
-        ld_mat(P.in1, r0, c0, lane, s, P.M, P.N, stg);
+        float v[CH];
         acc.load(kc, v);
+        // da = dh u act'(a), du = dh act(a)
+#pragma unroll 1
+        for (int o = 0; o < 2; ++o) {
+            float x[CH];
+            ld_mat(P.in[o], r0, c0, lane, x, P.M, P.N, stg);
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            s[j] *= v[j];  // da = dh u act'(a)
-            f[j] *= v[j];  // du = dh act(a)
+            for (int j = 0; j < CH; ++j) x[j] *= v[j];
+            st_mat(P.out[o], r0, c0, lane, x, P.M, P.N, stg);
         }
-        st_mat(P.out0, r0, c0, lane, s, P.M, P.N, stg);
-        st_mat(P.out1, r0, c0, lane, f, P.M, P.N, stg);
     }
+}
+
+template <bool kF32>
+__device__ __forceinline__ float exp_of(float z, float m, float ms) {
+    return kF32 ? expf(z - m) : ex2(fmaf(z, kLog2e, -ms));
 }
 
 template <bool kF32>
@@ -415,8 +421,7 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
     const int cb = u.tn * BN + half * (BN / 2);
     const int r = r0 + lane;
     const float ninf = __int_as_float(0xff800000);
-    const bool whole = cb + BN / 2 <= P.N;
-    if (!whole) {  // columns past the vocabulary: exp gives 0
+    if (cb + BN / 2 > P.N) {  // columns past the vocabulary: exp gives 0
 #pragma unroll
         for (int j = 0; j < BN / 2; ++j) z[j] = cb + j < P.N ? z[j] : ninf;
     }
@@ -436,17 +441,25 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
     }
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const float ms = m * kLog2e;
+    if (P.out[0].p) {
+        RegSrc src{z};
+#pragma unroll 1
+        for (int kc = 0; kc < 8; ++kc) {
+            float v[CH];
+            src.load(kc, v);
 #pragma unroll
-    for (int kc = 0; kc < 8; ++kc) {
-        float v[CH];
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            v[j] = kF32 ? expf(z[kc * CH + j] - m) : ex2(fmaf(z[kc * CH + j], kLog2e, -ms));
-            sum[j % 4] += v[j];
+            for (int j = 0; j < CH; ++j) {
+                v[j] = exp_of<kF32>(v[j], m, ms);
+                sum[j % 4] += v[j];
+            }
+            st_mat(P.out[0], r0, cb + kc * CH, lane, v, P.M, P.N, stg);
         }
-        if (P.out0.p) st_mat(P.out0, r0, cb + kc * CH, lane, v, P.M, P.N, stg);
+    } else {
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j) sum[j % 4] += exp_of<kF32>(z[j], m, ms);
     }
-    if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] =
+        make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
 template <int kKind, bool kF32>
@@ -680,6 +693,17 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
             bool active = r0 < P.M && c_first < P.N;
             uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
             const int buf = it & 1;
+            if (kKind == OPS_DGATE && u.part == 0 && r0 + lane < P.M) {
+                // this warp's share of the stored act and slope into L2, a
+                // mainloop ahead of their use
+#pragma unroll 1
+                for (int o = 0; o < 2; ++o) {
+                    const int es = P.in[o].type == ELEM_BF16 ? 2 : 4;
+                    const char* row = static_cast<const char*>(P.in[o].p) + (r0 + lane) * P.in[o].ld * es;
+                    for (int c = c_first; c < min(c_first + BN / 2, P.N); c += 128 / es)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(row + c * es)));
+                }
+            }
             if constexpr (kRegs) {
                 // add the chains up; each accumulator goes back to the MMAs
                 // before anything is done with the sum

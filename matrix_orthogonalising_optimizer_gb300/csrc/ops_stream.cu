@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) ops_stream_kernel(c
     if constexpr (kKind == OPS_STORE) {
         for (int i = threadIdx.x; i < R * T; i += kThreads) {
             const int tok = i / R, n = n0 + i % R;
-            if (tok < P.tokens && n < P.N) st1(P.out0, tok, n, v[i]);
+            if (tok < P.tokens && n < P.N) st1(P.out[0], tok, n, v[i]);
         }
     } else if constexpr (kKind == OPS_GATE) {
         for (int i = threadIdx.x; i < R * T / 2; i += kThreads) {
@@ -177,12 +177,12 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) ops_stream_kernel(c
             if (tok >= P.tokens || n >= P.N) continue;
             const float a = v[at], u = v[at + 8];
             const float gate = act_gate<false>(P.act, a), f = a * gate;
-            if (P.out1.p) {
-                st1(P.out1, tok, n, f);
-                st1(P.out2, tok, n, u * act_slope<false>(P.act, a, gate));
-                if (P.out3.p) st1(P.out3, tok, n, f * u);
+            if (P.out[1].p) {
+                st1(P.out[1], tok, n, f);
+                st1(P.out[2], tok, n, u * act_slope<false>(P.act, a, gate));
+                if (P.out[3].p) st1(P.out[3], tok, n, f * u);
             }
-            st1(P.out0, tok, n, f * u);
+            st1(P.out[0], tok, n, f * u);
         }
     } else {
         // R lanes per token: maximum and sum of exponentials of the block's columns
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) ops_stream_kernel(c
             for (int o = R / 2; o; o >>= 1) s += __shfl_xor_sync(tc::kFullMask, s, o);
             if (tok >= P.tokens || n >= P.N) continue;
             if (P.targets[tok] == n) P.target_logit[tok] = z;
-            if (P.out0.p) st1(P.out0, tok, n, e);
+            if (P.out[0].p) st1(P.out[0], tok, n, e);
             if (i % R == 0) P.stats[static_cast<int64_t>(tok) * P.nblk + tile] = make_float2(m, s);
         }
     }

@@ -199,7 +199,8 @@ def norm_reference(x, w, b, eps):
 
 
 NORM_SHAPES = [(1, 1), (1, 768), (3, 7), (5, 64), (2, 1000), (37, 1001), (700, 96), (1300, 2048), (3, 4096),
-               (640, 4100), (20, 8192), (9, 12000), (33, 16384), (5, 16400), (3, 40001)]
+               (640, 4100), (20, 8192), (9, 12000), (33, 16384), (5, 16400), (3, 40001), (1250, 4096),
+               (2000, 96), (1217, 16384), (1500, 8192), (1300, 12288), (5000, 8), (3001, 520)]
 
 
 @pytest.mark.gpu
