@@ -420,10 +420,12 @@ int dmuon_layer_norm_backward(const void* dy, const void* x, const void* weight,
  * with act = a sigmoid(a) (SILU) or a Phi(a), Phi the normal distribution
  * function (GELU).  Both projections, the activation and the product are one
  * kernel on the tensor cores.  saved_act, saved_slope, saved_h: tokens x hidden
- * each, receive act(a), u act'(a) and h for the backward pass, or all NULL.
- * bf16: these, h as the next product's operand, and da and du below are the
- * only values rounded to bf16 on the way, once each from fp32 (keeping a and u
- * instead would save one array and cost a second rounding in every gradient).
+ * each, receive act(a), u act'(a) and h for the backward pass, or all NULL;
+ * saved_h in dtype, the other two in saved_dtype: DMUON_FP32, or dtype.
+ * bf16: h, da and du (below), the operands of the next products, are rounded to
+ * bf16 once from fp32; with saved_dtype DMUON_FP32 nothing else is, with
+ * DMUON_BF16 (half the memory) act(a) and u act'(a) are too, which takes the
+ * gradients' error from 1.4 to 1.7 roundings of their own type.
  * fp32: every product runs as six products of bf16 parts (x = hi + mid + lo),
  * which keeps fp32 accuracy.  tokens in [0, 2^24], dim and hidden in
  * [1, 2^20].  Widths that are a multiple of 8 are read in place; bf16 matrices
@@ -433,8 +435,8 @@ int dmuon_layer_norm_backward(const void* dy, const void* x, const void* weight,
 /* Workspace of the forward or the backward pass (0 for sizes it refuses, and for no tokens). */
 size_t dmuon_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype, int32_t backward);
 int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const void* w_up, const void* w_down, void* y,
-                            void* saved_act, void* saved_slope, void* saved_h, int64_t tokens, int64_t dim,
-                            int64_t hidden, int32_t dtype, int32_t activation, void* workspace,
+                            void* saved_act, void* saved_slope, void* saved_h, int32_t saved_dtype, int64_t tokens,
+                            int64_t dim, int64_t hidden, int32_t dtype, int32_t activation, void* workspace,
                             size_t workspace_bytes, void* stream);
 /* With dh = dy w_down, da = dh saved_slope, du = dh saved_act:
  *   dx = da w_gate + du w_up,  dw_gate = da^T x,  dw_up = du^T x,  dw_down = dy^T saved_h.
@@ -444,9 +446,10 @@ int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const void* w_up,
  * DMUON_ERR_UNSUPPORTED_DEVICE (not sm_103) or DMUON_ERR_CUDA, like the
  * forward pass. */
 int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up, const void* w_down,
-                             const void* saved_act, const void* saved_slope, const void* saved_h, void* dx,
-                             void* dw_gate, void* dw_up, void* dw_down, int64_t tokens, int64_t dim, int64_t hidden,
-                             int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+                             const void* saved_act, const void* saved_slope, const void* saved_h,
+                             int32_t saved_dtype, void* dx, void* dw_gate, void* dw_up, void* dw_down, int64_t tokens,
+                             int64_t dim, int64_t hidden, int32_t dtype, void* workspace, size_t workspace_bytes,
+                             void* stream);
 
 /* ---- vocabulary loss --------------------------------------------------------
  *

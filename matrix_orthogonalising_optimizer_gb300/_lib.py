@@ -81,10 +81,11 @@ SIGNATURES = {
     "dmuon_layer_norm_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int32]),
     "dmuon_layer_norm_backward": (c_int, [c_void_p] * 8 + [c_int64, c_int64, c_int32, c_void_p, c_size_t, c_void_p]),
     "dmuon_gated_ffn_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int32]),
-    "dmuon_gated_ffn_forward": (c_int, [c_void_p] * 8 + [c_int64, c_int64, c_int64, c_int32, c_int32, c_void_p,
-                                                         c_size_t, c_void_p]),
-    "dmuon_gated_ffn_backward": (c_int, [c_void_p] * 12 + [c_int64, c_int64, c_int64, c_int32, c_void_p, c_size_t,
-                                                           c_void_p]),
+    "dmuon_gated_ffn_forward": (c_int, [c_void_p] * 8 + [c_int32, c_int64, c_int64, c_int64, c_int32, c_int32,
+                                                         c_void_p, c_size_t, c_void_p]),
+    "dmuon_gated_ffn_backward": (c_int, [c_void_p] * 8 + [c_int32] + [c_void_p] * 4 + [c_int64, c_int64, c_int64,
+                                                                                      c_int32, c_void_p, c_size_t,
+                                                                                      c_void_p]),
     "dmuon_vocab_loss_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int32, c_uint64]),
     "dmuon_vocab_loss": (c_int, [c_void_p] * 4 + [c_int64] + [c_void_p] * 4 + [c_int64, c_int64, c_int64, c_int32,
                                                                                c_uint64, c_void_p, c_size_t,

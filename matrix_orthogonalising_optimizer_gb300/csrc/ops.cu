@@ -34,7 +34,10 @@ int fail(int code, const std::string& msg) {
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 constexpr int64_t kMaxVocab = int64_t(1) << 22;
-constexpr int kChain = 8;         // K = 512 per chain of MMAs under register sums
+// K slabs per chain of MMAs under register sums: 512 deep for logits of bf16
+// operands, 256 for fp32 operands (their error against 64-bit products: 1.5e-6
+// with 512, against about 9e-7 of fp32 FMAs)
+constexpr int kChain = 8, kChainF32 = 4;
 constexpr int kMaxLaunches = 4;   // GEMM launches of one call (of one piece)
 constexpr int kSlots = 192;       // partial-sum slots: 48 MiB
 constexpr int kTails = 192;       // split tiles per launch
@@ -246,11 +249,11 @@ int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a
 }
 
 // Schedules a call's launches and zeroes the counters they need.
-int schedule(OpsLaunch* l, int launches, const Common& common, cudaStream_t s, const char* where) {
+int schedule(OpsLaunch* l, int launches, const Common& common, bool f32, cudaStream_t s, const char* where) {
     int pairs = 0;
     OPS_CUDA(ops_pairs(&pairs));
     for (int i = 0; i < launches; ++i) {
-        l[i].chain = kChain;
+        l[i].chain = f32 ? kChainF32 : kChain;
         common.bind(l[i], i);
         ops_schedule(l[i], pairs, kSlots, kTails);
     }
@@ -352,6 +355,13 @@ struct FfnLayout {
         bytes = a.off;
     }
 };
+
+// act(a) and u act'(a) are kept in the tensors' type or in fp32.
+int check_saved(int32_t saved, int32_t dtype, const char* where) {
+    if (saved != DMUON_FP32 && saved != dtype)
+        return fail(DMUON_ERR_UNSUPPORTED_DTYPE, std::string(where) + ": saved_dtype must be dtype or DMUON_FP32");
+    return DMUON_OK;
+}
 
 bool ffn_sizes_ok(int64_t n, int64_t d, int64_t f) {
     return in_range(n, 0, kMaxTokens) && in_range(d, 1, kMaxWidth) && in_range(f, 1, kMaxWidth);
@@ -546,9 +556,9 @@ extern "C" size_t dmuon_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, i
 }
 
 extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const void* w_up, const void* w_down,
-                                       void* y, void* saved_act, void* saved_slope, void* saved_h, int64_t tokens,
-                                       int64_t dim, int64_t hidden, int32_t dtype, int32_t activation, void* workspace,
-                                       size_t workspace_bytes, void* stream) {
+                                       void* y, void* saved_act, void* saved_slope, void* saved_h,
+                                       int32_t saved_dtype, int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype,
+                                       int32_t activation, void* workspace, size_t workspace_bytes, void* stream) {
     const char* where = "dmuon_gated_ffn_forward";
     OPS_TRY(check_ffn(tokens, dim, hidden, dtype, where));
     if (activation != DMUON_ACT_SILU && activation != DMUON_ACT_GELU)
@@ -556,6 +566,7 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
     if ((saved_act == nullptr) != (saved_slope == nullptr) || (saved_act == nullptr) != (saved_h == nullptr))
         return fail(DMUON_ERR_INVALID_ARG,
                     std::string(where) + ": saved_act, saved_slope and saved_h are stored together or not at all");
+    if (saved_act) OPS_TRY(check_saved(saved_dtype, dtype, where));
     if (tokens == 0) return DMUON_OK;
     OPS_TRY(check_ptr(x, "x", where));
     OPS_TRY(check_ptr(w_gate, "w_gate", where));
@@ -579,8 +590,8 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
         a.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
         a.out[0] = out_of(L.h);
         if (saved_act) {
-            a.out[1] = user_mat(saved_act, hidden, f32);
-            a.out[2] = user_mat(saved_slope, hidden, f32);
+            a.out[1] = user_mat(saved_act, hidden, saved_dtype == DMUON_FP32);
+            a.out[2] = user_mat(saved_slope, hidden, saved_dtype == DMUON_FP32);
         }
         OPS_CUDA(launch_ops_stream(a, OPS_GATE, s));
         a = stream_args(L.h, L.wd, dim, hidden);
@@ -597,13 +608,13 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
     P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
     P.out[0] = out_of(L.h);
     if (saved_act) {
-        P.out[1] = user_mat(saved_act, hidden, f32);
-        P.out[2] = user_mat(saved_slope, hidden, f32);
+        P.out[1] = user_mat(saved_act, hidden, saved_dtype == DMUON_FP32);
+        P.out[2] = user_mat(saved_slope, hidden, saved_dtype == DMUON_FP32);
         if (L.h.p != saved_h) P.out[3] = user_mat(saved_h, hidden, f32);
     }
     OPS_TRY(set_problem(l[1].p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false));
     l[1].p[0].out[0] = user_mat(y, dim, f32);
-    OPS_TRY(schedule(l, 2, L.common, s, where));
+    OPS_TRY(schedule(l, 2, L.common, f32, s, where));
     OPS_CUDA(L.pack.run(s));
     OPS_CUDA(launch_ops_gemm(l[0], OPS_GATE, f32, s));
     OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
@@ -612,11 +623,12 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
 
 extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up,
                                         const void* w_down, const void* saved_act, const void* saved_slope,
-                                        const void* saved_h, void* dx, void* dw_gate, void* dw_up, void* dw_down,
-                                        int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype, void* workspace,
-                                        size_t workspace_bytes, void* stream) {
+                                        const void* saved_h, int32_t saved_dtype, void* dx, void* dw_gate, void* dw_up,
+                                        void* dw_down, int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
     const char* where = "dmuon_gated_ffn_backward";
     OPS_TRY(check_ffn(tokens, dim, hidden, dtype, where));
+    OPS_TRY(check_saved(saved_dtype, dtype, where));
     OPS_TRY(check_ptr(dw_gate, "dw_gate", where));
     OPS_TRY(check_ptr(dw_up, "dw_up", where));
     OPS_TRY(check_ptr(dw_down, "dw_down", where));
@@ -646,8 +658,8 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     l[0].n = 1;
     OpsProblem& P = l[0].p[0];
     OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false));
-    P.in[0] = user_mat(saved_slope, hidden, f32);
-    P.in[1] = user_mat(saved_act, hidden, f32);
+    P.in[0] = user_mat(saved_slope, hidden, saved_dtype == DMUON_FP32);
+    P.in[1] = user_mat(saved_act, hidden, saved_dtype == DMUON_FP32);
     P.out[0] = out_of(L.da);
     P.out[1] = out_of(L.du);
     // dx and the three weight gradients in one launch, the longest K first
@@ -665,7 +677,7 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     const Operand a[2] = {L.da, L.du}, b[2] = {L.wg, L.wu};
     OPS_TRY(set_problem(p[k], tokens, dim, hidden, a, false, b, true, 2, false));
     p[k].out[0] = user_mat(dx, dim, f32);
-    OPS_TRY(schedule(l, 2, L.common, s, where));
+    OPS_TRY(schedule(l, 2, L.common, f32, s, where));
     OPS_CUDA(L.pack.run(s));
     OPS_CUDA(launch_ops_gemm(l[0], OPS_DGATE, f32, s));
     OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
@@ -738,7 +750,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             W.out[0] = last ? user_mat(dweight, dim, f32) : sum;
             if (i > 0) W.in[0] = sum;
         }
-        OPS_TRY(schedule(l, 2, L.common, s, where));
+        OPS_TRY(schedule(l, 2, L.common, f32, s, where));
         if (i == 0) OPS_CUDA(L.pack.run(s));
         if (L.stream) {
             OpsStream a = stream_args(xp, L.w, vocab, dim);

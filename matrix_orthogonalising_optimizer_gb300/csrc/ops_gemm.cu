@@ -165,11 +165,15 @@ __device__ __forceinline__ void ld_staged(const T* base, int64_t ld, int r0, int
                                           int N, float* stg) {
     const int c = lane % CH;
     const T* p = base + static_cast<int64_t>(r0) * ld + c0 + c;
-#pragma unroll 8
-    for (int i = 0; i < 16; ++i) {
+    // all loads before the first store: the compiler cannot tell the staging
+    // slice from the matrix and would wait for each in turn
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
         const int r = 2 * i + lane / CH;
-        stg[r * kStageLd + c] = r0 + r < M && c0 + c < N ? static_cast<float>(p[r * ld]) : 0.0f;
+        v[i] = r0 + r < M && c0 + c < N ? static_cast<float>(p[r * ld]) : 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) stg[(2 * i + lane / CH) * kStageLd + c] = v[i];
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < CH; ++j) v[j] = stg[lane * kStageLd + j];
@@ -236,8 +240,11 @@ __device__ __forceinline__ void st_mat(const OpsMat& m, int r0, int c0, int lane
     }
 }
 
-__device__ __forceinline__ void ld_mat(const OpsMat& m, int r0, int c0, int lane, float (&x)[CH], int M, int N,
-                                       float* stg) {
+// A load in two halves, so that several can be in flight: ld_issue's words are
+// the lane's 16-byte pieces (or, for a staged chunk, its finished values), which
+// ld_finish regroups.
+__device__ __forceinline__ void ld_issue(const OpsMat& m, int r0, int c0, int lane, float (&x)[CH], int M, int N,
+                                         float* stg) {
     if (!m.vec || c0 + CH > N) {
         if (m.type == ELEM_BF16)
             ld_staged(static_cast<const __nv_bfloat16*>(m.p), m.ld, r0, c0, lane, x, M, N, stg);
@@ -245,41 +252,43 @@ __device__ __forceinline__ void ld_mat(const OpsMat& m, int r0, int c0, int lane
             ld_staged(static_cast<const float*>(m.p), m.ld, r0, c0, lane, x, M, N, stg);
         return;
     }
-    if (m.type == ELEM_BF16) {
-        const bool odd = lane & 1;
-        const int ra = r0 + (lane & ~1);
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(m.p) + static_cast<int64_t>(ra) * m.ld + c0 +
-                                 8 * odd;
-        uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
-        if (ra < M) a = *reinterpret_cast<const uint4*>(p);
-        if (ra + 1 < M) b = *reinterpret_cast<const uint4*>(p + m.ld);
-        const uint32_t d0[4] = {a.x, a.y, a.z, a.w}, d1[4] = {b.x, b.y, b.z, b.w};
-        uint32_t w[8];
+    // bf16: two rows of a lane pair, 8 elements each; fp32: four rows of a quad, 4 each
+    const bool bf = m.type == ELEM_BF16;
+    const int rq = r0 + (bf ? lane & ~1 : lane & ~3);
+    const int es = bf ? 2 : 4;
+    const char* p = static_cast<const char*>(m.p) + (static_cast<int64_t>(rq) * m.ld + c0) * es +
+                    16 * (bf ? lane & 1 : lane & 3);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t recv = __shfl_xor_sync(kFullMask, odd ? d0[k] : d1[k], 1);
-            w[k] = odd ? recv : d0[k];
-            w[4 + k] = odd ? d1[k] : recv;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float2 f = unpack_bf16x2(w[k]);
-            x[2 * k] = f.x;
-            x[2 * k + 1] = f.y;
-        }
-    } else {
-        const int rq = r0 + (lane & ~3);
-        const float* p = static_cast<const float*>(m.p) + static_cast<int64_t>(rq) * m.ld + c0 + 4 * (lane & 3);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (rq + j < M) q = *reinterpret_cast<const float4*>(p + j * m.ld);
-            x[4 * j] = q.x;
-            x[4 * j + 1] = q.y;
-            x[4 * j + 2] = q.z;
-            x[4 * j + 3] = q.w;
-        }
+    for (int j = 0; j < 4; ++j) {
+        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if ((j < 2 || !bf) && rq + j < M) q = *reinterpret_cast<const float4*>(p + j * m.ld * es);
+        x[4 * j] = q.x;
+        x[4 * j + 1] = q.y;
+        x[4 * j + 2] = q.z;
+        x[4 * j + 3] = q.w;
+    }
+}
+
+__device__ __forceinline__ void ld_finish(const OpsMat& m, int c0, int lane, float (&x)[CH], int N) {
+    if (!m.vec || c0 + CH > N) return;
+    if (m.type != ELEM_BF16) {
         quad_transpose(x, lane);
+        return;
+    }
+    const bool odd = lane & 1;
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t d0 = __float_as_uint(x[k]), d1 = __float_as_uint(x[4 + k]);
+        const uint32_t recv = __shfl_xor_sync(kFullMask, odd ? d0 : d1, 1);
+        w[k] = odd ? recv : d0;
+        w[4 + k] = odd ? d1 : recv;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float2 f = unpack_bf16x2(w[k]);
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
     }
 }
 
@@ -354,7 +363,8 @@ __device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Un
         acc.load(kc, v);
         if (P.in[0].p) {
             float add[CH];
-            ld_mat(P.in[0], r0, c0, lane, add, P.M, P.N, stg);
+            ld_issue(P.in[0], r0, c0, lane, add, P.M, P.N, stg);
+            ld_finish(P.in[0], c0, lane, add, P.N);
 #pragma unroll
             for (int j = 0; j < CH; ++j) v[j] += add[j];
         }
@@ -396,15 +406,18 @@ __device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Un
     for (int kc = 0; kc < 8; ++kc) {
         const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
         if (c0 >= P.N) break;
-        float v[CH];
-        acc.load(kc, v);
         // da = dh u act'(a), du = dh act(a)
+        float s[CH], f[CH], v[CH];
+        ld_issue(P.in[0], r0, c0, lane, s, P.M, P.N, stg);
+        ld_issue(P.in[1], r0, c0, lane, f, P.M, P.N, stg);
+        acc.load(kc, v);
+        ld_finish(P.in[0], c0, lane, s, P.N);
+        ld_finish(P.in[1], c0, lane, f, P.N);
 #pragma unroll 1
         for (int o = 0; o < 2; ++o) {
             float x[CH];
-            ld_mat(P.in[o], r0, c0, lane, x, P.M, P.N, stg);
 #pragma unroll
-            for (int j = 0; j < CH; ++j) x[j] *= v[j];
+            for (int j = 0; j < CH; ++j) x[j] = (o ? f[j] : s[j]) * v[j];
             st_mat(P.out[o], r0, c0, lane, x, P.M, P.N, stg);
         }
     }

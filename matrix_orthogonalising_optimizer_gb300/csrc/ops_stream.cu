@@ -47,7 +47,8 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 
 __device__ __forceinline__ void st1(const OpsMat& m, int64_t r, int64_t c, float v) {
-    static_cast<__nv_bfloat16*>(m.p)[r * m.ld + c] = __float2bfloat16_rn(v);
+    if (m.type == ELEM_BF16) static_cast<__nv_bfloat16*>(m.p)[r * m.ld + c] = __float2bfloat16_rn(v);
+    else static_cast<float*>(m.p)[r * m.ld + c] = v;
 }
 
 template <int kKind, int NT, int MT>

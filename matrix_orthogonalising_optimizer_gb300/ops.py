@@ -158,7 +158,7 @@ def gated_ffn_workspace(tokens, dim, hidden, dtype="bf16", backward=False) -> in
 def gated_ffn(x, w_gate, w_up, w_down, activation="silu", save=False, workspace=None, stream=None):
     """``y = h w_down^T`` with ``h = act(a) * u``, ``a = x w_gate^T``, ``u = x w_up^T``; with
     ``save`` ``(y, saved, h)``, what the backward pass reads: ``saved`` is the pair
-    ``(act(a), u act'(a))``."""
+    ``(act(a), u act'(a))``, in fp32, or with ``save="compact"`` in x's dtype."""
     dt, dev, shape = x.dtype, x.device, x.shape
     dim, hidden = shape[-1], w_gate.shape[0]
     tokens = x.numel() // dim if dim else 0
@@ -171,13 +171,14 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu", save=False, workspace=
                               lambda: gated_ffn(x, w_gate, w_up, w_down, activation, save, workspace))
     s = _raw_stream(dev.index)
     y = torch.empty_like(x)
-    saved, h = (None, None), None
+    saved, h, kind = (None, None), None, dt
     if save:
         h = torch.empty(*shape[:-1], hidden, dtype=dt, device=dev)
-        saved = (torch.empty_like(h), torch.empty_like(h))
+        kind = dt if save == "compact" else torch.float32
+        saved = (torch.empty_like(h, dtype=kind), torch.empty_like(h, dtype=kind))
     wp, wb, _keep = _space(workspace, lambda: gated_ffn_workspace(tokens, dim, hidden, dt), dev)
     st = _lib.load().dmuon_gated_ffn_forward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
-                                             y.data_ptr(), _ptr(saved[0]), _ptr(saved[1]), _ptr(h), tokens, dim,
+                                             y.data_ptr(), _ptr(saved[0]), _ptr(saved[1]), _ptr(h), _dtype(kind), tokens, dim,
                                              hidden, _dtype(dt), act, wp, wb, s)
     _lib.check(st, "dmuon_gated_ffn_forward")
     return (y, saved, h) if save else y
@@ -193,8 +194,9 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, h, activation="silu",
     tokens = x.numel() // dim if dim else 0
     inner = (*shape[:-1], hidden)
     _check("gated_ffn_backward", dev, dt, ("x", x, shape), ("dy", dy, shape), ("w_gate", w_gate, (hidden, dim)),
-           ("w_up", w_up, (hidden, dim)), ("w_down", w_down, (dim, hidden)), ("saved[0]", saved[0], inner),
-           ("saved[1]", saved[1], inner), ("h", h, inner))
+           ("w_up", w_up, (hidden, dim)), ("w_down", w_down, (dim, hidden)), ("h", h, inner))
+    kind = saved[0].dtype
+    _check("gated_ffn_backward", dev, kind, ("saved[0]", saved[0], inner), ("saved[1]", saved[1], inner))
     _act(activation)
 
     if _elsewhere(stream, dev):
@@ -206,7 +208,7 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, h, activation="silu",
     wp, wb, _keep = _space(workspace, lambda: gated_ffn_workspace(tokens, dim, hidden, dt, backward=True), dev)
     st = _lib.load().dmuon_gated_ffn_backward(dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
                                               w_down.data_ptr(), saved[0].data_ptr(), saved[1].data_ptr(),
-                                              h.data_ptr(), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
+                                              h.data_ptr(), _dtype(kind), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
                                               dwd.data_ptr(), tokens, dim, hidden, _dtype(dt), wp, wb, s)
     _lib.check(st, "dmuon_gated_ffn_backward")
     return dx, dwg, dwu, dwd

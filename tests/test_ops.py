@@ -97,9 +97,10 @@ def test_gated_ffn_refusals(lib):
     # fp32 operands are packed into bf16 parts
     assert lib.dmuon_gated_ffn_workspace_bytes(4, 64, 128, _lib.FP32, 0) > need + 6 * 3 * 64 * 128
 
-    def fwd(x=P16, y=P16, slope=P16, h=P16, tokens=4, dim=64, hidden=128, dtype=_lib.BF16, act=0, ws=P16, n=need):
-        return lib.dmuon_gated_ffn_forward(x, P16, P16, P16, y, P16, slope, h, tokens, dim, hidden, dtype, act, ws, n,
-                                           None)
+    def fwd(x=P16, y=P16, slope=P16, h=P16, saved=_lib.FP32, tokens=4, dim=64, hidden=128, dtype=_lib.BF16, act=0,
+            ws=P16, n=need):
+        return lib.dmuon_gated_ffn_forward(x, P16, P16, P16, y, P16, slope, h, saved, tokens, dim, hidden,
+                                           dtype, act, ws, n, None)
 
     for bad in (dict(tokens=-1), dict(tokens=(1 << 24) + 1), dict(dim=0), dict(hidden=0), dict(hidden=1 << 21)):
         assert fwd(**bad) == _lib.ERR_INVALID_ARG
@@ -107,6 +108,8 @@ def test_gated_ffn_refusals(lib):
     assert fwd(act=2) == _lib.ERR_INVALID_ARG and "activation" in err(lib)
     assert fwd(slope=None) == _lib.ERR_INVALID_ARG and "together" in err(lib)
     assert fwd(h=None) == _lib.ERR_INVALID_ARG
+    assert fwd(saved=3) == _lib.ERR_UNSUPPORTED_DTYPE
+    assert fwd(saved=_lib.BF16, dtype=_lib.FP32) == _lib.ERR_UNSUPPORTED_DTYPE
     assert fwd(x=None) == _lib.ERR_INVALID_ARG
     assert fwd(y=P16 + 4) == _lib.ERR_ALIGN
     assert fwd(ws=None) == _lib.ERR_NO_WORKSPACE
@@ -114,9 +117,11 @@ def test_gated_ffn_refusals(lib):
     assert fwd(n=need - 1) == _lib.ERR_WORKSPACE_TOO_SMALL
     assert fwd(tokens=0, ws=None) == _lib.OK
 
-    def bwd(dy=P16, dwd=P16, ws=P16, n=back):
-        return lib.dmuon_gated_ffn_backward(dy, P16, P16, P16, P16, P16, P16, P16, P16, P16, P16, dwd, 4, 64, 128,
-                                            _lib.BF16, ws, n, None)
+    def bwd(dy=P16, dwd=P16, ws=P16, n=back, saved=_lib.BF16):
+        return lib.dmuon_gated_ffn_backward(dy, P16, P16, P16, P16, P16, P16, P16, saved, P16, P16, P16, dwd, 4, 64,
+                                            128, _lib.BF16, ws, n, None)
+
+    assert bwd(saved=-1) == _lib.ERR_UNSUPPORTED_DTYPE
 
     assert bwd(dy=None) == _lib.ERR_INVALID_ARG
     assert bwd(dwd=P16 + 2) == _lib.ERR_ALIGN
@@ -300,7 +305,9 @@ def test_gated_ffn(n, d, f, dtype):
     dt = DT[dtype]
     act = "gelu" if (n + d + f) % 2 else "silu"
     x, wg, wu, wd, dy = ffn_inputs(n, d, f, dt, n * 7 + d * 3 + f)
-    y, (f_act, f_slope), h_out = pkg.gated_ffn(x, wg, wu, wd, activation=act, save=True)
+    save = "compact" if n % 3 == 0 else True
+    y, (f_act, f_slope), h_out = pkg.gated_ffn(x, wg, wu, wd, activation=act, save=save)
+    assert f_act.dtype == f_slope.dtype == (dt if save == "compact" else torch.float32)
     assert torch.equal(y, pkg.gated_ffn(x, wg, wu, wd, activation=act))
     X, G, UP, D, DY = (t.double() for t in (x, wg, wu, wd, dy))
     u = U[dt]
@@ -310,9 +317,10 @@ def test_gated_ffn(n, d, f, dtype):
     h = p * eu
     # |act'| <= 1.13 and |act''| <= 0.8
     perr = FN * p.abs() + 1.2 * da_
-    within(f_act, p, u * p.abs() + (1 + u) * perr, "act")
+    us = U[f_act.dtype]
+    within(f_act, p, us * p.abs() + (1 + us) * perr, "act")
     serr = FN * dpb + 0.8 * da_
-    within(f_slope, dp * eu, u * (dp * eu).abs() + (1 + u) * (serr * (eu.abs() + du_) + dpb * du_), "slope")
+    within(f_slope, dp * eu, us * (dp * eu).abs() + (1 + us) * (serr * (eu.abs() + du_) + dpb * du_), "slope")
     herr = FN * h.abs() + 1.2 * (da_ * eu.abs() + du_ * p.abs() + da_ * du_)
     within(h_out, h, u * h.abs() + (1 + u) * herr, "h")
     # the operand h is rounded once for bf16
