@@ -773,7 +773,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         a.ignore = ignore_index;
         a.vocab = vocab;
         a.nblk = L.nblk;
-        a.shift = L.block == 128 ? 7 : L.block == 32 ? 5 : 4;
+        while ((1 << a.shift) < L.block) ++a.shift;
         int segs = 1;
         if (grad) {
             a.e = L.e;

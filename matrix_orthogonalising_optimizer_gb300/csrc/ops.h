@@ -92,7 +92,7 @@ struct OpsStream {
     const int64_t* targets;
 };
 
-constexpr int kStreamTokens = 32;  // most rows ops_stream takes
+constexpr int kStreamTokens = 16;  // most rows ops_stream takes
 int ops_stream_block(int64_t tokens);  // LOGITS: columns per statistics block
 cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s);
 

@@ -402,17 +402,29 @@ __device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Uni
 template <bool kF32, typename Src>
 __device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
                                           float* stg) {
+    const int cb = u.tn * BN + half * (BN / 2);
+    // da = dh u act'(a), du = dh act(a); the next chunk's loads are issued before
+    // this one's stores
+    float ns[CH], nf[CH];
+    ld_issue(P.in[0], r0, cb, lane, ns, P.M, P.N, stg);
+    ld_issue(P.in[1], r0, cb, lane, nf, P.M, P.N, stg);
 #pragma unroll 1
     for (int kc = 0; kc < 8; ++kc) {
-        const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
+        const int c0 = cb + kc * CH;
         if (c0 >= P.N) break;
-        // da = dh u act'(a), du = dh act(a)
         float s[CH], f[CH], v[CH];
-        ld_issue(P.in[0], r0, c0, lane, s, P.M, P.N, stg);
-        ld_issue(P.in[1], r0, c0, lane, f, P.M, P.N, stg);
-        acc.load(kc, v);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            s[j] = ns[j];
+            f[j] = nf[j];
+        }
         ld_finish(P.in[0], c0, lane, s, P.N);
         ld_finish(P.in[1], c0, lane, f, P.N);
+        if (kc < 7 && c0 + CH < P.N) {
+            ld_issue(P.in[0], r0, c0 + CH, lane, ns, P.M, P.N, stg);
+            ld_issue(P.in[1], r0, c0 + CH, lane, nf, P.M, P.N, stg);
+        }
+        acc.load(kc, v);
 #pragma unroll 1
         for (int o = 0; o < 2; ++o) {
             float x[CH];
@@ -556,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                     mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 0));
                     mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 1));
                 } else {
-                    t = wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
+                    // the first unit is known without the leader's word
+                    t = k == 0 ? t_next : wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
                     release_tile(S.tile_empty, k);
                 }
                 if (t >= total) {
@@ -881,57 +894,101 @@ cudaError_t ops_pairs(int* pairs) {
     });
 }
 
-// Work units.  A launch ends when its last unit does: with T equal tiles on P
-// pairs the last round leaves P - T mod P pairs idle.  The tiles of that round
-// are split into S K ranges, S minimising the round's time: ceil(rem S / P)
-// units of total / S slabs plus what a unit costs beside its slabs, and the
-// partial sums that the last unit of a tile loads one after the other (all in
-// slabs, about 0.35 us).  In a launch of several products the longest tiles come
-// first (the caller's order), and a product whose tiles are long against the
-// launch's share per pair is split throughout.
+// Work units.  Whole tiles are split into S ranges of K where that shortens the
+// launch.  The estimate, in slabs (about 0.35 us each), is measured on tiles of a
+// few hundred tokens: a unit costs its slabs and kUnitCost; a unit of a split
+// tile kStoreCost more (its partial sum's way to L2 and the arrival), and the
+// tile's last unit kPartCost for each part it adds up.
+//  - One product: T equal tiles on P pairs leave P - T mod P pairs idle in the
+//    last round, so the tiles of that round are the ones split.
+//  - Several products: the estimate is the larger of the work per pair and the
+//    longest unit (which the caller places first); the product with the longest
+//    unit is split further while that lowers it.
+namespace {
+
+constexpr double kUnitCost = 4.0, kStoreCost = 10.0, kPartCost = 8.0;
+constexpr int kMinSlabs = 8, kMaxSplit = 32;
+
+// The longest chain of a tile of `total` slabs in s ranges, and its work.
+double unit_cost(int total, int s) {
+    return static_cast<double>(total) / s + kUnitCost + (s > 1 ? kStoreCost + kPartCost * s : 0.0);
+}
+double tile_work(int total, int s) {
+    return total + s * kUnitCost + (s > 1 ? s * kStoreCost + kPartCost * s : 0.0);
+}
+
+}  // namespace
+
 void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
-    constexpr double kUnitCost = 4.0, kStoreCost = 12.0, kPartCost = 3.0;  // slabs
-    constexpr int kMinSlabs = 8;         // per range
-    double work = 0.0;
-    for (int i = 0; i < l.n; ++i)
-        work += static_cast<double>(l.p[i].tiles_m) * l.p[i].tiles_n * l.p[i].slabs * l.p[i].nseg;
-    const double share = work / pairs;  // slabs per pair
+    int split[kOpsMaxProblems], rem[kOpsMaxProblems];
+    for (int i = 0; i < l.n; ++i) {
+        split[i] = 1;
+        rem[i] = l.p[i].tiles_m * l.p[i].tiles_n;
+    }
+    if (l.n == 1) {
+        const int total = l.p[0].slabs * l.p[0].nseg;
+        rem[0] %= pairs;
+        double best = total + kUnitCost;
+        for (int s = 2; s <= kMaxSplit && rem[0] > 0 && total / s >= kMinSlabs; ++s) {
+            const int64_t rounds = (static_cast<int64_t>(rem[0]) * s + pairs - 1) / pairs;
+            const double c = (rounds - 1) * (static_cast<double>(total) / s + kUnitCost + kStoreCost) +
+                             unit_cost(total, s);
+            if (c < best) {
+                best = c;
+                split[0] = s;
+            }
+        }
+    } else {
+        const auto estimate = [&](int* longest) {
+            double work = 0.0, most = 0.0;
+            for (int i = 0; i < l.n; ++i) {
+                const int total = l.p[i].slabs * l.p[i].nseg;
+                work += tile_work(total, split[i]) * l.p[i].tiles_m * l.p[i].tiles_n;
+                const double c = unit_cost(total, split[i]);
+                if (c > most) {
+                    most = c;
+                    *longest = i;
+                }
+            }
+            return work / pairs > most ? work / pairs : most;
+        };
+        int longest = 0;
+        double best = estimate(&longest);
+        for (;;) {
+            const int k = longest, total = l.p[k].slabs * l.p[k].nseg, was = split[k];
+            int s = was + 1, unused = 0;
+            double c = best;
+            for (; s <= kMaxSplit && total / s >= kMinSlabs; ++s) {
+                split[k] = s;
+                c = estimate(&unused);
+                if (c < best) break;
+            }
+            if (!(c < best)) {
+                split[k] = was;
+                break;
+            }
+            best = c;
+            longest = unused;
+        }
+    }
     int unit = 0, tail = 0, slot = 0;
     for (int i = 0; i < l.n; ++i) {
         OpsProblem& p = l.p[i];
-        const int tiles = p.tiles_m * p.tiles_n, total = p.slabs * p.nseg;
-        int rem = 0, best = 1;
-        if (l.n == 1) {
-            rem = tiles % pairs;
-            double cost = total + kUnitCost;
-            for (int s = 2; s <= 32 && rem > 0 && total / s >= kMinSlabs; ++s) {
-                const double c = static_cast<double>((static_cast<int64_t>(rem) * s + pairs - 1) / pairs) *
-                                     (static_cast<double>(total) / s + kUnitCost) +
-                                 kStoreCost + kPartCost * s;
-                if (c < cost) {
-                    cost = c;
-                    best = s;
-                }
-            }
-        } else if (total > 0.25 * share) {
-            rem = tiles;
-            best = static_cast<int>(4.0 * total / share) + 1;
-            if (best > 12) best = 12;
-            if (best > total / kMinSlabs) best = total / kMinSlabs;
+        const int tiles = p.tiles_m * p.tiles_n;
+        int r = rem[i], s = split[i];
+        while (s > 1 && static_cast<int64_t>(r) * s > slots - slot) --s;
+        if (s <= 1 || r > tails - tail) {
+            r = 0;
+            s = 1;
         }
-        while (best > 1 && (static_cast<int64_t>(rem) * best > slots - slot || rem > tails - tail)) --best;
-        if (best <= 1 || rem > tails - tail) {
-            rem = 0;
-            best = 1;
-        }
-        p.whole = tiles - rem;
-        p.split = best;
+        p.whole = tiles - r;
+        p.split = s;
         p.unit_begin = unit;
         p.tail_begin = tail;
         p.slot_begin = slot;
-        unit += p.whole + rem * best;
-        tail += rem;
-        slot += rem * best;
+        unit += p.whole + r * s;
+        tail += r;
+        slot += r * s;
     }
     l.total_units = unit;
 }

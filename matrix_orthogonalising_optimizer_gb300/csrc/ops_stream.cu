@@ -29,6 +29,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
+// Per instance, by n8 tiles of x rows (1: up to 8 rows, 2: up to 16): 16-row
+// weight tiles of a warp, K pieces loaded at a time, resident blocks per SM, and
+// the blocks per SM below which K is shared by a cluster.  Measured at 4096 x
+// 14336 (block) and 4096 x 131072 (loss): one row 56 and 158 us, 16 rows 60 and
+// 180; deeper unrolling, more residents or wider clusters each lost 4 to 50 %.
+__host__ __device__ constexpr int kTiles(int nt) { return nt; }
+__host__ __device__ constexpr int kUnroll(int nt) { return nt + 1; }
+__host__ __device__ constexpr int kResident(int nt) { return nt == 1 ? 4 : 2; }
+constexpr int kSpread(int nt) { return nt == 1 ? 2 : 1; }
+
 __device__ __forceinline__ uint4 ld_stream(const __nv_bfloat16* p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -52,9 +62,9 @@ __device__ __forceinline__ void st1(const OpsMat& m, int64_t r, int64_t c, float
 }
 
 template <int kKind, int NT, int MT>
-__global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) ops_stream_kernel(const __grid_constant__ OpsStream P) {
+__global__ void __launch_bounds__(kThreads, kResident(NT)) ops_stream_kernel(const __grid_constant__ OpsStream P) {
     constexpr int R = 16 * MT, T = 8 * NT;     // weight rows, x rows of the block's result
-    constexpr int U = MT == 1 ? 4 : 2;         // K pieces loaded at a time
+    constexpr int U = kUnroll(NT);         // K pieces loaded at a time
     __shared__ float part[kWarps][R * T];      // [warp][token][row]
     __shared__ float sum[R * T];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -210,14 +220,12 @@ using Kernel = void (*)(OpsStream);
 
 template <int kKind>
 Kernel pick(int tokens) {
-    if (tokens <= 8) return ops_stream_kernel<kKind, 1, 1>;
-    if (tokens <= 16) return ops_stream_kernel<kKind, 2, 2>;
-    return ops_stream_kernel<kKind, 4, 2>;
+    return tokens <= 8 ? ops_stream_kernel<kKind, 1, kTiles(1)> : ops_stream_kernel<kKind, 2, kTiles(2)>;
 }
 
 }  // namespace
 
-int ops_stream_block(int64_t tokens) { return tokens <= 8 ? 16 : 32; }
+int ops_stream_block(int64_t tokens) { return 16 * kTiles(tokens <= 8 ? 1 : 2); }
 
 cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s) {
     int dev = 0, sms = 0;
@@ -226,12 +234,12 @@ cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s) 
     static PerDevice count;
     e = count.get(dev, &sms, [&](int* out) { return cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev); });
     if (e != cudaSuccess) return e;
-    const int rows = (a.tokens <= 8 ? 16 : 32) / (kind == OPS_GATE ? 2 : 1);
+    const int rows = ops_stream_block(a.tokens) / (kind == OPS_GATE ? 2 : 1);
     const int tiles = (a.N + rows - 1) / rows;
-    // at least about six blocks per SM, so the last round is short; a block keeps
-    // at least two rounds of its eight warps
+    // a block keeps at least two rounds of its eight warps
+    const int spread = kSpread(a.tokens <= 8 ? 1 : 2);
     int cluster = 1;
-    while (cluster < 8 && tiles * cluster < 6 * sms && a.K / (cluster * 2) >= 2 * 32 * kWarps) cluster *= 2;
+    while (cluster < 8 && tiles * cluster < spread * sms && a.K / (cluster * 2) >= 2 * 32 * kWarps) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
