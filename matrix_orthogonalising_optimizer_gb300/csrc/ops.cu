@@ -197,7 +197,7 @@ OpsMat user_mat(const void* p, int64_t ld, bool f32) {
 
 // ------------------------------------------------------------ products
 
-int encode(CUtensorMap* map, const Operand& o, bool mn) {
+int encode(CUtensorMap* map, const Operand& o, bool mn, int rows) {
     static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -211,8 +211,8 @@ int encode(CUtensorMap* map, const Operand& o, bool mn) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
                                 static_cast<cuuint64_t>(o.parts)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld * 2), static_cast<cuuint64_t>(o.part * 2)};
-    // K-major: 64 deep x 128 rows; MN-major: 64 columns x 64 deep
-    const cuuint32_t box[3] = {64, mn ? 64u : 128u, 1};
+    // K-major: 64 deep x `rows`; MN-major: 64 columns x 64 deep
+    const cuuint32_t box[3] = {64, mn ? 64u : static_cast<cuuint32_t>(rows), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -224,10 +224,11 @@ int encode(CUtensorMap* map, const Operand& o, bool mn) {
 // D (M x N) = sum over sources of A_s B_s, K deep each.  `dual`: B's two
 // sources are two matrices of N rows against one A.
 int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a, bool a_mn, const Operand* b,
-                bool b_mn, int sources, bool dual) {
+                bool b_mn, int sources, bool dual, int bn) {
     const int na = dual ? 1 : sources;
-    for (int s = 0; s < na; ++s) OPS_TRY(encode(&P.a[s], a[s], a_mn));
-    for (int s = 0; s < sources; ++s) OPS_TRY(encode(&P.b[s], b[s], b_mn));
+    for (int s = 0; s < na; ++s) OPS_TRY(encode(&P.a[s], a[s], a_mn, 128));
+    for (int s = 0; s < sources; ++s) OPS_TRY(encode(&P.b[s], b[s], b_mn, bn / 2));
+    P.bn = bn;
     P.maps_a = na;
     P.maps_b = sources;
     P.M = static_cast<int32_t>(M);
@@ -237,7 +238,7 @@ int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a
     P.b_mn = b_mn;
     P.dual = dual;
     P.tiles_m = static_cast<int32_t>(ceil_div(M, 256));
-    P.tiles_n = static_cast<int32_t>(ceil_div(N, dual ? 128 : 256));
+    P.tiles_n = static_cast<int32_t>(ceil_div(N, dual ? bn / 2 : bn));
     // part products above 2^-24 of the whole, the smallest first
     static const int kPairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
     const bool f32 = a[0].parts > 1;
@@ -248,10 +249,14 @@ int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a
     return DMUON_OK;
 }
 
+// Columns per tile of a launch's only product.
+int tile_columns(int64_t M, int64_t N, int64_t K, bool dual, bool f32, int pairs) {
+    return ops_tile_columns(M, N, ceil_div(K, 64) * (f32 ? 6 : 1), dual, pairs);
+}
+
 // Schedules a call's launches and zeroes the counters they need.
-int schedule(OpsLaunch* l, int launches, const Common& common, bool f32, cudaStream_t s, const char* where) {
-    int pairs = 0;
-    OPS_CUDA(ops_pairs(&pairs));
+int schedule(OpsLaunch* l, int launches, const Common& common, bool f32, int pairs, cudaStream_t s,
+             const char* where) {
     for (int i = 0; i < launches; ++i) {
         l[i].chain = f32 ? kChainF32 : kChain;
         common.bind(l[i], i);
@@ -600,11 +605,14 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
         OPS_CUDA(launch_ops_stream(a, OPS_STORE, s));
         return DMUON_OK;
     }
+    int pairs = 0;
+    OPS_CUDA(ops_pairs(&pairs));
     OpsLaunch l[2] = {};
     l[0].n = l[1].n = 1;
     OpsProblem& P = l[0].p[0];
     const Operand b[2] = {L.wg, L.wu};
-    OPS_TRY(set_problem(P, tokens, hidden, dim, &L.x, false, b, false, 2, true));
+    OPS_TRY(set_problem(P, tokens, hidden, dim, &L.x, false, b, false, 2, true,
+                        tile_columns(tokens, hidden, dim, true, f32, pairs)));
     P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
     P.out[0] = out_of(L.h);
     if (saved_act) {
@@ -612,9 +620,10 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
         P.out[2] = user_mat(saved_slope, hidden, saved_dtype == DMUON_FP32);
         if (L.h.p != saved_h) P.out[3] = user_mat(saved_h, hidden, f32);
     }
-    OPS_TRY(set_problem(l[1].p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false));
+    OPS_TRY(set_problem(l[1].p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false,
+                        tile_columns(tokens, dim, hidden, false, f32, pairs)));
     l[1].p[0].out[0] = user_mat(y, dim, f32);
-    OPS_TRY(schedule(l, 2, L.common, f32, s, where));
+    OPS_TRY(schedule(l, 2, L.common, f32, pairs, s, where));
     OPS_CUDA(L.pack.run(s));
     OPS_CUDA(launch_ops_gemm(l[0], OPS_GATE, f32, s));
     OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
@@ -653,11 +662,14 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     FfnLayout L(static_cast<char*>(workspace), x, w_gate, w_up, w_down, dy, saved_h, tokens, dim, hidden, f32, true);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
+    int pairs = 0;
+    OPS_CUDA(ops_pairs(&pairs));
     OpsLaunch l[2] = {};
     // dh = dy Wd; the epilogue turns it into da and du
     l[0].n = 1;
     OpsProblem& P = l[0].p[0];
-    OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false));
+    OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false,
+                        tile_columns(tokens, hidden, dim, false, f32, pairs)));
     P.in[0] = user_mat(saved_slope, hidden, saved_dtype == DMUON_FP32);
     P.in[1] = user_mat(saved_act, hidden, saved_dtype == DMUON_FP32);
     P.out[0] = out_of(L.da);
@@ -666,18 +678,21 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     l[1].n = 4;
     OpsProblem* p = l[1].p;
     const bool dx_first = 2 * hidden >= tokens;
+    // 128-column tiles while all products' tiles fit the pairs at once
+    const auto tiles = [](int64_t m, int64_t n, int bn) { return ceil_div(m, 256) * ceil_div(n, bn); };
+    const int bn = tiles(tokens, dim, 128) + 2 * tiles(hidden, dim, 128) + tiles(dim, hidden, 128) <= pairs ? 128 : 256;
     int k = dx_first ? 1 : 0;
-    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.da, true, &L.x, true, 1, false));
+    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.da, true, &L.x, true, 1, false, bn));
     p[k++].out[0] = user_mat(dw_gate, dim, f32);
-    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.du, true, &L.x, true, 1, false));
+    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.du, true, &L.x, true, 1, false, bn));
     p[k++].out[0] = user_mat(dw_up, dim, f32);
-    OPS_TRY(set_problem(p[k], dim, hidden, tokens, &L.dy, true, &L.h, true, 1, false));
+    OPS_TRY(set_problem(p[k], dim, hidden, tokens, &L.dy, true, &L.h, true, 1, false, bn));
     p[k++].out[0] = user_mat(dw_down, hidden, f32);
     k = dx_first ? 0 : 3;
     const Operand a[2] = {L.da, L.du}, b[2] = {L.wg, L.wu};
-    OPS_TRY(set_problem(p[k], tokens, dim, hidden, a, false, b, true, 2, false));
+    OPS_TRY(set_problem(p[k], tokens, dim, hidden, a, false, b, true, 2, false, bn));
     p[k].out[0] = user_mat(dx, dim, f32);
-    OPS_TRY(schedule(l, 2, L.common, f32, s, where));
+    OPS_TRY(schedule(l, 2, L.common, f32, pairs, s, where));
     OPS_CUDA(L.pack.run(s));
     OPS_CUDA(launch_ops_gemm(l[0], OPS_DGATE, f32, s));
     OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
@@ -720,6 +735,8 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
     LossLayout L(static_cast<char*>(workspace), x, weight, tokens, dim, vocab, f32, grad, budget);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
+    int pairs = 0;
+    OPS_CUDA(ops_pairs(&pairs));
     const int64_t es = f32 ? 4 : 2;
     for (int64_t i = 0; i < L.pieces; ++i) {
         const int64_t r0 = i * L.piece, n = std::min(L.piece, tokens - r0);
@@ -730,7 +747,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         if (!L.stream) {
             l[0].n = 1;
             OpsProblem& P = l[0].p[0];
-            OPS_TRY(set_problem(P, n, vocab, dim, &xp, false, &L.w, false, 1, false));
+            OPS_TRY(set_problem(P, n, vocab, dim, &xp, false, &L.w, false, 1, false, 256));
             P.stats = L.stats;
             P.nblk = L.nblk;
             P.target_logit = L.target_logit;
@@ -740,17 +757,19 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         if (grad) {
             l[1].n = 2;
             const int kx = vocab >= n ? 0 : 1;
-            OPS_TRY(set_problem(l[1].p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false));
+            const int bn = ceil_div(n, 256) * ceil_div(dim, 128) + ceil_div(vocab, 256) * ceil_div(dim, 128) <= pairs
+                               ? 128 : 256;
+            OPS_TRY(set_problem(l[1].p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false, bn));
             l[1].p[kx].out[0] = user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
             OpsProblem& W = l[1].p[1 - kx];
-            OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false));
+            OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false, bn));
             // the sum over pieces stays in fp32: rounded once, with the last piece
             const OpsMat sum = L.dw_sum ? user_mat(L.dw_sum, up(dim, 4), true) : user_mat(dweight, dim, f32);
             const bool last = i + 1 == L.pieces;
             W.out[0] = last ? user_mat(dweight, dim, f32) : sum;
             if (i > 0) W.in[0] = sum;
         }
-        OPS_TRY(schedule(l, 2, L.common, f32, s, where));
+        OPS_TRY(schedule(l, 2, L.common, f32, pairs, s, where));
         if (i == 0) OPS_CUDA(L.pack.run(s));
         if (L.stream) {
             OpsStream a = stream_args(xp, L.w, vocab, dim);

@@ -40,13 +40,14 @@ struct OpsMat {
 // reads source, A part and B part from seg[s]; every segment is `slabs` 64-deep
 // K slabs long (a ragged end is zero-filled by TMA).  A is K-major (stored
 // M x K) or MN-major (stored K x M), B likewise (N x K or K x N).  `dual`: B is
-// two matrices of N rows, source maps b[0] and b[1], and a pair tile is 128
-// columns of each (CTA rank r loads those of matrix r), so accumulator columns
-// 0..127 belong to the first and 128..255 to the second.
+// two matrices of N rows, source maps b[0] and b[1], and a pair tile is bn / 2
+// columns of each (CTA rank r loads those of matrix r), so the lower half of the
+// accumulator's columns belongs to the first and the upper half to the second.
 struct OpsProblem {
     CUtensorMap a[2], b[2];
     int32_t maps_a, maps_b;     // tensor maps in use
     int32_t M, N;
+    int32_t bn;                 // columns of a pair tile: 256, or 128 (not LOGITS)
     int32_t slabs, nseg;
     uint16_t seg[kOpsMaxSegs];  // source | A part << 4 | B part << 8
     int32_t a_mn, b_mn, dual;
@@ -99,6 +100,8 @@ cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s);
 constexpr int64_t kOpsSlotFloats = 256 * 256;  // one partial accumulator of a pair tile
 constexpr int kOpsTailCounts = 16;             // counters per split tile
 
+// Columns per pair tile for a launch's only product.  Host only.
+int ops_tile_columns(int64_t M, int64_t N, int64_t total_slabs, bool dual, int pairs);
 // Splits the launch's problems into work units (see OpsProblem) for `pairs`
 // resident CTA pairs; `slots` partial-sum slots are available.  Host only.
 void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails);

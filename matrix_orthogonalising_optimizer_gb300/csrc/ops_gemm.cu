@@ -50,7 +50,6 @@ constexpr int kPair = 2;
 constexpr int kThreads = 384;
 constexpr int OP_BYTES = 128 * 128;             // one CTA's share of an operand slab
 constexpr int MN_BOX_BYTES = SLAB_K * 128;      // one MN-major box: 64 K-rows x 128 B
-constexpr uint32_t STAGE_TX = kPair * 2 * OP_BYTES;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kTileRing = 4;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
@@ -74,10 +73,10 @@ struct __align__(1024) Smem {
     float stage[kEpiWarps][32 * kStageLd];  // a 32 x 16 chunk per epilogue warp (rows of unaligned matrices)
 };
 
-__host__ __device__ constexpr uint32_t make_idesc(bool a_mn, bool b_mn) {
-    // kind::f16: bf16 A and B, fp32 D, M = 256 (the pair), N = 256
+__device__ __forceinline__ uint32_t make_idesc(bool a_mn, bool b_mn, int bn) {
+    // kind::f16: bf16 A and B, fp32 D, M = 256 (the pair), N = bn
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>((kPair * BM) >> 4) << 24);
+           (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>((kPair * BM) >> 4) << 24);
 }
 
 struct Unit {
@@ -230,13 +229,21 @@ __device__ __forceinline__ void st_mat(const OpsMat& m, int r0, int c0, int lane
         return;
     }
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(m.p);
-#pragma unroll 1
-    for (int k = 0; k < kF32Parts; ++k) {
+    if (m.part == 0) {
         st_bf16(p, m.ld, m.vec, r0, c0, lane, v, M, N, stg);
-        if (m.part == 0) break;
-        p += m.part;
+        return;
+    }
+    // parts: each the value left over rounded to 8 bits (half up, by integer
+    // addition: conversions issue at a quarter of the rate); the three are exact
+#pragma unroll 1
+    for (int k = 0; k < kF32Parts; ++k, p += m.part) {
+        float h[CH];
 #pragma unroll
-        for (int j = 0; j < CH; ++j) v[j] = bf16_rest(v[j]);
+        for (int j = 0; j < CH; ++j) {
+            h[j] = __uint_as_float((__float_as_uint(v[j]) + 0x8000u) & 0xffff0000u);
+            v[j] = fabsf(h[j]) <= 3.4e38f ? v[j] - h[j] : 0.0f;
+        }
+        st_bf16(p, m.ld, m.vec, r0, c0, lane, h, M, N, stg);
     }
 }
 
@@ -293,24 +300,37 @@ __device__ __forceinline__ void ld_finish(const OpsMat& m, int c0, int lane, flo
 }
 
 // ------------------------------------------------------- accumulator source
-// A warp's share of an accumulator is 128 columns of 32 rows, in eight chunks of
-// 16: columns 128 half .. of the tile, or for the dual tile columns 64 half ..
-// of each of its two matrices (chunks 0..3 and 4..7).
+// A warp's share of an accumulator is bn / 2 columns of 32 rows: columns (bn / 2)
+// half .. of the tile, or for the dual tile columns (bn / 4) half .. of each of its
+// two matrices.  It is worked off in chunks of 16 columns; chunk ci of eight (dual:
+// ci / 4 is the matrix) starts at this accumulator column.  With bn = 128 the
+// upper chunks (of each matrix) do not exist.
 
 template <int kKind>
-__device__ __forceinline__ int chunk_col(int half, int ci) {
-    if (kKind == OPS_GATE) return (ci >> 2) * (BN / 2) + half * (BN / 4) + (ci & 3) * CH;
-    return half * (BN / 2) + ci * CH;
+__device__ __forceinline__ int chunk_col(int bn, int half, int ci) {
+    if (kKind == OPS_GATE) return (ci >> 2) * (bn / 2) + half * (bn / 4) + (ci & 3) * CH;
+    return half * (bn / 2) + ci * CH;
+}
+
+template <int kKind>
+__device__ __forceinline__ bool chunk_in(int bn, int ci) {
+    return bn == BN || (kKind == OPS_GATE ? (ci & 3) < 2 : ci < 4);
+}
+
+// First output column of a warp's share, and its chunks (per matrix).
+template <int kKind>
+__device__ __forceinline__ int first_col(int bn, int tn, int half) {
+    return kKind == OPS_GATE ? tn * (bn / 2) + half * (bn / 4) : tn * bn + half * (bn / 2);
 }
 
 // Sums left in TMEM (one chain of MMAs over the tile's whole K range).
 template <int kKind>
 struct TmemSrc {
     uint32_t taddr;
-    int half;
+    int bn, half;
     __device__ __forceinline__ void load(int ci, float (&v)[CH]) {
         __syncwarp();
-        tmem_ld16(taddr + static_cast<uint32_t>(chunk_col<kKind>(half, ci)), v);
+        tmem_ld16(taddr + static_cast<uint32_t>(chunk_col<kKind>(bn, half, ci)), v);
     }
     __device__ __forceinline__ void load_pair(int ci, float (&a)[CH], float (&b)[CH]) {
         load(ci, a);
@@ -356,8 +376,8 @@ template <bool kF32, typename Src>
 __device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
                                           float* stg) {
 #pragma unroll 1
-    for (int kc = 0; kc < 8; ++kc) {
-        const int c0 = u.tn * BN + half * (BN / 2) + kc * CH;
+    for (int kc = 0; kc < P.bn / 32; ++kc) {
+        const int c0 = first_col<OPS_STORE>(P.bn, u.tn, half) + kc * CH;
         if (c0 >= P.N) break;
         float v[CH];
         acc.load(kc, v);
@@ -376,8 +396,8 @@ template <bool kF32, typename Src>
 __device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
                                          float* stg) {
 #pragma unroll 1
-    for (int kc = 0; kc < 4; ++kc) {
-        const int c0 = u.tn * (BN / 2) + half * (BN / 4) + kc * CH;
+    for (int kc = 0; kc < P.bn / 64; ++kc) {
+        const int c0 = first_col<OPS_GATE>(P.bn, u.tn, half) + kc * CH;
         if (c0 >= P.N) break;
         float f[CH], s[CH], h[CH];
         acc.load_pair(kc, f, h);
@@ -402,14 +422,14 @@ __device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Uni
 template <bool kF32, typename Src>
 __device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
                                           float* stg) {
-    const int cb = u.tn * BN + half * (BN / 2);
+    const int cb = first_col<OPS_DGATE>(P.bn, u.tn, half), chunks = P.bn / 32;
     // da = dh u act'(a), du = dh act(a); the next chunk's loads are issued before
     // this one's stores
     float ns[CH], nf[CH];
     ld_issue(P.in[0], r0, cb, lane, ns, P.M, P.N, stg);
     ld_issue(P.in[1], r0, cb, lane, nf, P.M, P.N, stg);
 #pragma unroll 1
-    for (int kc = 0; kc < 8; ++kc) {
+    for (int kc = 0; kc < chunks; ++kc) {
         const int c0 = cb + kc * CH;
         if (c0 >= P.N) break;
         float s[CH], f[CH], v[CH];
@@ -420,7 +440,7 @@ __device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Un
         }
         ld_finish(P.in[0], c0, lane, s, P.N);
         ld_finish(P.in[1], c0, lane, f, P.N);
-        if (kc < 7 && c0 + CH < P.N) {
+        if (kc + 1 < chunks && c0 + CH < P.N) {
             ld_issue(P.in[0], r0, c0 + CH, lane, ns, P.M, P.N, stg);
             ld_issue(P.in[1], r0, c0 + CH, lane, nf, P.M, P.N, stg);
         }
@@ -581,7 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                 const int slabs = P.slabs;
                 const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
                 const int a_row = (2 * u.tm + rank) * BM;
-                const int b_col = P.dual ? u.tn * (BN / 2) : u.tn * BN + rank * (BN / kPair);
+                const int half_n = P.bn / 2;  // this CTA's columns of B
+                const int b_col = P.dual ? u.tn * half_n : u.tn * P.bn + rank * half_n;
+                const uint32_t tx = kPair * (OP_BYTES + half_n * 128);
+                const bool wide = half_n > 64;
                 int seg = u.kb0 / slabs, within = (u.kb0 - seg * slabs) * SLAB_K;
                 const int seg_end = slabs * SLAB_K;
                 const CUtensorMap *ma = nullptr, *mb = nullptr;
@@ -601,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_expect_tx(&S.full[stage], STAGE_TX);
+                    if (rank == 0) mbar_expect_tx(&S.full[stage], tx);
                     ++n_issued;
                     const uint32_t fb = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
                     if (!a_mn) {
@@ -614,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                         tma_load_3d_pair(S.b[stage], mb, fb, within, b_col, pb);
                     } else {
                         tma_load_3d_pair(S.b[stage], mb, fb, b_col, within, pb);
-                        tma_load_3d_pair(S.b[stage] + MN_BOX_BYTES, mb, fb, b_col + 64, within, pb);
+                        if (wide) tma_load_3d_pair(S.b[stage] + MN_BOX_BYTES, mb, fb, b_col + 64, within, pb);
                     }
                     within += SLAB_K;
                     if (within == seg_end) {
@@ -660,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                 if (t >= total) break;
                 const Unit u = decode_unit(L, t);
                 const bool a_mn = L.p[u.p].a_mn != 0, b_mn = L.p[u.p].b_mn != 0;
-                const uint32_t idesc = make_idesc(a_mn, b_mn);
+                const uint32_t idesc = make_idesc(a_mn, b_mn, L.p[u.p].bn);
                 const uint64_t a0 = a_mn ? a_m : a_k, b0 = b_mn ? b_m : b_k;
                 const uint64_t a_step = a_mn ? step_mn : step_k, b_step = b_mn ? step_mn : step_k;
                 // one accumulator per chain of MMAs: the unit's whole K range, or
@@ -715,7 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
             const OpsProblem& P = L.p[u.p];
             const int r0 = (2 * u.tm + rank) * BM + q * 32;
             // false: this warp's rows or columns lie outside the matrix
-            const int c_first = kKind == OPS_GATE ? u.tn * (BN / 2) + half * (BN / 4) : u.tn * BN + half * (BN / 2);
+            const int bn = kKind == OPS_LOGITS ? BN : P.bn;
+            const int c_first = first_col<kKind>(bn, u.tn, half);
             bool active = r0 < P.M && c_first < P.N;
             uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
             const int buf = it & 1;
@@ -726,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                 for (int o = 0; o < 2; ++o) {
                     const int es = P.in[o].type == ELEM_BF16 ? 2 : 4;
                     const char* row = static_cast<const char*>(P.in[o].p) + (r0 + lane) * P.in[o].ld * es;
-                    for (int c = c_first; c < min(c_first + BN / 2, P.N); c += 128 / es)
+                    for (int c = c_first; c < min(c_first + bn / 2, P.N); c += 128 / es)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(row + c * es)));
                 }
             }
@@ -743,9 +767,10 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                         const uint32_t base = taddr + static_cast<uint32_t>((it & 1) * BN);
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
+                            if (!chunk_in<kKind>(bn, 2 * b)) continue;
                             float v[32];
                             __syncwarp();
-                            tmem_ld32(base + static_cast<uint32_t>(chunk_col<kKind>(half, 2 * b)), v);
+                            tmem_ld32(base + static_cast<uint32_t>(chunk_col<kKind>(bn, half, 2 * b)), v);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) r[b * 32 + j] += v[j];
                         }
@@ -769,26 +794,27 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
             };
             if (active && u.split == 1) {
                 if constexpr (kRegs) finish(RegSrc{r});
-                else finish(TmemSrc<kKind>{taddr, half});
+                else finish(TmemSrc<kKind>{taddr, bn, half});
             } else if (active) {
                 // store this unit's partial sum [column][row]; the last unit of
                 // the tile adds them all up, in K order
                 float* slot = L.partials + static_cast<int64_t>(u.slot) * kOpsSlotFloats +
                               static_cast<int64_t>(rank) * BN * BM + q * 32;
-                const auto inside = [&](int tcol) {
-                    return (kKind == OPS_GATE ? u.tn * (BN / 2) + tcol % (BN / 2) : u.tn * BN + tcol) < P.N;
+                const auto inside = [&](int ci, int tcol) {
+                    return chunk_in<kKind>(bn, ci) &&
+                           (kKind == OPS_GATE ? u.tn * (bn / 2) + tcol % (bn / 2) : u.tn * bn + tcol) < P.N;
                 };
                 constexpr int kUnroll = kRegs ? 8 : 1;
 #pragma unroll kUnroll
                 for (int ci = 0; ci < 8; ++ci) {
-                    const int tcol = chunk_col<kKind>(half, ci);
-                    if (!inside(tcol)) continue;
+                    const int tcol = chunk_col<kKind>(bn, half, ci);
+                    if (!inside(ci, tcol)) continue;
                     float v[CH];
                     if constexpr (kRegs) {
 #pragma unroll
                         for (int j = 0; j < CH; ++j) v[j] = r[ci * CH + j];
                     } else {
-                        TmemSrc<kKind>{taddr, half}.load(ci, v);
+                        TmemSrc<kKind>{taddr, bn, half}.load(ci, v);
                     }
                     float* p = slot + static_cast<int64_t>(u.part) * kOpsSlotFloats + static_cast<int64_t>(tcol) * BM +
                                lane;
@@ -812,8 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                         const float* p = slot + i * kOpsSlotFloats + lane;
 #pragma unroll
                         for (int ci = 0; ci < 8; ++ci) {
-                            const int tcol = chunk_col<kKind>(half, ci);
-                            if (inside(tcol)) {
+                            const int tcol = chunk_col<kKind>(bn, half, ci);
+                            if (inside(ci, tcol)) {
 #pragma unroll
                                 for (int j = 0; j < CH; ++j) sum[ci * CH + j] += __ldcg(p + (tcol + j) * BM);
                             }
@@ -918,6 +944,17 @@ double tile_work(int total, int s) {
 }
 
 }  // namespace
+
+// A 128-column tile halves a unit's epilogue and takes 0.65 of its slab time, so it
+// wins where the 256-column tiles would leave pairs idle: rounds of units times
+// the cost of one (epilogue and start about 12 and 8 slabs).
+int ops_tile_columns(int64_t M, int64_t N, int64_t total_slabs, bool dual, int pairs) {
+    const auto cost = [&](int bn, double slab, double fixed) {
+        const int64_t tiles = (M + 255) / 256 * ((N + (dual ? bn / 2 : bn) - 1) / (dual ? bn / 2 : bn));
+        return static_cast<double>((tiles + pairs - 1) / pairs) * (slab * total_slabs + fixed);
+    };
+    return cost(128, 0.65, 8.0) < cost(256, 1.0, 12.0) ? 128 : 256;
+}
 
 void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
     int split[kOpsMaxProblems], rem[kOpsMaxProblems];

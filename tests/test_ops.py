@@ -295,7 +295,8 @@ def ffn_inputs(n, d, f, dt, seed):
 
 FFN_SHAPES = [(1, 64, 128), (1, 1, 1), (2, 72, 200), (17, 128, 96), (129, 64, 257), (257, 200, 384), (300, 101, 333),
               (512, 256, 768), (31, 2048, 512), (5, 64, 5000), (1000, 520, 264), (64, 4096, 64),
-              (8, 2056, 104), (16, 40, 1032), (23, 1032, 2000), (32, 8, 8), (9, 520, 7)]
+              (8, 2056, 104), (16, 40, 1032), (23, 1032, 2000), (32, 8, 8), (9, 520, 7),
+              (1500, 64, 1280), (4000, 72, 640), (300, 1300, 1400)]
 
 
 @pytest.mark.gpu
