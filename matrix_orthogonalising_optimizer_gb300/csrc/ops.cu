@@ -226,7 +226,13 @@ int encode(CUtensorMap* map, const Operand& o, bool mn, int rows) {
 int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a, bool a_mn, const Operand* b,
                 bool b_mn, int sources, bool dual, int bn) {
     const int na = dual ? 1 : sources;
-    for (int s = 0; s < na; ++s) OPS_TRY(encode(&P.a[s], a[s], a_mn, 128));
+    // With fewer than 256 rows in all, the rows of A beyond M are not loaded (TMA
+    // spends about two cycles per 128-byte row, filled or not): what their place
+    // in shared memory holds only reaches accumulator rows that are never stored.
+    const int rows = a_mn || M > 128 ? 128 : static_cast<int>(up(M, 8));
+    P.a_rows[0] = rows;
+    P.a_rows[1] = a_mn || M > 128 ? 128 : 0;
+    for (int s = 0; s < na; ++s) OPS_TRY(encode(&P.a[s], a[s], a_mn, rows));
     for (int s = 0; s < sources; ++s) OPS_TRY(encode(&P.b[s], b[s], b_mn, bn / 2));
     P.bn = bn;
     P.maps_a = na;
@@ -312,8 +318,8 @@ int check_device(const char* where) {
 
 // The streaming kernel takes bf16 products of a few rows whose K it can read in
 // whole 16-byte pieces.
-bool use_stream(int64_t tokens, int64_t k0, int64_t k1, bool f32) {
-    return !f32 && tokens <= kStreamTokens && k0 % 8 == 0 && k1 % 8 == 0;
+bool use_stream(int64_t tokens, int64_t most, int64_t k0, int64_t k1, bool f32) {
+    return !f32 && tokens <= most && k0 % 8 == 0 && k1 % 8 == 0;
 }
 
 OpsStream stream_args(const Operand& x, const Operand& w, int64_t N, int64_t K) {
@@ -503,7 +509,7 @@ struct LossLayout {
         common.lay(a);
         x = pack.add(a, px, n, d);
         w = pack.add(a, pw, v, d);
-        stream = use_stream(n, d, 8, f32);
+        stream = use_stream(n, kStreamLossTokens, d, 8, f32);
         if (stream) block = ops_stream_block(n);
         nblk = static_cast<int>(ceil_div(v, block));
         const int64_t ld = up(v, 8);
@@ -589,7 +595,7 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (use_stream(tokens, dim, hidden, f32)) {
+    if (use_stream(tokens, kStreamTokens, dim, hidden, f32)) {
         OpsStream a = stream_args(L.x, L.wg, hidden, dim);
         a.w[1] = static_cast<const __nv_bfloat16*>(L.wu.p);
         a.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;

@@ -48,6 +48,7 @@ struct OpsProblem {
     int32_t maps_a, maps_b;     // tensor maps in use
     int32_t M, N;
     int32_t bn;                 // columns of a pair tile: 256, or 128 (not LOGITS)
+    int32_t a_rows[2];          // rows of A that CTA rank 0 / 1 loads: 128, fewer if M is below one tile
     int32_t slabs, nseg;
     uint16_t seg[kOpsMaxSegs];  // source | A part << 4 | B part << 8
     int32_t a_mn, b_mn, dual;
@@ -93,7 +94,7 @@ struct OpsStream {
     const int64_t* targets;
 };
 
-constexpr int kStreamTokens = 16;  // most rows ops_stream takes
+constexpr int kStreamTokens = 32, kStreamLossTokens = 16;  // most rows the streaming kernel takes
 int ops_stream_block(int64_t tokens);  // LOGITS: columns per statistics block
 cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s);
 

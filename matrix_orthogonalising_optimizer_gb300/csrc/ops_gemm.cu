@@ -603,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                 const int a_row = (2 * u.tm + rank) * BM;
                 const int half_n = P.bn / 2;  // this CTA's columns of B
                 const int b_col = P.dual ? u.tn * half_n : u.tn * P.bn + rank * half_n;
-                const uint32_t tx = kPair * (OP_BYTES + half_n * 128);
+                const uint32_t tx = 128 * (P.a_rows[0] + P.a_rows[1] + P.bn);
+                const bool load_a = P.a_rows[rank] > 0;
                 const bool wide = half_n > 64;
                 int seg = u.kb0 / slabs, within = (u.kb0 - seg * slabs) * SLAB_K;
                 const int seg_end = slabs * SLAB_K;
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                     ++n_issued;
                     const uint32_t fb = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
                     if (!a_mn) {
-                        tma_load_3d_pair(S.a[stage], ma, fb, within, a_row, pa);
+                        if (load_a) tma_load_3d_pair(S.a[stage], ma, fb, within, a_row, pa);
                     } else {
                         tma_load_3d_pair(S.a[stage], ma, fb, a_row, within, pa);
                         tma_load_3d_pair(S.a[stage] + MN_BOX_BYTES, ma, fb, a_row + 64, within, pa);

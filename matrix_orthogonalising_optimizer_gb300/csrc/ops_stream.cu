@@ -29,13 +29,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Per instance, by n8 tiles of x rows (1: up to 8 rows, 2: up to 16): 16-row
+// Per instance, by n8 tiles of x rows (1: up to 8 rows, 2: 16, 4: 32): 16-row
 // weight tiles of a warp, K pieces loaded at a time, resident blocks per SM, and
 // the blocks per SM below which K is shared by a cluster.  Measured at 4096 x
 // 14336 (block) and 4096 x 131072 (loss): one row 56 and 158 us, 16 rows 60 and
 // 180; deeper unrolling, more residents or wider clusters each lost 4 to 50 %.
-__host__ __device__ constexpr int kTiles(int nt) { return nt; }
-__host__ __device__ constexpr int kUnroll(int nt) { return nt + 1; }
+__host__ __device__ constexpr int kTiles(int nt) { return nt == 1 ? 1 : 2; }
+__host__ __device__ constexpr int kUnroll(int nt) { return nt == 4 ? 1 : nt + 1; }
 __host__ __device__ constexpr int kResident(int nt) { return nt == 1 ? 4 : 2; }
 constexpr int kSpread(int nt) { return nt == 1 ? 2 : 1; }
 
@@ -65,7 +65,9 @@ template <int kKind, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, kResident(NT)) ops_stream_kernel(const __grid_constant__ OpsStream P) {
     constexpr int R = 16 * MT, T = 8 * NT;     // weight rows, x rows of the block's result
     constexpr int U = kUnroll(NT);         // K pieces loaded at a time
-    __shared__ float part[kWarps][R * T];      // [warp][token][row]
+    // the warps' sums [token][row]; large results in two rounds of four warps
+    constexpr int kParts = R * T > 1024 ? kWarps / 2 : kWarps;
+    __shared__ float part[kParts][R * T];
     __shared__ float sum[R * T];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     uint32_t rank, cluster;
@@ -141,17 +143,24 @@ __global__ void __launch_bounds__(kThreads, kResident(NT)) ops_stream_kernel(con
         if (p + U * kWarps < p1) load_w(p + U * kWarps);
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int round = 0; round < kWarps / kParts; ++round) {
+        if (warp / kParts == round) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                part[warp][(8 * n + 2 * t + (i & 1)) * R + 16 * m + 8 * (i >> 1) + g] = c[m][n][i];
-    __syncthreads();
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float& p = part[warp % kParts][(8 * n + 2 * t + (i & 1)) * R + 16 * m + 8 * (i >> 1) + g];
+                        p = round ? p + c[m][n][i] : c[m][n][i];
+                    }
+        }
+        __syncthreads();
+    }
     for (int i = threadIdx.x; i < R * T; i += kThreads) {
         float s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) s += part[k][i];
+        for (int k = 0; k < kParts; ++k) s += part[k][i];
         sum[i] = s;
     }
     if (cluster > 1) {
@@ -220,12 +229,15 @@ using Kernel = void (*)(OpsStream);
 
 template <int kKind>
 Kernel pick(int tokens) {
-    return tokens <= 8 ? ops_stream_kernel<kKind, 1, kTiles(1)> : ops_stream_kernel<kKind, 2, kTiles(2)>;
+    if (tokens <= 8) return ops_stream_kernel<kKind, 1, kTiles(1)>;
+    if constexpr (kKind != OPS_LOGITS)
+        if (tokens > 16) return ops_stream_kernel<kKind, 4, kTiles(4)>;
+    return ops_stream_kernel<kKind, 2, kTiles(2)>;
 }
 
 }  // namespace
 
-int ops_stream_block(int64_t tokens) { return 16 * kTiles(tokens <= 8 ? 1 : 2); }
+int ops_stream_block(int64_t tokens) { return 16 * kTiles(tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4); }
 
 cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s) {
     int dev = 0, sms = 0;
