@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
     constexpr bool kRegs = kF32 || kKind == OPS_LOGITS;
     extern __shared__ uint8_t smem_raw[];
     Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x / 32;
+    const int warp = __shfl_sync(kFullMask, static_cast<int>(threadIdx.x) / 32, 0);  // uniform to the compiler
     const int lane = threadIdx.x % 32;
 
     if (threadIdx.x == 0) {
@@ -562,35 +562,43 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
 
     if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ------------------------------------------------ TMA producer
+            // (the whole warp runs the loop, one elected lane issues)
+            const uint32_t e = elect_one();
+            const uint32_t sa = saddr(S.a[0]), sb = saddr(S.b[0]);
             uint32_t stage = 0, phase = 0, n_issued = 0;
             bool ok = true;
             const uint32_t full0 = mapa(saddr(&S.full[0]), 0);
             // the first unit is the pair's own index; a launch with more units
             // than pairs hands out the others from the counter
             const int pairs = static_cast<int>(gridDim.x) / kPair;
-            int t_next = static_cast<int>(blockIdx.x) / kPair;
+            int t_next = static_cast<int>(blockIdx.x) / kPair;  // lane 0's counts
             const bool more = total > pairs;
             for (int k = 0; ok; ++k) {
                 int t;
                 if (rank == 0) {
                     const int slot = k % kTileRing;
                     const uint32_t ph = static_cast<uint32_t>(k / kTileRing) & 1u;
-                    if (!mbar_wait<true>(&S.tile_empty[slot], ph ^ 1u, &g_ops_status)) {
+                    if (!__all_sync(kFullMask, mbar_wait<true>(&S.tile_empty[slot], ph ^ 1u, &g_ops_status))) {
                         ok = false;
                         break;
                     }
-                    t = t_next < total ? t_next : total;
-                    if (t < total) t_next = more ? pairs + atomicAdd(L.counter, 1) : total;
-                    S.tile_slot[slot] = t;
-                    st_cluster_u32(mapa(saddr(&S.tile_slot[slot]), 1), t);
-                    mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 0));
-                    mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 1));
+                    t = min(__shfl_sync(kFullMask, t_next, 0), total);
+                    if (lane == 0) {
+                        if (t < total) t_next = more ? pairs + atomicAdd(L.counter, 1) : total;
+                        S.tile_slot[slot] = t;
+                        st_cluster_u32(mapa(saddr(&S.tile_slot[slot]), 1), t);
+                        mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 0));
+                        mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 1));
+                    }
+                    __syncwarp();
                 } else {
                     // the first unit is known without the leader's word
                     t = k == 0 ? t_next : wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
-                    release_tile(S.tile_empty, k);
+                    t = __shfl_sync(kFullMask, t, 0);
+                    if (lane == 0) release_tile(S.tile_empty, k);
+                    __syncwarp();
                 }
                 if (t >= total) {
                     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -604,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                 const int half_n = P.bn / 2;  // this CTA's columns of B
                 const int b_col = P.dual ? u.tn * half_n : u.tn * P.bn + rank * half_n;
                 const uint32_t tx = 128 * (P.a_rows[0] + P.a_rows[1] + P.bn);
-                const bool load_a = P.a_rows[rank] > 0;
-                const bool wide = half_n > 64;
+                const uint32_t e_a = P.a_rows[rank] > 0 ? e : 0u, e_b2 = half_n > 64 ? e : 0u;
+                const uint32_t e_tx = rank == 0 ? e : 0u;
                 int seg = u.kb0 / slabs, within = (u.kb0 - seg * slabs) * SLAB_K;
                 const int seg_end = slabs * SLAB_K;
                 const CUtensorMap *ma = nullptr, *mb = nullptr;
@@ -621,24 +629,25 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                         pb = sg >> 8;
                         fresh = false;
                     }
-                    if (!mbar_wait<false>(&S.empty[stage], phase ^ 1, &g_ops_status)) {
+                    if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[stage], phase ^ 1, &g_ops_status))) {
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_expect_tx(&S.full[stage], tx);
+                    mbar_expect_tx_if(e_tx, &S.full[stage], tx);
                     ++n_issued;
                     const uint32_t fb = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
+                    const uint32_t da = sa + stage * OP_BYTES, db = sb + stage * OP_BYTES;
                     if (!a_mn) {
-                        if (load_a) tma_load_3d_pair(S.a[stage], ma, fb, within, a_row, pa);
+                        tma_load_3d_pair(e_a, da, ma, fb, within, a_row, pa);
                     } else {
-                        tma_load_3d_pair(S.a[stage], ma, fb, a_row, within, pa);
-                        tma_load_3d_pair(S.a[stage] + MN_BOX_BYTES, ma, fb, a_row + 64, within, pa);
+                        tma_load_3d_pair(e, da, ma, fb, a_row, within, pa);
+                        tma_load_3d_pair(e, da + MN_BOX_BYTES, ma, fb, a_row + 64, within, pa);
                     }
                     if (!b_mn) {
-                        tma_load_3d_pair(S.b[stage], mb, fb, within, b_col, pb);
+                        tma_load_3d_pair(e, db, mb, fb, within, b_col, pb);
                     } else {
-                        tma_load_3d_pair(S.b[stage], mb, fb, b_col, within, pb);
-                        if (wide) tma_load_3d_pair(S.b[stage] + MN_BOX_BYTES, mb, fb, b_col + 64, within, pb);
+                        tma_load_3d_pair(e, db, mb, fb, b_col, within, pb);
+                        tma_load_3d_pair(e_b2, db + MN_BOX_BYTES, mb, fb, b_col + 64, within, pb);
                     }
                     within += SLAB_K;
                     if (within == seg_end) {
@@ -663,24 +672,28 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                 // the MMA's releases of the last ring round: no commit is still
                 // in flight towards this CTA when the pair leaves
                 for (int i = 0; i < STAGES && ok; ++i) {
-                    ok = mbar_wait<true>(&S.empty[stage], phase ^ 1, &g_ops_status);
+                    ok = __all_sync(kFullMask, mbar_wait<true>(&S.empty[stage], phase ^ 1, &g_ops_status));
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------ MMA issuer (leader)
+            const uint32_t e = elect_one();
             uint32_t stage = 0, phase = 0;
             bool ok = true;
+            const uint32_t empty0 = saddr(&S.empty[0]), acc0 = saddr(&S.acc_full[0]);
             const uint64_t a_k = smem_desc(saddr(S.a[0]), 0, 1024), a_m = smem_desc(saddr(S.a[0]), MN_BOX_BYTES, 1024);
             const uint64_t b_k = smem_desc(saddr(S.b[0]), 0, 1024), b_m = smem_desc(saddr(S.b[0]), MN_BOX_BYTES, 1024);
             constexpr uint64_t step_k = (UMMA_K * 2) >> 4, step_mn = (UMMA_K * 128) >> 4;
             int it = 0;
             for (int k = 0; ok; ++k) {
-                const int t = wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
-                release_tile(S.tile_empty, k);
+                const int t = __shfl_sync(
+                    kFullMask, wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total), 0);
+                if (lane == 0) release_tile(S.tile_empty, k);
+                __syncwarp();
                 if (t >= total) break;
                 const Unit u = decode_unit(L, t);
                 const bool a_mn = L.p[u.p].a_mn != 0, b_mn = L.p[u.p].b_mn != 0;
@@ -693,14 +706,14 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                     const int c1 = kRegs && c0 + L.chain < u.kb1 ? c0 + L.chain : u.kb1;
                     const int buf = it & 1;
                     const uint32_t use = static_cast<uint32_t>(it >> 1);
-                    if (!mbar_wait<true>(&S.acc_empty[buf], (use & 1) ^ 1, &g_ops_status)) {
+                    if (!__all_sync(kFullMask, mbar_wait<true>(&S.acc_empty[buf], (use & 1) ^ 1, &g_ops_status))) {
                         ok = false;
                         break;
                     }
                     fence_after();
                     const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
                     for (int kb = c0; kb < c1; ++kb) {
-                        if (!mbar_wait<false>(&S.full[stage], phase, &g_ops_status)) {
+                        if (!__all_sync(kFullMask, mbar_wait<false>(&S.full[stage], phase, &g_ops_status))) {
                             ok = false;
                             break;
                         }
@@ -709,15 +722,15 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                         const uint64_t bd = b0 + static_cast<uint64_t>(stage) * (OP_BYTES >> 4);
 #pragma unroll
                         for (int kk = 0; kk < SLAB_K / UMMA_K; ++kk)
-                            umma_bf16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb != c0 || kk) ? 1u : 0u);
-                        umma_commit_pair(&S.empty[stage], kPairMask);
+                            umma_bf16_pair(e, d, ad + kk * a_step, bd + kk * b_step, idesc, (kb != c0 || kk) ? 1u : 0u);
+                        umma_commit_pair(e, empty0 + stage * static_cast<uint32_t>(sizeof(uint64_t)), kPairMask);
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1;
                         }
                     }
                     // also on failure: covers every MMA issued so far
-                    umma_commit_pair(&S.acc_full[buf], kPairMask);
+                    umma_commit_pair(e, acc0 + buf * static_cast<uint32_t>(sizeof(uint64_t)), kPairMask);
                     c0 = c1;
                 }
             }
