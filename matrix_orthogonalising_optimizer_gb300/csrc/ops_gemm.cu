@@ -127,7 +127,7 @@ __device__ __forceinline__ int wait_tile(uint64_t* full, const int32_t* slots, i
 }
 
 __device__ __forceinline__ void release_tile(uint64_t* empty, int k) {
-    mbar_arrive_cluster(mapa(saddr(&empty[k % kTileRing]), 0));
+    mbar_arrive_cluster_relaxed(mapa(saddr(&empty[k % kTileRing]), 0));
 }
 
 // ------------------------------------------------------- matrix accesses
@@ -587,10 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                     t = min(__shfl_sync(kFullMask, t_next, 0), total);
                     if (lane == 0) {
                         if (t < total) t_next = more ? pairs + atomicAdd(L.counter, 1) : total;
-                        S.tile_slot[slot] = t;
-                        st_cluster_u32(mapa(saddr(&S.tile_slot[slot]), 1), t);
-                        mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 0));
-                        mbar_arrive_cluster(mapa(saddr(&S.tile_full[slot]), 1));
+#pragma unroll
+                        for (int c = 0; c < kPair; ++c)
+                            send_u32(mapa(saddr(&S.tile_slot[slot]), c), t, mapa(saddr(&S.tile_full[slot]), c));
                     }
                     __syncwarp();
                 } else {

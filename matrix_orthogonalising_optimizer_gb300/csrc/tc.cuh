@@ -128,16 +128,19 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
     return r;
 }
 
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, int32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// Hands a value to a CTA of the cluster: the store itself counts on the mbarrier
+// there (one arrival, 4 bytes), so neither side pays for a release at cluster
+// scope, which waits for all of the thread's earlier memory operations.
+__device__ __forceinline__ void send_u32(uint32_t dst, int32_t v, uint32_t bar) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 4;" ::"r"(bar) : "memory");
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst), "r"(v),
+                 "r"(bar)
+                 : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// Without release ordering: for a signal that covers no memory operation of
-// the arriving thread (an accumulator whose tcgen05.ld have all completed).
+// Arrive without release ordering, on an mbarrier of either CTA: for a signal
+// that covers no memory operation of the arriving thread but completed reads (an
+// accumulator whose tcgen05.ld have all completed, a slot read by an acquire).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
