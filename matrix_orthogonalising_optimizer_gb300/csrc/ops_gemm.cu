@@ -945,7 +945,7 @@ cudaError_t ops_pairs(int* pairs) {
 //    unit is split further while that lowers it.
 namespace {
 
-constexpr double kUnitCost = 4.0, kStoreCost = 10.0, kPartCost = 8.0;
+constexpr double kUnitCost = 4.0, kStoreCost = 14.0, kPartCost = 12.0;
 constexpr int kMinSlabs = 8, kMaxSplit = 32;
 
 // The longest chain of a tile of `total` slabs in s ranges, and its work.

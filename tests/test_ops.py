@@ -587,3 +587,17 @@ def test_operators_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_example_trains(dtype):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_residual_lm.py")
+    spec = importlib.util.spec_from_file_location("train_residual_lm", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses = mod.train(steps=60, vocab=500, dim=128, hidden=384, tokens=2000, dtype=DT[dtype])
+    # the first loss is near log(vocab); sixty steps at least halve it
+    assert abs(losses[0] - math.log(500)) < 1.5 and losses[-1] < 0.5 * losses[0]
