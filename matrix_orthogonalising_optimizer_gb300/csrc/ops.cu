@@ -38,6 +38,10 @@ constexpr int64_t kMaxVocab = int64_t(1) << 22;
 // operands, 256 for fp32 operands (their error against 64-bit products: 1.5e-6
 // with 512, against about 9e-7 of fp32 FMAs)
 constexpr int kChain = 8, kChainF32 = 4;
+// bf16 sums over more slabs than kLongSum (131072 deep) are added up in registers
+// too, from chains of kLongChain slabs: 2048 truncated additions drift by at most
+// 2^-13 of the sum
+constexpr int kLongSum = 2048, kLongChain = 512;
 constexpr int kMaxLaunches = 4;   // GEMM launches of one call (of one piece)
 constexpr int kSlots = 192;       // partial-sum slots: 48 MiB
 constexpr int kTails = 192;       // split tiles per launch
@@ -61,8 +65,8 @@ struct Arena {
 
 // Counters and partial sums of a call's GEMM launches.
 struct Common {
-    int32_t* counters;  // [kMaxLaunches] unit counters, 64 ints apart, then the tail counts
-    float* partials;
+    int32_t* counters = nullptr;  // [kMaxLaunches] unit counters, 64 ints apart, then the tail counts
+    float* partials = nullptr;
     static constexpr int64_t kTailInts = int64_t(kTails) * kOpsTailCounts;
     static constexpr int64_t kInts = kMaxLaunches * (64 + kTailInts);
     void lay(Arena& a) {
@@ -260,11 +264,24 @@ int tile_columns(int64_t M, int64_t N, int64_t K, bool dual, bool f32, int pairs
     return ops_tile_columns(M, N, ceil_div(K, 64) * (f32 ? 6 : 1), dual, pairs);
 }
 
-// Schedules a call's launches and zeroes the counters they need.
-int schedule(OpsLaunch* l, int launches, const Common& common, bool f32, int pairs, cudaStream_t s,
-             const char* where) {
+bool is_long(const OpsLaunch& l) {
+    bool r = false;
+    for (int k = 0; k < l.n; ++k) r = r || l.p[k].slabs * l.p[k].nseg > kLongSum;
+    return r;
+}
+
+// The instance with fp32 arithmetic and register sums also takes long sums of
+// bf16 products.
+cudaError_t launch(const OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s) {
+    return launch_ops_gemm(l, kind, f32 || is_long(l), s);
+}
+
+// Schedules a call's launches (`logits`: the first computes logits) and zeroes the
+// counters they need.
+int schedule(OpsLaunch* l, int launches, const Common& common, bool f32, bool logits, int pairs,
+             cudaStream_t s, const char* where) {
     for (int i = 0; i < launches; ++i) {
-        l[i].chain = f32 ? kChainF32 : kChain;
+        l[i].chain = f32 ? kChainF32 : logits && i == 0 ? kChain : kLongChain;
         common.bind(l[i], i);
         ops_schedule(l[i], pairs, kSlots, kTails);
     }
@@ -316,19 +333,20 @@ int check_device(const char* where) {
     return DMUON_OK;
 }
 
-// The streaming kernel takes bf16 products of a few rows whose K it can read in
+// The streaming kernels take products of a few rows whose K they can read in
 // whole 16-byte pieces.
 bool use_stream(int64_t tokens, int64_t most, int64_t k0, int64_t k1, bool f32) {
-    return !f32 && tokens <= most && k0 % 8 == 0 && k1 % 8 == 0;
+    const int64_t vec = f32 ? 4 : 8;
+    return tokens <= most && k0 % vec == 0 && k1 % vec == 0;
 }
 
-OpsStream stream_args(const Operand& x, const Operand& w, int64_t N, int64_t K) {
+OpsStream stream_args(const void* x, const void* w, int64_t tokens, int64_t N, int64_t K) {
     OpsStream a = {};
-    a.x = static_cast<const __nv_bfloat16*>(x.p);
-    a.w[0] = static_cast<const __nv_bfloat16*>(w.p);
-    a.ldx = x.ld;
-    a.ldw = w.ld;
-    a.tokens = static_cast<int32_t>(x.rows);
+    a.x = x;
+    a.w[0] = w;
+    a.ldx = K;
+    a.ldw = K;
+    a.tokens = static_cast<int32_t>(tokens);
     a.N = static_cast<int32_t>(N);
     a.K = static_cast<int32_t>(K);
     return a;
@@ -348,6 +366,12 @@ struct FfnLayout {
               const void* ph, int64_t n, int64_t d, int64_t f, bool f32, bool backward)
         : pack(f32) {
         Arena a{base};
+        if (!backward && use_stream(n, kStreamTokens, d, f, f32)) {
+            h.p = a.take<char>(n * f * (f32 ? 4 : 2));
+            if (ph) h.p = ph;
+            bytes = a.off;
+            return;
+        }
         common.lay(a);
         x = pack.add(a, px, n, d);
         wg = pack.add(a, pg, f, d);
@@ -506,11 +530,13 @@ struct LossLayout {
                uint64_t budget)
         : pack(f32) {
         Arena a{base};
-        common.lay(a);
-        x = pack.add(a, px, n, d);
-        w = pack.add(a, pw, v, d);
-        stream = use_stream(n, kStreamLossTokens, d, 8, f32);
-        if (stream) block = ops_stream_block(n);
+        stream = use_stream(n, f32 ? kStreamTokens : kStreamLossTokens, d, d, f32);
+        if (stream) block = ops_stream_block(n, f32);
+        if (grad || !stream) {
+            common.lay(a);
+            x = pack.add(a, px, n, d);
+            w = pack.add(a, pw, v, d);
+        }
         nblk = static_cast<int>(ceil_div(v, block));
         const int64_t ld = up(v, 8);
         // bytes of one token's logits: statistics, exponentials, gradients
@@ -596,19 +622,20 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
     OPS_TRY(check_device(where));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (use_stream(tokens, kStreamTokens, dim, hidden, f32)) {
-        OpsStream a = stream_args(L.x, L.wg, hidden, dim);
-        a.w[1] = static_cast<const __nv_bfloat16*>(L.wu.p);
+        // h in dtype, in the caller's saved_h if there is one
+        OpsStream a = stream_args(x, w_gate, tokens, hidden, dim);
+        a.w[1] = w_up;
         a.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
-        a.out[0] = out_of(L.h);
+        a.out[0] = user_mat(L.h.p, hidden, f32);
         if (saved_act) {
             a.out[1] = user_mat(saved_act, hidden, saved_dtype == DMUON_FP32);
             a.out[2] = user_mat(saved_slope, hidden, saved_dtype == DMUON_FP32);
         }
-        OPS_CUDA(launch_ops_stream(a, OPS_GATE, s));
-        a = stream_args(L.h, L.wd, dim, hidden);
+        OPS_CUDA(launch_ops_stream(a, OPS_GATE, f32, s));
+        a = stream_args(L.h.p, w_down, tokens, dim, hidden);
         a.after = 1;
         a.out[0] = user_mat(y, dim, f32);
-        OPS_CUDA(launch_ops_stream(a, OPS_STORE, s));
+        OPS_CUDA(launch_ops_stream(a, OPS_STORE, f32, s));
         return DMUON_OK;
     }
     int pairs = 0;
@@ -629,10 +656,10 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
     OPS_TRY(set_problem(l[1].p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false,
                         tile_columns(tokens, dim, hidden, false, f32, pairs)));
     l[1].p[0].out[0] = user_mat(y, dim, f32);
-    OPS_TRY(schedule(l, 2, L.common, f32, pairs, s, where));
+    OPS_TRY(schedule(l, 2, L.common, f32, false, pairs, s, where));
     OPS_CUDA(L.pack.run(s));
-    OPS_CUDA(launch_ops_gemm(l[0], OPS_GATE, f32, s));
-    OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
+    OPS_CUDA(launch(l[0], OPS_GATE, f32, s));
+    OPS_CUDA(launch(l[1], OPS_STORE, f32, s));
     return DMUON_OK;
 }
 
@@ -698,10 +725,10 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     const Operand a[2] = {L.da, L.du}, b[2] = {L.wg, L.wu};
     OPS_TRY(set_problem(p[k], tokens, dim, hidden, a, false, b, true, 2, false, bn));
     p[k].out[0] = user_mat(dx, dim, f32);
-    OPS_TRY(schedule(l, 2, L.common, f32, pairs, s, where));
+    OPS_TRY(schedule(l, 2, L.common, f32, false, pairs, s, where));
     OPS_CUDA(L.pack.run(s));
-    OPS_CUDA(launch_ops_gemm(l[0], OPS_DGATE, f32, s));
-    OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
+    OPS_CUDA(launch(l[0], OPS_DGATE, f32, s));
+    OPS_CUDA(launch(l[1], OPS_STORE, f32, s));
     return DMUON_OK;
 }
 
@@ -775,16 +802,16 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             W.out[0] = last ? user_mat(dweight, dim, f32) : sum;
             if (i > 0) W.in[0] = sum;
         }
-        OPS_TRY(schedule(l, 2, L.common, f32, pairs, s, where));
+        OPS_TRY(schedule(l, 2, L.common, f32, true, pairs, s, where));
         if (i == 0) OPS_CUDA(L.pack.run(s));
         if (L.stream) {
-            OpsStream a = stream_args(xp, L.w, vocab, dim);
+            OpsStream a = stream_args(static_cast<const char*>(x) + r0 * dim * es, weight, n, vocab, dim);
             a.stats = L.stats;
             a.nblk = L.nblk;
             a.target_logit = L.target_logit;
             a.targets = targets + r0;
-            if (grad) a.out[0] = out_of(L.dz);
-            OPS_CUDA(launch_ops_stream(a, OPS_LOGITS, s));
+            if (grad) a.out[0] = OpsMat{L.e, L.dz.ld, f32 ? ELEM_F32 : ELEM_BF16, 1, 0};
+            OPS_CUDA(launch_ops_stream(a, OPS_LOGITS, f32, s));
         } else {
             OPS_CUDA(launch_ops_gemm(l[0], OPS_LOGITS, f32, s));
         }
@@ -814,7 +841,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         if (f32) loss_row_kernel<true><<<grid, kRowThreads, 0, s>>>(a);
         else loss_row_kernel<false><<<grid, kRowThreads, 0, s>>>(a);
         OPS_CUDA(cudaGetLastError());
-        if (grad) OPS_CUDA(launch_ops_gemm(l[1], OPS_STORE, f32, s));
+        if (grad) OPS_CUDA(launch(l[1], OPS_STORE, f32, s));
     }
     return DMUON_OK;
 }

@@ -78,12 +78,12 @@ struct OpsLaunch {
 };
 
 // Product of a few rows x (tokens x K) with weight rows (N x K, twice for the
-// gated block), bf16, K a multiple of 8: the weights are streamed once through
-// registers (ops_stream.cu).
+// gated block), bf16 or fp32, rows of 16-byte stride: the weights are streamed
+// once through registers (ops_stream.cu).
 struct OpsStream {
-    const __nv_bfloat16* x;
-    const __nv_bfloat16* w[2];  // [0]; GATE: gate and up
-    int64_t ldx, ldw;           // elements, multiples of 8
+    const void* x;
+    const void* w[2];           // [0]; GATE: gate and up
+    int64_t ldx, ldw;           // elements, multiples of 16 bytes
     int32_t tokens, N, K;
     int32_t act;
     int32_t after;              // the launch directly follows the library's own kernel, which did not write w
@@ -95,8 +95,8 @@ struct OpsStream {
 };
 
 constexpr int kStreamTokens = 32, kStreamLossTokens = 16;  // most rows the streaming kernel takes
-int ops_stream_block(int64_t tokens);  // LOGITS: columns per statistics block
-cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s);
+int ops_stream_block(int64_t tokens, bool f32);  // LOGITS: columns per statistics block
+cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, bool f32, cudaStream_t s);
 
 constexpr int64_t kOpsSlotFloats = 256 * 256;  // one partial accumulator of a pair tile
 constexpr int kOpsTailCounts = 16;             // counters per split tile

@@ -39,7 +39,7 @@ __host__ __device__ constexpr int kUnroll(int nt) { return nt == 4 ? 1 : nt + 1;
 __host__ __device__ constexpr int kResident(int nt) { return nt == 1 ? 4 : 2; }
 constexpr int kSpread(int nt) { return nt == 1 ? 2 : 1; }
 
-__device__ __forceinline__ uint4 ld_stream(const __nv_bfloat16* p) {
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -59,6 +59,81 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 __device__ __forceinline__ void st1(const OpsMat& m, int64_t r, int64_t c, float v) {
     if (m.type == ELEM_BF16) static_cast<__nv_bfloat16*>(m.p)[r * m.ld + c] = __float2bfloat16_rn(v);
     else static_cast<float*>(m.p)[r * m.ld + c] = v;
+}
+
+// The end of a block: the warps' sums part[k][token * R + row] (every thread has
+// passed a barrier after writing them), the cluster's, and the element-wise part.
+// Rows tok0 .. tok0 + T - 1 of x, output columns n0 ..; for the gated block a
+// gate's up value is UP rows further on.
+template <int kKind, bool kF32, int R, int T, int UP, int kParts>
+__device__ __forceinline__ void finish(const OpsStream& P, float (&part)[kParts][R * T], float (&sum)[R * T], int tile,
+                                       int n0, int tok0, uint32_t rank, uint32_t cluster) {
+    for (int i = threadIdx.x; i < R * T; i += kThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) s += part[k][i];
+        sum[i] = s;
+    }
+    if (cluster > 1) {
+        tc::cluster_sync();
+        if (rank == 0) {
+            for (int i = threadIdx.x; i < R * T; i += kThreads) {
+                float s = sum[i];
+                for (uint32_t k = 1; k < cluster; ++k) {
+                    float v;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(v)
+                                 : "r"(tc::mapa(tc::saddr(&sum[i]), k))
+                                 : "memory");
+                    s += v;
+                }
+                part[0][i] = s;
+            }
+        }
+        tc::cluster_sync();  // the leader has read the others' shared memory
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
+    const float* v = cluster > 1 ? part[0] : sum;
+    if constexpr (kKind == OPS_STORE) {
+        for (int i = threadIdx.x; i < R * T; i += kThreads) {
+            const int tok = tok0 + i / R, n = n0 + i % R;
+            if (tok < P.tokens && n < P.N) st1(P.out[0], tok, n, v[i]);
+        }
+    } else if constexpr (kKind == OPS_GATE) {
+        for (int i = threadIdx.x; i < R * T / 2; i += kThreads) {
+            const int tok = tok0 + i / (R / 2), j = i % (R / 2), n = n0 + j;
+            const int at = i / (R / 2) * R + 2 * UP * (j / UP) + j % UP;
+            if (tok >= P.tokens || n >= P.N) continue;
+            const float a = v[at], u = v[at + UP];
+            const float gate = act_gate<kF32>(P.act, a), f = a * gate;
+            if (P.out[1].p) {
+                st1(P.out[1], tok, n, f);
+                st1(P.out[2], tok, n, u * act_slope<kF32>(P.act, a, gate));
+                if (P.out[3].p) st1(P.out[3], tok, n, f * u);
+            }
+            st1(P.out[0], tok, n, f * u);
+        }
+    } else {
+        // R lanes per token: maximum and sum of exponentials of the block's columns
+        const float ninf = __int_as_float(0xff800000);
+        for (int i = threadIdx.x; i < R * T; i += kThreads) {
+            const int tok = tok0 + i / R, n = n0 + i % R;
+            const float z = n < P.N ? v[i] : ninf;
+            float m = z;
+#pragma unroll
+            for (int o = R / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(tc::kFullMask, m, o));
+            const float e = kF32 ? expf(z - m) : ex2((z - m) * kLog2e);
+            float s = e;
+#pragma unroll
+            for (int o = R / 2; o; o >>= 1) s += __shfl_xor_sync(tc::kFullMask, s, o);
+            if (tok >= P.tokens || n >= P.N) continue;
+            if (P.targets[tok] == n) P.target_logit[tok] = z;
+            if (P.out[0].p) st1(P.out[0], tok, n, e);
+            if (i % R == 0) P.stats[static_cast<int64_t>(tok) * P.nblk + tile] = make_float2(m, s);
+        }
+    }
 }
 
 template <int kKind, int NT, int MT>
@@ -84,11 +159,13 @@ __global__ void __launch_bounds__(kThreads, kResident(NT)) ops_stream_kernel(con
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int n = kKind == OPS_GATE ? n0 + 8 * m + g : n0 + 16 * m + 8 * h + g;
-            wp[m][h] = P.w[kKind == OPS_GATE ? h : 0] + static_cast<int64_t>(min(n, P.N - 1)) * P.ldw + 8 * t;
+            wp[m][h] = static_cast<const __nv_bfloat16*>(P.w[kKind == OPS_GATE ? h : 0]) +
+                       static_cast<int64_t>(min(n, P.N - 1)) * P.ldw + 8 * t;
         }
     const __nv_bfloat16* xp[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xp[n] = P.x + static_cast<int64_t>(min(8 * n + g, P.tokens - 1)) * P.ldx + 8 * t;
+    for (int n = 0; n < NT; ++n)
+        xp[n] = static_cast<const __nv_bfloat16*>(P.x) + static_cast<int64_t>(min(8 * n + g, P.tokens - 1)) * P.ldx + 8 * t;
 
     // K pieces of 32: the cluster's blocks take contiguous shares, a block's
     // warps every eighth piece of its share
@@ -157,78 +234,98 @@ __global__ void __launch_bounds__(kThreads, kResident(NT)) ops_stream_kernel(con
         }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < R * T; i += kThreads) {
-        float s = 0.0f;
+    finish<kKind, false, R, T, 8, kParts>(P, part, sum, tile, n0, 0, rank, cluster);
+}
+
+// fp32: the same stream with FFMA (the tensor cores would need the weights in
+// bf16 parts: a packed copy costs four times their read).  A warp holds R = 8
+// weight rows (gated block: 4 of each projection) and T = 8 rows of x; a lane
+// loads four consecutive k of each, and the 64 sums are reduced over the lanes
+// at the end by halving.  More rows of x take further blocks that find the
+// weights in L2.
+constexpr int kF32Rows = 8;
+
+template <int kKind>
+__global__ void __launch_bounds__(kThreads, 2) ops_stream_f32_kernel(const __grid_constant__ OpsStream P) {
+    constexpr int R = kF32Rows, T = 8, UP = R / 2;
+    __shared__ float part[kWarps][R * T];
+    __shared__ float sum[R * T];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint32_t rank, cluster;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(cluster));
+    const int groups = (P.tokens + T - 1) / T;
+    const int tile = blockIdx.x / cluster / groups, tok0 = blockIdx.x / cluster % groups * T;
+    const int n0 = tile * (kKind == OPS_GATE ? R / 2 : R);
+    const float* wp[R];
+    const float* xp[T];
 #pragma unroll
-        for (int k = 0; k < kParts; ++k) s += part[k][i];
-        sum[i] = s;
+    for (int r = 0; r < R; ++r) {
+        const int n = kKind == OPS_GATE ? n0 + r % UP : n0 + r;
+        wp[r] = static_cast<const float*>(P.w[kKind == OPS_GATE ? r / UP : 0]) +
+                static_cast<int64_t>(min(n, P.N - 1)) * P.ldw + 4 * lane;
     }
-    if (cluster > 1) {
-        tc::cluster_sync();
-        if (rank == 0) {
-            for (int i = threadIdx.x; i < R * T; i += kThreads) {
-                float s = sum[i];
-                for (uint32_t k = 1; k < cluster; ++k) {
-                    float v;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(v)
-                                 : "r"(tc::mapa(tc::saddr(&sum[i]), k))
-                                 : "memory");
-                    s += v;
-                }
-                part[0][i] = s;
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        xp[t] = static_cast<const float*>(P.x) + static_cast<int64_t>(min(tok0 + t, P.tokens - 1)) * P.ldx + 4 * lane;
+    const int pieces = (P.K + 127) / 128;
+    const int p0 = static_cast<int>(static_cast<int64_t>(pieces) * rank / cluster);
+    const int p1 = static_cast<int>(static_cast<int64_t>(pieces) * (rank + 1) / cluster);
+    float acc[T * R];
+#pragma unroll
+    for (int i = 0; i < T * R; ++i) acc[i] = 0.0f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 w[R];
+    const auto load_w = [&](int p) {
+        const bool in = p < p1 && p * 128 + 4 * lane < P.K;
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r] = in ? ld_stream(wp[r] + p * 128) : zero;
+    };
+    if (P.after) load_w(p0 + warp);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!P.after) load_w(p0 + warp);
+    for (int p = p0 + warp; p < p1; p += kWarps) {
+        const bool in = p * 128 + 4 * lane < P.K;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (in) x = *reinterpret_cast<const float4*>(xp[t] + p * 128);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float& s = acc[t * R + r];
+                s = fmaf(__uint_as_float(w[r].x), x.x, s);
+                s = fmaf(__uint_as_float(w[r].y), x.y, s);
+                s = fmaf(__uint_as_float(w[r].z), x.z, s);
+                s = fmaf(__uint_as_float(w[r].w), x.w, s);
             }
         }
-        tc::cluster_sync();  // the leader has read the others' shared memory
-        if (rank != 0) return;
-    } else {
-        __syncthreads();
+        load_w(p + kWarps);
     }
-    const float* v = cluster > 1 ? part[0] : sum;
-    if constexpr (kKind == OPS_STORE) {
-        for (int i = threadIdx.x; i < R * T; i += kThreads) {
-            const int tok = i / R, n = n0 + i % R;
-            if (tok < P.tokens && n < P.N) st1(P.out[0], tok, n, v[i]);
-        }
-    } else if constexpr (kKind == OPS_GATE) {
-        for (int i = threadIdx.x; i < R * T / 2; i += kThreads) {
-            const int tok = i / (R / 2), j = i % (R / 2), n = n0 + j;
-            const int at = tok * R + 16 * (j / 8) + j % 8;
-            if (tok >= P.tokens || n >= P.N) continue;
-            const float a = v[at], u = v[at + 8];
-            const float gate = act_gate<false>(P.act, a), f = a * gate;
-            if (P.out[1].p) {
-                st1(P.out[1], tok, n, f);
-                st1(P.out[2], tok, n, u * act_slope<false>(P.act, a, gate));
-                if (P.out[3].p) st1(P.out[3], tok, n, f * u);
-            }
-            st1(P.out[0], tok, n, f * u);
-        }
-    } else {
-        // R lanes per token: maximum and sum of exponentials of the block's columns
-        const float ninf = __int_as_float(0xff800000);
-        for (int i = threadIdx.x; i < R * T; i += kThreads) {
-            const int tok = i / R, n = n0 + i % R;
-            const float z = n < P.N ? v[i] : ninf;
-            float m = z;
+    // reduce-scatter over the lanes: each step halves the sums a lane holds
 #pragma unroll
-            for (int o = R / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(tc::kFullMask, m, o));
-            const float e = ex2((z - m) * kLog2e);
-            float s = e;
+    for (int o = 16, n = T * R / 2; o; o >>= 1, n >>= 1) {
+        const bool hi = (lane & o) != 0;
 #pragma unroll
-            for (int o = R / 2; o; o >>= 1) s += __shfl_xor_sync(tc::kFullMask, s, o);
-            if (tok >= P.tokens || n >= P.N) continue;
-            if (P.targets[tok] == n) P.target_logit[tok] = z;
-            if (P.out[0].p) st1(P.out[0], tok, n, e);
-            if (i % R == 0) P.stats[static_cast<int64_t>(tok) * P.nblk + tile] = make_float2(m, s);
+        for (int i = 0; i < n; ++i) {
+            const float send = hi ? acc[i] : acc[i + n];
+            const float keep = hi ? acc[i + n] : acc[i];
+            acc[i] = keep + __shfl_xor_sync(tc::kFullMask, send, o);
         }
     }
+    const int at = (lane >> 4 & 1) * 32 + (lane >> 3 & 1) * 16 + (lane >> 2 & 1) * 8 + (lane >> 1 & 1) * 4 +
+                   (lane & 1) * 2;
+    part[warp][at] = acc[0];
+    part[warp][at + 1] = acc[1];
+    __syncthreads();
+    finish<kKind, true, R, T, UP, kWarps>(P, part, sum, tile, n0, tok0, rank, cluster);
 }
 
 using Kernel = void (*)(OpsStream);
 
 template <int kKind>
-Kernel pick(int tokens) {
+Kernel pick(int tokens, bool f32) {
+    if (f32) return ops_stream_f32_kernel<kKind>;
     if (tokens <= 8) return ops_stream_kernel<kKind, 1, kTiles(1)>;
     if constexpr (kKind != OPS_LOGITS)
         if (tokens > 16) return ops_stream_kernel<kKind, 4, kTiles(4)>;
@@ -237,21 +334,24 @@ Kernel pick(int tokens) {
 
 }  // namespace
 
-int ops_stream_block(int64_t tokens) { return 16 * kTiles(tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4); }
+int ops_stream_block(int64_t tokens, bool f32) {
+    if (f32) return kF32Rows;
+    return 16 * kTiles(tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4);
+}
 
-cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s) {
+cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, bool f32, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     static PerDevice count;
     e = count.get(dev, &sms, [&](int* out) { return cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev); });
     if (e != cudaSuccess) return e;
-    const int rows = ops_stream_block(a.tokens) / (kind == OPS_GATE ? 2 : 1);
-    const int tiles = (a.N + rows - 1) / rows;
+    const int rows = ops_stream_block(a.tokens, f32) / (kind == OPS_GATE ? 2 : 1);
+    const int tiles = (a.N + rows - 1) / rows * (f32 ? (a.tokens + 7) / 8 : 1);
     // a block keeps at least two rounds of its eight warps
-    const int spread = kSpread(a.tokens <= 8 ? 1 : 2);
+    const int spread = f32 ? 2 : kSpread(a.tokens <= 8 ? 1 : 2), piece = f32 ? 128 : 32;
     int cluster = 1;
-    while (cluster < 8 && tiles * cluster < spread * sms && a.K / (cluster * 2) >= 2 * 32 * kWarps) cluster *= 2;
+    while (cluster < 8 && tiles * cluster < spread * sms && a.K / (cluster * 2) >= 2 * piece * kWarps) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -265,9 +365,9 @@ cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, cudaStream_t s) 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const Kernel k = kind == OPS_GATE ? pick<OPS_GATE>(a.tokens)
-                     : kind == OPS_LOGITS ? pick<OPS_LOGITS>(a.tokens)
-                                          : pick<OPS_STORE>(a.tokens);
+    const Kernel k = kind == OPS_GATE     ? pick<OPS_GATE>(a.tokens, f32)
+                     : kind == OPS_LOGITS ? pick<OPS_LOGITS>(a.tokens, f32)
+                                          : pick<OPS_STORE>(a.tokens, f32);
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
