@@ -464,8 +464,8 @@ int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, 
  *   dz = coef (softmax(z) - onehot(target)),  dx = dz weight,  dweight = dz^T x.
  * The vocabulary is visited in pieces of 128 columns whose maximum and sum of
  * exponentials are kept; for the gradient the exponentials of a piece of the
- * tokens are held in the workspace (bf16, or fp32 for fp32 tensors) and turned
- * into dz there, so the logits are computed once.  Tokens are taken in pieces
+ * tokens are held in the workspace (16 bits each, or fp32 for fp32 tensors) and
+ * turned into dz there, so the logits are computed once.  Tokens are taken in pieces
  * whose logits fit `budget` bytes (0: 2 GiB; at least 256 tokens), and dweight
  * is summed over the pieces in fp32.  tokens in [0, 2^24], dim in [1, 2^20],
  * vocab in [1, 2^22].  Status codes as for the gated block. */

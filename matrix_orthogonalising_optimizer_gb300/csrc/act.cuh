@@ -42,4 +42,20 @@ __device__ __forceinline__ float act_slope(int act, float a, float gate) {
     return gate + a * pdf;
 }
 
+// An exponential relative to its block's maximum, 0 <= e <= 1, in 16 bits: 5
+// exponent and 11 mantissa bits of the fp32 value (relative error 2^-12), zero
+// below 2^-31.  bf16 would round the probability once more, by 2^-8, before the
+// gradient's own rounding.  NaN keeps the largest code and decodes to NaN.
+constexpr uint32_t kE16Base = 96u << 11;  // exponent of 2^-31
+
+__device__ __forceinline__ uint32_t e16_encode(float e) {
+    const uint32_t b = (__float_as_uint(e) + 0x800u) >> 12;  // 8 + 11 bits, rounded half up
+    return b <= kE16Base ? 0u : min(b - kE16Base, 0xffffu);
+}
+
+__device__ __forceinline__ float e16_decode(uint32_t c) {
+    if (c == 0xffffu) return __int_as_float(0x7fc00000);
+    return c ? __uint_as_float((c + kE16Base) << 12) : 0.0f;
+}
+
 }  // namespace dmuon

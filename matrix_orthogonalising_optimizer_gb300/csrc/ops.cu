@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "act.cuh"
 #include "dmuon.h"
 #include "ops.h"
 #include "tc.cuh"
@@ -180,11 +181,11 @@ struct Packer {
 };
 
 // A bf16 (parts) buffer written by one product's epilogue and read by others.
-Operand scratch(Arena& a, int64_t rows, int64_t cols, int parts) {
+Operand scratch(Arena& a, int64_t rows, int64_t cols, int parts, int64_t pad = 8) {
     Operand o;
     o.rows = rows;
     o.cols = cols;
-    o.ld = up(cols, 8);
+    o.ld = up(cols, pad);
     o.parts = parts;
     o.part = rows * o.ld;
     o.p = a.take<__nv_bfloat16>(o.part * parts);
@@ -417,7 +418,7 @@ struct LossRowArgs {
     const float* coef;          // NULL: 1
     float* loss;
     float* lse;
-    const void* e;              // exponentials (bf16 or fp32), NULL: losses only
+    const void* e;              // exponentials (16-bit codes or fp32), NULL: losses only
     __nv_bfloat16* dz;          // logit gradients, kF32Parts parts for fp32
     int64_t ld, part, ignore;
     int64_t vocab;
@@ -484,13 +485,12 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
             v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
             v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
         } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.e) + off);
+            const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.e) + off);
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 f = tc::unpack_bf16x2(w[k]);
-                v[2 * k] = f.x;
-                v[2 * k + 1] = f.y;
+                v[2 * k] = e16_decode(w[k] & 0xffffu);
+                v[2 * k + 1] = e16_decode(w[k] >> 16);
             }
         }
         const float scale = c * expf(st[c0 >> a.shift].x - lse);
@@ -538,7 +538,7 @@ struct LossLayout {
             w = pack.add(a, pw, v, d);
         }
         nblk = static_cast<int>(ceil_div(v, block));
-        const int64_t ld = up(v, 8);
+        const int64_t ld = up(v, 16);  // whole epilogue chunks
         // bytes of one token's logits: statistics, exponentials, gradients
         const int64_t row = 8 * nblk + (grad ? (f32 ? 10 : 2) * ld : 0);
         const int64_t limit = static_cast<int64_t>(std::min<uint64_t>(budget ? budget : kDefaultBudget, 1ull << 46));
@@ -550,7 +550,7 @@ struct LossLayout {
         stats = a.take<float2>(piece * nblk);
         target_logit = a.take<float>(piece);
         if (grad) {
-            dz = scratch(a, piece, v, f32 ? kF32Parts : 1);
+            dz = scratch(a, piece, v, f32 ? kF32Parts : 1, 16);
             e = f32 ? static_cast<void*>(a.take<float>(piece * ld)) : const_cast<void*>(dz.p);
             if (!f32 && pieces > 1) dw_sum = a.take<float>(v * up(d, 4));
         }

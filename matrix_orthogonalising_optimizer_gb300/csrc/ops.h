@@ -61,6 +61,7 @@ struct OpsProblem {
     // epilogue
     int32_t act;
     OpsMat out[4];  // STORE: D | GATE: h, act, u act', h again | DGATE: da, du | LOGITS: exponentials
+                    // (fp32, or 16-bit codes, rows padded to whole 16-column chunks)
     OpsMat in[2];   // STORE: in[0] = addend (fp32) | DGATE: u act', act
     float2* stats;            // LOGITS: [M][nblk] (max, sum of exp) of 128-column blocks
     int32_t nblk;

@@ -179,15 +179,9 @@ __device__ __forceinline__ void ld_staged(const T* base, int64_t ld, int r0, int
     __syncwarp();
 }
 
-__device__ __forceinline__ void st_bf16(__nv_bfloat16* base, int64_t ld, bool vec, int r0, int c0, int lane,
-                                        const float (&v)[CH], int M, int N, float* stg) {
-    if (!vec || c0 + CH > N) {
-        st_staged(base, ld, r0, c0, lane, v, M, N, stg);
-        return;
-    }
-    uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+// A whole chunk of 16-bit elements, two per word, in 16-byte-aligned rows.
+__device__ __forceinline__ void st_words(void* base, int64_t ld, int r0, int c0, int lane, const uint32_t (&w)[8],
+                                         int M) {
     const bool odd = lane & 1;
     uint32_t d0[4], d1[4];
 #pragma unroll
@@ -198,9 +192,21 @@ __device__ __forceinline__ void st_bf16(__nv_bfloat16* base, int64_t ld, bool ve
         d1[k] = odd ? keep : recv;  // row (lane | 1),  half `odd`
     }
     const int ra = r0 + (lane & ~1);
-    __nv_bfloat16* p = base + static_cast<int64_t>(ra) * ld + c0 + 8 * odd;
+    uint16_t* p = static_cast<uint16_t*>(base) + static_cast<int64_t>(ra) * ld + c0 + 8 * odd;
     if (ra < M) *reinterpret_cast<uint4*>(p) = make_uint4(d0[0], d0[1], d0[2], d0[3]);
     if (ra + 1 < M) *reinterpret_cast<uint4*>(p + ld) = make_uint4(d1[0], d1[1], d1[2], d1[3]);
+}
+
+__device__ __forceinline__ void st_bf16(__nv_bfloat16* base, int64_t ld, bool vec, int r0, int c0, int lane,
+                                        const float (&v)[CH], int M, int N, float* stg) {
+    if (!vec || c0 + CH > N) {
+        st_staged(base, ld, r0, c0, lane, v, M, N, stg);
+        return;
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    st_words(base, ld, r0, c0, lane, w, M);
 }
 
 __device__ __forceinline__ void st_f32(float* base, int64_t ld, bool vec, int r0, int c0, int lane,
@@ -490,6 +496,7 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
         RegSrc src{z};
 #pragma unroll 1
         for (int kc = 0; kc < 8; ++kc) {
+            if (cb + kc * CH >= P.N) break;
             float v[CH];
             src.load(kc, v);
 #pragma unroll
@@ -497,7 +504,16 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
                 v[j] = exp_of<kF32>(v[j], m, ms);
                 sum[j % 4] += v[j];
             }
-            st_mat(P.out[0], r0, cb + kc * CH, lane, v, P.M, P.N, stg);
+            // rows are padded to whole chunks, so every chunk is stored whole
+            if constexpr (kF32) {
+                st_f32(static_cast<float*>(P.out[0].p), P.out[0].ld, true, r0, cb + kc * CH, lane, v, P.M,
+                       static_cast<int>(P.out[0].ld), stg);
+            } else {
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = e16_encode(v[2 * k]) | e16_encode(v[2 * k + 1]) << 16;
+                st_words(P.out[0].p, P.out[0].ld, r0, cb + kc * CH, lane, w, P.M);
+            }
         }
     } else {
 #pragma unroll

@@ -130,7 +130,11 @@ __device__ __forceinline__ void finish(const OpsStream& P, float (&part)[kParts]
             for (int o = R / 2; o; o >>= 1) s += __shfl_xor_sync(tc::kFullMask, s, o);
             if (tok >= P.tokens || n >= P.N) continue;
             if (P.targets[tok] == n) P.target_logit[tok] = z;
-            if (P.out[0].p) st1(P.out[0], tok, n, e);
+            if (P.out[0].p) {
+                const int64_t at = tok * P.out[0].ld + n;
+                if constexpr (kF32) static_cast<float*>(P.out[0].p)[at] = e;
+                else static_cast<uint16_t*>(P.out[0].p)[at] = static_cast<uint16_t>(e16_encode(e));
+            }
             if (i % R == 0) P.stats[static_cast<int64_t>(tok) * P.nblk + tile] = make_float2(m, s);
         }
     }

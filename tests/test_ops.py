@@ -441,9 +441,11 @@ def check_loss(x, w, t, coef, out, ignore=-100):
     p = torch.softmax(z, 1)
     hot = torch.zeros_like(p).scatter_(1, idx, 1.0)
     dz = c * (p - hot)
-    # exponentials and dz are each rounded to bf16; the logits' errors shift p by twice as much
-    op = 2 * U[dt] if dt == torch.bfloat16 else 2.0 ** -22
-    dzb = (op + U[dt] ** 2 + FN) * dz.abs() + c * p * (2 * (ez + fl)[:, None])
+    # bf16: exponentials keep 12 bits, those below 2^-31 of their block's largest are dropped,
+    # and dz is rounded to bf16; the logits' errors shift p by twice as much
+    op = U[dt] + 2.0 ** -12 if dt == torch.bfloat16 else 2.0 ** -22
+    drop = 2.0 ** -31 if dt == torch.bfloat16 else 0.0
+    dzb = (op + U[dt] ** 2 + FN) * dz.abs() + c * (p * (2 * (ez + fl)[:, None]) + drop)
     edx, edw = dz @ W, dz.T @ X
     u = U[dt]
     within(dx, edx, u * edx.abs() + (1 + u) * (dzb @ W.abs() + acc(w.shape[0], dt) * (dz.abs() @ W.abs())), "dx")
