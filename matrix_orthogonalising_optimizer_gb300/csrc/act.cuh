@@ -45,7 +45,7 @@ __device__ __forceinline__ float act_slope(int act, float a, float gate) {
 // An exponential relative to its block's maximum, 0 <= e <= 1, in 16 bits: 5
 // exponent and 11 mantissa bits of the fp32 value (relative error 2^-12), zero
 // below 2^-31.  bf16 would round the probability once more, by 2^-8, before the
-// gradient's own rounding.  NaN keeps the largest code and decodes to NaN.
+// gradient's own rounding.  (A NaN reaches the gradient through lse.)
 constexpr uint32_t kE16Base = 96u << 11;  // exponent of 2^-31
 
 __device__ __forceinline__ uint32_t e16_encode(float e) {
@@ -54,7 +54,6 @@ __device__ __forceinline__ uint32_t e16_encode(float e) {
 }
 
 __device__ __forceinline__ float e16_decode(uint32_t c) {
-    if (c == 0xffffu) return __int_as_float(0x7fc00000);
     return c ? __uint_as_float((c + kE16Base) << 12) : 0.0f;
 }
 

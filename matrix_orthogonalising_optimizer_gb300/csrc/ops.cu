@@ -474,30 +474,38 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
     }
     if (!a.e) return;
     const float c = valid ? (a.coef ? a.coef[row] : 1.0f) : 0.0f;
+    const int tg = valid ? static_cast<int>(t >> 3) : -1, tk = static_cast<int>(t & 7);  // the target's group, place
     const int g0 = blockIdx.y * a.seg_groups, g1 = min(a.groups, g0 + a.seg_groups);
     for (int g = g0 + tid; g < g1; g += kRowThreads) {
-        const int64_t c0 = static_cast<int64_t>(g) * 8;
+        const int c0 = g * 8;
         const int64_t off = row * a.ld + c0;
         float v[8];
-        if (kF32) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.e) + off);
-            const float4 x = p[0], y = p[1];
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-            v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        if (!valid) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
         } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.e) + off);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const float scale = c * expf(st[c0 >> a.shift].x - lse);
+            if (kF32) {
+                const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.e) + off);
+                const float4 x = p[0], y = p[1];
+                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.e) + off);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[2 * k] = e16_decode(w[k] & 0xffffu);
-                v[2 * k + 1] = e16_decode(w[k] >> 16);
+                for (int k = 0; k < 4; ++k) {
+                    v[2 * k] = e16_decode(w[k] & 0xffffu);
+                    v[2 * k + 1] = e16_decode(w[k] >> 16);
+                }
             }
-        }
-        const float scale = c * expf(st[c0 >> a.shift].x - lse);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[k] = valid ? v[k] * scale : 0.0f;
-            if (valid && c0 + k == t) v[k] = c * expm1f(-nll);
+            for (int k = 0; k < 8; ++k) v[k] *= scale;
+            if (g == tg) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k == tk) v[k] = c * expm1f(-nll);
+            }
         }
         __nv_bfloat16* d = a.dz + off;
 #pragma unroll
