@@ -24,6 +24,11 @@
 // memory, each block writes one partial row, and a second kernel adds the
 // partial rows in a fixed order, so the result does not depend on scheduling.
 // Rows wider than a group holds take three plain passes (wide kernels).
+//
+// Measured at 16384 x 4096 in bf16: forward 49 us (268 MB at 5.5 TB/s, 82 % of the
+// copy rate; launch and first rows are about 5 us of it), backward 73 us with the
+// reduction (403 MB at 5.5 TB/s).  Before the rings and the packed arithmetic:
+// 52 and 122 us, 14 and 40 instructions per element.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -863,10 +868,10 @@ cudaError_t run_registers(const NormArgs& a, bool bwd, int max_grid, int* grid, 
 }
 
 // Forward ring: four vectors per thread, so a 4096-column bf16 row belongs to
-// four warps (one vector per thread and sixteen warps: 65 us instead of 47 for
-// 16384 x 4096, the two block-wide reductions bound it).  Backward: the column
-// sums take 16 registers per vector, so a thread holds one vector and more only
-// in rows wider than 16 warps.
+// four warps (one vector per thread and sixteen warps: 65 us instead of 50 for
+// 16384 x 4096, the two block-wide reductions bound it).  Backward: two vectors
+// per thread, whose column sums take 32 registers (one vector: 93 us instead of
+// 73), more only in rows wider than 16 warps.
 template <typename T>
 cudaError_t run_shape(int64_t vecs, const NormArgs& a, bool bwd, bool ring, int max_grid, int* grid, cudaStream_t s) {
     if (ring && !bwd) {

@@ -260,9 +260,14 @@ int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a
     return DMUON_OK;
 }
 
+OpsShape shape_of(int64_t M, int64_t N, int64_t K, int sources, bool f32, bool dual = false) {
+    return OpsShape{M, N, static_cast<int32_t>(ceil_div(K, 64) * sources * (f32 ? 6 : 1)), dual ? 1 : 0, 256};
+}
+
 // Columns per tile of a launch's only product.
-int tile_columns(int64_t M, int64_t N, int64_t K, bool dual, bool f32, int pairs) {
-    return ops_tile_columns(M, N, ceil_div(K, 64) * (f32 ? 6 : 1), dual, pairs);
+int tile_columns(OpsShape s, int pairs) {
+    ops_tile_columns(&s, 1, pairs);
+    return s.bn;
 }
 
 bool is_long(const OpsLaunch& l) {
@@ -653,7 +658,7 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
     OpsProblem& P = l[0].p[0];
     const Operand b[2] = {L.wg, L.wu};
     OPS_TRY(set_problem(P, tokens, hidden, dim, &L.x, false, b, false, 2, true,
-                        tile_columns(tokens, hidden, dim, true, f32, pairs)));
+                        tile_columns(shape_of(tokens, hidden, dim, 1, f32, true), pairs)));
     P.act = activation == DMUON_ACT_GELU ? OPS_GELU : OPS_SILU;
     P.out[0] = out_of(L.h);
     if (saved_act) {
@@ -662,7 +667,7 @@ extern "C" int dmuon_gated_ffn_forward(const void* x, const void* w_gate, const 
         if (L.h.p != saved_h) P.out[3] = user_mat(saved_h, hidden, f32);
     }
     OPS_TRY(set_problem(l[1].p[0], tokens, dim, hidden, &L.h, false, &L.wd, false, 1, false,
-                        tile_columns(tokens, dim, hidden, false, f32, pairs)));
+                        tile_columns(shape_of(tokens, dim, hidden, 1, f32), pairs)));
     l[1].p[0].out[0] = user_mat(y, dim, f32);
     OPS_TRY(schedule(l, 2, L.common, f32, false, pairs, s, where));
     OPS_CUDA(L.pack.run(s));
@@ -710,7 +715,7 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     l[0].n = 1;
     OpsProblem& P = l[0].p[0];
     OPS_TRY(set_problem(P, tokens, hidden, dim, &L.dy, false, &L.wd, true, 1, false,
-                        tile_columns(tokens, hidden, dim, false, f32, pairs)));
+                        tile_columns(shape_of(tokens, hidden, dim, 1, f32), pairs)));
     P.in[0] = user_mat(saved_slope, hidden, saved_dtype == DMUON_FP32);
     P.in[1] = user_mat(saved_act, hidden, saved_dtype == DMUON_FP32);
     P.out[0] = out_of(L.da);
@@ -719,19 +724,21 @@ extern "C" int dmuon_gated_ffn_backward(const void* dy, const void* x, const voi
     l[1].n = 4;
     OpsProblem* p = l[1].p;
     const bool dx_first = 2 * hidden >= tokens;
-    // 128-column tiles while all products' tiles fit the pairs at once
-    const auto tiles = [](int64_t m, int64_t n, int bn) { return ceil_div(m, 256) * ceil_div(n, bn); };
-    const int bn = tiles(tokens, dim, 128) + 2 * tiles(hidden, dim, 128) + tiles(dim, hidden, 128) <= pairs ? 128 : 256;
     int k = dx_first ? 1 : 0;
-    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.da, true, &L.x, true, 1, false, bn));
+    OpsShape sh[4];
+    sh[k] = sh[k + 1] = shape_of(hidden, dim, tokens, 1, f32);
+    sh[k + 2] = shape_of(dim, hidden, tokens, 1, f32);
+    sh[dx_first ? 0 : 3] = shape_of(tokens, dim, hidden, 2, f32);
+    ops_tile_columns(sh, 4, pairs);
+    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.da, true, &L.x, true, 1, false, sh[k].bn));
     p[k++].out[0] = user_mat(dw_gate, dim, f32);
-    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.du, true, &L.x, true, 1, false, bn));
+    OPS_TRY(set_problem(p[k], hidden, dim, tokens, &L.du, true, &L.x, true, 1, false, sh[k].bn));
     p[k++].out[0] = user_mat(dw_up, dim, f32);
-    OPS_TRY(set_problem(p[k], dim, hidden, tokens, &L.dy, true, &L.h, true, 1, false, bn));
+    OPS_TRY(set_problem(p[k], dim, hidden, tokens, &L.dy, true, &L.h, true, 1, false, sh[k].bn));
     p[k++].out[0] = user_mat(dw_down, hidden, f32);
     k = dx_first ? 0 : 3;
     const Operand a[2] = {L.da, L.du}, b[2] = {L.wg, L.wu};
-    OPS_TRY(set_problem(p[k], tokens, dim, hidden, a, false, b, true, 2, false, bn));
+    OPS_TRY(set_problem(p[k], tokens, dim, hidden, a, false, b, true, 2, false, sh[k].bn));
     p[k].out[0] = user_mat(dx, dim, f32);
     OPS_TRY(schedule(l, 2, L.common, f32, false, pairs, s, where));
     OPS_CUDA(L.pack.run(s));
@@ -798,12 +805,14 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         if (grad) {
             l[1].n = 2;
             const int kx = vocab >= n ? 0 : 1;
-            const int bn = ceil_div(n, 256) * ceil_div(dim, 128) + ceil_div(vocab, 256) * ceil_div(dim, 128) <= pairs
-                               ? 128 : 256;
-            OPS_TRY(set_problem(l[1].p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false, bn));
+            OpsShape sh[2];
+            sh[kx] = shape_of(n, dim, vocab, 1, f32);
+            sh[1 - kx] = shape_of(vocab, dim, n, 1, f32);
+            ops_tile_columns(sh, 2, pairs);
+            OPS_TRY(set_problem(l[1].p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false, sh[kx].bn));
             l[1].p[kx].out[0] = user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
             OpsProblem& W = l[1].p[1 - kx];
-            OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false, bn));
+            OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false, sh[1 - kx].bn));
             // the sum over pieces stays in fp32: rounded once, with the last piece
             const OpsMat sum = L.dw_sum ? user_mat(L.dw_sum, up(dim, 4), true) : user_mat(dweight, dim, f32);
             const bool last = i + 1 == L.pieces;

@@ -102,8 +102,14 @@ cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, bool f32, cudaSt
 constexpr int64_t kOpsSlotFloats = 256 * 256;  // one partial accumulator of a pair tile
 constexpr int kOpsTailCounts = 16;             // counters per split tile
 
-// Columns per pair tile for a launch's only product.  Host only.
-int ops_tile_columns(int64_t M, int64_t N, int64_t total_slabs, bool dual, int pairs);
+// What the schedule of a launch depends on, of one product: its K in slabs over
+// all segments, and the columns per tile.
+struct OpsShape {
+    int64_t M, N;
+    int32_t total, dual, bn;
+};
+// Chooses the columns per tile of a launch's products.  Host only.
+void ops_tile_columns(OpsShape* p, int n, int pairs);
 // Splits the launch's problems into work units (see OpsProblem) for `pairs`
 // resident CTA pairs; `slots` partial-sum slots are available.  Host only.
 void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails);

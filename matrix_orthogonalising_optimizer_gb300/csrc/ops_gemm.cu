@@ -17,7 +17,10 @@
 // 128 r .. of B in its own shared memory) takes 32 KB of operands per CTA and
 // 64-deep K slab from L2 for 8.4 MFLOP, and six such stages are in flight.
 // Two 256-column TMEM accumulators let the eight epilogue warps work on one
-// tile while the next one's MMAs run.
+// tile while the next one's MMAs run.  Measured at 8192 x 4096 x 14336 and 4096 x
+// 4096 x 131072: tensor pipe 92 to 99 % active (DGATE 77 %: 1.4 GB of stored
+// activations and gradients beside the operands), the whole training step
+// 5.1 to 5.4 ms = 1.61 to 1.71 PFLOP/s, where the power cap sets the clock.
 //
 // Schedule: units are taken in order from a counter (neighbouring tiles stay
 // together in L2).  Tiles that would leave most pairs idle at the end of a
@@ -950,10 +953,11 @@ cudaError_t ops_pairs(int* pairs) {
 }
 
 // Work units.  Whole tiles are split into S ranges of K where that shortens the
-// launch.  The estimate, in slabs (about 0.35 us each), is measured on tiles of a
-// few hundred tokens: a unit costs its slabs and kUnitCost; a unit of a split
-// tile kStoreCost more (its partial sum's way to L2 and the arrival), and the
-// tile's last unit kPartCost for each part it adds up.
+// launch.  The estimate, in 64-deep slabs of a 256 x 256 tile (about 0.3 us each), is
+// measured on tiles of a few hundred tokens: a unit costs its slabs (0.65 of them
+// with 128-column tiles) and kUnitCost, the epilogue kEpiCost per 256 columns; a
+// unit of a split tile kStoreCost more (its partial sum's way to L2 and the
+// arrival), and the tile's last unit kPartCost for each part it adds up.
 //  - One product: T equal tiles on P pairs leave P - T mod P pairs idle in the
 //    last round, so the tiles of that round are the ones split.
 //  - Several products: the estimate is the larger of the work per pair and the
@@ -961,100 +965,125 @@ cudaError_t ops_pairs(int* pairs) {
 //    unit is split further while that lowers it.
 namespace {
 
-constexpr double kUnitCost = 4.0, kStoreCost = 14.0, kPartCost = 12.0;
+constexpr double kUnitCost = 4.0, kEpiCost = 8.0, kStoreCost = 14.0, kPartCost = 12.0;
 constexpr int kMinSlabs = 8, kMaxSplit = 32;
 
-// The longest chain of a tile of `total` slabs in s ranges, and its work.
-double unit_cost(int total, int s) {
-    return static_cast<double>(total) / s + kUnitCost + (s > 1 ? kStoreCost + kPartCost * s : 0.0);
-}
-double tile_work(int total, int s) {
-    return total + s * kUnitCost + (s > 1 ? s * kStoreCost + kPartCost * s : 0.0);
-}
+double slab_cost(int bn) { return bn == 256 ? 1.0 : 0.65; }
 
-}  // namespace
-
-// A 128-column tile halves a unit's epilogue and takes 0.65 of its slab time, so it
-// wins where the 256-column tiles would leave pairs idle: rounds of units times
-// the cost of one (epilogue and start about 12 and 8 slabs).
-int ops_tile_columns(int64_t M, int64_t N, int64_t total_slabs, bool dual, int pairs) {
-    const auto cost = [&](int bn, double slab, double fixed) {
-        const int64_t tiles = (M + 255) / 256 * ((N + (dual ? bn / 2 : bn) - 1) / (dual ? bn / 2 : bn));
-        return static_cast<double>((tiles + pairs - 1) / pairs) * (slab * total_slabs + fixed);
-    };
-    return cost(128, 0.65, 8.0) < cost(256, 1.0, 12.0) ? 128 : 256;
+// The longest chain of a tile in s ranges of K, and its work.
+double unit_cost(const OpsShape& p, int s) {
+    return slab_cost(p.bn) * p.total / s + kUnitCost + kEpiCost * p.bn / 256 + (s > 1 ? kStoreCost + kPartCost * s : 0.0);
+}
+double tile_work(const OpsShape& p, int s) {
+    return slab_cost(p.bn) * p.total + s * kUnitCost + kEpiCost * p.bn / 256 +
+           (s > 1 ? s * kStoreCost + kPartCost * s : 0.0);
 }
 
-void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
-    int split[kOpsMaxProblems], rem[kOpsMaxProblems];
-    for (int i = 0; i < l.n; ++i) {
+int64_t tiles_of(const OpsShape& p) {
+    const int n = p.dual ? p.bn / 2 : p.bn;
+    return (p.M + 255) / 256 * ((p.N + n - 1) / n);
+}
+
+// Ranges per split tile of each product and the tiles to split; the launch's estimate.
+double plan_splits(const OpsShape* p, int n, int pairs, int* split, int64_t* rem) {
+    for (int i = 0; i < n; ++i) {
         split[i] = 1;
-        rem[i] = l.p[i].tiles_m * l.p[i].tiles_n;
+        rem[i] = tiles_of(p[i]);
     }
-    if (l.n == 1) {
-        const int total = l.p[0].slabs * l.p[0].nseg;
+    if (n == 1) {
+        const int64_t tiles = rem[0];
         rem[0] %= pairs;
-        double best = total + kUnitCost;
-        for (int s = 2; s <= kMaxSplit && rem[0] > 0 && total / s >= kMinSlabs; ++s) {
-            const int64_t rounds = (static_cast<int64_t>(rem[0]) * s + pairs - 1) / pairs;
-            const double c = (rounds - 1) * (static_cast<double>(total) / s + kUnitCost + kStoreCost) +
-                             unit_cost(total, s);
+        double best = unit_cost(p[0], 1);
+        for (int s = 2; s <= kMaxSplit && rem[0] > 0 && p[0].total / s >= kMinSlabs; ++s) {
+            const int64_t rounds = (rem[0] * s + pairs - 1) / pairs;
+            const double c = (rounds - 1) * (slab_cost(p[0].bn) * p[0].total / s + kUnitCost + kStoreCost) +
+                             unit_cost(p[0], s);
             if (c < best) {
                 best = c;
                 split[0] = s;
             }
         }
-    } else {
-        const auto estimate = [&](int* longest) {
-            double work = 0.0, most = 0.0;
-            for (int i = 0; i < l.n; ++i) {
-                const int total = l.p[i].slabs * l.p[i].nseg;
-                work += tile_work(total, split[i]) * l.p[i].tiles_m * l.p[i].tiles_n;
-                const double c = unit_cost(total, split[i]);
-                if (c > most) {
-                    most = c;
-                    *longest = i;
-                }
+        return static_cast<double>(tiles / pairs) * unit_cost(p[0], 1) + (rem[0] ? best : 0.0);
+    }
+    const auto estimate = [&](int* longest) {
+        double work = 0.0, most = 0.0;
+        for (int i = 0; i < n; ++i) {
+            work += tile_work(p[i], split[i]) * static_cast<double>(tiles_of(p[i]));
+            const double c = unit_cost(p[i], split[i]);
+            if (c > most) {
+                most = c;
+                *longest = i;
             }
-            return work / pairs > most ? work / pairs : most;
-        };
-        int longest = 0;
-        double best = estimate(&longest);
-        for (;;) {
-            const int k = longest, total = l.p[k].slabs * l.p[k].nseg, was = split[k];
-            int s = was + 1, unused = 0;
-            double c = best;
-            for (; s <= kMaxSplit && total / s >= kMinSlabs; ++s) {
-                split[k] = s;
-                c = estimate(&unused);
-                if (c < best) break;
-            }
-            if (!(c < best)) {
-                split[k] = was;
-                break;
-            }
-            best = c;
-            longest = unused;
+        }
+        return work / pairs > most ? work / pairs : most;
+    };
+    int longest = 0;
+    double best = estimate(&longest);
+    for (;;) {
+        const int k = longest, was = split[k];
+        int s = was + 1, now = 0;
+        double c = best;
+        for (; s <= kMaxSplit && p[k].total / s >= kMinSlabs; ++s) {
+            split[k] = s;
+            c = estimate(&now);
+            if (c < best) break;
+        }
+        if (!(c < best)) {
+            split[k] = was;
+            return best;
+        }
+        best = c;
+        longest = now;
+    }
+}
+
+}  // namespace
+
+// Each product's columns per tile: every combination of 128 and 256 is estimated
+// (at most 16).
+void ops_tile_columns(OpsShape* p, int n, int pairs) {
+    int split[kOpsMaxProblems], choice = 0;
+    int64_t rem[kOpsMaxProblems];
+    double best = 0.0;
+    for (int c = 0; c < 1 << n; ++c) {
+        for (int i = 0; i < n; ++i) p[i].bn = c >> i & 1 ? 128 : 256;
+        const double e = plan_splits(p, n, pairs, split, rem);
+        if (c == 0 || e < best) {
+            best = e;
+            choice = c;
         }
     }
+    for (int i = 0; i < n; ++i) p[i].bn = choice >> i & 1 ? 128 : 256;
+}
+
+void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
+    OpsShape shape[kOpsMaxProblems];
+    int split[kOpsMaxProblems];
+    int64_t rem[kOpsMaxProblems];
+    for (int i = 0; i < l.n; ++i) {
+        const OpsProblem& p = l.p[i];
+        shape[i] = OpsShape{p.M, p.N, p.slabs * p.nseg, p.dual, p.bn};
+    }
+    if (l.n > 0) plan_splits(shape, l.n, pairs, split, rem);
     int unit = 0, tail = 0, slot = 0;
     for (int i = 0; i < l.n; ++i) {
         OpsProblem& p = l.p[i];
         const int tiles = p.tiles_m * p.tiles_n;
-        int r = rem[i], s = split[i];
-        while (s > 1 && static_cast<int64_t>(r) * s > slots - slot) --s;
+        int64_t r = rem[i];
+        int s = split[i];
+        while (s > 1 && r * s > slots - slot) --s;
         if (s <= 1 || r > tails - tail) {
             r = 0;
             s = 1;
         }
-        p.whole = tiles - r;
+        p.whole = tiles - static_cast<int>(r);
         p.split = s;
         p.unit_begin = unit;
         p.tail_begin = tail;
         p.slot_begin = slot;
-        unit += p.whole + r * s;
-        tail += r;
-        slot += r * s;
+        unit += p.whole + static_cast<int>(r) * s;
+        tail += static_cast<int>(r);
+        slot += static_cast<int>(r) * s;
     }
     l.total_units = unit;
 }

@@ -15,8 +15,9 @@
 // k of its row, of which elements (0,1), (2,3) serve one MMA and (4,5), (6,7)
 // the next as the fragment's two column pairs.  The sum over k does not depend
 // on which k sits in which slot as long as weights and x agree, and both are
-// loaded alike.  The tcgen05 kernel needs the weights in shared memory and 256
-// rows of x per tile: at one row it read them at 2.4 TB/s.
+// loaded alike.  The tcgen05 kernel needs the weights in shared memory and waits
+// for whole tiles: at one row of 4096 x 14336 it took 125 us, this one 56 (352 MB
+// at 6.3 TB/s, 94 % of the copy rate).
 #include <cuda_bf16.h>
 
 #include "act.cuh"
