@@ -36,12 +36,8 @@
 #include <string>
 
 #include "dmuon.h"
-#include "internal.h"
+#include "ops.h"
 #include "tc.cuh"
-
-namespace dmuon {
-void set_last_error(const std::string& msg);
-}
 
 namespace {
 
@@ -322,6 +318,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const __grid_cons
             st_vec(static_cast<T*>(a.out) + row * a.cols, (k * TPR + tr) * V, a.cols, al, x);
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!a.partial) return;
     float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
     if constexpr (G > 1) {
@@ -622,6 +619,7 @@ __global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(
             phase ^= 1;
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!a.partial) return;
     float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
     if constexpr (G > 1) {
@@ -670,6 +668,7 @@ __global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial, int n, int cols, T* dw, T* db) {
     __shared__ float red[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // column of the 2 x cols pair
     float s = 0.0f;
@@ -1069,11 +1068,12 @@ extern "C" int dmuon_layer_norm_backward(const void* dy, const void* x, const vo
     }
     if (!sums) return DMUON_OK;
     const int grid = static_cast<int>((2 * cols + 31) / 32);
-    if (bf)
-        norm_reduce_kernel<<<grid, 1024, 0, s>>>(a.partial, partials, a.cols, static_cast<__nv_bfloat16*>(dweight),
-                                                 static_cast<__nv_bfloat16*>(dbias));
-    else
-        norm_reduce_kernel<<<grid, 1024, 0, s>>>(a.partial, partials, a.cols, static_cast<float*>(dweight),
-                                                 static_cast<float*>(dbias));
-    return cuda_result(cudaGetLastError(), where);
+    const dim3 blocks(static_cast<unsigned>(grid));
+    const cudaError_t e = bf ? dmuon::launch_dependent(norm_reduce_kernel<__nv_bfloat16>, blocks, 1024, s, a.partial,
+                                                       partials, a.cols, static_cast<__nv_bfloat16*>(dweight),
+                                                       static_cast<__nv_bfloat16*>(dbias))
+                             : dmuon::launch_dependent(norm_reduce_kernel<float>, blocks, 1024, s, a.partial, partials,
+                                                       a.cols, static_cast<float*>(dweight),
+                                                       static_cast<float*>(dbias));
+    return cuda_result(e, where);
 }

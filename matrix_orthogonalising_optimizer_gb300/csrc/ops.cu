@@ -122,6 +122,7 @@ struct PackArgs {
 // parts, x = hi + mid + lo, or bf16 values copied.  Memory-bound; only fp32
 // operands and row strides that are not a multiple of 16 bytes come here.
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; g < a.groups;
          g += static_cast<int64_t>(gridDim.x) * 256) {
         int k = 0;
@@ -175,8 +176,7 @@ struct Packer {
     cudaError_t run(cudaStream_t s) const {
         if (args.groups == 0) return cudaSuccess;
         const int64_t blocks = std::min<int64_t>(ceil_div(args.groups, 256), 4096);
-        pack_kernel<<<static_cast<int>(blocks), 256, 0, s>>>(args);
-        return cudaGetLastError();
+        return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(blocks)), 256, s, args);
     }
 };
 
@@ -443,6 +443,7 @@ constexpr int kRowThreads = 256;
 template <bool kF32>
 __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_constant__ LossRowArgs a) {
     __shared__ float red[kRowThreads / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float2* st = a.stats + row * a.nblk;
@@ -855,9 +856,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             a.seg_groups = static_cast<int32_t>(ceil_div(a.groups, segs));
         }
         const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(segs));
-        if (f32) loss_row_kernel<true><<<grid, kRowThreads, 0, s>>>(a);
-        else loss_row_kernel<false><<<grid, kRowThreads, 0, s>>>(a);
-        OPS_CUDA(cudaGetLastError());
+        OPS_CUDA(launch_dependent(f32 ? loss_row_kernel<true> : loss_row_kernel<false>, grid, kRowThreads, s, a));
         if (grad) OPS_CUDA(launch(l[1], OPS_STORE, f32, s));
     }
     return DMUON_OK;

@@ -16,6 +16,23 @@ namespace dmuon {
 
 void set_last_error(const std::string& msg);
 
+// Launch of a kernel that begins with griddepcontrol.wait: it may be placed while
+// the stream's previous kernel finishes (programmatic dependent launch), which
+// takes 1 to 2 us off a chain of short kernels.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 constexpr int kOpsMaxProblems = 4;
 constexpr int kOpsMaxSegs = 12;
 
