@@ -536,6 +536,61 @@ def test_vocab_loss_repeats_bitwise():
         assert all(torch.equal(a, b) for a, b in zip(out, first))
 
 
+# ---------------------------------------------------------------- offsets past 2^31, alignment
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    # the last rows of tensors of more than 2^31 elements equal the same rows alone,
+    # within the roundings of two different kernels
+    free = torch.cuda.mem_get_info()[0]
+    if free < 60 << 30:
+        pytest.skip("needs 60 GB of free device memory")
+    g = gen(6)
+    rows, cols = 140000, 16384
+    x = torch.empty(rows, cols, device="cuda", dtype=torch.bfloat16)
+    x[-4:] = randn(g, 4, cols)
+    x[:-4] = 1.0
+    dy = torch.zeros_like(x)
+    dy[-4:] = randn(g, 4, cols)
+    y, mean, rstd = pkg.layer_norm(x)
+    dx, dw, db = pkg.layer_norm_backward(dy, x, None, mean, rstd)
+    ys, ms, rs = pkg.layer_norm(x[-4:].clone())
+    dxs, dws, dbs = pkg.layer_norm_backward(dy[-4:].clone(), x[-4:].clone(), None, ms, rs)
+    assert torch.allclose(y[-4:].float(), ys.float(), rtol=2.0 ** -7, atol=2.0 ** -8)
+    assert torch.allclose(dx[-4:].float(), dxs.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+    assert torch.allclose(dw.float(), dws.float(), rtol=2.0 ** -7, atol=2.0 ** -6) and not y[:-4].any()
+    del x, dy, y, dx
+    n, d, f = 160000, 64, 14336
+    x = torch.zeros(n, d, device="cuda", dtype=torch.bfloat16)
+    dy = torch.zeros_like(x)
+    x[-40:], dy[-40:] = randn(g, 40, d), randn(g, 40, d)
+    wg, wu, wd = randn(g, f, d, std=0.1), randn(g, f, d, std=0.1), randn(g, d, f, std=0.01)
+    y, saved, h = pkg.gated_ffn(x, wg, wu, wd, save="compact")
+    out = pkg.gated_ffn_backward(dy, x, wg, wu, wd, saved, h)
+    xs, dys = x[-40:].clone(), dy[-40:].clone()
+    ysm, saveds, hs = pkg.gated_ffn(xs, wg, wu, wd, save="compact")
+    outs = pkg.gated_ffn_backward(dys, xs, wg, wu, wd, saveds, hs)
+    for a, b in ((y[-40:], ysm), (h[-40:], hs), (saved[1][-40:], saveds[1]), (out[0][-40:], outs[0]), *zip(out[1:], outs[1:])):
+        # two roundings of operands and one of the result, in norm
+        assert float((a.double() - b.double()).norm()) <= 3 * 2.0 ** -8 * float(b.double().norm())
+    assert not y[:-40].any() and not out[0][:-40].any()
+
+
+@pytest.mark.gpu
+def test_misaligned_views_are_refused():
+    buf = torch.zeros(4 * 16 + 1, dtype=torch.bfloat16, device="cuda")
+    x = buf[1:].view(4, 16)  # contiguous, but two bytes past a 16-byte boundary
+    w = torch.zeros(32, 16, dtype=torch.bfloat16, device="cuda")
+    d = torch.zeros(16, 32, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: pkg.layer_norm(x), lambda: pkg.gated_ffn(x, w, w, d),
+                 lambda: pkg.vocab_loss(x, w, torch.zeros(4, dtype=torch.int64, device="cuda"))):
+        with pytest.raises(_lib.DmuonError) as e:
+            call()
+        assert e.value.status == _lib.ERR_ALIGN
+    with pytest.raises(ValueError, match="contiguous"):
+        pkg.gated_ffn(torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda")[:, :16], w, w, d)
+
+
 # ---------------------------------------------------------------- differences, streams, graphs
 
 @pytest.mark.gpu
