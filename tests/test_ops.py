@@ -298,7 +298,7 @@ FFN_SHAPES = [(1, 64, 128), (1, 1, 1), (2, 72, 200), (17, 128, 96), (129, 64, 25
               (512, 256, 768), (31, 2048, 512), (5, 64, 5000), (1000, 520, 264), (64, 4096, 64),
               (8, 2056, 104), (16, 40, 1032), (23, 1032, 2000), (32, 8, 8), (9, 520, 7),
               (1500, 64, 1280), (4000, 72, 640), (300, 1300, 1400),
-              (7, 1028, 260), (12, 132, 2052), (26, 300, 100)]
+              (7, 1028, 260), (12, 132, 2052), (26, 300, 100), (40, 16384, 72)]
 
 
 @pytest.mark.gpu
@@ -352,10 +352,11 @@ def test_gated_ffn(n, d, f, dtype):
 
 
 @pytest.mark.gpu
-def test_gated_ffn_repeats_bitwise_and_leading_dimensions():
-    # shapes whose launches split tiles along K: the sums' order is fixed
-    x, wg, wu, wd, dy = ffn_inputs(96, 1024, 1536, torch.bfloat16, 5)
-    ws = torch.empty(pkg.gated_ffn_workspace(96, 1024, 1536, backward=True), dtype=torch.uint8, device="cuda")
+@pytest.mark.parametrize("n,d,f", [(96, 1024, 1536), (48, 16384, 200), (20, 512, 8192)])
+def test_gated_ffn_repeats_bitwise(n, d, f):
+    # K deep enough that launches split tiles along it: the sums' order is fixed
+    x, wg, wu, wd, dy = ffn_inputs(n, d, f, torch.bfloat16, 5)
+    ws = torch.empty(pkg.gated_ffn_workspace(n, d, f, backward=True), dtype=torch.uint8, device="cuda")
     first = None
     for _ in range(5):
         ws.random_(0, 255)  # nothing is kept between calls
@@ -364,8 +365,14 @@ def test_gated_ffn_repeats_bitwise_and_leading_dimensions():
         if first is None:
             first = [t.clone() for t in out]
         assert all(torch.equal(a, b) for a, b in zip(out, first))
-    y3, saved3, h3 = pkg.gated_ffn(x.view(4, 24, 1024), wg, wu, wd, save=True)
-    assert y3.shape == (4, 24, 1024) and h3.shape == (4, 24, 1536) and torch.equal(y3.view(96, 1024), first[0])
+
+
+@pytest.mark.gpu
+def test_gated_ffn_leading_dimensions():
+    x, wg, wu, wd, dy = ffn_inputs(96, 1024, 1536, torch.bfloat16, 5)
+    y, _, _ = pkg.gated_ffn(x, wg, wu, wd, save=True)
+    y3, _, h3 = pkg.gated_ffn(x.view(4, 24, 1024), wg, wu, wd, save=True)
+    assert y3.shape == (4, 24, 1024) and h3.shape == (4, 24, 1536) and torch.equal(y3.view(96, 1024), y)
 
 
 @pytest.mark.gpu
@@ -454,7 +461,7 @@ def check_loss(x, w, t, coef, out, ignore=-100):
 
 LOSS_SHAPES = [(1, 64, 1), (1, 64, 1000), (3, 1, 5), (2, 8, 129), (17, 100, 255), (130, 64, 1003), (257, 136, 640),
                (300, 512, 10007), (5, 2048, 700), (600, 72, 128), (8, 40, 33), (16, 1032, 4099), (32, 264, 1000),
-               (9, 2052, 70), (27, 36, 3001)]
+               (9, 2052, 70), (27, 36, 3001), (40, 16384, 300)]
 
 
 @pytest.mark.gpu
@@ -524,9 +531,10 @@ def test_vocab_loss_large_logits():
 
 
 @pytest.mark.gpu
-def test_vocab_loss_repeats_bitwise():
-    x, w, t, coef = loss_inputs(70, 1024, 2049, torch.bfloat16, 21)
-    ws = torch.empty(pkg.vocab_loss_workspace(70, 1024, 2049, grad=True), dtype=torch.uint8, device="cuda")
+@pytest.mark.parametrize("n,d,v", [(70, 1024, 2049), (70, 16384, 1000), (12, 256, 4000)])
+def test_vocab_loss_repeats_bitwise(n, d, v):
+    x, w, t, coef = loss_inputs(n, d, v, torch.bfloat16, 21)
+    ws = torch.empty(pkg.vocab_loss_workspace(n, d, v, grad=True), dtype=torch.uint8, device="cuda")
     first = None
     for _ in range(4):
         ws.random_(0, 255)
