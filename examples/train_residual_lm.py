@@ -71,7 +71,8 @@ class Model:
             dx = dx + dres
             dnorms.insert(0, (dw, db))
             dmatrices = dblock + dmatrices
-        dembed = torch.zeros_like(self.embed, dtype=torch.float32).index_add_(0, tokens, dx.float()).to(self.embed.dtype)
+        dembed = torch.zeros_like(self.embed, dtype=torch.float32).index_add_(0, tokens, dx.float())
+        dembed = dembed.to(self.embed.dtype)
         self.steps += 1
         self.muon.step(self.matrices, dmatrices, self.momenta, lr=lr_muon, beta=0.95, wd=0.0)
         dm.adamw_step(self.others, [dembed, dhead, *(t for pair in dnorms for t in pair)], self.avg, self.sq,

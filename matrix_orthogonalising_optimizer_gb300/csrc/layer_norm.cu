@@ -12,10 +12,10 @@
 // finished mean -- no difference of large sums.  All arithmetic is fp32, one
 // rounding per stored value.
 //
-// Many aligned rows (ring kernels): persistent groups; bulk asynchronous copies
+// Aligned rows, unless they are few and short (ring kernels): persistent groups; bulk asynchronous copies
 // bring each group's next rows into a shared-memory ring while it works on the
 // current one, so the loads in flight do not cost registers, and the arithmetic
-// runs on packed pairs (fma.rn.f32x2).  Fewer rows, or rows that do not start on
+// runs on packed pairs (fma.rn.f32x2).  Few rows, or rows that do not start on
 // 16 bytes (register kernels): a row is spread over as many threads as hold it
 // and the next row is loaded into registers ahead.
 //
@@ -441,7 +441,8 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ Ring make_ring(uint8_t* smem, uint32_t bytes, int arrays, int stages, int groups, int g, int tr) {
+__device__ __forceinline__ Ring make_ring(uint8_t* smem, uint32_t bytes, int arrays, int stages, int groups, int g,
+                                          int tr) {
     // barriers first, then the groups' rows
     Ring r;
     r.full = reinterpret_cast<uint64_t*>(smem) + g * kMaxStages;
@@ -461,7 +462,9 @@ __host__ __device__ constexpr int ring_bwd_threads(int wpr) { return wpr > 8 ? w
 __host__ __device__ constexpr int ring_groups(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }
 
 template <typename T, int VPT, int WPR>
-__global__ void __launch_bounds__(ring_groups(WPR) * WPR * 32, 512 / (ring_groups(WPR) * WPR * 32)) norm_fwd_ring_kernel(const __grid_constant__ NormArgs a) {
+__global__ void
+__launch_bounds__(ring_groups(WPR) * WPR * 32, 512 / (ring_groups(WPR) * WPR * 32)) norm_fwd_ring_kernel(
+    const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>, TPR = WPR * 32, G = ring_groups(WPR);
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ GroupRed<WPR, 1> red[G][2];
@@ -500,7 +503,8 @@ __global__ void __launch_bounds__(ring_groups(WPR) * WPR * 32, 512 / (ring_group
         group_sum<WPR>(s, red[g][0], 1 + g);
         // the whole group has its part of the row in registers (WPR = 1: the
         // warp's shuffles ordered its reads): refill the stage
-        if (tr == 0 && row + a.stages * stride < a.rows) ring.issue(stage, x0 + (row + a.stages * stride) * a.cols, nullptr);
+        if (tr == 0 && row + a.stages * stride < a.rows)
+            ring.issue(stage, x0 + (row + a.stages * stride) * a.cols, nullptr);
         const float mean = s[0] * inv;
         s2 = both(0.0f);
 #pragma unroll
@@ -539,7 +543,8 @@ __global__ void __launch_bounds__(ring_groups(WPR) * WPR * 32, 512 / (ring_group
 }
 
 template <typename T, int VPT, int WPR>
-__global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(WPR)) norm_bwd_ring_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(WPR)) norm_bwd_ring_kernel(
+    const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>, TPR = WPR * 32, G = ring_bwd_threads(WPR) / TPR;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ GroupRed<WPR, 2> red[G][2];
@@ -553,17 +558,41 @@ __global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(
             const int64_t r = first + s * stride;
             if (r < a.rows) ring.issue(s, x0 + r * a.cols, d0 + r * a.cols);
         }
-    float2 w[VPT][V / 2], dw[VPT][V / 2], db[VPT][V / 2];
+    // kAgain: four vectors' column sums leave no registers for n and g, which are
+    // computed once more from the row in shared memory for dx; the row's stage is
+    // then refilled one row later
+    constexpr bool kAgain = VPT == 4;
+    constexpr int kKeep = kAgain ? 1 : VPT;
+    uint4 w[VPT];
+    float2 dw[VPT][V / 2], db[VPT][V / 2];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        unpack2<T>(a.w ? ld_raw(static_cast<const T*>(a.w), (k * TPR + tr) * V, a.cols, true) : make_uint4(0, 0, 0, 0),
-                   w[k]);
+        w[k] = a.w ? ld_raw(static_cast<const T*>(a.w), (k * TPR + tr) * V, a.cols, true) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) dw[k][j] = db[k][j] = both(0.0f);
+    }
+    // n, g (and dy, for the sums) of vector k of the row in the given stage
+    const auto vec = [&](int stage, int k, float mean, float rstd, float2 (&n)[V / 2], float2 (&gr)[V / 2],
+                         float2 (&d)[V / 2]) {
+        const int c = (k * TPR + tr) * V;
+        uint4 qx = make_uint4(0, 0, 0, 0), qd = qx;
+        if (c < a.cols) {
+            qx = *reinterpret_cast<const uint4*>(ring.at(stage, 0) + c * sizeof(T));
+            qd = *reinterpret_cast<const uint4*>(ring.at(stage, 1) + c * sizeof(T));
+        }
+        float2 wv[V / 2];
+        unpack2<T>(qx, n);
+        unpack2<T>(qd, d);
+        unpack2<T>(w[k], wv);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
-            if (!a.w) w[k][j] = both(1.0f);
-            dw[k][j] = db[k][j] = both(0.0f);
+            n[j] = mul2(add2(n[j], both(-mean)), both(rstd));
+            gr[j] = a.w ? mul2(d[j], wv[j]) : d[j];
         }
-    }
+    };
+    const auto refill = [&](int stage, int64_t r) {
+        if (tr == 0 && r < a.rows) ring.issue(stage, x0 + r * a.cols, d0 + r * a.cols);
+    };
     const float inv = 1.0f / static_cast<float>(a.cols);
     int stage = 0, flip = 0;
     uint32_t phase = 0;
@@ -575,44 +604,39 @@ __global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(
             nr = a.rstd[row + stride];
         }
         ring.wait(stage, phase);
-        float2 n[VPT][V / 2], gr[VPT][V / 2], s1 = both(0.0f), s2 = both(0.0f);
+        float2 n[kKeep][V / 2], gr[kKeep][V / 2], s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * TPR + tr) * V;
-            uint4 qx = make_uint4(0, 0, 0, 0), qd = qx;
-            if (c < a.cols) {
-                qx = *reinterpret_cast<const uint4*>(ring.at(stage, 0) + c * sizeof(T));
-                qd = *reinterpret_cast<const uint4*>(ring.at(stage, 1) + c * sizeof(T));
-            }
+            const int q = kAgain ? 0 : k;
             float2 d[V / 2];
-            unpack2<T>(qx, n[k]);
-            unpack2<T>(qd, d);
+            vec(stage, k, mean, rstd, n[q], gr[q], d);
             // a vector past the row is never stored, and its d = 0 adds nothing
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
-                n[k][j] = mul2(add2(n[k][j], both(-mean)), both(rstd));
-                gr[k][j] = mul2(d[j], w[k][j]);
-                s1 = add2(s1, gr[k][j]);
-                s2 = fma2(gr[k][j], n[k][j], s2);
-                dw[k][j] = fma2(d[j], n[k][j], dw[k][j]);
+                s1 = add2(s1, gr[q][j]);
+                s2 = fma2(gr[q][j], n[q][j], s2);
+                dw[k][j] = fma2(d[j], n[q][j], dw[k][j]);
                 db[k][j] = add2(db[k][j], d[j]);
             }
         }
         float s[2] = {s1.x + s1.y, s2.x + s2.y};
         group_sum<WPR>(s, red[g][flip], 1 + g);
-        if (tr == 0) {
-            const int64_t r = row + a.stages * stride;
-            if (r < a.rows) ring.issue(stage, x0 + r * a.cols, d0 + r * a.cols);
-        }
+        // past the barrier the group has read this row (kAgain: is done with the
+        // row before)
+        if (!kAgain) refill(stage, row + a.stages * stride);
+        else if (row != first) refill(stage ? stage - 1 : a.stages - 1, row + (a.stages - 1) * stride);
         const float2 m1 = both(-s[0] * inv), m2 = both(-s[1] * inv);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * TPR + tr) * V;
+            const int c = (k * TPR + tr) * V, q = kAgain ? 0 : k;
+            if (kAgain) {
+                float2 d[V / 2];
+                vec(stage, k, mean, rstd, n[q], gr[q], d);
+            }
+            float2 o[V / 2];
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j)
-                n[k][j] = mul2(fma2(n[k][j], m2, add2(gr[k][j], m1)), both(rstd));
-            if (c < a.cols)
-                *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.cols + c) = pack2<T>(n[k]);
+            for (int j = 0; j < V / 2; ++j) o[j] = mul2(fma2(n[q][j], m2, add2(gr[q][j], m1)), both(rstd));
+            if (c < a.cols) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.cols + c) = pack2<T>(o);
         }
         if (++stage == a.stages) {
             stage = 0;
@@ -791,16 +815,30 @@ Shape choose(int64_t vecs, int vpt) {
     return {};
 }
 
-// Ring kernels: enough rows that every group passes over several.
-bool use_ring(int64_t rows, const NormArgs& a, int sms) { return a.aligned && rows >= 8 * static_cast<int64_t>(sms); }
+// Ring kernels: rows that start on 16 bytes, enough of them to give every SM a
+// block; backward over rows that take a block each, any number.  Below that the
+// register kernels' wider groups finish a row sooner.  Measured in bf16, 152 SMs,
+// register -> ring kernels:
+//   forward     768 columns (4 rows per block): 320 rows 2.3 -> 2.6 us, 640 rows
+//               2.8 -> 2.8, 1300 rows 3.6 -> 3.1;  4096 columns (1 row): 80 rows
+//               2.5 -> 2.6, 160 rows 2.9 -> 2.7, 1300 rows 8.4 -> 6.0
+//   backward    768 columns (4 rows): 320 rows 4.9 -> 5.2, 640 rows 6.7 -> 5.6;
+//               4096 columns (1 row): 8 rows 7.9 -> 5.8, 320 rows 20.1 -> 10.9;
+//               12288 columns: 8 rows 25.3 -> 13.3, 1300 rows 150 -> 39
+bool use_ring(int64_t vecs, const NormArgs& a, bool bwd, int sms) {
+    const int wpr = choose(vecs, bwd ? 2 : 4).wpr;
+    const int groups = bwd ? ring_bwd_threads(wpr) / (32 * wpr) : ring_groups(wpr);
+    return a.aligned && ((bwd && groups == 1) || a.rows >= static_cast<int64_t>(groups) * sms);
+}
 
 size_t ring_bytes(int groups, int arrays, int stages, int64_t cols, int es) {
     return (static_cast<size_t>(groups) * kMaxStages * 8 + 15) / 16 * 16 +
            static_cast<size_t>(groups) * stages * arrays * cols * es;
 }
 
-// Rows per ring: up to four, as many as kRingBytes holds (at least two do: the
-// widest group's row is 32 KB).
+// Rows per ring: up to kMaxStages, as many as kRingBytes holds.  At least two do
+// (the widest group's row is 32 KB per array), which the backward kernel needs
+// where it refills a stage one row late.
 int ring_stages(int groups, int arrays, int64_t cols, int es) {
     const size_t row = static_cast<size_t>(groups) * arrays * cols * es;
     return static_cast<int>(std::min<size_t>(kMaxStages, kRingBytes / row));
@@ -870,7 +908,9 @@ cudaError_t run_registers(const NormArgs& a, bool bwd, int max_grid, int* grid, 
 // four warps (one vector per thread and sixteen warps: 65 us instead of 50 for
 // 16384 x 4096, the two block-wide reductions bound it).  Backward: two vectors
 // per thread, whose column sums take 32 registers (one vector: 93 us instead of
-// 73), more only in rows wider than 16 warps.
+// 73), four only in rows wider than 16 warps, which then read the row in shared
+// memory twice instead of keeping n and g (1300 x 12288: 47.5 us with spills, 39
+// now).
 template <typename T>
 cudaError_t run_shape(int64_t vecs, const NormArgs& a, bool bwd, bool ring, int max_grid, int* grid, cudaStream_t s) {
     if (ring && !bwd) {
@@ -986,7 +1026,7 @@ extern "C" int dmuon_layer_norm_forward(const void* x, const void* weight, const
         else norm_fwd_wide_kernel<float><<<grid, 1024, 0, s>>>(a);
         return cuda_result(cudaGetLastError(), where);
     }
-    const bool ring = use_ring(rows, a, sms);
+    const bool ring = use_ring(vecs, a, false, sms);
     const int most = ring ? 64 * sms : 4 * sms;
     int grid = 0;
     return cuda_result(bf ? run_shape<__nv_bfloat16>(vecs, a, false, ring, most, &grid, s)
@@ -1060,7 +1100,7 @@ extern "C" int dmuon_layer_norm_backward(const void* dy, const void* x, const vo
             }
         } else {
             const int most = static_cast<int>(std::min<int64_t>(4 * sms, partial_rows(rows)));
-            const bool ring = use_ring(rows, a, sms);
+            const bool ring = use_ring(vecs, a, true, sms);
             e = bf ? run_shape<__nv_bfloat16>(vecs, a, true, ring, most, &partials, s)
                    : run_shape<float>(vecs, a, true, ring, most, &partials, s);
         }

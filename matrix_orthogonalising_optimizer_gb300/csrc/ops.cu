@@ -410,7 +410,8 @@ bool ffn_sizes_ok(int64_t n, int64_t d, int64_t f) {
 
 int check_ffn(int64_t n, int64_t d, int64_t f, int32_t dtype, const char* where) {
     if (!ffn_sizes_ok(n, d, f))
-        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": tokens must be in [0, 2^24], dim and hidden in [1, 2^20]");
+        return fail(DMUON_ERR_INVALID_ARG,
+                    std::string(where) + ": tokens must be in [0, 2^24], dim and hidden in [1, 2^20]");
     return check_dtype(dtype, where);
 }
 

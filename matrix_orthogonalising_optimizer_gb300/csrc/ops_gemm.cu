@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
         const OpsProblem& P = L.p[lane / 4];
         const bool of_b = lane & 2, second = lane & 1;
         if (!second || (of_b ? P.maps_b : P.maps_a) > 1)
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(of_b ? &P.b[second] : &P.a[second]))
+            asm volatile("prefetch.tensormap [%0];" ::"l"(
+                             reinterpret_cast<uint64_t>(of_b ? &P.b[second] : &P.a[second]))
                          : "memory");
     }
     // programmatic dependent launch: global memory only after the previous
@@ -972,7 +973,8 @@ double slab_cost(int bn) { return bn == 256 ? 1.0 : 0.65; }
 
 // The longest chain of a tile in s ranges of K, and its work.
 double unit_cost(const OpsShape& p, int s) {
-    return slab_cost(p.bn) * p.total / s + kUnitCost + kEpiCost * p.bn / 256 + (s > 1 ? kStoreCost + kPartCost * s : 0.0);
+    return slab_cost(p.bn) * p.total / s + kUnitCost + kEpiCost * p.bn / 256 +
+           (s > 1 ? kStoreCost + kPartCost * s : 0.0);
 }
 double tile_work(const OpsShape& p, int s) {
     return slab_cost(p.bn) * p.total + s * kUnitCost + kEpiCost * p.bn / 256 +

@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kThreads, kResident(NT)) ops_stream_kernel(con
     const __nv_bfloat16* xp[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-        xp[n] = static_cast<const __nv_bfloat16*>(P.x) + static_cast<int64_t>(min(8 * n + g, P.tokens - 1)) * P.ldx + 8 * t;
+        xp[n] = static_cast<const __nv_bfloat16*>(P.x) +
+                static_cast<int64_t>(min(8 * n + g, P.tokens - 1)) * P.ldx + 8 * t;
 
     // K pieces of 32: the cluster's blocks take contiguous shares, a block's
     // warps every eighth piece of its share
@@ -349,7 +350,8 @@ cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, bool f32, cudaSt
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     static PerDevice count;
-    e = count.get(dev, &sms, [&](int* out) { return cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev); });
+    e = count.get(dev, &sms,
+                  [&](int* out) { return cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev); });
     if (e != cudaSuccess) return e;
     const int rows = ops_stream_block(a.tokens, f32) / (kind == OPS_GATE ? 2 : 1);
     const int tiles = (a.N + rows - 1) / rows * (f32 ? (a.tokens + 7) / 8 : 1);

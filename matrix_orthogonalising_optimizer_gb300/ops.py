@@ -178,8 +178,8 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu", save=False, workspace=
         saved = (torch.empty_like(h, dtype=kind), torch.empty_like(h, dtype=kind))
     wp, wb, _keep = _space(workspace, lambda: gated_ffn_workspace(tokens, dim, hidden, dt), dev)
     st = _lib.load().dmuon_gated_ffn_forward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
-                                             y.data_ptr(), _ptr(saved[0]), _ptr(saved[1]), _ptr(h), _dtype(kind), tokens, dim,
-                                             hidden, _dtype(dt), act, wp, wb, s)
+                                             y.data_ptr(), _ptr(saved[0]), _ptr(saved[1]), _ptr(h), _dtype(kind),
+                                             tokens, dim, hidden, _dtype(dt), act, wp, wb, s)
     _lib.check(st, "dmuon_gated_ffn_forward")
     return (y, saved, h) if save else y
 
@@ -231,8 +231,8 @@ def _vocab_loss(where, x, weight, targets, coef, ignore_index, workspace, budget
 
     if _elsewhere(stream, dev):
         return _run_elsewhere(stream, (x, weight, targets, coef, workspace),
-                              lambda: _vocab_loss(where, x, weight, targets, coef, ignore_index, workspace, budget, None,
-                                                  grad))
+                              lambda: _vocab_loss(where, x, weight, targets, coef, ignore_index, workspace, budget,
+                                                  None, grad))
     s = _raw_stream(dev.index)
     loss = torch.empty(rows, dtype=torch.float32, device=dev)
     lse = torch.empty_like(loss)

@@ -206,7 +206,8 @@ def norm_reference(x, w, b, eps):
 
 NORM_SHAPES = [(1, 1), (1, 768), (3, 7), (5, 64), (2, 1000), (37, 1001), (700, 96), (1300, 2048), (3, 4096),
                (640, 4100), (20, 8192), (9, 12000), (33, 16384), (5, 16400), (3, 40001), (1250, 4096),
-               (2000, 96), (1217, 16384), (1500, 8192), (1300, 12288), (5000, 8), (3001, 520)]
+               (2000, 96), (1217, 16384), (1500, 8192), (1300, 12288), (5000, 8), (3001, 520),
+               (650, 768), (170, 4096), (400, 16384)]
 
 
 @pytest.mark.gpu
@@ -578,7 +579,8 @@ def test_offsets_past_32_bits():
     xs, dys = x[-40:].clone(), dy[-40:].clone()
     ysm, saveds, hs = pkg.gated_ffn(xs, wg, wu, wd, save="compact")
     outs = pkg.gated_ffn_backward(dys, xs, wg, wu, wd, saveds, hs)
-    for a, b in ((y[-40:], ysm), (h[-40:], hs), (saved[1][-40:], saveds[1]), (out[0][-40:], outs[0]), *zip(out[1:], outs[1:])):
+    for a, b in ((y[-40:], ysm), (h[-40:], hs), (saved[1][-40:], saveds[1]), (out[0][-40:], outs[0]),
+                 *zip(out[1:], outs[1:])):
         # two roundings of operands and one of the result, in norm
         assert float((a.double() - b.double()).norm()) <= 3 * 2.0 ** -8 * float(b.double().norm())
     assert not y[:-40].any() and not out[0][:-40].any()
