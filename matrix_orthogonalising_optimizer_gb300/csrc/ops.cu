@@ -545,7 +545,7 @@ struct LossLayout {
                uint64_t budget)
         : pack(f32) {
         Arena a{base};
-        stream = use_stream(n, f32 ? kStreamTokens : kStreamLossTokens, d, d, f32);
+        stream = use_stream(n, f32 ? kStreamLossTokensF32 : kStreamLossTokens, d, d, f32);
         if (stream) block = ops_stream_block(n, f32);
         if (grad || !stream) {
             common.lay(a);

@@ -112,7 +112,16 @@ struct OpsStream {
     const int64_t* targets;
 };
 
-constexpr int kStreamTokens = 32, kStreamLossTokens = 16;  // most rows the streaming kernel takes
+// Most rows the streaming kernel takes: of the gated block, and of the loss in
+// bf16 and fp32.  Measured, streaming -> tcgen05 kernel:
+//   block  bf16, 4096 x 14336: 8 rows 57 -> 88 us, 16 rows 61 -> 88, 32 rows 88 -> 89;
+//          1024 x 2816: 32 rows 13.4 -> 22.8
+//          fp32, 4096 x 14336: 16 rows 365 -> 675 us, 32 rows 708 -> 664;
+//          1024 x 2816: 32 rows 53 -> 81
+//   loss   bf16, 4096 x 131072: 8 rows 162 -> 172 us, 16 rows 179 -> 173;
+//          1024 x 32000: 8 rows 18 -> 24, 16 rows 24.2 -> 24.2
+//          fp32, 1024 x 32000: 16 rows 95 -> 124 us, 24 rows 137 -> 124
+constexpr int kStreamTokens = 32, kStreamLossTokens = 8, kStreamLossTokensF32 = 16;
 int ops_stream_block(int64_t tokens, bool f32);  // LOGITS: columns per statistics block
 cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, bool f32, cudaStream_t s);
 

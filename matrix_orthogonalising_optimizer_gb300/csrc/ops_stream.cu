@@ -33,8 +33,8 @@ constexpr int kWarps = kThreads / 32;
 // Per instance, by n8 tiles of x rows (1: up to 8 rows, 2: 16, 4: 32): 16-row
 // weight tiles of a warp, K pieces loaded at a time, resident blocks per SM, and
 // the blocks per SM below which K is shared by a cluster.  Measured at 4096 x
-// 14336 (block) and 4096 x 131072 (loss): one row 56 and 158 us, 16 rows 60 and
-// 180; deeper unrolling, more residents or wider clusters each lost 4 to 50 %.
+// 14336 (block) and 4096 x 131072 (loss): one row 56 and 158 us, 16 rows of the
+// block 60; deeper unrolling, more residents or wider clusters each lost 4 to 50 %.
 __host__ __device__ constexpr int kTiles(int nt) { return nt == 1 ? 1 : 2; }
 __host__ __device__ constexpr int kUnroll(int nt) { return nt == 4 ? 1 : nt + 1; }
 __host__ __device__ constexpr int kResident(int nt) { return nt == 1 ? 4 : 2; }
@@ -332,10 +332,11 @@ using Kernel = void (*)(OpsStream);
 template <int kKind>
 Kernel pick(int tokens, bool f32) {
     if (f32) return ops_stream_f32_kernel<kKind>;
-    if (tokens <= 8) return ops_stream_kernel<kKind, 1, kTiles(1)>;
-    if constexpr (kKind != OPS_LOGITS)
+    if constexpr (kKind != OPS_LOGITS) {  // at most kStreamLossTokens rows
         if (tokens > 16) return ops_stream_kernel<kKind, 4, kTiles(4)>;
-    return ops_stream_kernel<kKind, 2, kTiles(2)>;
+        if (tokens > 8) return ops_stream_kernel<kKind, 2, kTiles(2)>;
+    }
+    return ops_stream_kernel<kKind, 1, kTiles(1)>;
 }
 
 }  // namespace
