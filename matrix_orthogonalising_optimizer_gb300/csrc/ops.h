@@ -114,8 +114,8 @@ struct OpsStream {
 
 // Most rows the streaming kernel takes: of the gated block, and of the loss in
 // bf16 and fp32.  Measured, streaming -> tcgen05 kernel:
-//   block  bf16, 4096 x 14336: 8 rows 57 -> 88 us, 16 rows 61 -> 88, 32 rows 88 -> 89;
-//          1024 x 2816: 32 rows 13.4 -> 22.8
+//   block  bf16, 4096 x 14336: 8 rows 57 -> 88 us, 16 rows 60 -> 88, 32 rows 74 -> 89;
+//          1024 x 2816: 32 rows 12.8 -> 22.8
 //          fp32, 4096 x 14336: 16 rows 365 -> 675 us, 32 rows 708 -> 664;
 //          1024 x 2816: 32 rows 53 -> 81
 //   loss   bf16, 4096 x 131072: 8 rows 162 -> 172 us, 16 rows 179 -> 173;

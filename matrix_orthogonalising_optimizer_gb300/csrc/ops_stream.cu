@@ -30,14 +30,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Per instance, by n8 tiles of x rows (1: up to 8 rows, 2: 16, 4: 32): 16-row
-// weight tiles of a warp, K pieces loaded at a time, resident blocks per SM, and
-// the blocks per SM below which K is shared by a cluster.  Measured at 4096 x
-// 14336 (block) and 4096 x 131072 (loss): one row 56 and 158 us, 16 rows of the
-// block 60; deeper unrolling, more residents or wider clusters each lost 4 to 50 %.
+// Per instance, by n8 tiles of x rows (1: up to 8 rows, 2: 16, 3: 24, 4: 32):
+// 16-row weight tiles of a warp, K pieces loaded at a time, resident blocks per
+// SM, whether x is loaded a piece ahead, and the blocks per SM below which K is
+// shared by a cluster.  Measured at 4096 x 14336 (block) and 4096 x 131072 (loss):
+// one row 56 and 156 us, 16, 24 and 32 rows of the block 60, 64 and 74; deeper
+// unrolling, more residents or wider clusters each lost 4 to 50 %.  Above 16 rows
+// the x rows come from L2 as often as the weights (9.6 TB/s together), and their
+// latency was the bound before they were loaded ahead (24 rows 87, 32 rows 88 us);
+// up to 16 rows the registers are better spent on weights in flight (16 rows 60
+// us, 61 with x ahead).
 __host__ __device__ constexpr int kTiles(int nt) { return nt == 1 ? 1 : 2; }
-__host__ __device__ constexpr int kUnroll(int nt) { return nt == 4 ? 1 : nt + 1; }
+__host__ __device__ constexpr int kUnroll(int nt) { return nt > 2 ? 2 : nt + 1; }
 __host__ __device__ constexpr int kResident(int nt) { return nt == 1 ? 4 : 2; }
+__host__ __device__ constexpr bool kAhead(int nt) { return nt > 2; }
 constexpr int kSpread(int nt) { return nt == 1 ? 2 : 1; }
 
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
@@ -186,44 +192,62 @@ __global__ void __launch_bounds__(kThreads, kResident(NT)) ops_stream_kernel(con
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[m][n][i] = 0.0f;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 w[U][MT][2];
-    const auto load_w = [&](int p) {
+    // pieces of 32 k; pieces past p1 are zero
+    uint4 w[U][MT][2], x[kAhead(NT) ? 2 : U][NT];
+    const auto load_w = [&](int p, int u) {
+        const int k = p * 32;
+        const bool in = p < p1 && k + 8 * t < P.K;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (p + u * kWarps) * 32;
-            const bool in = p + u * kWarps < p1 && k + 8 * t < P.K;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int h = 0; h < 2; ++h) w[u][m][h] = in ? ld_stream(wp[m][h] + k) : zero;
+    };
+    const auto load_x = [&](int p, int i) {
+        const int k = p * 32;
+        const bool in = p < p1 && k + 8 * t < P.K;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) w[u][m][h] = in ? ld_stream(wp[m][h] + k) : zero;
-        }
+        for (int n = 0; n < NT; ++n) x[i][n] = in ? *reinterpret_cast<const uint4*>(xp[n] + k) : zero;
+    };
+    const auto multiply = [&](int u, int i) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma(c[m][n], w[u][m][0].x, w[u][m][1].x, w[u][m][0].y, w[u][m][1].y, x[i][n].x, x[i][n].y);
+                mma(c[m][n], w[u][m][0].z, w[u][m][1].z, w[u][m][0].w, w[u][m][1].w, x[i][n].z, x[i][n].w);
+            }
+    };
+    const auto load_round = [&](int p) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) load_w(p + u * kWarps, u);
     };
     // programmatic dependent launch: after the library's own kernel the weights
     // may be read before that kernel has finished (it waited for everything
     // before it, and writes no weights); x and all outputs wait
-    if (P.after) load_w(p0 + warp);
+    if (P.after) load_round(p0 + warp);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!P.after) load_w(p0 + warp);
-    for (int p = p0 + warp; p < p1; p += U * kWarps) {
-        uint4 x[U][NT];
+    if (!P.after) load_round(p0 + warp);
+    if constexpr (kAhead(NT)) {
+        // each piece of the weights is replaced by the one U ahead as soon as it
+        // is used, each piece of x by the next but one
+        load_x(p0 + warp, 0);
+        for (int p = p0 + warp; p < p1; p += U * kWarps) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (p + u * kWarps) * 32;
-            const bool in = p + u * kWarps < p1 && k + 8 * t < P.K;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) x[u][n] = in ? *reinterpret_cast<const uint4*>(xp[n] + k) : zero;
+            for (int u = 0; u < U; ++u) {
+                load_x(p + (u + 1) * kWarps, (u + 1) & 1);
+                multiply(u, u & 1);
+                load_w(p + (u + U) * kWarps, u);
+            }
         }
+    } else {
+        for (int p = p0 + warp; p < p1; p += U * kWarps) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u) load_x(p + u * kWarps, u);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma(c[m][n], w[u][m][0].x, w[u][m][1].x, w[u][m][0].y, w[u][m][1].y, x[u][n].x, x[u][n].y);
-                    mma(c[m][n], w[u][m][0].z, w[u][m][1].z, w[u][m][0].w, w[u][m][1].w, x[u][n].z, x[u][n].w);
-                }
-        if (p + U * kWarps < p1) load_w(p + U * kWarps);
+            for (int u = 0; u < U; ++u) multiply(u, u);
+            if (p + U * kWarps < p1) load_round(p + U * kWarps);
+        }
     }
 #pragma unroll
     for (int round = 0; round < kWarps / kParts; ++round) {
@@ -333,7 +357,8 @@ template <int kKind>
 Kernel pick(int tokens, bool f32) {
     if (f32) return ops_stream_f32_kernel<kKind>;
     if constexpr (kKind != OPS_LOGITS) {  // at most kStreamLossTokens rows
-        if (tokens > 16) return ops_stream_kernel<kKind, 4, kTiles(4)>;
+        if (tokens > 24) return ops_stream_kernel<kKind, 4, kTiles(4)>;
+        if (tokens > 16) return ops_stream_kernel<kKind, 3, kTiles(3)>;
         if (tokens > 8) return ops_stream_kernel<kKind, 2, kTiles(2)>;
     }
     return ops_stream_kernel<kKind, 1, kTiles(1)>;

@@ -299,7 +299,8 @@ FFN_SHAPES = [(1, 64, 128), (1, 1, 1), (2, 72, 200), (17, 128, 96), (129, 64, 25
               (512, 256, 768), (31, 2048, 512), (5, 64, 5000), (1000, 520, 264), (64, 4096, 64),
               (8, 2056, 104), (16, 40, 1032), (23, 1032, 2000), (32, 8, 8), (9, 520, 7),
               (1500, 64, 1280), (4000, 72, 640), (300, 1300, 1400),
-              (7, 1028, 260), (12, 132, 2052), (26, 300, 100), (40, 16384, 72)]
+              (7, 1028, 260), (12, 132, 2052), (26, 300, 100), (40, 16384, 72),
+              (24, 2560, 1544), (29, 1544, 2560)]
 
 
 @pytest.mark.gpu
