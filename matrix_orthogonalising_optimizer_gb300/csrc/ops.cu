@@ -64,6 +64,14 @@ struct Arena {
     }
 };
 
+// Zeroes a launch's counters: n ints, a multiple of 64, at 256 bytes.  A kernel
+// rather than a memset, so that the GEMM launched after it as a programmatic
+// dependent sets up its barriers and tensor memory meanwhile.
+__global__ void __launch_bounds__(1024) zero_kernel(int4* p, int n) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int i = blockIdx.x * 1024 + threadIdx.x; i < n / 4; i += gridDim.x * 1024) p[i] = make_int4(0, 0, 0, 0);
+}
+
 // Counters and partial sums of a call's GEMM launches.
 struct Common {
     int32_t* counters = nullptr;  // [kMaxLaunches] unit counters, 64 ints apart, then the tail counts
@@ -89,7 +97,10 @@ struct Common {
             if (split) ints = kMaxLaunches * 64 + (i + 1) * kTailInts;
             else if (l[i].total_units > pairs) ints = std::max<int64_t>(ints, (i + 1) * 64);
         }
-        return ints ? cudaMemsetAsync(counters, 0, ints * sizeof(int32_t), s) : cudaSuccess;
+        if (ints == 0) return cudaSuccess;
+        zero_kernel<<<static_cast<int>(ceil_div(ints, 4096)), 1024, 0, s>>>(reinterpret_cast<int4*>(counters),
+                                                                         static_cast<int>(ints));
+        return cudaGetLastError();
     }
 };
 
