@@ -118,9 +118,11 @@ struct OpsStream {
 //          1024 x 2816: 32 rows 12.8 -> 22.8
 //          fp32, 4096 x 14336: 16 rows 365 -> 675 us, 32 rows 708 -> 664;
 //          1024 x 2816: 32 rows 53 -> 81
-//   loss   bf16, 4096 x 131072: 8 rows 162 -> 172 us, 16 rows 179 -> 173;
-//          1024 x 32000: 8 rows 18 -> 24, 16 rows 24.2 -> 24.2
-//          fp32, 1024 x 32000: 16 rows 95 -> 124 us, 24 rows 137 -> 124
+//   loss   bf16, 4096 x 131072: 8 rows 157 -> 167 us, 16 rows 175 -> 167;
+//          4096 x 32000: 8 rows 47 -> 53, 16 rows 52 -> 53;
+//          1024 x 32000: 8 rows 18.0 -> 22.6, 16 rows 24.2 -> 22.6
+//          fp32, 4096 x 32000: 16 rows 261 -> 450 us, 24 rows 403 -> 449;
+//          1024 x 32000: 16 rows 95 -> 124, 24 rows 137 -> 124
 constexpr int kStreamTokens = 32, kStreamLossTokens = 8, kStreamLossTokensF32 = 16;
 int ops_stream_block(int64_t tokens, bool f32);  // LOGITS: columns per statistics block
 cudaError_t launch_ops_stream(const OpsStream& a, int32_t kind, bool f32, cudaStream_t s);

@@ -149,16 +149,18 @@ __device__ __forceinline__ void st_staged(T* base, int64_t ld, int r0, int c0, i
     for (int j = 0; j < CH; ++j) stg[lane * kStageLd + j] = v[j];
     __syncwarp();
     const int c = lane % CH;
-    T* p = base + static_cast<int64_t>(r0) * ld + c0 + c;
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-        const int r = 2 * i + lane / CH;
-        const float x = stg[r * kStageLd + c];
-        if (r0 + r < M && c0 + c < N) {
-            if constexpr (sizeof(T) == 2) p[r * ld] = __float2bfloat16_rn(x);
-            else p[r * ld] = x;
+    T* p = base + (r0 + static_cast<int64_t>(lane / CH)) * ld + c0 + c;
+    const int rows = c0 + c < N ? M - r0 - lane / CH : 0;
+    // all loads before the first store (as ld_staged)
+    float x[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) x[i] = stg[(2 * i + lane / CH) * kStageLd + c];
+#pragma unroll
+    for (int i = 0; i < CH; ++i, p += 2 * ld)
+        if (2 * i < rows) {
+            if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(x[i]);
+            else *p = x[i];
         }
-    }
     __syncwarp();
 }
 
@@ -410,12 +412,24 @@ __device__ __forceinline__ void epi_gate(const OpsProblem& P, Src acc, const Uni
         if (c0 >= P.N) break;
         float f[CH], s[CH], h[CH];
         acc.load_pair(kc, f, h);
+        // one branch per chunk: the activations' instructions are fetched apart
+        const auto activate = [&](auto act, auto save) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const float a = f[j], w = h[j], g = act_gate<kF32>(P.act, a);
-            f[j] = a * g;
-            h[j] = f[j] * w;
-            if (P.out[1].p) s[j] = w * act_slope<kF32>(P.act, a, g);
+            for (int j = 0; j < CH; ++j) {
+                const float a = f[j], w = h[j], g = act_gate<kF32>(decltype(act)::value, a);
+                f[j] = a * g;
+                h[j] = f[j] * w;
+                if (decltype(save)::value) s[j] = w * act_slope<kF32>(decltype(act)::value, a, g);
+            }
+        };
+        using Silu = std::integral_constant<int, OPS_SILU>;
+        using Gelu = std::integral_constant<int, OPS_GELU>;
+        if (P.act == OPS_SILU) {
+            if (P.out[1].p) activate(Silu{}, std::true_type{});
+            else activate(Silu{}, std::false_type{});
+        } else {
+            if (P.out[1].p) activate(Gelu{}, std::true_type{});
+            else activate(Gelu{}, std::false_type{});
         }
 #pragma unroll 1
         for (int o = 0; o < 4; ++o) {
