@@ -150,12 +150,13 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
         }
         __nv_bfloat16* d = it.dst + r * it.ld + c0;
         const int parts = a.f32 ? kF32Parts : 1;
+        const bool plain = tc::all_plain(v);
         for (int p = 0; p < parts; ++p) {
+            uint32_t w[8];
+            tc::bf16_parts(v, w, plain);
             *reinterpret_cast<uint4*>(d + p * it.part) =
-                make_uint4(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]), tc::pack_bf16x2(v[4], v[5]),
-                           tc::pack_bf16x2(v[6], v[7]));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = tc::bf16_rest(v[j]);
+                make_uint4(tc::pack_parts(w[0], w[1]), tc::pack_parts(w[2], w[3]), tc::pack_parts(w[4], w[5]),
+                           tc::pack_parts(w[6], w[7]));
         }
     }
 }
@@ -526,15 +527,20 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
             }
         }
         __nv_bfloat16* d = a.dz + off;
+        if constexpr (kF32) {
+            const bool plain = tc::all_plain(v);
 #pragma unroll
-        for (int p = 0; p < (kF32 ? kF32Parts : 1); ++p) {
-            *reinterpret_cast<uint4*>(d + p * a.part) =
+            for (int p = 0; p < kF32Parts; ++p) {
+                uint32_t w[8];
+                tc::bf16_parts(v, w, plain);
+                *reinterpret_cast<uint4*>(d + p * a.part) =
+                    make_uint4(tc::pack_parts(w[0], w[1]), tc::pack_parts(w[2], w[3]), tc::pack_parts(w[4], w[5]),
+                               tc::pack_parts(w[6], w[7]));
+            }
+        } else {
+            *reinterpret_cast<uint4*>(d) =
                 make_uint4(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]), tc::pack_bf16x2(v[4], v[5]),
                            tc::pack_bf16x2(v[6], v[7]));
-            if (kF32) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = tc::bf16_rest(v[k]);
-            }
         }
     }
 }

@@ -244,17 +244,22 @@ __device__ __forceinline__ void st_mat(const OpsMat& m, int r0, int c0, int lane
         st_bf16(p, m.ld, m.vec, r0, c0, lane, v, M, N, stg);
         return;
     }
-    // parts: each the value left over rounded to 8 bits (half up, by integer
-    // addition: conversions issue at a quarter of the rate); the three are exact
+    const bool plain = all_plain(v);
 #pragma unroll 1
     for (int k = 0; k < kF32Parts; ++k, p += m.part) {
-        float h[CH];
+        uint32_t h[CH];
+        bf16_parts(v, h, plain);
+        if (m.vec && c0 + CH <= N) {
+            uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            h[j] = __uint_as_float((__float_as_uint(v[j]) + 0x8000u) & 0xffff0000u);
-            v[j] = fabsf(h[j]) <= 3.4e38f ? v[j] - h[j] : 0.0f;
+            for (int j = 0; j < 8; ++j) w[j] = pack_parts(h[2 * j], h[2 * j + 1]);
+            st_words(p, m.ld, r0, c0, lane, w, M);
+        } else {
+            float x[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) x[j] = __uint_as_float(h[j]);
+            st_staged(p, m.ld, r0, c0, lane, x, M, N, stg);
         }
-        st_bf16(p, m.ld, m.vec, r0, c0, lane, h, M, N, stg);
     }
 }
 

@@ -224,12 +224,43 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
 
-// What a bf16 rounding of v leaves over (0 where the rounded value is not
-// finite, so an infinity stays one instead of turning into inf - inf).
-__device__ __forceinline__ float bf16_rest(float v) {
-    const float h = __bfloat162float(__float2bfloat16_rn(v));
-    return fabsf(h) <= 3.4e38f ? v - h : 0.0f;
+// Whether all values are well inside the range of bf16: none infinite, NaN or
+// rounded to infinity.
+template <int N>
+__device__ __forceinline__ bool all_plain(const float (&v)[N]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+    return top < 0x7f7f8000u;
 }
+
+// The leading bf16 parts of the values, in the words' upper halves; v becomes
+// what is left over, so three calls take fp32 values apart exactly.  Rounded half
+// up, by integer addition (conversions issue at a quarter of the rate).  `plain`:
+// all_plain() held before the first call.  Else values that would round to
+// infinity are cut off instead, and an infinity or NaN stays one and leaves
+// nothing, so that the parts do not turn into inf - inf.
+template <int N>
+__device__ __forceinline__ void bf16_parts(float (&v)[N], uint32_t (&h)[N], bool plain) {
+    if (plain) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            h[j] = (__float_as_uint(v[j]) + 0x8000u) & 0xffff0000u;
+            v[j] -= __uint_as_float(h[j]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const uint32_t b = __float_as_uint(v[j]), mag = b & 0x7fffffffu;
+        h[j] = (b + 0x8000u) & 0xffff0000u;
+        if (mag >= 0x7f7f8000u) h[j] = (b & 0xffff0000u) | (mag > 0x7f800000u ? 0x00400000u : 0u);
+        v[j] = mag >= 0x7f800000u ? 0.0f : v[j] - __uint_as_float(h[j]);
+    }
+}
+
+// Two parts in one word.
+__device__ __forceinline__ uint32_t pack_parts(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
 // 4 x 4 transpose of 16-byte blocks within each lane quad: block q of lane
 // i (words 4q .. 4q+3) ends in block i of lane q.  Its own inverse.

@@ -687,3 +687,52 @@ def test_example_trains(dtype):
     losses = mod.train(steps=60, vocab=500, dim=128, hidden=384, tokens=2000, dtype=DT[dtype])
     # the first loss is near log(vocab); sixty steps at least halve it
     assert abs(losses[0] - math.log(500)) < 1.5 and losses[-1] < 0.5 * losses[0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("tokens", [8, 40])
+def test_nan_stays_in_its_row(tokens, dtype):
+    """A NaN reaches every result that depends on it, and no other row."""
+    dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(21)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").mul(0.5).to(dt)
+
+    x, dy = rand(tokens, 64), rand(tokens, 64)
+    wg, wu, wd, w = rand(96, 64), rand(96, 64), rand(64, 96), rand(200, 64)
+    bad = torch.arange(tokens, device="cuda") == 3
+    xn, dyn = x.clone(), dy.clone()
+    xn[3, 5] = dyn[3, 7] = float("nan")
+
+    def rows(t):
+        assert torch.equal(t.isnan().all(1), bad) and torch.equal(t.isnan().any(1), bad)
+
+    for act in ("silu", "gelu"):
+        for save in (False, True):
+            r = pkg.gated_ffn(xn, wg, wu, wd, activation=act, save=save)
+            rows(r[0] if save else r)
+        y, saved, h = pkg.gated_ffn(x, wg, wu, wd, activation=act, save=True)
+        dx, dwg, dwu, dwd = pkg.gated_ffn_backward(dyn, x, wg, wu, wd, saved, h)
+        rows(dx)
+        assert dwg.isnan().all() and dwu.isnan().all() and dwd[7].isnan().all() and dwd.isnan().sum() == 96
+    targets = torch.zeros(tokens, dtype=torch.int64, device="cuda")
+    loss, lse, dx, dw = pkg.vocab_loss_grad(xn, w, targets)
+    assert torch.equal(loss.isnan(), bad) and torch.equal(lse.isnan(), bad)
+    rows(dx)
+    assert dw.isnan().all()
+
+
+@pytest.mark.gpu
+def test_largest_fp32_values():
+    """fp32 values next to the largest are not rounded to infinity on their way to the tensor cores."""
+    big = torch.finfo(torch.float32).max
+    x = torch.zeros(40, 64, device="cuda")
+    x[:, 0] = big
+    w = torch.zeros(200, 64, device="cuda")
+    w[:, 0] = torch.linspace(1, 1.99, 200, device="cuda") * 2.0 ** -126
+    _, lse = pkg.vocab_loss(x, w, torch.zeros(40, dtype=torch.int64, device="cuda"))
+    z = w[:, 0].double() * big
+    # a part of w below the smallest normal number may count as zero: 2^-8 of a logit, all below 8
+    assert torch.allclose(lse.double(), torch.logsumexp(z, 0).expand(40), rtol=0, atol=2.0 ** -5 + 2.0 ** -20)
