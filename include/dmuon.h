@@ -427,7 +427,8 @@ int dmuon_layer_norm_backward(const void* dy, const void* x, const void* weight,
  * DMUON_BF16 (half the memory) act(a) and u act'(a) are too, which takes the
  * gradients' error from 1.4 to 1.7 roundings of their own type.
  * fp32: every product runs as six products of bf16 parts (x = hi + mid + lo),
- * which keeps fp32 accuracy.  tokens in [0, 2^24], dim and hidden in
+ * which keeps fp32 accuracy (an infinite operand may give NaN where one product
+ * would give an infinity).  tokens in [0, 2^24], dim and hidden in
  * [1, 2^20].  Widths that are a multiple of 8 are read in place; bf16 matrices
  * of other widths, and fp32 ones, are first copied into the workspace. */
 #define DMUON_ACT_SILU 0
