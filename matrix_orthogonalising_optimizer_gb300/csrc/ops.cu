@@ -43,6 +43,13 @@ constexpr int kChain = 8, kChainF32 = 4;
 // too, from chains of kLongChain slabs: 2048 truncated additions drift by at most
 // 2^-13 of the sum
 constexpr int kLongSum = 2048, kLongChain = 512;
+// Up to this many bf16 tokens the logit gradients are kept in two bf16 parts: in one,
+// the target's rounding, most of a token's gradient, is off by up to 2^-8, and a few
+// tokens do not average that out (3 tokens, 64 x 5169: error of dW 2.8e-3 against
+// 1.7e-3 of the result's own rounding).  The parts are rows of one product for dx,
+// which reads W once, and two part products of dW (3 tokens, 4096 x 131072: 687 us
+// with one part, 690 with two, 961 with W read for each).
+constexpr int kPartTokens = 32;
 constexpr int kMaxLaunches = 4;   // GEMM launches of one call (of one piece)
 constexpr int kSlots = 192;       // partial-sum slots: 48 MiB
 constexpr int kTails = 192;       // split tiles per launch
@@ -262,13 +269,12 @@ int set_problem(OpsProblem& P, int64_t M, int64_t N, int64_t K, const Operand* a
     P.dual = dual;
     P.tiles_m = static_cast<int32_t>(ceil_div(M, 256));
     P.tiles_n = static_cast<int32_t>(ceil_div(N, dual ? bn / 2 : bn));
-    // part products above 2^-24 of the whole, the smallest first
+    // products of the operands' parts above 2^-24 of the whole, the smallest first
     static const int kPairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
-    const bool f32 = a[0].parts > 1;
     P.nseg = 0;
-    for (int i = f32 ? 0 : 5; i < 6; ++i)
-        for (int s = 0; s < na; ++s)
-            P.seg[P.nseg++] = static_cast<uint16_t>(s | kPairs[i][0] << 4 | kPairs[i][1] << 8);
+    for (const auto& pair : kPairs)
+        for (int s = 0; s < na && pair[0] < a[0].parts && pair[1] < b[0].parts; ++s)
+            P.seg[P.nseg++] = static_cast<uint16_t>(s | pair[0] << 4 | pair[1] << 8);
     return DMUON_OK;
 }
 
@@ -437,12 +443,13 @@ struct LossRowArgs {
     float* loss;
     float* lse;
     const void* e;              // exponentials (16-bit codes or fp32), NULL: losses only
-    __nv_bfloat16* dz;          // logit gradients, kF32Parts parts for fp32
+    __nv_bfloat16* dz;          // logit gradients in `parts` bf16 parts
     int64_t ld, part, ignore;
     int64_t vocab;
     int32_t nblk, shift;        // statistics blocks of a row, log2 of their columns
     int32_t groups;             // 8-column groups of a row
     int32_t seg_groups;         // groups per blockIdx.y
+    int32_t parts;              // kF32Parts for fp32, 2 or 1 for bf16
 };
 
 constexpr int kRowThreads = 256;
@@ -527,10 +534,10 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
             }
         }
         __nv_bfloat16* d = a.dz + off;
-        if constexpr (kF32) {
+        if (kF32 || a.parts > 1) {
             const bool plain = tc::all_plain(v);
 #pragma unroll
-            for (int p = 0; p < kF32Parts; ++p) {
+            for (int p = 0; p < (kF32 ? kF32Parts : 2); ++p) {
                 uint32_t w[8];
                 tc::bf16_parts(v, w, plain);
                 *reinterpret_cast<uint4*>(d + p * a.part) =
@@ -545,6 +552,15 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
     }
 }
 
+// dx = bf16(s_r + s_(n+r)): the sums of the two parts' rows.
+__global__ void __launch_bounds__(256) add_parts_kernel(const float* s, int64_t ld, int n, int dim,
+                                                        __nv_bfloat16* dx) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int r = blockIdx.y;
+    for (int c = blockIdx.x * 256 + threadIdx.x; c < dim; c += gridDim.x * 256)
+        dx[static_cast<int64_t>(r) * dim + c] = __float2bfloat16_rn(s[r * ld + c] + s[(n + r) * ld + c]);
+}
+
 struct LossLayout {
     Common common;
     Packer pack;
@@ -552,6 +568,7 @@ struct LossLayout {
     void* e = nullptr;         // exponentials (bf16: in dz's buffer)
     float2* stats = nullptr;
     float* target_logit = nullptr;
+    float* dx_sum = nullptr;   // bf16, two parts: fp32 dx of each part
     float* dw_sum = nullptr;   // fp32 sum of dW over pieces (bf16, more than one piece)
     int64_t piece = 0, pieces = 0;  // tokens per piece
     bool stream;               // a few rows: the streaming kernel
@@ -582,8 +599,9 @@ struct LossLayout {
         stats = a.take<float2>(piece * nblk);
         target_logit = a.take<float>(piece);
         if (grad) {
-            dz = scratch(a, piece, v, f32 ? kF32Parts : 1, 16);
+            dz = scratch(a, piece, v, f32 ? kF32Parts : n <= kPartTokens ? 2 : 1, 16);
             e = f32 ? static_cast<void*>(a.take<float>(piece * ld)) : const_cast<void*>(dz.p);
+            if (!f32 && dz.parts > 1) dx_sum = a.take<float>(2 * n * up(d, 4));
             if (!f32 && pieces > 1) dw_sum = a.take<float>(v * up(d, 4));
         }
         bytes = a.off;
@@ -825,11 +843,17 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             l[1].n = 2;
             const int kx = vocab >= n ? 0 : 1;
             OpsShape sh[2];
-            sh[kx] = shape_of(n, dim, vocab, 1, f32);
-            sh[1 - kx] = shape_of(vocab, dim, n, 1, f32);
+            Operand rows = dz;
+            if (L.dx_sum) {  // the second part's rows follow the first's
+                rows.rows = 2 * n;
+                rows.parts = 1;
+            }
+            sh[kx] = shape_of(rows.rows, dim, vocab, 1, f32);
+            sh[1 - kx] = shape_of(vocab, dim, n, f32 ? 1 : dz.parts, f32);
             ops_tile_columns(sh, 2, pairs);
-            OPS_TRY(set_problem(l[1].p[kx], n, dim, vocab, &dz, false, &L.w, true, 1, false, sh[kx].bn));
-            l[1].p[kx].out[0] = user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
+            OPS_TRY(set_problem(l[1].p[kx], rows.rows, dim, vocab, &rows, false, &L.w, true, 1, false, sh[kx].bn));
+            l[1].p[kx].out[0] = L.dx_sum ? user_mat(L.dx_sum, up(dim, 4), true)
+                                         : user_mat(static_cast<char*>(dx) + r0 * dim * es, dim, f32);
             OpsProblem& W = l[1].p[1 - kx];
             OPS_TRY(set_problem(W, vocab, dim, n, &dz, true, &xp, true, 1, false, sh[1 - kx].bn));
             // the sum over pieces stays in fp32: rounded once, with the last piece
@@ -868,6 +892,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             a.dz = static_cast<__nv_bfloat16*>(const_cast<void*>(L.dz.p));
             a.ld = L.dz.ld;
             a.part = L.dz.part;
+            a.parts = L.dz.parts;
             a.groups = static_cast<int32_t>(ceil_div(vocab, 8));
             // a few rows: share each row among blocks, so that about 1200 run
             segs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.groups, 1024), 1200 / n)));
@@ -876,6 +901,11 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(segs));
         OPS_CUDA(launch_dependent(f32 ? loss_row_kernel<true> : loss_row_kernel<false>, grid, kRowThreads, s, a));
         if (grad) OPS_CUDA(launch(l[1], OPS_STORE, f32, s));
+        if (L.dx_sum)
+            OPS_CUDA(launch_dependent(add_parts_kernel,
+                                      dim3(static_cast<unsigned>(ceil_div(dim, 256)), static_cast<unsigned>(n)), 256, s,
+                                      L.dx_sum, up(dim, 4), static_cast<int>(n), static_cast<int>(dim),
+                                      static_cast<__nv_bfloat16*>(dx)));
     }
     return DMUON_OK;
 }

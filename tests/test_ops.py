@@ -736,3 +736,23 @@ def test_largest_fp32_values():
     z = w[:, 0].double() * big
     # a part of w below the smallest normal number may count as zero: 2^-8 of a logit, all below 8
     assert torch.allclose(lse.double(), torch.logsumexp(z, 0).expand(40), rtol=0, atol=2.0 ** -5 + 2.0 ** -20)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [1, 3, 12, 32])
+def test_vocab_loss_grad_of_few_tokens(tokens):
+    """A few tokens' gradients are as good as the rounding of the result."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn(tokens, 1024, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(1000, 1024, generator=g, device="cuda") * 0.001).bfloat16()
+    targets = torch.arange(tokens, device="cuda") * 7
+    # coef (p - 1) halfway between two bf16 values, where a rounding of it costs most
+    coef = torch.full((tokens,), 1.005, device="cuda")
+    _, _, dx, dw = pkg.vocab_loss_grad(x, w, targets, coef=coef)
+    dz = torch.softmax(x.double() @ w.double().T, 1)
+    dz[torch.arange(tokens, device="cuda"), targets] -= 1
+    dz *= coef.double()[:, None]
+    # a rounding to bf16 is off by 2^-8 of the value at most, spread evenly: 2^-8 / sqrt(3) in norm (5 % for the
+    # spread of a sample); the exponentials' codes by 2^-12
+    for got, want in ((dx, dz @ w.double()), (dw, dz.T @ x.double())):
+        assert float((got.double() - want).norm() / want.norm()) <= 1.05 * 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -12
