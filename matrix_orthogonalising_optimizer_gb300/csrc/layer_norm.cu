@@ -429,15 +429,22 @@ struct Ring {
     uint64_t* full;
     uint32_t bytes;  // of one row
     int arrays;
-    bool dead;       // a wait gave up: the results are lost (status), the loop goes on
+    bool dead;       // a wait gave up: the results are lost (status), the loop goes on without copies
     __device__ __forceinline__ uint8_t* at(int stage, int k) const { return rows + (stage * arrays + k) * bytes; }
     __device__ __forceinline__ void issue(int stage, const void* a, const void* b) {
+        if (dead) return;
         mbar_expect_tx(&full[stage], bytes * arrays);
         bulk_load(at(stage, 0), a, bytes, &full[stage]);
         if (arrays > 1) bulk_load(at(stage, 1), b, bytes, &full[stage]);
     }
-    __device__ __forceinline__ void wait(int stage, uint32_t phase) {
-        if (!dead) dead = !mbar_wait<false>(&full[stage], phase, &g_norm_status);
+    // `issuer`: the thread that issues the copies.  Where its wait gives up, it waits
+    // once more (with the same limit) for each stage's copy still under way, so that
+    // none lands after the block has left.
+    __device__ __forceinline__ void wait(int stage, uint32_t phase, int stages, bool issuer) {
+        if (dead || mbar_wait<false>(&full[stage], phase, &g_norm_status)) return;
+        dead = true;
+        for (int s = 0; issuer && s < stages; ++s)
+            mbar_wait<false>(&full[s], s < stage ? phase ^ 1 : phase, &g_norm_status);
     }
 };
 
@@ -487,7 +494,7 @@ __launch_bounds__(ring_groups(WPR) * WPR * 32, 512 / (ring_groups(WPR) * WPR * 3
     int stage = 0;
     uint32_t phase = 0;
     for (int64_t row = first; row < a.rows; row += stride) {
-        ring.wait(stage, phase);
+        ring.wait(stage, phase, a.stages, tr == 0);
         float2 x[VPT][V / 2];
         float2 s2 = both(0.0f);
 #pragma unroll
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(
             nm = a.mean[row + stride];
             nr = a.rstd[row + stride];
         }
-        ring.wait(stage, phase);
+        ring.wait(stage, phase, a.stages, tr == 0);
         float2 n[kKeep][V / 2], gr[kKeep][V / 2], s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
