@@ -587,13 +587,16 @@ __global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(
             qx = *reinterpret_cast<const uint4*>(ring.at(stage, 0) + c * sizeof(T));
             qd = *reinterpret_cast<const uint4*>(ring.at(stage, 1) + c * sizeof(T));
         }
+        // past the row n is zero too: -mean rstd could be infinite, and its product
+        // with g = 0 NaN
+        const float2 shift = both(c < a.cols ? -mean : 0.0f);
         float2 wv[V / 2];
         unpack2<T>(qx, n);
         unpack2<T>(qd, d);
         unpack2<T>(w[k], wv);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
-            n[j] = mul2(add2(n[j], both(-mean)), both(rstd));
+            n[j] = mul2(add2(n[j], shift), both(rstd));
             gr[j] = a.w ? mul2(d[j], wv[j]) : d[j];
         }
     };
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(ring_bwd_threads(WPR), 512 / ring_bwd_threads(
             const int q = kAgain ? 0 : k;
             float2 d[V / 2];
             vec(stage, k, mean, rstd, n[q], gr[q], d);
-            // a vector past the row is never stored, and its d = 0 adds nothing
+            // a vector past the row is never stored, and its d = n = 0 adds nothing
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
                 s1 = add2(s1, gr[q][j]);
