@@ -483,9 +483,12 @@ __device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Un
     }
 }
 
+// exp(z - m).  The difference is taken before it is scaled: in z log2(e) - m log2(e),
+// one FMA, the rounding of m log2(e) stays as an error of the exponent, and at
+// |m| of 10^10 (masked logits) the maximum's own exponential became infinite.
 template <bool kF32>
-__device__ __forceinline__ float exp_of(float z, float m, float ms) {
-    return kF32 ? expf(z - m) : ex2(fmaf(z, kLog2e, -ms));
+__device__ __forceinline__ float exp_of(float z, float m) {
+    return kF32 ? expf(z - m) : ex2((z - m) * kLog2e);
 }
 
 template <bool kF32>
@@ -513,7 +516,6 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
         P.target_logit[r] = zt;
     }
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float ms = m * kLog2e;
     if (P.out[0].p) {
         RegSrc src{z};
 #pragma unroll 1
@@ -523,7 +525,7 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
             src.load(kc, v);
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                v[j] = exp_of<kF32>(v[j], m, ms);
+                v[j] = exp_of<kF32>(v[j], m);
                 sum[j % 4] += v[j];
             }
             // rows are padded to whole chunks, so every chunk is stored whole
@@ -539,7 +541,7 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j) sum[j % 4] += exp_of<kF32>(z[j], m, ms);
+        for (int j = 0; j < BN / 2; ++j) sum[j % 4] += exp_of<kF32>(z[j], m);
     }
     if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] =
         make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));

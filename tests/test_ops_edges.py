@@ -1,4 +1,5 @@
-"""Edges of the training operators: schedules of many short units, rows of huge values.
+"""Edges of the training operators: schedules of many short units, rows of huge values,
+masked logits.
 
 Bounds as in test_ops.py, whose plain fp64 forms are used.
 """
@@ -41,3 +42,43 @@ def test_norm_backward_of_huge_constant_rows(dtype, rows):
     want = rstd.double()[:, None] * (dy.double() - dy.double().mean(1, keepdim=True))
     within(dx, want, U[dt] * want.abs() + 2.0 ** -20 * rstd.double()[:, None] * dy.double().abs().amax(1, True), "dx")
     assert not dw.any()
+
+
+def masked_inputs(tokens, dt, seed):
+    """A vocabulary of 640 whose columns 128 to 255 and 512 on (whole statistics blocks of
+    every kernel) and 300 to 307 are masked through a feature that is 1 in every token."""
+    x, w, t, coef = loss_inputs(tokens, 64, 640, dt, seed)
+    x[:, 0] = 1.0
+    w[:, 0] = 0.0
+    mask = torch.zeros(640, dtype=torch.bool, device="cuda")
+    mask[128:256] = mask[512:] = mask[300:308] = True
+    kept = torch.cumsum(~mask, 0) - 1
+    w[mask] = 0.0
+    t = torch.where(t >= 0, t % 128, t)  # targets are not masked
+    return x, w, t, coef, mask, kept
+
+
+def check_masked(x, w, t, coef, mask, kept, grads=True):
+    """The masked columns have no part in the loss and get no gradient."""
+    t2 = torch.where(t >= 0, kept[t.clamp(min=0)], t)
+    check_loss(x, w[~mask], t2, None, pkg.vocab_loss(x, w, t))
+    loss, lse, dx, dw = pkg.vocab_loss_grad(x, w, t, coef=coef)
+    assert not dw[mask].any()
+    if grads:
+        check_loss(x, w[~mask], t2, coef, (loss, lse, dx, dw[~mask]))
+    else:  # dx of feature 0 is 0 times infinity
+        check_loss(x, w[~mask], t2, None, (loss, lse))
+        out = (loss, lse, dx[:, 1:].contiguous(), dw[~mask])
+        assert torch.isfinite(out[2]).all() and torch.isfinite(out[3]).all()
+    assert pkg.ops_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [-1e9, -1e10, -1e20, -1e30, "lowest"])
+@pytest.mark.parametrize("tokens", [3, 12, 40, 300])
+def test_vocab_loss_masked_blocks(tokens, value, dtype):
+    """Finite logits far below the others, a whole block of columns of them."""
+    x, w, t, coef, mask, kept = masked_inputs(tokens, DT[dtype], 40 + tokens)
+    w[mask, 0] = torch.finfo(torch.bfloat16).min if value == "lowest" else value
+    check_masked(x, w, t, coef, mask, kept)
