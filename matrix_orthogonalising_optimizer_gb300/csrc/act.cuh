@@ -42,6 +42,11 @@ __device__ __forceinline__ float act_slope(int act, float a, float gate) {
     return gate + a * pdf;
 }
 
+// What is subtracted from a block's logits before their exponentials are taken: the
+// maximum m or, where there is no finite logit (m = -inf), 0, so that they are 0
+// and not exp(-inf + inf).
+__device__ __forceinline__ float exp_shift(float m) { return m == __int_as_float(0xff800000) ? 0.0f : m; }
+
 // An exponential relative to its block's maximum, 0 <= e <= 1, in 16 bits: 5
 // exponent and 11 mantissa bits of the fp32 value (relative error 2^-12), zero
 // below 2^-31.  bf16 would round the probability once more, by 2^-8, before the

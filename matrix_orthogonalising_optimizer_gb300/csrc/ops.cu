@@ -455,7 +455,8 @@ struct LossRowArgs {
 constexpr int kRowThreads = 256;
 
 // Row pass of the loss.  Each block reduces its row's (max, sum) blocks to
-// lse = M + log sum_b s_b exp(m_b - M) in a fixed order; the first writes the
+// lse = M + log sum_b s_b exp(m_b - M) in a fixed order (blocks without a finite
+// logit have s_b = 0, a row without one lse = -inf and a NaN loss and gradient); the first writes the
 // loss, and each turns its share of the row's exponentials e = exp(z - m_b)
 // into logit gradients dz = c e exp(m_b - lse), the target's as c expm1(z_t -
 // lse), which keeps the digits of p - 1 where p is near 1.  Memory-bound: 4
@@ -477,10 +478,11 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
 #pragma unroll
     for (int w = 1; w < kRowThreads / 32; ++w) m = fmaxf(m, red[w]);
     __syncthreads();
+    const float ms = exp_shift(m);
     float s = 0.0f;
     for (int b = tid; b < a.nblk; b += kRowThreads) {
         const float2 v = st[b];
-        s += v.y * expf(v.x - m);
+        s += v.y * expf(v.x - ms);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(tc::kFullMask, s, o);

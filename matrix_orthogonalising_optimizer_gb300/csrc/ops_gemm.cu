@@ -516,6 +516,7 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
         P.target_logit[r] = zt;
     }
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float ms = exp_shift(m);
     if (P.out[0].p) {
         RegSrc src{z};
 #pragma unroll 1
@@ -525,7 +526,7 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
             src.load(kc, v);
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                v[j] = exp_of<kF32>(v[j], m);
+                v[j] = exp_of<kF32>(v[j], ms);
                 sum[j % 4] += v[j];
             }
             // rows are padded to whole chunks, so every chunk is stored whole
@@ -541,7 +542,7 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j) sum[j % 4] += exp_of<kF32>(z[j], m);
+        for (int j = 0; j < BN / 2; ++j) sum[j % 4] += exp_of<kF32>(z[j], ms);
     }
     if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] =
         make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));

@@ -131,7 +131,7 @@ __device__ __forceinline__ void finish(const OpsStream& P, float (&part)[kParts]
             float m = z;
 #pragma unroll
             for (int o = R / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(tc::kFullMask, m, o));
-            const float e = kF32 ? expf(z - m) : ex2((z - m) * kLog2e);
+            const float ms = exp_shift(m), e = kF32 ? expf(z - ms) : ex2((z - ms) * kLog2e);
             float s = e;
 #pragma unroll
             for (int o = R / 2; o; o >>= 1) s += __shfl_xor_sync(tc::kFullMask, s, o);

@@ -3,6 +3,8 @@ masked logits.
 
 Bounds as in test_ops.py, whose plain fp64 forms are used.
 """
+import math
+
 import pytest
 import torch
 
@@ -82,3 +84,46 @@ def test_vocab_loss_masked_blocks(tokens, value, dtype):
     x, w, t, coef, mask, kept = masked_inputs(tokens, DT[dtype], 40 + tokens)
     w[mask, 0] = torch.finfo(torch.bfloat16).min if value == "lowest" else value
     check_masked(x, w, t, coef, mask, kept)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,tokens", [("bf16", 3), ("bf16", 12), ("bf16", 40), ("bf16", 300), ("fp32", 3),
+                                          ("fp32", 12), ("fp32", 40), ("fp32", 300)])
+def test_vocab_loss_infinitely_masked_blocks(dtype, tokens):
+    """Logits of -inf: weights of -inf, or for the fp32 products that take a weight apart
+    (which such a weight turns into NaN) logits beyond the range."""
+    x, w, t, coef, mask, kept = masked_inputs(tokens, DT[dtype], 50 + tokens)
+    apart = dtype == "fp32" and tokens > 16
+    if apart:
+        x[:, 0] = 4.0
+    w[mask, 0] = -3e38 if apart else -math.inf
+    check_masked(x, w, t, coef, mask, kept, grads=apart)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [3, 12, 40, 300])
+def test_vocab_loss_masked_by_the_lowest_fp32_value(tokens):
+    x, w, t, coef, mask, kept = masked_inputs(tokens, torch.float32, 40 + tokens)
+    w[mask, 0] = torch.finfo(torch.float32).min
+    check_masked(x, w, t, coef, mask, kept)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("tokens", [3, 12, 40])
+def test_vocab_loss_of_a_row_of_minus_infinity(tokens, dtype):
+    """A token without a finite logit has no softmax: NaN, and only in its row; none if it is ignored."""
+    dt = DT[dtype]
+    x, w, t, _ = loss_inputs(tokens, 64, 512, dt, 70 + tokens)
+    t[t < 0] = 5
+    x[:, 0] = 0.0
+    x[1] = 0.0
+    x[1, 0] = 16.0
+    w[:, 0] = -3e38
+    bad = torch.arange(tokens, device="cuda") == 1
+    loss, lse, dx, dw = pkg.vocab_loss_grad(x, w, t)
+    assert torch.equal(loss.isnan(), bad) and lse[1] == -math.inf and torch.isfinite(lse[~bad]).all()
+    assert dx[1].isnan().all() and torch.isfinite(dx[~bad]).all()
+    t[1] = -100
+    loss, lse, dx, dw = pkg.vocab_loss_grad(x, w, t)
+    assert loss[1] == 0 and not dx[1].any() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
