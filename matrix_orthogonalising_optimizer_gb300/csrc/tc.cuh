@@ -237,9 +237,11 @@ __device__ __forceinline__ bool all_plain(const float (&v)[N]) {
 // The leading bf16 parts of the values, in the words' upper halves; v becomes
 // what is left over, so three calls take fp32 values apart exactly.  Rounded half
 // up, by integer addition (conversions issue at a quarter of the rate).  `plain`:
-// all_plain() held before the first call.  Else values that would round to
-// infinity are cut off instead, and an infinity or NaN stays one and leaves
-// nothing, so that the parts do not turn into inf - inf.
+// all_plain() held before the first call.  Else every part is cut off instead of
+// rounded (as exact: 3 x 8 bits), so that neither a part nor the sum of the leading
+// ones exceeds the value, which next to the largest one would be infinite, and an
+// infinity or NaN stays one and leaves nothing, so that the parts do not turn into
+// inf - inf.
 template <int N>
 __device__ __forceinline__ void bf16_parts(float (&v)[N], uint32_t (&h)[N], bool plain) {
     if (plain) {
@@ -253,8 +255,7 @@ __device__ __forceinline__ void bf16_parts(float (&v)[N], uint32_t (&h)[N], bool
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const uint32_t b = __float_as_uint(v[j]), mag = b & 0x7fffffffu;
-        h[j] = (b + 0x8000u) & 0xffff0000u;
-        if (mag >= 0x7f7f8000u) h[j] = (b & 0xffff0000u) | (mag > 0x7f800000u ? 0x00400000u : 0u);
+        h[j] = (b & 0xffff0000u) | (mag > 0x7f800000u ? 0x00400000u : 0u);
         v[j] = mag >= 0x7f800000u ? 0.0f : v[j] - __uint_as_float(h[j]);
     }
 }

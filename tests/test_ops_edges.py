@@ -127,3 +127,24 @@ def test_vocab_loss_of_a_row_of_minus_infinity(tokens, dtype):
     t[1] = -100
     loss, lse, dx, dw = pkg.vocab_loss_grad(x, w, t)
     assert loss[1] == 0 and not dx[1].any() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("tokens", [12, 40])
+def test_products_of_the_largest_fp32_value(tokens, sign):
+    """1 times the largest fp32 value is that value, whichever kernel multiplies."""
+    big = sign * torch.finfo(torch.float32).max
+    x = torch.zeros(tokens, 64, device="cuda")
+    w = torch.zeros(300, 64, device="cuda")
+    x[:, 0] = 1.0
+    w[:, 0] = big
+    _, lse = pkg.vocab_loss(x, w, torch.zeros(tokens, dtype=torch.int64, device="cuda"))
+    assert (lse == big).all()
+    # and where it shares its 16-byte group with other values, these stay exact to fp32
+    w = torch.randn(300, 64, generator=gen(8), device="cuda")
+    w[:, 0] = big
+    x = torch.randn(tokens, 64, generator=gen(9), device="cuda")
+    x[:, 0] = 0.0
+    t = torch.randint(0, 300, (tokens,), generator=gen(10), device="cuda")
+    check_loss(x, w * (torch.arange(64, device="cuda") > 0), t, None, pkg.vocab_loss(x, w, t))
