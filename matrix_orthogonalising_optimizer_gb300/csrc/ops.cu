@@ -458,8 +458,11 @@ constexpr int kRowThreads = 256;
 // lse = M + log sum_b s_b exp(m_b - M) in a fixed order (blocks without a finite
 // logit have s_b = 0, a row without one lse = -inf and a NaN loss and gradient); the first writes the
 // loss, and each turns its share of the row's exponentials e = exp(z - m_b)
-// into logit gradients dz = c e exp(m_b - lse), the target's as c expm1(z_t -
-// lse), which keeps the digits of p - 1 where p is near 1.  Memory-bound: 4
+// into logit gradients dz = c e exp(m_b - M) / S with S the sum, the target's as
+// c expm1(-loss), so that p and 1 are not subtracted (what is left is the rounding
+// of S, about 2^-23 of 1).  The loss is (M - z_t) + log S: lse itself loses log S
+// where |M| is large (all of it for a row of equal masked logits), and with it the
+// loss and every p.  Memory-bound: 4
 // bytes per bf16 logit, in place.
 template <bool kF32>
 __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_constant__ LossRowArgs a) {
@@ -491,17 +494,18 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
     s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kRowThreads / 32; ++w) s += red[w];
-    const float lse = m + logf(s);
+    const float ls = logf(s);
     const int64_t t = a.targets[row];
     const bool ignored = t == a.ignore;
     const bool valid = !ignored && t >= 0 && t < a.vocab;
-    const float nll = valid ? lse - a.target_logit[row] : 0.0f;
+    const float nll = valid ? (m - a.target_logit[row]) + ls : 0.0f;
     if (blockIdx.y == 0 && tid == 0) {
-        a.lse[row] = lse;
+        a.lse[row] = m + ls;
         a.loss[row] = valid || ignored ? nll : __int_as_float(0x7fc00000);
     }
     if (!a.e) return;
     const float c = valid ? (a.coef ? a.coef[row] : 1.0f) : 0.0f;
+    const float cs = c / s;
     const int tg = valid ? static_cast<int>(t >> 3) : -1, tk = static_cast<int>(t & 7);  // the target's group, place
     const int g0 = blockIdx.y * a.seg_groups, g1 = min(a.groups, g0 + a.seg_groups);
     for (int g = g0 + tid; g < g1; g += kRowThreads) {
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = 0.0f;
         } else {
-            const float scale = c * expf(st[c0 >> a.shift].x - lse);
+            const float scale = cs * expf(st[c0 >> a.shift].x - ms);
             if (kF32) {
                 const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.e) + off);
                 const float4 x = p[0], y = p[1];

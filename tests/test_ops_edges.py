@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import matrix_orthogonalising_optimizer_gb300 as pkg
-from test_ops import U, check_loss, gen, loss_inputs, randn, within
+from test_ops import FN, U, check_loss, gen, loss_inputs, randn, within
 
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
 
@@ -148,3 +148,30 @@ def test_products_of_the_largest_fp32_value(tokens, sign):
     x[:, 0] = 0.0
     t = torch.randint(0, 300, (tokens,), generator=gen(10), device="cuda")
     check_loss(x, w * (torch.arange(64, device="cuda") > 0), t, None, pkg.vocab_loss(x, w, t))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [-1e10, -1e30, 1e4, 1e10, "lowest"])
+@pytest.mark.parametrize("tokens", [3, 12, 40])
+def test_vocab_loss_of_a_wholly_masked_row(tokens, value, dtype):
+    """A token whose logits are all the same, far from zero: the loss is log(vocab) and the
+    probabilities are 1 / vocab, although lse itself cannot hold log(vocab) beside them."""
+    dt = DT[dtype]
+    v = 512
+    x, w, t, _ = loss_inputs(tokens, 64, v, dt, 60 + tokens)
+    t[t < 0] = 5
+    x[:, 0] = 0.0
+    x[1] = 0.0
+    x[1, 0] = 1.0
+    w[:, 0] = torch.finfo(dt).min if value == "lowest" else value
+    loss, lse, dx, dw = pkg.vocab_loss_grad(x, w, t)
+    assert float((loss[1] - math.log(v)).abs()) <= FN * math.log(v)
+    assert float((lse[1].double() - w[0, 0].double()).abs()) <= 2.0 ** -23 * float(w[0, 0].abs()) + math.log(v) + 1e-3
+    # the gradient of feature 0 of the weights is this token's alone: x is 0 there in the others
+    p = torch.full((v,), 1.0 / v, device="cuda", dtype=torch.double)
+    p[t[1]] -= 1
+    within(dw[:, 0], p, (2 * U[dt] + U[dt] ** 2 + FN + 2.0 ** -12 * (dt == torch.bfloat16)) * p.abs(), "dweight")
+    # the other tokens
+    rest = torch.arange(tokens, device="cuda") != 1
+    check_loss(x[rest], w * (torch.arange(64, device="cuda") > 0), t[rest], None, (loss[rest], lse[rest]))
