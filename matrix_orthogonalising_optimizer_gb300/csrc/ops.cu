@@ -46,7 +46,8 @@ constexpr int kLongSum = 2048, kLongChain = 512;
 // Up to this many bf16 tokens the logit gradients are kept in two bf16 parts: in one,
 // the target's rounding, most of a token's gradient, is off by up to 2^-8, and a few
 // tokens do not average that out (3 tokens, 64 x 5169: error of dW 2.8e-3 against
-// 1.7e-3 of the result's own rounding).  The parts are rows of one product for dx,
+// 1.7e-3 of the result's own rounding).  More tokens do where their roundings differ,
+// which the coefficients' common factor sees to (common_factor).  The parts are rows of one product for dx,
 // which reads W once, and two part products of dW (3 tokens, 4096 x 131072: 687 us
 // with one part, 690 with two, 961 with W read for each).
 constexpr int kPartTokens = 32;
@@ -71,12 +72,55 @@ struct Arena {
     }
 };
 
-// Zeroes a launch's counters: n ints, a multiple of 64, at 256 bytes.  A kernel
-// rather than a memset, so that the GEMM launched after it as a programmatic
-// dependent sets up its barriers and tensor memory meanwhile.
-__global__ void __launch_bounds__(1024) zero_kernel(int4* p, int n) {
+// The coefficients of a call's tokens and where their common factor goes.
+struct CoefArgs {
+    const float* coef;  // NULL: nothing to do
+    const int64_t* targets;
+    int64_t n, ignore, vocab;
+    float* factor;
+};
+
+// The factor, in [1, 2), that is left out of the logit gradients' bf16 values and
+// multiplied into the products' sums: the significand of the largest coefficient
+// that counts.  With the usual one coefficient for all tokens what is left is a
+// power of two, which adds no rounding; left in, its rounding is the same in every
+// token's target, most of a token's gradient, so that no number of tokens averages
+// it out (1 / 255 is off by 2^-8: error of dx and dW 4.1e-3 at 255 tokens, 256 x
+// 5169, untrained; now 1.7e-3, that of the results' own rounding).  What is left is
+// the rounding of 1 - p: 2.0e-3 in all where the tokens' p differ, 2.2e-3 where all
+// p are near 1 / 500.  A significand, not the coefficient, so that dz keeps its
+// range; a maximum, so that no order matters.
+__device__ __forceinline__ void common_factor(const CoefArgs& c) {
+    __shared__ uint32_t red[32];
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < c.n; i += 1024) {
+        const int64_t t = c.targets[i];
+        const uint32_t b = __float_as_uint(c.coef[i]) & 0x7fffffffu;
+        if (t != c.ignore && t >= 0 && t < c.vocab && b < 0x7f800000u) top = max(top, b);
+    }
+    top = __reduce_max_sync(tc::kFullMask, top);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        top = __reduce_max_sync(tc::kFullMask, red[threadIdx.x]);
+        // no normal coefficient: 1
+        if (threadIdx.x == 0) *c.factor = __uint_as_float(0x3f800000u | (top < 0x00800000u ? 0u : top & 0x7fffffu));
+    }
+}
+
+// Zeroes a launch's counters: n ints, a multiple of 64, at 256 bytes; a further
+// block finds the coefficients' common factor.  A kernel rather than a memset, so
+// that the GEMM launched after it as a programmatic dependent sets up its barriers
+// and tensor memory meanwhile.
+__global__ void __launch_bounds__(1024) zero_kernel(int4* p, int n, const __grid_constant__ CoefArgs c) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = blockIdx.x * 1024 + threadIdx.x; i < n / 4; i += gridDim.x * 1024) p[i] = make_int4(0, 0, 0, 0);
+    const int blocks = gridDim.x - (c.coef ? 1 : 0);
+    if (static_cast<int>(blockIdx.x) == blocks) {
+        common_factor(c);
+        return;
+    }
+    for (int i = blockIdx.x * 1024 + threadIdx.x; i < n / 4; i += blocks * 1024) p[i] = make_int4(0, 0, 0, 0);
 }
 
 // Counters and partial sums of a call's GEMM launches.
@@ -95,8 +139,9 @@ struct Common {
         l.partials = partials;
     }
     // Zeroes the counters that the scheduled launches use (none where every
-    // unit is some pair's first and no tile is split).
-    cudaError_t clear(const OpsLaunch* l, int launches, int pairs, cudaStream_t s) const {
+    // unit is some pair's first and no tile is split), and finds the
+    // coefficients' common factor where there are some.
+    cudaError_t clear(const OpsLaunch* l, int launches, int pairs, const CoefArgs& coef, cudaStream_t s) const {
         int64_t ints = 0;
         for (int i = 0; i < launches; ++i) {
             bool split = false;
@@ -104,9 +149,9 @@ struct Common {
             if (split) ints = kMaxLaunches * 64 + (i + 1) * kTailInts;
             else if (l[i].total_units > pairs) ints = std::max<int64_t>(ints, (i + 1) * 64);
         }
-        if (ints == 0) return cudaSuccess;
-        zero_kernel<<<static_cast<int>(ceil_div(ints, 4096)), 1024, 0, s>>>(reinterpret_cast<int4*>(counters),
-                                                                         static_cast<int>(ints));
+        const int blocks = static_cast<int>(ceil_div(ints, 4096)) + (coef.coef ? 1 : 0);
+        if (blocks == 0) return cudaSuccess;
+        zero_kernel<<<blocks, 1024, 0, s>>>(reinterpret_cast<int4*>(counters), static_cast<int>(ints), coef);
         return cudaGetLastError();
     }
 };
@@ -303,13 +348,13 @@ cudaError_t launch(const OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s) {
 // Schedules a call's launches (`logits`: the first computes logits) and zeroes the
 // counters they need.
 int schedule(OpsLaunch* l, int launches, const Common& common, bool f32, bool logits, int pairs,
-             cudaStream_t s, const char* where) {
+             cudaStream_t s, const char* where, const CoefArgs& coef = {}) {
     for (int i = 0; i < launches; ++i) {
         l[i].chain = f32 ? kChainF32 : logits && i == 0 ? kChain : kLongChain;
         common.bind(l[i], i);
         ops_schedule(l[i], pairs, kSlots, kTails);
     }
-    OPS_CUDA(common.clear(l, launches, pairs, s));
+    OPS_CUDA(common.clear(l, launches, pairs, coef, s));
     return DMUON_OK;
 }
 
@@ -440,6 +485,7 @@ struct LossRowArgs {
     const float* target_logit;  // [rows]
     const int64_t* targets;
     const float* coef;          // NULL: 1
+    const float* factor;        // left out of dz, NULL: 1
     float* loss;
     float* lse;
     const void* e;              // exponentials (16-bit codes or fp32), NULL: losses only
@@ -504,7 +550,8 @@ __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_cons
         a.loss[row] = valid || ignored ? nll : __int_as_float(0x7fc00000);
     }
     if (!a.e) return;
-    const float c = valid ? (a.coef ? a.coef[row] : 1.0f) : 0.0f;
+    float c = valid ? (a.coef ? a.coef[row] : 1.0f) : 0.0f;
+    if (a.factor) c /= *a.factor;
     const float cs = c / s;
     const int tg = valid ? static_cast<int>(t >> 3) : -1, tk = static_cast<int>(t & 7);  // the target's group, place
     const int g0 = blockIdx.y * a.seg_groups, g1 = min(a.groups, g0 + a.seg_groups);
@@ -574,6 +621,7 @@ struct LossLayout {
     void* e = nullptr;         // exponentials (bf16: in dz's buffer)
     float2* stats = nullptr;
     float* target_logit = nullptr;
+    float* factor = nullptr;   // bf16, one part: left out of dz
     float* dx_sum = nullptr;   // bf16, two parts: fp32 dx of each part
     float* dw_sum = nullptr;   // fp32 sum of dW over pieces (bf16, more than one piece)
     int64_t piece = 0, pieces = 0;  // tokens per piece
@@ -607,6 +655,7 @@ struct LossLayout {
         if (grad) {
             dz = scratch(a, piece, v, f32 ? kF32Parts : n <= kPartTokens ? 2 : 1, 16);
             e = f32 ? static_cast<void*>(a.take<float>(piece * ld)) : const_cast<void*>(dz.p);
+            if (!f32 && dz.parts == 1) factor = a.take<float>(1);
             if (!f32 && dz.parts > 1) dx_sum = a.take<float>(2 * n * up(d, 4));
             if (!f32 && pieces > 1) dw_sum = a.take<float>(v * up(d, 4));
         }
@@ -829,6 +878,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
     int pairs = 0;
     OPS_CUDA(ops_pairs(&pairs));
     const int64_t es = f32 ? 4 : 2;
+    float* factor = coef ? L.factor : nullptr;  // all coefficients 1: as it is
     for (int64_t i = 0; i < L.pieces; ++i) {
         const int64_t r0 = i * L.piece, n = std::min(L.piece, tokens - r0);
         const Operand xp = rows_of(L.x, r0, n), dz = rows_of(L.dz, 0, n);
@@ -867,8 +917,11 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             const bool last = i + 1 == L.pieces;
             W.out[0] = last ? user_mat(dweight, dim, f32) : sum;
             if (i > 0) W.in[0] = sum;
+            l[1].p[0].scale = l[1].p[1].scale = factor;
         }
-        OPS_TRY(schedule(l, 2, L.common, f32, true, pairs, s, where));
+        CoefArgs first = {};
+        if (factor && i == 0) first = CoefArgs{coef, targets, tokens, ignore_index, vocab, factor};
+        OPS_TRY(schedule(l, 2, L.common, f32, true, pairs, s, where, first));
         if (i == 0) OPS_CUDA(L.pack.run(s));
         if (L.stream) {
             OpsStream a = stream_args(static_cast<const char*>(x) + r0 * dim * es, weight, n, vocab, dim);
@@ -886,6 +939,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         a.target_logit = L.target_logit;
         a.targets = targets + r0;
         a.coef = coef ? coef + r0 : nullptr;
+        a.factor = factor;
         a.loss = loss + r0;
         a.lse = lse + r0;
         a.ignore = ignore_index;

@@ -80,6 +80,7 @@ struct OpsProblem {
     OpsMat out[4];  // STORE: D | GATE: h, act, u act', h again | DGATE: da, du | LOGITS: exponentials
                     // (fp32, or 16-bit codes, rows padded to whole 16-column chunks)
     OpsMat in[2];   // STORE: in[0] = addend (fp32) | DGATE: u act', act
+    const float* scale;       // STORE: the sums' factor (the addend is not scaled), NULL: 1
     float2* stats;            // LOGITS: [M][nblk] (max, sum of exp) of 128-column blocks
     int32_t nblk;
     float* target_logit;      // LOGITS: [M]

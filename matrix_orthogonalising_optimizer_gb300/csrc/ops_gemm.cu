@@ -391,12 +391,15 @@ struct RegSrc {
 template <bool kF32, typename Src>
 __device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
                                           float* stg) {
+    const float scale = P.scale ? *P.scale : 1.0f;
 #pragma unroll 1
     for (int kc = 0; kc < P.bn / 32; ++kc) {
         const int c0 = first_col<OPS_STORE>(P.bn, u.tn, half) + kc * CH;
         if (c0 >= P.N) break;
         float v[CH];
         acc.load(kc, v);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) v[j] *= scale;
         if (P.in[0].p) {
             float add[CH];
             ld_issue(P.in[0], r0, c0, lane, add, P.M, P.N, stg);

@@ -1,5 +1,5 @@
 """Edges of the training operators: schedules of many short units, rows of huge values,
-masked logits.
+masked logits, coefficients.
 
 Bounds as in test_ops.py, whose plain fp64 forms are used.
 """
@@ -175,3 +175,46 @@ def test_vocab_loss_of_a_wholly_masked_row(tokens, value, dtype):
     # the other tokens
     rest = torch.arange(tokens, device="cuda") != 1
     check_loss(x[rest], w * (torch.arange(64, device="cuda") > 0), t[rest], None, (loss[rest], lse[rest]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("coefs", ["1.005", "1/n", "mixed"])
+@pytest.mark.parametrize("tokens,budget", [(33, 0), (255, 0), (509, 0), (509, 1), (1021, 0)])
+def test_vocab_loss_grad_of_equal_coefficients(tokens, budget, coefs):
+    """One coefficient for all tokens, halfway between two bf16 values: its rounding, the same
+    in every token's gradient, would not average out.  The bound is that of a few tokens."""
+    g = torch.Generator(device="cuda").manual_seed(32)
+    x = torch.randn(tokens, 1024, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(1000, 1024, generator=g, device="cuda") * 0.001).bfloat16()
+    targets = torch.arange(tokens, device="cuda") * 7 % 1000
+    coef = torch.full((tokens,), 1.0 / tokens if coefs == "1/n" else 1.005, device="cuda")
+    if coefs == "mixed":  # powers of two apart, some negative, some zero; a NaN where nothing counts
+        coef *= 2.0 ** (torch.arange(tokens, device="cuda") % 5) * (1 - 2 * (torch.arange(tokens, device="cuda") % 2))
+        coef[::9] = 0.0
+        coef[4] = math.nan
+        targets[4] = -100
+    _, _, dx, dw = pkg.vocab_loss_grad(x, w, targets, coef=coef, budget=budget)
+    dz = torch.softmax(x.double() @ w.double().T, 1)
+    dz.scatter_add_(1, targets.clamp(min=0)[:, None], -torch.ones(tokens, 1, device="cuda", dtype=torch.double))
+    dz *= torch.where(targets >= 0, coef, torch.zeros_like(coef)).double()[:, None]
+    for got, want in ((dx, dz @ w.double()), (dw, dz.T @ x.double())):
+        assert float((got.double() - want).norm() / want.norm()) <= 1.05 * 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -12
+
+
+@pytest.mark.gpu
+def test_vocab_loss_grad_unusual_coefficients():
+    x, w, t, _ = loss_inputs(60, 72, 500, torch.bfloat16, 33)
+    zero = torch.zeros(60, device="cuda")
+    _, _, dx, dw = pkg.vocab_loss_grad(x, w, t, coef=zero)
+    assert not dx.any() and not dw.any()
+    for c in (1e-38, 1e-20, 2.0 ** 100):  # dz keeps the range of the coefficients
+        coef = torch.full((60,), c, device="cuda")
+        check_loss(x, w, t, coef, pkg.vocab_loss_grad(x, w, t, coef=coef))
+    # an infinite coefficient stays in its token's dx
+    inf = torch.full((60,), 0.5, device="cuda")
+    inf[2] = math.inf
+    t[2] = 3
+    _, _, dx, _ = pkg.vocab_loss_grad(x, w, t, coef=inf)
+    ref = pkg.vocab_loss_grad(x, w, t, coef=torch.full((60,), 0.5, device="cuda"))[2]
+    rest = torch.arange(60, device="cuda") != 2
+    assert not torch.isfinite(dx[2]).any() and torch.equal(dx[rest], ref[rest])
