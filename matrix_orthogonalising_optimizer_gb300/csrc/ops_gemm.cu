@@ -638,24 +638,13 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                     }
                     __syncwarp();
                 } else {
-                    // The first unit is known without the leader's word, which is
-                    // waited for, and its slot released, before the second unit.
-                    // Without that wait slot 0's barrier could still be in its first
-                    // phase at unit kTileRing, where the parity of the second reads
-                    // as complete: nothing orders the leader's sends to different
-                    // slots.  A release before the wait would let the leader send
-                    // twice, and the wait would miss the first phase.
-                    if (k == 0) {
-                        t = t_next;
-                    } else {
-                        t = 0;
-                        for (int j = k == 1 ? 0 : k; j <= k && t < total; ++j) {
-                            t = __shfl_sync(
-                                kFullMask, wait_tile(S.tile_full, S.tile_slot, j, &g_ops_status, total), 0);
-                            if (lane == 0) release_tile(S.tile_empty, j);
-                            __syncwarp();
-                        }
-                    }
+                    // every unit in turn, the first too: slot 0's barrier must be past
+                    // its first phase before unit kTileRing is looked for there, where
+                    // the parity of the second reads as complete until then
+                    t = wait_tile(S.tile_full, S.tile_slot, k, &g_ops_status, total);
+                    t = __shfl_sync(kFullMask, t, 0);
+                    if (lane == 0) release_tile(S.tile_empty, k);
+                    __syncwarp();
                 }
                 if (t >= total) {
                     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
