@@ -357,9 +357,13 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const __grid_cons
 
 // ------------------------------------------------ ring kernels
 
+using dmuon::tc::add2;
+using dmuon::tc::both;
+using dmuon::tc::fma2;
 using dmuon::tc::mbar_expect_tx;
 using dmuon::tc::mbar_init;
 using dmuon::tc::mbar_wait;
+using dmuon::tc::mul2;
 using dmuon::tc::saddr;
 
 constexpr int kMaxStages = 3;
@@ -371,36 +375,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(saddr(bar))
                  : "memory");
 }
-
-// Pairs of fp32 values in one instruction.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
-        "mov.b64 {%0, %1}, z;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
-        "mov.b64 {%0, %1}, z;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 template <typename T>
 __device__ __forceinline__ void unpack2(const uint4& q, float2 (&v)[kVec<T> / 2]) {

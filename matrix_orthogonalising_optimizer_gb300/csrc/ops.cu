@@ -109,18 +109,22 @@ __device__ __forceinline__ void common_factor(const CoefArgs& c) {
     }
 }
 
-// Zeroes a launch's counters: n ints, a multiple of 64, at 256 bytes; a further
-// block finds the coefficients' common factor.  A kernel rather than a memset, so
-// that the GEMM launched after it as a programmatic dependent sets up its barriers
-// and tensor memory meanwhile.
-__global__ void __launch_bounds__(1024) zero_kernel(int4* p, int n, const __grid_constant__ CoefArgs c) {
+// Zeroes a launch's counters: n ints, a multiple of 64, at 256 bytes.  A kernel
+// rather than a memset, so that the GEMM launched after it as a programmatic
+// dependent sets up its barriers and tensor memory meanwhile.
+__global__ void __launch_bounds__(1024) zero_kernel(int4* p, int n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int blocks = gridDim.x - (c.coef ? 1 : 0);
-    if (static_cast<int>(blockIdx.x) == blocks) {
+    for (int i = blockIdx.x * 1024 + threadIdx.x; i < n / 4; i += gridDim.x * 1024) p[i] = make_int4(0, 0, 0, 0);
+}
+
+// The same, and the last block finds the coefficients' common factor.
+__global__ void __launch_bounds__(1024) zero_factor_kernel(int4* p, int n, const __grid_constant__ CoefArgs c) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x + 1 == gridDim.x) {
         common_factor(c);
         return;
     }
-    for (int i = blockIdx.x * 1024 + threadIdx.x; i < n / 4; i += blocks * 1024) p[i] = make_int4(0, 0, 0, 0);
+    for (int i = blockIdx.x * 1024 + threadIdx.x; i < n / 4; i += (gridDim.x - 1) * 1024) p[i] = make_int4(0, 0, 0, 0);
 }
 
 // Counters and partial sums of a call's GEMM launches.
@@ -149,9 +153,10 @@ struct Common {
             if (split) ints = kMaxLaunches * 64 + (i + 1) * kTailInts;
             else if (l[i].total_units > pairs) ints = std::max<int64_t>(ints, (i + 1) * 64);
         }
-        const int blocks = static_cast<int>(ceil_div(ints, 4096)) + (coef.coef ? 1 : 0);
-        if (blocks == 0) return cudaSuccess;
-        zero_kernel<<<blocks, 1024, 0, s>>>(reinterpret_cast<int4*>(counters), static_cast<int>(ints), coef);
+        int4* p = reinterpret_cast<int4*>(counters);
+        const int n = static_cast<int>(ints), blocks = static_cast<int>(ceil_div(ints, 4096));
+        if (coef.coef) zero_factor_kernel<<<blocks + 1, 1024, 0, s>>>(p, n, coef);
+        else if (ints > 0) zero_kernel<<<blocks, 1024, 0, s>>>(p, n);
         return cudaGetLastError();
     }
 };
@@ -917,7 +922,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
             const bool last = i + 1 == L.pieces;
             W.out[0] = last ? user_mat(dweight, dim, f32) : sum;
             if (i > 0) W.in[0] = sum;
-            l[1].p[0].scale = l[1].p[1].scale = factor;
+            l[1].scale = factor;
         }
         CoefArgs first = {};
         if (factor && i == 0) first = CoefArgs{coef, targets, tokens, ignore_index, vocab, factor};
@@ -960,7 +965,7 @@ extern "C" int dmuon_vocab_loss(const void* x, const void* weight, const int64_t
         }
         const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(segs));
         OPS_CUDA(launch_dependent(f32 ? loss_row_kernel<true> : loss_row_kernel<false>, grid, kRowThreads, s, a));
-        if (grad) OPS_CUDA(launch(l[1], OPS_STORE, f32, s));
+        if (grad) OPS_CUDA(launch(l[1], factor ? OPS_STORE_SCALED : OPS_STORE, f32, s));
         if (L.dx_sum)
             OPS_CUDA(launch_dependent(add_parts_kernel,
                                       dim3(static_cast<unsigned>(ceil_div(dim, 256)), static_cast<unsigned>(n)), 256, s,

@@ -41,7 +41,8 @@ constexpr int kOpsMaxSegs = 12;
 // six part products above 2^-24 of the whole, the smallest first.
 constexpr int kF32Parts = 3;
 
-enum OpsEpi : int32_t { OPS_STORE = 0, OPS_GATE = 1, OPS_DGATE = 2, OPS_LOGITS = 3 };
+enum OpsEpi : int32_t { OPS_STORE = 0, OPS_GATE = 1, OPS_DGATE = 2, OPS_LOGITS = 3, OPS_STORE_SCALED = 4 };
+constexpr int kOpsKinds = 5;
 enum OpsAct : int32_t { OPS_SILU = 0, OPS_GELU = 1 };
 
 // A row-major matrix an epilogue reads or writes.
@@ -77,10 +78,9 @@ struct OpsProblem {
     int32_t slot_begin;  // first partial-sum slot
     // epilogue
     int32_t act;
-    OpsMat out[4];  // STORE: D | GATE: h, act, u act', h again | DGATE: da, du | LOGITS: exponentials
+    OpsMat out[4];  // STORE, STORE_SCALED: D | GATE: h, act, u act', h again | DGATE: da, du | LOGITS: exponentials
                     // (fp32, or 16-bit codes, rows padded to whole 16-column chunks)
     OpsMat in[2];   // STORE: in[0] = addend (fp32) | DGATE: u act', act
-    const float* scale;       // STORE: the sums' factor (the addend is not scaled), NULL: 1
     float2* stats;            // LOGITS: [M][nblk] (max, sum of exp) of 128-column blocks
     int32_t nblk;
     float* target_logit;      // LOGITS: [M]
@@ -94,6 +94,7 @@ struct OpsLaunch {
     int32_t* counter;      // unit counter, zero at launch
     int32_t* tail_count;   // arrivals per (split tile, CTA rank, epilogue warp), zero at launch
     float* partials;       // split tiles' partial sums
+    const float* scale;    // STORE_SCALED: the sums' factor (the addend is not scaled)
 };
 
 // Product of a few rows x (tokens x K) with weight rows (N x K, twice for the

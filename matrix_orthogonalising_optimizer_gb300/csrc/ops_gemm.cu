@@ -388,18 +388,20 @@ struct RegSrc {
 // inlined per output and unrolled, spent 6 to 11 us per fp32 chunk on
 // instruction fetches.
 
-template <bool kF32, typename Src>
-__device__ __forceinline__ void epi_store(const OpsProblem& P, Src acc, const Unit& u, int half, int r0, int lane,
-                                          float* stg) {
-    const float scale = P.scale ? *P.scale : 1.0f;
+template <bool kScaled, typename Src>
+__device__ __forceinline__ void epi_store(const OpsProblem& P, const float* factor, Src acc, const Unit& u, int half,
+                                          int r0, int lane, float* stg) {
+    const float scale = kScaled ? *factor : 1.0f;
 #pragma unroll 1
     for (int kc = 0; kc < P.bn / 32; ++kc) {
         const int c0 = first_col<OPS_STORE>(P.bn, u.tn, half) + kc * CH;
         if (c0 >= P.N) break;
         float v[CH];
         acc.load(kc, v);
+        if constexpr (kScaled) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) v[j] *= scale;
+            for (int j = 0; j < CH; ++j) v[j] *= scale;
+        }
         if (P.in[0].p) {
             float add[CH];
             ld_issue(P.in[0], r0, c0, lane, add, P.M, P.N, stg);
@@ -489,9 +491,17 @@ __device__ __forceinline__ void epi_dgate(const OpsProblem& P, Src acc, const Un
 // exp(z - m).  The difference is taken before it is scaled: in z log2(e) - m log2(e),
 // one FMA, the rounding of m log2(e) stays as an error of the exponent, and at
 // |m| of 10^10 (masked logits) the maximum's own exponential became infinite.
+// Two at a time: the subtraction and the scaling then cost what the FMA did.
 template <bool kF32>
-__device__ __forceinline__ float exp_of(float z, float m) {
-    return kF32 ? expf(z - m) : ex2((z - m) * kLog2e);
+__device__ __forceinline__ void exp_pair(float& a, float& b, float m) {
+    if constexpr (kF32) {
+        a = expf(a - m);
+        b = expf(b - m);
+    } else {
+        const float2 t = mul2(add2(make_float2(a, b), both(-m)), both(kLog2e));
+        a = ex2(t.x);
+        b = ex2(t.y);
+    }
 }
 
 template <bool kF32>
@@ -528,9 +538,10 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
             float v[CH];
             src.load(kc, v);
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                v[j] = exp_of<kF32>(v[j], ms);
+            for (int j = 0; j < CH; j += 2) {
+                exp_pair<kF32>(v[j], v[j + 1], ms);
                 sum[j % 4] += v[j];
+                sum[j % 4 + 1] += v[j + 1];
             }
             // rows are padded to whole chunks, so every chunk is stored whole
             if constexpr (kF32) {
@@ -545,7 +556,11 @@ __device__ __forceinline__ void epi_logits(const OpsProblem& P, const Unit& u, i
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j) sum[j % 4] += exp_of<kF32>(z[j], ms);
+        for (int j = 0; j < BN / 2; j += 2) {
+            exp_pair<kF32>(z[j], z[j + 1], ms);
+            sum[j % 4] += z[j];
+            sum[j % 4 + 1] += z[j + 1];
+        }
     }
     if (r < P.M) P.stats[static_cast<int64_t>(r) * P.nblk + 2 * u.tn + half] =
         make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -847,7 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1) ops_gemm_kernel(const __grid_cons
                 ++it;
             }
             const auto finish = [&](auto acc) {
-                if constexpr (kKind == OPS_STORE) epi_store<kF32>(P, acc, u, half, r0, lane, stg);
+                if constexpr (kKind == OPS_STORE || kKind == OPS_STORE_SCALED)
+                    epi_store<kKind == OPS_STORE_SCALED>(P, L.scale, acc, u, half, r0, lane, stg);
                 else if constexpr (kKind == OPS_GATE) epi_gate<kF32>(P, acc, u, half, r0, lane, stg);
                 else if constexpr (kKind == OPS_DGATE) epi_dgate<kF32>(P, acc, u, half, r0, lane, stg);
                 else epi_logits<kF32>(P, u, half, r0, lane, acc.r, stg);
@@ -935,6 +951,8 @@ Kernel kernel_of(int32_t kind, bool f32) {
     switch (kind) {
         case OPS_STORE: return f32 ? ops_gemm_kernel<OPS_STORE, true> : ops_gemm_kernel<OPS_STORE, false>;
         case OPS_GATE: return f32 ? ops_gemm_kernel<OPS_GATE, true> : ops_gemm_kernel<OPS_GATE, false>;
+        case OPS_STORE_SCALED:
+            return f32 ? ops_gemm_kernel<OPS_STORE_SCALED, true> : ops_gemm_kernel<OPS_STORE_SCALED, false>;
         case OPS_DGATE: return f32 ? ops_gemm_kernel<OPS_DGATE, true> : ops_gemm_kernel<OPS_DGATE, false>;
         default: return f32 ? ops_gemm_kernel<OPS_LOGITS, true> : ops_gemm_kernel<OPS_LOGITS, false>;
     }
@@ -953,7 +971,7 @@ cudaError_t ops_pairs(int* pairs) {
     // per device with that device current
     return cache.get(dev, pairs, [&](int* out) {
         cudaError_t r = cudaSuccess;
-        for (int kind = 0; kind < 4 && r == cudaSuccess; ++kind)
+        for (int kind = 0; kind < kOpsKinds && r == cudaSuccess; ++kind)
             for (int f = 0; f < 2 && r == cudaSuccess; ++f)
                 r = cudaFuncSetAttribute(kernel_of(kind, f != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSmemBytes));
