@@ -477,10 +477,10 @@ int dmuon_vocab_loss(const void* x, const void* weight, const int64_t* targets, 
                      int64_t dim, int64_t vocab, int32_t dtype, uint64_t budget, void* workspace,
                      size_t workspace_bytes, void* stream);
 
-/* Synchronous: DMUON_ERR_DEVICE_TIMEOUT if a wait inside a layer norm's, gated
- * block's or vocabulary loss's kernel on the current device gave up (about 2 s; its
- * outputs are then not complete) since the last call, else DMUON_OK; clears
- * the flag. */
+/* Waits for all streams of the current device, then DMUON_ERR_DEVICE_TIMEOUT if a
+ * wait inside a layer norm's, gated block's or vocabulary loss's kernel on it gave
+ * up (about 2 s; its outputs are then not complete) since the last call, else
+ * DMUON_OK; clears the flag.  Not during a stream's capture. */
 int dmuon_ops_status(void);
 
 #ifdef __cplusplus

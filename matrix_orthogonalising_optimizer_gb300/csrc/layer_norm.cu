@@ -965,12 +965,7 @@ int64_t partial_rows(int64_t rows) { return std::min<int64_t>(rows, kMaxPartials
 
 namespace dmuon {
 
-cudaError_t norm_read_status(int32_t* v) {
-    const int32_t zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(v, g_norm_status, sizeof(*v));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_norm_status, &zero, sizeof(zero));
-    return e;
-}
+cudaError_t norm_status_word(void** p) { return cudaGetSymbolAddress(p, g_norm_status); }
 
 }  // namespace dmuon
 

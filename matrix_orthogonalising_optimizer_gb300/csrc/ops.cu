@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "act.cuh"
 #include "dmuon.h"
@@ -672,6 +673,10 @@ bool loss_sizes_ok(int64_t n, int64_t d, int64_t v) {
     return in_range(n, 0, kMaxTokens) && in_range(d, 1, kMaxWidth) && in_range(v, 1, kMaxVocab);
 }
 
+// Reads and clears both time-out flags in one step, so that none set meanwhile is lost.
+__device__ int32_t g_taken;
+__global__ void take_status_kernel(int32_t* a, int32_t* b) { g_taken = atomicExch(a, 0) | atomicExch(b, 0); }
+
 // Rows [r0, r0 + n) of an operand.
 Operand rows_of(const Operand& o, int64_t r0, int64_t n) {
     Operand s = o;
@@ -686,10 +691,20 @@ Operand rows_of(const Operand& o, int64_t r0, int64_t n) {
 using namespace dmuon;
 
 extern "C" int dmuon_ops_status(void) {
-    int32_t v = 0, w = 0;
-    if (ops_read_status(&v) != cudaSuccess || norm_read_status(&w) != cudaSuccess)
-        return fail(DMUON_ERR_CUDA, "dmuon_ops_status: cannot read the status flags");
-    return v || w ? DMUON_ERR_DEVICE_TIMEOUT : DMUON_OK;
+    const char* where = "dmuon_ops_status";
+    static std::mutex one;  // g_taken serves one caller at a time
+    std::lock_guard<std::mutex> lock(one);
+    void *gemm = nullptr, *norm = nullptr;
+    OPS_CUDA(ops_status_word(&gemm));
+    OPS_CUDA(norm_status_word(&norm));
+    // every stream's calls: a copy alone would wait for the legacy stream and those
+    // that synchronise with it
+    OPS_CUDA(cudaDeviceSynchronize());
+    take_status_kernel<<<1, 1>>>(static_cast<int32_t*>(gemm), static_cast<int32_t*>(norm));
+    OPS_CUDA(cudaGetLastError());
+    int32_t v = 0;
+    OPS_CUDA(cudaMemcpyFromSymbol(&v, g_taken, sizeof(v)));
+    return v ? DMUON_ERR_DEVICE_TIMEOUT : DMUON_OK;
 }
 
 extern "C" size_t dmuon_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t hidden, int32_t dtype,

@@ -144,8 +144,8 @@ void ops_tile_columns(OpsShape* p, int n, int pairs);
 // resident CTA pairs; `slots` partial-sum slots are available.  Host only.
 void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails);
 cudaError_t ops_pairs(int* pairs);  // resident CTA pairs of the GEMM kernel on the current device
-cudaError_t ops_read_status(int32_t* v);  // reads and clears the GEMM's time-out flag
-cudaError_t norm_read_status(int32_t* v);  // the same of the layer norm's ring kernels
+cudaError_t ops_status_word(void** p);   // the GEMM's time-out flag on the current device
+cudaError_t norm_status_word(void** p);  // the same of the layer norm's ring kernels
 cudaError_t launch_ops_gemm(const OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s);
 
 }  // namespace dmuon

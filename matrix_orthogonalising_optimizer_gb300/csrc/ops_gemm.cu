@@ -1135,12 +1135,7 @@ void ops_schedule(OpsLaunch& l, int pairs, int slots, int tails) {
     l.total_units = unit;
 }
 
-cudaError_t ops_read_status(int32_t* v) {
-    const int32_t zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(v, g_ops_status, sizeof(*v));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_ops_status, &zero, sizeof(zero));
-    return e;
-}
+cudaError_t ops_status_word(void** p) { return cudaGetSymbolAddress(p, g_ops_status); }
 
 cudaError_t launch_ops_gemm(const OpsLaunch& l, int32_t kind, bool f32, cudaStream_t s) {
     if (l.total_units <= 0) return cudaSuccess;

@@ -93,7 +93,8 @@ def _space(workspace, need, device):
 
 
 def ops_status() -> int:
-    """Status of the operators' device-side waits on the current device (0 = fine); clears it."""
+    """Status of the operators' device-side waits on the current device (0 = fine), once all its
+    streams have finished; clears it."""
     return int(_lib.load().dmuon_ops_status())
 
 

@@ -1,5 +1,5 @@
 """Edges of the training operators: schedules of many short units, rows of huge values,
-masked logits, coefficients.
+masked logits, coefficients, status.
 
 Bounds as in test_ops.py, whose plain fp64 forms are used.
 """
@@ -218,3 +218,18 @@ def test_vocab_loss_grad_unusual_coefficients():
     ref = pkg.vocab_loss_grad(x, w, t, coef=torch.full((60,), 0.5, device="cuda"))[2]
     rest = torch.arange(60, device="cuda") != 2
     assert not torch.isfinite(dx[2]).any() and torch.equal(dx[rest], ref[rest])
+
+
+@pytest.mark.gpu
+def test_status_waits_for_every_stream():
+    x = torch.randn(64, 256, device="cuda")
+    side = torch.cuda.Stream()
+    pkg.layer_norm(x)  # what a first call loads is loaded
+    assert pkg.ops_status() == 0
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+    pkg.layer_norm(x, stream=side)
+    assert not side.query()
+    assert pkg.ops_status() == 0
+    assert side.query()
