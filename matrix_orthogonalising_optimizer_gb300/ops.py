@@ -87,8 +87,8 @@ def _space(workspace, need, device):
     """(pointer, bytes, tensor) of the caller's workspace, or of a new one of need() bytes."""
     if workspace is None:
         workspace = torch.empty(need(), dtype=torch.uint8, device=device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the device of the first argument")
     return workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), workspace
 
 

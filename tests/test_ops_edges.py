@@ -1,14 +1,16 @@
 """Edges of the training operators: schedules of many short units, rows of huge values,
-masked logits, coefficients, status.
+masked logits, coefficients, status, refusals.
 
 Bounds as in test_ops.py, whose plain fp64 forms are used.
 """
 import math
+from types import SimpleNamespace
 
 import pytest
 import torch
 
 import matrix_orthogonalising_optimizer_gb300 as pkg
+from matrix_orthogonalising_optimizer_gb300 import ops
 from test_ops import FN, U, check_loss, gen, loss_inputs, randn, within
 
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
@@ -233,3 +235,10 @@ def test_status_waits_for_every_stream():
     assert not side.query()
     assert pkg.ops_status() == 0
     assert side.query()
+
+
+def test_workspace_of_another_device_is_refused():
+    ws = SimpleNamespace(is_cuda=True, device=torch.device("cuda:1"), is_contiguous=lambda: True,
+                         data_ptr=lambda: 1 << 20, numel=lambda: 1 << 20, element_size=lambda: 1)
+    with pytest.raises(ValueError, match="workspace"):
+        ops._space(ws, lambda: 16, torch.device("cuda:0"))
