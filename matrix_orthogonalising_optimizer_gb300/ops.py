@@ -12,6 +12,10 @@ and a workspace that is not passed in are allocated on that stream, and the
 caller orders it after the work that produced the inputs.  ``workspace`` is a
 uint8 tensor of at least the bytes that the ``*_workspace`` function gives, to be
 reused from call to call on one stream.
+
+Autograd does not record these calls.  The forward functions refuse inputs that
+require gradients unless they are called under ``torch.no_grad()``; the gradients
+come from ``layer_norm_backward``, ``gated_ffn_backward`` and ``vocab_loss_grad``.
 """
 from __future__ import annotations
 
@@ -53,6 +57,16 @@ def _check(where, dev, dt, *tensors):
         if t is not None and not (t.is_cuda and t.dtype is dt and t.shape == shape and t.is_contiguous()
                                   and t.device == dev):
             _refuse(where, name, t, dt, shape, dev)
+
+
+def _no_graph(where, *tensors):
+    """Autograd does not see these calls: results cut off from a graph that is being
+    recorded would lose the inputs' gradients without a word."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{where}: an input requires gradients, but autograd does not record this call: make it "
+                                 "under torch.no_grad() and take the gradients from the functions that return them")
 
 
 def _elsewhere(stream, dev):
@@ -105,6 +119,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, stream=None):
     dt, dev, shape = x.dtype, x.device, x.shape
     cols = shape[-1]
     _check("layer_norm", dev, dt, ("x", x, shape), ("weight", weight, (cols,)), ("bias", bias, (cols,)))
+    _no_graph("layer_norm", x, weight, bias)
     rows = x.numel() // cols if cols else 0
 
     if _elsewhere(stream, dev):
@@ -165,6 +180,7 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu", save=False, workspace=
     tokens = x.numel() // dim if dim else 0
     _check("gated_ffn", dev, dt, ("x", x, shape), ("w_gate", w_gate, (hidden, dim)), ("w_up", w_up, (hidden, dim)),
            ("w_down", w_down, (dim, hidden)))
+    _no_graph("gated_ffn", x, w_gate, w_up, w_down)
     act = _act(activation)
 
     if _elsewhere(stream, dev):
@@ -229,6 +245,8 @@ def _vocab_loss(where, x, weight, targets, coef, ignore_index, workspace, budget
     _check(where, dev, dt, ("x", x, x.shape), ("weight", weight, (vocab, dim)))
     _check(where, dev, torch.int64, ("targets", targets, rows))
     _check(where, dev, torch.float32, ("coef", coef, rows))
+    if not grad:
+        _no_graph(where, x, weight)
 
     if _elsewhere(stream, dev):
         return _run_elsewhere(stream, (x, weight, targets, coef, workspace),

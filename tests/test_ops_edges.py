@@ -242,3 +242,22 @@ def test_workspace_of_another_device_is_refused():
                          data_ptr=lambda: 1 << 20, numel=lambda: 1 << 20, element_size=lambda: 1)
     with pytest.raises(ValueError, match="workspace"):
         ops._space(ws, lambda: 16, torch.device("cuda:0"))
+
+
+@pytest.mark.gpu
+def test_inputs_that_require_gradients_are_refused():
+    x = torch.randn(4, 16, device="cuda", dtype=torch.bfloat16)
+    w, d = torch.randn(32, 16, device="cuda").bfloat16(), torch.randn(16, 32, device="cuda").bfloat16()
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    p, q = torch.nn.Parameter(w), torch.ones(16, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    calls = [lambda: pkg.layer_norm(x, q), lambda: pkg.gated_ffn(x, p, w, d),
+             lambda: pkg.gated_ffn(x, w, p, d, save=True), lambda: pkg.vocab_loss(x, p, t)]
+    for call in calls:
+        with pytest.raises(ValueError, match="autograd"):
+            call()
+        with torch.no_grad():
+            call()
+    # functions that return the gradients take them
+    y, mean, rstd = pkg.layer_norm(x, q.detach())
+    pkg.layer_norm_backward(x, x, q, mean, rstd)
+    pkg.vocab_loss_grad(x, p, t)
