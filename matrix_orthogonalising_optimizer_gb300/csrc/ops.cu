@@ -82,32 +82,38 @@ struct CoefArgs {
 };
 
 // The factor, in [1, 2), that is left out of the logit gradients' bf16 values and
-// multiplied into the products' sums: the significand of the largest coefficient
-// that counts.  With the usual one coefficient for all tokens what is left is a
-// power of two, which adds no rounding; left in, its rounding is the same in every
-// token's target, most of a token's gradient, so that no number of tokens averages
-// it out (1 / 255 is off by 2^-8: error of dx and dW 4.1e-3 at 255 tokens, 256 x
-// 5169, untrained; now 1.7e-3, that of the results' own rounding).  What is left is
-// the rounding of 1 - p: 2.0e-3 in all where the tokens' p differ, 2.2e-3 where all
-// p are near 1 / 500.  A significand, not the coefficient, so that dz keeps its
-// range; a maximum, so that no order matters.
+// multiplied into the products' sums: the significand of a coefficient that counts.
+// With the usual one coefficient for all tokens what is left is a power of two,
+// which adds no rounding; left in, its rounding is the same in every token's target,
+// most of a token's gradient, so that no number of tokens averages it out (1 / 255
+// is off by 2^-8: error of dx and dW 4.1e-3 at 255 tokens, 256 x 5169, untrained; now
+// 1.7e-3, that of the results' own rounding).  What is left is the rounding of
+// 1 - p: 2.0e-3 in all where the tokens' p differ, 2.2e-3 where all p are near
+// 1 / 500.  A significand, not the coefficient, so that dz keeps its range; the
+// largest of 4096 tokens, the first that have one, so that no order matters and one
+// block does not read millions.
 __device__ __forceinline__ void common_factor(const CoefArgs& c) {
     __shared__ uint32_t red[32];
-    uint32_t top = 0;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < c.n; i += 1024) {
-        const int64_t t = c.targets[i];
-        const uint32_t b = __float_as_uint(c.coef[i]) & 0x7fffffffu;
-        if (t != c.ignore && t >= 0 && t < c.vocab && b < 0x7f800000u) top = max(top, b);
+    float factor = 1.0f;  // no normal coefficient
+    for (int64_t i0 = threadIdx.x; i0 - threadIdx.x < c.n; i0 += 4096) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t i = i0 + 1024 * k;
+            if (i >= c.n) break;
+            const int64_t t = c.targets[i];
+            const uint32_t b = __float_as_uint(c.coef[i]) & 0x7fffffffu;
+            if (t != c.ignore && t >= 0 && t < c.vocab && b >= 0x00800000u && b < 0x7f800000u) top = max(top, b);
+        }
+        if (!__syncthreads_or(top != 0)) continue;
+        top = __reduce_max_sync(tc::kFullMask, top);
+        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
+        __syncthreads();
+        top = __reduce_max_sync(tc::kFullMask, red[threadIdx.x % 32]);
+        factor = __uint_as_float(0x3f800000u | (top & 0x7fffffu));
+        break;
     }
-    top = __reduce_max_sync(tc::kFullMask, top);
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        top = __reduce_max_sync(tc::kFullMask, red[threadIdx.x]);
-        // no normal coefficient: 1
-        if (threadIdx.x == 0) *c.factor = __uint_as_float(0x3f800000u | (top < 0x00800000u ? 0u : top & 0x7fffffu));
-    }
+    if (threadIdx.x == 0) *c.factor = factor;
 }
 
 // Zeroes a launch's counters: n ints, a multiple of 64, at 256 bytes.  A kernel

@@ -180,8 +180,8 @@ def test_vocab_loss_of_a_wholly_masked_row(tokens, value, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("coefs", ["1.005", "1/n", "mixed"])
-@pytest.mark.parametrize("tokens,budget", [(33, 0), (255, 0), (509, 0), (509, 1), (1021, 0)])
+@pytest.mark.parametrize("coefs", ["1.005", "1/n", "mixed", "late"])
+@pytest.mark.parametrize("tokens,budget", [(33, 0), (255, 0), (509, 0), (509, 1), (1021, 0), (9001, 0)])
 def test_vocab_loss_grad_of_equal_coefficients(tokens, budget, coefs):
     """One coefficient for all tokens, halfway between two bf16 values: its rounding, the same
     in every token's gradient, would not average out.  The bound is that of a few tokens."""
@@ -195,6 +195,9 @@ def test_vocab_loss_grad_of_equal_coefficients(tokens, budget, coefs):
         coef[::9] = 0.0
         coef[4] = math.nan
         targets[4] = -100
+    if coefs == "late":  # nothing counts at first
+        coef[:tokens - tokens // 3] = 0.0
+        targets[:tokens // 3] = -100
     _, _, dx, dw = pkg.vocab_loss_grad(x, w, targets, coef=coef, budget=budget)
     dz = torch.softmax(x.double() @ w.double().T, 1)
     dz.scatter_add_(1, targets.clamp(min=0)[:, None], -torch.ones(tokens, 1, device="cuda", dtype=torch.double))
