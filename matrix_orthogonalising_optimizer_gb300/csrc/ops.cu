@@ -41,9 +41,11 @@ constexpr int64_t kMaxVocab = int64_t(1) << 22;
 // with 512, against about 9e-7 of fp32 FMAs)
 constexpr int kChain = 8, kChainF32 = 4;
 // bf16 sums over more slabs than kLongSum (131072 deep) are added up in registers
-// too, from chains of kLongChain slabs: 2048 truncated additions drift by at most
-// 2^-13 of the sum
-constexpr int kLongSum = 2048, kLongChain = 512;
+// too, from chains of kLongChain slabs, so that they drift by less than 2^-13 of
+// the sum.  Measured on 140000 terms of one sign: 8.6e-4 of the sum too little in one
+// chain (9.8e-8 per 16 terms), 1.4e-4 in chains of 512 slabs, 5.1e-5 in these; a
+// sum of kLongSum slabs, left in one chain, can lose 8e-4, a fifth of a bf16 ulp.
+constexpr int kLongSum = 2048, kLongChain = 256;
 // Up to this many bf16 tokens the logit gradients are kept in two bf16 parts: in one,
 // the target's rounding, most of a token's gradient, is off by up to 2^-8, and a few
 // tokens do not average that out (3 tokens, 64 x 5169: error of dW 2.8e-3 against
