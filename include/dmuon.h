@@ -463,10 +463,18 @@ int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, 
  * With dx and dweight (both or neither) also the gradients of
  * sum_i coef[i] loss[i] (coef NULL: 1):
  *   dz = coef (softmax(z) - onehot(target)),  dx = dz weight,  dweight = dz^T x.
- * The vocabulary is visited in pieces of 128 columns whose maximum and sum of
+ * The vocabulary is visited in pieces of up to 128 columns whose maximum and sum of
  * exponentials are kept; for the gradient the exponentials of a piece of the
  * tokens are held in the workspace (16 bits each, or fp32 for fp32 tensors) and
- * turned into dz there, so the logits are computed once.  Tokens are taken in pieces
+ * turned into dz there, so the logits are computed once.  The 16 bits are good to
+ * 2^-12, and a probability below 2^-31 of its piece's largest counts as 0 in the
+ * gradient (not in loss and lse).  bf16: dz is rounded to bf16 once, after a common
+ * factor of the coefficients is taken out (32 tokens or fewer: kept in two parts).
+ * Masked columns: a logit far below its token's largest, or -inf, has probability
+ * 0 and no gradient.  A token whose logits are all one finite value has loss
+ * log(vocab); one without a finite logit, or with a logit of +inf or NaN, has a NaN
+ * loss and gradient.  fp32 weights and hidden states are taken apart as in the gated
+ * block, so an infinite one may give NaN (mask with a finite value).  Tokens are taken in pieces
  * whose logits fit `budget` bytes (0: 2 GiB; at least 256 tokens), and dweight
  * is summed over the pieces in fp32.  tokens in [0, 2^24], dim in [1, 2^20],
  * vocab in [1, 2^22].  Status codes as for the gated block. */

@@ -514,16 +514,15 @@ struct LossRowArgs {
 
 constexpr int kRowThreads = 256;
 
-// Row pass of the loss.  Each block reduces its row's (max, sum) blocks to
-// lse = M + log sum_b s_b exp(m_b - M) in a fixed order (blocks without a finite
-// logit have s_b = 0, a row without one lse = -inf and a NaN loss and gradient); the first writes the
-// loss, and each turns its share of the row's exponentials e = exp(z - m_b)
-// into logit gradients dz = c e exp(m_b - M) / S with S the sum, the target's as
-// c expm1(-loss), so that p and 1 are not subtracted (what is left is the rounding
-// of S, about 2^-23 of 1).  The loss is (M - z_t) + log S: lse itself loses log S
-// where |M| is large (all of it for a row of equal masked logits), and with it the
-// loss and every p.  Memory-bound: 4
-// bytes per bf16 logit, in place.
+// Row pass of the loss.  Each block reduces its row's (max, sum) blocks to the
+// maximum M and S = sum_b s_b exp(m_b - M), lse = M + log S, in a fixed order (a block
+// without a finite logit has s_b = 0; a row without one gets lse = -inf, a NaN loss
+// and a NaN gradient).  The first writes the loss, and each turns its share of the
+// row's exponentials e = exp(z - m_b) into logit gradients dz = c e exp(m_b - M) / S,
+// the target's as c expm1(-loss), so that p and 1 are not subtracted (what is left is
+// the rounding of S, about 2^-23 of 1).  The loss is (M - z_t) + log S: lse itself
+// loses log S where |M| is large (all of it for a row of equal masked logits), and
+// with it the loss and every p.  Memory-bound: 4 bytes per bf16 logit, in place.
 template <bool kF32>
 __global__ void __launch_bounds__(kRowThreads) loss_row_kernel(const __grid_constant__ LossRowArgs a) {
     __shared__ float red[kRowThreads / 32];
