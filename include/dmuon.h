@@ -473,8 +473,9 @@ int dmuon_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, 
  * Masked columns: a logit far below its token's largest, or -inf, has probability
  * 0 and no gradient.  A token whose logits are all one finite value has loss
  * log(vocab); one without a finite logit, or with a logit of +inf or NaN, has a NaN
- * loss and gradient.  fp32 weights and hidden states are taken apart as in the gated
- * block, so an infinite one may give NaN (mask with a finite value).  Tokens are taken in pieces
+ * loss and gradient.  Mask with finite weights: an infinite one makes dx NaN (0 times
+ * infinity), and in fp32, where operands are taken apart as in the gated block, maybe
+ * the loss.  Tokens are taken in pieces
  * whose logits fit `budget` bytes (0: 2 GiB; at least 256 tokens), and dweight
  * is summed over the pieces in fp32.  tokens in [0, 2^24], dim in [1, 2^20],
  * vocab in [1, 2^22].  Status codes as for the gated block. */

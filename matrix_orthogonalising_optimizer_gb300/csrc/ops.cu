@@ -50,9 +50,9 @@ constexpr int kLongSum = 2048, kLongChain = 256;
 // the target's rounding, most of a token's gradient, is off by up to 2^-8, and a few
 // tokens do not average that out (3 tokens, 64 x 5169: error of dW 2.8e-3 against
 // 1.7e-3 of the result's own rounding).  More tokens do where their roundings differ,
-// which the coefficients' common factor sees to (common_factor).  The parts are rows of one product for dx,
-// which reads W once, and two part products of dW (3 tokens, 4096 x 131072: 687 us
-// with one part, 690 with two, 961 with W read for each).
+// which the coefficients' common factor sees to (common_factor).  The parts are rows
+// of one product for dx, which reads W once, and two part products of dW (3 tokens,
+// 4096 x 131072: 687 us with one part, 690 with two, 961 with W read for each).
 constexpr int kPartTokens = 32;
 constexpr int kMaxLaunches = 4;   // GEMM launches of one call (of one piece)
 constexpr int kSlots = 192;       // partial-sum slots: 48 MiB
