@@ -486,8 +486,95 @@ int dmuon_vocab_loss(const void* x, const void* weight, const int64_t* targets, 
                      int64_t dim, int64_t vocab, int32_t dtype, uint64_t budget, void* workspace,
                      size_t workspace_bytes, void* stream);
 
+/* ---- head norms and position rotation --------------------------------------
+ *
+ * A tensor of tokens x heads x dim as these calls read it: element (t, h, d) at
+ * p[t * token_stride + h * head_stride + d], strides in elements, at least dim and at
+ * most 2^36 (one that no access uses may have any value) -- e.g. the queries inside
+ * the output of one projection for queries, keys and values.  p needs the alignment
+ * of its elements only; rows off 16-byte boundaries take slower kernels. */
+typedef struct {
+    const void* p;
+    int64_t token_stride;
+    int64_t head_stride;
+} dmuon_heads_t;
+
+/* Angles of the rotation: table[p][i] = cos(p base^(-2 i / rotary)) for i < rotary / 2 and
+ * their sines behind them, fp32 rounded from 64 bits, p < positions.  positions in
+ * [0, 2^24], rotary even in [2, 256], base > 0. */
+int dmuon_rotary_table(float* table, int64_t positions, int32_t rotary, double base, void* stream);
+
+/* Queries and keys of an attention, each row (a head of a token) by itself:
+ *   r = 1 / sqrt(mean(x^2) + eps),  n = x r weight       (norm = 0: n = x)
+ * and of n the first `rotary` elements in pairs (a, b) turned by the angle of the token's
+ * position, a cos - b sin and a sin + b cos; the others unchanged.  Pair i is
+ * (i, i + rotary / 2) or, interleaved, (2 i, 2 i + 1).
+ * q: tokens x heads x dim, k: tokens x kv_heads x dim.  q_out, k_out: contiguous.
+ * q_weight, k_weight: dim elements or NULL (1); NULL without norm.  positions: tokens
+ * int64, table: table_rows x rotary from dmuon_rotary_table; table NULL: no rotation
+ * (positions may be NULL).  A position outside [0, table_rows) makes the rotated
+ * elements of its token NaN.  tokens in [0, 2^24], heads and kv_heads in [1, 1024], dim in
+ * [1, 256], rotary even in [2, dim], eps >= 0.  Returns DMUON_OK, DMUON_ERR_INVALID_ARG,
+ * DMUON_ERR_UNSUPPORTED_DTYPE, DMUON_ERR_ALIGN, DMUON_ERR_UNSUPPORTED_DEVICE or
+ * DMUON_ERR_CUDA. */
+int dmuon_qk_norm_rotary_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, const int64_t* positions,
+                                 const float* table, int64_t table_rows, int32_t rotary, int32_t interleaved,
+                                 const void* q_weight, const void* k_weight, int32_t norm, float eps, void* q_out,
+                                 void* k_out, int64_t tokens, int32_t heads, int32_t kv_heads, int32_t dim,
+                                 int32_t dtype, void* stream);
+/* Workspace of the backward pass (0 for sizes it refuses). */
+size_t dmuon_qk_norm_rotary_workspace_bytes(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t dim,
+                                            int32_t dtype);
+/* From the gradients of q_out and k_out, and the forward pass's inputs (q and k are
+ * not read without norm), with dn = the gradient turned back and g = dn weight:
+ *   dx = r (g - x r mean(g x r)),  dweight = sum over tokens and heads of dn x r
+ * dq, dk: contiguous.  dq_weight, dk_weight may each be NULL (not computed; both NULL: no
+ * workspace needed; NULL without norm); with no tokens they are zero. */
+int dmuon_qk_norm_rotary_backward(const dmuon_heads_t* dq_out, const dmuon_heads_t* dk_out, const dmuon_heads_t* q,
+                                  const dmuon_heads_t* k, const int64_t* positions, const float* table,
+                                  int64_t table_rows, int32_t rotary, int32_t interleaved, const void* q_weight,
+                                  const void* k_weight, int32_t norm, float eps, void* dq, void* dk, void* dq_weight,
+                                  void* dk_weight, int64_t tokens, int32_t heads, int32_t kv_heads, int32_t dim,
+                                  int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- attention ----------------------------------------------------------------
+ *
+ * Attention over whole sequences, `sequences` of them packed one behind the other:
+ *   s_ij = scale q_i k_j over the keys j that i sees: those of its own sequence, with
+ *   causal only j <= i;  lse_i = log sum_j exp(s_ij),  o_i = sum_j exp(s_ij - lse_i) v_j
+ * q: tokens x heads x dim; k, v: tokens x kv_heads x dim; heads is a multiple of kv_heads,
+ * and heads / kv_heads query heads in a row share a key head.  o: tokens x heads x dim
+ * contiguous, lse: heads x tokens floats.
+ * offsets: sequences + 1 int64 on the device, not decreasing, in [0, tokens]: sequence s
+ * is tokens [offsets[s], offsets[s + 1]), maybe empty.  NULL: equal sequences of
+ * tokens / sequences.  (Other offsets give unspecified results; no access leaves the
+ * tensors.)  Tokens before the first or behind the last sequence see nothing: o = 0,
+ * lse = -inf, gradients 0, whatever values they hold; no sequence reads another's.
+ * Within a sequence a NaN or an infinity may reach the outputs of all its tokens.
+ * No logits are stored.  bf16 on the tensor cores: exp(s - lse) and the gradient ds are
+ * rounded to bf16 once, as operands of the next product; rows off 16-byte boundaries, and
+ * fp32, run as fp32 FMAs.  tokens in [0, 2^24], sequences in [1, 2^20], heads in
+ * [1, 1024], dim in [1, 128], scale finite and > 0 (usually 1 / sqrt(dim)).  Status codes as
+ * for the gated block. */
+size_t dmuon_attention_workspace_bytes(int64_t sequences, int64_t tokens, int32_t heads, int32_t kv_heads,
+                                       int32_t dim, int32_t dtype, int32_t backward);
+int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, const dmuon_heads_t* v,
+                            const int64_t* offsets, int64_t sequences, void* o, float* lse, int64_t tokens,
+                            int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype, int32_t causal, float scale,
+                            void* workspace, size_t workspace_bytes, void* stream);
+/* From the gradient d_o of o and the forward pass's inputs and outputs:
+ *   delta_i = d_o_i o_i,  ds_ij = exp(s_ij - lse_i) (d_o_i v_j - delta_i)
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i exp(s_ij - lse_i) d_o_i
+ * dk and dv are summed over the query heads that share the key head, in a fixed order.
+ * dq, dk, dv: contiguous. */
+int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_heads_t* q, const dmuon_heads_t* k,
+                             const dmuon_heads_t* v, const void* o, const float* lse, const int64_t* offsets,
+                             int64_t sequences, void* dq, void* dk, void* dv, int64_t tokens, int32_t heads,
+                             int32_t kv_heads, int32_t dim, int32_t dtype, int32_t causal, float scale,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Waits for all streams of the current device, then DMUON_ERR_DEVICE_TIMEOUT if a
- * wait inside a layer norm's, gated block's or vocabulary loss's kernel on it gave
+ * wait inside a layer norm's, gated block's, vocabulary loss's or attention's kernel gave
  * up (about 2 s; its outputs are then not complete) since the last call, else
  * DMUON_OK; clears the flag.  Not during a stream's capture. */
 int dmuon_ops_status(void);

@@ -21,8 +21,10 @@ from ._lib import (  # noqa: F401
 
 _OPS = ("layer_norm", "layer_norm_backward", "layer_norm_workspace", "gated_ffn", "gated_ffn_backward",
         "gated_ffn_workspace", "vocab_loss", "vocab_loss_grad", "vocab_loss_workspace", "ops_status")
+_ATTN = ("rotary_table", "qk_norm_rotary", "qk_norm_rotary_backward", "qk_norm_rotary_workspace", "attention",
+         "attention_backward", "attention_workspace")
 
-__all__ = ["Muon", "dmuon_plan", "dmuon_step", "assign_owners", "adamw_step", "load", *_OPS]
+__all__ = ["Muon", "dmuon_plan", "dmuon_step", "assign_owners", "adamw_step", "load", *_OPS, *_ATTN]
 
 _DTYPES = {"bf16": BF16, "fp32": FP32}
 _PREC = {"bf16": PREC_BF16, "fp32": PREC_FP32}
@@ -41,6 +43,10 @@ def __getattr__(name):
     if name in _OPS:
         from . import ops
         globals()[name] = getattr(ops, name)
+        return globals()[name]
+    if name in _ATTN:
+        from . import attn
+        globals()[name] = getattr(attn, name)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

@@ -37,6 +37,10 @@ class Options(ctypes.Structure):
                 ("small_m", c_int32), ("tile_rule", c_int32), ("workspace_budget", c_uint64)]
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("p", c_void_p), ("token_stride", c_int64), ("head_stride", c_int64)]
+
+
 class BucketInfo(ctypes.Structure):
     _fields_ = [("dtype", c_int32), ("route", c_int32), ("mm_engine", c_int32), ("tile", c_int32),
                 ("m", c_int64), ("n", c_int64), ("count", c_int64), ("per_matrix_bytes", c_int64)]
@@ -90,6 +94,19 @@ SIGNATURES = {
     "dmuon_vocab_loss": (c_int, [c_void_p] * 4 + [c_int64] + [c_void_p] * 4 + [c_int64, c_int64, c_int64, c_int32,
                                                                                c_uint64, c_void_p, c_size_t,
                                                                                c_void_p]),
+    "dmuon_rotary_table": (c_int, [c_void_p, c_int64, c_int32, c_double, c_void_p]),
+    "dmuon_qk_norm_rotary_forward": (c_int, [POINTER(Heads)] * 2 + [c_void_p, c_void_p, c_int64, c_int32, c_int32,
+                                                                    c_void_p, c_void_p, c_int32, c_float, c_void_p,
+                                                                    c_void_p, c_int64] + [c_int32] * 4 + [c_void_p]),
+    "dmuon_qk_norm_rotary_workspace_bytes": (c_size_t, [c_int64] + [c_int32] * 4),
+    "dmuon_qk_norm_rotary_backward": (c_int, [POINTER(Heads)] * 4 + [c_void_p, c_void_p, c_int64, c_int32, c_int32,
+                                                                     c_void_p, c_void_p, c_int32, c_float]
+                                      + [c_void_p] * 4 + [c_int64] + [c_int32] * 4 + [c_void_p, c_size_t, c_void_p]),
+    "dmuon_attention_workspace_bytes": (c_size_t, [c_int64, c_int64] + [c_int32] * 5),
+    "dmuon_attention_forward": (c_int, [POINTER(Heads)] * 3 + [c_void_p, c_int64, c_void_p, c_void_p, c_int64]
+                                + [c_int32] * 5 + [c_float, c_void_p, c_size_t, c_void_p]),
+    "dmuon_attention_backward": (c_int, [POINTER(Heads)] * 4 + [c_void_p, c_void_p, c_void_p, c_int64] + [c_void_p] * 3
+                                 + [c_int64] + [c_int32] * 5 + [c_float, c_void_p, c_size_t, c_void_p]),
     "dmuon_ops_status": (c_int, []),
 }
 

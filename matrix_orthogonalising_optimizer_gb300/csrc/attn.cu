@@ -1,0 +1,143 @@
+// Host side of attention: argument checks, workspace layout, choice of kernels.
+#include <algorithm>
+#include <cmath>
+
+#include "act.cuh"
+#include "attn.h"
+#include "checks.h"
+
+namespace dmuon {
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int64_t kMaxSequences = int64_t(1) << 20;
+constexpr int kMaxHeads = 1024, kMaxDim = 128;
+
+bool sizes_ok(int64_t tokens, int64_t sequences, int64_t heads, int64_t kv_heads, int64_t dim) {
+    return in_range(tokens, 0, kMaxTokens) && in_range(sequences, 1, kMaxSequences) && in_range(heads, 1, kMaxHeads) &&
+           in_range(kv_heads, 1, heads) && heads % kv_heads == 0 && in_range(dim, 1, kMaxDim);
+}
+
+int set_heads(AttnHeads& h, const dmuon_heads_t* t, int64_t tokens, int64_t heads, int64_t dim, int es,
+              const char* name, const char* where) {
+    if (!t) return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": " + name + " is NULL");
+    OPS_TRY(check_ptr(t->p, name, where, static_cast<size_t>(es)));
+    const int64_t most = int64_t(1) << 36;
+    if ((tokens > 1 && !in_range(t->token_stride, dim, most)) || (heads > 1 && !in_range(t->head_stride, dim, most)))
+        return fail(DMUON_ERR_INVALID_ARG,
+                    std::string(where) + ": strides of " + name + " must be at least dim, and at most 2^36");
+    h.p = t->p;
+    // a stride that no access uses has any value
+    h.token = tokens > 1 ? t->token_stride : dim;
+    h.head = heads > 1 ? t->head_stride : dim;
+    return DMUON_OK;
+}
+
+// What both directions check, and the arguments they share.
+int common(AttnArgs& a, const dmuon_heads_t* q, const dmuon_heads_t* k, const dmuon_heads_t* v,
+           const int64_t* offsets, int64_t sequences, int64_t tokens, int32_t heads, int32_t kv_heads, int32_t dim,
+           int32_t dtype, int32_t causal, float scale, const char* where) {
+    if (!sizes_ok(tokens, sequences, heads, kv_heads, dim))
+        return fail(DMUON_ERR_INVALID_ARG,
+                    std::string(where) + ": tokens must be in [0, 2^24], sequences in [1, 2^20], heads in [1, 1024] and "
+                                         "a multiple of kv_heads, dim in [1, 128]");
+    OPS_TRY(check_dtype(dtype, where));
+    if (!(scale > 0.0f) || !std::isfinite(scale))
+        return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": scale must be finite and > 0");
+    if (!offsets && tokens % sequences != 0)
+        return fail(DMUON_ERR_INVALID_ARG,
+                    std::string(where) + ": without offsets tokens must be a multiple of sequences");
+    if (offsets) OPS_TRY(check_ptr(offsets, "offsets", where, 8));
+    a.offsets = offsets;
+    a.tokens = tokens;
+    a.length = tokens / sequences;
+    a.sequences = static_cast<int32_t>(sequences);
+    a.heads = heads;
+    a.kv_heads = kv_heads;
+    a.group = heads / kv_heads;
+    a.dim = dim;
+    a.causal = causal != 0;
+    a.fill = offsets ? static_cast<int32_t>(std::min<int64_t>(ceil_div(tokens, 64), 4)) : 0;
+    a.scale = scale;
+    a.scale_log2 = scale * kLog2e;
+    if (tokens == 0) return DMUON_OK;
+    const int es = dtype == DMUON_FP32 ? 4 : 2;
+    OPS_TRY(set_heads(a.q, q, tokens, heads, dim, es, "q", where));
+    OPS_TRY(set_heads(a.k, k, tokens, kv_heads, dim, es, "k", where));
+    OPS_TRY(set_heads(a.v, v, tokens, kv_heads, dim, es, "v", where));
+    return DMUON_OK;
+}
+
+struct Layout {
+    float* delta = nullptr;
+    size_t bytes = 0;
+    Layout(char* base, int64_t tokens, int64_t heads, bool backward) {
+        Arena a{base};
+        if (backward) delta = a.take<float>(tokens * heads);
+        bytes = a.off;
+    }
+};
+
+}  // namespace
+}  // namespace dmuon
+
+using namespace dmuon;
+
+extern "C" size_t dmuon_attention_workspace_bytes(int64_t sequences, int64_t tokens, int32_t heads, int32_t kv_heads,
+                                                  int32_t dim, int32_t dtype, int32_t backward) {
+    if (!sizes_ok(tokens, sequences, heads, kv_heads, dim) ||
+        check_dtype(dtype, "dmuon_attention_workspace_bytes") != DMUON_OK)
+        return 0;
+    return Layout(nullptr, tokens, heads, backward != 0).bytes;
+}
+
+extern "C" int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, const dmuon_heads_t* v,
+                                       const int64_t* offsets, int64_t sequences, void* o, float* lse, int64_t tokens,
+                                       int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype, int32_t causal,
+                                       float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* where = "dmuon_attention_forward";
+    AttnArgs a = {};
+    OPS_TRY(common(a, q, k, v, offsets, sequences, tokens, heads, kv_heads, dim, dtype, causal, scale, where));
+    if (tokens == 0) return DMUON_OK;
+    OPS_TRY(check_ptr(o, "o", where));
+    OPS_TRY(check_ptr(lse, "lse", where));
+    const Layout L(static_cast<char*>(workspace), tokens, heads, false);
+    OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
+    OPS_TRY(check_device(where));
+    a.out = o;
+    a.lse = lse;
+    OPS_CUDA(attn_simt_forward(a, dtype == DMUON_FP32, static_cast<cudaStream_t>(stream)));
+    return DMUON_OK;
+}
+
+extern "C" int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_heads_t* q, const dmuon_heads_t* k,
+                                        const dmuon_heads_t* v, const void* o, const float* lse,
+                                        const int64_t* offsets, int64_t sequences, void* dq, void* dk, void* dv,
+                                        int64_t tokens, int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype,
+                                        int32_t causal, float scale, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+    const char* where = "dmuon_attention_backward";
+    AttnArgs a = {};
+    OPS_TRY(common(a, q, k, v, offsets, sequences, tokens, heads, kv_heads, dim, dtype, causal, scale, where));
+    if (tokens == 0) return DMUON_OK;
+    const bool f32 = dtype == DMUON_FP32;
+    OPS_TRY(set_heads(a.d_o, d_o, tokens, heads, dim, f32 ? 4 : 2, "d_o", where));
+    OPS_TRY(check_ptr(o, "o", where));
+    OPS_TRY(check_ptr(lse, "lse", where));
+    OPS_TRY(check_ptr(dq, "dq", where));
+    OPS_TRY(check_ptr(dk, "dk", where));
+    OPS_TRY(check_ptr(dv, "dv", where));
+    const Layout L(static_cast<char*>(workspace), tokens, heads, true);
+    OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
+    OPS_TRY(check_device(where));
+    a.o = o;
+    a.lse = const_cast<float*>(lse);
+    a.delta = L.delta;
+    a.out = dq;
+    a.dk = dk;
+    a.dv = dv;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    OPS_CUDA(attn_delta(a, f32, s));
+    OPS_CUDA(attn_simt_backward(a, f32, s));
+    return DMUON_OK;
+}

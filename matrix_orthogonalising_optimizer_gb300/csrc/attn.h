@@ -1,0 +1,98 @@
+// Attention: the arguments its kernels share, and how a block finds its rows in
+// a packed batch.  Not part of the C ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace dmuon {
+
+// One tensor of tokens x heads x dim: strides in elements, a head's row contiguous.
+struct AttnHeads {
+    const void* p;
+    int64_t token, head;
+};
+
+struct AttnArgs {
+    AttnHeads q, k, v, d_o;    // queries, keys, values, gradient of the outputs
+    const void* o;             // tokens x heads x dim, contiguous like the outputs
+    void* out;                 // forward: o | backward: dq
+    void* dk;
+    void* dv;
+    float* lse;                // [heads][tokens]
+    float* delta;              // [heads][tokens]: do . o
+    const int64_t* offsets;    // sequences + 1, or NULL: equal sequences of `length` tokens
+    int64_t tokens, length;
+    int32_t sequences;
+    int32_t heads, kv_heads, group, dim;
+    int32_t causal;
+    int32_t slots;             // row tiles of a head (an upper bound: see attn_slots)
+    int32_t fill;              // blocks behind them that clear the rows of no sequence
+    float scale, scale_log2;   // scale_log2 = scale * log2(e)
+};
+
+// A tile of `T` rows of one sequence.  Which tiles exist is only known on the
+// device, so the grid has room for every split of the tokens into n sequences:
+// sequence s, which begins at token b, owns the slots from b / T + s on.  Up to the
+// next sequence's first slot that is at least one slot per T rows or part of T rows;
+// the slots that are too many find nothing and return.
+__host__ __device__ inline int64_t attn_slots(int64_t tokens, int64_t sequences, int tile) {
+    return tokens / tile + sequences;
+}
+
+struct AttnTile {
+    int64_t begin;  // the sequence's first token
+    int32_t len;    // its tokens
+    int32_t tile;   // index of the tile in the sequence
+};
+
+__device__ __forceinline__ int64_t attn_offset(const AttnArgs& a, int64_t s) {
+    if (!a.offsets) return s * a.length;
+    const int64_t o = a.offsets[s];
+    return o < 0 ? 0 : o > a.tokens ? a.tokens : o;  // no access outside, whatever the offsets say
+}
+
+// The tile at a slot, by all 32 lanes of a warp (each round splits the sequences
+// left into 32).  False: the slot holds none.
+__device__ __forceinline__ bool attn_find(const AttnArgs& a, int64_t slot, int T, AttnTile& t) {
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, count = a.sequences;
+    while (count > 1) {
+        const int64_t step = (count + 31) / 32, i = lo + lane * step;
+        const bool before = i < lo + count && attn_offset(a, i) / T + i <= slot;
+        const unsigned m = __ballot_sync(0xffffffffu, before);
+        const int c = m == 0 ? 0 : 31 - __clz(m);
+        const int64_t end = lo + count;
+        lo += c * step;
+        count = step < end - lo ? step : end - lo;
+    }
+    const int64_t b = attn_offset(a, lo), e = attn_offset(a, lo + 1);
+    const int64_t k = slot - (b / T + lo);
+    t.begin = b;
+    t.len = static_cast<int32_t>(e - b);
+    t.tile = static_cast<int32_t>(k);
+    return k >= 0 && b + k * T < e;
+}
+
+// Clears the rows of no sequence -- before the first and behind the last -- of one
+// head: o = 0, lse = -inf, gradients 0.  Block f of `a.fill`.
+template <typename T>
+__device__ __forceinline__ void attn_clear(const AttnArgs& a, T* x, float* lse, int heads, int head, int f) {
+    const int64_t first = attn_offset(a, 0), last = attn_offset(a, a.sequences);
+    const int64_t outside = first + (a.tokens - (last > first ? last : first));
+    for (int64_t i = f; i < outside; i += a.fill) {
+        const int64_t row = i < first ? i : i - first + (last > first ? last : first);
+        for (int c = threadIdx.x; c < a.dim; c += blockDim.x) x[(row * heads + head) * a.dim + c] = T(0.0f);
+        if (lse && threadIdx.x == 0) lse[head * a.tokens + row] = __int_as_float(0xff800000);
+    }
+}
+
+// FFMA kernels (attn_simt.cu): any strides, either type.
+cudaError_t attn_simt_forward(const AttnArgs& a, bool f32, cudaStream_t s);
+cudaError_t attn_simt_backward(const AttnArgs& a, bool f32, cudaStream_t s);
+// delta, for both backward passes
+cudaError_t attn_delta(const AttnArgs& a, bool f32, cudaStream_t s);
+
+}  // namespace dmuon

@@ -1,0 +1,458 @@
+// Attention in fp32 FFMA arithmetic, forward and backward: fp32 tensors, and bf16
+// ones whose rows the tensor-core kernels cannot read (rows off 16 bytes).
+//
+//   s_ij = scale q_i k_j over the keys j that i sees,  lse_i = log sum_j exp s_ij
+//   p = exp(s - lse),  o_i = sum_j p_ij v_j
+//   ds_ij = p_ij (do_i v_j - delta_i),  delta_i = do_i o_i
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
+//
+// One pass over the keys per 64 queries with the running maximum and sum of the
+// softmax; the backward pass takes p from lse, once per 64 queries for dq and once
+// per 64 keys for dk and dv (summed over the query heads that share the key head), so
+// every sum has one owner and a fixed order.  A block of 256 threads forms 64 x 64
+// products, 4 x 4 per thread; all tiles lie row by row in shared memory as fp32,
+// dim + 4 floats apart: 16-byte reads of eight rows then cover all banks.
+#include <cmath>
+
+#include "act.cuh"
+#include "attn.h"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace dmuon {
+namespace {
+
+constexpr int T = 64;           // queries and keys of a tile
+constexpr int kThreads = 256;   // 16 x 16: thread (ty, tx) holds rows ty + 16 r, columns tx + 16 c
+constexpr int LP = T + 4;       // row stride of a T x T tile
+constexpr unsigned kFull = 0xffffffffu;
+
+template <typename E>
+__device__ __forceinline__ float to_f(E v) {
+    if constexpr (sizeof(E) == 2) return __bfloat162float(v);
+    else return v;
+}
+
+template <typename E>
+__device__ __forceinline__ E from_f(float v) {
+    if constexpr (sizeof(E) == 2) return __float2bfloat16_rn(v);
+    else return v;
+}
+
+// T rows of a head into shared memory, zero behind `rows` and `dim`.  `vec`: rows
+// start on 16-byte boundaries and dim is a multiple of 4.
+template <typename E, int DP>
+__device__ __forceinline__ void load_tile(float* dst, const AttnHeads& h, int64_t row0, int rows, int head, int dim,
+                                          bool vec) {
+    constexpr int LD = DP + 4;
+    const E* base = static_cast<const E*>(h.p) + row0 * h.token + head * h.head;
+    if (vec) {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < T * (DP / 4); i += kThreads) {
+            const int r = i / (DP / 4), c = i % (DP / 4) * 4;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < rows && c < dim) {
+                const E* p = base + r * h.token + c;
+                if constexpr (sizeof(E) == 4) {
+                    v = *reinterpret_cast<const float4*>(p);
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(p);
+                    const float2 a = tc::unpack_bf16x2(w.x), b = tc::unpack_bf16x2(w.y);
+                    v = make_float4(a.x, a.y, b.x, b.y);
+                }
+            }
+            *reinterpret_cast<float4*>(dst + r * LD + c) = v;
+        }
+        return;
+    }
+#pragma unroll 4
+    for (int i = threadIdx.x; i < T * DP; i += kThreads) {
+        const int r = i / DP, c = i % DP;
+        dst[r * LD + c] = r < rows && c < dim ? to_f<E>(base[r * h.token + c]) : 0.0f;
+    }
+}
+
+// acc[r][c] = sum_d A[ty + 16 r][d] B[tx + 16 c][d]
+template <int DP>
+__device__ __forceinline__ void product_nt(float (&acc)[4][4], const float* A, const float* B, int dim4) {
+    constexpr int LD = DP + 4;
+    const float* a0 = A + (threadIdx.x / 16) * LD;
+    const float* b0 = B + (threadIdx.x % 16) * LD;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
+#pragma unroll 2
+    for (int d = 0; d < dim4; d += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(a0 + 16 * r * LD + d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4*>(b0 + 16 * c * LD + d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                acc[r][c] = fmaf(a[r].x, b[c].x, acc[r][c]);
+                acc[r][c] = fmaf(a[r].y, b[c].y, acc[r][c]);
+                acc[r][c] = fmaf(a[r].z, b[c].z, acc[r][c]);
+                acc[r][c] = fmaf(a[r].w, b[c].w, acc[r][c]);
+            }
+    }
+}
+
+// acc[r][k] += sum_j P[ty + 16 r][j] V[j][4 tx + 64 (k / 4) + k % 4]
+template <int DP>
+__device__ __forceinline__ void product_nn(float (&acc)[4][DP / 16], const float* P, const float* V) {
+    constexpr int LD = DP + 4;
+    const float* p0 = P + (threadIdx.x / 16) * LP;
+    const float* v0 = V + 4 * (threadIdx.x % 16);
+#pragma unroll 2
+    for (int j = 0; j < T; j += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(p0 + 16 * r * LP + j);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c) {
+                const float4 v = *reinterpret_cast<const float4*>(v0 + (j + jj) * LD + 64 * c);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float w = jj == 0 ? p[r].x : jj == 1 ? p[r].y : jj == 2 ? p[r].z : p[r].w;
+                    acc[r][4 * c] = fmaf(w, v.x, acc[r][4 * c]);
+                    acc[r][4 * c + 1] = fmaf(w, v.y, acc[r][4 * c + 1]);
+                    acc[r][4 * c + 2] = fmaf(w, v.z, acc[r][4 * c + 2]);
+                    acc[r][4 * c + 3] = fmaf(w, v.w, acc[r][4 * c + 3]);
+                }
+            }
+    }
+}
+
+// Rows ty + 16 r < rows of a contiguous tokens x heads x dim tensor, times f[r].
+template <typename E, int DP>
+__device__ __forceinline__ void store_rows(void* out, const float (&acc)[4][DP / 16], const float (&f)[4],
+                                           int64_t row0, int rows, int heads, int head, int dim) {
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = ty + 16 * r;
+        if (i >= rows) continue;
+        E* p = static_cast<E*>(out) + ((row0 + i) * heads + head) * static_cast<int64_t>(dim);
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            const int d = 4 * tx + 64 * (k / 4) + k % 4;
+            if (d < dim) p[d] = from_f<E>(acc[r][k] * f[r]);
+        }
+    }
+}
+
+// Sum and maximum over the 16 lanes that share a row.
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+    for (int s = 8; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, s));
+    return v;
+}
+
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int s = 8; s >= 1; s >>= 1) v += __shfl_xor_sync(kFull, v, s);
+    return v;
+}
+
+struct Block {
+    AttnTile t;
+    int head, row0, rows, tiles;
+};
+
+// The block's tile: heads run fastest, tiles of a sequence from its end where the
+// last ones have most to do (`last_first`).  False: nothing left to do.
+template <typename E>
+__device__ __forceinline__ bool take_block(const AttnArgs& a, int heads, bool last_first, E* out, E* out2, float* lse,
+                                           Block& b) {
+    const int64_t slot = blockIdx.x / heads;
+    b.head = static_cast<int>(blockIdx.x - slot * heads);
+    if (slot >= a.slots) {
+        attn_clear(a, out, lse, heads, b.head, static_cast<int>(slot - a.slots));
+        if (out2) attn_clear(a, out2, nullptr, heads, b.head, static_cast<int>(slot - a.slots));
+        return false;
+    }
+    if (!attn_find(a, slot, T, b.t)) return false;
+    b.tiles = (b.t.len + T - 1) / T;
+    const int tile = last_first ? b.tiles - 1 - b.t.tile : b.t.tile;
+    b.row0 = tile * T;
+    b.rows = min(T, b.t.len - b.row0);
+    return true;
+}
+
+template <typename E>
+__device__ __forceinline__ bool vec_rows(const AttnHeads& h, int dim) {
+    constexpr int n = 16 / sizeof(E);
+    return reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.token % n == 0 && h.head % n == 0 && dim % 4 == 0;
+}
+
+template <typename E, int DP>
+__global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int LD = DP + 4;
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + T * LD, *V = K + T * LD, *P = V + T * LD;
+    Block b;
+    if (!take_block(a, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), a.lse, b)) return;
+    const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
+    load_tile<E, DP>(Q, a.q, b.t.begin + b.row0, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
+    float acc[4][DP / 16], top[4], sum[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        top[r] = __int_as_float(0xff800000);
+        sum[r] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) acc[r][k] = 0.0f;
+    }
+    const int end = a.causal ? b.row0 + b.rows : b.t.len;  // keys that any of the rows sees
+    for (int j0 = 0; j0 < end; j0 += T) {
+        const int keys = min(T, b.t.len - j0);
+        __syncthreads();
+        load_tile<E, DP>(K, a.k, b.t.begin + j0, keys, kv, a.dim, vk);
+        load_tile<E, DP>(V, a.v, b.t.begin + j0, keys, kv, a.dim, vv);
+        __syncthreads();
+        float s[4][4];
+        product_nt<DP>(s, Q, K, dim4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = b.row0 + ty + 16 * r;
+            const int seen = a.causal ? min(i + 1 - j0, keys) : keys;
+            float m = top[r];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (tx + 16 * c >= seen) s[r][c] = __int_as_float(0xff800000);
+                m = fmaxf(m, s[r][c]);
+            }
+            m = row_max(m);
+            // from the maximum before scaling, so that large logits keep their differences
+            const float base = exp_shift(m) * a.scale_log2, old = ex2(fmaf(top[r], a.scale_log2, -base));
+            top[r] = m;
+            float part = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float e = ex2(fmaf(s[r][c], a.scale_log2, -base));
+                part += e;
+                P[(ty + 16 * r) * LP + tx + 16 * c] = e;
+            }
+            sum[r] = fmaf(sum[r], old, row_sum(part));
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) acc[r][k] *= old;
+        }
+        __syncwarp();  // a row of P is written and read by one half warp
+        product_nn<DP>(acc, P, V);
+    }
+    float f[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        f[r] = 1.0f / sum[r];
+        const int i = ty + 16 * r;
+        if (tx == 0 && i < b.rows)
+            a.lse[b.head * a.tokens + b.t.begin + b.row0 + i] = fmaf(top[r], a.scale, logf(sum[r]));
+    }
+    store_rows<E, DP>(a.out, acc, f, b.t.begin + b.row0, b.rows, a.heads, b.head, a.dim);
+}
+
+template <typename E, int DP>
+__global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int LD = DP + 4;
+    extern __shared__ float sm[];
+    float *Q = sm, *O = Q + T * LD, *K = O + T * LD, *V = K + T * LD, *P = V + T * LD;
+    Block b;
+    if (!take_block(a, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), nullptr, b)) return;
+    const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
+    const int64_t row = b.t.begin + b.row0;
+    load_tile<E, DP>(Q, a.q, row, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
+    load_tile<E, DP>(O, a.d_o, row, b.rows, b.head, a.dim, vec_rows<E>(a.d_o, a.dim));
+    float acc[4][DP / 16], lse[4], delta[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = ty + 16 * r;
+        const bool in = i < b.rows;
+        lse[r] = in ? a.lse[b.head * a.tokens + row + i] * kLog2e : 0.0f;
+        delta[r] = in ? a.delta[b.head * a.tokens + row + i] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) acc[r][k] = 0.0f;
+    }
+    const int end = a.causal ? b.row0 + b.rows : b.t.len;
+    for (int j0 = 0; j0 < end; j0 += T) {
+        const int keys = min(T, b.t.len - j0);
+        __syncthreads();
+        load_tile<E, DP>(K, a.k, b.t.begin + j0, keys, kv, a.dim, vk);
+        load_tile<E, DP>(V, a.v, b.t.begin + j0, keys, kv, a.dim, vv);
+        __syncthreads();
+        float s[4][4], g[4][4];
+        product_nt<DP>(s, Q, K, dim4);
+        product_nt<DP>(g, O, V, dim4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = b.row0 + ty + 16 * r;
+            const int seen = a.causal ? min(i + 1 - j0, keys) : keys;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float p = ex2(fmaf(s[r][c], a.scale_log2, -lse[r]));
+                P[(ty + 16 * r) * LP + tx + 16 * c] = tx + 16 * c < seen ? p * (g[r][c] - delta[r]) : 0.0f;
+            }
+        }
+        __syncwarp();
+        product_nn<DP>(acc, P, K);
+    }
+    const float f[4] = {a.scale, a.scale, a.scale, a.scale};
+    store_rows<E, DP>(a.out, acc, f, row, b.rows, a.heads, b.head, a.dim);
+}
+
+template <typename E, int DP>
+__global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int LD = DP + 4;
+    extern __shared__ float sm[];
+    float *K = sm, *V = K + T * LD, *Q = V + T * LD, *O = Q + T * LD, *P = O + T * LD, *G = P + T * LP;
+    Block b;
+    if (!take_block(a, a.kv_heads, false, static_cast<E*>(a.dk), static_cast<E*>(a.dv), nullptr, b)) return;
+    const int dim4 = (a.dim + 3) / 4 * 4, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const bool vq = vec_rows<E>(a.q, a.dim), vo = vec_rows<E>(a.d_o, a.dim);
+    const int64_t row = b.t.begin + b.row0;
+    load_tile<E, DP>(K, a.k, row, b.rows, b.head, a.dim, vec_rows<E>(a.k, a.dim));
+    load_tile<E, DP>(V, a.v, row, b.rows, b.head, a.dim, vec_rows<E>(a.v, a.dim));
+    float dk[4][DP / 16], dv[4][DP / 16];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) dk[r][k] = dv[r][k] = 0.0f;
+    const int first = a.causal ? b.row0 : 0;  // the first query that sees any of the keys
+    for (int head = b.head * a.group; head < (b.head + 1) * a.group; ++head) {
+        for (int i0 = first; i0 < b.t.len; i0 += T) {
+            const int queries = min(T, b.t.len - i0);
+            __syncthreads();
+            load_tile<E, DP>(Q, a.q, b.t.begin + i0, queries, head, a.dim, vq);
+            load_tile<E, DP>(O, a.d_o, b.t.begin + i0, queries, head, a.dim, vo);
+            __syncthreads();
+            float s[4][4], g[4][4];
+            product_nt<DP>(s, K, Q, dim4);
+            product_nt<DP>(g, V, O, dim4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int i = tx + 16 * c;
+                const int64_t at = head * a.tokens + b.t.begin + i0 + i;
+                const bool in = i < queries;
+                const float lse = in ? a.lse[at] * kLog2e : 0.0f, delta = in ? a.delta[at] : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = ty + 16 * r;
+                    const bool seen = in && (!a.causal || b.row0 + j <= i0 + i);
+                    const float p = seen ? ex2(fmaf(s[r][c], a.scale_log2, -lse)) : 0.0f;
+                    P[j * LP + i] = p;
+                    G[j * LP + i] = seen ? p * (g[r][c] - delta) : 0.0f;
+                }
+            }
+            __syncwarp();
+            product_nn<DP>(dv, P, O);
+            product_nn<DP>(dk, G, Q);
+        }
+    }
+    const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f}, f[4] = {a.scale, a.scale, a.scale, a.scale};
+    store_rows<E, DP>(a.dv, dv, one, row, b.rows, a.kv_heads, b.head, a.dim);
+    store_rows<E, DP>(a.dk, dk, f, row, b.rows, a.kv_heads, b.head, a.dim);
+}
+
+// delta = do . o, one warp per row.  Rows of no sequence are never read later.
+template <typename E>
+__global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttnArgs a) {
+    const int64_t rows = a.tokens * a.heads;
+    const int lane = threadIdx.x % 32;
+    for (int64_t r = blockIdx.x * 8ll + threadIdx.x / 32; r < rows; r += gridDim.x * 8ll) {
+        const int64_t token = r / a.heads;
+        const int head = static_cast<int>(r - token * a.heads);
+        const E* o = static_cast<const E*>(a.o) + r * a.dim;
+        const E* d = static_cast<const E*>(a.d_o.p) + token * a.d_o.token + head * a.d_o.head;
+        float sum = 0.0f;
+        for (int c = lane; c < a.dim; c += 32) sum = fmaf(to_f<E>(o[c]), to_f<E>(d[c]), sum);
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+        if (lane == 0) a.delta[head * a.tokens + token] = sum;
+    }
+}
+
+constexpr size_t tiles_bytes(int tiles, int squares, int dp) {
+    return static_cast<size_t>(tiles * T * (dp + 4) + squares * T * LP) * sizeof(float);
+}
+
+template <typename E, int DP>
+cudaError_t attributes() {
+    cudaError_t e = cudaFuncSetAttribute(forward_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(tiles_bytes(3, 1, DP)));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dq_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(tiles_bytes(4, 1, DP)));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dkv_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(tiles_bytes(4, 2, DP)));
+    return e;
+}
+
+// Shared-memory attributes of all instances, once per device.
+cudaError_t prepare() {
+    static PerDevice cache;
+    int dev = 0, ok = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return cache.get(dev, &ok, [](int* out) {
+        *out = 1;
+        cudaError_t r = attributes<float, 64>();
+        if (r == cudaSuccess) r = attributes<float, 128>();
+        if (r == cudaSuccess) r = attributes<__nv_bfloat16, 64>();
+        if (r == cudaSuccess) r = attributes<__nv_bfloat16, 128>();
+        return r;
+    });
+}
+
+template <typename E, int DP>
+cudaError_t forward(AttnArgs a, cudaStream_t s) {
+    a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, T));
+    const unsigned grid = static_cast<unsigned>(a.slots + a.fill) * a.heads;
+    forward_kernel<E, DP><<<grid, kThreads, tiles_bytes(3, 1, DP), s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename E, int DP>
+cudaError_t backward(AttnArgs a, cudaStream_t s) {
+    a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, T));
+    const unsigned rows = static_cast<unsigned>(a.slots + a.fill);
+    dq_kernel<E, DP><<<rows * a.heads, kThreads, tiles_bytes(4, 1, DP), s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    dkv_kernel<E, DP><<<rows * a.kv_heads, kThreads, tiles_bytes(4, 2, DP), s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_simt_forward(const AttnArgs& a, bool f32, cudaStream_t s) {
+    const cudaError_t e = prepare();
+    if (e != cudaSuccess) return e;
+    if (f32) return a.dim <= 64 ? forward<float, 64>(a, s) : forward<float, 128>(a, s);
+    return a.dim <= 64 ? forward<__nv_bfloat16, 64>(a, s) : forward<__nv_bfloat16, 128>(a, s);
+}
+
+cudaError_t attn_simt_backward(const AttnArgs& a, bool f32, cudaStream_t s) {
+    const cudaError_t e = prepare();
+    if (e != cudaSuccess) return e;
+    if (f32) return a.dim <= 64 ? backward<float, 64>(a, s) : backward<float, 128>(a, s);
+    return a.dim <= 64 ? backward<__nv_bfloat16, 64>(a, s) : backward<__nv_bfloat16, 128>(a, s);
+}
+
+cudaError_t attn_delta(const AttnArgs& a, bool f32, cudaStream_t s) {
+    const int64_t blocks = (a.tokens * a.heads + 7) / 8;
+    const unsigned grid = static_cast<unsigned>(blocks < 4864 ? blocks : 4864);
+    if (f32) delta_kernel<float><<<grid, 256, 0, s>>>(a);
+    else delta_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace dmuon
