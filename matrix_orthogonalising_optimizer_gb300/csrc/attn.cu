@@ -68,6 +68,39 @@ int common(AttnArgs& a, const dmuon_heads_t* q, const dmuon_heads_t* k, const dm
     return DMUON_OK;
 }
 
+// Whether TMA reads the rows in place.
+bool tma_rows(const AttnHeads& h) {
+    return reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.token % 8 == 0 && h.head % 8 == 0;
+}
+
+// The tensor-core kernels take what TMA reads and what 16-byte stores write.
+bool tensor_cores(const AttnArgs& a, int32_t dtype, bool backward) {
+    return dtype == DMUON_BF16 && a.dim % 8 == 0 && tma_rows(a.q) && tma_rows(a.k) && tma_rows(a.v) &&
+           (!backward || tma_rows(a.d_o));
+}
+
+int encode(CUtensorMap* map, const AttnHeads& h, int64_t tokens, int heads, int dim) {
+    const auto enc = tensor_map_encoder();
+    if (!enc) return fail(DMUON_ERR_CUDA, "cuTensorMapEncodeTiled entry point not found");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(h.head * 2), static_cast<cuuint64_t>(h.token * 2)};
+    const cuuint32_t box[3] = {64, 1, 128}, estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(h.p), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(DMUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
+    return DMUON_OK;
+}
+
+int set_maps(AttnMaps& m, const AttnArgs& a) {
+    OPS_TRY(encode(&m.q, a.q, a.tokens, a.heads, a.dim));
+    OPS_TRY(encode(&m.k, a.k, a.tokens, a.kv_heads, a.dim));
+    OPS_TRY(encode(&m.v, a.v, a.tokens, a.kv_heads, a.dim));
+    if (a.d_o.p) OPS_TRY(encode(&m.d_o, a.d_o, a.tokens, a.heads, a.dim));
+    return DMUON_OK;
+}
+
 struct Layout {
     float* delta = nullptr;
     size_t bytes = 0;
@@ -106,7 +139,14 @@ extern "C" int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads
     OPS_TRY(check_device(where));
     a.out = o;
     a.lse = lse;
-    OPS_CUDA(attn_simt_forward(a, dtype == DMUON_FP32, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tensor_cores(a, dtype, false)) {
+        AttnMaps m = {};
+        OPS_TRY(set_maps(m, a));
+        OPS_CUDA(attn_tc_forward(a, m, s));
+    } else {
+        OPS_CUDA(attn_simt_forward(a, dtype == DMUON_FP32, s));
+    }
     return DMUON_OK;
 }
 

@@ -89,6 +89,13 @@ __device__ __forceinline__ void attn_clear(const AttnArgs& a, T* x, float* lse, 
     }
 }
 
+// Tensor-core kernels: bf16, rows of 16-byte stride, dim a multiple of 8.
+struct AttnMaps {
+    CUtensorMap q, k, v, d_o;  // dim x heads x tokens, boxes of 64 x 1 x 128
+};
+cudaError_t attn_tc_forward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s);
+cudaError_t attn_fwd_status_word(void** p);  // the forward kernel's time-out flag on the current device
+
 // FFMA kernels (attn_simt.cu): any strides, either type.
 cudaError_t attn_simt_forward(const AttnArgs& a, bool f32, cudaStream_t s);
 cudaError_t attn_simt_backward(const AttnArgs& a, bool f32, cudaStream_t s);

@@ -202,10 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
     load_tile<E, DP>(Q, a.q, b.t.begin + b.row0, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
-    float acc[4][DP / 16], top[4], sum[4];
+    float acc[4][DP / 16], top[4], base[4], sum[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         top[r] = __int_as_float(0xff800000);
+        base[r] = 0.0f;
         sum[r] = 0.0f;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) acc[r][k] = 0.0f;
@@ -230,13 +231,17 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                 m = fmaxf(m, s[r][c]);
             }
             m = row_max(m);
-            // from the maximum before scaling, so that large logits keep their differences
-            const float base = exp_shift(m) * a.scale_log2, old = ex2(fmaf(top[r], a.scale_log2, -base));
+            // what is subtracted is rounded, the same for all of a row's exponentials: the
+            // factor between two maxima comes from the rounded values, and is exactly 1 where
+            // the maximum stays
+            const float fresh = exp_shift(m) * a.scale_log2;
+            const float old = top[r] == __int_as_float(0xff800000) ? 0.0f : ex2(base[r] - fresh);
             top[r] = m;
+            base[r] = fresh;
             float part = 0.0f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float e = ex2(fmaf(s[r][c], a.scale_log2, -base));
+                const float e = ex2(fmaf(s[r][c], a.scale_log2, -fresh));
                 part += e;
                 P[(ty + 16 * r) * LP + tx + 16 * c] = e;
             }
@@ -253,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
         f[r] = 1.0f / sum[r];
         const int i = ty + 16 * r;
         if (tx == 0 && i < b.rows)
-            a.lse[b.head * a.tokens + b.t.begin + b.row0 + i] = fmaf(top[r], a.scale, logf(sum[r]));
+            a.lse[b.head * a.tokens + b.t.begin + b.row0 + i] =
+                (base[r] + log2f(sum[r])) * 0.6931471805599453f;
     }
     store_rows<E, DP>(a.out, acc, f, b.t.begin + b.row0, b.rows, a.heads, b.head, a.dim);
 }

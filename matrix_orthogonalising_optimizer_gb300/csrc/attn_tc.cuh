@@ -1,0 +1,97 @@
+// What the tensor-core kernels of attention share: tiles in shared memory, their
+// descriptors, the products of one 128-row tile, and the end of a CTA.
+//
+// A tile is 128 rows of a head as TMA brings them: one or two boxes of 64 columns,
+// rows of 128 bytes, 128-byte swizzle; columns behind `dim` and rows behind the tensor
+// read as zero.  The same bytes serve as an operand whose contraction runs over the
+// columns (K-major: s = q k^T) and over the rows (MN-major: o = p v).
+#pragma once
+
+#include "act.cuh"
+#include "attn.h"
+#include "tc.cuh"
+
+namespace dmuon {
+namespace attn {
+
+using namespace tc;
+
+constexpr int kRows = 128;
+constexpr int kBox = kRows * 128;  // bytes of a box
+
+template <int DP>
+constexpr int kTile = DP / 64 * kBox;  // bytes of a tile
+
+// M = 128; b_mn: B's contraction runs over its rows.
+__device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return smem_desc(addr, 0, 1024); }
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) { return smem_desc(addr, kBox, 1024); }
+
+// D (128 x 128) = A B^T over the tiles' columns.
+template <int DP>
+__device__ __forceinline__ void product_cols(uint32_t e, uint32_t d, uint64_t a, uint64_t b) {
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) {
+        const uint64_t step = static_cast<uint64_t>((k / 4 * kBox + k % 4 * 32) >> 4);
+        umma_bf16(e, d, a + step, b + step, idesc_of(kRows, false), k != 0 ? 1u : 0u);
+    }
+}
+
+// D (128 x DP) (+)= P B over 16 n rows of B, from row 16 k0 on; P in TMEM.
+template <int DP>
+__device__ __forceinline__ void product_rows(uint32_t e, uint32_t d, uint32_t p, uint64_t b, int k0, int n, bool add) {
+#pragma unroll
+    for (int k = 0; k < n; ++k)
+        umma_bf16_ts(e, d, p + static_cast<uint32_t>(8 * k), b + static_cast<uint64_t>(((k0 + k) * 2048) >> 4),
+                     idesc_of(DP, true), add || k != 0 ? 1u : 0u);
+}
+
+// Loads the tile that begins at a token.
+template <int DP>
+__device__ __forceinline__ void load_tile(uint32_t e, uint32_t dst, const CUtensorMap* map, uint32_t bar, int head,
+                                          int token) {
+#pragma unroll
+    for (int b = 0; b < DP / 64; ++b) tma_load_3d(e, dst + b * kBox, map, bar, 64 * b, head, token);
+}
+
+// Rows [first, 128) of a tile, which belong to another sequence or to none, become
+// zero: their weight in a product over the rows is 0, but 0 times an infinity or NaN
+// is not.  By `threads` threads; visible to the tensor cores after a barrier.
+template <int DP>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int first, int thread, int threads) {
+    const int pieces = (kRows - first) * 8;
+    for (int b = 0; b < DP / 64; ++b)
+        for (int i = thread; i < pieces; i += threads)
+            *reinterpret_cast<uint4*>(tile + b * kBox + first * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+template <int kCols>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(slot)), "n"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+template <int kCols>
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(kCols) : "memory");
+}
+
+// 32 values of a row times f, as bf16, to columns c0 .. of a row of `dim` (a multiple of 8).
+__device__ __forceinline__ void store_row32(__nv_bfloat16* row, const float (&v)[32], float f, int c0, int dim) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (c0 + 8 * k < dim)
+            *reinterpret_cast<uint4*>(row + c0 + 8 * k) =
+                make_uint4(pack_bf16x2(v[8 * k] * f, v[8 * k + 1] * f), pack_bf16x2(v[8 * k + 2] * f, v[8 * k + 3] * f),
+                           pack_bf16x2(v[8 * k + 4] * f, v[8 * k + 5] * f),
+                           pack_bf16x2(v[8 * k + 6] * f, v[8 * k + 7] * f));
+}
+
+}  // namespace attn
+}  // namespace dmuon

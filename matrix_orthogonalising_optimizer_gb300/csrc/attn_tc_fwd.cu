@@ -1,0 +1,351 @@
+// Attention forward on the tensor cores (bf16, rows of 16-byte stride).
+//
+//   s = q k^T, p = exp(scale s - m), o = sum_j p v / sum_j p
+//
+// A CTA takes 256 queries of one head (two tiles of 128) and runs over their keys, 128
+// at a time.  Per tile and key tile the tensor cores form s (128 x 128, in TMEM), a
+// warpgroup turns it into p in bf16 in the same TMEM columns -- a thread has a
+// whole row, so maximum and sum need no exchange --, and the tensor cores add p v to the
+// tile's output in TMEM.  The two tiles alternate: while the warpgroup of one works, the
+// tensor cores run the other's products.  The output is not rescaled whenever the
+// row's maximum grows but only when it has grown by 2^8 since the last time (p then
+// reaches 2^8 at most, exact in fp32 sums and as precise in bf16); s of the tile is
+// complete only after the product before it, so the warpgroup may do that itself.
+//
+// Warp 0 loads (a ring of K and V tiles), warp 1 issues the MMAs, warps 4 .. work on the
+// softmax, one warpgroup per tile.
+//
+// Bound: the tensor cores, 4 * 128 * 128 * dim operations per pair of tiles -- at dim =
+// 128 1024 cycles, against 512 of exponentials and about 400 of instruction issue.
+#include "attn_tc.cuh"
+#include "internal.h"
+#include "ops.h"
+
+namespace dmuon {
+namespace attn {
+namespace {
+
+__device__ int32_t g_status = 0;
+
+constexpr int kSoftWarp0 = 4;
+
+template <int DP, int NT>
+struct Cfg {
+    static constexpr int kThreads = 128 + 128 * NT;
+    static constexpr int kStages = DP == 128 ? 5 : NT == 2 ? 8 : 4;
+    static constexpr uint32_t kCols = NT == 2 ? 512 : 256;
+    static constexpr int kRegsLow = 56, kRegsSoft = NT == 2 ? 224 : 200;  // shares of 168 x 3 or 128 x 2
+    static constexpr int kMinBlocks = DP == 64 && NT == 1 ? 2 : 1;
+};
+
+template <int DP, int NT>
+struct __align__(1024) Smem {
+    uint8_t q[NT][kTile<DP>];
+    uint8_t kv[Cfg<DP, NT>::kStages][kTile<DP>];
+    uint64_t q_full;
+    uint64_t full[Cfg<DP, NT>::kStages];
+    uint64_t empty[Cfg<DP, NT>::kStages];
+    uint64_t s_full[NT];
+    uint64_t p_ready[NT];
+    uint64_t o_full[NT];
+    uint64_t drained;
+    uint32_t tmem;
+};
+
+// Growth of a row's maximum, in powers of two, that is left in p.
+constexpr float kLazy = 8.0f;
+
+template <int DP, int NT>
+__global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks)
+    forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
+                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using C = Cfg<DP, NT>;
+    constexpr int NS = C::kStages;
+    extern __shared__ uint8_t raw[];
+    Smem<DP, NT>& S = *reinterpret_cast<Smem<DP, NT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t slot = blockIdx.x / a.heads;
+    const int head = static_cast<int>(blockIdx.x - slot * a.heads);
+    if (slot >= a.slots) {
+        attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, head, static_cast<int>(slot - a.slots));
+        return;
+    }
+    AttnTile t;
+    if (!attn_find(a, slot, NT * kRows, t)) return;
+    // the tiles with most keys first
+    const int row0 = (a.causal ? (t.len - 1) / (NT * kRows) - t.tile : t.tile) * NT * kRows;
+    const int token0 = static_cast<int>(t.begin);
+    // key tiles of each query tile, 0 where it has no rows
+    int n[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int first = row0 + i * kRows;
+        const int keys = a.causal ? min(t.len, first + kRows) : t.len;
+        n[i] = first < t.len ? (keys + kRows - 1) / kRows : 0;
+    }
+    const int steps = n[NT - 1] > n[0] ? n[NT - 1] : n[0];
+
+    if (warp == 1) {
+        tmem_alloc<C::kCols>(&S.tmem);
+    } else if (warp == 0 && lane == 0) {
+        mbar_init(&S.q_full, 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < NT; ++i) {
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_ready[i], 4);
+            mbar_init(&S.o_full[i], 1);
+        }
+        mbar_init(&S.drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = S.tmem;
+    const uint32_t t_s = tmem, t_o = tmem + NT * kRows;
+
+    if (warp < kSoftWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLow));
+        if (warp == 0) {
+            // ------------------------------------------------ loads
+            const uint32_t e = elect_one();
+            mbar_expect_tx_if(e, &S.q_full, (n[NT - 1] > 0 ? NT : 1) * kTile<DP>);
+            for (int i = 0; i < NT; ++i)
+                if (n[i] > 0) load_tile<DP>(e, saddr(S.q[i]), &mq, saddr(&S.q_full), head, token0 + row0 + i * kRows);
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int i = 0; i < 2 * steps && ok; ++i) {
+                if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[stage], phase ^ 1, &g_status))) {
+                    ok = false;
+                    break;
+                }
+                mbar_expect_tx_if(e, &S.full[stage], kTile<DP>);
+                load_tile<DP>(e, saddr(S.kv[stage]), i & 1 ? &mv : &mk, saddr(&S.full[stage]), head / a.group,
+                              token0 + i / 2 * kRows);
+                if (++stage == NS) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMAs
+            const uint32_t e = elect_one();
+            const uint32_t q0 = saddr(S.q[0]), kv0 = saddr(S.kv[0]);
+            int stage = 0;
+            uint32_t phase = 0;
+            const auto wait = [&](uint64_t* bar, uint32_t parity) {
+                const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &g_status));
+                fence_after();
+                return r;
+            };
+            const auto next = [&] {
+                if (++stage == NS) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
+            bool ok = wait(&S.q_full, 0) && wait(&S.full[0], 0);
+            if (ok) {
+                for (int i = 0; i < NT; ++i) {
+                    if (n[i] == 0) continue;
+                    product_cols<DP>(e, t_s + i * kRows, desc_k(q0 + i * kTile<DP>), desc_k(kv0));
+                    umma_commit(e, saddr(&S.s_full[i]));
+                }
+                umma_commit(e, saddr(&S.empty[0]));
+                next();
+            }
+            for (int j = 0; j < steps && ok; ++j) {
+                const int sv = stage;
+                ok = wait(&S.full[stage], phase);
+                next();
+                const int sk = stage;
+                const bool more = j + 1 < steps;
+                if (ok && more) {
+                    // not before the products that it waits behind: the load is far ahead
+                    ok = wait(&S.full[stage], phase);
+                    next();
+                }
+                for (int i = 0; i < NT && ok; ++i) {
+                    if (j >= n[i]) continue;
+                    ok = wait(&S.p_ready[i], j & 1);
+                    if (!ok) break;
+                    product_rows<DP>(e, t_o + i * DP, t_s + i * kRows, desc_mn(kv0 + sv * kTile<DP>), 0, 8, j > 0);
+                    if (j + 1 < n[i]) {
+                        product_cols<DP>(e, t_s + i * kRows, desc_k(q0 + i * kTile<DP>),
+                                         desc_k(kv0 + sk * kTile<DP>));
+                        umma_commit(e, saddr(&S.s_full[i]));
+                    } else {
+                        umma_commit(e, saddr(&S.o_full[i]));
+                    }
+                }
+                umma_commit(e, saddr(&S.empty[sv]));
+                if (more) umma_commit(e, saddr(&S.empty[sk]));
+            }
+            // also after a wait that gave up: no MMA or commit is under way when the CTA leaves
+            umma_commit(e, saddr(&S.drained));
+            mbar_wait<false>(&S.drained, 0, &g_status);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
+        // ------------------------------------------------ softmax
+        const int tile = (warp - kSoftWarp0) / 4, quarter = warp % 4, thread = threadIdx.x % 128;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t ts = t_s + tile * kRows + lanes, to = t_o + tile * DP + lanes;
+        const int row = row0 + tile * kRows + thread;
+        const int count = NT == 2 && tile == 1 ? n[NT - 1] : n[0];
+        const float c = a.scale_log2;
+        float top = __int_as_float(0xff800000), base = 0.0f, sum = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < count; ++j) {
+            ok = __all_sync(kFullMask, mbar_wait<false>(&S.s_full[tile], j & 1, &g_status));
+            if (!ok) break;
+            fence_after();
+            float s[kRows];
+            tmem_ld128(ts, s);
+            const int keys = min(kRows, t.len - j * kRows);
+            if (keys < kRows || (a.causal && j + 1 == count)) {
+                const int seen = a.causal ? min(row + 1 - j * kRows, keys) : keys;
+#pragma unroll
+                for (int k = 0; k < kRows; ++k)
+                    if (k >= seen) s[k] = __int_as_float(0xff800000);
+            }
+            float m[4] = {top, top, top, top};
+#pragma unroll
+            for (int k = 0; k < kRows; k += 8)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) m[x] = fmaxf(m[x], fmaxf(s[k + 2 * x], s[k + 2 * x + 1]));
+            const float grown = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            if (j == 0) {
+                top = grown;
+                base = exp_shift(top) * c;
+            } else if (__any_sync(kFullMask, (grown - top) * c > kLazy)) {
+                // (a row without a finite logit so far has added nothing)
+                const float fresh = exp_shift(grown) * c;
+                const float f = top == __int_as_float(0xff800000) ? 0.0f : ex2(base - fresh);
+                top = grown;
+                base = fresh;
+                sum *= f;
+#pragma unroll
+                for (int k = 0; k < DP; k += 32) {
+                    float o[32];
+                    uint32_t w[32];
+                    tmem_ld32(to + k, o);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(o[x] * f);
+                    tmem_st32(to + k, w);
+                }
+            }
+            const float2 c2 = both(c), b2 = both(-base);
+            float2 part[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float2 x = fma2(make_float2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), c2, b2);
+                    const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                    part[k % 4] = add2(part[k % 4], p);
+                    w[k] = pack_bf16x2(p.x, p.y);
+                }
+                tmem_st32(ts + 32 * h, w);
+            }
+            const float2 all = add2(add2(part[0], part[1]), add2(part[2], part[3]));
+            sum += all.x + all.y;
+            tmem_st_wait();
+            if (keys < kRows) {
+                // the values of keys behind the sequence
+                const int v = 2 * j + 1;
+                ok = __all_sync(kFullMask, mbar_wait<false>(&S.full[v % NS], (v / NS) & 1, &g_status));
+                if (!ok) break;
+                clear_rows<DP>(S.kv[v % NS], keys, thread, 128);
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_ready[tile]);
+        }
+        if (ok && count > 0) ok = __all_sync(kFullMask, mbar_wait<false>(&S.o_full[tile], 0, &g_status));
+        if (ok && count > 0) {
+            fence_after();
+            const int64_t token = t.begin + row;
+            const float f = 1.0f / sum;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (token * a.heads + head) * a.dim;
+#pragma unroll 1
+            for (int k = 0; k < DP; k += 32) {
+                float o[32];
+                __syncwarp();
+                tmem_ld32(to + k, o);
+                if (row < t.len) store_row32(out, o, f, k, a.dim);
+            }
+            // from what was subtracted, so that lse and p belong together
+            if (row < t.len) a.lse[head * a.tokens + token] = (base + log2f(sum)) * 0.6931471805599453f;
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        fence_after();
+        tmem_free<C::kCols>(tmem);
+    }
+}
+
+template <int DP, int NT>
+constexpr size_t smem_bytes() {
+    return sizeof(Smem<DP, NT>) + 1024;
+}
+
+template <int DP, int NT>
+cudaError_t attribute() {
+    return cudaFuncSetAttribute(forward_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem_bytes<DP, NT>()));
+}
+
+cudaError_t prepare() {
+    static PerDevice cache;
+    int dev = 0, ok = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return cache.get(dev, &ok, [](int* out) {
+        *out = 1;
+        cudaError_t r = attribute<64, 1>();
+        if (r == cudaSuccess) r = attribute<64, 2>();
+        if (r == cudaSuccess) r = attribute<128, 1>();
+        if (r == cudaSuccess) r = attribute<128, 2>();
+        return r;
+    });
+}
+
+template <int DP, int NT>
+cudaError_t launch(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
+    a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, NT * kRows));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.slots + a.fill) * a.heads);
+    cfg.blockDim = dim3(Cfg<DP, NT>::kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<DP, NT>();
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, forward_kernel<DP, NT>, a, m.q, m.k, m.v);
+}
+
+}  // namespace
+}  // namespace attn
+
+cudaError_t attn_fwd_status_word(void** p) { return cudaGetSymbolAddress(p, attn::g_status); }
+
+cudaError_t attn_tc_forward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s) {
+    const cudaError_t e = attn::prepare();
+    if (e != cudaSuccess) return e;
+    return a.dim <= 64 ? attn::launch<64, 2>(a, m, s) : attn::launch<128, 2>(a, m, s);
+}
+
+}  // namespace dmuon

@@ -1,6 +1,8 @@
 // Argument checks and workspace layout that the operators' entry points share.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
@@ -69,6 +71,20 @@ struct Arena {
 }
 
 [[maybe_unused]] bool in_range(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+
+// The driver's tensor-map encoder; NULL if it has none.
+[[maybe_unused]] PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)
+                   : nullptr;
+    }();
+    return enc;
+}
 
 [[maybe_unused]] int check_device(const char* where) {
     static PerDevice cache;  // compute capability, 10 major + minor

@@ -3,13 +3,12 @@
 // kernels around the shared tensor-core GEMM (ops_gemm.cu) -- the operand
 // pack (fp32 into bf16 parts, rows whose stride TMA cannot take into padded
 // ones) and the loss's row pass.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 #include <mutex>
 
 #include "act.cuh"
+#include "attn.h"
 #include "checks.h"
 #include "dmuon.h"
 #include "ops.h"
@@ -42,6 +41,7 @@ constexpr int kPartTokens = 32;
 constexpr int kMaxLaunches = 4;   // GEMM launches of one call (of one piece)
 constexpr int kSlots = 192;       // partial-sum slots: 48 MiB
 constexpr int kTails = 192;       // split tiles per launch
+constexpr int kStatusWords = 3;   // kernels with bounded waits: GEMM, layer norm, attention
 constexpr uint64_t kDefaultBudget = uint64_t(2) << 30;
 
 // ------------------------------------------------------------ workspace
@@ -252,15 +252,7 @@ OpsMat user_mat(const void* p, int64_t ld, bool f32) {
 // ------------------------------------------------------------ products
 
 int encode(CUtensorMap* map, const Operand& o, bool mn, int rows) {
-    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e =
-            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-        return e == cudaSuccess && q == cudaDriverEntryPointSuccess
-                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)
-                   : nullptr;
-    }();
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return fail(DMUON_ERR_CUDA, "cuTensorMapEncodeTiled entry point not found");
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
                                 static_cast<cuuint64_t>(o.parts)};
@@ -609,9 +601,16 @@ bool loss_sizes_ok(int64_t n, int64_t d, int64_t v) {
     return in_range(n, 0, kMaxTokens) && in_range(d, 1, kMaxWidth) && in_range(v, 1, kMaxVocab);
 }
 
-// Reads and clears both time-out flags in one step, so that none set meanwhile is lost.
+// Reads and clears the time-out flags in one step, so that none set meanwhile is lost.
+struct StatusWords {
+    void* p[kStatusWords];
+};
 __device__ int32_t g_taken;
-__global__ void take_status_kernel(int32_t* a, int32_t* b) { g_taken = atomicExch(a, 0) | atomicExch(b, 0); }
+__global__ void take_status_kernel(StatusWords w) {
+    int32_t v = 0;
+    for (int i = 0; i < kStatusWords; ++i) v |= atomicExch(static_cast<int32_t*>(w.p[i]), 0);
+    g_taken = v;
+}
 
 // Rows [r0, r0 + n) of an operand.
 Operand rows_of(const Operand& o, int64_t r0, int64_t n) {
@@ -630,13 +629,14 @@ extern "C" int dmuon_ops_status(void) {
     const char* where = "dmuon_ops_status";
     static std::mutex one;  // g_taken serves one caller at a time
     std::lock_guard<std::mutex> lock(one);
-    void *gemm = nullptr, *norm = nullptr;
-    OPS_CUDA(ops_status_word(&gemm));
-    OPS_CUDA(norm_status_word(&norm));
+    StatusWords words = {};
+    OPS_CUDA(ops_status_word(&words.p[0]));
+    OPS_CUDA(norm_status_word(&words.p[1]));
+    OPS_CUDA(attn_fwd_status_word(&words.p[2]));
     // every stream's calls: a copy alone would wait for the legacy stream and those
     // that synchronise with it
     OPS_CUDA(cudaDeviceSynchronize());
-    take_status_kernel<<<1, 1>>>(static_cast<int32_t*>(gemm), static_cast<int32_t*>(norm));
+    take_status_kernel<<<1, 1>>>(words);
     OPS_CUDA(cudaGetLastError());
     int32_t v = 0;
     OPS_CUDA(cudaMemcpyFromSymbol(&v, g_taken, sizeof(v)));
