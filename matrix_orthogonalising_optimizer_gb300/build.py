@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libdmuon.so")
 SOURCES = ["dmuon.cu", "momentum.cu", "gemm_tc.cu", "gemm_simt.cu", "noalloc.cu", "owners.cpp", "adamw.cu",
            "layer_norm.cu", "ops.cu", "ops_gemm.cu", "ops_stream.cu", "rotary.cu", "attn.cu", "attn_simt.cu",
-           "attn_tc_fwd.cu"]
+           "attn_tc_fwd.cu", "attn_tc_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

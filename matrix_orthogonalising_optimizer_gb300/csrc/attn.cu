@@ -178,6 +178,12 @@ extern "C" int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_he
     a.dv = dv;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     OPS_CUDA(attn_delta(a, f32, s));
-    OPS_CUDA(attn_simt_backward(a, f32, s));
+    if (tensor_cores(a, dtype, true)) {
+        AttnMaps m = {};
+        OPS_TRY(set_maps(m, a));
+        OPS_CUDA(attn_tc_backward(a, m, s));
+    } else {
+        OPS_CUDA(attn_simt_backward(a, f32, s));
+    }
     return DMUON_OK;
 }

@@ -94,7 +94,9 @@ struct AttnMaps {
     CUtensorMap q, k, v, d_o;  // dim x heads x tokens, boxes of 64 x 1 x 128
 };
 cudaError_t attn_tc_forward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s);
-cudaError_t attn_fwd_status_word(void** p);  // the forward kernel's time-out flag on the current device
+cudaError_t attn_tc_backward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s);
+cudaError_t attn_fwd_status_word(void** p);  // the kernels' time-out flags on the current device
+cudaError_t attn_bwd_status_word(void** p);
 
 // FFMA kernels (attn_simt.cu): any strides, either type.
 cudaError_t attn_simt_forward(const AttnArgs& a, bool f32, cudaStream_t s);

@@ -1,0 +1,530 @@
+// Attention backward on the tensor cores (bf16, rows of 16-byte stride).
+//
+//   p = exp(scale s - lse), dp = do v^T, ds = p (dp - delta)
+//   dv = p^T do, dk = scale ds^T q          (a CTA per 128 keys, over the queries)
+//   dq = scale ds k                         (a CTA per 128 queries, over the keys)
+//
+// s and dp are formed twice, once for each side: seven products of 128 x 128 x dim
+// where five would do.  In return every gradient is summed by one CTA in TMEM in a
+// fixed order -- no atomics, no fp32 partial sums through L2 --, and p and ds never
+// pass through shared memory: the side of the keys works on s^T = k q^T, whose rows
+// are what dv and dk need as the left operand in TMEM, the side of the queries on s.
+// Both kinds of CTA are one launch, so that one fills the other's last wave.
+//
+// Keys: TMEM holds s^T and dp^T (p^T and ds^T take their place, bf16), dv and dk.  The
+// tensor cores run dv_i, s_{i+1}, dk_i, dp_{i+1}: the exponentials of tile i + 1 fall
+// under dk_i and dp_{i+1}, and ds_i under dv_i and s_{i+1}.  The query heads that share
+// the key head follow one another.
+// Queries: two buffers of s (ds takes their place), dp and dq; the tensor cores run
+// s_{i+1} while ds_i is made, then dp_{i+1} and dq_i.
+//
+// Warp 0 loads, warp 1 issues the MMAs, warp 2 fetches lse and delta of the query tiles
+// (side of the keys), warps 4 to 11 do the element-wise work, half of the columns
+// each warpgroup.
+#include "attn_tc.cuh"
+#include "internal.h"
+#include "ops.h"
+
+namespace dmuon {
+namespace attn {
+namespace {
+
+__device__ int32_t g_status = 0;
+
+constexpr int kThreads = 384;
+constexpr int kEltWarp0 = 4, kEltWarps = 8;
+constexpr uint32_t kCols = 512;
+constexpr int kRegsLow = 56, kRegsElt = 224;  // 56 + 2 x 224 = 3 x 168: the launch's registers
+
+template <int DP>
+constexpr int kStages = DP == 128 ? 5 : 8;
+
+template <int DP>
+struct __align__(1024) Smem {
+    uint8_t own[2][kTile<DP>];  // queries: Q, dO | keys: K, V
+    uint8_t ring[kStages<DP>][kTile<DP>];
+    float stat[2][2][kRows];    // keys: -lse log2(e) and -delta of two query tiles
+    uint64_t own_full;
+    uint64_t full[kStages<DP>];
+    uint64_t empty[kStages<DP>];
+    uint64_t s_full[2];
+    uint64_t g_full;            // dp
+    uint64_t p_ready;
+    uint64_t ds_ready;
+    uint64_t stat_full[2];
+    uint64_t stat_empty[2];
+    uint64_t done;
+    uint32_t tmem;
+};
+
+template <int DP>
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages<DP>) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+    const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &g_status));
+    fence_after();
+    return r;
+}
+
+// One arrival per warp, after its TMEM stores and its writes to shared memory.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+    tmem_st_wait();
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// Loads the CTA's own two tiles, then `steps` pairs through the ring: pair i of
+// (first, second) begins at row(i) of head(i).
+template <int DP, typename F>
+__device__ __forceinline__ void produce(Smem<DP>& S, const CUtensorMap* own0, const CUtensorMap* own1, int own_head,
+                                        int own_token, const CUtensorMap* r0, const CUtensorMap* r1, int steps, F where) {
+    const uint32_t e = elect_one();
+    mbar_expect_tx_if(e, &S.own_full, 2 * kTile<DP>);
+    load_tile<DP>(e, saddr(S.own[0]), own0, saddr(&S.own_full), own_head, own_token);
+    load_tile<DP>(e, saddr(S.own[1]), own1, saddr(&S.own_full), own_head, own_token);
+    Ring<DP> r;
+    for (int i = 0; i < 2 * steps; ++i) {
+        if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[r.stage], r.phase ^ 1, &g_status))) return;
+        int head, token;
+        where(i / 2, head, token);
+        mbar_expect_tx_if(e, &S.full[r.stage], kTile<DP>);
+        load_tile<DP>(e, saddr(S.ring[r.stage]), i & 1 ? r1 : r0, saddr(&S.full[r.stage]), head, token);
+        r.next();
+    }
+}
+
+// 64 columns, packed, into TMEM columns t .. t + 31.
+__device__ __forceinline__ void store_cols64(uint32_t t, const float (&v)[64]) {
+    uint32_t w[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    tmem_st32(t, w);
+}
+
+template <int DP>
+__device__ __forceinline__ void store_cols(__nv_bfloat16* row, uint32_t t, int c0, int c1, float f, int dim, bool in) {
+#pragma unroll 1
+    for (int k = c0; k < c1; k += 32) {
+        float v[32];
+        __syncwarp();
+        tmem_ld32(t + k, v);
+        if (in) store_row32(row, v, f, k, dim);
+    }
+}
+
+// ---------------------------------------------------------------- side of the keys
+
+template <int DP, bool kElt>
+__device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq, const CUtensorMap* mk,
+                                          const CUtensorMap* mv, const CUtensorMap* mo, const AttnTile& t, int kv,
+                                          int warp, int lane, uint32_t tmem) {
+    const int token0 = static_cast<int>(t.begin), row0 = t.tile * kRows;
+    const int first = a.causal ? row0 : 0;                             // the first query that sees any of the keys
+    const int per_head = (t.len - first + kRows - 1) / kRows, steps = per_head * a.group;
+    const uint32_t t_s = tmem, t_g = tmem + kRows, t_dv = tmem + 2 * kRows, t_dk = t_dv + DP;
+    const auto where = [&](int i, int& head, int& row) {
+        const int h = i / per_head;
+        head = kv * a.group + h;
+        row = first + (i - h * per_head) * kRows;
+    };
+    if (!kElt && warp == 0) {
+        produce<DP>(S, mk, mv, kv, token0 + row0, mq, mo, steps, [&](int i, int& head, int& token) {
+            where(i, head, token);
+            token += token0;
+        });
+    } else if (!kElt && warp == 1) {
+        const uint32_t e = elect_one();
+        const uint32_t own = saddr(S.own[0]), ring = saddr(S.ring[0]);
+        const uint64_t dk_k = desc_k(own), dk_v = desc_k(own + kTile<DP>);
+        Ring<DP> r;
+        bool ok = wait_warp(&S.own_full, 0) && wait_warp(&S.full[0], 0);
+        int sq = 0, so = 0;  // ring slots of the tile at hand
+        if (ok) {
+            product_cols<DP>(e, t_s, dk_k, desc_k(ring));
+            umma_commit(e, saddr(&S.s_full[0]));
+            r.next();
+            so = r.stage;
+            ok = wait_warp(&S.full[r.stage], r.phase);
+        }
+        if (ok) {
+            product_cols<DP>(e, t_g, dk_v, desc_k(ring + so * kTile<DP>));
+            umma_commit(e, saddr(&S.g_full));
+            r.next();
+        }
+        for (int i = 0; i < steps && ok; ++i) {
+            const bool more = i + 1 < steps;
+            const int sq1 = r.stage;
+            ok = wait_warp(&S.p_ready, i & 1);
+            if (!ok) break;
+            product_rows<DP>(e, t_dv, t_s, desc_mn(ring + so * kTile<DP>), 0, 4, i > 0);
+            product_rows<DP>(e, t_dv, t_s + 64, desc_mn(ring + so * kTile<DP>), 4, 4, true);
+            umma_commit(e, saddr(&S.empty[so]));
+            if (more) {
+                ok = wait_warp(&S.full[r.stage], r.phase);
+                if (!ok) break;
+                product_cols<DP>(e, t_s, dk_k, desc_k(ring + sq1 * kTile<DP>));
+                umma_commit(e, saddr(&S.s_full[0]));
+                r.next();
+                so = r.stage;
+            }
+            ok = wait_warp(&S.ds_ready, i & 1);
+            if (!ok) break;
+            product_rows<DP>(e, t_dk, t_g, desc_mn(ring + sq * kTile<DP>), 0, 4, i > 0);
+            product_rows<DP>(e, t_dk, t_g + 64, desc_mn(ring + sq * kTile<DP>), 4, 4, true);
+            umma_commit(e, saddr(&S.empty[sq]));
+            if (more) {
+                ok = wait_warp(&S.full[r.stage], r.phase);
+                if (!ok) break;
+                product_cols<DP>(e, t_g, dk_v, desc_k(ring + so * kTile<DP>));
+                umma_commit(e, saddr(&S.g_full));
+                r.next();
+                sq = sq1;
+            }
+        }
+        // also after a wait that gave up: no MMA or commit is under way when the CTA leaves
+        umma_commit(e, saddr(&S.done));
+        mbar_wait<false>(&S.done, 0, &g_status);
+    } else if (!kElt && warp == 2) {
+        for (int i = 0; i < steps; ++i) {
+            const int st = i & 1;
+            if (!wait_warp(&S.stat_empty[st], ((i >> 1) & 1) ^ 1)) break;
+            int head, row;
+            where(i, head, row);
+            const int64_t at = head * a.tokens + token0 + row;
+#pragma unroll
+            for (int k = lane; k < kRows; k += 32) {
+                const bool in = row + k < t.len;
+                S.stat[st][0][k] = in ? a.lse[at + k] * -kLog2e : 0.0f;
+                S.stat[st][1][k] = in ? -a.delta[at + k] : 0.0f;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.stat_full[st]);
+        }
+    } else if (kElt) {
+        const int half = (warp - kEltWarp0) / 4, thread = threadIdx.x - 32 * kEltWarp0, r = thread % kRows;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        const uint32_t ts = t_s + 64 * half + lanes, tg = t_g + 64 * half + lanes;
+        const float2 c2 = both(a.scale_log2);
+        bool ok = true;
+        for (int i = 0; i < steps && ok; ++i) {
+            const int st = i & 1;
+            int head, row;
+            where(i, head, row);
+            const int queries = min(kRows, t.len - row);
+            // columns of this half that see key r: [lo, hi)
+            const bool masked = queries < kRows || (a.causal && row == row0);
+            const int lo = (a.causal ? row0 + r - row : 0) - 64 * half, hi = queries - 64 * half;
+            ok = wait_warp(&S.stat_full[st], (i >> 1) & 1) && wait_warp(&S.s_full[0], i & 1);
+            if (!ok) break;
+            float p[64];
+            tmem_ld64(ts, p);
+            const float4* nl = reinterpret_cast<const float4*>(&S.stat[st][0][64 * half]);
+#pragma unroll
+            for (int k = 0; k < 64; k += 4) {
+                const float4 l = nl[k / 4];
+                const float2 x = fma2(make_float2(p[k], p[k + 1]), c2, make_float2(l.x, l.y));
+                const float2 y = fma2(make_float2(p[k + 2], p[k + 3]), c2, make_float2(l.z, l.w));
+                p[k] = ex2(x.x);
+                p[k + 1] = ex2(x.y);
+                p[k + 2] = ex2(y.x);
+                p[k + 3] = ex2(y.y);
+            }
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                    if (k < lo || k >= hi) p[k] = 0.0f;
+            }
+            store_cols64(ts, p);
+            if (queries < kRows) {
+                // query rows behind the sequence, of dO before dv reads it, of Q before dk does
+                const int o = 2 * i + 1;
+                ok = wait_warp(&S.full[o % kStages<DP>], (o / kStages<DP>) & 1);
+                if (!ok) break;
+                clear_rows<DP>(S.ring[o % kStages<DP>], queries, thread, 256);
+                clear_rows<DP>(S.ring[2 * i % kStages<DP>], queries, thread, 256);
+            }
+            arrive_warp(&S.p_ready, lane);
+            ok = wait_warp(&S.g_full, i & 1);
+            if (!ok) break;
+            const float4* nd = reinterpret_cast<const float4*>(&S.stat[st][1][64 * half]);
+            uint32_t w[32];
+#pragma unroll
+            for (int h = 0; h < 64; h += 32) {
+                float g[32];
+                tmem_ld32(tg + h, g);
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 d = nd[(h + k) / 4];
+                    float2 x = add2(make_float2(g[k], g[k + 1]), make_float2(d.x, d.y));
+                    float2 y = add2(make_float2(g[k + 2], g[k + 3]), make_float2(d.z, d.w));
+                    x = mul2(x, make_float2(p[h + k], p[h + k + 1]));
+                    y = mul2(y, make_float2(p[h + k + 2], p[h + k + 3]));
+                    if (masked) {
+                        // not 0 times what the columns behind the sequence hold
+                        x.x = h + k < lo || h + k >= hi ? 0.0f : x.x;
+                        x.y = h + k + 1 < lo || h + k + 1 >= hi ? 0.0f : x.y;
+                        y.x = h + k + 2 < lo || h + k + 2 >= hi ? 0.0f : y.x;
+                        y.y = h + k + 3 < lo || h + k + 3 >= hi ? 0.0f : y.y;
+                    }
+                    w[(h + k) / 2] = pack_bf16x2(x.x, x.y);
+                    w[(h + k) / 2 + 1] = pack_bf16x2(y.x, y.y);
+                }
+            }
+            tmem_st32(tg, w);
+            arrive_warp(&S.ds_ready, lane);
+            if (lane == 0) mbar_arrive(&S.stat_empty[st]);
+        }
+        if (ok && wait_warp(&S.done, 0)) {
+            // one warpgroup stores dv, the other dk
+            const int64_t token = t.begin + row0 + r;
+            void* out = half ? a.dk : a.dv;
+            store_cols<DP>(static_cast<__nv_bfloat16*>(out) + (token * a.kv_heads + kv) * a.dim,
+                           (half ? t_dk : t_dv) + lanes, 0, DP, half ? a.scale : 1.0f, a.dim, row0 + r < t.len);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- side of the queries
+
+template <int DP, bool kElt>
+__device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq,
+                                             const CUtensorMap* mk, const CUtensorMap* mv, const CUtensorMap* mo,
+                                             const AttnTile& t, int head, int warp, int lane, uint32_t tmem) {
+    // the tiles with most keys first
+    const int token0 = static_cast<int>(t.begin);
+    const int row0 = (a.causal ? (t.len - 1) / kRows - t.tile : t.tile) * kRows;
+    const int keys_all = a.causal ? min(t.len, row0 + kRows) : t.len;
+    const int steps = (keys_all + kRows - 1) / kRows;
+    const uint32_t t_s = tmem, t_g = tmem + 2 * kRows, t_dq = tmem + 3 * kRows;
+    if (!kElt && warp == 0) {
+        produce<DP>(S, mq, mo, head, token0 + row0, mk, mv, steps, [&](int i, int& h, int& token) {
+            h = head / a.group;
+            token = token0 + i * kRows;
+        });
+    } else if (!kElt && warp == 1) {
+        const uint32_t e = elect_one();
+        const uint32_t own = saddr(S.own[0]), ring = saddr(S.ring[0]);
+        const uint64_t d_q = desc_k(own), d_o = desc_k(own + kTile<DP>);
+        Ring<DP> r;
+        bool ok = wait_warp(&S.own_full, 0) && wait_warp(&S.full[0], 0);
+        int sk = 0;
+        if (ok) {
+            product_cols<DP>(e, t_s, d_q, desc_k(ring));
+            umma_commit(e, saddr(&S.s_full[0]));
+            r.next();
+            ok = wait_warp(&S.full[r.stage], r.phase);
+        }
+        if (ok) {
+            product_cols<DP>(e, t_g, d_o, desc_k(ring + r.stage * kTile<DP>));
+            umma_commit(e, saddr(&S.g_full));
+            umma_commit(e, saddr(&S.empty[r.stage]));
+            r.next();
+        }
+        for (int i = 0; i < steps && ok; ++i) {
+            const bool more = i + 1 < steps;
+            const int sk1 = r.stage, b = i & 1;
+            if (more) {
+                // the other buffer's ds was read by the product before
+                ok = wait_warp(&S.full[r.stage], r.phase);
+                if (!ok) break;
+                product_cols<DP>(e, t_s + (b ^ 1) * kRows, d_q, desc_k(ring + sk1 * kTile<DP>));
+                umma_commit(e, saddr(&S.s_full[b ^ 1]));
+                r.next();
+            }
+            ok = wait_warp(&S.ds_ready, i & 1);
+            if (!ok) break;
+            if (more) {
+                ok = wait_warp(&S.full[r.stage], r.phase);
+                if (!ok) break;
+                product_cols<DP>(e, t_g, d_o, desc_k(ring + r.stage * kTile<DP>));
+                umma_commit(e, saddr(&S.g_full));
+                umma_commit(e, saddr(&S.empty[r.stage]));
+                r.next();
+            }
+            product_rows<DP>(e, t_dq, t_s + b * kRows, desc_mn(ring + sk * kTile<DP>), 0, 4, i > 0);
+            product_rows<DP>(e, t_dq, t_s + b * kRows + 64, desc_mn(ring + sk * kTile<DP>), 4, 4, true);
+            umma_commit(e, saddr(&S.empty[sk]));
+            sk = sk1;
+        }
+        umma_commit(e, saddr(&S.done));
+        mbar_wait<false>(&S.done, 0, &g_status);
+    } else if (kElt) {
+        const int half = (warp - kEltWarp0) / 4, thread = threadIdx.x - 32 * kEltWarp0, r = thread % kRows;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        const uint32_t tg = t_g + 64 * half + lanes;
+        const int row = row0 + r;
+        const bool in = row < t.len;
+        const int64_t token = t.begin + row;
+        const float2 c2 = both(a.scale_log2);
+        const float2 nl = both(in ? a.lse[head * a.tokens + token] * -kLog2e : 0.0f);
+        const float2 nd = both(in ? -a.delta[head * a.tokens + token] : 0.0f);
+        bool ok = true;
+        for (int i = 0; i < steps && ok; ++i) {
+            const int b = i & 1, keys = min(kRows, t.len - i * kRows);
+            const uint32_t ts = t_s + b * kRows + 64 * half + lanes;
+            ok = wait_warp(&S.s_full[b], (i >> 1) & 1);
+            if (!ok) break;
+            float p[64];
+            tmem_ld64(ts, p);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+                const float2 x = fma2(make_float2(p[k], p[k + 1]), c2, nl);
+                p[k] = ex2(x.x);
+                p[k + 1] = ex2(x.y);
+            }
+            ok = wait_warp(&S.g_full, i & 1);
+            if (!ok) break;
+            const bool masked = keys < kRows || (a.causal && i + 1 == steps);
+            const int seen = (a.causal ? min(row + 1 - i * kRows, keys) : keys) - 64 * half;
+            uint32_t w[32];
+#pragma unroll
+            for (int h = 0; h < 64; h += 32) {
+                float g[32];
+                tmem_ld32(tg + h, g);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float2 x = mul2(make_float2(p[h + k], p[h + k + 1]), add2(make_float2(g[k], g[k + 1]), nd));
+                    if (masked) {
+                        x.x = h + k < seen ? x.x : 0.0f;
+                        x.y = h + k + 1 < seen ? x.y : 0.0f;
+                    }
+                    w[(h + k) / 2] = pack_bf16x2(x.x, x.y);
+                }
+            }
+            tmem_st32(ts, w);
+            if (keys < kRows) clear_rows<DP>(S.ring[2 * i % kStages<DP>], keys, thread, 256);  // keys behind the sequence
+            arrive_warp(&S.ds_ready, lane);
+        }
+        if (ok && wait_warp(&S.done, 0))
+            store_cols<DP>(static_cast<__nv_bfloat16*>(a.out) + (token * a.heads + head) * a.dim, t_dq + lanes,
+                           half * (DP / 2), (half + 1) * (DP / 2), a.scale, a.dim, in);
+    }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    backward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
+                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                    const __grid_constant__ CUtensorMap mo) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Smem<DP>& S = *reinterpret_cast<Smem<DP>*>(raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // blocks of the keys, then blocks of the queries
+    const int64_t per_slot = a.kv_heads, rows = static_cast<int64_t>(a.slots) + a.fill;
+    int64_t block = blockIdx.x;
+    const bool keys = block < rows * per_slot;
+    if (!keys) block -= rows * per_slot;
+    const int heads = keys ? a.kv_heads : a.heads;
+    const int64_t slot = block / heads;
+    const int head = static_cast<int>(block - slot * heads);
+    if (slot >= a.slots) {
+        const int f = static_cast<int>(slot - a.slots);
+        if (keys) attn_clear(a, static_cast<__nv_bfloat16*>(a.dk), nullptr, heads, head, f);
+        attn_clear(a, static_cast<__nv_bfloat16*>(keys ? a.dv : a.out), nullptr, heads, head, f);
+        return;
+    }
+    AttnTile t;
+    if (!attn_find(a, slot, kRows, t)) return;
+    if (saddr(raw) % 1024 != 0) {  // no room was taken for aligning it here
+        if (threadIdx.x == 0) atomicExch(&g_status, 1);
+        return;
+    }
+    if (warp == 1) {
+        tmem_alloc<kCols>(&S.tmem);
+    } else if (warp == 0 && lane == 0) {
+        mbar_init(&S.own_full, 1);
+        for (int i = 0; i < kStages<DP>; ++i) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.stat_full[i], 1);
+            mbar_init(&S.stat_empty[i], kEltWarps);
+        }
+        mbar_init(&S.g_full, 1);
+        mbar_init(&S.p_ready, kEltWarps);
+        mbar_init(&S.ds_ready, kEltWarps);
+        mbar_init(&S.done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = S.tmem;
+    if (warp < kEltWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+        if (keys) keys_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
+        else queries_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsElt));
+        if (keys) keys_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
+        else queries_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        fence_after();
+        tmem_free<kCols>(tmem);
+    }
+}
+
+template <int DP>
+cudaError_t attribute() {
+    static_assert(sizeof(Smem<DP>) <= 232448, "shared memory of a block");
+    return cudaFuncSetAttribute(backward_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(sizeof(Smem<DP>)));
+}
+
+cudaError_t prepare() {
+    static PerDevice cache;
+    int dev = 0, ok = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return cache.get(dev, &ok, [](int* out) {
+        *out = 1;
+        const cudaError_t r = attribute<64>();
+        return r == cudaSuccess ? attribute<128>() : r;
+    });
+}
+
+template <int DP>
+cudaError_t launch(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
+    a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, kRows));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.slots + a.fill) * (a.heads + a.kv_heads));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Smem<DP>);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, backward_kernel<DP>, a, m.q, m.k, m.v, m.d_o);
+}
+
+}  // namespace
+}  // namespace attn
+
+cudaError_t attn_bwd_status_word(void** p) { return cudaGetSymbolAddress(p, attn::g_status); }
+
+cudaError_t attn_tc_backward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s) {
+    const cudaError_t e = attn::prepare();
+    if (e != cudaSuccess) return e;
+    return a.dim <= 64 ? attn::launch<64>(a, m, s) : attn::launch<128>(a, m, s);
+}
+
+}  // namespace dmuon

@@ -41,7 +41,7 @@ constexpr int kPartTokens = 32;
 constexpr int kMaxLaunches = 4;   // GEMM launches of one call (of one piece)
 constexpr int kSlots = 192;       // partial-sum slots: 48 MiB
 constexpr int kTails = 192;       // split tiles per launch
-constexpr int kStatusWords = 3;   // kernels with bounded waits: GEMM, layer norm, attention
+constexpr int kStatusWords = 4;   // kernels with bounded waits: GEMM, layer norm, attention
 constexpr uint64_t kDefaultBudget = uint64_t(2) << 30;
 
 // ------------------------------------------------------------ workspace
@@ -633,6 +633,7 @@ extern "C" int dmuon_ops_status(void) {
     OPS_CUDA(ops_status_word(&words.p[0]));
     OPS_CUDA(norm_status_word(&words.p[1]));
     OPS_CUDA(attn_fwd_status_word(&words.p[2]));
+    OPS_CUDA(attn_bwd_status_word(&words.p[3]));
     // every stream's calls: a copy alone would wait for the legacy stream and those
     // that synchronise with it
     OPS_CUDA(cudaDeviceSynchronize());
