@@ -6,15 +6,27 @@
 //      token's position: a cos - b sin, a sin + b cos; the others unchanged
 //   dn = dy turned back, dw = sum dn x r, g = dn w, dx = r (g - x r mean(g x r))
 //
-// HBM-bound: a row is read once, held in registers as fp32 and written once.  One
-// warp per row; the row goes through shared memory once so that any pairing can
-// be formed.
+// HBM-bound: a row is read once, held in registers as fp32 and written once.
+//
+// Vector kernels (rows on 16 bytes, dim and rotary multiples of 16): a lane holds 16
+// elements of a row, and both elements of each of their pairs -- columns 8 t .. and
+// rotary / 2 + 8 t .., or 16 t .. interleaved --, so the rotation needs no exchange.
+// A warp goes over the heads of one token, 32 / (dim / 16) rows at a time, with the
+// position's cos and sin in registers; a few tokens are shared out among more warps.
+// The rows come through shared memory by cp.async, so that the bytes in flight do not
+// cost registers.  The weights' gradients stay in the lanes'
+// registers over all of a warp's rows; the block adds them up in a fixed order, and a
+// second kernel the blocks' sums.
+//
+// Other rows: one warp per row, which goes through shared memory once so that any
+// pairing can be formed.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
 
 #include "checks.h"
+#include "tc.cuh"
 
 namespace dmuon {
 namespace {
@@ -25,7 +37,7 @@ constexpr int kWarps = 8;
 constexpr int kPer = kMaxDim / 32;  // elements of a lane
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int kMaxHeads = 1024;
-constexpr int kMaxPartials = 608;   // blocks of the backward pass: rows of partial sums
+constexpr int kMaxBlocks = 304;     // two per SM; backward: rows of partial sums
 
 struct Rows {
     const void* x;
@@ -34,6 +46,8 @@ struct Rows {
     void* out;
     int64_t x_token, x_head, dy_token, dy_head;
     int32_t heads;
+    int32_t first, blocks;     // the blocks that work on them
+    int32_t split, per;        // vector kernels: warps that share a token's heads, steps of each
 };
 
 struct RotArgs {
@@ -43,7 +57,7 @@ struct RotArgs {
     int64_t tokens, table_rows;
     int32_t dim, rotary, interleaved, norm;
     float eps;
-    float* partial;            // backward: [blocks][2][dim], NULL: no weight gradients
+    float* partial;            // backward: [blocks][dim], NULL: no weight gradients
 };
 
 template <typename E>
@@ -79,111 +93,506 @@ __device__ __forceinline__ float turned(const RotArgs& a, const float* s, const 
 template <typename E, bool kBack>
 __global__ void __launch_bounds__(32 * kWarps) rows_kernel(const __grid_constant__ RotArgs a) {
     __shared__ float rows[kWarps][kMaxDim];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     float* s = rows[warp];
-    for (int part = 0; part < 2; ++part) {
-        const Rows& R = a.r[part];
-        float dw[kPer];
+    const Rows& R = a.r[blockIdx.x < static_cast<unsigned>(a.r[1].first) ? 0 : 1];
+    float dw[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) dw[i] = 0.0f;
-        const int64_t n = a.tokens * R.heads;
-        for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp; row < n; row += gridDim.x * kWarps) {
-            const int64_t token = row / R.heads, head = row - token * R.heads;
-            const float* cs = nullptr;
-            if (a.table) {
-                const int64_t p = a.positions[token];
-                if (p >= 0 && p < a.table_rows) cs = a.table + p * a.rotary;
-            }
-            const E* px = static_cast<const E*>(R.x) + token * R.x_token + head * R.x_head;
-            const E* w = static_cast<const E*>(R.w);
-            E* out = static_cast<E*>(R.out) + row * a.dim;
-            float x[kPer], r = 1.0f;
-            if (!kBack || a.norm) {
+    for (int i = 0; i < kPer; ++i) dw[i] = 0.0f;
+    const int64_t n = a.tokens * R.heads;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x - R.first) * kWarps + warp; row < n; row += R.blocks * kWarps) {
+        const int64_t token = row / R.heads, head = row - token * R.heads;
+        const float* cs = nullptr;
+        if (a.table) {
+            const int64_t p = a.positions[token];
+            if (p >= 0 && p < a.table_rows) cs = a.table + p * a.rotary;
+        }
+        const E* px = static_cast<const E*>(R.x) + token * R.x_token + head * R.x_head;
+        const E* w = static_cast<const E*>(R.w);
+        E* out = static_cast<E*>(R.out) + row * a.dim;
+        float x[kPer], r = 1.0f;
+        if (!kBack || a.norm) {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) x[i] = lane + 32 * i < a.dim ? to_f<E>(px[lane + 32 * i]) : 0.0f;
-            }
-            if (a.norm) {
-                float q = 0.0f;
+            for (int i = 0; i < kPer; ++i) x[i] = lane + 32 * i < a.dim ? to_f<E>(px[lane + 32 * i]) : 0.0f;
+        }
+        if (a.norm) {
+            float q = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) q = fmaf(x[i], x[i], q);
-                r = 1.0f / sqrtf(warp_sum(q) / static_cast<float>(a.dim) + a.eps);
-            }
-            if constexpr (!kBack) {
+            for (int i = 0; i < kPer; ++i) q = fmaf(x[i], x[i], q);
+            r = 1.0f / sqrtf(warp_sum(q) / static_cast<float>(a.dim) + a.eps);
+        }
+        if constexpr (!kBack) {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e < a.dim) s[e] = a.norm ? x[i] * r * (w ? to_f<E>(w[e]) : 1.0f) : x[i];
-                }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e < a.dim) out[e] = from_f<E>(turned(a, s, cs, e, 1.0f));
-                }
-            } else {
-                const E* pd = static_cast<const E*>(R.dy) + token * R.dy_token + head * R.dy_head;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e < a.dim) s[e] = to_f<E>(pd[e]);
-                }
-                __syncwarp();
-                float g[kPer], dot = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int e = lane + 32 * i;
-                    g[i] = e < a.dim ? turned(a, s, cs, e, -1.0f) : 0.0f;
-                    if (a.norm && e < a.dim) {
-                        x[i] *= r;
-                        dw[i] = fmaf(g[i], x[i], dw[i]);
-                        if (w) g[i] *= to_f<E>(w[e]);
-                        dot = fmaf(g[i], x[i], dot);
-                    }
-                }
-                if (a.norm) dot = warp_sum(dot) / static_cast<float>(a.dim);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e < a.dim) out[e] = from_f<E>(a.norm ? r * (g[i] - x[i] * dot) : g[i]);
-                }
+            for (int i = 0; i < kPer; ++i) {
+                const int e = lane + 32 * i;
+                if (e < a.dim) s[e] = a.norm ? x[i] * r * (w ? to_f<E>(w[e]) : 1.0f) : x[i];
             }
             __syncwarp();
-        }
-        if constexpr (kBack) {
-            if (!a.partial) continue;
-            // the block's sums, warp after warp
-            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) s[lane + 32 * i] = dw[i];
-            __syncthreads();
-            for (int e = threadIdx.x; e < a.dim; e += 32 * kWarps) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) sum += rows[k][e];
-                a.partial[(static_cast<int64_t>(blockIdx.x) * 2 + part) * a.dim + e] = sum;
+            for (int i = 0; i < kPer; ++i) {
+                const int e = lane + 32 * i;
+                if (e < a.dim) out[e] = from_f<E>(turned(a, s, cs, e, 1.0f));
             }
-            __syncthreads();
+        } else {
+            const E* pd = static_cast<const E*>(R.dy) + token * R.dy_token + head * R.dy_head;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int e = lane + 32 * i;
+                if (e < a.dim) s[e] = to_f<E>(pd[e]);
+            }
+            __syncwarp();
+            float g[kPer], dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int e = lane + 32 * i;
+                g[i] = e < a.dim ? turned(a, s, cs, e, -1.0f) : 0.0f;
+                if (a.norm && e < a.dim) {
+                    x[i] *= r;
+                    dw[i] = fmaf(g[i], x[i], dw[i]);
+                    if (w) g[i] *= to_f<E>(w[e]);
+                    dot = fmaf(g[i], x[i], dot);
+                }
+            }
+            if (a.norm) dot = warp_sum(dot) / static_cast<float>(a.dim);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int e = lane + 32 * i;
+                if (e < a.dim) out[e] = from_f<E>(a.norm ? r * (g[i] - x[i] * dot) : g[i]);
+            }
+        }
+        __syncwarp();
+    }
+    if constexpr (kBack) {
+        if (!a.partial) return;
+        // the block's sums, warp after warp
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) s[lane + 32 * i] = dw[i];
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.dim; e += 32 * kWarps) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) sum += rows[k][e];
+            a.partial[static_cast<int64_t>(blockIdx.x) * a.dim + e] = sum;
         }
     }
 }
 
-// Weight gradients from the partial sums [n][2][dim], always in the same order: 32
-// columns per block, 32 threads each.
+// ---------------------------------------------------------------- vector kernels
+
+// Eight elements that a lane holds as one or two 16-byte words, 32 lanes apart.
 template <typename E>
-__global__ void __launch_bounds__(1024) reduce_kernel(const float* partial, int n, int dim, void* dq, void* dk) {
+__device__ __forceinline__ void unpack8(const uint4* d, int step, float (&v)[8]) {
+    if constexpr (sizeof(E) == 2) {
+        const uint4 w = *d;
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = tc::unpack_bf16x2(u[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 w = d[i * step];
+            v[4 * i] = __uint_as_float(w.x);
+            v[4 * i + 1] = __uint_as_float(w.y);
+            v[4 * i + 2] = __uint_as_float(w.z);
+            v[4 * i + 3] = __uint_as_float(w.w);
+        }
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ void store8(E* p, const float (&v)[8]) {
+    if constexpr (sizeof(E) == 2) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]),
+                                                  tc::pack_bf16x2(v[4], v[5]), tc::pack_bf16x2(v[6], v[7]));
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::saddr(dst)), "l"(src) : "memory");
+}
+
+// Eight elements into the words of unpack8.
+template <typename E>
+__device__ __forceinline__ void copy8(uint4* dst, const E* src) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(E)) / 2; ++i) copy16(dst + 32 * i, src + 16 / sizeof(E) * i);
+}
+
+// Elements i and i + 1, for packed arithmetic.
+__device__ __forceinline__ float2 pair(const float (&v)[8], int i) { return make_float2(v[i], v[i + 1]); }
+__device__ __forceinline__ void set(float (&v)[8], int i, float2 x) {
+    v[i] = x.x;
+    v[i + 1] = x.y;
+}
+__device__ __forceinline__ float2 negated(float2 x) { return make_float2(-x.x, -x.y); }
+
+// Two stored vectors as the elements a and b of eight pairs, and back.
+template <bool kInter>
+__device__ __forceinline__ void to_pairs(const float (&v0)[8], const float (&v1)[8], float (&a)[8], float (&b)[8]) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        a[p] = !kInter ? v0[p] : p < 4 ? v0[2 * (p % 4)] : v1[2 * (p % 4)];
+        b[p] = !kInter ? v1[p] : p < 4 ? v0[2 * (p % 4) + 1] : v1[2 * (p % 4) + 1];
+    }
+}
+
+template <bool kInter>
+__device__ __forceinline__ void from_pairs(const float (&a)[8], const float (&b)[8], float (&v0)[8], float (&v1)[8]) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        v0[p] = !kInter ? a[p] : p % 2 ? b[p / 2] : a[p / 2];
+        v1[p] = !kInter ? b[p] : p % 2 ? b[4 + p / 2] : a[4 + p / 2];
+    }
+}
+
+// Stages of a warp's ring (8 KB of rows), and its shared memory.
+template <typename E, bool kBack>
+constexpr int kStages = (sizeof(E) == 2 ? 8 : 4) / (kBack ? 2 : 1);
+
+template <typename E, int G, bool kBack>
+struct WarpRing {
+    static constexpr int kWords = static_cast<int>(sizeof(E)) * (kBack ? 2 : 1);  // 16-byte words of a lane and stage
+    uint4 x[kStages<E, kBack>][kWords][32];
+    float4 cs[kStages<E, kBack>][4][G];  // per token: cos of pairs 8 t .., their sines
+    int64_t pos[kStages<E, kBack>];
+};
+
+// G: lanes of a row, a power of two with 16 G >= dim.  Steps of a warp: 32 / G heads of
+// a token; the rows come through the lanes' own slots of a ring by cp.async, a whole
+// ring ahead, and cos and sin with a token's first step.
+template <typename E, int G, bool kBack, bool kInter>
+__global__ void __launch_bounds__(32 * kWarps, 2) vector_kernel(const __grid_constant__ RotArgs a) {
+    constexpr int R = 32 / G, S = kStages<E, kBack>, H = static_cast<int>(sizeof(E)) / 2;  // H words per eight elements
+    extern __shared__ __align__(16) uint8_t raw[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = lane % G;
+    WarpRing<E, G, kBack>& ring = reinterpret_cast<WarpRing<E, G, kBack>*>(raw)[warp];
+    const bool in = 16 * t < a.dim;  // this lane holds elements
+    const int half = a.rotary / 2;
+    const bool turns = 8 * t < half;
+    const int c0 = kInter ? 16 * t : turns ? 8 * t : a.rotary + 16 * (t - half / 8);
+    const int c1 = kInter ? c0 + 8 : turns ? half + 8 * t : c0 + 8;
+    const float inv = 1.0f / static_cast<float>(a.dim);
+    const Rows& Q = a.r[blockIdx.x < static_cast<unsigned>(a.r[1].first) ? 0 : 1];
+    const int heads = Q.heads, split = Q.split, per = Q.per;
+    float wa[8], wb[8], dwa[8], dwb[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        wa[p] = wb[p] = 1.0f;
+        dwa[p] = dwb[p] = 0.0f;
+    }
+    if (Q.w && in) {
+        float v0[8], v1[8];
+        unpack8<E>(reinterpret_cast<const uint4*>(static_cast<const E*>(Q.w) + c0), 1, v0);
+        unpack8<E>(reinterpret_cast<const uint4*>(static_cast<const E*>(Q.w) + c1), 1, v1);
+        to_pairs<kInter>(v0, v1, wa, wb);
+    }
+    // item = token * split + share; a warp's items are `stride` apart
+    const int stride = Q.blocks * kWarps, first = static_cast<int>(blockIdx.x - Q.first) * kWarps + warp;
+    const int step_token = stride / split, step_share = stride - step_token * split;
+    const auto advance = [&](int& token, int& share) {
+        token += step_token;
+        share += step_share;
+        if (share >= split) {
+            share -= split;
+            ++token;
+        }
+    };
+    const int tokens = static_cast<int>(a.tokens);
+
+    // the loads' place: item, step of it, ring slots
+    int ld_token = first / split, ld_share = first - ld_token * split, ld_k = 0, ld_slot = 0, ld_tok = 0;
+    // a position is fetched one item ahead of the copy of its cos and sin
+    int64_t next = half > 0 && ld_token < tokens ? a.positions[ld_token] : 0;
+    const auto issue = [&] {
+        if (ld_token < tokens) {
+            const int64_t token = ld_token;
+            const int h = (ld_share + ld_k * split) * R + lane / G;
+            if (in && h < heads) {
+                uint4* d = &ring.x[ld_slot][0][lane];
+                if (!kBack || a.norm) {
+                    const E* p = static_cast<const E*>(Q.x) + token * Q.x_token + h * Q.x_head;
+                    copy8(d, p + c0);
+                    copy8(d + 32 * H, p + c1);
+                }
+                if constexpr (kBack) {
+                    const E* p = static_cast<const E*>(Q.dy) + token * Q.dy_token + h * Q.dy_head;
+                    copy8(d + 64 * H, p + c0);
+                    copy8(d + 96 * H, p + c1);
+                }
+            }
+            if (ld_k == 0 && half > 0) {
+                if (lane < G && turns) {
+                    const bool inside = next >= 0 && next < a.table_rows;
+                    const float* p = a.table + (inside ? next : 0) * a.rotary + 8 * t;
+                    copy16(&ring.cs[ld_tok][0][t], p);
+                    copy16(&ring.cs[ld_tok][1][t], p + 4);
+                    copy16(&ring.cs[ld_tok][2][t], p + half);
+                    copy16(&ring.cs[ld_tok][3][t], p + half + 4);
+                    if (lane == 0) ring.pos[ld_tok] = next;
+                }
+            }
+            if (++ld_k == per) {
+                ld_k = 0;
+                advance(ld_token, ld_share);
+                if (half > 0 && ld_token < tokens) next = a.positions[ld_token];
+                if (++ld_tok == S) ld_tok = 0;
+            }
+            if (++ld_slot == S) ld_slot = 0;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i + 1 < S; ++i) issue();
+
+    float cs[8], sn[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        cs[p] = 1.0f;
+        sn[p] = 0.0f;
+    }
+    int token = first / split, share = first - token * split;
+    int k = 0, slot = 0, tok = 0;
+    while (token < tokens) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncwarp();
+        if (k == 0 && turns) {
+            const int64_t pos = ring.pos[tok];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 c = ring.cs[tok][i][t], s = ring.cs[tok][2 + i][t];
+                cs[4 * i] = c.x, cs[4 * i + 1] = c.y, cs[4 * i + 2] = c.z, cs[4 * i + 3] = c.w;
+                sn[4 * i] = s.x, sn[4 * i + 1] = s.y, sn[4 * i + 2] = s.z, sn[4 * i + 3] = s.w;
+            }
+            if (pos < 0 || pos >= a.table_rows) {
+#pragma unroll
+                for (int p = 0; p < 8; ++p) cs[p] = sn[p] = __int_as_float(0x7fffffff);
+            }
+        }
+        issue();
+        const int h = (share + k * split) * R + lane / G;
+        const bool active = in && h < heads;
+        const uint4* d = &ring.x[slot][0][lane];
+        float v0[8], v1[8], p[8], q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v0[i] = v1[i] = 0.0f;
+        if (active && (!kBack || a.norm)) {
+            unpack8<E>(d, 32, v0);
+            unpack8<E>(d + 32 * H, 32, v1);
+        }
+        to_pairs<kInter>(v0, v1, p, q);
+        float r = 1.0f;
+        if (a.norm) {
+            float2 s2 = tc::both(0.0f);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                s2 = tc::fma2(pair(p, i), pair(p, i), s2);
+                s2 = tc::fma2(pair(q, i), pair(q, i), s2);
+            }
+            float s = s2.x + s2.y;
+#pragma unroll
+            for (int x = G / 2; x >= 1; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
+            r = rsqrtf(fmaf(s, inv, a.eps));
+        }
+        const float2 r2 = tc::both(r);
+        if constexpr (!kBack) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float2 m = pair(p, i), n = pair(q, i);
+                if (a.norm) {
+                    m = tc::mul2(m, tc::mul2(r2, pair(wa, i)));
+                    n = tc::mul2(n, tc::mul2(r2, pair(wb, i)));
+                }
+                set(p, i, tc::fma2(m, pair(cs, i), negated(tc::mul2(n, pair(sn, i)))));
+                set(q, i, tc::fma2(m, pair(sn, i), tc::mul2(n, pair(cs, i))));
+            }
+            from_pairs<kInter>(p, q, v0, v1);
+        } else {
+            float g[8], u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v0[i] = v1[i] = 0.0f;
+            if (active) {
+                unpack8<E>(d + 64 * H, 32, v0);
+                unpack8<E>(d + 96 * H, 32, v1);
+            }
+            to_pairs<kInter>(v0, v1, g, u);
+            float2 dot2 = tc::both(0.0f);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float2 m = tc::fma2(pair(g, i), pair(cs, i), tc::mul2(pair(u, i), pair(sn, i)));
+                float2 n = tc::fma2(pair(u, i), pair(cs, i), negated(tc::mul2(pair(g, i), pair(sn, i))));
+                if (a.norm) {
+                    const float2 x = tc::mul2(pair(p, i), r2), y = tc::mul2(pair(q, i), r2);
+                    set(p, i, x);
+                    set(q, i, y);
+                    if (active) {
+                        set(dwa, i, tc::fma2(m, x, pair(dwa, i)));
+                        set(dwb, i, tc::fma2(n, y, pair(dwb, i)));
+                    }
+                    m = tc::mul2(m, pair(wa, i));
+                    n = tc::mul2(n, pair(wb, i));
+                    dot2 = tc::fma2(m, x, tc::fma2(n, y, dot2));
+                }
+                set(g, i, m);
+                set(u, i, n);
+            }
+            if (a.norm) {
+                float dot = dot2.x + dot2.y;
+#pragma unroll
+                for (int x = G / 2; x >= 1; x >>= 1) dot += __shfl_xor_sync(kFull, dot, x);
+                const float2 off = tc::both(-dot * inv);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    set(g, i, tc::mul2(r2, tc::fma2(pair(p, i), off, pair(g, i))));
+                    set(u, i, tc::mul2(r2, tc::fma2(pair(q, i), off, pair(u, i))));
+                }
+            }
+            from_pairs<kInter>(g, u, v0, v1);
+        }
+        if (active) {
+            E* out = static_cast<E*>(Q.out) + (static_cast<int64_t>(token) * heads + h) * a.dim;
+            store8(out + c0, v0);
+            store8(out + c1, v1);
+        }
+        if (++k == per) {
+            k = 0;
+            advance(token, share);
+            if (++tok == S) tok = 0;
+        }
+        if (++slot == S) slot = 0;
+    }
+    if constexpr (kBack) {
+        if (!a.partial) return;
+        // the warp's row groups, then the block's warps
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        float(*sums)[16 * G] = reinterpret_cast<float(*)[16 * G]>(raw);
+#pragma unroll
+        for (int s = G; s < 32; s <<= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dwa[i] += __shfl_xor_sync(kFull, dwa[i], s);
+                dwb[i] += __shfl_xor_sync(kFull, dwb[i], s);
+            }
+        if (in && lane < G) {
+            float v0[8], v1[8];
+            from_pairs<kInter>(dwa, dwb, v0, v1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sums[warp][c0 + i] = v0[i];
+                sums[warp][c1 + i] = v1[i];
+            }
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.dim; e += 32 * kWarps) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sum += sums[w][e];
+            a.partial[static_cast<int64_t>(blockIdx.x) * a.dim + e] = sum;
+        }
+    }
+}
+
+// Whether the vector kernels can take the call.
+bool vectors(const RotArgs& a, int es, bool back) {
+    const int64_t n = 16 / es;
+    bool ok = a.dim % 16 == 0 && a.rotary % 16 == 0;
+    for (const Rows& r : a.r) {
+        if (!back || a.norm)
+            ok = ok && reinterpret_cast<uintptr_t>(r.x) % 16 == 0 && r.x_token % n == 0 && r.x_head % n == 0;
+        if (back) ok = ok && reinterpret_cast<uintptr_t>(r.dy) % 16 == 0 && r.dy_token % n == 0 && r.dy_head % n == 0;
+    }
+    return ok;
+}
+
+// The blocks of the queries and, behind them, of the keys: in proportion to their
+// rows, no more than they can use, at least one each.
+int set_blocks(Rows (&r)[2], int64_t tokens) {
+    const int64_t all = r[0].heads + r[1].heads;
+    for (int i = 0; i < 2; ++i)
+        r[i].blocks = static_cast<int32_t>(std::max<int64_t>(
+            1, std::min<int64_t>(ceil_div(tokens * r[i].heads, kWarps), (kMaxBlocks - 1) * r[i].heads / all)));
+    r[0].first = 0;
+    r[1].first = r[0].blocks;
+    return r[0].blocks + r[1].blocks;
+}
+
+template <typename E, int G, bool kBack>
+cudaError_t run_vector(RotArgs a, int blocks, cudaStream_t s) {
+    constexpr int R = 32 / G;
+    // a token's heads are shared among warps until each has 16 items or more, so that
+    // their unequal counts cost a few percent at most
+    for (Rows& r : a.r) {
+        const int64_t chunks = ceil_div(r.heads, R);
+        r.split = static_cast<int32_t>(std::min<int64_t>(chunks, ceil_div(16 * r.blocks * kWarps, a.tokens)));
+        r.per = static_cast<int32_t>(ceil_div(chunks, r.split));
+    }
+    const auto kernel = a.interleaved ? vector_kernel<E, G, kBack, true> : vector_kernel<E, G, kBack, false>;
+    constexpr int bytes = kWarps * static_cast<int>(sizeof(WarpRing<E, G, kBack>));
+    static PerDevice cache[2];  // the shared-memory attribute, once per device
+    int dev = 0, ok = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cache[a.interleaved].get(dev, &ok, [&](int* out) {
+            *out = 1;
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename E, bool kBack>
+cudaError_t run_rows(const RotArgs& a, int blocks, cudaStream_t s) {
+    if (vectors(a, sizeof(E), kBack)) {
+        if (a.dim <= 16) return run_vector<E, 1, kBack>(a, blocks, s);
+        if (a.dim <= 32) return run_vector<E, 2, kBack>(a, blocks, s);
+        if (a.dim <= 64) return run_vector<E, 4, kBack>(a, blocks, s);
+        if (a.dim <= 128) return run_vector<E, 8, kBack>(a, blocks, s);
+        return run_vector<E, 16, kBack>(a, blocks, s);
+    }
+    return launch_dependent(rows_kernel<E, kBack>, dim3(static_cast<unsigned>(blocks)), 32 * kWarps, s, a);
+}
+
+// Weight gradients from the partial sums [blocks][dim], always in the same order: 32
+// columns per block, 32 threads each; blockIdx.y: queries, keys.
+template <typename E>
+__global__ void __launch_bounds__(1024) reduce_kernel(const float* partial, int nq, int nk, int dim, void* dq,
+                                                      void* dk) {
     __shared__ float sums[32][33];
-    const int col = blockIdx.x * 32 + threadIdx.x % 32, group = threadIdx.x / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool keys = blockIdx.y != 0;
+    const int col = blockIdx.x * 32 + threadIdx.x % 32, group = threadIdx.x / 32, n = keys ? nk : nq;
+    if (keys) partial += static_cast<int64_t>(nq) * dim;
     float sum = 0.0f;
-    if (col < 2 * dim)
-        for (int i = group; i < n; i += 32) sum += partial[static_cast<int64_t>(i) * 2 * dim + col];
+    if (col < dim)
+        for (int i = group; i < n; i += 32) sum += partial[static_cast<int64_t>(i) * dim + col];
     sums[group][threadIdx.x % 32] = sum;
     __syncthreads();
-    if (group != 0 || col >= 2 * dim) return;
+    void* out = keys ? dk : dq;
+    if (group != 0 || col >= dim || !out) return;
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) sum += sums[i][threadIdx.x];
-    void* out = col < dim ? dq : dk;
-    if (out) static_cast<E*>(out)[col < dim ? col : col - dim] = from_f<E>(sum);
+    static_cast<E*>(out)[col] = from_f<E>(sum);
 }
 
 // cos and sin of position * base^(-2 i / rotary), in 64 bits until they are rounded:
@@ -214,11 +623,6 @@ int check_heads(const dmuon_heads_t* t, int64_t tokens, int64_t heads, int64_t d
 bool sizes_ok(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim) {
     return in_range(tokens, 0, kMaxTokens) && in_range(heads, 1, kMaxHeads) && in_range(kv_heads, 1, kMaxHeads) &&
            in_range(dim, 1, kMaxDim);
-}
-
-int blocks_of(int64_t tokens, int heads, int kv_heads) {
-    return static_cast<int>(
-        std::min<int64_t>(std::max<int64_t>(1, ceil_div(tokens * std::max(heads, kv_heads), kWarps)), kMaxPartials));
 }
 
 // What both directions check, and the arguments they share.
@@ -286,7 +690,7 @@ extern "C" size_t dmuon_qk_norm_rotary_workspace_bytes(int64_t tokens, int32_t h
     if (!sizes_ok(tokens, heads, kv_heads, dim) ||
         check_dtype(dtype, "dmuon_qk_norm_rotary_workspace_bytes") != DMUON_OK)
         return 0;
-    return static_cast<size_t>(blocks_of(tokens, heads, kv_heads)) * 2 * dim * sizeof(float);
+    return static_cast<size_t>(kMaxBlocks) * dim * sizeof(float);
 }
 
 extern "C" int dmuon_qk_norm_rotary_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, const int64_t* positions,
@@ -314,11 +718,9 @@ extern "C" int dmuon_qk_norm_rotary_forward(const dmuon_heads_t* q, const dmuon_
     a.r[0].out = q_out;
     a.r[1].out = k_out;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid =
-        static_cast<unsigned>(std::min<int64_t>(ceil_div(tokens * std::max(heads, kv_heads), kWarps), 152 * 8 * 4));
-    if (dtype == DMUON_FP32) rows_kernel<float, false><<<grid, 32 * kWarps, 0, s>>>(a);
-    else rows_kernel<__nv_bfloat16, false><<<grid, 32 * kWarps, 0, s>>>(a);
-    OPS_CUDA(cudaGetLastError());
+    const int blocks = set_blocks(a.r, tokens);
+    const bool f32 = dtype == DMUON_FP32;
+    OPS_CUDA((f32 ? run_rows<float, false>(a, blocks, s) : run_rows<__nv_bfloat16, false>(a, blocks, s)));
     return DMUON_OK;
 }
 
@@ -367,18 +769,13 @@ extern "C" int dmuon_qk_norm_rotary_backward(const dmuon_heads_t* dq_out, const 
     OPS_TRY(check_device(where));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f32 = dtype == DMUON_FP32;
-    const int blocks = tokens > 0 ? blocks_of(tokens, heads, kv_heads) : 0;
+    const int blocks = tokens > 0 ? set_blocks(a.r, tokens) : 0;
     a.partial = sums ? static_cast<float*>(workspace) : nullptr;
-    if (blocks > 0) {
-        if (f32) rows_kernel<float, true><<<blocks, 32 * kWarps, 0, s>>>(a);
-        else rows_kernel<__nv_bfloat16, true><<<blocks, 32 * kWarps, 0, s>>>(a);
-        OPS_CUDA(cudaGetLastError());
-    }
+    if (blocks > 0) OPS_CUDA((f32 ? run_rows<float, true>(a, blocks, s) : run_rows<__nv_bfloat16, true>(a, blocks, s)));
     if (sums) {
-        const unsigned grid = static_cast<unsigned>(ceil_div(2 * dim, 32));
-        if (f32) reduce_kernel<float><<<grid, 1024, 0, s>>>(a.partial, blocks, dim, dq_weight, dk_weight);
-        else reduce_kernel<__nv_bfloat16><<<grid, 1024, 0, s>>>(a.partial, blocks, dim, dq_weight, dk_weight);
-        OPS_CUDA(cudaGetLastError());
+        const dim3 grid(static_cast<unsigned>(ceil_div(dim, 32)), 2);
+        OPS_CUDA(launch_dependent(f32 ? reduce_kernel<float> : reduce_kernel<__nv_bfloat16>, grid, 1024, s, a.partial,
+                                  a.r[0].blocks, a.r[1].blocks, dim, dq_weight, dk_weight));
     }
     return DMUON_OK;
 }
