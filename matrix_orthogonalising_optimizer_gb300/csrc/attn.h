@@ -70,10 +70,12 @@ __device__ __forceinline__ bool attn_find(const AttnArgs& a, int64_t slot, int T
     }
     const int64_t b = attn_offset(a, lo), e = attn_offset(a, lo + 1);
     const int64_t k = slot - (b / T + lo);
-    t.begin = b;
-    t.len = static_cast<int32_t>(e - b);
-    t.tile = static_cast<int32_t>(k);
-    return k >= 0 && b + k * T < e;
+    // from one lane: the compiler then knows them to be the same in all, and keeps what
+    // follows from them in uniform registers, where MMAs and copies take their operands
+    t.begin = __shfl_sync(0xffffffffu, static_cast<int32_t>(b), 0);  // tokens < 2^31
+    t.len = __shfl_sync(0xffffffffu, static_cast<int32_t>(e - b), 0);
+    t.tile = __shfl_sync(0xffffffffu, static_cast<int32_t>(k), 0);
+    return __shfl_sync(0xffffffffu, k >= 0 && b + k * T < e ? 1 : 0, 0) != 0;
 }
 
 // Clears the rows of no sequence -- before the first and behind the last -- of one

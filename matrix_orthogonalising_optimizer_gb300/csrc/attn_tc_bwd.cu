@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap mo) {
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem<DP>& S = *reinterpret_cast<Smem<DP>*>(raw);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // blocks of the keys, then blocks of the queries
     const int64_t per_slot = a.kv_heads, rows = static_cast<int64_t>(a.slots) + a.fill;
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = S.tmem;
+    const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);  // uniform, as attn_find's results
     if (warp < kEltWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (keys) keys_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);

@@ -17,6 +17,7 @@
 //
 // Bound: the tensor cores, 4 * 128 * 128 * dim operations per pair of tiles -- at dim =
 // 128 1024 cycles, against 512 of exponentials and about 400 of instruction issue.
+#include <cstdlib>
 #include "attn_tc.cuh"
 #include "internal.h"
 #include "ops.h"
@@ -32,38 +33,65 @@ constexpr int kSoftWarp0 = 4;
 template <int DP, int NT>
 struct Cfg {
     static constexpr int kThreads = 128 + 128 * NT;
-    static constexpr int kStages = DP == 128 ? 5 : NT == 2 ? 8 : 4;
+    static constexpr int kBuffers = NT == 1 ? 1 : DP == 64 ? 3 : 2;  // of s, in TMEM
+    static constexpr bool kHalves = kBuffers == 2;                   // p is handed over in two halves
+    static constexpr int kStages = NT == 2 ? (DP == 128 ? 5 : 8) : (DP == 128 ? 2 : 4);
     static constexpr uint32_t kCols = NT == 2 ? 512 : 256;
     static constexpr int kRegsLow = 56, kRegsSoft = NT == 2 ? 224 : 200;  // shares of 168 x 3 or 128 x 2
-    static constexpr int kMinBlocks = DP == 64 && NT == 1 ? 2 : 1;
 };
 
 template <int DP, int NT>
 struct __align__(1024) Smem {
+    using C = Cfg<DP, NT>;
     uint8_t q[NT][kTile<DP>];
-    uint8_t kv[Cfg<DP, NT>::kStages][kTile<DP>];
+    uint8_t kv[C::kStages][kTile<DP>];
     uint64_t q_full;
-    uint64_t full[Cfg<DP, NT>::kStages];
-    uint64_t empty[Cfg<DP, NT>::kStages];
-    uint64_t s_full[NT];
-    uint64_t p_ready[NT];
+    uint64_t full[C::kStages];
+    uint64_t empty[C::kStages];
+    uint64_t s_full[C::kBuffers];
+    uint64_t p_half[C::kBuffers];
+    uint64_t p_ready[C::kBuffers];
+    uint64_t pv_done[NT][2];  // products of the even and the odd key tiles
     uint64_t o_full[NT];
     uint64_t drained;
     uint32_t tmem;
 };
 
+// The products of a CTA, in the order in which the tensor cores run them: unit u is key
+// tile j of query tile i, alternating between the query tiles while both have keys
+// left.  Its s lies in buffer u % kBuffers.
+struct Units {
+    int n[2], lo, more;  // key tiles of each query tile, the fewer, the query tile with more
+    __device__ __forceinline__ int count() const { return n[0] + n[1]; }
+    __device__ __forceinline__ int of(int i, int j) const { return j < lo ? 2 * j + i : lo + j; }
+    __device__ __forceinline__ void at(int u, int& i, int& j) const {
+        const bool both = u < 2 * lo;
+        i = both ? u & 1 : more;
+        j = both ? u >> 1 : u - lo;
+    }
+};
+
+// Place of K_j and V_j in the ring's order, `steps` tiles each: as the tensor cores
+// first need them (with three buffers s runs a tile further ahead).
+template <int kBuffers>
+__device__ __forceinline__ int place(bool v, int j, int steps) {
+    if (kBuffers < 3) return 2 * j + (v ? 1 : 0);
+    if (!v) return j == 0 ? 0 : 2 * j - 1;
+    return j + 1 < steps ? 2 * j + 2 : 2 * j + 1;
+}
+
 // Growth of a row's maximum, in powers of two, that is left in p.
 constexpr float kLazy = 8.0f;
 
 template <int DP, int NT>
-__global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks)
+__global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
     forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     using C = Cfg<DP, NT>;
-    constexpr int NS = C::kStages;
+    constexpr int NS = C::kStages, NB = C::kBuffers;
     extern __shared__ uint8_t raw[];
     Smem<DP, NT>& S = *reinterpret_cast<Smem<DP, NT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t slot = blockIdx.x / a.heads;
@@ -77,15 +105,17 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
     // the tiles with most keys first
     const int row0 = (a.causal ? (t.len - 1) / (NT * kRows) - t.tile : t.tile) * NT * kRows;
     const int token0 = static_cast<int>(t.begin);
-    // key tiles of each query tile, 0 where it has no rows
-    int n[NT];
+    Units units;
+    units.n[1] = 0;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int first = row0 + i * kRows;
         const int keys = a.causal ? min(t.len, first + kRows) : t.len;
-        n[i] = first < t.len ? (keys + kRows - 1) / kRows : 0;
+        units.n[i] = first < t.len ? (keys + kRows - 1) / kRows : 0;  // 0: no rows
     }
-    const int steps = n[NT - 1] > n[0] ? n[NT - 1] : n[0];
+    units.lo = min(units.n[0], units.n[1]);
+    units.more = units.n[1] > units.n[0] ? 1 : 0;
+    const int steps = max(units.n[0], units.n[1]);
 
     if (warp == 1) {
         tmem_alloc<C::kCols>(&S.tmem);
@@ -95,9 +125,14 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
             mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], 1);
         }
-        for (int i = 0; i < NT; ++i) {
+        for (int i = 0; i < NB; ++i) {
             mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_half[i], 4);
             mbar_init(&S.p_ready[i], 4);
+        }
+        for (int i = 0; i < NT; ++i) {
+            mbar_init(&S.pv_done[i][0], 1);
+            mbar_init(&S.pv_done[i][1], 1);
             mbar_init(&S.o_full[i], 1);
         }
         mbar_init(&S.drained, 1);
@@ -106,17 +141,18 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = S.tmem;
-    const uint32_t t_s = tmem, t_o = tmem + NT * kRows;
+    const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);  // uniform, as attn_find's results
+    const uint32_t t_s = tmem, t_o = tmem + NB * kRows;
 
     if (warp < kSoftWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLow));
         if (warp == 0) {
             // ------------------------------------------------ loads
             const uint32_t e = elect_one();
-            mbar_expect_tx_if(e, &S.q_full, (n[NT - 1] > 0 ? NT : 1) * kTile<DP>);
+            mbar_expect_tx_if(e, &S.q_full, (units.n[1] > 0 ? 2 : 1) * kTile<DP>);
             for (int i = 0; i < NT; ++i)
-                if (n[i] > 0) load_tile<DP>(e, saddr(S.q[i]), &mq, saddr(&S.q_full), head, token0 + row0 + i * kRows);
+                if (units.n[i] > 0)
+                    load_tile<DP>(e, saddr(S.q[i]), &mq, saddr(&S.q_full), head, token0 + row0 + i * kRows);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -125,9 +161,15 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
                     ok = false;
                     break;
                 }
+                bool v = (i & 1) != 0;
+                int tile = i / 2;
+                if (NB == 3 && i > 0) {  // K0 K1 V0 K2 V1 .. V_last
+                    v = i % 2 == 0 || i + 1 == 2 * steps;
+                    tile = i + 1 == 2 * steps ? steps - 1 : v ? i / 2 - 1 : (i + 1) / 2;
+                }
                 mbar_expect_tx_if(e, &S.full[stage], kTile<DP>);
-                load_tile<DP>(e, saddr(S.kv[stage]), i & 1 ? &mv : &mk, saddr(&S.full[stage]), head / a.group,
-                              token0 + i / 2 * kRows);
+                load_tile<DP>(e, saddr(S.kv[stage]), v ? &mv : &mk, saddr(&S.full[stage]), head / a.group,
+                              token0 + tile * kRows);
                 if (++stage == NS) {
                     stage = 0;
                     phase ^= 1;
@@ -137,55 +179,42 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
             // ------------------------------------------------ MMAs
             const uint32_t e = elect_one();
             const uint32_t q0 = saddr(S.q[0]), kv0 = saddr(S.kv[0]);
-            int stage = 0;
-            uint32_t phase = 0;
+            const int total = units.count();
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
                 const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &g_status));
                 fence_after();
                 return r;
             };
-            const auto next = [&] {
-                if (++stage == NS) {
-                    stage = 0;
-                    phase ^= 1;
-                }
+            // s of unit u into its buffer, which the product NB units before has left
+            const auto form_s = [&](int u) {
+                int i, j;
+                units.at(u, i, j);
+                const int at = place<NB>(false, j, steps), slot = at % NS;
+                if (!wait(&S.full[slot], (at / NS) & 1)) return false;
+                product_cols<DP>(e, t_s + u % NB * kRows, desc_k(q0 + i * kTile<DP>), desc_k(kv0 + slot * kTile<DP>));
+                umma_commit(e, saddr(&S.s_full[u % NB]));
+                if (i == 1 || j >= units.lo) umma_commit(e, saddr(&S.empty[slot]));  // K_j's last use
+                return true;
             };
-            bool ok = wait(&S.q_full, 0) && wait(&S.full[0], 0);
-            if (ok) {
-                for (int i = 0; i < NT; ++i) {
-                    if (n[i] == 0) continue;
-                    product_cols<DP>(e, t_s + i * kRows, desc_k(q0 + i * kTile<DP>), desc_k(kv0));
-                    umma_commit(e, saddr(&S.s_full[i]));
-                }
-                umma_commit(e, saddr(&S.empty[0]));
-                next();
-            }
-            for (int j = 0; j < steps && ok; ++j) {
-                const int sv = stage;
-                ok = wait(&S.full[stage], phase);
-                next();
-                const int sk = stage;
-                const bool more = j + 1 < steps;
-                if (ok && more) {
-                    // not before the products that it waits behind: the load is far ahead
-                    ok = wait(&S.full[stage], phase);
-                    next();
-                }
-                for (int i = 0; i < NT && ok; ++i) {
-                    if (j >= n[i]) continue;
-                    ok = wait(&S.p_ready[i], j & 1);
+            bool ok = wait(&S.q_full, 0);
+            for (int u = 0; u < NB && u < total && ok; ++u) ok = form_s(u);
+            for (int u = 0; u < total && ok; ++u) {
+                int i, j;
+                units.at(u, i, j);
+                const int at = place<NB>(true, j, steps), slot = at % NS, b = u % NB;
+                const uint32_t parity = (u / NB) & 1;
+                const uint64_t v = desc_mn(kv0 + slot * kTile<DP>);
+                ok = wait(&S.full[slot], (at / NS) & 1) && wait(C::kHalves ? &S.p_half[b] : &S.p_ready[b], parity);
+                if (!ok) break;
+                product_rows<DP>(e, t_o + i * DP, t_s + b * kRows, v, 0, C::kHalves ? 4 : 8, j > 0);
+                if (C::kHalves) {
+                    ok = wait(&S.p_ready[b], parity);
                     if (!ok) break;
-                    product_rows<DP>(e, t_o + i * DP, t_s + i * kRows, desc_mn(kv0 + sv * kTile<DP>), 0, 8, j > 0);
-                    if (j + 1 < n[i]) {
-                        product_cols<DP>(e, t_s + i * kRows, desc_k(q0 + i * kTile<DP>),
-                                         desc_k(kv0 + sk * kTile<DP>));
-                        umma_commit(e, saddr(&S.s_full[i]));
-                    } else {
-                        umma_commit(e, saddr(&S.o_full[i]));
-                    }
+                    product_rows<DP>(e, t_o + i * DP, t_s + b * kRows + 32, v, 4, 4, true);
                 }
-                umma_commit(e, saddr(&S.empty[sv]));
-                if (more) umma_commit(e, saddr(&S.empty[sk]));
+                umma_commit(e, saddr(j + 1 == (i ? units.n[1] : units.n[0]) ? &S.o_full[i] : &S.pv_done[i][j & 1]));
+                if (i == 1 || j >= units.lo) umma_commit(e, saddr(&S.empty[slot]));
+                if (u + NB < total) ok = form_s(u + NB);
             }
             // also after a wait that gave up: no MMA or commit is under way when the CTA leaves
             umma_commit(e, saddr(&S.drained));
@@ -196,16 +225,22 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
         // ------------------------------------------------ softmax
         const int tile = (warp - kSoftWarp0) / 4, quarter = warp % 4, thread = threadIdx.x % 128;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t ts = t_s + tile * kRows + lanes, to = t_o + tile * DP + lanes;
+        const uint32_t to = t_o + tile * DP + lanes;
         const int row = row0 + tile * kRows + thread;
-        const int count = NT == 2 && tile == 1 ? n[NT - 1] : n[0];
+        const int count = tile ? units.n[1] : units.n[0];
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &g_status));
+            fence_after();
+            return r;
+        };
         const float c = a.scale_log2;
         float top = __int_as_float(0xff800000), base = 0.0f, sum = 0.0f;
         bool ok = true;
         for (int j = 0; j < count; ++j) {
-            ok = __all_sync(kFullMask, mbar_wait<false>(&S.s_full[tile], j & 1, &g_status));
+            const int u = units.of(tile, j), b = u % NB;
+            const uint32_t ts = t_s + b * kRows + lanes;
+            ok = wait(&S.s_full[b], (u / NB) & 1);
             if (!ok) break;
-            fence_after();
             float s[kRows];
             tmem_ld128(ts, s);
             const int keys = min(kRows, t.len - j * kRows);
@@ -231,6 +266,10 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
                 top = grown;
                 base = fresh;
                 sum *= f;
+                // s of this unit was formed after the product of tile j - 3 at the earliest, so
+                // the parity means no other phase
+                ok = wait(&S.pv_done[tile][(j - 1) & 1], ((j - 1) >> 1) & 1);
+                if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < DP; k += 32) {
                     float o[32];
@@ -240,6 +279,13 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
                     for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(o[x] * f);
                     tmem_st32(to + k, w);
                 }
+            }
+            if (keys < kRows) {
+                // the values of keys behind the sequence
+                const int at = place<NB>(true, j, steps);
+                ok = wait(&S.full[at % NS], (at / NS) & 1);
+                if (!ok) break;
+                clear_rows<DP>(S.kv[at % NS], keys, thread, 128);
             }
             const float2 c2 = both(c), b2 = both(-base);
             float2 part[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
@@ -254,24 +300,17 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, Cfg<DP, NT>::kMinBlocks
                     w[k] = pack_bf16x2(p.x, p.y);
                 }
                 tmem_st32(ts + 32 * h, w);
+                if (h == 1 || C::kHalves) {
+                    tmem_st_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(h == 0 ? &S.p_half[b] : &S.p_ready[b]);
+                }
             }
             const float2 all = add2(add2(part[0], part[1]), add2(part[2], part[3]));
             sum += all.x + all.y;
-            tmem_st_wait();
-            if (keys < kRows) {
-                // the values of keys behind the sequence
-                const int v = 2 * j + 1;
-                ok = __all_sync(kFullMask, mbar_wait<false>(&S.full[v % NS], (v / NS) & 1, &g_status));
-                if (!ok) break;
-                clear_rows<DP>(S.kv[v % NS], keys, thread, 128);
-            }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.p_ready[tile]);
         }
-        if (ok && count > 0) ok = __all_sync(kFullMask, mbar_wait<false>(&S.o_full[tile], 0, &g_status));
-        if (ok && count > 0) {
-            fence_after();
+        if (ok && count > 0 && wait(&S.o_full[tile], 0)) {
             const int64_t token = t.begin + row;
             const float f = 1.0f / sum;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (token * a.heads + head) * a.dim;
@@ -345,6 +384,7 @@ cudaError_t attn_fwd_status_word(void** p) { return cudaGetSymbolAddress(p, attn
 cudaError_t attn_tc_forward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s) {
     const cudaError_t e = attn::prepare();
     if (e != cudaSuccess) return e;
+    if (getenv("NT1")) return a.dim <= 64 ? attn::launch<64, 1>(a, m, s) : attn::launch<128, 1>(a, m, s);
     return a.dim <= 64 ? attn::launch<64, 2>(a, m, s) : attn::launch<128, 2>(a, m, s);
 }
 
