@@ -55,27 +55,31 @@ __device__ __forceinline__ int64_t attn_offset(const AttnArgs& a, int64_t s) {
 }
 
 // The tile at a slot, by all 32 lanes of a warp (each round splits the sequences
-// left into 32).  False: the slot holds none.
-__device__ __forceinline__ bool attn_find(const AttnArgs& a, int64_t slot, int T, AttnTile& t) {
+// left into 32; up to 31 sequences take one round of loads).  False: the slot holds none.
+__device__ __forceinline__ bool attn_find(const AttnArgs& a, int32_t slot, int T, AttnTile& t) {
     const int lane = threadIdx.x & 31;
-    int64_t lo = 0, count = a.sequences;
-    while (count > 1) {
-        const int64_t step = (count + 31) / 32, i = lo + lane * step;
-        const bool before = i < lo + count && attn_offset(a, i) / T + i <= slot;
-        const unsigned m = __ballot_sync(0xffffffffu, before);
+    int32_t lo = 0, count = a.sequences, b = 0, e = 0;  // tokens < 2^31
+    do {
+        const int32_t step = (count + 31) / 32, i = lo + lane * step;
+        const bool there = lane * step <= count;  // also the end of the last one
+        const int32_t o = there ? static_cast<int32_t>(attn_offset(a, i < a.sequences ? i : a.sequences)) : 0;
+        const unsigned m = __ballot_sync(0xffffffffu, lane * step < count && o / T + i <= slot);
         const int c = m == 0 ? 0 : 31 - __clz(m);
-        const int64_t end = lo + count;
+        b = __shfl_sync(0xffffffffu, o, c);
+        e = __shfl_sync(0xffffffffu, o, c + 1 < 32 ? c + 1 : c);
+        const int32_t end = lo + count;
         lo += c * step;
+        if (step == 1 && c == 31) e = static_cast<int32_t>(attn_offset(a, lo + 1));
         count = step < end - lo ? step : end - lo;
-    }
-    const int64_t b = attn_offset(a, lo), e = attn_offset(a, lo + 1);
-    const int64_t k = slot - (b / T + lo);
+        if (step == 1) count = 0;
+    } while (count > 0);
+    const int32_t k = slot - (b / T + lo);
     // from one lane: the compiler then knows them to be the same in all, and keeps what
     // follows from them in uniform registers, where MMAs and copies take their operands
-    t.begin = __shfl_sync(0xffffffffu, static_cast<int32_t>(b), 0);  // tokens < 2^31
-    t.len = __shfl_sync(0xffffffffu, static_cast<int32_t>(e - b), 0);
-    t.tile = __shfl_sync(0xffffffffu, static_cast<int32_t>(k), 0);
-    return __shfl_sync(0xffffffffu, k >= 0 && b + k * T < e ? 1 : 0, 0) != 0;
+    t.begin = __shfl_sync(0xffffffffu, b, 0);
+    t.len = __shfl_sync(0xffffffffu, e - b, 0);
+    t.tile = __shfl_sync(0xffffffffu, k, 0);
+    return __shfl_sync(0xffffffffu, k >= 0 && b + static_cast<int64_t>(k) * T < e ? 1 : 0, 0) != 0;
 }
 
 // Clears the rows of no sequence -- before the first and behind the last -- of one

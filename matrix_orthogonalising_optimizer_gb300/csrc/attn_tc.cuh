@@ -82,15 +82,39 @@ __device__ __forceinline__ void tmem_free(uint32_t base) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(kCols) : "memory");
 }
 
-// 32 values of a row times f, as bf16, to columns c0 .. of a row of `dim` (a multiple of 8).
-__device__ __forceinline__ void store_row32(__nv_bfloat16* row, const float (&v)[32], float f, int c0, int dim) {
+// A warp's 32 rows of an accumulator (64 kBoxes columns at TMEM address t, this lane's
+// row) times f, as bf16, to `rows` rows of `dim` elements (a multiple of 8), `ld` apart.
+// They pass through the warp's 4 KB slices of a finished tile's boxes in shared memory,
+// so that an instruction stores whole 128-byte pieces: row by row from the lanes it
+// touches 32 lines, and a tile took 1 us.
+template <int kBoxes>
+__device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t t, float f, __nv_bfloat16* out, int64_t ld,
+                                           int rows, int dim, int lane) {
+    const int chunk = lane % 8;
+#pragma unroll 1
+    for (int b = 0; b < kBoxes; ++b, stage += kBox) {
+        uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (c0 + 8 * k < dim)
-            *reinterpret_cast<uint4*>(row + c0 + 8 * k) =
-                make_uint4(pack_bf16x2(v[8 * k] * f, v[8 * k + 1] * f), pack_bf16x2(v[8 * k + 2] * f, v[8 * k + 3] * f),
-                           pack_bf16x2(v[8 * k + 4] * f, v[8 * k + 5] * f),
-                           pack_bf16x2(v[8 * k + 6] * f, v[8 * k + 7] * f));
+        for (int h = 0; h < 2; ++h) {
+            float v[32];
+            tmem_ld32(t + 64 * b + 32 * h, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mine[(4 * h + k) ^ chunk] =
+                    make_uint4(pack_bf16x2(v[8 * k] * f, v[8 * k + 1] * f), pack_bf16x2(v[8 * k + 2] * f, v[8 * k + 3] * f),
+                               pack_bf16x2(v[8 * k + 4] * f, v[8 * k + 5] * f),
+                               pack_bf16x2(v[8 * k + 6] * f, v[8 * k + 7] * f));
+        }
+        __syncwarp();
+        const int c = 64 * b + 8 * chunk;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + lane / 8;
+            const uint4 w = reinterpret_cast<const uint4*>(stage + r * 128)[chunk ^ (r % 8)];
+            if (r < rows && c < dim) *reinterpret_cast<uint4*>(out + r * ld + c) = w;
+        }
+        __syncwarp();
+    }
 }
 
 }  // namespace attn

@@ -54,7 +54,9 @@ struct __align__(1024) Smem {
     uint64_t stat_full[2];
     uint64_t stat_empty[2];
     uint64_t done;
+    AttnTile tile;
     uint32_t tmem;
+    int32_t any;
 };
 
 template <int DP>
@@ -109,17 +111,6 @@ __device__ __forceinline__ void store_cols64(uint32_t t, const float (&v)[64]) {
 #pragma unroll
     for (int k = 0; k < 32; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
     tmem_st32(t, w);
-}
-
-template <int DP>
-__device__ __forceinline__ void store_cols(__nv_bfloat16* row, uint32_t t, int c0, int c1, float f, int dim, bool in) {
-#pragma unroll 1
-    for (int k = c0; k < c1; k += 32) {
-        float v[32];
-        __syncwarp();
-        tmem_ld32(t + k, v);
-        if (in) store_row32(row, v, f, k, dim);
-    }
 }
 
 // ---------------------------------------------------------------- side of the keys
@@ -286,10 +277,11 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
         }
         if (ok && wait_warp(&S.done, 0)) {
             // one warpgroup stores dv, the other dk
-            const int64_t token = t.begin + row0 + r;
-            void* out = half ? a.dk : a.dv;
-            store_cols<DP>(static_cast<__nv_bfloat16*>(out) + (token * a.kv_heads + kv) * a.dim,
-                           (half ? t_dk : t_dv) + lanes, 0, DP, half ? a.scale : 1.0f, a.dim, row0 + r < t.len);
+            const int quarter = warp % 4;
+            const int64_t first = t.begin + row0 + 32 * quarter;
+            store_rows<DP / 64>(S.own[half] + quarter * 4096, (half ? t_dk : t_dv) + lanes, half ? a.scale : 1.0f,
+                                static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (first * a.kv_heads + kv) * a.dim,
+                                static_cast<int64_t>(a.kv_heads) * a.dim, t.len - row0 - 32 * quarter, a.dim, lane);
         }
     }
 }
@@ -405,9 +397,14 @@ __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, con
             if (keys < kRows) clear_rows<DP>(S.ring[2 * i % kStages<DP>], keys, thread, 256);  // keys behind the sequence
             arrive_warp(&S.ds_ready, lane);
         }
-        if (ok && wait_warp(&S.done, 0))
-            store_cols<DP>(static_cast<__nv_bfloat16*>(a.out) + (token * a.heads + head) * a.dim, t_dq + lanes,
-                           half * (DP / 2), (half + 1) * (DP / 2), a.scale, a.dim, in);
+        // a box of 64 columns each warpgroup
+        if (64 * half < DP && ok && wait_warp(&S.done, 0)) {
+            const int quarter = warp % 4;
+            const int64_t first = t.begin + row0 + 32 * quarter;
+            store_rows<1>(S.own[0] + half * kBox + quarter * 4096, t_dq + 64 * half + lanes, a.scale,
+                          static_cast<__nv_bfloat16*>(a.out) + (first * a.heads + head) * a.dim + 64 * half,
+                          static_cast<int64_t>(a.heads) * a.dim, t.len - row0 - 32 * quarter, a.dim - 64 * half, lane);
+        }
     }
 }
 
@@ -419,30 +416,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem<DP>& S = *reinterpret_cast<Smem<DP>*>(raw);
     const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     // blocks of the keys, then blocks of the queries
-    const int64_t per_slot = a.kv_heads, rows = static_cast<int64_t>(a.slots) + a.fill;
-    int64_t block = blockIdx.x;
-    const bool keys = block < rows * per_slot;
-    if (!keys) block -= rows * per_slot;
-    const int heads = keys ? a.kv_heads : a.heads;
-    const int64_t slot = block / heads;
-    const int head = static_cast<int>(block - slot * heads);
+    const unsigned first = static_cast<unsigned>(a.slots + a.fill) * a.kv_heads;
+    const bool keys = blockIdx.x < first;
+    const unsigned block = keys ? blockIdx.x : blockIdx.x - first, heads = keys ? a.kv_heads : a.heads;
+    const int slot = static_cast<int>(block / heads), head = static_cast<int>(block - slot * heads);
     if (slot >= a.slots) {
-        const int f = static_cast<int>(slot - a.slots);
-        if (keys) attn_clear(a, static_cast<__nv_bfloat16*>(a.dk), nullptr, heads, head, f);
-        attn_clear(a, static_cast<__nv_bfloat16*>(keys ? a.dv : a.out), nullptr, heads, head, f);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int f = slot - a.slots;
+        if (keys) attn_clear(a, static_cast<__nv_bfloat16*>(a.dk), nullptr, a.kv_heads, head, f);
+        attn_clear(a, static_cast<__nv_bfloat16*>(keys ? a.dv : a.out), nullptr, static_cast<int>(heads), head, f);
         return;
     }
-    AttnTile t;
-    if (!attn_find(a, slot, kRows, t)) return;
     if (saddr(raw) % 1024 != 0) {  // no room was taken for aligning it here
         if (threadIdx.x == 0) atomicExch(&g_status, 1);
         return;
     }
     if (warp == 1) {
         tmem_alloc<kCols>(&S.tmem);
-    } else if (warp == 0 && lane == 0) {
+    } else if (warp == 2 && lane == 0) {
         mbar_init(&S.own_full, 1);
         for (int i = 0; i < kStages<DP>; ++i) {
             mbar_init(&S.full[i], 1);
@@ -458,11 +450,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&S.ds_ready, kEltWarps);
         mbar_init(&S.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (warp == 0) {
+        // meanwhile, and only after the kernels before have finished
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        AttnTile found;
+        const bool any = attn_find(a, slot, kRows, found);
+        if (lane == 0) {
+            S.tile = found;
+            S.any = any;
+        }
     }
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);  // uniform, as attn_find's results
+    // from one lane: uniform, as MMAs and copies take their operands
+    const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);
+    const bool any = __shfl_sync(kFullMask, S.any, 0) != 0;
+    AttnTile t;
+    t.begin = __shfl_sync(kFullMask, static_cast<int32_t>(S.tile.begin), 0);
+    t.len = __shfl_sync(kFullMask, S.tile.len, 0);
+    t.tile = __shfl_sync(kFullMask, S.tile.tile, 0);
+    if (!any) {
+        if (warp == 1) tmem_free<kCols>(tmem);
+        return;
+    }
     if (warp < kEltWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (keys) keys_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);

@@ -54,7 +54,9 @@ struct __align__(1024) Smem {
     uint64_t pv_done[NT][2];  // products of the even and the odd key tiles
     uint64_t o_full[NT];
     uint64_t drained;
+    AttnTile tile;
     uint32_t tmem;
+    int32_t any;
 };
 
 // The products of a CTA, in the order in which the tensor cores run them: unit u is key
@@ -93,33 +95,16 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
     Smem<DP, NT>& S = *reinterpret_cast<Smem<DP, NT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t slot = blockIdx.x / a.heads;
-    const int head = static_cast<int>(blockIdx.x - slot * a.heads);
+    const int slot = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.heads));
+    const int head = static_cast<int>(blockIdx.x - static_cast<unsigned>(slot) * a.heads);
     if (slot >= a.slots) {
-        attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, head, static_cast<int>(slot - a.slots));
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, head, slot - a.slots);
         return;
     }
-    AttnTile t;
-    if (!attn_find(a, slot, NT * kRows, t)) return;
-    // the tiles with most keys first
-    const int row0 = (a.causal ? (t.len - 1) / (NT * kRows) - t.tile : t.tile) * NT * kRows;
-    const int token0 = static_cast<int>(t.begin);
-    Units units;
-    units.n[1] = 0;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int first = row0 + i * kRows;
-        const int keys = a.causal ? min(t.len, first + kRows) : t.len;
-        units.n[i] = first < t.len ? (keys + kRows - 1) / kRows : 0;  // 0: no rows
-    }
-    units.lo = min(units.n[0], units.n[1]);
-    units.more = units.n[1] > units.n[0] ? 1 : 0;
-    const int steps = max(units.n[0], units.n[1]);
-
     if (warp == 1) {
         tmem_alloc<C::kCols>(&S.tmem);
-    } else if (warp == 0 && lane == 0) {
+    } else if (warp == 2 && lane == 0) {
         mbar_init(&S.q_full, 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(&S.full[i], 1);
@@ -137,11 +122,45 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
         }
         mbar_init(&S.drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (warp == 0) {
+        // meanwhile, and only after the kernels before have finished
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        AttnTile found;
+        const bool any = attn_find(a, slot, NT * kRows, found);
+        if (lane == 0) {
+            S.tile = found;
+            S.any = any;
+        }
     }
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);  // uniform, as attn_find's results
+    // from one lane: uniform, as MMAs and copies take their operands
+    const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);
+    const bool any = __shfl_sync(kFullMask, S.any, 0) != 0;
+    AttnTile t;
+    t.begin = __shfl_sync(kFullMask, static_cast<int32_t>(S.tile.begin), 0);
+    t.len = __shfl_sync(kFullMask, S.tile.len, 0);
+    t.tile = __shfl_sync(kFullMask, S.tile.tile, 0);
+    if (!any) {
+        if (warp == 1) tmem_free<C::kCols>(tmem);
+        return;
+    }
+    // the tiles with most keys first
+    const int row0 = (a.causal ? (t.len - 1) / (NT * kRows) - t.tile : t.tile) * NT * kRows;
+    const int token0 = static_cast<int>(t.begin);
+    Units units;
+    units.n[1] = 0;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int first = row0 + i * kRows;
+        const int keys = a.causal ? min(t.len, first + kRows) : t.len;
+        units.n[i] = first < t.len ? (keys + kRows - 1) / kRows : 0;  // 0: no rows
+    }
+    units.lo = min(units.n[0], units.n[1]);
+    units.more = units.n[1] > units.n[0] ? 1 : 0;
+    const int steps = max(units.n[0], units.n[1]);
+
     const uint32_t t_s = tmem, t_o = tmem + NB * kRows;
 
     if (warp < kSoftWarp0) {
@@ -311,16 +330,10 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
             sum += all.x + all.y;
         }
         if (ok && count > 0 && wait(&S.o_full[tile], 0)) {
-            const int64_t token = t.begin + row;
-            const float f = 1.0f / sum;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (token * a.heads + head) * a.dim;
-#pragma unroll 1
-            for (int k = 0; k < DP; k += 32) {
-                float o[32];
-                __syncwarp();
-                tmem_ld32(to + k, o);
-                if (row < t.len) store_row32(out, o, f, k, a.dim);
-            }
+            const int64_t token = t.begin + row, first = token - lane;
+            store_rows<DP / 64>(S.q[tile] + quarter * 4096, to, 1.0f / sum,
+                                static_cast<__nv_bfloat16*>(a.out) + (first * a.heads + head) * a.dim,
+                                static_cast<int64_t>(a.heads) * a.dim, t.len - (row - lane), a.dim, lane);
             // from what was subtracted, so that lse and p belong together
             if (row < t.len) a.lse[head * a.tokens + token] = (base + log2f(sum)) * 0.6931471805599453f;
         }

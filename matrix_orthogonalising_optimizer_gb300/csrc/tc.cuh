@@ -75,34 +75,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_
     }
 }
 
-// The same, polling without the suspension that try_wait allows: its wake-up costs
-// hundreds of cycles, which a warp that issues MMAs does not have.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(saddr(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, int32_t* status) {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 1024; ++i)
-            if (mbar_test(bar, parity)) return true;
-        if (globaltimer() - t0 > kWaitNs) {
-            atomicExch(status, 1);
-            return false;
-        }
-    }
-}
-
 // The copies and MMAs below are issued by the one lane whose `e` is not zero, but
 // their warp runs the code around them as a whole: operands that are uniform over
 // the warp then live in uniform registers, where these instructions take them.
