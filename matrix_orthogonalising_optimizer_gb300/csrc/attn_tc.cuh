@@ -41,6 +41,15 @@ __device__ __forceinline__ void product_cols(uint32_t e, uint32_t d, uint64_t a,
     }
 }
 
+// The same with A in TMEM.
+template <int DP>
+__device__ __forceinline__ void product_cols_ts(uint32_t e, uint32_t d, uint32_t a, uint64_t b) {
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k)
+        umma_bf16_ts(e, d, a + static_cast<uint32_t>(8 * k), b + static_cast<uint64_t>((k / 4 * kBox + k % 4 * 32) >> 4),
+                     idesc_of(kRows, false), k != 0 ? 1u : 0u);
+}
+
 // D (128 x DP) (+)= P B over 16 n rows of B, from row 16 k0 on; P in TMEM.
 template <int DP>
 __device__ __forceinline__ void product_rows(uint32_t e, uint32_t d, uint32_t p, uint64_t b, int k0, int n, bool add) {

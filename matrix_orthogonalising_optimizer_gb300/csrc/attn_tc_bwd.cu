@@ -41,16 +41,19 @@ constexpr int kStages = DP == 128 ? 5 : 8;
 
 template <int DP>
 struct __align__(1024) Smem {
-    uint8_t own[2][kTile<DP>];  // queries: Q, dO | keys: K, V
+    uint8_t own[2][kTile<DP>];  // keys: K, V | queries: dO; the second is a slot of the ring, Q its first tile
     uint8_t ring[kStages<DP>][kTile<DP>];
     float stat[2][2][kRows];    // keys: -lse log2(e) and -delta of two query tiles
     uint64_t own_full;
-    uint64_t full[kStages<DP>];
-    uint64_t empty[kStages<DP>];
-    uint64_t s_full[2];
+    uint64_t full[kStages<DP> + 1];
+    uint64_t empty[kStages<DP> + 1];
+    uint64_t s_full;            // s, or s and dp
     uint64_t g_full;            // dp
+    uint64_t taken;             // s and dp are in registers
     uint64_t p_ready;
-    uint64_t ds_ready;
+    uint64_t ds_ready;          // ds, or p and ds
+    uint64_t used;              // they have been read
+    uint64_t q_ready;
     uint64_t stat_full[2];
     uint64_t stat_empty[2];
     uint64_t done;
@@ -59,12 +62,12 @@ struct __align__(1024) Smem {
     int32_t any;
 };
 
-template <int DP>
+template <int kSlots>
 struct Ring {
     int stage = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ void next() {
-        if (++stage == kStages<DP>) {
+        if (++stage == kSlots) {
             stage = 0;
             phase ^= 1;
         }
@@ -85,22 +88,25 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
-// Loads the CTA's own two tiles, then `steps` pairs through the ring: pair i of
-// (first, second) begins at row(i) of head(i).
-template <int DP, typename F>
-__device__ __forceinline__ void produce(Smem<DP>& S, const CUtensorMap* own0, const CUtensorMap* own1, int own_head,
-                                        int own_token, const CUtensorMap* r0, const CUtensorMap* r1, int steps, F where) {
-    const uint32_t e = elect_one();
-    mbar_expect_tx_if(e, &S.own_full, 2 * kTile<DP>);
-    load_tile<DP>(e, saddr(S.own[0]), own0, saddr(&S.own_full), own_head, own_token);
-    load_tile<DP>(e, saddr(S.own[1]), own1, saddr(&S.own_full), own_head, own_token);
-    Ring<DP> r;
-    for (int i = 0; i < 2 * steps; ++i) {
+// One arrival per warp, after its TMEM loads.
+__device__ __forceinline__ void release_warp(uint64_t* bar, int lane) {
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// Loads tiles 0 .. count - 1 through a ring of kSlots at `slots`: what(i, map, head, token)
+// says which.
+template <int DP, int kSlots, typename F>
+__device__ __forceinline__ void produce(Smem<DP>& S, uint32_t e, const uint8_t* slots, int count, F what) {
+    Ring<kSlots> r;
+    for (int i = 0; i < count; ++i) {
         if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[r.stage], r.phase ^ 1, &g_status))) return;
+        const CUtensorMap* map;
         int head, token;
-        where(i / 2, head, token);
+        what(i, map, head, token);
         mbar_expect_tx_if(e, &S.full[r.stage], kTile<DP>);
-        load_tile<DP>(e, saddr(S.ring[r.stage]), i & 1 ? r1 : r0, saddr(&S.full[r.stage]), head, token);
+        load_tile<DP>(e, saddr(slots) + r.stage * kTile<DP>, map, saddr(&S.full[r.stage]), head, token);
         r.next();
     }
 }
@@ -115,72 +121,89 @@ __device__ __forceinline__ void store_cols64(uint32_t t, const float (&v)[64]) {
 
 // ---------------------------------------------------------------- side of the keys
 
+// TMEM columns.  Heads of up to 64 leave room for p and ds beside s and dp, which then
+// make way for the next tile as soon as they are in registers.
+template <int DP>
+struct KeysCols {
+    static constexpr bool kApart = DP == 64;
+    static constexpr uint32_t kS = 0, kG = kRows;
+    static constexpr uint32_t kP = kApart ? 256 : kS, kDs = kApart ? 320 : kG;
+    static constexpr uint32_t kDv = kApart ? 384 : 256, kDk = kDv + DP;
+    static constexpr uint32_t kHalf = kApart ? 32 : 64;  // between the halves of p and ds
+};
+
 template <int DP, bool kElt>
 __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq, const CUtensorMap* mk,
                                           const CUtensorMap* mv, const CUtensorMap* mo, const AttnTile& t, int kv,
                                           int warp, int lane, uint32_t tmem) {
+    using C = KeysCols<DP>;
+    constexpr int NS = kStages<DP>;
     const int token0 = static_cast<int>(t.begin), row0 = t.tile * kRows;
     const int first = a.causal ? row0 : 0;                             // the first query that sees any of the keys
     const int per_head = (t.len - first + kRows - 1) / kRows, steps = per_head * a.group;
-    const uint32_t t_s = tmem, t_g = tmem + kRows, t_dv = tmem + 2 * kRows, t_dk = t_dv + DP;
     const auto where = [&](int i, int& head, int& row) {
         const int h = i / per_head;
         head = kv * a.group + h;
         row = first + (i - h * per_head) * kRows;
     };
     if (!kElt && warp == 0) {
-        produce<DP>(S, mk, mv, kv, token0 + row0, mq, mo, steps, [&](int i, int& head, int& token) {
-            where(i, head, token);
+        const uint32_t e = elect_one();
+        mbar_expect_tx_if(e, &S.own_full, 2 * kTile<DP>);
+        load_tile<DP>(e, saddr(S.own[0]), mk, saddr(&S.own_full), kv, token0 + row0);
+        load_tile<DP>(e, saddr(S.own[1]), mv, saddr(&S.own_full), kv, token0 + row0);
+        produce<DP, NS>(S, e, S.ring[0], 2 * steps, [&](int i, const CUtensorMap*& map, int& head, int& token) {
+            where(i / 2, head, token);
             token += token0;
+            map = i & 1 ? mo : mq;
         });
     } else if (!kElt && warp == 1) {
         const uint32_t e = elect_one();
         const uint32_t own = saddr(S.own[0]), ring = saddr(S.ring[0]);
         const uint64_t dk_k = desc_k(own), dk_v = desc_k(own + kTile<DP>);
-        Ring<DP> r;
-        bool ok = wait_warp(&S.own_full, 0) && wait_warp(&S.full[0], 0);
+        Ring<NS> r;
         int sq = 0, so = 0;  // ring slots of the tile at hand
-        if (ok) {
-            product_cols<DP>(e, t_s, dk_k, desc_k(ring));
-            umma_commit(e, saddr(&S.s_full[0]));
+        // s, and dp, of the next tile of the ring
+        const auto form = [&](uint32_t cols, uint64_t key, uint64_t* full, int& slot) {
+            slot = r.stage;
+            if (!wait_warp(&S.full[slot], r.phase)) return false;
+            product_cols<DP>(e, tmem + cols, key, desc_k(ring + slot * kTile<DP>));
+            if (full) umma_commit(e, saddr(full));
             r.next();
-            so = r.stage;
-            ok = wait_warp(&S.full[r.stage], r.phase);
-        }
-        if (ok) {
-            product_cols<DP>(e, t_g, dk_v, desc_k(ring + so * kTile<DP>));
-            umma_commit(e, saddr(&S.g_full));
-            r.next();
-        }
+            return true;
+        };
+        const auto add = [&](uint32_t cols, uint32_t p, int slot, bool more) {
+            product_rows<DP>(e, tmem + cols, tmem + p, desc_mn(ring + slot * kTile<DP>), 0, 4, more);
+            product_rows<DP>(e, tmem + cols, tmem + p + C::kHalf, desc_mn(ring + slot * kTile<DP>), 4, 4, true);
+        };
+        bool ok = wait_warp(&S.own_full, 0) && form(C::kS, dk_k, C::kApart ? nullptr : &S.s_full, sq) &&
+                  form(C::kG, dk_v, C::kApart ? &S.s_full : &S.g_full, so);
         for (int i = 0; i < steps && ok; ++i) {
             const bool more = i + 1 < steps;
-            const int sq1 = r.stage;
-            ok = wait_warp(&S.p_ready, i & 1);
-            if (!ok) break;
-            product_rows<DP>(e, t_dv, t_s, desc_mn(ring + so * kTile<DP>), 0, 4, i > 0);
-            product_rows<DP>(e, t_dv, t_s + 64, desc_mn(ring + so * kTile<DP>), 4, 4, true);
-            umma_commit(e, saddr(&S.empty[so]));
-            if (more) {
-                ok = wait_warp(&S.full[r.stage], r.phase);
+            int sq1 = 0, so1 = 0;
+            if constexpr (C::kApart) {
+                if (more)
+                    ok = wait_warp(&S.taken, i & 1) && form(C::kS, dk_k, nullptr, sq1) &&
+                         form(C::kG, dk_v, &S.s_full, so1);
+                ok = ok && wait_warp(&S.ds_ready, i & 1);
                 if (!ok) break;
-                product_cols<DP>(e, t_s, dk_k, desc_k(ring + sq1 * kTile<DP>));
-                umma_commit(e, saddr(&S.s_full[0]));
-                r.next();
-                so = r.stage;
-            }
-            ok = wait_warp(&S.ds_ready, i & 1);
-            if (!ok) break;
-            product_rows<DP>(e, t_dk, t_g, desc_mn(ring + sq * kTile<DP>), 0, 4, i > 0);
-            product_rows<DP>(e, t_dk, t_g + 64, desc_mn(ring + sq * kTile<DP>), 4, 4, true);
-            umma_commit(e, saddr(&S.empty[sq]));
-            if (more) {
-                ok = wait_warp(&S.full[r.stage], r.phase);
+                add(C::kDv, C::kP, so, i > 0);
+                umma_commit(e, saddr(&S.empty[so]));
+                add(C::kDk, C::kDs, sq, i > 0);
+                umma_commit(e, saddr(&S.empty[sq]));
+                umma_commit(e, saddr(&S.used));
+            } else {
+                ok = wait_warp(&S.p_ready, i & 1);
                 if (!ok) break;
-                product_cols<DP>(e, t_g, dk_v, desc_k(ring + so * kTile<DP>));
-                umma_commit(e, saddr(&S.g_full));
-                r.next();
-                sq = sq1;
+                add(C::kDv, C::kP, so, i > 0);
+                umma_commit(e, saddr(&S.empty[so]));
+                ok = (!more || form(C::kS, dk_k, &S.s_full, sq1)) && wait_warp(&S.ds_ready, i & 1);
+                if (!ok) break;
+                add(C::kDk, C::kDs, sq, i > 0);
+                umma_commit(e, saddr(&S.empty[sq]));
+                if (more) ok = form(C::kG, dk_v, &S.g_full, so1);
             }
+            sq = sq1;
+            so = so1;
         }
         // also after a wait that gave up: no MMA or commit is under way when the CTA leaves
         umma_commit(e, saddr(&S.done));
@@ -203,8 +226,9 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
         }
     } else if (kElt) {
         const int half = (warp - kEltWarp0) / 4, thread = threadIdx.x - 32 * kEltWarp0, r = thread % kRows;
-        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
-        const uint32_t ts = t_s + 64 * half + lanes, tg = t_g + 64 * half + lanes;
+        const uint32_t lanes = (static_cast<uint32_t>(warp % 4 * 32) << 16) + tmem;
+        const uint32_t ts = C::kS + 64 * half + lanes, tg = C::kG + 64 * half + lanes;
+        const uint32_t tp = C::kP + C::kHalf * half + lanes, td = C::kDs + C::kHalf * half + lanes;
         const float2 c2 = both(a.scale_log2);
         bool ok = true;
         for (int i = 0; i < steps && ok; ++i) {
@@ -215,10 +239,14 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
             // columns of this half that see key r: [lo, hi)
             const bool masked = queries < kRows || (a.causal && row == row0);
             const int lo = (a.causal ? row0 + r - row : 0) - 64 * half, hi = queries - 64 * half;
-            ok = wait_warp(&S.stat_full[st], (i >> 1) & 1) && wait_warp(&S.s_full[0], i & 1);
+            ok = wait_warp(&S.stat_full[st], (i >> 1) & 1) && wait_warp(&S.s_full, i & 1);
             if (!ok) break;
-            float p[64];
+            float p[64], g[C::kApart ? 64 : 32];
             tmem_ld64(ts, p);
+            if constexpr (C::kApart) {
+                tmem_ld64(tg, g);
+                release_warp(&S.taken, lane);
+            }
             const float4* nl = reinterpret_cast<const float4*>(&S.stat[st][0][64 * half]);
 #pragma unroll
             for (int k = 0; k < 64; k += 4) {
@@ -235,52 +263,59 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
                 for (int k = 0; k < 64; ++k)
                     if (k < lo || k >= hi) p[k] = 0.0f;
             }
-            store_cols64(ts, p);
+            if constexpr (C::kApart) {
+                // the products of the tile before have read p and ds
+                if (i > 0) ok = wait_warp(&S.used, (i - 1) & 1);
+                if (!ok) break;
+            }
+            store_cols64(tp, p);
             if (queries < kRows) {
                 // query rows behind the sequence, of dO before dv reads it, of Q before dk does
                 const int o = 2 * i + 1;
-                ok = wait_warp(&S.full[o % kStages<DP>], (o / kStages<DP>) & 1);
+                ok = wait_warp(&S.full[o % NS], (o / NS) & 1);
                 if (!ok) break;
-                clear_rows<DP>(S.ring[o % kStages<DP>], queries, thread, 256);
-                clear_rows<DP>(S.ring[2 * i % kStages<DP>], queries, thread, 256);
+                clear_rows<DP>(S.ring[o % NS], queries, thread, 256);
+                clear_rows<DP>(S.ring[2 * i % NS], queries, thread, 256);
             }
-            arrive_warp(&S.p_ready, lane);
-            ok = wait_warp(&S.g_full, i & 1);
-            if (!ok) break;
+            if constexpr (!C::kApart) {
+                arrive_warp(&S.p_ready, lane);
+                ok = wait_warp(&S.g_full, i & 1);
+                if (!ok) break;
+            }
             const float4* nd = reinterpret_cast<const float4*>(&S.stat[st][1][64 * half]);
-            uint32_t w[32];
 #pragma unroll
             for (int h = 0; h < 64; h += 32) {
-                float g[32];
-                tmem_ld32(tg + h, g);
+                if constexpr (!C::kApart) tmem_ld32(tg + h, reinterpret_cast<float(&)[32]>(g));
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    const float4 d = nd[(h + k) / 4];
-                    float2 x = add2(make_float2(g[k], g[k + 1]), make_float2(d.x, d.y));
-                    float2 y = add2(make_float2(g[k + 2], g[k + 3]), make_float2(d.z, d.w));
-                    x = mul2(x, make_float2(p[h + k], p[h + k + 1]));
-                    y = mul2(y, make_float2(p[h + k + 2], p[h + k + 3]));
-                    if (masked) {
-                        // not 0 times what the columns behind the sequence hold
-                        x.x = h + k < lo || h + k >= hi ? 0.0f : x.x;
-                        x.y = h + k + 1 < lo || h + k + 1 >= hi ? 0.0f : x.y;
-                        y.x = h + k + 2 < lo || h + k + 2 >= hi ? 0.0f : y.x;
-                        y.y = h + k + 3 < lo || h + k + 3 >= hi ? 0.0f : y.y;
-                    }
-                    w[(h + k) / 2] = pack_bf16x2(x.x, x.y);
-                    w[(h + k) / 2 + 1] = pack_bf16x2(y.x, y.y);
+                    const int n = h + k, m = C::kApart ? n : k;
+                    const float4 d = nd[n / 4];
+                    const float2 x = mul2(make_float2(p[n], p[n + 1]),
+                                          add2(make_float2(g[m], g[m + 1]), make_float2(d.x, d.y)));
+                    const float2 y = mul2(make_float2(p[n + 2], p[n + 3]),
+                                          add2(make_float2(g[m + 2], g[m + 3]), make_float2(d.z, d.w)));
+                    p[n] = x.x;
+                    p[n + 1] = x.y;
+                    p[n + 2] = y.x;
+                    p[n + 3] = y.y;
                 }
             }
-            tmem_st32(tg, w);
+            if (masked) {
+                // not 0 times what the columns behind the sequence hold
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                    if (k < lo || k >= hi) p[k] = 0.0f;
+            }
+            store_cols64(td, p);
             arrive_warp(&S.ds_ready, lane);
             if (lane == 0) mbar_arrive(&S.stat_empty[st]);
         }
         if (ok && wait_warp(&S.done, 0)) {
             // one warpgroup stores dv, the other dk
             const int quarter = warp % 4;
-            const int64_t first = t.begin + row0 + 32 * quarter;
-            store_rows<DP / 64>(S.own[half] + quarter * 4096, (half ? t_dk : t_dv) + lanes, half ? a.scale : 1.0f,
-                                static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (first * a.kv_heads + kv) * a.dim,
+            const int64_t out = t.begin + row0 + 32 * quarter;
+            store_rows<DP / 64>(S.own[half] + quarter * 4096, (half ? C::kDk : C::kDv) + lanes, half ? a.scale : 1.0f,
+                                static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (out * a.kv_heads + kv) * a.dim,
                                 static_cast<int64_t>(a.kv_heads) * a.dim, t.len - row0 - 32 * quarter, a.dim, lane);
         }
     }
@@ -288,121 +323,134 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
 
 // ---------------------------------------------------------------- side of the queries
 
+// TMEM columns: s, dp, ds, Q (the left operand of s, so that its place in shared memory
+// becomes one more slot of the ring), dq.
+constexpr uint32_t kQs = 0, kQg = 128, kQds = 256, kQq = 320, kQdq = 384;
+
 template <int DP, bool kElt>
 __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq,
                                              const CUtensorMap* mk, const CUtensorMap* mv, const CUtensorMap* mo,
                                              const AttnTile& t, int head, int warp, int lane, uint32_t tmem) {
+    constexpr int NS = kStages<DP> + 1;  // slots from own[1] on; Q passes through the first
     // the tiles with most keys first
     const int token0 = static_cast<int>(t.begin);
     const int row0 = (a.causal ? (t.len - 1) / kRows - t.tile : t.tile) * kRows;
     const int keys_all = a.causal ? min(t.len, row0 + kRows) : t.len;
     const int steps = (keys_all + kRows - 1) / kRows;
-    const uint32_t t_s = tmem, t_g = tmem + 2 * kRows, t_dq = tmem + 3 * kRows;
+    uint8_t* slots = S.own[1];
     if (!kElt && warp == 0) {
-        produce<DP>(S, mq, mo, head, token0 + row0, mk, mv, steps, [&](int i, int& h, int& token) {
-            h = head / a.group;
-            token = token0 + i * kRows;
+        const uint32_t e = elect_one();
+        mbar_expect_tx_if(e, &S.own_full, kTile<DP>);
+        load_tile<DP>(e, saddr(S.own[0]), mo, saddr(&S.own_full), head, token0 + row0);
+        produce<DP, NS>(S, e, slots, 1 + 2 * steps, [&](int i, const CUtensorMap*& map, int& h, int& token) {
+            const bool q = i == 0;
+            map = q ? mq : i & 1 ? mk : mv;
+            h = q ? head : head / a.group;
+            token = q ? token0 + row0 : token0 + (i - 1) / 2 * kRows;
         });
     } else if (!kElt && warp == 1) {
         const uint32_t e = elect_one();
-        const uint32_t own = saddr(S.own[0]), ring = saddr(S.ring[0]);
-        const uint64_t d_q = desc_k(own), d_o = desc_k(own + kTile<DP>);
-        Ring<DP> r;
-        bool ok = wait_warp(&S.own_full, 0) && wait_warp(&S.full[0], 0);
+        const uint32_t base = saddr(slots);
+        const uint64_t d_o = desc_k(saddr(S.own[0]));
+        Ring<NS> r;
+        r.next();
         int sk = 0;
-        if (ok) {
-            product_cols<DP>(e, t_s, d_q, desc_k(ring));
-            umma_commit(e, saddr(&S.s_full[0]));
+        // s and dp of the ring's next two tiles
+        const auto form = [&](int& slot) {
+            slot = r.stage;
+            if (!wait_warp(&S.full[slot], r.phase)) return false;
+            product_cols_ts<DP>(e, tmem + kQs, tmem + kQq, desc_k(base + slot * kTile<DP>));
             r.next();
-            ok = wait_warp(&S.full[r.stage], r.phase);
-        }
-        if (ok) {
-            product_cols<DP>(e, t_g, d_o, desc_k(ring + r.stage * kTile<DP>));
-            umma_commit(e, saddr(&S.g_full));
+            if (!wait_warp(&S.full[r.stage], r.phase)) return false;
+            product_cols<DP>(e, tmem + kQg, d_o, desc_k(base + r.stage * kTile<DP>));
+            umma_commit(e, saddr(&S.s_full));
             umma_commit(e, saddr(&S.empty[r.stage]));
             r.next();
-        }
+            return true;
+        };
+        bool ok = wait_warp(&S.q_ready, 0);
+        if (ok && lane == 0) mbar_arrive(&S.empty[0]);
+        __syncwarp();
+        ok = ok && wait_warp(&S.own_full, 0) && form(sk);
         for (int i = 0; i < steps && ok; ++i) {
-            const bool more = i + 1 < steps;
-            const int sk1 = r.stage, b = i & 1;
-            if (more) {
-                // the other buffer's ds was read by the product before
-                ok = wait_warp(&S.full[r.stage], r.phase);
-                if (!ok) break;
-                product_cols<DP>(e, t_s + (b ^ 1) * kRows, d_q, desc_k(ring + sk1 * kTile<DP>));
-                umma_commit(e, saddr(&S.s_full[b ^ 1]));
-                r.next();
-            }
-            ok = wait_warp(&S.ds_ready, i & 1);
+            int sk1 = 0;
+            if (i + 1 < steps) ok = wait_warp(&S.taken, i & 1) && form(sk1);
+            ok = ok && wait_warp(&S.ds_ready, i & 1);
             if (!ok) break;
-            if (more) {
-                ok = wait_warp(&S.full[r.stage], r.phase);
-                if (!ok) break;
-                product_cols<DP>(e, t_g, d_o, desc_k(ring + r.stage * kTile<DP>));
-                umma_commit(e, saddr(&S.g_full));
-                umma_commit(e, saddr(&S.empty[r.stage]));
-                r.next();
-            }
-            product_rows<DP>(e, t_dq, t_s + b * kRows, desc_mn(ring + sk * kTile<DP>), 0, 4, i > 0);
-            product_rows<DP>(e, t_dq, t_s + b * kRows + 64, desc_mn(ring + sk * kTile<DP>), 4, 4, true);
+            product_rows<DP>(e, tmem + kQdq, tmem + kQds, desc_mn(base + sk * kTile<DP>), 0, 8, i > 0);
             umma_commit(e, saddr(&S.empty[sk]));
+            umma_commit(e, saddr(&S.used));
             sk = sk1;
         }
         umma_commit(e, saddr(&S.done));
         mbar_wait<false>(&S.done, 0, &g_status);
     } else if (kElt) {
         const int half = (warp - kEltWarp0) / 4, thread = threadIdx.x - 32 * kEltWarp0, r = thread % kRows;
-        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
-        const uint32_t tg = t_g + 64 * half + lanes;
+        const uint32_t lanes = (static_cast<uint32_t>(warp % 4 * 32) << 16) + tmem;
         const int row = row0 + r;
         const bool in = row < t.len;
         const int64_t token = t.begin + row;
         const float2 c2 = both(a.scale_log2);
         const float2 nl = both(in ? a.lse[head * a.tokens + token] * -kLog2e : 0.0f);
         const float2 nd = both(in ? -a.delta[head * a.tokens + token] : 0.0f);
-        bool ok = true;
-        for (int i = 0; i < steps && ok; ++i) {
-            const int b = i & 1, keys = min(kRows, t.len - i * kRows);
-            const uint32_t ts = t_s + b * kRows + 64 * half + lanes;
-            ok = wait_warp(&S.s_full[b], (i >> 1) & 1);
-            if (!ok) break;
-            float p[64];
-            tmem_ld64(ts, p);
-#pragma unroll
-            for (int k = 0; k < 64; k += 2) {
-                const float2 x = fma2(make_float2(p[k], p[k + 1]), c2, nl);
-                p[k] = ex2(x.x);
-                p[k + 1] = ex2(x.y);
-            }
-            ok = wait_warp(&S.g_full, i & 1);
-            if (!ok) break;
-            const bool masked = keys < kRows || (a.causal && i + 1 == steps);
-            const int seen = (a.causal ? min(row + 1 - i * kRows, keys) : keys) - 64 * half;
+        bool ok = wait_warp(&S.full[0], 0);
+        if (ok) {
+            // Q into TMEM, half of each row's 16-byte pieces per warpgroup (DP / 4 words)
             uint32_t w[32];
 #pragma unroll
-            for (int h = 0; h < 64; h += 32) {
-                float g[32];
-                tmem_ld32(tg + h, g);
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float2 x = mul2(make_float2(p[h + k], p[h + k + 1]), add2(make_float2(g[k], g[k + 1]), nd));
-                    if (masked) {
-                        x.x = h + k < seen ? x.x : 0.0f;
-                        x.y = h + k + 1 < seen ? x.y : 0.0f;
-                    }
-                    w[(h + k) / 2] = pack_bf16x2(x.x, x.y);
-                }
+            for (int k = 0; k < DP / 16; ++k) {
+                const int piece = DP / 16 * half + k;
+                const uint4 x = *reinterpret_cast<const uint4*>(slots + piece / 8 * kBox + r * 128 +
+                                                                (piece % 8 ^ r % 8) * 16);
+                w[4 * k] = x.x;
+                w[4 * k + 1] = x.y;
+                w[4 * k + 2] = x.z;
+                w[4 * k + 3] = x.w;
             }
-            tmem_st32(ts, w);
-            if (keys < kRows) clear_rows<DP>(S.ring[2 * i % kStages<DP>], keys, thread, 256);  // keys behind the sequence
+            if constexpr (DP == 128) tmem_st32(lanes + kQq + 32 * half, w);
+            else tmem_st16(lanes + kQq + 16 * half, reinterpret_cast<const float(&)[16]>(w));
+            // the loads above before the ring's next copy into this place
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            arrive_warp(&S.q_ready, lane);
+        }
+        for (int i = 0; i < steps && ok; ++i) {
+            const int keys = min(kRows, t.len - i * kRows);
+            ok = wait_warp(&S.s_full, i & 1);
+            if (!ok) break;
+            float p[64], g[64];
+            tmem_ld64(lanes + kQs + 64 * half, p);
+            tmem_ld64(lanes + kQg + 64 * half, g);
+            release_warp(&S.taken, lane);
+            const bool masked = keys < kRows || (a.causal && i + 1 == steps);
+            const int seen = (a.causal ? min(row + 1 - i * kRows, keys) : keys) - 64 * half;
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+                float2 x = fma2(make_float2(p[k], p[k + 1]), c2, nl);
+                x = mul2(make_float2(ex2(x.x), ex2(x.y)), add2(make_float2(g[k], g[k + 1]), nd));
+                p[k] = x.x;
+                p[k + 1] = x.y;
+            }
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                    if (k >= seen) p[k] = 0.0f;
+            }
+            if (keys < kRows) {
+                // keys behind the sequence
+                clear_rows<DP>(slots + (1 + 2 * i) % NS * kTile<DP>, keys, thread, 256);
+            }
+            // the product of the tile before has read ds
+            if (i > 0) ok = wait_warp(&S.used, (i - 1) & 1);
+            if (!ok) break;
+            store_cols64(lanes + kQds + 32 * half, p);
             arrive_warp(&S.ds_ready, lane);
         }
         // a box of 64 columns each warpgroup
         if (64 * half < DP && ok && wait_warp(&S.done, 0)) {
             const int quarter = warp % 4;
-            const int64_t first = t.begin + row0 + 32 * quarter;
-            store_rows<1>(S.own[0] + half * kBox + quarter * 4096, t_dq + 64 * half + lanes, a.scale,
-                          static_cast<__nv_bfloat16*>(a.out) + (first * a.heads + head) * a.dim + 64 * half,
+            const int64_t out = t.begin + row0 + 32 * quarter;
+            store_rows<1>(S.own[0] + half * kBox + quarter * 4096, kQdq + 64 * half + lanes, a.scale,
+                          static_cast<__nv_bfloat16*>(a.out) + (out * a.heads + head) * a.dim + 64 * half,
                           static_cast<int64_t>(a.heads) * a.dim, t.len - row0 - 32 * quarter, a.dim - 64 * half, lane);
         }
     }
@@ -436,18 +484,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc<kCols>(&S.tmem);
     } else if (warp == 2 && lane == 0) {
         mbar_init(&S.own_full, 1);
-        for (int i = 0; i < kStages<DP>; ++i) {
+        for (int i = 0; i < kStages<DP> + 1; ++i) {
             mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&S.s_full[i], 1);
             mbar_init(&S.stat_full[i], 1);
             mbar_init(&S.stat_empty[i], kEltWarps);
         }
+        mbar_init(&S.s_full, 1);
         mbar_init(&S.g_full, 1);
+        mbar_init(&S.used, 1);
+        mbar_init(&S.taken, kEltWarps);
         mbar_init(&S.p_ready, kEltWarps);
         mbar_init(&S.ds_ready, kEltWarps);
+        mbar_init(&S.q_ready, kEltWarps);
         mbar_init(&S.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     } else if (warp == 0) {
