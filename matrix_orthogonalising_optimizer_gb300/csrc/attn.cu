@@ -101,12 +101,41 @@ int set_maps(AttnMaps& m, const AttnArgs& a) {
     return DMUON_OK;
 }
 
+// Blocks that share a key tile's queries.  The longest of them must not outlast the rest
+// of the launch: about group * tiles steps, against the whole backward pass's steps over
+// all SMs (a query tile's step costs 0.8 of a key tile's).  With sequences of the average
+// length.  Measured, one part -> as chosen: 2048 tokens, 32 / 1 heads of 128: 640 -> 110 us;
+// 1024 tokens, 16 / 2 heads of 128: 96 -> 38 us; fp32, 777 tokens, 6 / 2 heads of 80: 367 ->
+// 136 us.
+constexpr int kMaxParts = 16;
+
+int parts_of(int64_t sequences, int64_t tokens, int64_t heads, int64_t kv_heads, bool causal, bool tc) {
+    const int64_t tile = tc ? 128 : 64, sms = 152;
+    const double length = static_cast<double>(tokens) / static_cast<double>(sequences);
+    const double tiles = std::max(1.0, std::ceil(length / static_cast<double>(tile)));
+    const double pairs = causal ? tiles * (tiles + 1.0) / 2.0 : tiles * tiles;
+    // the FFMA kernels' two sides are separate launches, two blocks per SM
+    const double share = (tc ? 1.8 : 0.5) * static_cast<double>(heads * sequences) * pairs / sms;
+    const double longest = static_cast<double>(heads / kv_heads) * tiles;
+    // below 2.5 the partial sums cost more than the wait (2048 tokens, 8 heads of 128: 37 -> 60 us)
+    const double ratio = longest / std::max(share, 2.0);
+    return ratio < 2.5 ? 1 : static_cast<int>(std::min<double>({std::ceil(ratio), longest, kMaxParts}));
+}
+
 struct Layout {
     float* delta = nullptr;
+    float* partial = nullptr;
+    int parts = 1;
     size_t bytes = 0;
-    Layout(char* base, int64_t tokens, int64_t heads, bool backward) {
+    // the workspace serves either kind of kernels, causal or not
+    Layout(char* base, int64_t sequences, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim, bool backward) {
         Arena a{base};
-        if (backward) delta = a.take<float>(tokens * heads);
+        if (backward) {
+            delta = a.take<float>(tokens * heads);
+            for (int k = 0; k < 4; ++k)
+                parts = std::max(parts, parts_of(sequences, tokens, heads, kv_heads, (k & 1) != 0, (k & 2) != 0));
+            if (parts > 1) partial = a.take<float>(2 * parts * tokens * kv_heads * dim);
+        }
         bytes = a.off;
     }
 };
@@ -121,7 +150,7 @@ extern "C" size_t dmuon_attention_workspace_bytes(int64_t sequences, int64_t tok
     if (!sizes_ok(tokens, sequences, heads, kv_heads, dim) ||
         check_dtype(dtype, "dmuon_attention_workspace_bytes") != DMUON_OK)
         return 0;
-    return Layout(nullptr, tokens, heads, backward != 0).bytes;
+    return tokens == 0 ? 0 : Layout(nullptr, sequences, tokens, heads, kv_heads, dim, backward != 0).bytes;
 }
 
 extern "C" int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, const dmuon_heads_t* v,
@@ -134,7 +163,7 @@ extern "C" int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads
     if (tokens == 0) return DMUON_OK;
     OPS_TRY(check_ptr(o, "o", where));
     OPS_TRY(check_ptr(lse, "lse", where));
-    const Layout L(static_cast<char*>(workspace), tokens, heads, false);
+    const Layout L(static_cast<char*>(workspace), sequences, tokens, heads, kv_heads, dim, false);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
     a.out = o;
@@ -167,7 +196,7 @@ extern "C" int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_he
     OPS_TRY(check_ptr(dq, "dq", where));
     OPS_TRY(check_ptr(dk, "dk", where));
     OPS_TRY(check_ptr(dv, "dv", where));
-    const Layout L(static_cast<char*>(workspace), tokens, heads, true);
+    const Layout L(static_cast<char*>(workspace), sequences, tokens, heads, kv_heads, dim, true);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
     a.o = o;
@@ -177,13 +206,17 @@ extern "C" int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_he
     a.dk = dk;
     a.dv = dv;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool tc = tensor_cores(a, dtype, true);
+    a.parts = parts_of(sequences, tokens, heads, kv_heads, a.causal != 0, tc);
+    a.partial = L.partial;
     OPS_CUDA(attn_delta(a, f32, s));
-    if (tensor_cores(a, dtype, true)) {
+    if (tc) {
         AttnMaps m = {};
         OPS_TRY(set_maps(m, a));
         OPS_CUDA(attn_tc_backward(a, m, s));
     } else {
         OPS_CUDA(attn_simt_backward(a, f32, s));
     }
+    if (a.parts > 1) OPS_CUDA(attn_join(a, f32, s));
     return DMUON_OK;
 }

@@ -30,6 +30,8 @@ struct AttnArgs {
     int32_t causal;
     int32_t slots;             // row tiles of a head (an upper bound: see attn_slots)
     int32_t fill;              // blocks behind them that clear the rows of no sequence
+    int32_t parts;             // backward: blocks that share the queries of a key tile
+    float* partial;            // parts > 1: [2][parts][tokens][kv_heads][dim] sums of dk (unscaled) and dv
     float scale, scale_log2;   // scale_log2 = scale * log2(e)
 };
 
@@ -104,9 +106,20 @@ cudaError_t attn_tc_backward(const AttnArgs& a, const AttnMaps& m, cudaStream_t 
 cudaError_t attn_fwd_status_word(void** p);  // the kernels' time-out flags on the current device
 cudaError_t attn_bwd_status_word(void** p);
 
+// The range of a key tile's steps (query tiles of all its heads) that part p takes.
+__host__ __device__ inline int attn_part(int steps, int p, int parts) {
+    return static_cast<int>(static_cast<int64_t>(steps) * p / parts);
+}
+
+__device__ __forceinline__ float* attn_partial(const AttnArgs& a, int which, int part) {
+    return a.partial + (static_cast<int64_t>(which) * a.parts + part) * a.tokens * a.kv_heads * a.dim;
+}
+
 // FFMA kernels (attn_simt.cu): any strides, either type.
 cudaError_t attn_simt_forward(const AttnArgs& a, bool f32, cudaStream_t s);
 cudaError_t attn_simt_backward(const AttnArgs& a, bool f32, cudaStream_t s);
+// dk and dv from their partial sums, in the order of the parts
+cudaError_t attn_join(const AttnArgs& a, bool f32, cudaStream_t s);
 // delta, for both backward passes
 cudaError_t attn_delta(const AttnArgs& a, bool f32, cudaStream_t s);
 

@@ -18,6 +18,7 @@
 #include "act.cuh"
 #include "attn.h"
 #include "internal.h"
+#include "ops.h"
 #include "tc.cuh"
 
 namespace dmuon {
@@ -73,16 +74,18 @@ __device__ __forceinline__ void load_tile(float* dst, const AttnHeads& h, int64_
     }
 }
 
-// acc[r][c] = sum_d A[ty + 16 r][d] B[tx + 16 c][d]
+// acc[r][c] = sum_d A[ty + 16 r][d] B[tx + 16 c][d].  Packed arithmetic (two products an
+// instruction, the same rate) leaves the issue slots that the loads need.
 template <int DP>
 __device__ __forceinline__ void product_nt(float (&acc)[4][4], const float* A, const float* B, int dim4) {
     constexpr int LD = DP + 4;
     const float* a0 = A + (threadIdx.x / 16) * LD;
     const float* b0 = B + (threadIdx.x % 16) * LD;
+    float2 sum[4][4];  // even and odd d
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
+        for (int c = 0; c < 4; ++c) sum[r][c] = tc::both(0.0f);
 #pragma unroll 2
     for (int d = 0; d < dim4; d += 4) {
         float4 a[4], b[4];
@@ -94,17 +97,19 @@ __device__ __forceinline__ void product_nt(float (&acc)[4][4], const float* A, c
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                acc[r][c] = fmaf(a[r].x, b[c].x, acc[r][c]);
-                acc[r][c] = fmaf(a[r].y, b[c].y, acc[r][c]);
-                acc[r][c] = fmaf(a[r].z, b[c].z, acc[r][c]);
-                acc[r][c] = fmaf(a[r].w, b[c].w, acc[r][c]);
+                sum[r][c] = tc::fma2(make_float2(a[r].x, a[r].y), make_float2(b[c].x, b[c].y), sum[r][c]);
+                sum[r][c] = tc::fma2(make_float2(a[r].z, a[r].w), make_float2(b[c].z, b[c].w), sum[r][c]);
             }
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = sum[r][c].x + sum[r][c].y;
 }
 
-// acc[r][k] += sum_j P[ty + 16 r][j] V[j][4 tx + 64 (k / 4) + k % 4]
+// acc[r][k] += sum_j P[ty + 16 r][j] V[j][4 tx + 64 (k / 2) + 2 (k % 2) ..]
 template <int DP>
-__device__ __forceinline__ void product_nn(float (&acc)[4][DP / 16], const float* P, const float* V) {
+__device__ __forceinline__ void product_nn(float2 (&acc)[4][DP / 32], const float* P, const float* V) {
     constexpr int LD = DP + 4;
     const float* p0 = P + (threadIdx.x / 16) * LP;
     const float* v0 = V + 4 * (threadIdx.x % 16);
@@ -120,11 +125,9 @@ __device__ __forceinline__ void product_nn(float (&acc)[4][DP / 16], const float
                 const float4 v = *reinterpret_cast<const float4*>(v0 + (j + jj) * LD + 64 * c);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float w = jj == 0 ? p[r].x : jj == 1 ? p[r].y : jj == 2 ? p[r].z : p[r].w;
-                    acc[r][4 * c] = fmaf(w, v.x, acc[r][4 * c]);
-                    acc[r][4 * c + 1] = fmaf(w, v.y, acc[r][4 * c + 1]);
-                    acc[r][4 * c + 2] = fmaf(w, v.z, acc[r][4 * c + 2]);
-                    acc[r][4 * c + 3] = fmaf(w, v.w, acc[r][4 * c + 3]);
+                    const float2 w = tc::both(jj == 0 ? p[r].x : jj == 1 ? p[r].y : jj == 2 ? p[r].z : p[r].w);
+                    acc[r][2 * c] = tc::fma2(w, make_float2(v.x, v.y), acc[r][2 * c]);
+                    acc[r][2 * c + 1] = tc::fma2(w, make_float2(v.z, v.w), acc[r][2 * c + 1]);
                 }
             }
     }
@@ -132,7 +135,7 @@ __device__ __forceinline__ void product_nn(float (&acc)[4][DP / 16], const float
 
 // Rows ty + 16 r < rows of a contiguous tokens x heads x dim tensor, times f[r].
 template <typename E, int DP>
-__device__ __forceinline__ void store_rows(void* out, const float (&acc)[4][DP / 16], const float (&f)[4],
+__device__ __forceinline__ void store_rows(void* out, const float2 (&acc)[4][DP / 32], const float (&f)[4],
                                            int64_t row0, int rows, int heads, int head, int dim) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll
@@ -143,7 +146,7 @@ __device__ __forceinline__ void store_rows(void* out, const float (&acc)[4][DP /
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
             const int d = 4 * tx + 64 * (k / 4) + k % 4;
-            if (d < dim) p[d] = from_f<E>(acc[r][k] * f[r]);
+            if (d < dim) p[d] = from_f<E>((k % 2 ? acc[r][k / 2].y : acc[r][k / 2].x) * f[r]);
         }
     }
 }
@@ -169,10 +172,10 @@ struct Block {
 // The block's tile: heads run fastest, tiles of a sequence from its end where the
 // last ones have most to do (`last_first`).  False: nothing left to do.
 template <typename E>
-__device__ __forceinline__ bool take_block(const AttnArgs& a, int heads, bool last_first, E* out, E* out2, float* lse,
-                                           Block& b) {
-    const int slot = static_cast<int>(blockIdx.x / static_cast<unsigned>(heads));
-    b.head = static_cast<int>(blockIdx.x - static_cast<unsigned>(slot) * heads);
+__device__ __forceinline__ bool take_block(const AttnArgs& a, unsigned block, int heads, bool last_first, E* out, E* out2,
+                                           float* lse, Block& b) {
+    const int slot = static_cast<int>(block / static_cast<unsigned>(heads));
+    b.head = static_cast<int>(block - static_cast<unsigned>(slot) * heads);
     if (slot >= a.slots) {
         attn_clear(a, out, lse, heads, b.head, slot - a.slots);
         if (out2) attn_clear(a, out2, nullptr, heads, b.head, slot - a.slots);
@@ -198,19 +201,20 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + T * LD, *V = K + T * LD, *P = V + T * LD;
     Block b;
-    if (!take_block(a, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), a.lse, b)) return;
+    if (!take_block(a, blockIdx.x, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), a.lse, b)) return;
     const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
     load_tile<E, DP>(Q, a.q, b.t.begin + b.row0, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
-    float acc[4][DP / 16], top[4], base[4], sum[4];
+    float2 acc[4][DP / 32];
+    float top[4], base[4], sum[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         top[r] = __int_as_float(0xff800000);
         base[r] = 0.0f;
         sum[r] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) acc[r][k] = 0.0f;
+        for (int k = 0; k < DP / 32; ++k) acc[r][k] = tc::both(0.0f);
     }
     const int end = a.causal ? b.row0 + b.rows : b.t.len;  // keys that any of the rows sees
     for (int j0 = 0; j0 < end; j0 += T) {
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
             }
             sum[r] = fmaf(sum[r], old, row_sum(part));
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k) acc[r][k] *= old;
+            for (int k = 0; k < DP / 32; ++k) acc[r][k] = tc::mul2(acc[r][k], tc::both(old));
         }
         __syncwarp();  // a row of P is written and read by one half warp
         product_nn<DP>(acc, P, V);
@@ -271,14 +275,15 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
     extern __shared__ float sm[];
     float *Q = sm, *O = Q + T * LD, *K = O + T * LD, *V = K + T * LD, *P = V + T * LD;
     Block b;
-    if (!take_block(a, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), nullptr, b)) return;
+    if (!take_block(a, blockIdx.x, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), nullptr, b)) return;
     const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
     const int64_t row = b.t.begin + b.row0;
     load_tile<E, DP>(Q, a.q, row, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
     load_tile<E, DP>(O, a.d_o, row, b.rows, b.head, a.dim, vec_rows<E>(a.d_o, a.dim));
-    float acc[4][DP / 16], lse[4], delta[4];
+    float2 acc[4][DP / 32];
+    float lse[4], delta[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = ty + 16 * r;
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         lse[r] = in ? a.lse[b.head * a.tokens + row + i] * kLog2e : 0.0f;
         delta[r] = in ? a.delta[b.head * a.tokens + row + i] : 0.0f;
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) acc[r][k] = 0.0f;
+        for (int k = 0; k < DP / 32; ++k) acc[r][k] = tc::both(0.0f);
     }
     const int end = a.causal ? b.row0 + b.rows : b.t.len;
     for (int j0 = 0; j0 < end; j0 += T) {
@@ -321,51 +326,92 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
     extern __shared__ float sm[];
     float *K = sm, *V = K + T * LD, *Q = V + T * LD, *O = Q + T * LD, *P = O + T * LD, *G = P + T * LP;
     Block b;
-    if (!take_block(a, a.kv_heads, false, static_cast<E*>(a.dk), static_cast<E*>(a.dv), nullptr, b)) return;
+    const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.parts));
+    const unsigned block = blockIdx.x / static_cast<unsigned>(a.parts);
+    float *pk = nullptr, *pv = nullptr;  // this part's sums, where parts share the tile
+    if (a.parts > 1) {
+        pk = attn_partial(a, 0, part);
+        pv = attn_partial(a, 1, part);
+        if (!take_block(a, block, a.kv_heads, false, pk, pv, nullptr, b)) return;
+    } else if (!take_block(a, block, a.kv_heads, false, static_cast<E*>(a.dk), static_cast<E*>(a.dv), nullptr, b)) {
+        return;
+    }
     const int dim4 = (a.dim + 3) / 4 * 4, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vq = vec_rows<E>(a.q, a.dim), vo = vec_rows<E>(a.d_o, a.dim);
     const int64_t row = b.t.begin + b.row0;
     load_tile<E, DP>(K, a.k, row, b.rows, b.head, a.dim, vec_rows<E>(a.k, a.dim));
     load_tile<E, DP>(V, a.v, row, b.rows, b.head, a.dim, vec_rows<E>(a.v, a.dim));
-    float dk[4][DP / 16], dv[4][DP / 16];
+    float2 dk[4][DP / 32], dv[4][DP / 32];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) dk[r][k] = dv[r][k] = 0.0f;
+        for (int k = 0; k < DP / 32; ++k) dk[r][k] = dv[r][k] = tc::both(0.0f);
     const int first = a.causal ? b.row0 : 0;  // the first query that sees any of the keys
-    for (int head = b.head * a.group; head < (b.head + 1) * a.group; ++head) {
-        for (int i0 = first; i0 < b.t.len; i0 += T) {
-            const int queries = min(T, b.t.len - i0);
-            __syncthreads();
-            load_tile<E, DP>(Q, a.q, b.t.begin + i0, queries, head, a.dim, vq);
-            load_tile<E, DP>(O, a.d_o, b.t.begin + i0, queries, head, a.dim, vo);
-            __syncthreads();
-            float s[4][4], g[4][4];
-            product_nt<DP>(s, K, Q, dim4);
-            product_nt<DP>(g, V, O, dim4);
+    const int per_head = (b.t.len - first + T - 1) / T, steps = per_head * a.group;
+    const int end = attn_part(steps, part + 1, a.parts);
+    for (int step = attn_part(steps, part, a.parts); step < end; ++step) {
+        const int h = step / per_head, head = b.head * a.group + h, i0 = first + (step - h * per_head) * T;
+        const int queries = min(T, b.t.len - i0);
+        __syncthreads();
+        load_tile<E, DP>(Q, a.q, b.t.begin + i0, queries, head, a.dim, vq);
+        load_tile<E, DP>(O, a.d_o, b.t.begin + i0, queries, head, a.dim, vo);
+        __syncthreads();
+        float s[4][4], g[4][4];
+        product_nt<DP>(s, K, Q, dim4);
+        product_nt<DP>(g, V, O, dim4);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int i = tx + 16 * c;
-                const int64_t at = head * a.tokens + b.t.begin + i0 + i;
-                const bool in = i < queries;
-                const float lse = in ? a.lse[at] * kLog2e : 0.0f, delta = in ? a.delta[at] : 0.0f;
+        for (int c = 0; c < 4; ++c) {
+            const int i = tx + 16 * c;
+            const int64_t at = head * a.tokens + b.t.begin + i0 + i;
+            const bool in = i < queries;
+            const float lse = in ? a.lse[at] * kLog2e : 0.0f, delta = in ? a.delta[at] : 0.0f;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = ty + 16 * r;
-                    const bool seen = in && (!a.causal || b.row0 + j <= i0 + i);
-                    const float p = seen ? ex2(fmaf(s[r][c], a.scale_log2, -lse)) : 0.0f;
-                    P[j * LP + i] = p;
-                    G[j * LP + i] = seen ? p * (g[r][c] - delta) : 0.0f;
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int j = ty + 16 * r;
+                const bool seen = in && (!a.causal || b.row0 + j <= i0 + i);
+                const float p = seen ? ex2(fmaf(s[r][c], a.scale_log2, -lse)) : 0.0f;
+                P[j * LP + i] = p;
+                G[j * LP + i] = seen ? p * (g[r][c] - delta) : 0.0f;
             }
-            __syncwarp();
-            product_nn<DP>(dv, P, O);
-            product_nn<DP>(dk, G, Q);
         }
+        __syncwarp();
+        product_nn<DP>(dv, P, O);
+        product_nn<DP>(dk, G, Q);
     }
     const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f}, f[4] = {a.scale, a.scale, a.scale, a.scale};
+    if (a.parts > 1) {
+        store_rows<float, DP>(pv, dv, one, row, b.rows, a.kv_heads, b.head, a.dim);
+        store_rows<float, DP>(pk, dk, one, row, b.rows, a.kv_heads, b.head, a.dim);
+        return;
+    }
     store_rows<E, DP>(a.dv, dv, one, row, b.rows, a.kv_heads, b.head, a.dim);
     store_rows<E, DP>(a.dk, dk, f, row, b.rows, a.kv_heads, b.head, a.dim);
+}
+
+// dk (y = 0) and dv (1) from the partial sums of a.parts blocks, N elements a thread.
+template <typename E, int N>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    struct __align__(4 * N) In { float v[N]; };
+    struct __align__(sizeof(E) * N) Out { E v[N]; };
+    const int64_t n = a.tokens * a.kv_heads * a.dim;
+    const bool v = blockIdx.y != 0;
+    const float* p = attn_partial(a, v ? 1 : 0, 0);
+    E* out = static_cast<E*>(v ? a.dv : a.dk);
+    const float f = v ? 1.0f : a.scale;
+    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * N; i < n; i += gridDim.x * 256ll * N) {
+        float sum[N] = {};
+#pragma unroll 4
+        for (int k = 0; k < a.parts; ++k) {
+            const In x = *reinterpret_cast<const In*>(p + k * n + i);
+#pragma unroll
+            for (int c = 0; c < N; ++c) sum[c] += x.v[c];
+        }
+        Out y;
+#pragma unroll
+        for (int c = 0; c < N; ++c) y.v[c] = from_f<E>(sum[c] * f);
+        *reinterpret_cast<Out*>(out + i) = y;
+    }
 }
 
 // delta = do . o, one warp per row.  Rows of no sequence are never read later.
@@ -495,7 +541,7 @@ cudaError_t backward(AttnArgs a, cudaStream_t s) {
     dq_kernel<E, DP><<<rows * a.heads, kThreads, tiles_bytes(4, 1, DP), s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    dkv_kernel<E, DP><<<rows * a.kv_heads, kThreads, tiles_bytes(4, 2, DP), s>>>(a);
+    dkv_kernel<E, DP><<<rows * a.kv_heads * a.parts, kThreads, tiles_bytes(4, 2, DP), s>>>(a);
     return cudaGetLastError();
 }
 
@@ -513,6 +559,15 @@ cudaError_t attn_simt_backward(const AttnArgs& a, bool f32, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (f32) return a.dim <= 64 ? backward<float, 64>(a, s) : backward<float, 128>(a, s);
     return a.dim <= 64 ? backward<__nv_bfloat16, 64>(a, s) : backward<__nv_bfloat16, 128>(a, s);
+}
+
+cudaError_t attn_join(const AttnArgs& a, bool f32, cudaStream_t s) {
+    const int64_t n = a.tokens * a.kv_heads * a.dim;
+    const int each = a.dim % 4 == 0 ? 4 : 1;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((n / each + 255) / 256, 1216)), 2);
+    if (each == 4)
+        return launch_dependent(f32 ? join_kernel<float, 4> : join_kernel<__nv_bfloat16, 4>, grid, 256, s, a);
+    return launch_dependent(f32 ? join_kernel<float, 1> : join_kernel<__nv_bfloat16, 1>, grid, 256, s, a);
 }
 
 cudaError_t attn_delta(const AttnArgs& a, bool f32, cudaStream_t s) {

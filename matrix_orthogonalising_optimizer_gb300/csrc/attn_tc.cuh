@@ -126,5 +126,30 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t t, float f, 
     }
 }
 
+// The same in fp32, unscaled, 32 columns at a time.
+template <int kBoxes>
+__device__ __forceinline__ void store_rows_f32(uint8_t* stage, uint32_t t, float* out, int64_t ld, int rows, int dim,
+                                               int lane) {
+    const int chunk = lane % 8;
+    float4* mine = reinterpret_cast<float4*>(stage + lane * 128);
+#pragma unroll 1
+    for (int b = 0; b < 2 * kBoxes; ++b) {
+        float v[32];
+        tmem_ld32(t + 32 * b, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            mine[k ^ chunk] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        __syncwarp();
+        const int c = 32 * b + 4 * chunk;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + lane / 8;
+            const float4 w = reinterpret_cast<const float4*>(stage + r * 128)[chunk ^ (r % 8)];
+            if (r < rows && c < dim) *reinterpret_cast<float4*>(out + r * ld + c) = w;
+        }
+        __syncwarp();
+    }
+}
+
 }  // namespace attn
 }  // namespace dmuon

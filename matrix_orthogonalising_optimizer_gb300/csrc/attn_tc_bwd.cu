@@ -121,6 +121,24 @@ __device__ __forceinline__ void store_cols64(uint32_t t, const float (&v)[64]) {
 
 // ---------------------------------------------------------------- side of the keys
 
+// The steps [begin, end) that a part of a key tile takes: query tiles of all its heads,
+// from the first that sees any of the keys on.
+__device__ __forceinline__ int part_begin(const AttnArgs& a, const AttnTile& t, int part) {
+    const int queries = a.causal ? t.len - t.tile * kRows : t.len;
+    return attn_part((queries + kRows - 1) / kRows * a.group, part, a.parts);
+}
+
+// A part without steps: its sums are zero.
+__device__ __forceinline__ void clear_part(const AttnArgs& a, const AttnTile& t, int kv, int part) {
+    const int rows = min(kRows, t.len - t.tile * kRows);
+    const int64_t first = ((t.begin + t.tile * kRows) * a.kv_heads + kv) * a.dim;
+    for (int i = threadIdx.x; i < rows * a.dim; i += kThreads) {
+        const int64_t at = first + static_cast<int64_t>(i / a.dim) * a.kv_heads * a.dim + i % a.dim;
+        attn_partial(a, 0, part)[at] = 0.0f;
+        attn_partial(a, 1, part)[at] = 0.0f;
+    }
+}
+
 // TMEM columns.  Heads of up to 64 leave room for p and ds beside s and dp, which then
 // make way for the next tile as soon as they are in registers.
 template <int DP>
@@ -135,16 +153,17 @@ struct KeysCols {
 template <int DP, bool kElt>
 __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq, const CUtensorMap* mk,
                                           const CUtensorMap* mv, const CUtensorMap* mo, const AttnTile& t, int kv,
-                                          int warp, int lane, uint32_t tmem) {
+                                          int part, int warp, int lane, uint32_t tmem) {
     using C = KeysCols<DP>;
     constexpr int NS = kStages<DP>;
     const int token0 = static_cast<int>(t.begin), row0 = t.tile * kRows;
     const int first = a.causal ? row0 : 0;                             // the first query that sees any of the keys
-    const int per_head = (t.len - first + kRows - 1) / kRows, steps = per_head * a.group;
+    const int per_head = (t.len - first + kRows - 1) / kRows;
+    const int begin = part_begin(a, t, part), steps = part_begin(a, t, part + 1) - begin;
     const auto where = [&](int i, int& head, int& row) {
-        const int h = i / per_head;
+        const int h = (begin + i) / per_head;
         head = kv * a.group + h;
-        row = first + (i - h * per_head) * kRows;
+        row = first + (begin + i - h * per_head) * kRows;
     };
     if (!kElt && warp == 0) {
         const uint32_t e = elect_one();
@@ -314,7 +333,12 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
             // one warpgroup stores dv, the other dk
             const int quarter = warp % 4;
             const int64_t out = t.begin + row0 + 32 * quarter;
-            store_rows<DP / 64>(S.own[half] + quarter * 4096, (half ? C::kDk : C::kDv) + lanes, half ? a.scale : 1.0f,
+            if (a.parts > 1)
+                store_rows_f32<DP / 64>(S.own[half] + quarter * 4096, (half ? C::kDk : C::kDv) + lanes,
+                                        attn_partial(a, 1 - half, part) + (out * a.kv_heads + kv) * a.dim,
+                                        static_cast<int64_t>(a.kv_heads) * a.dim, t.len - row0 - 32 * quarter, a.dim,
+                                        lane);
+            else store_rows<DP / 64>(S.own[half] + quarter * 4096, (half ? C::kDk : C::kDv) + lanes, half ? a.scale : 1.0f,
                                 static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (out * a.kv_heads + kv) * a.dim,
                                 static_cast<int64_t>(a.kv_heads) * a.dim, t.len - row0 - 32 * quarter, a.dim, lane);
         }
@@ -465,13 +489,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     Smem<DP>& S = *reinterpret_cast<Smem<DP>*>(raw);
     const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     // blocks of the keys, then blocks of the queries
-    const unsigned first = static_cast<unsigned>(a.slots + a.fill) * a.kv_heads;
+    const unsigned first = static_cast<unsigned>(a.slots + a.fill) * a.kv_heads * a.parts;
     const bool keys = blockIdx.x < first;
-    const unsigned block = keys ? blockIdx.x : blockIdx.x - first, heads = keys ? a.kv_heads : a.heads;
+    const int part = keys ? static_cast<int>(blockIdx.x % static_cast<unsigned>(a.parts)) : 0;
+    const unsigned block = keys ? blockIdx.x / static_cast<unsigned>(a.parts) : blockIdx.x - first;
+    const unsigned heads = keys ? a.kv_heads : a.heads;
     const int slot = static_cast<int>(block / heads), head = static_cast<int>(block - slot * heads);
     if (slot >= a.slots) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const int f = slot - a.slots;
+        if (keys && a.parts > 1) {
+            attn_clear(a, attn_partial(a, 0, part), nullptr, a.kv_heads, head, f);
+            attn_clear(a, attn_partial(a, 1, part), nullptr, a.kv_heads, head, f);
+            return;
+        }
         if (keys) attn_clear(a, static_cast<__nv_bfloat16*>(a.dk), nullptr, a.kv_heads, head, f);
         attn_clear(a, static_cast<__nv_bfloat16*>(keys ? a.dv : a.out), nullptr, static_cast<int>(heads), head, f);
         return;
@@ -521,17 +552,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.begin = __shfl_sync(kFullMask, static_cast<int32_t>(S.tile.begin), 0);
     t.len = __shfl_sync(kFullMask, S.tile.len, 0);
     t.tile = __shfl_sync(kFullMask, S.tile.tile, 0);
-    if (!any) {
+    const bool empty = any && keys && a.parts > 1 && part_begin(a, t, part) == part_begin(a, t, part + 1);
+    if (empty) clear_part(a, t, head, part);
+    if (!any || empty) {
         if (warp == 1) tmem_free<kCols>(tmem);
         return;
     }
     if (warp < kEltWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
-        if (keys) keys_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
+        if (keys) keys_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
         else queries_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsElt));
-        if (keys) keys_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
+        if (keys) keys_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
         else queries_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
     }
     fence_before();
@@ -569,7 +602,7 @@ cudaError_t launch(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.slots + a.fill) * (a.heads + a.kv_heads));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.slots + a.fill) * (a.heads + a.kv_heads * a.parts));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Smem<DP>);
     cfg.stream = s;

@@ -17,7 +17,6 @@
 //
 // Bound: the tensor cores, 4 * 128 * 128 * dim operations per pair of tiles -- at dim =
 // 128 1024 cycles, against 512 of exponentials and about 400 of instruction issue.
-#include <cstdlib>
 #include "attn_tc.cuh"
 #include "internal.h"
 #include "ops.h"
@@ -397,8 +396,16 @@ cudaError_t attn_fwd_status_word(void** p) { return cudaGetSymbolAddress(p, attn
 cudaError_t attn_tc_forward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s) {
     const cudaError_t e = attn::prepare();
     if (e != cudaSuccess) return e;
-    if (getenv("NT1")) return a.dim <= 64 ? attn::launch<64, 1>(a, m, s) : attn::launch<128, 1>(a, m, s);
-    return a.dim <= 64 ? attn::launch<64, 2>(a, m, s) : attn::launch<128, 2>(a, m, s);
+    // One query tile per CTA, two CTAs per SM, where sequences are short: one CTA's start and
+    // end fall under the other's work.  Long ones: two tiles that share the keys.  Measured,
+    // two tiles -> one (8192 tokens of equal sequences, 32/8 heads of 128 | 12 of 64):
+    //   100 tokens each 123 -> 84 us | 43 -> 33;  512: 90 -> 80;  1024: | 43 -> 43;
+    //   1640: 130 -> 125;  2048: 143 -> 143;  8192: 334 -> 342 | 107 -> 119
+    // And where two tiles would leave SMs without a CTA (2048 tokens, 8 heads of 128: 31 -> 29).
+    const int64_t length = a.tokens / a.sequences;
+    const bool one = length <= (a.dim <= 64 ? 512 : 1536) || (a.tokens + 255) / 256 * a.heads < 152;
+    if (a.dim <= 64) return one ? attn::launch<64, 1>(a, m, s) : attn::launch<64, 2>(a, m, s);
+    return one ? attn::launch<128, 1>(a, m, s) : attn::launch<128, 2>(a, m, s);
 }
 
 }  // namespace dmuon
