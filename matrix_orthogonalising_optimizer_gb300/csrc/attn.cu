@@ -209,7 +209,7 @@ extern "C" int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_he
     const bool tc = tensor_cores(a, dtype, true);
     a.parts = parts_of(sequences, tokens, heads, kv_heads, a.causal != 0, tc);
     a.partial = L.partial;
-    OPS_CUDA(attn_delta(a, f32, s));
+    if (tc || f32) OPS_CUDA(attn_delta(a, f32, s));  // bf16 rows of the FFMA kernels: made there
     if (tc) {
         AttnMaps m = {};
         OPS_TRY(set_maps(m, a));

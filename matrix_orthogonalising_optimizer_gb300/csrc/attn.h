@@ -30,6 +30,7 @@ struct AttnArgs {
     int32_t causal;
     int32_t slots;             // row tiles of a head (an upper bound: see attn_slots)
     int32_t fill;              // blocks behind them that clear the rows of no sequence
+    int32_t whole;             // backward, tensor cores: sequences that may fit one tile
     int32_t parts;             // backward: blocks that share the queries of a key tile
     float* partial;            // parts > 1: [2][parts][tokens][kv_heads][dim] sums of dk (unscaled) and dv
     float scale, scale_log2;   // scale_log2 = scale * log2(e)

@@ -289,19 +289,19 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         const int i = ty + 16 * r;
         const bool in = i < b.rows;
         lse[r] = in ? a.lse[b.head * a.tokens + row + i] * kLog2e : 0.0f;
-        delta[r] = in ? a.delta[b.head * a.tokens + row + i] : 0.0f;
+        delta[r] = in && sizeof(E) == 4 ? a.delta[b.head * a.tokens + row + i] : 0.0f;
 #pragma unroll
         for (int k = 0; k < DP / 32; ++k) acc[r][k] = tc::both(0.0f);
     }
     const int end = a.causal ? b.row0 + b.rows : b.t.len;
-    for (int j0 = 0; j0 < end; j0 += T) {
+    // p and dp of the keys from j0 on, 0 where a row sees none
+    const auto form = [&](int j0, float (&p)[4][4], float (&g)[4][4]) {
         const int keys = min(T, b.t.len - j0);
         __syncthreads();
         load_tile<E, DP>(K, a.k, b.t.begin + j0, keys, kv, a.dim, vk);
         load_tile<E, DP>(V, a.v, b.t.begin + j0, keys, kv, a.dim, vv);
         __syncthreads();
-        float s[4][4], g[4][4];
-        product_nt<DP>(s, Q, K, dim4);
+        product_nt<DP>(p, Q, K, dim4);
         product_nt<DP>(g, O, V, dim4);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -309,10 +309,39 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
             const int seen = a.causal ? min(i + 1 - j0, keys) : keys;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float p = ex2(fmaf(s[r][c], a.scale_log2, -lse[r]));
-                P[(ty + 16 * r) * LP + tx + 16 * c] = tx + 16 * c < seen ? p * (g[r][c] - delta[r]) : 0.0f;
+                const bool in = tx + 16 * c < seen;
+                p[r][c] = in ? ex2(fmaf(p[r][c], a.scale_log2, -lse[r])) : 0.0f;
+                g[r][c] = in ? g[r][c] : 0.0f;
             }
         }
+    };
+    if constexpr (sizeof(E) == 2) {
+        // delta = sum p dp, in a pass of its own: do . o would hold the rounding of o to
+        // bf16, which shows where few keys count (dp - delta is then small beside dp)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) delta[r] = 0.0f;
+        for (int j0 = 0; j0 < end; j0 += T) {
+            float p[4][4], g[4][4];
+            form(j0, p, g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) delta[r] = fmaf(p[r][c], g[r][c], delta[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            delta[r] = row_sum(delta[r]);
+            const int i = ty + 16 * r;
+            if (tx == 0 && i < b.rows) a.delta[b.head * a.tokens + row + i] = delta[r];
+        }
+    }
+    for (int j0 = 0; j0 < end; j0 += T) {
+        float p[4][4], g[4][4];
+        form(j0, p, g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) P[(ty + 16 * r) * LP + tx + 16 * c] = p[r][c] * (g[r][c] - delta[r]);
         __syncwarp();
         product_nn<DP>(acc, P, K);
     }

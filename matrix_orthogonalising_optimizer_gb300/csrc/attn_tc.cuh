@@ -22,9 +22,9 @@ constexpr int kBox = kRows * 128;  // bytes of a box
 template <int DP>
 constexpr int kTile = DP / 64 * kBox;  // bytes of a tile
 
-// M = 128; b_mn: B's contraction runs over its rows.
-__device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+// M = 128; a_mn, b_mn: A's, B's contraction runs over its rows.
+__device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_mn, bool a_mn = false) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(kRows >> 4) << 24);
 }
 
@@ -57,6 +57,16 @@ __device__ __forceinline__ void product_rows(uint32_t e, uint32_t d, uint32_t p,
     for (int k = 0; k < n; ++k)
         umma_bf16_ts(e, d, p + static_cast<uint32_t>(8 * k), b + static_cast<uint64_t>(((k0 + k) * 2048) >> 4),
                      idesc_of(DP, true), add || k != 0 ? 1u : 0u);
+}
+
+// D (128 x DP) (+)= A B over B's 128 rows, A in shared memory: a 128 x 128 tile in two
+// boxes, its columns against B's rows, or (kRowsOfA) its rows: D = A^T B.
+template <int DP, bool kRowsOfA>
+__device__ __forceinline__ void product_tile(uint32_t e, uint32_t d, uint64_t a, uint64_t b, bool add) {
+#pragma unroll
+    for (int k = 0; k < kRows / 16; ++k)
+        umma_bf16(e, d, a + static_cast<uint64_t>((kRowsOfA ? k * 2048 : k / 4 * kBox + k % 4 * 32) >> 4),
+                  b + static_cast<uint64_t>((k * 2048) >> 4), idesc_of(DP, true, kRowsOfA), add || k != 0 ? 1u : 0u);
 }
 
 // Loads the tile that begins at a token.

@@ -14,9 +14,15 @@
 // Keys: TMEM holds s^T and dp^T (p^T and ds^T take their place, bf16), dv and dk.  The
 // tensor cores run dv_i, s_{i+1}, dk_i, dp_{i+1}: the exponentials of tile i + 1 fall
 // under dk_i and dp_{i+1}, and ds_i under dv_i and s_{i+1}.  The query heads that share
-// the key head follow one another.
-// Queries: two buffers of s (ds takes their place), dp and dq; the tensor cores run
-// s_{i+1} while ds_i is made, then dp_{i+1} and dq_i.
+// the key head follow one another.  (Heads of up to 64: as the queries.)
+// Queries: s, dp, ds, Q and dq; s and dp are taken into registers first, so that
+// s_{i+1} and dp_{i+1} run while ds_i is made, then dq_i.
+// Sequences of one tile: a CTA makes all three gradients (short_side).
+//
+// Bound: the tensor cores.  Per pair of 128-token tiles 7 * 512 cycles at dim = 128;
+// measured 2430 a step of the keys (2048 of MMAs) and about 2000 of the queries
+// (1536); 8192 tokens, 32/8 heads of 128, causal: 1.09 ms with delta, 1.26 PFLOP/s of the five products,
+// 1.77 of the seven.
 //
 // Warp 0 loads, warp 1 issues the MMAs, warp 2 fetches lse and delta of the query tiles
 // (side of the keys), warps 4 to 11 do the element-wise work, half of the columns
@@ -125,7 +131,7 @@ __device__ __forceinline__ void store_cols64(uint32_t t, const float (&v)[64]) {
 // from the first that sees any of the keys on.
 __device__ __forceinline__ int part_begin(const AttnArgs& a, const AttnTile& t, int part) {
     const int queries = a.causal ? t.len - t.tile * kRows : t.len;
-    return attn_part((queries + kRows - 1) / kRows * a.group, part, a.parts);
+    return attn_part((queries + kRows - 1) / kRows * a.group, part, a.parts);  // one tile: heads
 }
 
 // A part without steps: its sums are zero.
@@ -149,6 +155,21 @@ struct KeysCols {
     static constexpr uint32_t kDv = kApart ? 384 : 256, kDk = kDv + DP;
     static constexpr uint32_t kHalf = kApart ? 32 : 64;  // between the halves of p and ds
 };
+
+// The sums of a key tile: one warpgroup stores dv, the other dk, or their partial sums.
+template <int DP>
+__device__ __forceinline__ void store_keys(const AttnArgs& a, Smem<DP>& S, const AttnTile& t, int kv, int part, int half,
+                                           int quarter, uint32_t dk, uint32_t dv, uint32_t lanes, int lane) {
+    const int row = t.tile * kRows + 32 * quarter;
+    const int64_t at = ((t.begin + row) * a.kv_heads + kv) * a.dim, ld = static_cast<int64_t>(a.kv_heads) * a.dim;
+    uint8_t* stage = S.own[half] + quarter * 4096;
+    const uint32_t from = (half ? dk : dv) + lanes;
+    if (a.parts > 1)
+        store_rows_f32<DP / 64>(stage, from, attn_partial(a, 1 - half, part) + at, ld, t.len - row, a.dim, lane);
+    else
+        store_rows<DP / 64>(stage, from, half ? a.scale : 1.0f, static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + at, ld,
+                            t.len - row, a.dim, lane);
+}
 
 template <int DP, bool kElt>
 __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq, const CUtensorMap* mk,
@@ -329,19 +350,8 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
             arrive_warp(&S.ds_ready, lane);
             if (lane == 0) mbar_arrive(&S.stat_empty[st]);
         }
-        if (ok && wait_warp(&S.done, 0)) {
-            // one warpgroup stores dv, the other dk
-            const int quarter = warp % 4;
-            const int64_t out = t.begin + row0 + 32 * quarter;
-            if (a.parts > 1)
-                store_rows_f32<DP / 64>(S.own[half] + quarter * 4096, (half ? C::kDk : C::kDv) + lanes,
-                                        attn_partial(a, 1 - half, part) + (out * a.kv_heads + kv) * a.dim,
-                                        static_cast<int64_t>(a.kv_heads) * a.dim, t.len - row0 - 32 * quarter, a.dim,
-                                        lane);
-            else store_rows<DP / 64>(S.own[half] + quarter * 4096, (half ? C::kDk : C::kDv) + lanes, half ? a.scale : 1.0f,
-                                static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (out * a.kv_heads + kv) * a.dim,
-                                static_cast<int64_t>(a.kv_heads) * a.dim, t.len - row0 - 32 * quarter, a.dim, lane);
-        }
+        if (ok && wait_warp(&S.done, 0))
+            store_keys<DP>(a, S, t, kv, part, half, warp % 4, C::kDk, C::kDv, lanes, lane);
     }
 }
 
@@ -480,6 +490,143 @@ __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, con
     }
 }
 
+// ---------------------------------------------------------------- sequences of one tile
+
+// A sequence of up to 128 tokens: one CTA per key head (or per part of its query heads)
+// makes all three gradients, with s and dp formed once.  p and ds go through shared
+// memory, where the products read them either way round: dq = ds k, dk = ds^T q, dv = p^T do.
+// delta is the sum of p dp over the row at hand, not do . o: with few keys dp - delta
+// is small beside dp, and the rounding of o to bf16 shows in it (2 to 16 keys: error of dq
+// and dk 4e-3 to 5e-3 of their norm, with this 2.4e-3, which is that of ds and of the
+// gradients themselves).
+// TMEM: s, then dq; dp; dv; dk.  Shared memory: own = K, V; of the ring the last 64 KB hold p
+// and ds, the others are slots for Q and dO of one head after the other.
+template <int DP>
+constexpr int kShortSlots = DP == 128 ? 3 : 4;
+
+template <int DP, bool kElt>
+__device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq, const CUtensorMap* mk,
+                                           const CUtensorMap* mv, const CUtensorMap* mo, const AttnTile& t, int kv,
+                                           int part, int warp, int lane, uint32_t tmem) {
+    constexpr int NS = kShortSlots<DP>;
+    constexpr uint32_t kS = 0, kG = 128, kDv = 256, kDk = 256 + DP;
+    const int token0 = static_cast<int>(t.begin);
+    const int begin = attn_part(a.group, part, a.parts), steps = attn_part(a.group, part + 1, a.parts) - begin;
+    const int head0 = kv * a.group + begin;
+    uint8_t* p_tile = S.ring[kStages<DP> - 65536 / kTile<DP>];
+    uint8_t* ds_tile = p_tile + 32768;
+    if (!kElt && warp == 0) {
+        const uint32_t e = elect_one();
+        mbar_expect_tx_if(e, &S.own_full, 2 * kTile<DP>);
+        load_tile<DP>(e, saddr(S.own[0]), mk, saddr(&S.own_full), kv, token0);
+        load_tile<DP>(e, saddr(S.own[1]), mv, saddr(&S.own_full), kv, token0);
+        produce<DP, NS>(S, e, S.ring[0], 2 * steps, [&](int i, const CUtensorMap*& map, int& head, int& token) {
+            map = i & 1 ? mo : mq;
+            head = head0 + i / 2;
+            token = token0;
+        });
+    } else if (!kElt && warp == 1) {
+        const uint32_t e = elect_one();
+        const uint32_t own = saddr(S.own[0]), ring = saddr(S.ring[0]);
+        const uint32_t p = saddr(p_tile), ds = saddr(ds_tile);
+        bool ok = wait_warp(&S.own_full, 0);
+        for (int i = 0; i < steps && ok; ++i) {
+            const int nq = 2 * i, no = 2 * i + 1, sq = nq % NS, so = no % NS;
+            // dq of the head before has been read
+            ok = (i == 0 || wait_warp(&S.taken, (i - 1) & 1)) && wait_warp(&S.full[sq], (nq / NS) & 1);
+            if (!ok) break;
+            product_cols<DP>(e, tmem + kS, desc_k(ring + sq * kTile<DP>), desc_k(own));
+            ok = wait_warp(&S.full[so], (no / NS) & 1);
+            if (!ok) break;
+            product_cols<DP>(e, tmem + kG, desc_k(ring + so * kTile<DP>), desc_k(own + kTile<DP>));
+            umma_commit(e, saddr(&S.s_full));
+            ok = wait_warp(&S.ds_ready, i & 1);
+            if (!ok) break;
+            product_tile<DP, true>(e, tmem + kDv, desc_mn(p), desc_mn(ring + so * kTile<DP>), i > 0);
+            umma_commit(e, saddr(&S.empty[so]));
+            product_tile<DP, true>(e, tmem + kDk, desc_mn(ds), desc_mn(ring + sq * kTile<DP>), i > 0);
+            umma_commit(e, saddr(&S.empty[sq]));
+            product_tile<DP, false>(e, tmem + kS, desc_k(ds), desc_mn(own), false);
+            umma_commit(e, saddr(&S.used));
+        }
+        umma_commit(e, saddr(&S.done));
+        mbar_wait<false>(&S.done, 0, &g_status);
+    } else if (kElt) {
+        const int half = (warp - kEltWarp0) / 4, thread = threadIdx.x - 32 * kEltWarp0, r = thread % kRows;
+        const int quarter = warp % 4;
+        const uint32_t lanes = (static_cast<uint32_t>(quarter * 32) << 16) + tmem;
+        const bool in = r < t.len;
+        const int seen = (!in ? 0 : a.causal ? r + 1 : t.len) - 64 * half;  // columns of this half that row r sees
+        const float2 c2 = both(a.scale_log2);
+        bool ok = wait_warp(&S.own_full, 0);
+        if (ok && t.len < kRows) clear_rows<DP>(S.own[0], t.len, thread, 256);  // K: the rows of ds k
+        for (int i = 0; i < steps && ok; ++i) {
+            const int head = head0 + i;
+            const float2 nl = both(in ? a.lse[head * a.tokens + t.begin + r] * -kLog2e : 0.0f);
+            ok = wait_warp(&S.s_full, i & 1);
+            if (!ok) break;
+            float p[64], g[64];
+            tmem_ld64(lanes + kS + 64 * half, p);
+            tmem_ld64(lanes + kG + 64 * half, g);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+                const float2 x = fma2(make_float2(p[k], p[k + 1]), c2, nl);
+                p[k] = ex2(x.x);
+                p[k + 1] = ex2(x.y);
+            }
+            if (t.len < kRows || a.causal) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                    if (k >= seen) p[k] = g[k] = 0.0f;
+            }
+            float2 sum2 = both(0.0f);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2)
+                sum2 = fma2(make_float2(p[k], p[k + 1]), make_float2(g[k], g[k + 1]), sum2);
+            S.stat[i & 1][half][r] = sum2.x + sum2.y;
+            release_warp(&S.p_ready, lane);  // both halves of every row's sum
+            ok = wait_warp(&S.p_ready, i & 1);
+            if (!ok) break;
+            const float2 nd = both(-(S.stat[i & 1][0][r] + S.stat[i & 1][1][r]));
+            // this row's 128 bytes of the half's box, in 16-byte pieces
+            uint4* const prow = reinterpret_cast<uint4*>(p_tile + half * kBox + r * 128);
+            uint4* const drow = reinterpret_cast<uint4*>(ds_tile + half * kBox + r * 128);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                uint32_t w[4], d[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int n = 8 * c + 2 * k;
+                    const float2 x = make_float2(p[n], p[n + 1]);
+                    const float2 y = mul2(x, add2(make_float2(g[n], g[n + 1]), nd));
+                    w[k] = pack_bf16x2(x.x, x.y);
+                    d[k] = pack_bf16x2(y.x, y.y);
+                }
+                prow[c ^ (r % 8)] = make_uint4(w[0], w[1], w[2], w[3]);
+                drow[c ^ (r % 8)] = make_uint4(d[0], d[1], d[2], d[3]);
+            }
+            if (t.len < kRows) {
+                // rows behind the sequence, which meet zeros of p and ds
+                clear_rows<DP>(S.ring[2 * i % NS], t.len, thread, 256);
+                clear_rows<DP>(S.ring[(2 * i + 1) % NS], t.len, thread, 256);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            release_warp(&S.ds_ready, lane);
+            ok = wait_warp(&S.used, i & 1);
+            if (!ok) break;
+            // p's rows of this warp are free again: dq passes through them
+            if (64 * half < DP) {
+                const int64_t out = t.begin + 32 * quarter;
+                store_rows<1>(p_tile + half * kBox + quarter * 4096, lanes + kS + 64 * half, a.scale,
+                              static_cast<__nv_bfloat16*>(a.out) + (out * a.heads + head) * a.dim + 64 * half,
+                              static_cast<int64_t>(a.heads) * a.dim, t.len - 32 * quarter, a.dim - 64 * half, lane);
+            }
+            release_warp(&S.taken, lane);
+        }
+        if (ok && wait_warp(&S.done, 0)) store_keys<DP>(a, S, t, kv, part, half, quarter, kDk, kDv, lanes, lane);
+    }
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     backward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
@@ -488,14 +635,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem<DP>& S = *reinterpret_cast<Smem<DP>*>(raw);
     const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    // blocks of the keys, then blocks of the queries
+    // blocks of the keys, of the sequences of one tile, of the queries
     const unsigned first = static_cast<unsigned>(a.slots + a.fill) * a.kv_heads * a.parts;
-    const bool keys = blockIdx.x < first;
-    const int part = keys ? static_cast<int>(blockIdx.x % static_cast<unsigned>(a.parts)) : 0;
-    const unsigned block = keys ? blockIdx.x / static_cast<unsigned>(a.parts) : blockIdx.x - first;
-    const unsigned heads = keys ? a.kv_heads : a.heads;
+    const unsigned second = first + static_cast<unsigned>(a.whole) * a.kv_heads * a.parts;
+    const bool keys = blockIdx.x < first, whole = !keys && blockIdx.x < second;
+    const bool parts = keys || whole;
+    unsigned block = blockIdx.x - (keys ? 0 : whole ? first : second);
+    const int part = parts ? static_cast<int>(block % static_cast<unsigned>(a.parts)) : 0;
+    if (parts) block /= static_cast<unsigned>(a.parts);
+    const unsigned heads = parts ? a.kv_heads : a.heads;
     const int slot = static_cast<int>(block / heads), head = static_cast<int>(block - slot * heads);
-    if (slot >= a.slots) {
+    if (!whole && slot >= a.slots) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const int f = slot - a.slots;
         if (keys && a.parts > 1) {
@@ -536,7 +686,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // meanwhile, and only after the kernels before have finished
         asm volatile("griddepcontrol.wait;" ::: "memory");
         AttnTile found;
-        const bool any = attn_find(a, slot, kRows, found);
+        bool any;
+        if (whole) {
+            found.begin = attn_offset(a, slot);
+            found.len = static_cast<int32_t>(attn_offset(a, slot + 1) - found.begin);
+            found.tile = 0;
+            any = found.len > 0 && found.len <= kRows;
+        } else {
+            any = attn_find(a, slot, kRows, found) && found.len > kRows;
+        }
         if (lane == 0) {
             S.tile = found;
             S.any = any;
@@ -552,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.begin = __shfl_sync(kFullMask, static_cast<int32_t>(S.tile.begin), 0);
     t.len = __shfl_sync(kFullMask, S.tile.len, 0);
     t.tile = __shfl_sync(kFullMask, S.tile.tile, 0);
-    const bool empty = any && keys && a.parts > 1 && part_begin(a, t, part) == part_begin(a, t, part + 1);
+    const bool empty = any && parts && a.parts > 1 && part_begin(a, t, part) == part_begin(a, t, part + 1);
     if (empty) clear_part(a, t, head, part);
     if (!any || empty) {
         if (warp == 1) tmem_free<kCols>(tmem);
@@ -561,10 +719,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kEltWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (keys) keys_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
+        else if (whole) short_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
         else queries_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsElt));
         if (keys) keys_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
+        else if (whole) short_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
         else queries_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
     }
     fence_before();
@@ -598,11 +758,14 @@ cudaError_t prepare() {
 template <int DP>
 cudaError_t launch(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
     a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, kRows));
+    a.whole = a.sequences;
+    if (!a.offsets) (a.length <= kRows ? a.slots : a.whole) = 0;  // all of one kind
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.slots + a.fill) * (a.heads + a.kv_heads * a.parts));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.slots + a.fill) * (a.heads + a.kv_heads * a.parts) +
+                       static_cast<unsigned>(a.whole) * a.kv_heads * a.parts);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Smem<DP>);
     cfg.stream = s;
