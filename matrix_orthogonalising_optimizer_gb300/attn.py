@@ -19,22 +19,24 @@ __all__ = ["rotary_table", "qk_norm_rotary", "qk_norm_rotary_backward", "qk_norm
            "attention_backward", "attention_workspace"]
 
 
-def _heads(where, name, t, dtype, lead, heads, dim, dev):
-    """The C ABI's view of (*lead, heads, dim); refuses what it cannot describe."""
-    shape = (*lead, heads, dim)
-    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.device == dev):
+def _heads(where, name, t, dtype, shape, dev):
+    """The C ABI's view of a tensor of this shape (*lead, heads, dim); refuses what it cannot describe."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == dev):
         _refuse(where, name, t, dtype, shape, dev)
-    strides, step, span = t.stride(), None, None
-    if t.numel() and dim > 1 and strides[-1] != 1:
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1 and t.numel():
         raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
-    for n, s in zip(reversed(lead), reversed(strides[:-2])):
+    if len(shape) == 3:
+        return _lib.Heads(t.data_ptr(), strides[0], strides[1])
+    step, span = None, None
+    for n, s in zip(reversed(shape[:-2]), reversed(strides[:-2])):
         if n == 1:
             continue
         if step is not None and s != span and t.numel():
             raise ValueError(f"{where}: the leading dimensions of {name} must have one stride")
         step = s if step is None else step
         span = s * n
-    return _lib.Heads(t.data_ptr(), dim if step is None else step, strides[-2])
+    return _lib.Heads(t.data_ptr(), shape[-1] if step is None else step, strides[-2])
 
 
 def _rows(lead):
@@ -44,11 +46,19 @@ def _rows(lead):
     return n
 
 
-def _sizes(where, q, k):
-    """(dtype, device, leading dimensions, heads, key heads, dim) of a call."""
-    if q.dim() < 2 or k.dim() < 2:
+def _shapes(where, q, k):
+    """The shapes of q and, with q's leading dimensions and width, of k."""
+    qs = q.shape
+    if len(qs) < 2 or k.dim() < 2:
         raise ValueError(f"{where}: q and k must have a head and an element dimension")
-    return q.dtype, q.device, q.shape[:-2], q.shape[-2], k.shape[-2], q.shape[-1]
+    if len(qs) == 3:
+        return qs, (qs[0], k.shape[-2], qs[2])
+    return qs, (*qs[:-2], k.shape[-2], qs[-1])
+
+
+def _like(t):
+    """A contiguous tensor of t's shape."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 # ---------------------------------------------------------------- rotation
@@ -91,21 +101,21 @@ def qk_norm_rotary(q, k, positions=None, table=None, q_weight=None, k_weight=Non
     ``norm=False``) and turned by its token's position: ``positions`` are rows of ``table``
     (``rotary_table``), whose width is the number of leading elements that are turned (no table:
     none)."""
-    dt, dev, lead, heads, kv, dim = _sizes("qk_norm_rotary", q, k)
-    hq = _heads("qk_norm_rotary", "q", q, dt, lead, heads, dim, dev)
-    hk = _heads("qk_norm_rotary", "k", k, dt, lead, kv, dim, dev)
-    rows, rotary = _rotary_check("qk_norm_rotary", lead, dev, dt, dim, positions, table, q_weight, k_weight)
+    dt, dev = q.dtype, q.device
+    qs, ks = _shapes("qk_norm_rotary", q, k)
+    hq = _heads("qk_norm_rotary", "q", q, dt, qs, dev)
+    hk = _heads("qk_norm_rotary", "k", k, dt, ks, dev)
+    rows, rotary = _rotary_check("qk_norm_rotary", qs[:-2], dev, dt, qs[-1], positions, table, q_weight, k_weight)
     _no_graph("qk_norm_rotary", q, k, q_weight, k_weight)
 
     if _elsewhere(stream, dev):
         return _run_elsewhere(stream, (q, k, positions, table, q_weight, k_weight),
                               lambda: qk_norm_rotary(q, k, positions, table, q_weight, k_weight, norm, eps, interleaved))
     s = _raw_stream(dev.index)
-    qo = torch.empty(q.shape, dtype=dt, device=dev)
-    ko = torch.empty(k.shape, dtype=dt, device=dev)
+    qo, ko = _like(q), _like(k)
     st = _lib.load().dmuon_qk_norm_rotary_forward(hq, hk, _ptr(positions), _ptr(table), rows, rotary, int(interleaved),
                                                   _ptr(q_weight), _ptr(k_weight), int(norm), eps, qo.data_ptr(),
-                                                  ko.data_ptr(), _rows(lead), heads, kv, dim, _dtype(dt), s)
+                                                  ko.data_ptr(), _rows(qs[:-2]), qs[-2], ks[-2], qs[-1], _dtype(dt), s)
     _lib.check(st, "dmuon_qk_norm_rotary_forward")
     return qo, ko
 
@@ -120,21 +130,21 @@ def qk_norm_rotary_backward(dq, dk, q, k, positions=None, table=None, q_weight=N
     """``(dq, dk, dq_weight, dk_weight)`` from the gradients of ``qk_norm_rotary``'s outputs and its inputs;
     the gradient of a weight that was not given is None."""
     where = "qk_norm_rotary_backward"
-    dt, dev, lead, heads, kv, dim = _sizes(where, q, k)
-    hq = _heads(where, "q", q, dt, lead, heads, dim, dev)
-    hk = _heads(where, "k", k, dt, lead, kv, dim, dev)
-    gq = _heads(where, "dq", dq, dt, lead, heads, dim, dev)
-    gk = _heads(where, "dk", dk, dt, lead, kv, dim, dev)
-    rows, rotary = _rotary_check(where, lead, dev, dt, dim, positions, table, q_weight, k_weight)
+    dt, dev = q.dtype, q.device
+    qs, ks = _shapes(where, q, k)
+    hq = _heads(where, "q", q, dt, qs, dev)
+    hk = _heads(where, "k", k, dt, ks, dev)
+    gq = _heads(where, "dq", dq, dt, qs, dev)
+    gk = _heads(where, "dk", dk, dt, ks, dev)
+    rows, rotary = _rotary_check(where, qs[:-2], dev, dt, qs[-1], positions, table, q_weight, k_weight)
 
     if _elsewhere(stream, dev):
         return _run_elsewhere(stream, (q, k, dq, dk, positions, table, q_weight, k_weight, workspace),
                               lambda: qk_norm_rotary_backward(dq, dk, q, k, positions, table, q_weight, k_weight, norm,
                                                               eps, interleaved, workspace))
     s = _raw_stream(dev.index)
-    tokens = _rows(lead)
-    dx = torch.empty(q.shape, dtype=dt, device=dev)
-    dy = torch.empty(k.shape, dtype=dt, device=dev)
+    tokens, heads, kv, dim = _rows(qs[:-2]), qs[-2], ks[-2], qs[-1]
+    dx, dy = _like(q), _like(k)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     wp, wb, _keep = None, 0, None
@@ -161,10 +171,11 @@ def _sequences(where, lead, offsets, dev):
     """Sequences of the batch: those of ``offsets``, or one per row of the dimensions before the last."""
     if offsets is None:
         return max(1, _rows(lead[:-1]))
-    if offsets.dim() != 1 or offsets.shape[0] < 2:
+    shape = offsets.shape
+    if len(shape) != 1 or shape[0] < 2:
         raise ValueError(f"{where}: offsets must hold the sequences' starts and the last one's end")
-    _check(where, dev, torch.int64, ("offsets", offsets, offsets.shape))
-    return offsets.shape[0] - 1
+    _check(where, dev, torch.int64, ("offsets", offsets, shape))
+    return shape[0] - 1
 
 
 def attention(q, k, v, offsets=None, causal=True, scale=None, workspace=None, stream=None):
@@ -175,19 +186,20 @@ def attention(q, k, v, offsets=None, causal=True, scale=None, workspace=None, st
     different lengths one behind the other: sequence s is tokens offsets[s] to offsets[s + 1], and
     tokens outside all of them get o = 0 and lse = -inf.  Without offsets the tokens are one
     sequence, or (batch, tokens, heads, dim) a batch of equal ones.  ``lse`` is (heads, all tokens)."""
-    dt, dev, lead, heads, kv, dim = _sizes("attention", q, k)
-    tokens = _rows(lead)
-    hq = _heads("attention", "q", q, dt, lead, heads, dim, dev)
-    hk = _heads("attention", "k", k, dt, lead, kv, dim, dev)
-    hv = _heads("attention", "v", v, dt, lead, kv, dim, dev)
-    sequences = _sequences("attention", lead, offsets, dev)
+    dt, dev = q.dtype, q.device
+    qs, ks = _shapes("attention", q, k)
+    hq = _heads("attention", "q", q, dt, qs, dev)
+    hk = _heads("attention", "k", k, dt, ks, dev)
+    hv = _heads("attention", "v", v, dt, ks, dev)
+    sequences = _sequences("attention", qs[:-2], offsets, dev)
+    tokens, heads, kv, dim = qs[0] if len(qs) == 3 else _rows(qs[:-2]), qs[-2], ks[-2], qs[-1]
     _no_graph("attention", q, k, v)
 
     if _elsewhere(stream, dev):
         return _run_elsewhere(stream, (q, k, v, offsets, workspace),
                               lambda: attention(q, k, v, offsets, causal, scale, workspace))
     s = _raw_stream(dev.index)
-    o = torch.empty(q.shape, dtype=dt, device=dev)
+    o = _like(q)
     lse = torch.empty(heads, tokens, dtype=torch.float32, device=dev)
     wp, wb, _keep = _space(workspace, lambda: attention_workspace(tokens, heads, kv, dim, dt, sequences), dev)
     st = _lib.load().dmuon_attention_forward(hq, hk, hv, _ptr(offsets), sequences, o.data_ptr(), lse.data_ptr(), tokens,
@@ -201,23 +213,22 @@ def attention_backward(do, q, k, v, o, lse, offsets=None, causal=True, scale=Non
     """``(dq, dk, dv)`` from the gradient of ``o`` and the inputs and outputs of ``attention``; dk and dv
     are summed over the query heads that share a key head."""
     where = "attention_backward"
-    dt, dev, lead, heads, kv, dim = _sizes(where, q, k)
-    tokens = _rows(lead)
-    hq = _heads(where, "q", q, dt, lead, heads, dim, dev)
-    hk = _heads(where, "k", k, dt, lead, kv, dim, dev)
-    hv = _heads(where, "v", v, dt, lead, kv, dim, dev)
-    ho = _heads(where, "do", do, dt, lead, heads, dim, dev)
-    _check(where, dev, dt, ("o", o, q.shape))
+    dt, dev = q.dtype, q.device
+    qs, ks = _shapes(where, q, k)
+    hq = _heads(where, "q", q, dt, qs, dev)
+    hk = _heads(where, "k", k, dt, ks, dev)
+    hv = _heads(where, "v", v, dt, ks, dev)
+    ho = _heads(where, "do", do, dt, qs, dev)
+    tokens, heads, kv, dim = _rows(qs[:-2]), qs[-2], ks[-2], qs[-1]
+    _check(where, dev, dt, ("o", o, qs))
     _check(where, dev, torch.float32, ("lse", lse, (heads, tokens)))
-    sequences = _sequences(where, lead, offsets, dev)
+    sequences = _sequences(where, qs[:-2], offsets, dev)
 
     if _elsewhere(stream, dev):
         return _run_elsewhere(stream, (q, k, v, do, o, lse, offsets, workspace),
                               lambda: attention_backward(do, q, k, v, o, lse, offsets, causal, scale, workspace))
     s = _raw_stream(dev.index)
-    dq = torch.empty(q.shape, dtype=dt, device=dev)
-    dk = torch.empty(k.shape, dtype=dt, device=dev)
-    dv = torch.empty(k.shape, dtype=dt, device=dev)
+    dq, dk, dv = _like(q), _like(k), _like(v)
     wp, wb, _keep = _space(workspace, lambda: attention_workspace(tokens, heads, kv, dim, dt, sequences, True), dev)
     st = _lib.load().dmuon_attention_backward(ho, hq, hk, hv, o.data_ptr(), lse.data_ptr(), _ptr(offsets), sequences,
                                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), tokens, heads, kv, dim,
