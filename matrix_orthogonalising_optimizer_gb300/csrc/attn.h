@@ -30,8 +30,9 @@ struct AttnArgs {
     int32_t causal;
     int32_t slots;             // row tiles of a head (an upper bound: see attn_slots)
     int32_t fill;              // blocks behind them that clear the rows of no sequence
-    int32_t whole;             // backward, tensor cores: sequences that may fit one tile
+    int32_t whole;             // backward, tensor cores: sequences, where those of one tile have their own launch
     int32_t parts;             // backward: blocks that share the queries of a key tile
+    unsigned* counter;         // backward, tensor cores: [2] items taken; cleared with delta
     float* partial;            // parts > 1: [2][parts][tokens][kv_heads][dim] sums of dk (unscaled) and dv
     float scale, scale_log2;   // scale_log2 = scale * log2(e)
 };
@@ -88,13 +89,14 @@ __device__ __forceinline__ bool attn_find(const AttnArgs& a, int32_t slot, int T
 // Clears the rows of no sequence -- before the first and behind the last -- of one
 // head: o = 0, lse = -inf, gradients 0.  Block f of `a.fill`.
 template <typename T>
-__device__ __forceinline__ void attn_clear(const AttnArgs& a, T* x, float* lse, int heads, int head, int f) {
+__device__ __forceinline__ void attn_clear(const AttnArgs& a, T* x, float* lse, int heads, int head, int f, int thread,
+                                           int threads) {
     const int64_t first = attn_offset(a, 0), last = attn_offset(a, a.sequences);
     const int64_t outside = first + (a.tokens - (last > first ? last : first));
     for (int64_t i = f; i < outside; i += a.fill) {
         const int64_t row = i < first ? i : i - first + (last > first ? last : first);
-        for (int c = threadIdx.x; c < a.dim; c += blockDim.x) x[(row * heads + head) * a.dim + c] = T(0.0f);
-        if (lse && threadIdx.x == 0) lse[head * a.tokens + row] = __int_as_float(0xff800000);
+        for (int c = thread; c < a.dim; c += threads) x[(row * heads + head) * a.dim + c] = T(0.0f);
+        if (lse && thread == 0) lse[head * a.tokens + row] = __int_as_float(0xff800000);
     }
 }
 

@@ -177,8 +177,8 @@ __device__ __forceinline__ bool take_block(const AttnArgs& a, unsigned block, in
     const int slot = static_cast<int>(block / static_cast<unsigned>(heads));
     b.head = static_cast<int>(block - static_cast<unsigned>(slot) * heads);
     if (slot >= a.slots) {
-        attn_clear(a, out, lse, heads, b.head, slot - a.slots);
-        if (out2) attn_clear(a, out2, nullptr, heads, b.head, slot - a.slots);
+        attn_clear(a, out, lse, heads, b.head, slot - a.slots, threadIdx.x, blockDim.x);
+        if (out2) attn_clear(a, out2, nullptr, heads, b.head, slot - a.slots, threadIdx.x, blockDim.x);
         return false;
     }
     if (!attn_find(a, slot, T, b.t)) return false;
@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
 // delta = do . o, one warp per row.  Rows of no sequence are never read later.
 template <typename E>
 __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttnArgs a) {
+    if (a.counter && blockIdx.x == 0 && threadIdx.x < 2) a.counter[threadIdx.x] = 0;
     const int64_t rows = a.tokens * a.heads;
     const int lane = threadIdx.x % 32;
     for (int64_t r = blockIdx.x * 8ll + threadIdx.x / 32; r < rows; r += gridDim.x * 8ll) {
@@ -465,6 +466,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Attn
 // do, four rows' loads in flight (134 MB at 8192 tokens, 32 heads of 128: 48 -> 24 us).
 template <typename E, int G>
 __global__ void __launch_bounds__(256) delta_vector_kernel(const __grid_constant__ AttnArgs a) {
+    if (a.counter && blockIdx.x == 0 && threadIdx.x < 2) a.counter[threadIdx.x] = 0;
     constexpr int N = 16 / sizeof(E), R = 32 / G, U = 4;
     const int64_t rows = a.tokens * a.heads;
     const int lane = threadIdx.x % 32, c = lane % G * N;

@@ -9,7 +9,8 @@
 // fixed order -- no atomics, no fp32 partial sums through L2 --, and p and ds never
 // pass through shared memory: the side of the keys works on s^T = k q^T, whose rows
 // are what dv and dk need as the left operand in TMEM, the side of the queries on s.
-// Both kinds of CTA are one launch, so that one fills the other's last wave.
+// Both kinds of tile are items of one persistent launch, taken from a counter: one fills
+// the other's last wave, and the start of a CTA is paid once.
 //
 // Keys: TMEM holds s^T and dp^T (p^T and ds^T take their place, bf16), dv and dk.  The
 // tensor cores run dv_i, s_{i+1}, dk_i, dp_{i+1}: the exponentials of tile i + 1 fall
@@ -20,13 +21,17 @@
 // Sequences of one tile: a CTA makes all three gradients (short_side).
 //
 // Bound: the tensor cores.  Per pair of 128-token tiles 7 * 512 cycles at dim = 128;
-// measured 2430 a step of the keys (2048 of MMAs) and about 2000 of the queries
-// (1536); 8192 tokens, 32/8 heads of 128, causal: 1.09 ms with delta, 1.26 PFLOP/s of the five products,
-// 1.77 of the seven.
+// measured about 2300 a step of the keys (2048 of MMAs) and 1850 of the queries (1536), and 3
+// to 6 us a tile besides.  8192 tokens, 32/8 heads of 128, causal: 1.07 ms with delta,
+// 1.29 PFLOP/s of the five products, 1.80 of the seven; five documents packed into 8192
+// tokens 0.40 ms; 12 heads of 64 0.32 ms (element-wise work and hand-overs).
 //
-// Warp 0 loads, warp 1 issues the MMAs, warp 2 fetches lse and delta of the query tiles
-// (side of the keys), warps 4 to 11 do the element-wise work, half of the columns
+// Warp 0 loads and looks for the next item, warp 1 issues the MMAs, warp 2 fetches lse and
+// delta of the query tiles (side of the keys), warps 4 to 11 do the element-wise work, half of the columns
 // each warpgroup.
+#include <algorithm>
+#include <cstddef>
+
 #include "attn_tc.cuh"
 #include "internal.h"
 #include "ops.h"
@@ -40,10 +45,19 @@ __device__ int32_t g_status = 0;
 constexpr int kThreads = 384;
 constexpr int kEltWarp0 = 4, kEltWarps = 8;
 constexpr uint32_t kCols = 512;
-constexpr int kRegsLow = 56, kRegsElt = 224;  // 56 + 2 x 224 = 3 x 168: the launch's registers
+// 88 + 2 x 208 = 3 x 168: the launch's registers (with 56 the issuing warp spills: 3 % slower)
+constexpr int kRegsLow = 88, kRegsElt = 208;
 
 template <int DP>
 constexpr int kStages = DP == 128 ? 5 : 8;
+
+// What a CTA does next: a tile's gradients, or rows and partial sums to clear.
+enum Kind : int32_t { KEYS, WHOLE, QUERIES, CLEAR_KEYS, CLEAR_QUERIES, CLEAR_PART, NONE };
+
+struct Item {
+    int32_t kind, head, part;
+    int32_t begin, len, tile;  // of the sequence, as AttnTile; CLEAR_KEYS, CLEAR_QUERIES: tile is the share
+};
 
 template <int DP>
 struct __align__(1024) Smem {
@@ -63,9 +77,9 @@ struct __align__(1024) Smem {
     uint64_t stat_full[2];
     uint64_t stat_empty[2];
     uint64_t done;
-    AttnTile tile;
+    Item item[2];               // at hand, and the next
     uint32_t tmem;
-    int32_t any;
+    int32_t bad;                // a wait gave up
 };
 
 template <int kSlots>
@@ -80,8 +94,9 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
-    const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &g_status));
+template <int DP>
+__device__ __forceinline__ bool wait_warp(Smem<DP>& S, uint64_t* bar, uint32_t parity) {
+    const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &S.bad));
     fence_after();
     return r;
 }
@@ -107,7 +122,7 @@ template <int DP, int kSlots, typename F>
 __device__ __forceinline__ void produce(Smem<DP>& S, uint32_t e, const uint8_t* slots, int count, F what) {
     Ring<kSlots> r;
     for (int i = 0; i < count; ++i) {
-        if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[r.stage], r.phase ^ 1, &g_status))) return;
+        if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[r.stage], r.phase ^ 1, &S.bad))) return;
         const CUtensorMap* map;
         int head, token;
         what(i, map, head, token);
@@ -134,11 +149,17 @@ __device__ __forceinline__ int part_begin(const AttnArgs& a, const AttnTile& t, 
     return attn_part((queries + kRows - 1) / kRows * a.group, part, a.parts);  // one tile: heads
 }
 
+// The rows of no sequence, by the element-wise warps: share f of a.fill.
+template <typename T>
+__device__ __forceinline__ void clear_rows_of(const AttnArgs& a, T* x, int heads, int head, int f) {
+    attn_clear(a, x, nullptr, heads, head, f, threadIdx.x - 32 * kEltWarp0, 32 * kEltWarps);
+}
+
 // A part without steps: its sums are zero.
 __device__ __forceinline__ void clear_part(const AttnArgs& a, const AttnTile& t, int kv, int part) {
     const int rows = min(kRows, t.len - t.tile * kRows);
     const int64_t first = ((t.begin + t.tile * kRows) * a.kv_heads + kv) * a.dim;
-    for (int i = threadIdx.x; i < rows * a.dim; i += kThreads) {
+    for (int i = threadIdx.x - 32 * kEltWarp0; i < rows * a.dim; i += 32 * kEltWarps) {
         const int64_t at = first + static_cast<int64_t>(i / a.dim) * a.kv_heads * a.dim + i % a.dim;
         attn_partial(a, 0, part)[at] = 0.0f;
         attn_partial(a, 1, part)[at] = 0.0f;
@@ -205,7 +226,7 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
         // s, and dp, of the next tile of the ring
         const auto form = [&](uint32_t cols, uint64_t key, uint64_t* full, int& slot) {
             slot = r.stage;
-            if (!wait_warp(&S.full[slot], r.phase)) return false;
+            if (!wait_warp(S, &S.full[slot], r.phase)) return false;
             product_cols<DP>(e, tmem + cols, key, desc_k(ring + slot * kTile<DP>));
             if (full) umma_commit(e, saddr(full));
             r.next();
@@ -215,16 +236,16 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
             product_rows<DP>(e, tmem + cols, tmem + p, desc_mn(ring + slot * kTile<DP>), 0, 4, more);
             product_rows<DP>(e, tmem + cols, tmem + p + C::kHalf, desc_mn(ring + slot * kTile<DP>), 4, 4, true);
         };
-        bool ok = wait_warp(&S.own_full, 0) && form(C::kS, dk_k, C::kApart ? nullptr : &S.s_full, sq) &&
+        bool ok = wait_warp(S, &S.own_full, 0) && form(C::kS, dk_k, C::kApart ? nullptr : &S.s_full, sq) &&
                   form(C::kG, dk_v, C::kApart ? &S.s_full : &S.g_full, so);
         for (int i = 0; i < steps && ok; ++i) {
             const bool more = i + 1 < steps;
             int sq1 = 0, so1 = 0;
             if constexpr (C::kApart) {
                 if (more)
-                    ok = wait_warp(&S.taken, i & 1) && form(C::kS, dk_k, nullptr, sq1) &&
+                    ok = wait_warp(S, &S.taken, i & 1) && form(C::kS, dk_k, nullptr, sq1) &&
                          form(C::kG, dk_v, &S.s_full, so1);
-                ok = ok && wait_warp(&S.ds_ready, i & 1);
+                ok = ok && wait_warp(S, &S.ds_ready, i & 1);
                 if (!ok) break;
                 add(C::kDv, C::kP, so, i > 0);
                 umma_commit(e, saddr(&S.empty[so]));
@@ -232,11 +253,11 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
                 umma_commit(e, saddr(&S.empty[sq]));
                 umma_commit(e, saddr(&S.used));
             } else {
-                ok = wait_warp(&S.p_ready, i & 1);
+                ok = wait_warp(S, &S.p_ready, i & 1);
                 if (!ok) break;
                 add(C::kDv, C::kP, so, i > 0);
                 umma_commit(e, saddr(&S.empty[so]));
-                ok = (!more || form(C::kS, dk_k, &S.s_full, sq1)) && wait_warp(&S.ds_ready, i & 1);
+                ok = (!more || form(C::kS, dk_k, &S.s_full, sq1)) && wait_warp(S, &S.ds_ready, i & 1);
                 if (!ok) break;
                 add(C::kDk, C::kDs, sq, i > 0);
                 umma_commit(e, saddr(&S.empty[sq]));
@@ -247,11 +268,11 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
         }
         // also after a wait that gave up: no MMA or commit is under way when the CTA leaves
         umma_commit(e, saddr(&S.done));
-        mbar_wait<false>(&S.done, 0, &g_status);
+        mbar_wait<false>(&S.done, 0, &S.bad);
     } else if (!kElt && warp == 2) {
         for (int i = 0; i < steps; ++i) {
             const int st = i & 1;
-            if (!wait_warp(&S.stat_empty[st], ((i >> 1) & 1) ^ 1)) break;
+            if (!wait_warp(S, &S.stat_empty[st], ((i >> 1) & 1) ^ 1)) break;
             int head, row;
             where(i, head, row);
             const int64_t at = head * a.tokens + token0 + row;
@@ -279,7 +300,7 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
             // columns of this half that see key r: [lo, hi)
             const bool masked = queries < kRows || (a.causal && row == row0);
             const int lo = (a.causal ? row0 + r - row : 0) - 64 * half, hi = queries - 64 * half;
-            ok = wait_warp(&S.stat_full[st], (i >> 1) & 1) && wait_warp(&S.s_full, i & 1);
+            ok = wait_warp(S, &S.stat_full[st], (i >> 1) & 1) && wait_warp(S, &S.s_full, i & 1);
             if (!ok) break;
             float p[64], g[C::kApart ? 64 : 32];
             tmem_ld64(ts, p);
@@ -305,21 +326,21 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
             }
             if constexpr (C::kApart) {
                 // the products of the tile before have read p and ds
-                if (i > 0) ok = wait_warp(&S.used, (i - 1) & 1);
+                if (i > 0) ok = wait_warp(S, &S.used, (i - 1) & 1);
                 if (!ok) break;
             }
             store_cols64(tp, p);
             if (queries < kRows) {
                 // query rows behind the sequence, of dO before dv reads it, of Q before dk does
                 const int o = 2 * i + 1;
-                ok = wait_warp(&S.full[o % NS], (o / NS) & 1);
+                ok = wait_warp(S, &S.full[o % NS], (o / NS) & 1);
                 if (!ok) break;
                 clear_rows<DP>(S.ring[o % NS], queries, thread, 256);
                 clear_rows<DP>(S.ring[2 * i % NS], queries, thread, 256);
             }
             if constexpr (!C::kApart) {
                 arrive_warp(&S.p_ready, lane);
-                ok = wait_warp(&S.g_full, i & 1);
+                ok = wait_warp(S, &S.g_full, i & 1);
                 if (!ok) break;
             }
             const float4* nd = reinterpret_cast<const float4*>(&S.stat[st][1][64 * half]);
@@ -350,7 +371,7 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
             arrive_warp(&S.ds_ready, lane);
             if (lane == 0) mbar_arrive(&S.stat_empty[st]);
         }
-        if (ok && wait_warp(&S.done, 0))
+        if (ok && wait_warp(S, &S.done, 0))
             store_keys<DP>(a, S, t, kv, part, half, warp % 4, C::kDk, C::kDv, lanes, lane);
     }
 }
@@ -392,24 +413,24 @@ __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, con
         // s and dp of the ring's next two tiles
         const auto form = [&](int& slot) {
             slot = r.stage;
-            if (!wait_warp(&S.full[slot], r.phase)) return false;
+            if (!wait_warp(S, &S.full[slot], r.phase)) return false;
             product_cols_ts<DP>(e, tmem + kQs, tmem + kQq, desc_k(base + slot * kTile<DP>));
             r.next();
-            if (!wait_warp(&S.full[r.stage], r.phase)) return false;
+            if (!wait_warp(S, &S.full[r.stage], r.phase)) return false;
             product_cols<DP>(e, tmem + kQg, d_o, desc_k(base + r.stage * kTile<DP>));
             umma_commit(e, saddr(&S.s_full));
             umma_commit(e, saddr(&S.empty[r.stage]));
             r.next();
             return true;
         };
-        bool ok = wait_warp(&S.q_ready, 0);
+        bool ok = wait_warp(S, &S.q_ready, 0);
         if (ok && lane == 0) mbar_arrive(&S.empty[0]);
         __syncwarp();
-        ok = ok && wait_warp(&S.own_full, 0) && form(sk);
+        ok = ok && wait_warp(S, &S.own_full, 0) && form(sk);
         for (int i = 0; i < steps && ok; ++i) {
             int sk1 = 0;
-            if (i + 1 < steps) ok = wait_warp(&S.taken, i & 1) && form(sk1);
-            ok = ok && wait_warp(&S.ds_ready, i & 1);
+            if (i + 1 < steps) ok = wait_warp(S, &S.taken, i & 1) && form(sk1);
+            ok = ok && wait_warp(S, &S.ds_ready, i & 1);
             if (!ok) break;
             product_rows<DP>(e, tmem + kQdq, tmem + kQds, desc_mn(base + sk * kTile<DP>), 0, 8, i > 0);
             umma_commit(e, saddr(&S.empty[sk]));
@@ -417,7 +438,7 @@ __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, con
             sk = sk1;
         }
         umma_commit(e, saddr(&S.done));
-        mbar_wait<false>(&S.done, 0, &g_status);
+        mbar_wait<false>(&S.done, 0, &S.bad);
     } else if (kElt) {
         const int half = (warp - kEltWarp0) / 4, thread = threadIdx.x - 32 * kEltWarp0, r = thread % kRows;
         const uint32_t lanes = (static_cast<uint32_t>(warp % 4 * 32) << 16) + tmem;
@@ -427,7 +448,7 @@ __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, con
         const float2 c2 = both(a.scale_log2);
         const float2 nl = both(in ? a.lse[head * a.tokens + token] * -kLog2e : 0.0f);
         const float2 nd = both(in ? -a.delta[head * a.tokens + token] : 0.0f);
-        bool ok = wait_warp(&S.full[0], 0);
+        bool ok = wait_warp(S, &S.full[0], 0);
         if (ok) {
             // Q into TMEM, half of each row's 16-byte pieces per warpgroup (DP / 4 words)
             uint32_t w[32];
@@ -449,7 +470,7 @@ __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, con
         }
         for (int i = 0; i < steps && ok; ++i) {
             const int keys = min(kRows, t.len - i * kRows);
-            ok = wait_warp(&S.s_full, i & 1);
+            ok = wait_warp(S, &S.s_full, i & 1);
             if (!ok) break;
             float p[64], g[64];
             tmem_ld64(lanes + kQs + 64 * half, p);
@@ -474,13 +495,13 @@ __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, con
                 clear_rows<DP>(slots + (1 + 2 * i) % NS * kTile<DP>, keys, thread, 256);
             }
             // the product of the tile before has read ds
-            if (i > 0) ok = wait_warp(&S.used, (i - 1) & 1);
+            if (i > 0) ok = wait_warp(S, &S.used, (i - 1) & 1);
             if (!ok) break;
             store_cols64(lanes + kQds + 32 * half, p);
             arrive_warp(&S.ds_ready, lane);
         }
         // a box of 64 columns each warpgroup
-        if (64 * half < DP && ok && wait_warp(&S.done, 0)) {
+        if (64 * half < DP && ok && wait_warp(S, &S.done, 0)) {
             const int quarter = warp % 4;
             const int64_t out = t.begin + row0 + 32 * quarter;
             store_rows<1>(S.own[0] + half * kBox + quarter * 4096, kQdq + 64 * half + lanes, a.scale,
@@ -529,18 +550,18 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
         const uint32_t e = elect_one();
         const uint32_t own = saddr(S.own[0]), ring = saddr(S.ring[0]);
         const uint32_t p = saddr(p_tile), ds = saddr(ds_tile);
-        bool ok = wait_warp(&S.own_full, 0);
+        bool ok = wait_warp(S, &S.own_full, 0);
         for (int i = 0; i < steps && ok; ++i) {
             const int nq = 2 * i, no = 2 * i + 1, sq = nq % NS, so = no % NS;
             // dq of the head before has been read
-            ok = (i == 0 || wait_warp(&S.taken, (i - 1) & 1)) && wait_warp(&S.full[sq], (nq / NS) & 1);
+            ok = (i == 0 || wait_warp(S, &S.taken, (i - 1) & 1)) && wait_warp(S, &S.full[sq], (nq / NS) & 1);
             if (!ok) break;
             product_cols<DP>(e, tmem + kS, desc_k(ring + sq * kTile<DP>), desc_k(own));
-            ok = wait_warp(&S.full[so], (no / NS) & 1);
+            ok = wait_warp(S, &S.full[so], (no / NS) & 1);
             if (!ok) break;
             product_cols<DP>(e, tmem + kG, desc_k(ring + so * kTile<DP>), desc_k(own + kTile<DP>));
             umma_commit(e, saddr(&S.s_full));
-            ok = wait_warp(&S.ds_ready, i & 1);
+            ok = wait_warp(S, &S.ds_ready, i & 1);
             if (!ok) break;
             product_tile<DP, true>(e, tmem + kDv, desc_mn(p), desc_mn(ring + so * kTile<DP>), i > 0);
             umma_commit(e, saddr(&S.empty[so]));
@@ -550,7 +571,7 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
             umma_commit(e, saddr(&S.used));
         }
         umma_commit(e, saddr(&S.done));
-        mbar_wait<false>(&S.done, 0, &g_status);
+        mbar_wait<false>(&S.done, 0, &S.bad);
     } else if (kElt) {
         const int half = (warp - kEltWarp0) / 4, thread = threadIdx.x - 32 * kEltWarp0, r = thread % kRows;
         const int quarter = warp % 4;
@@ -558,12 +579,12 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
         const bool in = r < t.len;
         const int seen = (!in ? 0 : a.causal ? r + 1 : t.len) - 64 * half;  // columns of this half that row r sees
         const float2 c2 = both(a.scale_log2);
-        bool ok = wait_warp(&S.own_full, 0);
+        bool ok = wait_warp(S, &S.own_full, 0);
         if (ok && t.len < kRows) clear_rows<DP>(S.own[0], t.len, thread, 256);  // K: the rows of ds k
         for (int i = 0; i < steps && ok; ++i) {
             const int head = head0 + i;
             const float2 nl = both(in ? a.lse[head * a.tokens + t.begin + r] * -kLog2e : 0.0f);
-            ok = wait_warp(&S.s_full, i & 1);
+            ok = wait_warp(S, &S.s_full, i & 1);
             if (!ok) break;
             float p[64], g[64];
             tmem_ld64(lanes + kS + 64 * half, p);
@@ -585,7 +606,7 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
                 sum2 = fma2(make_float2(p[k], p[k + 1]), make_float2(g[k], g[k + 1]), sum2);
             S.stat[i & 1][half][r] = sum2.x + sum2.y;
             release_warp(&S.p_ready, lane);  // both halves of every row's sum
-            ok = wait_warp(&S.p_ready, i & 1);
+            ok = wait_warp(S, &S.p_ready, i & 1);
             if (!ok) break;
             const float2 nd = both(-(S.stat[i & 1][0][r] + S.stat[i & 1][1][r]));
             // this row's 128 bytes of the half's box, in 16-byte pieces
@@ -612,7 +633,7 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             release_warp(&S.ds_ready, lane);
-            ok = wait_warp(&S.used, i & 1);
+            ok = wait_warp(S, &S.used, i & 1);
             if (!ok) break;
             // p's rows of this warp are free again: dq passes through them
             if (64 * half < DP) {
@@ -623,11 +644,127 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
             }
             release_warp(&S.taken, lane);
         }
-        if (ok && wait_warp(&S.done, 0)) store_keys<DP>(a, S, t, kv, part, half, quarter, kDk, kDv, lanes, lane);
+        if (ok && wait_warp(S, &S.done, 0)) store_keys<DP>(a, S, t, kv, part, half, quarter, kDk, kDv, lanes, lane);
+    }
+}
+
+// The next of the launch's items that has something to do, by one warp: side of the keys,
+// then of the queries, each with the heavy ones first, or (kWhole) sequences of one tile.
+// A CTA begins with its own index and takes the others from a counter.
+template <bool kWhole>
+__device__ __forceinline__ Item next_item(const AttnArgs& a, bool first, int lane) {
+    // tiles of the keys, tiles of the queries, rows to clear (in the only launch, or this one)
+    const unsigned tiles = kWhole ? a.whole : a.slots, fill = kWhole && a.slots > 0 ? 0 : a.fill;
+    const unsigned keys_end = tiles * a.kv_heads * a.parts, tiles_end = keys_end + (kWhole ? 0 : tiles * a.heads);
+    const unsigned clear_end = tiles_end + fill * a.kv_heads * a.parts, end = clear_end + fill * a.heads;
+    Item item;
+    for (;; first = false) {
+        unsigned n = blockIdx.x;
+        if (!first) {
+            unsigned taken = 0;
+            if (lane == 0) taken = atomicAdd(a.counter + (kWhole ? 1 : 0), 1u);
+            n = gridDim.x + __shfl_sync(kFullMask, taken, 0);
+        }
+        item = Item{NONE, 0, 0, 0, 0, 0};
+        if (n >= end) return item;
+        const bool clear = n >= tiles_end, keys = clear ? n < clear_end : n < keys_end;
+        const unsigned heads = keys ? a.kv_heads : a.heads, parts = keys ? a.parts : 1;
+        n -= clear ? (keys ? tiles_end : clear_end) : (keys ? 0 : keys_end);
+        const unsigned tile = n / parts, slot = tile / heads;
+        item.part = static_cast<int>(n - tile * parts);
+        item.head = static_cast<int>(tile - slot * heads);
+        if (clear) {
+            item.kind = keys ? CLEAR_KEYS : CLEAR_QUERIES;
+            item.tile = static_cast<int>(slot);
+            return item;
+        }
+        item.kind = kWhole ? WHOLE : keys ? KEYS : QUERIES;
+        AttnTile t;
+        bool any;
+        if constexpr (kWhole) {
+            t.begin = attn_offset(a, slot);
+            t.len = static_cast<int32_t>(attn_offset(a, slot + 1) - t.begin);
+            t.tile = 0;
+            any = t.len > 0 && t.len <= kRows;
+        } else {
+            any = attn_find(a, static_cast<int>(slot), kRows, t) && (a.whole == 0 || t.len > kRows);
+        }
+        if (!any) continue;
+        item.begin = static_cast<int32_t>(t.begin);
+        item.len = t.len;
+        item.tile = t.tile;
+        if (parts > 1 && part_begin(a, t, item.part) == part_begin(a, t, item.part + 1)) item.kind = CLEAR_PART;
+        return item;
     }
 }
 
 template <int DP>
+__device__ __forceinline__ void init_barriers(Smem<DP>& S, int lane, bool again) {
+    // one barrier a lane, in the order of Smem
+    uint64_t* bar = &S.own_full + lane;
+    constexpr int n = static_cast<int>((offsetof(Smem<DP>, done) - offsetof(Smem<DP>, own_full)) / 8) + 1;
+    static_assert(n <= 32, "a barrier a lane");
+    if (lane >= n) return;
+    if (again) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+    const bool warps = bar == &S.taken || bar == &S.p_ready || bar == &S.ds_ready || bar == &S.q_ready ||
+                       (bar >= S.stat_empty && bar < S.stat_empty + 2);
+    mbar_init(bar, warps ? kEltWarps : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// All items of a CTA, by the helper warps (kElt false) or the element-wise ones.
+template <int DP, bool kElt, bool kWhole>
+__device__ __forceinline__ void work(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq, const CUtensorMap* mk,
+                                     const CUtensorMap* mv, const CUtensorMap* mo, int warp, int lane, uint32_t tmem) {
+    for (int n = 0;; ++n) {
+        const Item& next = S.item[n & 1];
+        // from one lane: uniform, as MMAs and copies take their operands
+        const int kind = __shfl_sync(kFullMask, next.kind, 0), head = __shfl_sync(kFullMask, next.head, 0);
+        const int part = __shfl_sync(kFullMask, next.part, 0);
+        AttnTile t;
+        t.begin = __shfl_sync(kFullMask, next.begin, 0);
+        t.len = __shfl_sync(kFullMask, next.len, 0);
+        t.tile = __shfl_sync(kFullMask, next.tile, 0);
+        if (kind == NONE) return;
+        if (kind == KEYS || kind == WHOLE || kind == QUERIES) {
+            if constexpr (kWhole) short_side<DP, kElt>(a, S, mq, mk, mv, mo, t, head, part, warp, lane, tmem);
+            else if (kind == KEYS) keys_side<DP, kElt>(a, S, mq, mk, mv, mo, t, head, part, warp, lane, tmem);
+            else queries_side<DP, kElt>(a, S, mq, mk, mv, mo, t, head, warp, lane, tmem);
+        } else if (kElt) {
+            // rows of no sequence, or a part without steps
+            if (kind == CLEAR_PART) {
+                clear_part(a, t, head, part);
+            } else if (kind == CLEAR_QUERIES) {
+                clear_rows_of(a, static_cast<__nv_bfloat16*>(a.out), a.heads, head, t.tile);
+            } else if (a.parts > 1) {
+                clear_rows_of(a, attn_partial(a, 0, part), a.kv_heads, head, t.tile);
+                clear_rows_of(a, attn_partial(a, 1, part), a.kv_heads, head, t.tile);
+            } else {
+                clear_rows_of(a, static_cast<__nv_bfloat16*>(a.dk), a.kv_heads, head, t.tile);
+                clear_rows_of(a, static_cast<__nv_bfloat16*>(a.dv), a.kv_heads, head, t.tile);
+            }
+        }
+        if (!kElt && warp == 0) {
+            // not before this item's last loads are issued: an item taken early would wait here
+            // while other SMs run dry
+            const Item item = next_item<kWhole>(a, false, lane);
+            if (lane == 0) S.item[(n + 1) & 1] = item;
+        }
+        // shared memory, TMEM and barriers pass to the next item
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_before();
+        __syncthreads();
+        if (__shfl_sync(kFullMask, S.bad, 0) != 0) return;  // uniform, or the next item would run without uniform registers
+        if (!kElt && warp == 2) init_barriers(S, lane, true);
+        __syncthreads();
+        fence_after();
+    }
+}
+
+// kWhole: the sequences of one tile, in a launch of their own (as another kind of item
+// of the other launch they slowed the others down by 3 to 10 %: the compiler's choices
+// for one kind of loop suffer from the next).
+template <int DP, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1)
     backward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -635,100 +772,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem<DP>& S = *reinterpret_cast<Smem<DP>*>(raw);
     const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    // blocks of the keys, of the sequences of one tile, of the queries
-    const unsigned first = static_cast<unsigned>(a.slots + a.fill) * a.kv_heads * a.parts;
-    const unsigned second = first + static_cast<unsigned>(a.whole) * a.kv_heads * a.parts;
-    const bool keys = blockIdx.x < first, whole = !keys && blockIdx.x < second;
-    const bool parts = keys || whole;
-    unsigned block = blockIdx.x - (keys ? 0 : whole ? first : second);
-    const int part = parts ? static_cast<int>(block % static_cast<unsigned>(a.parts)) : 0;
-    if (parts) block /= static_cast<unsigned>(a.parts);
-    const unsigned heads = parts ? a.kv_heads : a.heads;
-    const int slot = static_cast<int>(block / heads), head = static_cast<int>(block - slot * heads);
-    if (!whole && slot >= a.slots) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        const int f = slot - a.slots;
-        if (keys && a.parts > 1) {
-            attn_clear(a, attn_partial(a, 0, part), nullptr, a.kv_heads, head, f);
-            attn_clear(a, attn_partial(a, 1, part), nullptr, a.kv_heads, head, f);
-            return;
-        }
-        if (keys) attn_clear(a, static_cast<__nv_bfloat16*>(a.dk), nullptr, a.kv_heads, head, f);
-        attn_clear(a, static_cast<__nv_bfloat16*>(keys ? a.dv : a.out), nullptr, static_cast<int>(heads), head, f);
-        return;
-    }
     if (saddr(raw) % 1024 != 0) {  // no room was taken for aligning it here
         if (threadIdx.x == 0) atomicExch(&g_status, 1);
         return;
     }
     if (warp == 1) {
         tmem_alloc<kCols>(&S.tmem);
-    } else if (warp == 2 && lane == 0) {
-        mbar_init(&S.own_full, 1);
-        for (int i = 0; i < kStages<DP> + 1; ++i) {
-            mbar_init(&S.full[i], 1);
-            mbar_init(&S.empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&S.stat_full[i], 1);
-            mbar_init(&S.stat_empty[i], kEltWarps);
-        }
-        mbar_init(&S.s_full, 1);
-        mbar_init(&S.g_full, 1);
-        mbar_init(&S.used, 1);
-        mbar_init(&S.taken, kEltWarps);
-        mbar_init(&S.p_ready, kEltWarps);
-        mbar_init(&S.ds_ready, kEltWarps);
-        mbar_init(&S.q_ready, kEltWarps);
-        mbar_init(&S.done, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (warp == 2) {
+        init_barriers(S, lane, false);
+        if (lane == 0) S.bad = 0;
     } else if (warp == 0) {
         // meanwhile, and only after the kernels before have finished
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        AttnTile found;
-        bool any;
-        if (whole) {
-            found.begin = attn_offset(a, slot);
-            found.len = static_cast<int32_t>(attn_offset(a, slot + 1) - found.begin);
-            found.tile = 0;
-            any = found.len > 0 && found.len <= kRows;
-        } else {
-            any = attn_find(a, slot, kRows, found) && found.len > kRows;
-        }
-        if (lane == 0) {
-            S.tile = found;
-            S.any = any;
-        }
+        const Item item = next_item<kWhole>(a, true, lane);
+        if (lane == 0) S.item[0] = item;
     }
     fence_before();
     __syncthreads();
     fence_after();
-    // from one lane: uniform, as MMAs and copies take their operands
     const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);
-    const bool any = __shfl_sync(kFullMask, S.any, 0) != 0;
-    AttnTile t;
-    t.begin = __shfl_sync(kFullMask, static_cast<int32_t>(S.tile.begin), 0);
-    t.len = __shfl_sync(kFullMask, S.tile.len, 0);
-    t.tile = __shfl_sync(kFullMask, S.tile.tile, 0);
-    const bool empty = any && parts && a.parts > 1 && part_begin(a, t, part) == part_begin(a, t, part + 1);
-    if (empty) clear_part(a, t, head, part);
-    if (!any || empty) {
-        if (warp == 1) tmem_free<kCols>(tmem);
-        return;
-    }
     if (warp < kEltWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
-        if (keys) keys_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
-        else if (whole) short_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
-        else queries_side<DP, false>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
+        work<DP, false, kWhole>(a, S, &mq, &mk, &mv, &mo, warp, lane, tmem);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsElt));
-        if (keys) keys_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
-        else if (whole) short_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, part, warp, lane, tmem);
-        else queries_side<DP, true>(a, S, &mq, &mk, &mv, &mo, t, head, warp, lane, tmem);
+        work<DP, true, kWhole>(a, S, &mq, &mk, &mv, &mo, warp, lane, tmem);
     }
     fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && S.bad) atomicExch(&g_status, 1);
     if (warp == 1) {
         __syncwarp();
         fence_after();
@@ -736,42 +808,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int DP>
+template <int DP, bool kWhole>
 cudaError_t attribute() {
     static_assert(sizeof(Smem<DP>) <= 232448, "shared memory of a block");
-    return cudaFuncSetAttribute(backward_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(backward_kernel<DP, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(sizeof(Smem<DP>)));
 }
 
-cudaError_t prepare() {
+// Shared-memory attributes of all instances, once per device, and the device's SMs.
+cudaError_t prepare(int* sms) {
     static PerDevice cache;
-    int dev = 0, ok = 0;
+    int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return cache.get(dev, &ok, [](int* out) {
-        *out = 1;
-        const cudaError_t r = attribute<64>();
-        return r == cudaSuccess ? attribute<128>() : r;
+    return cache.get(dev, sms, [&](int* out) {
+        cudaError_t r = attribute<64, false>();
+        if (r == cudaSuccess) r = attribute<64, true>();
+        if (r == cudaSuccess) r = attribute<128, false>();
+        if (r == cudaSuccess) r = attribute<128, true>();
+        return r == cudaSuccess ? cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev) : r;
     });
 }
 
-template <int DP>
-cudaError_t launch(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
-    a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, kRows));
-    a.whole = a.sequences;
-    if (!a.offsets) (a.length <= kRows ? a.slots : a.whole) = 0;  // all of one kind
+// A persistent launch: a CTA per SM, fewer where there are fewer items.
+template <int DP, bool kWhole>
+cudaError_t launch(const AttnArgs& a, const AttnMaps& m, int64_t items, int sms, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.slots + a.fill) * (a.heads + a.kv_heads * a.parts) +
-                       static_cast<unsigned>(a.whole) * a.kv_heads * a.parts);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, sms)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Smem<DP>);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, backward_kernel<DP>, a, m.q, m.k, m.v, m.d_o);
+    return cudaLaunchKernelEx(&cfg, backward_kernel<DP, kWhole>, a, m.q, m.k, m.v, m.d_o);
+}
+
+// Sequences of one tile have their launch where the average one is no longer than
+// this; a few among longer ones are left to the other (their launch alone costs 3 us).
+constexpr int kShortAverage = 512;
+
+template <int DP>
+cudaError_t run(AttnArgs a, const AttnMaps& m, int sms, cudaStream_t s) {
+    const int64_t longest = a.offsets ? a.tokens : a.length, average = a.offsets ? a.tokens / a.sequences : a.length;
+    a.slots = longest <= kRows ? 0 : static_cast<int32_t>(attn_slots(a.tokens, a.sequences, kRows));
+    a.whole = longest <= kRows || (a.offsets && average <= kShortAverage) ? a.sequences : 0;
+    const int64_t keys = static_cast<int64_t>(a.kv_heads) * a.parts, both = a.heads + keys;
+    cudaError_t e = cudaSuccess;
+    if (a.whole > 0) e = launch<DP, true>(a, m, a.whole * keys + (a.slots > 0 ? 0 : a.fill * both), sms, s);
+    if (e == cudaSuccess && a.slots > 0) e = launch<DP, false>(a, m, (a.slots + a.fill) * both, sms, s);
+    return e;
 }
 
 }  // namespace
@@ -780,9 +868,10 @@ cudaError_t launch(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
 cudaError_t attn_bwd_status_word(void** p) { return cudaGetSymbolAddress(p, attn::g_status); }
 
 cudaError_t attn_tc_backward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s) {
-    const cudaError_t e = attn::prepare();
+    int sms = 0;
+    const cudaError_t e = attn::prepare(&sms);
     if (e != cudaSuccess) return e;
-    return a.dim <= 64 ? attn::launch<64>(a, m, s) : attn::launch<128>(a, m, s);
+    return a.dim <= 64 ? attn::run<64>(a, m, sms, s) : attn::run<128>(a, m, sms, s);
 }
 
 }  // namespace dmuon

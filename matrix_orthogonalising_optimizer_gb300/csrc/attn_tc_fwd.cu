@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
     const int head = static_cast<int>(blockIdx.x - static_cast<unsigned>(slot) * a.heads);
     if (slot >= a.slots) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, head, slot - a.slots);
+        attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, head, slot - a.slots, threadIdx.x, blockDim.x);
         return;
     }
     if (warp == 1) {
