@@ -29,6 +29,7 @@ struct AttnArgs {
     int32_t heads, kv_heads, group, dim;
     int32_t causal;
     int32_t slots;             // row tiles of a head (an upper bound: see attn_slots)
+    int32_t query_slots;       // FFMA backward: the same of the queries' blocks
     int32_t fill;              // blocks behind them that clear the rows of no sequence
     int32_t whole;             // backward, tensor cores: sequences, where those of one tile have their own launch
     int32_t parts;             // backward: blocks that share the queries of a key tile

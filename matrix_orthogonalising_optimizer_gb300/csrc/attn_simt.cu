@@ -14,6 +14,7 @@
 // dim + 4 floats apart: 16-byte reads of eight rows then cover all banks.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "act.cuh"
 #include "attn.h"
@@ -24,7 +25,7 @@
 namespace dmuon {
 namespace {
 
-constexpr int T = 64;           // queries and keys of a tile
+constexpr int T = 64;           // keys of a tile (side of the keys: and queries)
 constexpr int kThreads = 256;   // 16 x 16: thread (ty, tx) holds rows ty + 16 r, columns tx + 16 c
 constexpr int LP = T + 4;       // row stride of a T x T tile
 constexpr unsigned kFull = 0xffffffffu;
@@ -41,60 +42,97 @@ __device__ __forceinline__ E from_f(float v) {
     else return v;
 }
 
-// T rows of a head into shared memory, zero behind `rows` and `dim`.  `vec`: rows
-// start on 16-byte boundaries and dim is a multiple of 4.
-template <typename E, int DP>
+// N rows of a head on their way into shared memory, zero behind `rows` and `dim`.  fetch()
+// has all loads in flight at once and may run well before put(), so that a tile's
+// latency falls under the products of the one before.  `vec`: rows start on 16-byte
+// boundaries and dim is a multiple of 4; else put() loads element by element.
+template <typename E, int DP, int N = T>
+struct Tile {
+    static constexpr int LD = DP + 4, kEach = N * (DP / 4) / kThreads;
+    using Word = typename std::conditional<sizeof(E) == 4, float4, uint2>::type;
+    Word v[kEach];
+
+    __device__ __forceinline__ void fetch(const AttnHeads& h, int64_t row0, int rows, int head, int dim, bool vec) {
+        if (!vec) return;
+        const E* base = static_cast<const E*>(h.p) + row0 * h.token + head * h.head;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x + k * kThreads, r = i / (DP / 4), c = i % (DP / 4) * 4;
+            v[k] = Word{};
+            if (r < rows && c < dim) v[k] = *reinterpret_cast<const Word*>(base + r * h.token + c);
+        }
+    }
+    __device__ __forceinline__ void put(float* dst, const AttnHeads& h, int64_t row0, int rows, int head, int dim,
+                                        bool vec) const {
+        if (vec) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int i = threadIdx.x + k * kThreads, r = i / (DP / 4), c = i % (DP / 4) * 4;
+                float4 x;
+                if constexpr (sizeof(E) == 4) {
+                    x = v[k];
+                } else {
+                    const float2 a = tc::unpack_bf16x2(v[k].x), b = tc::unpack_bf16x2(v[k].y);
+                    x = make_float4(a.x, a.y, b.x, b.y);
+                }
+                *reinterpret_cast<float4*>(dst + r * LD + c) = x;
+            }
+            return;
+        }
+        const E* base = static_cast<const E*>(h.p) + row0 * h.token + head * h.head;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < N * DP; i += kThreads) {
+            const int r = i / DP, c = i % DP;
+            dst[r * LD + c] = r < rows && c < dim ? to_f<E>(base[r * h.token + c]) : 0.0f;
+        }
+    }
+};
+
+template <typename E, int DP, int N = T>
 __device__ __forceinline__ void load_tile(float* dst, const AttnHeads& h, int64_t row0, int rows, int head, int dim,
                                           bool vec) {
-    constexpr int LD = DP + 4;
-    const E* base = static_cast<const E*>(h.p) + row0 * h.token + head * h.head;
-    if (vec) {
-#pragma unroll 4
-        for (int i = threadIdx.x; i < T * (DP / 4); i += kThreads) {
-            const int r = i / (DP / 4), c = i % (DP / 4) * 4;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < rows && c < dim) {
-                const E* p = base + r * h.token + c;
-                if constexpr (sizeof(E) == 4) {
-                    v = *reinterpret_cast<const float4*>(p);
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2*>(p);
-                    const float2 a = tc::unpack_bf16x2(w.x), b = tc::unpack_bf16x2(w.y);
-                    v = make_float4(a.x, a.y, b.x, b.y);
-                }
-            }
-            *reinterpret_cast<float4*>(dst + r * LD + c) = v;
-        }
-        return;
-    }
-#pragma unroll 4
-    for (int i = threadIdx.x; i < T * DP; i += kThreads) {
-        const int r = i / DP, c = i % DP;
-        dst[r * LD + c] = r < rows && c < dim ? to_f<E>(base[r * h.token + c]) : 0.0f;
-    }
+    Tile<E, DP, N> t;
+    t.fetch(h, row0, rows, head, dim, vec);
+    t.put(dst, h, row0, rows, head, dim, vec);
 }
+
+// Two tiles of the same rows.
+template <typename E, int DP>
+struct Pair {
+    Tile<E, DP> a, b;
+    __device__ __forceinline__ void fetch(const AttnHeads& ha, const AttnHeads& hb, int64_t row0, int rows, int head,
+                                          int dim, bool va, bool vb) {
+        a.fetch(ha, row0, rows, head, dim, va);
+        b.fetch(hb, row0, rows, head, dim, vb);
+    }
+    __device__ __forceinline__ void put(float* da, float* db, const AttnHeads& ha, const AttnHeads& hb, int64_t row0,
+                                        int rows, int head, int dim, bool va, bool vb) const {
+        a.put(da, ha, row0, rows, head, dim, va);
+        b.put(db, hb, row0, rows, head, dim, vb);
+    }
+};
 
 // acc[r][c] = sum_d A[ty + 16 r][d] B[tx + 16 c][d].  Packed arithmetic (two products an
 // instruction, the same rate) leaves the issue slots that the loads need.
-template <int DP>
-__device__ __forceinline__ void product_nt(float (&acc)[4][4], const float* A, const float* B, int dim4) {
+template <int DP, int R>
+__device__ __forceinline__ void product_nt(float (&acc)[R][4], const float* A, const float* B, int dim4) {
     constexpr int LD = DP + 4;
     const float* a0 = A + (threadIdx.x / 16) * LD;
     const float* b0 = B + (threadIdx.x % 16) * LD;
-    float2 sum[4][4];  // even and odd d
+    float2 sum[R][4];  // even and odd d
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) sum[r][c] = tc::both(0.0f);
 #pragma unroll 2
     for (int d = 0; d < dim4; d += 4) {
-        float4 a[4], b[4];
+        float4 a[R], b[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(a0 + 16 * r * LD + d);
+        for (int r = 0; r < R; ++r) a[r] = *reinterpret_cast<const float4*>(a0 + 16 * r * LD + d);
 #pragma unroll
         for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4*>(b0 + 16 * c * LD + d);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 sum[r][c] = tc::fma2(make_float2(a[r].x, a[r].y), make_float2(b[c].x, b[c].y), sum[r][c]);
@@ -102,29 +140,29 @@ __device__ __forceinline__ void product_nt(float (&acc)[4][4], const float* A, c
             }
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[r][c] = sum[r][c].x + sum[r][c].y;
 }
 
 // acc[r][k] += sum_j P[ty + 16 r][j] V[j][4 tx + 64 (k / 2) + 2 (k % 2) ..]
-template <int DP>
-__device__ __forceinline__ void product_nn(float2 (&acc)[4][DP / 32], const float* P, const float* V) {
+template <int DP, int R>
+__device__ __forceinline__ void product_nn(float2 (&acc)[R][DP / 32], const float* P, const float* V) {
     constexpr int LD = DP + 4;
     const float* p0 = P + (threadIdx.x / 16) * LP;
     const float* v0 = V + 4 * (threadIdx.x % 16);
 #pragma unroll 2
     for (int j = 0; j < T; j += 4) {
-        float4 p[4];
+        float4 p[R];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(p0 + 16 * r * LP + j);
+        for (int r = 0; r < R; ++r) p[r] = *reinterpret_cast<const float4*>(p0 + 16 * r * LP + j);
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
             for (int c = 0; c < DP / 64; ++c) {
                 const float4 v = *reinterpret_cast<const float4*>(v0 + (j + jj) * LD + 64 * c);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
+                for (int r = 0; r < R; ++r) {
                     const float2 w = tc::both(jj == 0 ? p[r].x : jj == 1 ? p[r].y : jj == 2 ? p[r].z : p[r].w);
                     acc[r][2 * c] = tc::fma2(w, make_float2(v.x, v.y), acc[r][2 * c]);
                     acc[r][2 * c + 1] = tc::fma2(w, make_float2(v.z, v.w), acc[r][2 * c + 1]);
@@ -134,12 +172,12 @@ __device__ __forceinline__ void product_nn(float2 (&acc)[4][DP / 32], const floa
 }
 
 // Rows ty + 16 r < rows of a contiguous tokens x heads x dim tensor, times f[r].
-template <typename E, int DP>
-__device__ __forceinline__ void store_rows(void* out, const float2 (&acc)[4][DP / 32], const float (&f)[4],
+template <typename E, int DP, int R>
+__device__ __forceinline__ void store_rows(void* out, const float2 (&acc)[R][DP / 32], const float (&f)[R],
                                            int64_t row0, int rows, int heads, int head, int dim) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int i = ty + 16 * r;
         if (i >= rows) continue;
         E* p = static_cast<E*>(out) + ((row0 + i) * heads + head) * static_cast<int64_t>(dim);
@@ -171,7 +209,7 @@ struct Block {
 
 // The block's tile: heads run fastest, tiles of a sequence from its end where the
 // last ones have most to do (`last_first`).  False: nothing left to do.
-template <typename E>
+template <int N, typename E>
 __device__ __forceinline__ bool take_block(const AttnArgs& a, unsigned block, int heads, bool last_first, E* out, E* out2,
                                            float* lse, Block& b) {
     const int slot = static_cast<int>(block / static_cast<unsigned>(heads));
@@ -181,11 +219,11 @@ __device__ __forceinline__ bool take_block(const AttnArgs& a, unsigned block, in
         if (out2) attn_clear(a, out2, nullptr, heads, b.head, slot - a.slots, threadIdx.x, blockDim.x);
         return false;
     }
-    if (!attn_find(a, slot, T, b.t)) return false;
-    b.tiles = (b.t.len + T - 1) / T;
+    if (!attn_find(a, slot, N, b.t)) return false;
+    b.tiles = (b.t.len + N - 1) / N;
     const int tile = last_first ? b.tiles - 1 - b.t.tile : b.t.tile;
-    b.row0 = tile * T;
-    b.rows = min(T, b.t.len - b.row0);
+    b.row0 = tile * N;
+    b.rows = min(N, b.t.len - b.row0);
     return true;
 }
 
@@ -195,21 +233,21 @@ __device__ __forceinline__ bool vec_rows(const AttnHeads& h, int dim) {
     return reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.token % n == 0 && h.head % n == 0 && dim % 4 == 0;
 }
 
-template <typename E, int DP>
+template <typename E, int DP, int R>
 __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int LD = DP + 4;
     extern __shared__ float sm[];
-    float *Q = sm, *K = Q + T * LD, *V = K + T * LD, *P = V + T * LD;
+    float *Q = sm, *K = Q + 16 * R * LD, *V = K + T * LD, *P = V + T * LD;
     Block b;
-    if (!take_block(a, blockIdx.x, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), a.lse, b)) return;
+    if (!take_block<16 * R>(a, blockIdx.x, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), a.lse, b)) return;
     const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
-    load_tile<E, DP>(Q, a.q, b.t.begin + b.row0, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
-    float2 acc[4][DP / 32];
-    float top[4], base[4], sum[4];
+    load_tile<E, DP, 16 * R>(Q, a.q, b.t.begin + b.row0, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
+    float2 acc[R][DP / 32];
+    float top[R], base[R], sum[R];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
         top[r] = __int_as_float(0xff800000);
         base[r] = 0.0f;
         sum[r] = 0.0f;
@@ -217,16 +255,18 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
         for (int k = 0; k < DP / 32; ++k) acc[r][k] = tc::both(0.0f);
     }
     const int end = a.causal ? b.row0 + b.rows : b.t.len;  // keys that any of the rows sees
+    Pair<E, DP> next;
+    next.fetch(a.k, a.v, b.t.begin, min(T, b.t.len), kv, a.dim, vk, vv);
     for (int j0 = 0; j0 < end; j0 += T) {
         const int keys = min(T, b.t.len - j0);
         __syncthreads();
-        load_tile<E, DP>(K, a.k, b.t.begin + j0, keys, kv, a.dim, vk);
-        load_tile<E, DP>(V, a.v, b.t.begin + j0, keys, kv, a.dim, vv);
+        next.put(K, V, a.k, a.v, b.t.begin + j0, keys, kv, a.dim, vk, vv);
         __syncthreads();
-        float s[4][4];
+        if (j0 + T < end) next.fetch(a.k, a.v, b.t.begin + j0 + T, min(T, b.t.len - j0 - T), kv, a.dim, vk, vv);
+        float s[R][4];
         product_nt<DP>(s, Q, K, dim4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < R; ++r) {
             const int i = b.row0 + ty + 16 * r;
             const int seen = a.causal ? min(i + 1 - j0, keys) : keys;
             float m = top[r];
@@ -257,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
         __syncwarp();  // a row of P is written and read by one half warp
         product_nn<DP>(acc, P, V);
     }
-    float f[4];
+    float f[R];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
         f[r] = 1.0f / sum[r];
         const int i = ty + 16 * r;
         if (tx == 0 && i < b.rows)
@@ -269,23 +309,23 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     store_rows<E, DP>(a.out, acc, f, b.t.begin + b.row0, b.rows, a.heads, b.head, a.dim);
 }
 
-template <typename E, int DP>
-__global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__ AttnArgs a) {
+template <typename E, int DP, int R>
+__device__ __forceinline__ void dq_block(const AttnArgs& a, unsigned index, float* sm) {
     constexpr int LD = DP + 4;
-    extern __shared__ float sm[];
-    float *Q = sm, *O = Q + T * LD, *K = O + T * LD, *V = K + T * LD, *P = V + T * LD;
+    float *Q = sm, *O = Q + 16 * R * LD, *K = O + 16 * R * LD, *V = K + T * LD, *P = V + T * LD;
     Block b;
-    if (!take_block(a, blockIdx.x, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), nullptr, b)) return;
+    if (!take_block<16 * R>(a, index, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), nullptr, b))
+        return;
     const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
     const int64_t row = b.t.begin + b.row0;
-    load_tile<E, DP>(Q, a.q, row, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
-    load_tile<E, DP>(O, a.d_o, row, b.rows, b.head, a.dim, vec_rows<E>(a.d_o, a.dim));
-    float2 acc[4][DP / 32];
-    float lse[4], delta[4];
+    load_tile<E, DP, 16 * R>(Q, a.q, row, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
+    load_tile<E, DP, 16 * R>(O, a.d_o, row, b.rows, b.head, a.dim, vec_rows<E>(a.d_o, a.dim));
+    float2 acc[R][DP / 32];
+    float lse[R], delta[R];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int i = ty + 16 * r;
         const bool in = i < b.rows;
         lse[r] = in ? a.lse[b.head * a.tokens + row + i] * kLog2e : 0.0f;
@@ -294,17 +334,21 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         for (int k = 0; k < DP / 32; ++k) acc[r][k] = tc::both(0.0f);
     }
     const int end = a.causal ? b.row0 + b.rows : b.t.len;
+    Pair<E, DP> next;
+    const auto fetch = [&](int j0) {
+        next.fetch(a.k, a.v, b.t.begin + j0, min(T, b.t.len - j0), kv, a.dim, vk, vv);
+    };
     // p and dp of the keys from j0 on, 0 where a row sees none
-    const auto form = [&](int j0, float (&p)[4][4], float (&g)[4][4]) {
+    const auto form = [&](int j0, float (&p)[R][4], float (&g)[R][4]) {
         const int keys = min(T, b.t.len - j0);
         __syncthreads();
-        load_tile<E, DP>(K, a.k, b.t.begin + j0, keys, kv, a.dim, vk);
-        load_tile<E, DP>(V, a.v, b.t.begin + j0, keys, kv, a.dim, vv);
+        next.put(K, V, a.k, a.v, b.t.begin + j0, keys, kv, a.dim, vk, vv);
         __syncthreads();
+        if (j0 + T < end) fetch(j0 + T);
         product_nt<DP>(p, Q, K, dim4);
         product_nt<DP>(g, O, V, dim4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < R; ++r) {
             const int i = b.row0 + ty + 16 * r;
             const int seen = a.causal ? min(i + 1 - j0, keys) : keys;
 #pragma unroll
@@ -319,50 +363,53 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         // delta = sum p dp, in a pass of its own: do . o would hold the rounding of o to
         // bf16, which shows where few keys count (dp - delta is then small beside dp)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) delta[r] = 0.0f;
+        for (int r = 0; r < R; ++r) delta[r] = 0.0f;
+        fetch(0);
         for (int j0 = 0; j0 < end; j0 += T) {
-            float p[4][4], g[4][4];
+            float p[R][4], g[R][4];
             form(j0, p, g);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) delta[r] = fmaf(p[r][c], g[r][c], delta[r]);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < R; ++r) {
             delta[r] = row_sum(delta[r]);
             const int i = ty + 16 * r;
             if (tx == 0 && i < b.rows) a.delta[b.head * a.tokens + row + i] = delta[r];
         }
     }
+    fetch(0);
     for (int j0 = 0; j0 < end; j0 += T) {
-        float p[4][4], g[4][4];
+        float p[R][4], g[R][4];
         form(j0, p, g);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) P[(ty + 16 * r) * LP + tx + 16 * c] = p[r][c] * (g[r][c] - delta[r]);
         __syncwarp();
         product_nn<DP>(acc, P, K);
     }
-    const float f[4] = {a.scale, a.scale, a.scale, a.scale};
+    float f[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) f[r] = a.scale;
     store_rows<E, DP>(a.out, acc, f, row, b.rows, a.heads, b.head, a.dim);
 }
 
 template <typename E, int DP>
-__global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void dkv_block(const AttnArgs& a, unsigned index, float* sm) {
     constexpr int LD = DP + 4;
-    extern __shared__ float sm[];
     float *K = sm, *V = K + T * LD, *Q = V + T * LD, *O = Q + T * LD, *P = O + T * LD, *G = P + T * LP;
     Block b;
-    const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.parts));
-    const unsigned block = blockIdx.x / static_cast<unsigned>(a.parts);
+    const int part = static_cast<int>(index % static_cast<unsigned>(a.parts));
+    const unsigned block = index / static_cast<unsigned>(a.parts);
     float *pk = nullptr, *pv = nullptr;  // this part's sums, where parts share the tile
     if (a.parts > 1) {
         pk = attn_partial(a, 0, part);
         pv = attn_partial(a, 1, part);
-        if (!take_block(a, block, a.kv_heads, false, pk, pv, nullptr, b)) return;
-    } else if (!take_block(a, block, a.kv_heads, false, static_cast<E*>(a.dk), static_cast<E*>(a.dv), nullptr, b)) {
+        if (!take_block<T>(a, block, a.kv_heads, false, pk, pv, nullptr, b)) return;
+    } else if (!take_block<T>(a, block, a.kv_heads, false, static_cast<E*>(a.dk), static_cast<E*>(a.dv), nullptr, b)) {
         return;
     }
     const int dim4 = (a.dim + 3) / 4 * 4, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -381,9 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
     for (int step = attn_part(steps, part, a.parts); step < end; ++step) {
         const int h = step / per_head, head = b.head * a.group + h, i0 = first + (step - h * per_head) * T;
         const int queries = min(T, b.t.len - i0);
+        Pair<E, DP> tiles;
+        tiles.fetch(a.q, a.d_o, b.t.begin + i0, queries, head, a.dim, vq, vo);
         __syncthreads();
-        load_tile<E, DP>(Q, a.q, b.t.begin + i0, queries, head, a.dim, vq);
-        load_tile<E, DP>(O, a.d_o, b.t.begin + i0, queries, head, a.dim, vo);
+        tiles.put(Q, O, a.q, a.d_o, b.t.begin + i0, queries, head, a.dim, vq, vo);
         __syncthreads();
         float s[4][4], g[4][4];
         product_nt<DP>(s, K, Q, dim4);
@@ -415,6 +463,19 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
     }
     store_rows<E, DP>(a.dv, dv, one, row, b.rows, a.kv_heads, b.head, a.dim);
     store_rows<E, DP>(a.dk, dk, f, row, b.rows, a.kv_heads, b.head, a.dim);
+}
+
+// `keys` blocks for dk and dv, and behind them those for dq, 16 R queries each.
+template <typename E, int DP, int R>
+__global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_constant__ AttnArgs a, unsigned keys) {
+    extern __shared__ float sm[];
+    if (blockIdx.x < keys) {
+        dkv_block<E, DP>(a, blockIdx.x, sm);
+        return;
+    }
+    AttnArgs q = a;
+    q.slots = a.query_slots;
+    dq_block<E, DP, R>(q, blockIdx.x - keys, sm);
 }
 
 // dk (y = 0) and dv (1) from the partial sums of a.parts blocks, N elements a thread.
@@ -524,20 +585,27 @@ cudaError_t run_delta(const AttnArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-constexpr size_t tiles_bytes(int tiles, int squares, int dp) {
-    return static_cast<size_t>(tiles * T * (dp + 4) + squares * T * LP) * sizeof(float);
+// Shared memory: `rows` rows of queries (and of gradients), `tiles` tiles of T rows, and
+// `squares` x T logits' rows of stride LP.
+constexpr size_t tiles_bytes(int rows, int tiles, int squares, int dp) {
+    return static_cast<size_t>((rows + tiles * T) * (dp + 4) + squares * LP) * sizeof(float);
+}
+template <int DP, int R>
+constexpr size_t kForwardBytes = tiles_bytes(16 * R, 2, 16 * R, DP);
+template <int DP>
+constexpr size_t kBackwardBytes = tiles_bytes(0, 4, 2 * T, DP);  // of the keys' blocks; the queries' take less
+
+template <typename K>
+cudaError_t allow(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
 template <typename E, int DP>
 cudaError_t attributes() {
-    cudaError_t e = cudaFuncSetAttribute(forward_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(tiles_bytes(3, 1, DP)));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(dq_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(tiles_bytes(4, 1, DP)));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(dkv_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(tiles_bytes(4, 2, DP)));
+    cudaError_t e = allow(forward_kernel<E, DP, 4>, kForwardBytes<DP, 4>);
+    if (e == cudaSuccess) e = allow(forward_kernel<E, DP, 2>, kForwardBytes<DP, 2>);
+    if (e == cudaSuccess) e = allow(backward_kernel<E, DP, 4>, kBackwardBytes<DP>);
+    if (e == cudaSuccess) e = allow(backward_kernel<E, DP, 2>, kBackwardBytes<DP>);
     return e;
 }
 
@@ -557,23 +625,41 @@ cudaError_t prepare() {
     });
 }
 
-template <typename E, int DP>
+// Blocks of 32 queries where those of 64 leave SMs without one: each then takes half
+// as long (777 tokens, 6 / 2 heads of 80: forward 54 -> XX us, dq YY -> ZZ us).
+bool half_blocks(const AttnArgs& a) { return (a.tokens / T + 1) * a.heads < 2 * 152; }
+
+template <typename E, int DP, int R>
 cudaError_t forward(AttnArgs a, cudaStream_t s) {
-    a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, T));
+    a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, 16 * R));
     const unsigned grid = static_cast<unsigned>(a.slots + a.fill) * a.heads;
-    forward_kernel<E, DP><<<grid, kThreads, tiles_bytes(3, 1, DP), s>>>(a);
+    forward_kernel<E, DP, R><<<grid, kThreads, kForwardBytes<DP, R>, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename E, int DP>
+cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
+    return half_blocks(a) ? forward<E, DP, 2>(a, s) : forward<E, DP, 4>(a, s);
+}
+
+template <typename E, int DP, int R>
 cudaError_t backward(AttnArgs a, cudaStream_t s) {
     a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, T));
-    const unsigned rows = static_cast<unsigned>(a.slots + a.fill);
-    dq_kernel<E, DP><<<rows * a.heads, kThreads, tiles_bytes(4, 1, DP), s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    dkv_kernel<E, DP><<<rows * a.kv_heads * a.parts, kThreads, tiles_bytes(4, 2, DP), s>>>(a);
-    return cudaGetLastError();
+    a.query_slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, 16 * R));
+    const unsigned keys = static_cast<unsigned>(a.slots + a.fill) * a.kv_heads * a.parts;
+    const unsigned queries = static_cast<unsigned>(a.query_slots + a.fill) * a.heads;
+    const auto run = [&](unsigned k, unsigned q) {
+        backward_kernel<E, DP, R><<<k + q, kThreads, kBackwardBytes<DP>, s>>>(a, k);
+        return cudaGetLastError();
+    };
+    if (sizeof(E) == 4) return run(keys, queries);
+    const cudaError_t e = run(0, queries);  // makes the delta that the other reads
+    return e == cudaSuccess ? run(keys, 0) : e;
+}
+
+template <typename E, int DP>
+cudaError_t backward(const AttnArgs& a, cudaStream_t s) {
+    return half_blocks(a) ? backward<E, DP, 2>(a, s) : backward<E, DP, 4>(a, s);
 }
 
 }  // namespace
