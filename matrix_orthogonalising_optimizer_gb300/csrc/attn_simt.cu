@@ -6,12 +6,16 @@
 //   ds_ij = p_ij (do_i v_j - delta_i),  delta_i = do_i o_i
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
 //
-// One pass over the keys per 64 queries with the running maximum and sum of the
+// One pass over the keys per 64 (or 32) queries with the running maximum and sum of the
 // softmax; the backward pass takes p from lse, once per 64 queries for dq and once
 // per 64 keys for dk and dv (summed over the query heads that share the key head), so
 // every sum has one owner and a fixed order.  A block of 256 threads forms 64 x 64
 // products, 4 x 4 per thread; all tiles lie row by row in shared memory as fp32,
 // dim + 4 floats apart: 16-byte reads of eight rows then cover all banks.
+//
+// Bound: FFMA issue and the latency of few warps (one block per SM: 128 KB and more of
+// tiles, 200 registers).  Measured in fp32: 2048 tokens, 16 heads of 64, causal: forward 266 us
+// (16 TFLOP/s), backward 838 us (26); 777 tokens, 6 / 2 heads of 80: 45 and 83 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -541,7 +545,9 @@ __global__ void __launch_bounds__(256) delta_vector_kernel(const __grid_constant
             o[u] = d[u] = make_uint4(0, 0, 0, 0);
             at[u] = -1;
             if (r >= rows) continue;
-            const int64_t token = r / a.heads, head = r - token * a.heads;
+            // a 64-bit division would take longer than the row
+            const int64_t token = rows >> 32 ? r / a.heads : static_cast<uint32_t>(r) / static_cast<uint32_t>(a.heads);
+            const int64_t head = r - token * a.heads;
             at[u] = head * a.tokens + token;
             if (c >= a.dim) continue;
             o[u] = *reinterpret_cast<const uint4*>(static_cast<const E*>(a.o) + r * a.dim + c);
@@ -625,9 +631,11 @@ cudaError_t prepare() {
     });
 }
 
-// Blocks of 32 queries where those of 64 leave SMs without one: each then takes half
-// as long (777 tokens, 6 / 2 heads of 80: forward 54 -> XX us, dq YY -> ZZ us).
-bool half_blocks(const AttnArgs& a) { return (a.tokens / T + 1) * a.heads < 2 * 152; }
+// Blocks of 32 queries where those of 64 leave SMs without one: each then takes less time,
+// if not half.  Measured in fp32, 64 -> 32 queries, forward | backward: 777 tokens, 6 / 2
+// heads of 80 (90 blocks of 64) 53 -> 45 us | 96 -> 83; 1024 tokens, 8 heads of 128 (136) 131 -> 111 |
+// 317 -> 279; 12 heads of 64 (204) 78 -> 90 | 214 -> 233.
+bool half_blocks(const AttnArgs& a) { return (a.tokens / T + 1) * a.heads < 152; }
 
 template <typename E, int DP, int R>
 cudaError_t forward(AttnArgs a, cudaStream_t s) {
