@@ -25,6 +25,8 @@
 // (1.35 ms = 1.63 in a loop, under the power cap).  Heads of 64: the softmax (12 heads, 8192 tokens: 107 us,
 // 0.97 PFLOP/s).  Short sequences: start and end of a CTA, about 3 us (23 ragged ones of 356
 // tokens, 12 heads of 64: 32 us).
+#include <cstddef>
+
 #include "attn_tc.cuh"
 #include "internal.h"
 #include "ops.h"
@@ -47,6 +49,14 @@ struct Cfg {
     static constexpr int kRegsLow = 56, kRegsSoft = NT == 2 ? 224 : 200;  // shares of 168 x 3 or 128 x 2
 };
 
+// What a CTA does next.
+enum Kind : int32_t { TILE, CLEAR, NONE };
+
+struct Item {
+    int32_t kind, head;
+    int32_t begin, len, tile;  // of the sequence, as AttnTile; CLEAR: tile is the share
+};
+
 template <int DP, int NT>
 struct __align__(1024) Smem {
     using C = Cfg<DP, NT>;
@@ -61,9 +71,11 @@ struct __align__(1024) Smem {
     uint64_t pv_done[NT][2];  // products of the even and the odd key tiles
     uint64_t o_full[NT];
     uint64_t drained;
-    AttnTile tile;
+    uint4 claim;                // answer to the request for another block's index
+    uint64_t claimed;
+    Item item[2];               // at hand, and the next
     uint32_t tmem;
-    int32_t any;
+    int32_t bad;                // a wait gave up
 };
 
 // The products of a CTA, in the order in which the tensor cores run them: unit u is key
@@ -92,67 +104,79 @@ __device__ __forceinline__ int place(bool v, int j, int steps) {
 // Growth of a row's maximum, in powers of two, that is left in p.
 constexpr float kLazy = 8.0f;
 
+// The item of a block index.  False: its slot holds no tile.
+template <int NT>
+__device__ __forceinline__ bool find_item(const AttnArgs& a, unsigned block, Item& item) {
+    const unsigned slot = block / static_cast<unsigned>(a.heads);
+    item = Item{CLEAR, static_cast<int>(block - slot * a.heads), 0, 0, static_cast<int>(slot) - a.slots};
+    if (static_cast<int>(slot) >= a.slots) return true;
+    AttnTile t;
+    if (!attn_find(a, static_cast<int>(slot), NT * kRows, t)) return false;
+    item = Item{TILE, item.head, static_cast<int32_t>(t.begin), t.len, t.tile};
+    return true;
+}
+
+// The next item, by one warp: a CTA that has come to its end takes the place of a block
+// that has not started yet (cluster launch control), so that shared memory, TMEM and
+// barriers are set up once and the order stays that of the grid.  `asked` counts the
+// requests; none follows one that failed.
 template <int DP, int NT>
-__global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
-    forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
-                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+__device__ __forceinline__ Item next_item(const AttnArgs& a, Smem<DP, NT>& S, uint32_t& asked, int lane) {
+    Item item;
+    for (;;) {
+        if (lane == 0) {
+            mbar_expect_tx(&S.claimed, 16);
+            asm volatile(
+                "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                    saddr(&S.claim)),
+                "r"(saddr(&S.claimed))
+                : "memory");
+        }
+        __syncwarp();
+        const bool there = __all_sync(kFullMask, mbar_wait<false>(&S.claimed, asked & 1, &S.bad));
+        ++asked;
+        uint32_t got = 0, block = 0;
+        if (there)
+            asm volatile(
+                "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+                "ld.shared.b128 h, [%2];\n\t"
+                "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t"
+                "mov.u32 %1, 0;\n\t"
+                "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+                : "=r"(got), "=r"(block)
+                : "r"(saddr(&S.claim))
+                : "memory");
+        // the answer is read before the next one may come
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        item = Item{NONE, 0, 0, 0, 0};
+        if (__shfl_sync(kFullMask, got, 0) == 0) return item;
+        if (find_item<NT>(a, __shfl_sync(kFullMask, block, 0), item)) return item;
+    }
+}
+
+// One barrier a lane and turn, in the order of Smem.
+template <int DP, int NT>
+__device__ __forceinline__ void init_barriers(Smem<DP, NT>& S, int lane, bool again) {
+    using C = Cfg<DP, NT>;
+    using M = Smem<DP, NT>;
+    constexpr int n = static_cast<int>((offsetof(M, drained) - offsetof(M, q_full)) / 8) + 1;
+    for (int k = lane; k < n; k += 32) {
+        uint64_t* bar = &S.q_full + k;
+        if (again) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+        mbar_init(bar, bar >= S.p_half && bar < S.p_ready + C::kBuffers ? 4 : 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// A tile's output, by the helper warps (kSoft false) or those of the softmax.
+template <int DP, int NT, bool kSoft>
+__device__ __forceinline__ void run_tile(const AttnArgs& a, Smem<DP, NT>& S, const CUtensorMap* mq, const CUtensorMap* mk,
+                                         const CUtensorMap* mv, const AttnTile& t, int head, int warp, int lane,
+                                         uint32_t tmem) {
     using C = Cfg<DP, NT>;
     constexpr int NS = C::kStages, NB = C::kBuffers;
-    extern __shared__ uint8_t raw[];
-    Smem<DP, NT>& S = *reinterpret_cast<Smem<DP, NT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-
-    const int slot = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.heads));
-    const int head = static_cast<int>(blockIdx.x - static_cast<unsigned>(slot) * a.heads);
-    if (slot >= a.slots) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, head, slot - a.slots, threadIdx.x, blockDim.x);
-        return;
-    }
-    if (warp == 1) {
-        tmem_alloc<C::kCols>(&S.tmem);
-    } else if (warp == 2 && lane == 0) {
-        mbar_init(&S.q_full, 1);
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&S.full[i], 1);
-            mbar_init(&S.empty[i], 1);
-        }
-        for (int i = 0; i < NB; ++i) {
-            mbar_init(&S.s_full[i], 1);
-            mbar_init(&S.p_half[i], 4);
-            mbar_init(&S.p_ready[i], 4);
-        }
-        for (int i = 0; i < NT; ++i) {
-            mbar_init(&S.pv_done[i][0], 1);
-            mbar_init(&S.pv_done[i][1], 1);
-            mbar_init(&S.o_full[i], 1);
-        }
-        mbar_init(&S.drained, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    } else if (warp == 0) {
-        // meanwhile, and only after the kernels before have finished
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        AttnTile found;
-        const bool any = attn_find(a, slot, NT * kRows, found);
-        if (lane == 0) {
-            S.tile = found;
-            S.any = any;
-        }
-    }
-    fence_before();
-    __syncthreads();
-    fence_after();
-    // from one lane: uniform, as MMAs and copies take their operands
-    const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);
-    const bool any = __shfl_sync(kFullMask, S.any, 0) != 0;
-    AttnTile t;
-    t.begin = __shfl_sync(kFullMask, static_cast<int32_t>(S.tile.begin), 0);
-    t.len = __shfl_sync(kFullMask, S.tile.len, 0);
-    t.tile = __shfl_sync(kFullMask, S.tile.tile, 0);
-    if (!any) {
-        if (warp == 1) tmem_free<C::kCols>(tmem);
-        return;
-    }
     // the tiles with most keys first
     const int row0 = (a.causal ? (t.len - 1) / (NT * kRows) - t.tile : t.tile) * NT * kRows;
     const int token0 = static_cast<int>(t.begin);
@@ -170,20 +194,19 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
 
     const uint32_t t_s = tmem, t_o = tmem + NB * kRows;
 
-    if (warp < kSoftWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLow));
+    if constexpr (!kSoft) {
         if (warp == 0) {
             // ------------------------------------------------ loads
             const uint32_t e = elect_one();
             mbar_expect_tx_if(e, &S.q_full, (units.n[1] > 0 ? 2 : 1) * kTile<DP>);
             for (int i = 0; i < NT; ++i)
                 if (units.n[i] > 0)
-                    load_tile<DP>(e, saddr(S.q[i]), &mq, saddr(&S.q_full), head, token0 + row0 + i * kRows);
+                    load_tile<DP>(e, saddr(S.q[i]), mq, saddr(&S.q_full), head, token0 + row0 + i * kRows);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int i = 0; i < 2 * steps && ok; ++i) {
-                if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[stage], phase ^ 1, &g_status))) {
+                if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[stage], phase ^ 1, &S.bad))) {
                     ok = false;
                     break;
                 }
@@ -194,7 +217,7 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
                     tile = i + 1 == 2 * steps ? steps - 1 : v ? i / 2 - 1 : (i + 1) / 2;
                 }
                 mbar_expect_tx_if(e, &S.full[stage], kTile<DP>);
-                load_tile<DP>(e, saddr(S.kv[stage]), v ? &mv : &mk, saddr(&S.full[stage]), head / a.group,
+                load_tile<DP>(e, saddr(S.kv[stage]), v ? mv : mk, saddr(&S.full[stage]), head / a.group,
                               token0 + tile * kRows);
                 if (++stage == NS) {
                     stage = 0;
@@ -207,7 +230,7 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
             const uint32_t q0 = saddr(S.q[0]), kv0 = saddr(S.kv[0]);
             const int total = units.count();
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &g_status));
+                const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &S.bad));
                 fence_after();
                 return r;
             };
@@ -244,10 +267,9 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
             }
             // also after a wait that gave up: no MMA or commit is under way when the CTA leaves
             umma_commit(e, saddr(&S.drained));
-            mbar_wait<false>(&S.drained, 0, &g_status);
+            mbar_wait<false>(&S.drained, 0, &S.bad);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
         // ------------------------------------------------ softmax
         const int tile = (warp - kSoftWarp0) / 4, quarter = warp % 4, thread = threadIdx.x % 128;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -255,7 +277,7 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
         const int row = row0 + tile * kRows + thread;
         const int count = tile ? units.n[1] : units.n[0];
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
-            const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &g_status));
+            const bool r = __all_sync(kFullMask, mbar_wait<false>(bar, parity, &S.bad));
             fence_after();
             return r;
         };
@@ -345,8 +367,83 @@ __global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
             if (row < t.len) a.lse[head * a.tokens + token] = (base + log2f(sum)) * 0.6931471805599453f;
         }
     }
+}
+
+// All items of a CTA.
+template <int DP, int NT, bool kSoft>
+__device__ __forceinline__ void work(const AttnArgs& a, Smem<DP, NT>& S, const CUtensorMap* mq, const CUtensorMap* mk,
+                                     const CUtensorMap* mv, int warp, int lane, uint32_t tmem) {
+    uint32_t asked = 0;
+    for (int n = 0;; ++n) {
+        const Item& now = S.item[n & 1];
+        // from one lane: uniform, as MMAs and copies take their operands
+        const int kind = __shfl_sync(kFullMask, now.kind, 0), head = __shfl_sync(kFullMask, now.head, 0);
+        AttnTile t;
+        t.begin = __shfl_sync(kFullMask, now.begin, 0);
+        t.len = __shfl_sync(kFullMask, now.len, 0);
+        t.tile = __shfl_sync(kFullMask, now.tile, 0);
+        if (kind == NONE) return;
+        if (kind == TILE) {
+            run_tile<DP, NT, kSoft>(a, S, mq, mk, mv, t, head, warp, lane, tmem);
+        } else if (kSoft) {
+            attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, head, t.tile,
+                       threadIdx.x - 32 * kSoftWarp0, 128 * NT);
+        }
+        if (!kSoft && warp == 0) {
+            // after this item's last loads are issued
+            const Item item = next_item<DP, NT>(a, S, asked, lane);
+            if (lane == 0) S.item[(n + 1) & 1] = item;
+        }
+        // shared memory, TMEM and barriers pass to the next item
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_before();
+        __syncthreads();
+        if (__shfl_sync(kFullMask, S.bad, 0) != 0) return;
+        if (!kSoft && warp == 2) init_barriers(S, lane, true);
+        __syncthreads();
+        fence_after();
+    }
+}
+
+template <int DP, int NT>
+__global__ void __launch_bounds__(Cfg<DP, NT>::kThreads, NT == 1 ? 2 : 1)
+    forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
+                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using C = Cfg<DP, NT>;
+    extern __shared__ uint8_t raw[];
+    Smem<DP, NT>& S = *reinterpret_cast<Smem<DP, NT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const int warp = __shfl_sync(kFullMask, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    if (warp == 1) {
+        tmem_alloc<C::kCols>(&S.tmem);
+    } else if (warp == 2) {
+        init_barriers(S, lane, false);
+    } else if (warp == 0) {
+        if (lane == 0) {
+            mbar_init(&S.claimed, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            S.bad = 0;
+        }
+        // meanwhile, and only after the kernels before have finished
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        Item item;
+        // (a block without a tile ends here: its successor is another block of the grid)
+        if (!find_item<NT>(a, blockIdx.x, item)) item.kind = NONE;
+        if (lane == 0) S.item[0] = item;
+    }
     fence_before();
     __syncthreads();
+    fence_after();
+    const uint32_t tmem = __shfl_sync(kFullMask, S.tmem, 0);
+    if (warp < kSoftWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLow));
+        work<DP, NT, false>(a, S, &mq, &mk, &mv, warp, lane, tmem);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
+        work<DP, NT, true>(a, S, &mq, &mk, &mv, warp, lane, tmem);
+    }
+    fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && S.bad) atomicExch(&g_status, 1);
     if (warp == 1) {
         __syncwarp();
         fence_after();
