@@ -125,7 +125,6 @@ int parts_of(int64_t sequences, int64_t tokens, int64_t heads, int64_t kv_heads,
 struct Layout {
     float* delta = nullptr;
     float* partial = nullptr;
-    unsigned* counter = nullptr;
     int parts = 1;
     size_t bytes = 0;
     // the workspace serves either kind of kernels, causal or not
@@ -133,7 +132,6 @@ struct Layout {
         Arena a{base};
         if (backward) {
             delta = a.take<float>(tokens * heads);
-            counter = a.take<unsigned>(2);
             for (int k = 0; k < 4; ++k)
                 parts = std::max(parts, parts_of(sequences, tokens, heads, kv_heads, (k & 1) != 0, (k & 2) != 0));
             if (parts > 1) partial = a.take<float>(2 * parts * tokens * kv_heads * dim);
@@ -211,8 +209,8 @@ extern "C" int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_he
     const bool tc = tensor_cores(a, dtype, true);
     a.parts = parts_of(sequences, tokens, heads, kv_heads, a.causal != 0, tc);
     a.partial = L.partial;
-    a.counter = L.counter;
-    if (tc || f32) OPS_CUDA(attn_delta(a, f32, s));  // bf16 rows of the FFMA kernels: made there
+    // (bf16 rows of the FFMA kernels and sequences of one tile: made there)
+    if (tc ? attn_tc_needs_delta(a) : f32) OPS_CUDA(attn_delta(a, f32, s));
     if (tc) {
         AttnMaps m = {};
         OPS_TRY(set_maps(m, a));

@@ -33,7 +33,6 @@ struct AttnArgs {
     int32_t fill;              // blocks behind them that clear the rows of no sequence
     int32_t whole;             // backward, tensor cores: sequences, where those of one tile have their own launch
     int32_t parts;             // backward: blocks that share the queries of a key tile
-    unsigned* counter;         // backward, tensor cores: [2] items taken; cleared with delta
     float* partial;            // parts > 1: [2][parts][tokens][kv_heads][dim] sums of dk (unscaled) and dv
     float scale, scale_log2;   // scale_log2 = scale * log2(e)
 };
@@ -106,6 +105,7 @@ struct AttnMaps {
     CUtensorMap q, k, v, d_o;  // dim x heads x tokens, boxes of 64 x 1 x 128
 };
 cudaError_t attn_tc_forward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s);
+bool attn_tc_needs_delta(const AttnArgs& a);  // some sequence may be longer than one tile
 cudaError_t attn_tc_backward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s);
 cudaError_t attn_fwd_status_word(void** p);  // the kernels' time-out flags on the current device
 cudaError_t attn_bwd_status_word(void** p);

@@ -511,7 +511,6 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
 // delta = do . o, one warp per row.  Rows of no sequence are never read later.
 template <typename E>
 __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttnArgs a) {
-    if (a.counter && blockIdx.x == 0 && threadIdx.x < 2) a.counter[threadIdx.x] = 0;
     const int64_t rows = a.tokens * a.heads;
     const int lane = threadIdx.x % 32;
     for (int64_t r = blockIdx.x * 8ll + threadIdx.x / 32; r < rows; r += gridDim.x * 8ll) {
@@ -531,7 +530,6 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Attn
 // do, four rows' loads in flight (134 MB at 8192 tokens, 32 heads of 128: 48 -> 24 us).
 template <typename E, int G>
 __global__ void __launch_bounds__(256) delta_vector_kernel(const __grid_constant__ AttnArgs a) {
-    if (a.counter && blockIdx.x == 0 && threadIdx.x < 2) a.counter[threadIdx.x] = 0;
     constexpr int N = 16 / sizeof(E), R = 32 / G, U = 4;
     const int64_t rows = a.tokens * a.heads;
     const int lane = threadIdx.x % 32, c = lane % G * N;

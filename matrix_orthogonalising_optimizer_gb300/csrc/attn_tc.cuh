@@ -89,6 +89,42 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int first, int thread,
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// A CTA that has come to its end takes the place of a block that has not started yet
+// (cluster launch control): shared memory, TMEM and barriers are set up once, and the
+// order stays that of the grid.  By one warp: false if all blocks have started; `asked`
+// counts the requests on `claimed` (one arrival), and none may follow one that failed.
+__device__ __forceinline__ bool claim_block(uint4* claim, uint64_t* claimed, uint32_t& asked, uint32_t& block,
+                                            int32_t* bad, int lane) {
+    if (lane == 0) {
+        mbar_expect_tx(claimed, 16);
+        asm volatile(
+            "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                saddr(claim)),
+            "r"(saddr(claimed))
+            : "memory");
+    }
+    __syncwarp();
+    const bool there = __all_sync(kFullMask, mbar_wait<false>(claimed, asked & 1, bad));
+    ++asked;
+    uint32_t got = 0, index = 0;
+    if (there)
+        asm volatile(
+            "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+            "ld.shared.b128 h, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t"
+            "mov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+            : "=r"(got), "=r"(index)
+            : "r"(saddr(claim))
+            : "memory");
+    // the answer is read before the next one may come
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    block = __shfl_sync(kFullMask, index, 0);
+    return __shfl_sync(kFullMask, got, 0) != 0;
+}
+
 template <int kCols>
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(slot)), "n"(kCols)

@@ -9,8 +9,9 @@
 // fixed order -- no atomics, no fp32 partial sums through L2 --, and p and ds never
 // pass through shared memory: the side of the keys works on s^T = k q^T, whose rows
 // are what dv and dk need as the left operand in TMEM, the side of the queries on s.
-// Both kinds of tile are items of one persistent launch, taken from a counter: one fills
-// the other's last wave, and the start of a CTA is paid once.
+// Both kinds of tile are blocks of one launch, so that one fills the other's last wave, and
+// a CTA that has come to its end takes over the next block that has not started, without
+// another set-up.
 //
 // Keys: TMEM holds s^T and dp^T (p^T and ds^T take their place, bf16), dv and dk.  The
 // tensor cores run dv_i, s_{i+1}, dk_i, dp_{i+1}: the exponentials of tile i + 1 fall
@@ -23,13 +24,12 @@
 // Bound: the tensor cores.  Per pair of 128-token tiles 7 * 512 cycles at dim = 128;
 // measured about 2300 a step of the keys (2048 of MMAs) and 1850 of the queries (1536), and 3
 // to 6 us a tile besides.  8192 tokens, 32/8 heads of 128, causal: 1.07 ms with delta,
-// 1.29 PFLOP/s of the five products, 1.80 of the seven; five documents packed into 8192
-// tokens 0.40 ms; 12 heads of 64 0.32 ms (element-wise work and hand-overs).
+// 1.28 PFLOP/s of the five products, 1.80 of the seven; five documents packed into 8192
+// tokens 0.39 ms; 12 heads of 64 0.32 ms (element-wise work and hand-overs).
 //
 // Warp 0 loads and looks for the next item, warp 1 issues the MMAs, warp 2 fetches lse and
 // delta of the query tiles (side of the keys), warps 4 to 11 do the element-wise work, half of the columns
 // each warpgroup.
-#include <algorithm>
 #include <cstddef>
 
 #include "attn_tc.cuh"
@@ -77,6 +77,8 @@ struct __align__(1024) Smem {
     uint64_t stat_full[2];
     uint64_t stat_empty[2];
     uint64_t done;
+    uint4 claim;                // answer to the request for another block's index
+    uint64_t claimed;
     Item item[2];               // at hand, and the next
     uint32_t tmem;
     int32_t bad;                // a wait gave up
@@ -650,23 +652,18 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
 
 // The next of the launch's items that has something to do, by one warp: side of the keys,
 // then of the queries, each with the heavy ones first, or (kWhole) sequences of one tile.
-// A CTA begins with its own index and takes the others from a counter.
-template <bool kWhole>
-__device__ __forceinline__ Item next_item(const AttnArgs& a, bool first, int lane) {
+// A CTA begins with its own block index and then takes those of blocks not yet started.
+template <int DP, bool kWhole>
+__device__ __forceinline__ Item next_item(const AttnArgs& a, Smem<DP>& S, bool first, uint32_t& asked, int lane) {
     // tiles of the keys, tiles of the queries, rows to clear (in the only launch, or this one)
     const unsigned tiles = kWhole ? a.whole : a.slots, fill = kWhole && a.slots > 0 ? 0 : a.fill;
     const unsigned keys_end = tiles * a.kv_heads * a.parts, tiles_end = keys_end + (kWhole ? 0 : tiles * a.heads);
-    const unsigned clear_end = tiles_end + fill * a.kv_heads * a.parts, end = clear_end + fill * a.heads;
+    const unsigned clear_end = tiles_end + fill * a.kv_heads * a.parts;
     Item item;
-    for (;; first = false) {
+    for (;;) {
         unsigned n = blockIdx.x;
-        if (!first) {
-            unsigned taken = 0;
-            if (lane == 0) taken = atomicAdd(a.counter + (kWhole ? 1 : 0), 1u);
-            n = gridDim.x + __shfl_sync(kFullMask, taken, 0);
-        }
+        if (!first && !claim_block(&S.claim, &S.claimed, asked, n, &S.bad, lane)) return Item{NONE, 0, 0, 0, 0, 0};
         item = Item{NONE, 0, 0, 0, 0, 0};
-        if (n >= end) return item;
         const bool clear = n >= tiles_end, keys = clear ? n < clear_end : n < keys_end;
         const unsigned heads = keys ? a.kv_heads : a.heads, parts = keys ? a.parts : 1;
         n -= clear ? (keys ? tiles_end : clear_end) : (keys ? 0 : keys_end);
@@ -689,7 +686,11 @@ __device__ __forceinline__ Item next_item(const AttnArgs& a, bool first, int lan
         } else {
             any = attn_find(a, static_cast<int>(slot), kRows, t) && (a.whole == 0 || t.len > kRows);
         }
-        if (!any) continue;
+        if (!any) {
+            // a block that has nothing to do ends: the next of the grid follows it
+            if (first) return Item{NONE, 0, 0, 0, 0, 0};
+            continue;
+        }
         item.begin = static_cast<int32_t>(t.begin);
         item.len = t.len;
         item.tile = t.tile;
@@ -716,6 +717,7 @@ __device__ __forceinline__ void init_barriers(Smem<DP>& S, int lane, bool again)
 template <int DP, bool kElt, bool kWhole>
 __device__ __forceinline__ void work(const AttnArgs& a, Smem<DP>& S, const CUtensorMap* mq, const CUtensorMap* mk,
                                      const CUtensorMap* mv, const CUtensorMap* mo, int warp, int lane, uint32_t tmem) {
+    uint32_t asked = 0;  // requests for another block's index
     for (int n = 0;; ++n) {
         const Item& next = S.item[n & 1];
         // from one lane: uniform, as MMAs and copies take their operands
@@ -747,7 +749,7 @@ __device__ __forceinline__ void work(const AttnArgs& a, Smem<DP>& S, const CUten
         if (!kElt && warp == 0) {
             // not before this item's last loads are issued: an item taken early would wait here
             // while other SMs run dry
-            const Item item = next_item<kWhole>(a, false, lane);
+            const Item item = next_item<DP, kWhole>(a, S, false, asked, lane);
             if (lane == 0) S.item[(n + 1) & 1] = item;
         }
         // shared memory, TMEM and barriers pass to the next item
@@ -780,11 +782,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc<kCols>(&S.tmem);
     } else if (warp == 2) {
         init_barriers(S, lane, false);
-        if (lane == 0) S.bad = 0;
     } else if (warp == 0) {
+        if (lane == 0) {
+            mbar_init(&S.claimed, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            S.bad = 0;
+        }
         // meanwhile, and only after the kernels before have finished
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        const Item item = next_item<kWhole>(a, true, lane);
+        uint32_t none = 0;
+        const Item item = next_item<DP, kWhole>(a, S, true, none, lane);  // asks for no other block
         if (lane == 0) S.item[0] = item;
     }
     fence_before();
@@ -815,29 +822,29 @@ cudaError_t attribute() {
                                 static_cast<int>(sizeof(Smem<DP>)));
 }
 
-// Shared-memory attributes of all instances, once per device, and the device's SMs.
-cudaError_t prepare(int* sms) {
+// Shared-memory attributes of all instances, once per device.
+cudaError_t prepare() {
     static PerDevice cache;
-    int dev = 0;
+    int dev = 0, ok = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return cache.get(dev, sms, [&](int* out) {
+    return cache.get(dev, &ok, [](int* out) {
+        *out = 1;
         cudaError_t r = attribute<64, false>();
         if (r == cudaSuccess) r = attribute<64, true>();
         if (r == cudaSuccess) r = attribute<128, false>();
         if (r == cudaSuccess) r = attribute<128, true>();
-        return r == cudaSuccess ? cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev) : r;
+        return r;
     });
 }
 
-// A persistent launch: a CTA per SM, fewer where there are fewer items.
 template <int DP, bool kWhole>
-cudaError_t launch(const AttnArgs& a, const AttnMaps& m, int64_t items, int sms, cudaStream_t s) {
+cudaError_t launch(const AttnArgs& a, const AttnMaps& m, int64_t items, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, sms)));
+    cfg.gridDim = dim3(static_cast<unsigned>(items));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Smem<DP>);
     cfg.stream = s;
@@ -851,14 +858,14 @@ cudaError_t launch(const AttnArgs& a, const AttnMaps& m, int64_t items, int sms,
 constexpr int kShortAverage = 512;
 
 template <int DP>
-cudaError_t run(AttnArgs a, const AttnMaps& m, int sms, cudaStream_t s) {
+cudaError_t run(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
     const int64_t longest = a.offsets ? a.tokens : a.length, average = a.offsets ? a.tokens / a.sequences : a.length;
     a.slots = longest <= kRows ? 0 : static_cast<int32_t>(attn_slots(a.tokens, a.sequences, kRows));
     a.whole = longest <= kRows || (a.offsets && average <= kShortAverage) ? a.sequences : 0;
     const int64_t keys = static_cast<int64_t>(a.kv_heads) * a.parts, both = a.heads + keys;
     cudaError_t e = cudaSuccess;
-    if (a.whole > 0) e = launch<DP, true>(a, m, a.whole * keys + (a.slots > 0 ? 0 : a.fill * both), sms, s);
-    if (e == cudaSuccess && a.slots > 0) e = launch<DP, false>(a, m, (a.slots + a.fill) * both, sms, s);
+    if (a.whole > 0) e = launch<DP, true>(a, m, a.whole * keys + (a.slots > 0 ? 0 : a.fill * both), s);
+    if (e == cudaSuccess && a.slots > 0) e = launch<DP, false>(a, m, (a.slots + a.fill) * both, s);
     return e;
 }
 
@@ -867,11 +874,12 @@ cudaError_t run(AttnArgs a, const AttnMaps& m, int sms, cudaStream_t s) {
 
 cudaError_t attn_bwd_status_word(void** p) { return cudaGetSymbolAddress(p, attn::g_status); }
 
+bool attn_tc_needs_delta(const AttnArgs& a) { return (a.offsets ? a.tokens : a.length) > attn::kRows; }
+
 cudaError_t attn_tc_backward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s) {
-    int sms = 0;
-    const cudaError_t e = attn::prepare(&sms);
+    const cudaError_t e = attn::prepare();
     if (e != cudaSuccess) return e;
-    return a.dim <= 64 ? attn::run<64>(a, m, sms, s) : attn::run<128>(a, m, sms, s);
+    return a.dim <= 64 ? attn::run<64>(a, m, s) : attn::run<128>(a, m, s);
 }
 
 }  // namespace dmuon

@@ -116,44 +116,14 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, unsigned block, Ite
     return true;
 }
 
-// The next item, by one warp: a CTA that has come to its end takes the place of a block
-// that has not started yet (cluster launch control), so that shared memory, TMEM and
-// barriers are set up once and the order stays that of the grid.  `asked` counts the
-// requests; none follows one that failed.
+// The next item, by one warp, from the blocks that have not started.
 template <int DP, int NT>
 __device__ __forceinline__ Item next_item(const AttnArgs& a, Smem<DP, NT>& S, uint32_t& asked, int lane) {
     Item item;
-    for (;;) {
-        if (lane == 0) {
-            mbar_expect_tx(&S.claimed, 16);
-            asm volatile(
-                "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                    saddr(&S.claim)),
-                "r"(saddr(&S.claimed))
-                : "memory");
-        }
-        __syncwarp();
-        const bool there = __all_sync(kFullMask, mbar_wait<false>(&S.claimed, asked & 1, &S.bad));
-        ++asked;
-        uint32_t got = 0, block = 0;
-        if (there)
-            asm volatile(
-                "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
-                "ld.shared.b128 h, [%2];\n\t"
-                "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t"
-                "mov.u32 %1, 0;\n\t"
-                "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-                : "=r"(got), "=r"(block)
-                : "r"(saddr(&S.claim))
-                : "memory");
-        // the answer is read before the next one may come
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        item = Item{NONE, 0, 0, 0, 0};
-        if (__shfl_sync(kFullMask, got, 0) == 0) return item;
-        if (find_item<NT>(a, __shfl_sync(kFullMask, block, 0), item)) return item;
-    }
+    uint32_t block = 0;
+    while (claim_block(&S.claim, &S.claimed, asked, block, &S.bad, lane))
+        if (find_item<NT>(a, block, item)) return item;
+    return Item{NONE, 0, 0, 0, 0};
 }
 
 // One barrier a lane and turn, in the order of Smem.
@@ -503,12 +473,10 @@ cudaError_t attn_tc_forward(const AttnArgs& a, const AttnMaps& m, cudaStream_t s
     if (e != cudaSuccess) return e;
     // One query tile per CTA, two CTAs per SM, where sequences are short: one CTA's start and
     // end fall under the other's work.  Long ones: two tiles that share the keys.  Measured,
-    // two tiles -> one (8192 tokens of equal sequences, 32/8 heads of 128 | 12 of 64):
-    //   100 tokens each 123 -> 84 us | 43 -> 33;  512: 90 -> 80;  1024: | 43 -> 43;
-    //   1640: 130 -> 125;  2048: 143 -> 143;  8192: 334 -> 342 | 107 -> 119
-    // And where two tiles would leave SMs without a CTA (2048 tokens, 8 heads of 128: 31 -> 29).
-    const int64_t length = a.tokens / a.sequences;
-    const bool one = length <= (a.dim <= 64 ? 512 : 1536) || (a.tokens + 255) / 256 * a.heads < 152;
+    // two tiles -> one (8192 tokens, 32/8 heads of 128 | 12 of 64), sequences of about
+    //   100 tokens 100 -> 76 us | 37 -> 29;  356: | 35 -> 37;  512: 82 -> 80;  1024: | 41 -> 41;
+    //   1640: 123 -> 127;  2048: 137 -> 146;  8192: 332 -> 358 | 104 -> 117
+    const bool one = a.tokens / a.sequences <= (a.dim <= 64 ? 256 : 1024);
     if (a.dim <= 64) return one ? attn::launch<64, 1>(a, m, s) : attn::launch<64, 2>(a, m, s);
     return one ? attn::launch<128, 1>(a, m, s) : attn::launch<128, 2>(a, m, s);
 }
