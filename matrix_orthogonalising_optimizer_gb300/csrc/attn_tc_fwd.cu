@@ -252,6 +252,9 @@ __device__ __forceinline__ void run_tile(const AttnArgs& a, Smem<DP, NT>& S, con
             return r;
         };
         const float c = a.scale_log2;
+        // rows behind the sequence belong to the next one: they have no say in when the
+        // others are rescaled, which shows in the last bits
+        const float lazy = row < t.len ? kLazy : __int_as_float(0x7f800000);
         float top = __int_as_float(0xff800000), base = 0.0f, sum = 0.0f;
         bool ok = true;
         for (int j = 0; j < count; ++j) {
@@ -277,7 +280,7 @@ __device__ __forceinline__ void run_tile(const AttnArgs& a, Smem<DP, NT>& S, con
             if (j == 0) {
                 top = grown;
                 base = exp_shift(top) * c;
-            } else if (__any_sync(kFullMask, (grown - top) * c > kLazy)) {
+            } else if (__any_sync(kFullMask, (grown - top) * c > lazy)) {
                 // (a row without a finite logit so far has added nothing)
                 const float fresh = exp_shift(grown) * c;
                 const float f = top == __int_as_float(0xff800000) ? 0.0f : ex2(base - fresh);

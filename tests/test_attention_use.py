@@ -129,6 +129,61 @@ def test_padding_does_not_change_results(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths", [(300, 400), (300, 3000), (100, 28)])
+def test_values_of_the_next_sequence_do_not_show(lengths, d, dtype):
+    # rows of the next sequence lie in the same tile; here their logits grow much faster
+    n = sum(lengths)
+    q, k, v, do, _ = inputs([0, n], n, 4, 2, d, dtype, False, n)
+    off = torch.tensor([0, lengths[0], n], device="cuda")
+    results = []
+    for f in (1.0, 40.0):
+        a = [x.clone() for x in (q, k, v, do)]
+        for x in a:
+            x[lengths[0]:] *= f
+        o, lse = pkg.attention(*a[:3], off)
+        first = (o, lse.T, *pkg.attention_backward(a[3], *a[:3], o, lse, off))
+        results.append([x[:lengths[0]].clone() for x in first])
+    assert same(*results)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 128, 40, 33])
+def test_heads_before_tokens(dim, dtype):
+    # heads x tokens x dim tensors read in place, and a single token with any stride
+    q, k, v, do, _ = inputs([0, 290], 290, 4, 2, dim, dtype, False, dim)
+    table, pos = pkg.rotary_table(290, dim // 2 * 2), torch.arange(290, device="cuda")
+
+    def turn(x):
+        return x.transpose(0, 1).contiguous().transpose(0, 1)
+
+    def all_of(q, k, v, do):
+        a, b = pkg.qk_norm_rotary(q, k, pos[:len(q)], table)
+        o, lse = pkg.attention(q, k, v)
+        return a, b, o, lse, *pkg.attention_backward(do, q, k, v, o, lse)
+
+    for n in (290, 1):
+        x = [y[:n].contiguous() for y in (q, k, v, do)]
+        assert same(all_of(*(turn(y) for y in x)), all_of(*x))
+    assert same(all_of(*(turn(y)[:1] for y in (q, k, v, do))), all_of(*x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_mostly_padding(dtype):
+    # one short sequence somewhere in many tokens, odd sizes: everything else is cleared
+    for n, h, kv, d, at in ((20001, 3, 1, 72, 7000), (9000, 2, 2, 7, 0), (5000, 8, 2, 128, 4990)):
+        q, k, v, do, out = inputs([at, at + 10], n, h, kv, d, dtype, False, n)
+        off = torch.tensor([at, at + 10], device="cuda")
+        o, lse = pkg.attention(q, k, v, off)
+        for x in (o, *pkg.attention_backward(do, q, k, v, o, lse, off)):
+            assert not x[out].any() and x[~out].any()
+        assert (lse[:, out] == NEG).all() and lse[:, ~out].isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_elements_past_two_to_the_31(dtype):
     # 2.3e9 elements: the last tokens alone, as part of the whole and by themselves (two sequences of more
     # than one tile: shorter ones take other kernels where the average length is short)
