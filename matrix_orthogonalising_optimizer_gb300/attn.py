@@ -167,6 +167,10 @@ def attention_workspace(tokens, heads, kv_heads, dim, dtype="bf16", sequences=1,
                                                            int(backward)))
 
 
+def _scale(scale, dim):
+    return max(dim, 1) ** -0.5 if scale is None else scale
+
+
 def _sequences(where, lead, offsets, dev):
     """Sequences of the batch: those of ``offsets``, or one per row of the dimensions before the last."""
     if offsets is None:
@@ -204,7 +208,7 @@ def attention(q, k, v, offsets=None, causal=True, scale=None, workspace=None, st
     wp, wb, _keep = _space(workspace, lambda: attention_workspace(tokens, heads, kv, dim, dt, sequences), dev)
     st = _lib.load().dmuon_attention_forward(hq, hk, hv, _ptr(offsets), sequences, o.data_ptr(), lse.data_ptr(), tokens,
                                              heads, kv, dim, _dtype(dt), int(causal),
-                                             dim ** -0.5 if scale is None else scale, wp, wb, s)
+                                             _scale(scale, dim), wp, wb, s)
     _lib.check(st, "dmuon_attention_forward")
     return o, lse
 
@@ -232,7 +236,7 @@ def attention_backward(do, q, k, v, o, lse, offsets=None, causal=True, scale=Non
     wp, wb, _keep = _space(workspace, lambda: attention_workspace(tokens, heads, kv, dim, dt, sequences, True), dev)
     st = _lib.load().dmuon_attention_backward(ho, hq, hk, hv, o.data_ptr(), lse.data_ptr(), _ptr(offsets), sequences,
                                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), tokens, heads, kv, dim,
-                                              _dtype(dt), int(causal), dim ** -0.5 if scale is None else scale, wp, wb,
+                                              _dtype(dt), int(causal), _scale(scale, dim), wp, wb,
                                               s)
     _lib.check(st, "dmuon_attention_backward")
     return dq, dk, dv

@@ -12,10 +12,14 @@ namespace {
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxSequences = int64_t(1) << 20;
 constexpr int kMaxHeads = 1024, kMaxDim = 128;
+// Blocks of a launch: 2^31 - 1, less those that clear rows.  (Key tiles shared by several
+// blocks make fewer: there are at most 121 sequences then.)
+constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 256;
 
 bool sizes_ok(int64_t tokens, int64_t sequences, int64_t heads, int64_t kv_heads, int64_t dim) {
     return in_range(tokens, 0, kMaxTokens) && in_range(sequences, 1, kMaxSequences) && in_range(heads, 1, kMaxHeads) &&
-           in_range(kv_heads, 1, heads) && heads % kv_heads == 0 && in_range(dim, 1, kMaxDim);
+           in_range(kv_heads, 1, heads) && heads % kv_heads == 0 && in_range(dim, 1, kMaxDim) &&
+           (tokens / 32 + sequences) * (heads + kv_heads) < kMaxBlocks;
 }
 
 int set_heads(AttnHeads& h, const dmuon_heads_t* t, int64_t tokens, int64_t heads, int64_t dim, int es,
@@ -40,7 +44,8 @@ int common(AttnArgs& a, const dmuon_heads_t* q, const dmuon_heads_t* k, const dm
     if (!sizes_ok(tokens, sequences, heads, kv_heads, dim))
         return fail(DMUON_ERR_INVALID_ARG,
                     std::string(where) + ": tokens must be in [0, 2^24], sequences in [1, 2^20], heads in [1, 1024] and "
-                                         "a multiple of kv_heads, dim in [1, 128]");
+                                         "a multiple of kv_heads, dim in [1, 128], and "
+                                         "(tokens / 32 + sequences) * (heads + kv_heads) below 2^31 - 256");
     OPS_TRY(check_dtype(dtype, where));
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return fail(DMUON_ERR_INVALID_ARG, std::string(where) + ": scale must be finite and > 0");
@@ -57,7 +62,7 @@ int common(AttnArgs& a, const dmuon_heads_t* q, const dmuon_heads_t* k, const dm
     a.group = heads / kv_heads;
     a.dim = dim;
     a.causal = causal != 0;
-    a.fill = offsets ? static_cast<int32_t>(std::min<int64_t>(ceil_div(tokens, 64), 4)) : 0;
+    a.fill = offsets ? static_cast<int32_t>(std::min<int64_t>(ceil_div(tokens, 128), 152)) : 0;
     a.scale = scale;
     a.scale_log2 = scale * kLog2e;
     if (tokens == 0) return DMUON_OK;

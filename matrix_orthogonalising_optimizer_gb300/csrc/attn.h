@@ -30,7 +30,7 @@ struct AttnArgs {
     int32_t causal;
     int32_t slots;             // row tiles of a head (an upper bound: see attn_slots)
     int32_t query_slots;       // FFMA backward: the same of the queries' blocks
-    int32_t fill;              // blocks behind them that clear the rows of no sequence
+    int32_t fill;              // blocks behind all heads' that clear the rows of no sequence
     int32_t whole;             // backward, tensor cores: sequences, where those of one tile have their own launch
     int32_t parts;             // backward: blocks that share the queries of a key tile
     float* partial;            // parts > 1: [2][parts][tokens][kv_heads][dim] sums of dk (unscaled) and dv
@@ -86,18 +86,39 @@ __device__ __forceinline__ bool attn_find(const AttnArgs& a, int32_t slot, int T
     return __shfl_sync(0xffffffffu, k >= 0 && b + static_cast<int64_t>(k) * T < e ? 1 : 0, 0) != 0;
 }
 
-// Clears the rows of no sequence -- before the first and behind the last -- of one
-// head: o = 0, lse = -inf, gradients 0.  Block f of `a.fill`.
+// Clears elements [from, to) of x: share f of a.fill, 16 bytes a store.
 template <typename T>
-__device__ __forceinline__ void attn_clear(const AttnArgs& a, T* x, float* lse, int heads, int head, int f, int thread,
+__device__ __forceinline__ void attn_zero(const AttnArgs& a, T* x, int64_t from, int64_t to, int f, int thread,
+                                          int threads) {
+    constexpr int N = 16 / sizeof(T);
+    const int64_t off = reinterpret_cast<uintptr_t>(x) / sizeof(T) % N;  // from here on, in whole words
+    x -= off;
+    from += off;
+    to += off;
+    const int64_t lo = (from + N - 1) / N, hi = to / N;
+    for (int64_t i = lo + f * threads + thread; i < hi; i += a.fill * threads)
+        reinterpret_cast<uint4*>(x)[i] = make_uint4(0, 0, 0, 0);
+    if (f != 0) return;
+    const int64_t head = lo * N < to ? lo * N : to, tail = hi * N > head ? hi * N : head;
+    for (int64_t i = from + thread; i < head; i += threads) x[i] = T(0.0f);
+    for (int64_t i = tail + thread; i < to; i += threads) x[i] = T(0.0f);
+}
+
+// Clears the rows of no sequence -- before the first and behind the last -- of a tensor
+// tokens x heads x dim, and (lse given) sets their lse to -inf: share f of a.fill.
+// (Row by row and head by head, 4096 of 8192 tokens, 32 heads of 128, took 166 us.)
+template <typename T>
+__device__ __forceinline__ void attn_clear(const AttnArgs& a, T* x, float* lse, int heads, int f, int thread,
                                            int threads) {
-    const int64_t first = attn_offset(a, 0), last = attn_offset(a, a.sequences);
-    const int64_t outside = first + (a.tokens - (last > first ? last : first));
-    for (int64_t i = f; i < outside; i += a.fill) {
-        const int64_t row = i < first ? i : i - first + (last > first ? last : first);
-        for (int c = thread; c < a.dim; c += threads) x[(row * heads + head) * a.dim + c] = T(0.0f);
-        if (lse && thread == 0) lse[head * a.tokens + row] = __int_as_float(0xff800000);
-    }
+    const int64_t first = attn_offset(a, 0), end = attn_offset(a, a.sequences), last = end > first ? end : first;
+    const int64_t width = static_cast<int64_t>(heads) * a.dim;
+    attn_zero(a, x, 0, first * width, f, thread, threads);
+    attn_zero(a, x, last * width, a.tokens * width, f, thread, threads);
+    if (!lse) return;
+    const int64_t outside = first + a.tokens - last;
+    for (int h = 0; h < heads; ++h)
+        for (int64_t i = f * threads + thread; i < outside; i += a.fill * threads)
+            lse[h * a.tokens + (i < first ? i : i - first + last)] = __int_as_float(0xff800000);
 }
 
 // Tensor-core kernels: bf16, rows of 16-byte stride, dim a multiple of 8.

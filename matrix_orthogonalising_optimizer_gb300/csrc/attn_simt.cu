@@ -211,18 +211,17 @@ struct Block {
     int head, row0, rows, tiles;
 };
 
+// The share of the rows of no sequence that a block behind the tiles' clears; else negative.
+__device__ __forceinline__ int clear_share(const AttnArgs& a, unsigned block, unsigned tiles) {
+    return block < tiles * static_cast<unsigned>(a.slots) ? -1 : static_cast<int>(block - tiles * a.slots);
+}
+
 // The block's tile: heads run fastest, tiles of a sequence from its end where the
-// last ones have most to do (`last_first`).  False: nothing left to do.
-template <int N, typename E>
-__device__ __forceinline__ bool take_block(const AttnArgs& a, unsigned block, int heads, bool last_first, E* out, E* out2,
-                                           float* lse, Block& b) {
+// last ones have most to do (`last_first`).  False: the slot holds none.
+template <int N>
+__device__ __forceinline__ bool take_block(const AttnArgs& a, unsigned block, int heads, bool last_first, Block& b) {
     const int slot = static_cast<int>(block / static_cast<unsigned>(heads));
     b.head = static_cast<int>(block - static_cast<unsigned>(slot) * heads);
-    if (slot >= a.slots) {
-        attn_clear(a, out, lse, heads, b.head, slot - a.slots, threadIdx.x, blockDim.x);
-        if (out2) attn_clear(a, out2, nullptr, heads, b.head, slot - a.slots, threadIdx.x, blockDim.x);
-        return false;
-    }
     if (!attn_find(a, slot, N, b.t)) return false;
     b.tiles = (b.t.len + N - 1) / N;
     const int tile = last_first ? b.tiles - 1 - b.t.tile : b.t.tile;
@@ -243,7 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + 16 * R * LD, *V = K + T * LD, *P = V + T * LD;
     Block b;
-    if (!take_block<16 * R>(a, blockIdx.x, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), a.lse, b)) return;
+    const int share = clear_share(a, blockIdx.x, a.heads);
+    if (share >= 0) {
+        attn_clear(a, static_cast<E*>(a.out), a.lse, a.heads, share, threadIdx.x, kThreads);
+        return;
+    }
+    if (!take_block<16 * R>(a, blockIdx.x, a.heads, a.causal != 0, b)) return;
     const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
@@ -318,8 +322,12 @@ __device__ __forceinline__ void dq_block(const AttnArgs& a, unsigned index, floa
     constexpr int LD = DP + 4;
     float *Q = sm, *O = Q + 16 * R * LD, *K = O + 16 * R * LD, *V = K + T * LD, *P = V + T * LD;
     Block b;
-    if (!take_block<16 * R>(a, index, a.heads, a.causal != 0, static_cast<E*>(a.out), static_cast<E*>(nullptr), nullptr, b))
+    const int share = clear_share(a, index, a.heads);
+    if (share >= 0) {
+        attn_clear(a, static_cast<E*>(a.out), nullptr, a.heads, share, threadIdx.x, kThreads);
         return;
+    }
+    if (!take_block<16 * R>(a, index, a.heads, a.causal != 0, b)) return;
     const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
@@ -406,16 +414,19 @@ __device__ __forceinline__ void dkv_block(const AttnArgs& a, unsigned index, flo
     constexpr int LD = DP + 4;
     float *K = sm, *V = K + T * LD, *Q = V + T * LD, *O = Q + T * LD, *P = O + T * LD, *G = P + T * LP;
     Block b;
-    const int part = static_cast<int>(index % static_cast<unsigned>(a.parts));
-    const unsigned block = index / static_cast<unsigned>(a.parts);
-    float *pk = nullptr, *pv = nullptr;  // this part's sums, where parts share the tile
-    if (a.parts > 1) {
-        pk = attn_partial(a, 0, part);
-        pv = attn_partial(a, 1, part);
-        if (!take_block<T>(a, block, a.kv_heads, false, pk, pv, nullptr, b)) return;
-    } else if (!take_block<T>(a, block, a.kv_heads, false, static_cast<E*>(a.dk), static_cast<E*>(a.dv), nullptr, b)) {
+    const int share = clear_share(a, index, a.kv_heads * a.parts);
+    if (share >= 0) {
+        const auto clear = [&](auto* x) { attn_clear(a, x, nullptr, a.kv_heads, share, threadIdx.x, kThreads); };
+        if (a.parts > 1) {
+            for (int k = 0; k < 2 * a.parts; ++k) clear(attn_partial(a, 0, k));
+        } else {
+            clear(static_cast<E*>(a.dk));
+            clear(static_cast<E*>(a.dv));
+        }
         return;
     }
+    const int part = static_cast<int>(index % static_cast<unsigned>(a.parts));
+    if (!take_block<T>(a, index / static_cast<unsigned>(a.parts), a.kv_heads, false, b)) return;
     const int dim4 = (a.dim + 3) / 4 * 4, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const bool vq = vec_rows<E>(a.q, a.dim), vo = vec_rows<E>(a.d_o, a.dim);
     const int64_t row = b.t.begin + b.row0;
@@ -461,8 +472,8 @@ __device__ __forceinline__ void dkv_block(const AttnArgs& a, unsigned index, flo
     }
     const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f}, f[4] = {a.scale, a.scale, a.scale, a.scale};
     if (a.parts > 1) {
-        store_rows<float, DP>(pv, dv, one, row, b.rows, a.kv_heads, b.head, a.dim);
-        store_rows<float, DP>(pk, dk, one, row, b.rows, a.kv_heads, b.head, a.dim);
+        store_rows<float, DP>(attn_partial(a, 1, part), dv, one, row, b.rows, a.kv_heads, b.head, a.dim);
+        store_rows<float, DP>(attn_partial(a, 0, part), dk, one, row, b.rows, a.kv_heads, b.head, a.dim);
         return;
     }
     store_rows<E, DP>(a.dv, dv, one, row, b.rows, a.kv_heads, b.head, a.dim);
@@ -508,12 +519,12 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
     }
 }
 
-// delta = do . o, one warp per row.  Rows of no sequence are never read later.
+// delta = do . o of the rows of all sequences, one warp per row.
 template <typename E>
 __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttnArgs a) {
-    const int64_t rows = a.tokens * a.heads;
+    const int64_t first = attn_offset(a, 0) * a.heads, rows = attn_offset(a, a.sequences) * a.heads;
     const int lane = threadIdx.x % 32;
-    for (int64_t r = blockIdx.x * 8ll + threadIdx.x / 32; r < rows; r += gridDim.x * 8ll) {
+    for (int64_t r = first + blockIdx.x * 8ll + threadIdx.x / 32; r < rows; r += gridDim.x * 8ll) {
         const int64_t token = r / a.heads;
         const int head = static_cast<int>(r - token * a.heads);
         const E* o = static_cast<const E*>(a.o) + r * a.dim;
@@ -531,10 +542,10 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Attn
 template <typename E, int G>
 __global__ void __launch_bounds__(256) delta_vector_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int N = 16 / sizeof(E), R = 32 / G, U = 4;
-    const int64_t rows = a.tokens * a.heads;
+    const int64_t first = attn_offset(a, 0) * a.heads, rows = attn_offset(a, a.sequences) * a.heads;
     const int lane = threadIdx.x % 32, c = lane % G * N;
     const int64_t stride = gridDim.x * 8ll * R * U;
-    for (int64_t r0 = (blockIdx.x * 8ll + threadIdx.x / 32) * R * U; r0 < rows; r0 += stride) {
+    for (int64_t r0 = first + (blockIdx.x * 8ll + threadIdx.x / 32) * R * U; r0 < rows; r0 += stride) {
         uint4 o[U], d[U];
         int64_t at[U];
 #pragma unroll
@@ -638,7 +649,7 @@ bool half_blocks(const AttnArgs& a) { return (a.tokens / T + 1) * a.heads < 152;
 template <typename E, int DP, int R>
 cudaError_t forward(AttnArgs a, cudaStream_t s) {
     a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, 16 * R));
-    const unsigned grid = static_cast<unsigned>(a.slots + a.fill) * a.heads;
+    const unsigned grid = static_cast<unsigned>(a.slots) * a.heads + a.fill;
     forward_kernel<E, DP, R><<<grid, kThreads, kForwardBytes<DP, R>, s>>>(a);
     return cudaGetLastError();
 }
@@ -652,8 +663,8 @@ template <typename E, int DP, int R>
 cudaError_t backward(AttnArgs a, cudaStream_t s) {
     a.slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, T));
     a.query_slots = static_cast<int32_t>(attn_slots(a.tokens, a.sequences, 16 * R));
-    const unsigned keys = static_cast<unsigned>(a.slots + a.fill) * a.kv_heads * a.parts;
-    const unsigned queries = static_cast<unsigned>(a.query_slots + a.fill) * a.heads;
+    const unsigned keys = static_cast<unsigned>(a.slots) * a.kv_heads * a.parts + a.fill;
+    const unsigned queries = static_cast<unsigned>(a.query_slots) * a.heads + a.fill;
     const auto run = [&](unsigned k, unsigned q) {
         backward_kernel<E, DP, R><<<k + q, kThreads, kBackwardBytes<DP>, s>>>(a, k);
         return cudaGetLastError();

@@ -52,11 +52,11 @@ template <int DP>
 constexpr int kStages = DP == 128 ? 5 : 8;
 
 // What a CTA does next: a tile's gradients, or rows and partial sums to clear.
-enum Kind : int32_t { KEYS, WHOLE, QUERIES, CLEAR_KEYS, CLEAR_QUERIES, CLEAR_PART, NONE };
+enum Kind : int32_t { KEYS, WHOLE, QUERIES, CLEAR, CLEAR_PART, NONE };
 
 struct Item {
     int32_t kind, head, part;
-    int32_t begin, len, tile;  // of the sequence, as AttnTile; CLEAR_KEYS, CLEAR_QUERIES: tile is the share
+    int32_t begin, len, tile;  // of the sequence, as AttnTile; CLEAR: tile is the share
 };
 
 template <int DP>
@@ -153,8 +153,8 @@ __device__ __forceinline__ int part_begin(const AttnArgs& a, const AttnTile& t, 
 
 // The rows of no sequence, by the element-wise warps: share f of a.fill.
 template <typename T>
-__device__ __forceinline__ void clear_rows_of(const AttnArgs& a, T* x, int heads, int head, int f) {
-    attn_clear(a, x, nullptr, heads, head, f, threadIdx.x - 32 * kEltWarp0, 32 * kEltWarps);
+__device__ __forceinline__ void clear_rows_of(const AttnArgs& a, T* x, int heads, int f) {
+    attn_clear(a, x, nullptr, heads, f, threadIdx.x - 32 * kEltWarp0, 32 * kEltWarps);
 }
 
 // A part without steps: its sums are zero.
@@ -655,26 +655,25 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
 // A CTA begins with its own block index and then takes those of blocks not yet started.
 template <int DP, bool kWhole>
 __device__ __forceinline__ Item next_item(const AttnArgs& a, Smem<DP>& S, bool first, uint32_t& asked, int lane) {
-    // tiles of the keys, tiles of the queries, rows to clear (in the only launch, or this one)
-    const unsigned tiles = kWhole ? a.whole : a.slots, fill = kWhole && a.slots > 0 ? 0 : a.fill;
+    // tiles of the keys, tiles of the queries, rows to clear (once)
+    const unsigned tiles = kWhole ? a.whole : a.slots;
     const unsigned keys_end = tiles * a.kv_heads * a.parts, tiles_end = keys_end + (kWhole ? 0 : tiles * a.heads);
-    const unsigned clear_end = tiles_end + fill * a.kv_heads * a.parts;
     Item item;
     for (;;) {
         unsigned n = blockIdx.x;
         if (!first && !claim_block(&S.claim, &S.claimed, asked, n, &S.bad, lane)) return Item{NONE, 0, 0, 0, 0, 0};
         item = Item{NONE, 0, 0, 0, 0, 0};
-        const bool clear = n >= tiles_end, keys = clear ? n < clear_end : n < keys_end;
+        if (n >= tiles_end) {
+            item.kind = CLEAR;
+            item.tile = static_cast<int>(n - tiles_end);
+            return item;
+        }
+        const bool keys = n < keys_end;
         const unsigned heads = keys ? a.kv_heads : a.heads, parts = keys ? a.parts : 1;
-        n -= clear ? (keys ? tiles_end : clear_end) : (keys ? 0 : keys_end);
+        n -= keys ? 0 : keys_end;
         const unsigned tile = n / parts, slot = tile / heads;
         item.part = static_cast<int>(n - tile * parts);
         item.head = static_cast<int>(tile - slot * heads);
-        if (clear) {
-            item.kind = keys ? CLEAR_KEYS : CLEAR_QUERIES;
-            item.tile = static_cast<int>(slot);
-            return item;
-        }
         item.kind = kWhole ? WHOLE : keys ? KEYS : QUERIES;
         AttnTile t;
         bool any;
@@ -736,14 +735,14 @@ __device__ __forceinline__ void work(const AttnArgs& a, Smem<DP>& S, const CUten
             // rows of no sequence, or a part without steps
             if (kind == CLEAR_PART) {
                 clear_part(a, t, head, part);
-            } else if (kind == CLEAR_QUERIES) {
-                clear_rows_of(a, static_cast<__nv_bfloat16*>(a.out), a.heads, head, t.tile);
-            } else if (a.parts > 1) {
-                clear_rows_of(a, attn_partial(a, 0, part), a.kv_heads, head, t.tile);
-                clear_rows_of(a, attn_partial(a, 1, part), a.kv_heads, head, t.tile);
             } else {
-                clear_rows_of(a, static_cast<__nv_bfloat16*>(a.dk), a.kv_heads, head, t.tile);
-                clear_rows_of(a, static_cast<__nv_bfloat16*>(a.dv), a.kv_heads, head, t.tile);
+                clear_rows_of(a, static_cast<__nv_bfloat16*>(a.out), a.heads, t.tile);
+                if (a.parts > 1) {
+                    for (int k = 0; k < 2 * a.parts; ++k) clear_rows_of(a, attn_partial(a, 0, k), a.kv_heads, t.tile);
+                } else {
+                    clear_rows_of(a, static_cast<__nv_bfloat16*>(a.dk), a.kv_heads, t.tile);
+                    clear_rows_of(a, static_cast<__nv_bfloat16*>(a.dv), a.kv_heads, t.tile);
+                }
             }
         }
         if (!kElt && warp == 0) {
@@ -864,8 +863,8 @@ cudaError_t run(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
     a.whole = longest <= kRows || (a.offsets && average <= kShortAverage) ? a.sequences : 0;
     const int64_t keys = static_cast<int64_t>(a.kv_heads) * a.parts, both = a.heads + keys;
     cudaError_t e = cudaSuccess;
-    if (a.whole > 0) e = launch<DP, true>(a, m, a.whole * keys + (a.slots > 0 ? 0 : a.fill * both), s);
-    if (e == cudaSuccess && a.slots > 0) e = launch<DP, false>(a, m, (a.slots + a.fill) * both, s);
+    if (a.whole > 0) e = launch<DP, true>(a, m, a.whole * keys + (a.slots > 0 ? 0 : a.fill), s);
+    if (e == cudaSuccess && a.slots > 0) e = launch<DP, false>(a, m, a.slots * both + a.fill, s);
     return e;
 }
 

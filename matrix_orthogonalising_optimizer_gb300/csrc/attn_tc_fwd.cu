@@ -108,11 +108,12 @@ constexpr float kLazy = 8.0f;
 template <int NT>
 __device__ __forceinline__ bool find_item(const AttnArgs& a, unsigned block, Item& item) {
     const unsigned slot = block / static_cast<unsigned>(a.heads);
-    item = Item{CLEAR, static_cast<int>(block - slot * a.heads), 0, 0, static_cast<int>(slot) - a.slots};
+    const int head = static_cast<int>(block - slot * a.heads);
+    item = Item{CLEAR, 0, 0, 0, static_cast<int>(block - static_cast<unsigned>(a.slots) * a.heads)};
     if (static_cast<int>(slot) >= a.slots) return true;
     AttnTile t;
     if (!attn_find(a, static_cast<int>(slot), NT * kRows, t)) return false;
-    item = Item{TILE, item.head, static_cast<int32_t>(t.begin), t.len, t.tile};
+    item = Item{TILE, head, static_cast<int32_t>(t.begin), t.len, t.tile};
     return true;
 }
 
@@ -359,8 +360,8 @@ __device__ __forceinline__ void work(const AttnArgs& a, Smem<DP, NT>& S, const C
         if (kind == TILE) {
             run_tile<DP, NT, kSoft>(a, S, mq, mk, mv, t, head, warp, lane, tmem);
         } else if (kSoft) {
-            attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, head, t.tile,
-                       threadIdx.x - 32 * kSoftWarp0, 128 * NT);
+            attn_clear(a, static_cast<__nv_bfloat16*>(a.out), a.lse, a.heads, t.tile, threadIdx.x - 32 * kSoftWarp0,
+                       128 * NT);
         }
         if (!kSoft && warp == 0) {
             // after this item's last loads are issued
@@ -457,7 +458,7 @@ cudaError_t launch(AttnArgs a, const AttnMaps& m, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.slots + a.fill) * a.heads);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.slots) * a.heads + a.fill);
     cfg.blockDim = dim3(Cfg<DP, NT>::kThreads);
     cfg.dynamicSmemBytes = smem_bytes<DP, NT>();
     cfg.stream = s;

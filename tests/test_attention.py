@@ -102,6 +102,11 @@ def test_attention_refusals(lib):
         assert fwd(**bad) == _lib.ERR_ALIGN, bad
     assert fwd(tokens=0, q=None, o=None) == _lib.OK
     assert "multiple of sequences" in (fwd(offsets=None, sequences=3), err(lib))[1]
+    # more blocks than a launch may have
+    assert fwd(heads=1024, kv=1024, sequences=1 << 20, q=view(token=1 << 16), k=view(token=1 << 16),
+               v=view(token=1 << 16)) == _lib.ERR_INVALID_ARG
+    assert lib.dmuon_attention_workspace_bytes(1 << 20, 8, 1024, 1024, 64, _lib.BF16, 1) == 0
+    assert lib.dmuon_attention_workspace_bytes(1, 1 << 24, 1024, 1024, 128, _lib.BF16, 1) > 0
 
     need = lib.dmuon_attention_workspace_bytes(2, 8, 8, 2, 64, _lib.BF16, 1)
     assert need >= 8 * 8 * 4
@@ -442,6 +447,8 @@ def test_python_refusals_on_the_gpu():
                 lambda: pkg.attention_backward(q, q, k, k, q, torch.zeros(4, 7, device="cuda"))):
         with pytest.raises(ValueError):
             bad()
+    with pytest.raises(pkg.DmuonError, match="dim in"):
+        pkg.attention(q[..., :0].contiguous(), k[..., :0].contiguous(), k[..., :0].contiguous())
     with pytest.raises(pkg.DmuonError, match="strides"):
         pkg.attention(q, k[:1].expand(8, 2, 64), k)
     with pytest.raises(pkg.DmuonError, match="multiple of kv_heads"):
