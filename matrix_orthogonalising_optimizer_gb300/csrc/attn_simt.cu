@@ -31,8 +31,14 @@ namespace {
 
 constexpr int T = 64;           // keys of a tile (side of the keys: and queries)
 constexpr int kThreads = 256;   // 16 x 16: thread (ty, tx) holds rows ty + 16 r, columns tx + 16 c
-constexpr int LP = T + 4;       // row stride of a T x T tile
+constexpr int LP = T + 16;      // row stride of a T x T tile: a warp's two rows on different banks
 constexpr unsigned kFull = 0xffffffffu;
+
+// A warp holds two rows of threads, in alternate lanes: neighbours then read the same
+// 16 bytes of a column's operand, and the load takes two cycles of the shared memory; with a
+// half warp per row it takes four.
+__device__ __forceinline__ int row_of() { return threadIdx.x / 32 * 2 + threadIdx.x % 2; }
+__device__ __forceinline__ int col_of() { return threadIdx.x % 32 / 2; }
 
 template <typename E>
 __device__ __forceinline__ float to_f(E v) {
@@ -121,8 +127,8 @@ struct Pair {
 template <int DP, int R>
 __device__ __forceinline__ void product_nt(float (&acc)[R][4], const float* A, const float* B, int dim4) {
     constexpr int LD = DP + 4;
-    const float* a0 = A + (threadIdx.x / 16) * LD;
-    const float* b0 = B + (threadIdx.x % 16) * LD;
+    const float* a0 = A + row_of() * LD;
+    const float* b0 = B + col_of() * LD;
     float2 sum[R][4];  // even and odd d
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -153,8 +159,8 @@ __device__ __forceinline__ void product_nt(float (&acc)[R][4], const float* A, c
 template <int DP, int R>
 __device__ __forceinline__ void product_nn(float2 (&acc)[R][DP / 32], const float* P, const float* V) {
     constexpr int LD = DP + 4;
-    const float* p0 = P + (threadIdx.x / 16) * LP;
-    const float* v0 = V + 4 * (threadIdx.x % 16);
+    const float* p0 = P + row_of() * LP;
+    const float* v0 = V + 4 * col_of();
 #pragma unroll 2
     for (int j = 0; j < T; j += 4) {
         float4 p[R];
@@ -179,7 +185,7 @@ __device__ __forceinline__ void product_nn(float2 (&acc)[R][DP / 32], const floa
 template <typename E, int DP, int R>
 __device__ __forceinline__ void store_rows(void* out, const float2 (&acc)[R][DP / 32], const float (&f)[R],
                                            int64_t row0, int rows, int heads, int head, int dim) {
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int ty = row_of(), tx = col_of();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = ty + 16 * r;
@@ -196,13 +202,13 @@ __device__ __forceinline__ void store_rows(void* out, const float2 (&acc)[R][DP 
 // Sum and maximum over the 16 lanes that share a row.
 __device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-    for (int s = 8; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, s));
+    for (int s = 16; s >= 2; s >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, s));
     return v;
 }
 
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-    for (int s = 8; s >= 1; s >>= 1) v += __shfl_xor_sync(kFull, v, s);
+    for (int s = 16; s >= 2; s >>= 1) v += __shfl_xor_sync(kFull, v, s);
     return v;
 }
 
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     }
     if (!take_block<16 * R>(a, blockIdx.x, a.heads, a.causal != 0, b)) return;
     const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int ty = row_of(), tx = col_of();
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
     load_tile<E, DP, 16 * R>(Q, a.q, b.t.begin + b.row0, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
     float2 acc[R][DP / 32];
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
 #pragma unroll
             for (int k = 0; k < DP / 32; ++k) acc[r][k] = tc::mul2(acc[r][k], tc::both(old));
         }
-        __syncwarp();  // a row of P is written and read by one half warp
+        __syncwarp();  // a row of P is written and read by one warp
         product_nn<DP>(acc, P, V);
     }
     float f[R];
@@ -329,7 +335,7 @@ __device__ __forceinline__ void dq_block(const AttnArgs& a, unsigned index, floa
     }
     if (!take_block<16 * R>(a, index, a.heads, a.causal != 0, b)) return;
     const int kv = b.head / a.group, dim4 = (a.dim + 3) / 4 * 4;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int ty = row_of(), tx = col_of();
     const bool vk = vec_rows<E>(a.k, a.dim), vv = vec_rows<E>(a.v, a.dim);
     const int64_t row = b.t.begin + b.row0;
     load_tile<E, DP, 16 * R>(Q, a.q, row, b.rows, b.head, a.dim, vec_rows<E>(a.q, a.dim));
@@ -427,7 +433,7 @@ __device__ __forceinline__ void dkv_block(const AttnArgs& a, unsigned index, flo
     }
     const int part = static_cast<int>(index % static_cast<unsigned>(a.parts));
     if (!take_block<T>(a, index / static_cast<unsigned>(a.parts), a.kv_heads, false, b)) return;
-    const int dim4 = (a.dim + 3) / 4 * 4, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int dim4 = (a.dim + 3) / 4 * 4, ty = row_of(), tx = col_of();
     const bool vq = vec_rows<E>(a.q, a.dim), vo = vec_rows<E>(a.d_o, a.dim);
     const int64_t row = b.t.begin + b.row0;
     load_tile<E, DP>(K, a.k, row, b.rows, b.head, a.dim, vec_rows<E>(a.k, a.dim));
@@ -538,64 +544,66 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Attn
 }
 
 // The same where rows start on 16-byte boundaries: G lanes a row, 16 bytes each of o and
-// do, four rows' loads in flight (134 MB at 8192 tokens, 32 heads of 128: 48 -> 24 us).
+// do; a warp takes 32 / G * 4 tokens of one head, all their loads in flight, so that what it
+// stores lies together.
 template <typename E, int G>
 __global__ void __launch_bounds__(256) delta_vector_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int N = 16 / sizeof(E), R = 32 / G, U = 4;
-    const int64_t first = attn_offset(a, 0) * a.heads, rows = attn_offset(a, a.sequences) * a.heads;
+    const int64_t first = attn_offset(a, 0), end = attn_offset(a, a.sequences);
     const int lane = threadIdx.x % 32, c = lane % G * N;
-    const int64_t stride = gridDim.x * 8ll * R * U;
-    for (int64_t r0 = first + (blockIdx.x * 8ll + threadIdx.x / 32) * R * U; r0 < rows; r0 += stride) {
-        uint4 o[U], d[U];
-        int64_t at[U];
+    // < 2^31: at most 2^24 / 4 tokens' groups of 1024 heads, divided in 32 bits
+    const uint32_t unit = blockIdx.x * 8u + threadIdx.x / 32, group = unit / static_cast<uint32_t>(a.heads);
+    const int head = static_cast<int>(unit - group * static_cast<uint32_t>(a.heads));
+    const int64_t token0 = first + static_cast<int64_t>(group) * (R * U) + lane / G;
+    const E* po = static_cast<const E*>(a.o) + (token0 * a.heads + head) * a.dim + c;
+    const E* pd = static_cast<const E*>(a.d_o.p) + token0 * a.d_o.token + head * a.d_o.head + c;
+    uint4 o[U], d[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = r0 + u * R + lane / G;
-            o[u] = d[u] = make_uint4(0, 0, 0, 0);
-            at[u] = -1;
-            if (r >= rows) continue;
-            // a 64-bit division would take longer than the row
-            const int64_t token = rows >> 32 ? r / a.heads : static_cast<uint32_t>(r) / static_cast<uint32_t>(a.heads);
-            const int64_t head = r - token * a.heads;
-            at[u] = head * a.tokens + token;
-            if (c >= a.dim) continue;
-            o[u] = *reinterpret_cast<const uint4*>(static_cast<const E*>(a.o) + r * a.dim + c);
-            d[u] = *reinterpret_cast<const uint4*>(static_cast<const E*>(a.d_o.p) + token * a.d_o.token +
-                                                   head * a.d_o.head + c);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t x[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, y[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(E) == 2) {
-                    const float2 p = tc::unpack_bf16x2(x[i]), q = tc::unpack_bf16x2(y[i]);
-                    sum = fmaf(p.x, q.x, fmaf(p.y, q.y, sum));
-                } else {
-                    sum = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), sum);
-                }
-            }
-#pragma unroll
-            for (int s = G / 2; s >= 1; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
-            if (lane % G == 0 && at[u] >= 0) a.delta[at[u]] = sum;
-        }
+    for (int u = 0; u < U; ++u) {
+        o[u] = d[u] = make_uint4(0, 0, 0, 0);
+        if (c >= a.dim || token0 + u * R >= end) continue;
+        o[u] = *reinterpret_cast<const uint4*>(po + static_cast<int64_t>(u * R) * a.heads * a.dim);
+        d[u] = *reinterpret_cast<const uint4*>(pd + u * R * a.d_o.token);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t x[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, y[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(E) == 2) {
+                const float2 p = tc::unpack_bf16x2(x[i]), q = tc::unpack_bf16x2(y[i]);
+                sum = fmaf(p.x, q.x, fmaf(p.y, q.y, sum));
+            } else {
+                sum = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), sum);
+            }
+        }
+#pragma unroll
+        for (int s = G / 2; s >= 1; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+        if (lane % G == 0 && token0 + u * R < end) a.delta[head * a.tokens + token0 + u * R] = sum;
+    }
+}
+
+template <typename E, int G>
+void launch_delta_vector(const AttnArgs& a, cudaStream_t s) {
+    constexpr int tokens = 32 / G * 4;  // of a warp
+    const int64_t units = (a.tokens + tokens - 1) / tokens * a.heads;
+    delta_vector_kernel<E, G><<<static_cast<unsigned>((units + 7) / 8), 256, 0, s>>>(a);
 }
 
 template <typename E>
 cudaError_t run_delta(const AttnArgs& a, cudaStream_t s) {
     constexpr int n = 16 / sizeof(E);
-    const auto grid = [](int64_t rows, int per) { return static_cast<unsigned>(std::min<int64_t>((rows + per - 1) / per, 1216)); };
-    const int64_t rows = a.tokens * a.heads;
-    if (a.dim % n == 0 && reinterpret_cast<uintptr_t>(a.d_o.p) % 16 == 0 && a.d_o.token % n == 0 && a.d_o.head % n == 0) {
+    if (a.dim % n == 0 && reinterpret_cast<uintptr_t>(a.d_o.p) % 16 == 0 && a.d_o.token % n == 0 &&
+        a.d_o.head % n == 0) {
         const int lanes = a.dim / n;
-        if (lanes <= 4) delta_vector_kernel<E, 4><<<grid(rows, 256), 256, 0, s>>>(a);
-        else if (lanes <= 8) delta_vector_kernel<E, 8><<<grid(rows, 128), 256, 0, s>>>(a);
-        else if (lanes <= 16) delta_vector_kernel<E, 16><<<grid(rows, 64), 256, 0, s>>>(a);
-        else delta_vector_kernel<E, 32><<<grid(rows, 32), 256, 0, s>>>(a);
+        if (lanes <= 4) launch_delta_vector<E, 4>(a, s);
+        else if (lanes <= 8) launch_delta_vector<E, 8>(a, s);
+        else if (lanes <= 16) launch_delta_vector<E, 16>(a, s);
+        else launch_delta_vector<E, 32>(a, s);
     } else {
-        delta_kernel<E><<<grid(rows, 8), 256, 0, s>>>(a);
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a.tokens * a.heads + 7) / 8, 1216));
+        delta_kernel<E><<<grid, 256, 0, s>>>(a);
     }
     return cudaGetLastError();
 }
