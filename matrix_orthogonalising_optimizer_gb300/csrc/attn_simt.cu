@@ -13,9 +13,10 @@
 // products, 4 x 4 per thread; all tiles lie row by row in shared memory as fp32,
 // dim + 4 floats apart: 16-byte reads of eight rows then cover all banks.
 //
-// Bound: FFMA issue and the latency of few warps (one block per SM: 128 KB and more of
-// tiles, 200 registers).  Measured in fp32: 2048 tokens, 16 heads of 64, causal: forward 266 us
-// (16 TFLOP/s), backward 838 us (26); 777 tokens, 6 / 2 heads of 80: 45 and 83 us.
+// Bound: FFMA (about half of its rate) and shared-memory loads (4 x 4 products take 8 loads of
+// 2 cycles each per 32 FMA instructions); a second block per SM adds nothing.  Measured in
+// fp32: 2048 tokens, 16 heads of 64, causal: forward 231 us (19 TFLOP/s), backward 705 us (30);
+// 777 tokens, 6 / 2 heads of 80: 36 and 70 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -36,7 +37,7 @@ constexpr unsigned kFull = 0xffffffffu;
 
 // A warp holds two rows of threads, in alternate lanes: neighbours then read the same
 // 16 bytes of a column's operand, and the load takes two cycles of the shared memory; with a
-// half warp per row it takes four.
+// half warp per row it takes four (777 tokens: forward 45 -> 37 us, backward 82 -> 68).
 __device__ __forceinline__ int row_of() { return threadIdx.x / 32 * 2 + threadIdx.x % 2; }
 __device__ __forceinline__ int col_of() { return threadIdx.x % 32 / 2; }
 
@@ -134,7 +135,7 @@ __device__ __forceinline__ void product_nt(float (&acc)[R][4], const float* A, c
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) sum[r][c] = tc::both(0.0f);
-#pragma unroll 2
+#pragma unroll 4
     for (int d = 0; d < dim4; d += 4) {
         float4 a[R], b[4];
 #pragma unroll
@@ -161,7 +162,7 @@ __device__ __forceinline__ void product_nn(float2 (&acc)[R][DP / 32], const floa
     constexpr int LD = DP + 4;
     const float* p0 = P + row_of() * LP;
     const float* v0 = V + 4 * col_of();
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < T; j += 4) {
         float4 p[R];
 #pragma unroll
@@ -545,13 +546,14 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Attn
 
 // The same where rows start on 16-byte boundaries: G lanes a row, 16 bytes each of o and
 // do; a warp takes 32 / G * 4 tokens of one head, all their loads in flight, so that what it
-// stores lies together.
+// stores lies together (134 MB at 8192 tokens, 32 heads of 128: 22 us, 6.1 TB/s; with a token's
+// heads in a row 33 us).
 template <typename E, int G>
 __global__ void __launch_bounds__(256) delta_vector_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int N = 16 / sizeof(E), R = 32 / G, U = 4;
     const int64_t first = attn_offset(a, 0), end = attn_offset(a, a.sequences);
     const int lane = threadIdx.x % 32, c = lane % G * N;
-    // < 2^31: at most 2^24 / 4 tokens' groups of 1024 heads, divided in 32 bits
+    // divided in 32 bits: o has fewer than 2^38 elements, a unit at least 2^7
     const uint32_t unit = blockIdx.x * 8u + threadIdx.x / 32, group = unit / static_cast<uint32_t>(a.heads);
     const int head = static_cast<int>(unit - group * static_cast<uint32_t>(a.heads));
     const int64_t token0 = first + static_cast<int64_t>(group) * (R * U) + lane / G;
@@ -650,8 +652,9 @@ cudaError_t prepare() {
 
 // Blocks of 32 queries where those of 64 leave SMs without one: each then takes less time,
 // if not half.  Measured in fp32, 64 -> 32 queries, forward | backward: 777 tokens, 6 / 2
-// heads of 80 (90 blocks of 64) 53 -> 45 us | 96 -> 83; 1024 tokens, 8 heads of 128 (136) 131 -> 111 |
-// 317 -> 279; 12 heads of 64 (204) 78 -> 90 | 214 -> 233.
+// heads of 80 (about 90 blocks of 64) 49 -> 36 us | 95 -> 70; 1024 tokens, 8 heads of 128 (136)
+// 121 -> 84 | 295 -> 230; 12 heads of 64 (204) 68 -> 70 | 184 -> 184; 2048 tokens, 16 heads
+// of 64 (528) 231 -> 299 | 703 -> 789.
 bool half_blocks(const AttnArgs& a) { return (a.tokens / T + 1) * a.heads < 152; }
 
 template <typename E, int DP, int R>

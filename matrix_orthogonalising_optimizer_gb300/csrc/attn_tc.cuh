@@ -24,8 +24,8 @@ constexpr int kTile = DP / 64 * kBox;  // bytes of a tile
 
 // M = 128; a_mn, b_mn: A's, B's contraction runs over its rows.
 __device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_mn, bool a_mn = false) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(kRows >> 4) << 24);
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
 }
 
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return smem_desc(addr, 0, 1024); }
@@ -46,8 +46,9 @@ template <int DP>
 __device__ __forceinline__ void product_cols_ts(uint32_t e, uint32_t d, uint32_t a, uint64_t b) {
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k)
-        umma_bf16_ts(e, d, a + static_cast<uint32_t>(8 * k), b + static_cast<uint64_t>((k / 4 * kBox + k % 4 * 32) >> 4),
-                     idesc_of(kRows, false), k != 0 ? 1u : 0u);
+        umma_bf16_ts(e, d, a + static_cast<uint32_t>(8 * k),
+                     b + static_cast<uint64_t>((k / 4 * kBox + k % 4 * 32) >> 4), idesc_of(kRows, false),
+                     k != 0 ? 1u : 0u);
 }
 
 // D (128 x DP) (+)= P B over 16 n rows of B, from row 16 k0 on; P in TMEM.
@@ -156,7 +157,8 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t t, float f, 
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 mine[(4 * h + k) ^ chunk] =
-                    make_uint4(pack_bf16x2(v[8 * k] * f, v[8 * k + 1] * f), pack_bf16x2(v[8 * k + 2] * f, v[8 * k + 3] * f),
+                    make_uint4(pack_bf16x2(v[8 * k] * f, v[8 * k + 1] * f),
+                               pack_bf16x2(v[8 * k + 2] * f, v[8 * k + 3] * f),
                                pack_bf16x2(v[8 * k + 4] * f, v[8 * k + 5] * f),
                                pack_bf16x2(v[8 * k + 6] * f, v[8 * k + 7] * f));
         }

@@ -25,11 +25,11 @@
 // measured about 2300 a step of the keys (2048 of MMAs) and 1850 of the queries (1536), and 3
 // to 6 us a tile besides.  8192 tokens, 32/8 heads of 128, causal: 1.07 ms with delta,
 // 1.28 PFLOP/s of the five products, 1.80 of the seven; five documents packed into 8192
-// tokens 0.39 ms; 12 heads of 64 0.32 ms (element-wise work and hand-overs).
+// tokens 0.38 ms; 12 heads of 64 0.32 ms (element-wise work and hand-overs).
 //
 // Warp 0 loads and looks for the next item, warp 1 issues the MMAs, warp 2 fetches lse and
-// delta of the query tiles (side of the keys), warps 4 to 11 do the element-wise work, half of the columns
-// each warpgroup.
+// delta of the query tiles (side of the keys), warps 4 to 11 do the element-wise work, half of
+// the columns each warpgroup.
 #include <cstddef>
 
 #include "attn_tc.cuh"
@@ -755,7 +755,8 @@ __device__ __forceinline__ void work(const AttnArgs& a, Smem<DP>& S, const CUten
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         fence_before();
         __syncthreads();
-        if (__shfl_sync(kFullMask, S.bad, 0) != 0) return;  // uniform, or the next item would run without uniform registers
+        // from one lane, or the next item would run without uniform registers
+        if (__shfl_sync(kFullMask, S.bad, 0) != 0) return;
         if (!kElt && warp == 2) init_barriers(S, lane, true);
         __syncthreads();
         fence_after();

@@ -17,14 +17,15 @@
 // first of which the tensor cores take while the second is made.
 //
 // Warp 0 loads (a ring of K and V tiles), warp 1 issues the MMAs, warps 4 .. work on the
-// softmax, one warpgroup per tile.
+// softmax, one warpgroup per tile.  A CTA that has come to its end takes over the next block
+// that has not started, without another set-up.
 //
 // Bound: the tensor cores, 4 * 128 * 128 * dim operations per pair of tiles -- at dim =
 // 128 1024 cycles, against 512 of exponentials (32 a cycle and SM) and about 670 of all the
-// softmax's pipes.  Measured: 16384 tokens, 32/8 heads of 128, causal: 1.23 ms, 1.78 PFLOP/s, 91 % of cuBLAS's burst rate
-// (1.35 ms = 1.63 in a loop, under the power cap).  Heads of 64: the softmax (12 heads, 8192 tokens: 107 us,
-// 0.97 PFLOP/s).  Short sequences: start and end of a CTA, about 3 us (23 ragged ones of 356
-// tokens, 12 heads of 64: 32 us).
+// softmax's pipes.  Measured: 16384 tokens, 32/8 heads of 128, causal: 1.22 ms, 1.80 PFLOP/s,
+// 92 % of cuBLAS's burst rate (1.37 ms = 1.61 in a loop, under the power cap).  Heads of 64: the
+// softmax (12 heads, 8192 tokens: 107 us, 0.97 PFLOP/s).  Short sequences: start and end of a
+// tile, about 3 us (23 ragged ones of 356 tokens, 12 heads of 64: 32 us).
 #include <cstddef>
 
 #include "attn_tc.cuh"

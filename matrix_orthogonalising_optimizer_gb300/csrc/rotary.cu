@@ -6,7 +6,9 @@
 //      token's position: a cos - b sin, a sin + b cos; the others unchanged
 //   dn = dy turned back, dw = sum dn x r, g = dn w, dx = r (g - x r mean(g x r))
 //
-// HBM-bound: a row is read once, held in registers as fp32 and written once.
+// HBM-bound: a row is read once, held in registers as fp32 and written once.  Measured: 16384
+// tokens, 32/8 heads of 128: forward 58 us (6.0 TB/s, 89 % of the copy rate), backward 84 us
+// with the weights' gradients (6.1 TB/s).
 //
 // Vector kernels (rows on 16 bytes, dim and rotary multiples of 16): a lane holds 16
 // elements of a row, and both elements of each of their pairs -- columns 8 t .. and
