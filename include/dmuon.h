@@ -552,8 +552,9 @@ int dmuon_qk_norm_rotary_backward(const dmuon_heads_t* dq_out, const dmuon_heads
  * lse = -inf, gradients 0, whatever values they hold; no sequence reads another's.
  * Within a sequence a NaN or an infinity may reach the outputs of all its tokens.
  * No logits are stored.  bf16 on the tensor cores: exp(s - lse) and the gradient ds are
- * rounded to bf16 once, as operands of the next product; rows off 16-byte boundaries, and
- * fp32, run as fp32 FMAs.  Equal calls give equal bits; which kernels run goes by the
+ * rounded to bf16 once, as operands of the next product (dim no multiple of 8: from padded
+ * copies of q, k, v and d_o in the workspace); fp32, and bf16 rows that begin off 16-byte
+ * boundaries though dim is a multiple of 8, run as fp32 FMAs, much slower.  Equal calls give equal bits; which kernels run goes by the
  * type, alignment and sizes, the number of tokens and sequences among them, so that a
  * sequence in another batch may differ in its roundings.  tokens in [0, 2^24], sequences in
  * [1, 2^20], heads in [1, 1024], (tokens / 32 + sequences) * (heads + kv_heads) below
@@ -570,7 +571,7 @@ int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, cons
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i exp(s_ij - lse_i) d_o_i
  * dk and dv are summed over the query heads that share the key head, in a fixed order.
  * (In bf16 delta is taken from o as it was rounded; for sequences of up to 128 tokens in
- * batches of short ones, and off 16-byte boundaries, it is the sum of p d_o v instead, and o
+ * batches of short ones, and in FMAs, it is the sum of p d_o v instead, and o
  * is not read.)
  * dq, dk, dv: contiguous. */
 int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_heads_t* q, const dmuon_heads_t* k,

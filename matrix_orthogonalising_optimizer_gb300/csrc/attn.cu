@@ -78,11 +78,17 @@ bool tma_rows(const AttnHeads& h) {
     return reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.token % 8 == 0 && h.head % 8 == 0;
 }
 
-// The tensor-core kernels take what TMA reads and what 16-byte stores write.
+// The tensor-core kernels take what TMA reads.
 bool tensor_cores(const AttnArgs& a, int32_t dtype, bool backward) {
     return dtype == DMUON_BF16 && a.dim % 8 == 0 && tma_rows(a.q) && tma_rows(a.k) && tma_rows(a.v) &&
            (!backward || tma_rows(a.d_o));
 }
+
+// bf16 rows whose length is no multiple of 16 bytes are copied to rows padded with zeros for
+// the tensor cores.  Measured, FFMA kernels -> copies, forward | backward: 8192 tokens, 8 heads of
+// 50: 2526 -> 86 us | 9007 -> 277; 512 tokens, 8 heads of 50: 59 -> 18 | 144 -> 29; 100
+// tokens, 12 heads of 50: 18 -> 16 | 58 -> 23; 37 tokens: 12 -> 16 | 40 -> 23.
+bool packs(int64_t dim, int32_t dtype) { return dtype == DMUON_BF16 && dim % 8 != 0; }
 
 int encode(CUtensorMap* map, const AttnHeads& h, int64_t tokens, int heads, int dim) {
     const auto enc = tensor_map_encoder();
@@ -104,6 +110,20 @@ int set_maps(AttnMaps& m, const AttnArgs& a) {
     OPS_TRY(encode(&m.v, a.v, a.tokens, a.kv_heads, a.dim));
     if (a.d_o.p) OPS_TRY(encode(&m.d_o, a.d_o, a.tokens, a.heads, a.dim));
     return DMUON_OK;
+}
+
+// The same of padded copies, which a launch makes in the workspace.
+int set_packed_maps(AttnMaps& m, const AttnArgs& a, __nv_bfloat16* space, cudaStream_t s, const char* where) {
+    AttnArgs b = a;
+    b.dim = static_cast<int32_t>(up(a.dim, 8));
+    for (AttnHeads* h : {&b.q, &b.k, &b.v, &b.d_o}) {
+        if (!h->p) continue;
+        const int64_t heads = h == &b.q || h == &b.d_o ? a.heads : a.kv_heads;
+        *h = AttnHeads{space, heads * b.dim, b.dim};
+        space += a.tokens * heads * b.dim;
+    }
+    OPS_CUDA(attn_pack(a, b, s));
+    return set_maps(m, b);
 }
 
 // Blocks that share a key tile's queries.  The longest of them must not outlast the rest
@@ -130,10 +150,12 @@ int parts_of(int64_t sequences, int64_t tokens, int64_t heads, int64_t kv_heads,
 struct Layout {
     float* delta = nullptr;
     float* partial = nullptr;
+    __nv_bfloat16* packed = nullptr;  // copies of q, k, v and d_o, where they are made
     int parts = 1;
     size_t bytes = 0;
     // the workspace serves either kind of kernels, causal or not
-    Layout(char* base, int64_t sequences, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim, bool backward) {
+    Layout(char* base, int64_t sequences, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim, int32_t dtype,
+           bool backward) {
         Arena a{base};
         if (backward) {
             delta = a.take<float>(tokens * heads);
@@ -141,6 +163,8 @@ struct Layout {
                 parts = std::max(parts, parts_of(sequences, tokens, heads, kv_heads, (k & 1) != 0, (k & 2) != 0));
             if (parts > 1) partial = a.take<float>(2 * parts * tokens * kv_heads * dim);
         }
+        if (packs(dim, dtype))
+            packed = a.take<__nv_bfloat16>(tokens * ((backward ? 2 : 1) * heads + 2 * kv_heads) * up(dim, 8));
         bytes = a.off;
     }
 };
@@ -155,7 +179,7 @@ extern "C" size_t dmuon_attention_workspace_bytes(int64_t sequences, int64_t tok
     if (!sizes_ok(tokens, sequences, heads, kv_heads, dim) ||
         check_dtype(dtype, "dmuon_attention_workspace_bytes") != DMUON_OK)
         return 0;
-    return tokens == 0 ? 0 : Layout(nullptr, sequences, tokens, heads, kv_heads, dim, backward != 0).bytes;
+    return tokens == 0 ? 0 : Layout(nullptr, sequences, tokens, heads, kv_heads, dim, dtype, backward != 0).bytes;
 }
 
 extern "C" int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, const dmuon_heads_t* v,
@@ -168,15 +192,16 @@ extern "C" int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads
     if (tokens == 0) return DMUON_OK;
     OPS_TRY(check_ptr(o, "o", where));
     OPS_TRY(check_ptr(lse, "lse", where));
-    const Layout L(static_cast<char*>(workspace), sequences, tokens, heads, kv_heads, dim, false);
+    const Layout L(static_cast<char*>(workspace), sequences, tokens, heads, kv_heads, dim, dtype, false);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
     a.out = o;
     a.lse = lse;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (tensor_cores(a, dtype, false)) {
+    const bool pack = packs(dim, dtype);
+    if (pack || tensor_cores(a, dtype, false)) {
         AttnMaps m = {};
-        OPS_TRY(set_maps(m, a));
+        OPS_TRY(pack ? set_packed_maps(m, a, L.packed, s, where) : set_maps(m, a));
         OPS_CUDA(attn_tc_forward(a, m, s));
     } else {
         OPS_CUDA(attn_simt_forward(a, dtype == DMUON_FP32, s));
@@ -201,7 +226,7 @@ extern "C" int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_he
     OPS_TRY(check_ptr(dq, "dq", where));
     OPS_TRY(check_ptr(dk, "dk", where));
     OPS_TRY(check_ptr(dv, "dv", where));
-    const Layout L(static_cast<char*>(workspace), sequences, tokens, heads, kv_heads, dim, true);
+    const Layout L(static_cast<char*>(workspace), sequences, tokens, heads, kv_heads, dim, dtype, true);
     OPS_TRY(check_workspace(workspace, workspace_bytes, L.bytes, where));
     OPS_TRY(check_device(where));
     a.o = o;
@@ -211,14 +236,14 @@ extern "C" int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_he
     a.dk = dk;
     a.dv = dv;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool tc = tensor_cores(a, dtype, true);
+    const bool pack = packs(dim, dtype), tc = pack || tensor_cores(a, dtype, true);
     a.parts = parts_of(sequences, tokens, heads, kv_heads, a.causal != 0, tc);
     a.partial = L.partial;
     // (bf16 rows of the FFMA kernels and sequences of one tile: made there)
     if (tc ? attn_tc_needs_delta(a) : f32) OPS_CUDA(attn_delta(a, f32, s));
     if (tc) {
         AttnMaps m = {};
-        OPS_TRY(set_maps(m, a));
+        OPS_TRY(pack ? set_packed_maps(m, a, L.packed, s, where) : set_maps(m, a));
         OPS_CUDA(attn_tc_backward(a, m, s));
     } else {
         OPS_CUDA(attn_simt_backward(a, f32, s));

@@ -121,7 +121,8 @@ __device__ __forceinline__ void attn_clear(const AttnArgs& a, T* x, float* lse, 
             lse[h * a.tokens + (i < first ? i : i - first + last)] = __int_as_float(0xff800000);
 }
 
-// Tensor-core kernels: bf16, rows of 16-byte stride, dim a multiple of 8.
+// Tensor-core kernels: bf16, rows of 16-byte stride in the maps (the outputs' rows may have
+// any length).
 struct AttnMaps {
     CUtensorMap q, k, v, d_o;  // dim x heads x tokens, boxes of 64 x 1 x 128
 };
@@ -145,6 +146,8 @@ cudaError_t attn_simt_forward(const AttnArgs& a, bool f32, cudaStream_t s);
 cudaError_t attn_simt_backward(const AttnArgs& a, bool f32, cudaStream_t s);
 // dk and dv from their partial sums, in the order of the parts
 cudaError_t attn_join(const AttnArgs& a, bool f32, cudaStream_t s);
+// the rows of a.q, a.k, a.v, a.d_o (bf16) to those of b, contiguous, zeros behind a.dim
+cudaError_t attn_pack(const AttnArgs& a, const AttnArgs& b, cudaStream_t s);
 // delta, for both backward passes
 cudaError_t attn_delta(const AttnArgs& a, bool f32, cudaStream_t s);
 

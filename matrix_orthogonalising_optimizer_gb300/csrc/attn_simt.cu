@@ -1,5 +1,5 @@
 // Attention in fp32 FFMA arithmetic, forward and backward: fp32 tensors, and bf16
-// ones whose rows the tensor-core kernels cannot read (rows off 16 bytes).
+// ones whose rows begin off 16-byte boundaries although their length is a multiple of 16 bytes.
 //
 //   s_ij = scale q_i k_j over the keys j that i sees,  lse_i = log sum_j exp s_ij
 //   p = exp(s - lse),  o_i = sum_j p_ij v_j
@@ -586,6 +586,27 @@ __global__ void __launch_bounds__(256) delta_vector_kernel(const __grid_constant
     }
 }
 
+// Rows of bf16 into padded ones, eight elements a thread; blockIdx.y: q, k, v, do.
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnArgs b) {
+    const int which = blockIdx.y;
+    const AttnHeads& in = which == 0 ? a.q : which == 1 ? a.k : which == 2 ? a.v : a.d_o;
+    const AttnHeads& out = which == 0 ? b.q : which == 1 ? b.k : which == 2 ? b.v : b.d_o;
+    const uint32_t heads = which % 3 == 0 ? a.heads : a.kv_heads, pieces = static_cast<uint32_t>(b.dim) / 8;
+    const int64_t rows = a.tokens * heads, count = rows * pieces;
+    const bool small = count < (int64_t(1) << 32);  // divided in 32 bits
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
+        const int64_t row = small ? static_cast<uint32_t>(i) / pieces : i / pieces;
+        const int64_t token = small ? static_cast<uint32_t>(row) / heads : row / heads;
+        const int c = static_cast<int>(i - row * pieces) * 8;
+        const uint16_t* p = static_cast<const uint16_t*>(in.p) + token * in.token + (row - token * heads) * in.head + c;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = (c + 2 * k < a.dim ? p[2 * k] : 0u) | (c + 2 * k + 1 < a.dim ? p[2 * k + 1] : 0u) << 16;
+        static_cast<uint4*>(const_cast<void*>(out.p))[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 template <typename E, int G>
 void launch_delta_vector(const AttnArgs& a, cudaStream_t s) {
     constexpr int tokens = 32 / G * 4;  // of a warp
@@ -713,6 +734,13 @@ cudaError_t attn_join(const AttnArgs& a, bool f32, cudaStream_t s) {
     if (each == 4)
         return launch_dependent(f32 ? join_kernel<float, 4> : join_kernel<__nv_bfloat16, 4>, grid, 256, s, a);
     return launch_dependent(f32 ? join_kernel<float, 1> : join_kernel<__nv_bfloat16, 1>, grid, 256, s, a);
+}
+
+cudaError_t attn_pack(const AttnArgs& a, const AttnArgs& b, cudaStream_t s) {
+    const int64_t most = a.tokens * a.heads * (b.dim / 8);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((most + 255) / 256, 2432)), a.d_o.p ? 4 : 3);
+    pack_kernel<<<grid, 256, 0, s>>>(a, b);
+    return cudaGetLastError();
 }
 
 cudaError_t attn_delta(const AttnArgs& a, bool f32, cudaStream_t s) {

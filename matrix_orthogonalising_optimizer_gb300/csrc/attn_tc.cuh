@@ -139,8 +139,8 @@ __device__ __forceinline__ void tmem_free(uint32_t base) {
 }
 
 // A warp's 32 rows of an accumulator (64 kBoxes columns at TMEM address t, this lane's
-// row) times f, as bf16, to `rows` rows of `dim` elements (a multiple of 8), `ld` apart.
-// They pass through the warp's 4 KB slices of a finished tile's boxes in shared memory,
+// row) times f, as bf16, to `rows` rows of `dim` elements, `ld` apart (one by one where dim is
+// no multiple of 8).  They pass through the warp's 4 KB slices of a finished tile's boxes in shared memory,
 // so that an instruction stores whole 128-byte pieces: row by row from the lanes it
 // touches 32 lines, and a tile took 1 us.
 template <int kBoxes>
@@ -164,6 +164,15 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t t, float f, 
         }
         __syncwarp();
         const int c = 64 * b + 8 * chunk;
+        if (dim % 8 != 0) {
+#pragma unroll 1
+            for (int r = 0; r < min(rows, 32); ++r)
+                for (int x = lane; x < min(64, dim - 64 * b); x += 32)
+                    out[r * ld + 64 * b + x] =
+                        reinterpret_cast<const __nv_bfloat16*>(stage + r * 128)[((x / 8) ^ (r % 8)) * 8 + x % 8];
+            __syncwarp();
+            continue;
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int r = 4 * k + lane / 8;
@@ -189,6 +198,15 @@ __device__ __forceinline__ void store_rows_f32(uint8_t* stage, uint32_t t, float
             mine[k ^ chunk] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
         __syncwarp();
         const int c = 32 * b + 4 * chunk;
+        if (dim % 8 != 0) {
+#pragma unroll 1
+            for (int r = 0; r < min(rows, 32); ++r)
+                if (32 * b + lane < dim)
+                    out[r * ld + 32 * b + lane] =
+                        reinterpret_cast<const float*>(stage + r * 128)[((lane / 4) ^ (r % 8)) * 4 + lane % 4];
+            __syncwarp();
+            continue;
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int r = 4 * k + lane / 8;

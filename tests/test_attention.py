@@ -110,6 +110,9 @@ def test_attention_refusals(lib):
 
     need = lib.dmuon_attention_workspace_bytes(2, 8, 8, 2, 64, _lib.BF16, 1)
     assert need >= 8 * 8 * 4
+    # padded copies of rows that are no multiple of 16 bytes
+    assert lib.dmuon_attention_workspace_bytes(1, 8, 8, 2, 33, _lib.BF16, 0) >= 8 * (8 + 2 + 2) * 40 * 2
+    assert lib.dmuon_attention_workspace_bytes(1, 8, 8, 2, 33, _lib.FP32, 0) == 0
     assert lib.dmuon_attention_workspace_bytes(2, 8, 8, 3, 64, _lib.BF16, 1) == 0
 
     def bwd(g=view(token=512), o=P16, lse=P16, dk=P16, ws=P16, n=need):
@@ -357,6 +360,23 @@ def test_attention(case, dtype, causal, fused):
     offsets, n, h, kv, d = case
     q, k, v, do, out = inputs(offsets, n, h, kv, d, dtype, fused, n + d)
     check(q, k, v, do, offsets, causal, out)
+    assert pkg.ops_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("offsets,n,h,kv,d", [([0, 260, 700], 710, 4, 1, 64), ([0, 90, 130], 130, 2, 2, 128),
+                                              ([0, 700], 700, 16, 2, 100), ([0, 3, 515], 520, 8, 2, 127),
+                                              ([0, 400], 400, 2, 2, 65), ([0, 100, 200, 300], 310, 6, 3, 12)])
+def test_attention_rows_off_16_bytes(offsets, n, h, kv, d, causal):
+    # bf16 rows that begin at odd elements: of a length that is a multiple of 16 bytes, and of others
+    q, k, v, do, out = inputs(offsets, n, h, kv, d, "bf16", False, n)
+    x = []
+    for y in (q, k, v, do):
+        wide = torch.full((n, y.shape[1], d + 5), float("nan"), dtype=y.dtype, device="cuda")
+        wide[..., 3:3 + d] = y
+        x.append(wide[..., 3:3 + d])
+    check(*x, offsets, causal, out)
     assert pkg.ops_status() == 0
 
 
