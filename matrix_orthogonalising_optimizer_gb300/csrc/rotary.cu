@@ -36,10 +36,10 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxDim = 256;
 constexpr int kWarps = 8;
-constexpr int kPer = kMaxDim / 32;  // elements of a lane
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int kMaxHeads = 1024;
-constexpr int kMaxBlocks = 304;     // two per SM; backward: rows of partial sums
+constexpr int kVectorBlocks = 304;  // two per SM; backward: rows of partial sums
+constexpr int kRowBlocks = 608;     // four per SM, of the kernel for any rows (a row in flight per warp)
 
 struct Rows {
     const void* x;
@@ -80,89 +80,89 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Turns the row in `s` (shared memory) and returns element e; `sign` -1: back.
-// cs: the position's cos and sin, NULL: the position is outside the table.
-__device__ __forceinline__ float turned(const RotArgs& a, const float* s, const float* cs, int e, float sign) {
-    if (e >= a.rotary || !a.table) return s[e];
-    const int half = a.rotary / 2;
-    const int pair = a.interleaved ? e / 2 : e < half ? e : e - half;
-    const bool second = a.interleaved ? (e & 1) != 0 : e >= half;
-    const int other = a.interleaved ? e ^ 1 : second ? e - half : e + half;
-    const float c = cs ? cs[pair] : __int_as_float(0x7fffffff), n = cs ? cs[half + pair] : c;
-    return fmaf(s[e], c, (second ? sign : -sign) * s[other] * n);
-}
-
-template <typename E, bool kBack>
-__global__ void __launch_bounds__(32 * kWarps) rows_kernel(const __grid_constant__ RotArgs a) {
-    __shared__ float rows[kWarps][kMaxDim];
+// kPer: elements of a lane, 32 kPer >= dim.
+template <typename E, bool kBack, int kPer>
+__global__ void __launch_bounds__(32 * kWarps, kPer <= 4 ? 4 : 2) rows_kernel(const __grid_constant__ RotArgs a) {
+    __shared__ float rows[kWarps][32 * kPer];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     float* s = rows[warp];
     const Rows& R = a.r[blockIdx.x < static_cast<unsigned>(a.r[1].first) ? 0 : 1];
-    float dw[kPer];
+    // of this lane's elements: the place of the other one of the pair, of the pair's cos in a
+    // row of the table (negative: not turned), the sign of its sine, the weight
+    const int half = a.rotary / 2;
+    int other[kPer], at[kPer];
+    float sign[kPer], w[kPer], dw[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) dw[i] = 0.0f;
+    for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 32 * i;
+        const bool second = a.interleaved ? (e & 1) != 0 : e >= half;
+        other[i] = a.interleaved ? e ^ 1 : second ? e - half : e + half;
+        at[i] = e >= a.rotary ? -1 : a.interleaved ? e / 2 : second ? e - half : e;
+        sign[i] = second != kBack ? 1.0f : -1.0f;
+        w[i] = R.w && e < a.dim ? to_f<E>(static_cast<const E*>(R.w)[e]) : 1.0f;
+        dw[i] = 0.0f;
+    }
+    const float inv = 1.0f / static_cast<float>(a.dim);
     const int64_t n = a.tokens * R.heads;
     for (int64_t row = static_cast<int64_t>(blockIdx.x - R.first) * kWarps + warp; row < n; row += R.blocks * kWarps) {
-        const int64_t token = row / R.heads, head = row - token * R.heads;
-        const float* cs = nullptr;
-        if (a.table) {
-            const int64_t p = a.positions[token];
-            if (p >= 0 && p < a.table_rows) cs = a.table + p * a.rotary;
-        }
+        // a 64-bit division takes longer than the row
+        const int64_t token = n >> 32 ? row / R.heads : static_cast<uint32_t>(row) / static_cast<uint32_t>(R.heads);
+        const int64_t head = row - token * R.heads;
         const E* px = static_cast<const E*>(R.x) + token * R.x_token + head * R.x_head;
-        const E* w = static_cast<const E*>(R.w);
+        const E* pd = static_cast<const E*>(R.dy) + token * R.dy_token + head * R.dy_head;
         E* out = static_cast<E*>(R.out) + row * a.dim;
-        float x[kPer], r = 1.0f;
-        if (!kBack || a.norm) {
+        const int64_t position = a.table ? a.positions[token] : 0;
+        float x[kPer], g[kPer], c[kPer], sn[kPer], r = 1.0f;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = lane + 32 * i < a.dim ? to_f<E>(px[lane + 32 * i]) : 0.0f;
+        for (int i = 0; i < kPer; ++i) {
+            const int e = lane + 32 * i;
+            x[i] = (!kBack || a.norm) && e < a.dim ? to_f<E>(px[e]) : 0.0f;
+            if constexpr (kBack) g[i] = e < a.dim ? to_f<E>(pd[e]) : 0.0f;
+        }
+        const bool inside = position >= 0 && position < a.table_rows;
+        const float* cs = a.table + (inside ? position : 0) * a.rotary;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            c[i] = 1.0f;
+            sn[i] = 0.0f;
+            if (at[i] >= 0) {
+                c[i] = inside ? cs[at[i]] : __int_as_float(0x7fffffff);
+                sn[i] = sign[i] * cs[half + at[i]];
+            }
         }
         if (a.norm) {
             float q = 0.0f;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) q = fmaf(x[i], x[i], q);
-            r = 1.0f / sqrtf(warp_sum(q) / static_cast<float>(a.dim) + a.eps);
+            r = rsqrtf(fmaf(warp_sum(q), inv, a.eps));
         }
-        if constexpr (!kBack) {
+        // y = n c + (the other one) sin
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.dim) s[e] = a.norm ? x[i] * r * (w ? to_f<E>(w[e]) : 1.0f) : x[i];
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.dim) out[e] = from_f<E>(turned(a, s, cs, e, 1.0f));
-            }
-        } else {
-            const E* pd = static_cast<const E*>(R.dy) + token * R.dy_token + head * R.dy_head;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.dim) s[e] = to_f<E>(pd[e]);
-            }
-            __syncwarp();
-            float g[kPer], dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int e = lane + 32 * i;
-                g[i] = e < a.dim ? turned(a, s, cs, e, -1.0f) : 0.0f;
-                if (a.norm && e < a.dim) {
-                    x[i] *= r;
-                    dw[i] = fmaf(g[i], x[i], dw[i]);
-                    if (w) g[i] *= to_f<E>(w[e]);
-                    dot = fmaf(g[i], x[i], dot);
-                }
-            }
-            if (a.norm) dot = warp_sum(dot) / static_cast<float>(a.dim);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.dim) out[e] = from_f<E>(a.norm ? r * (g[i] - x[i] * dot) : g[i]);
-            }
+        for (int i = 0; i < kPer; ++i) {
+            if constexpr (!kBack) g[i] = a.norm ? x[i] * (r * w[i]) : x[i];
+            s[lane + 32 * i] = g[i];
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (at[i] >= 0) g[i] = fmaf(g[i], c[i], s[other[i]] * sn[i]);
+        if (kBack && a.norm) {
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                x[i] *= r;
+                dw[i] = fmaf(g[i], x[i], dw[i]);
+                g[i] *= w[i];
+                dot = fmaf(g[i], x[i], dot);
+            }
+            dot = warp_sum(dot) * inv;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) g[i] = r * (g[i] - x[i] * dot);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (lane + 32 * i < a.dim) out[lane + 32 * i] = from_f<E>(g[i]);
         __syncwarp();
     }
     if constexpr (kBack) {
@@ -518,11 +518,11 @@ bool vectors(const RotArgs& a, int es, bool back) {
 
 // The blocks of the queries and, behind them, of the keys: in proportion to their
 // rows, no more than they can use, at least one each.
-int set_blocks(Rows (&r)[2], int64_t tokens) {
+int set_blocks(Rows (&r)[2], int64_t tokens, int most) {
     const int64_t all = r[0].heads + r[1].heads;
     for (int i = 0; i < 2; ++i)
         r[i].blocks = static_cast<int32_t>(std::max<int64_t>(
-            1, std::min<int64_t>(ceil_div(tokens * r[i].heads, kWarps), (kMaxBlocks - 1) * r[i].heads / all)));
+            1, std::min<int64_t>(ceil_div(tokens * r[i].heads, kWarps), (most - 1) * r[i].heads / all)));
     r[0].first = 0;
     r[1].first = r[0].blocks;
     return r[0].blocks + r[1].blocks;
@@ -563,15 +563,20 @@ cudaError_t run_vector(RotArgs a, int blocks, cudaStream_t s) {
 }
 
 template <typename E, bool kBack>
-cudaError_t run_rows(const RotArgs& a, int blocks, cudaStream_t s) {
-    if (vectors(a, sizeof(E), kBack)) {
+cudaError_t run_rows(RotArgs& a, cudaStream_t s) {
+    const bool vector = vectors(a, sizeof(E), kBack);
+    const int blocks = set_blocks(a.r, a.tokens, vector ? kVectorBlocks : kRowBlocks);
+    if (vector) {
         if (a.dim <= 16) return run_vector<E, 1, kBack>(a, blocks, s);
         if (a.dim <= 32) return run_vector<E, 2, kBack>(a, blocks, s);
         if (a.dim <= 64) return run_vector<E, 4, kBack>(a, blocks, s);
         if (a.dim <= 128) return run_vector<E, 8, kBack>(a, blocks, s);
         return run_vector<E, 16, kBack>(a, blocks, s);
     }
-    return launch_dependent(rows_kernel<E, kBack>, dim3(static_cast<unsigned>(blocks)), 32 * kWarps, s, a);
+    const auto kernel = a.dim <= 64    ? rows_kernel<E, kBack, 2>
+                        : a.dim <= 128 ? rows_kernel<E, kBack, 4>
+                                       : rows_kernel<E, kBack, 8>;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(blocks)), 32 * kWarps, s, a);
 }
 
 // Weight gradients from the partial sums [blocks][dim], always in the same order: 32
@@ -692,7 +697,7 @@ extern "C" size_t dmuon_qk_norm_rotary_workspace_bytes(int64_t tokens, int32_t h
     if (!sizes_ok(tokens, heads, kv_heads, dim) ||
         check_dtype(dtype, "dmuon_qk_norm_rotary_workspace_bytes") != DMUON_OK)
         return 0;
-    return static_cast<size_t>(kMaxBlocks) * dim * sizeof(float);
+    return static_cast<size_t>(kRowBlocks) * dim * sizeof(float);
 }
 
 extern "C" int dmuon_qk_norm_rotary_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, const int64_t* positions,
@@ -720,9 +725,8 @@ extern "C" int dmuon_qk_norm_rotary_forward(const dmuon_heads_t* q, const dmuon_
     a.r[0].out = q_out;
     a.r[1].out = k_out;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int blocks = set_blocks(a.r, tokens);
     const bool f32 = dtype == DMUON_FP32;
-    OPS_CUDA((f32 ? run_rows<float, false>(a, blocks, s) : run_rows<__nv_bfloat16, false>(a, blocks, s)));
+    OPS_CUDA((f32 ? run_rows<float, false>(a, s) : run_rows<__nv_bfloat16, false>(a, s)));
     return DMUON_OK;
 }
 
@@ -771,9 +775,8 @@ extern "C" int dmuon_qk_norm_rotary_backward(const dmuon_heads_t* dq_out, const 
     OPS_TRY(check_device(where));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f32 = dtype == DMUON_FP32;
-    const int blocks = tokens > 0 ? set_blocks(a.r, tokens) : 0;
     a.partial = sums ? static_cast<float*>(workspace) : nullptr;
-    if (blocks > 0) OPS_CUDA((f32 ? run_rows<float, true>(a, blocks, s) : run_rows<__nv_bfloat16, true>(a, blocks, s)));
+    if (tokens > 0) OPS_CUDA((f32 ? run_rows<float, true>(a, s) : run_rows<__nv_bfloat16, true>(a, s)));
     if (sums) {
         const dim3 grid(static_cast<unsigned>(ceil_div(dim, 32)), 2);
         OPS_CUDA(launch_dependent(f32 ? reduce_kernel<float> : reduce_kernel<__nv_bfloat16>, grid, 1024, s, a.partial,
