@@ -21,7 +21,10 @@
 // second kernel the blocks' sums.
 //
 // Other rows: one warp per row, which goes through shared memory once so that any
-// pairing can be formed.
+// pairing can be formed.  A warp's rows follow one another, so that a token's cos and sin
+// serve its heads and the next row is fetched ahead.  Measured, bf16, 16384 tokens, 32/8 heads of
+// 120: forward 133 us (2.4 TB/s), backward 197 us; 764 and 830 us with rows dealt out one by
+// one.  Bound: instructions, element by element.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -104,33 +107,54 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 4 ? 4 : 2) rows_kernel(co
         dw[i] = 0.0f;
     }
     const float inv = 1.0f / static_cast<float>(a.dim);
-    const int64_t n = a.tokens * R.heads;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x - R.first) * kWarps + warp; row < n; row += R.blocks * kWarps) {
-        // a 64-bit division takes longer than the row
-        const int64_t token = n >> 32 ? row / R.heads : static_cast<uint32_t>(row) / static_cast<uint32_t>(R.heads);
-        const int64_t head = row - token * R.heads;
+    // a warp's rows follow one another: a token's cos and sin serve all its heads, and the next
+    // row is on its way while one is worked on
+    const int64_t n = a.tokens * R.heads, unit = static_cast<int64_t>(blockIdx.x - R.first) * kWarps + warp;
+    const int64_t units = static_cast<int64_t>(R.blocks) * kWarps, end = n * (unit + 1) / units;
+    int64_t row = n * unit / units, token = row / R.heads;
+    int head = static_cast<int>(row - token * R.heads);
+    E xn[kPer], gn[kPer];
+    const auto fetch = [&](int64_t token, int64_t head) {
         const E* px = static_cast<const E*>(R.x) + token * R.x_token + head * R.x_head;
         const E* pd = static_cast<const E*>(R.dy) + token * R.dy_token + head * R.dy_head;
-        E* out = static_cast<E*>(R.out) + row * a.dim;
-        const int64_t position = a.table ? a.positions[token] : 0;
-        float x[kPer], g[kPer], c[kPer], sn[kPer], r = 1.0f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = lane + 32 * i;
-            x[i] = (!kBack || a.norm) && e < a.dim ? to_f<E>(px[e]) : 0.0f;
-            if constexpr (kBack) g[i] = e < a.dim ? to_f<E>(pd[e]) : 0.0f;
+            xn[i] = (!kBack || a.norm) && e < a.dim ? px[e] : E(0.0f);
+            if constexpr (kBack) gn[i] = e < a.dim ? pd[e] : E(0.0f);
         }
-        const bool inside = position >= 0 && position < a.table_rows;
-        const float* cs = a.table + (inside ? position : 0) * a.rotary;
+    };
+    if (row < end) fetch(token, head);
+    bool fresh = true;
+    float c[kPer], sn[kPer];
+    for (; row < end; ++row) {
+        E* out = static_cast<E*>(R.out) + row * a.dim;
+        float x[kPer], g[kPer], r = 1.0f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            c[i] = 1.0f;
-            sn[i] = 0.0f;
-            if (at[i] >= 0) {
-                c[i] = inside ? cs[at[i]] : __int_as_float(0x7fffffff);
-                sn[i] = sign[i] * cs[half + at[i]];
+            x[i] = to_f<E>(xn[i]);
+            if constexpr (kBack) g[i] = to_f<E>(gn[i]);
+        }
+        if (fresh) {
+            const int64_t position = a.table ? a.positions[token] : 0;
+            const bool inside = position >= 0 && position < a.table_rows;
+            const float* cs = a.table + (inside ? position : 0) * a.rotary;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                c[i] = 1.0f;
+                sn[i] = 0.0f;
+                if (at[i] >= 0) {
+                    c[i] = inside ? cs[at[i]] : __int_as_float(0x7fffffff);
+                    sn[i] = sign[i] * cs[half + at[i]];
+                }
             }
         }
+        fresh = ++head == R.heads;
+        if (fresh) {
+            head = 0;
+            ++token;
+        }
+        if (row + 1 < end) fetch(token, head);
         if (a.norm) {
             float q = 0.0f;
 #pragma unroll
