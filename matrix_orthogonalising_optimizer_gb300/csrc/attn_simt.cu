@@ -15,7 +15,7 @@
 //
 // Bound: FFMA (about half of its rate) and shared-memory loads (4 x 4 products take 8 loads of
 // 2 cycles each per 32 FMA instructions); a second block per SM adds nothing.  Measured in
-// fp32: 2048 tokens, 16 heads of 64, causal: forward 231 us (19 TFLOP/s), backward 705 us (30);
+// fp32: 2048 tokens, 16 heads of 64, causal: forward 231 us (19 TFLOP/s), backward 720 us (30);
 // 777 tokens, 6 / 2 heads of 80: 36 and 70 us.
 #include <algorithm>
 #include <cmath>
@@ -213,6 +213,12 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// Whether row i of a sequence sees one key only: p is 1 then and ds exactly 0, not what the
+// roundings of dp and delta leave of it.
+__device__ __forceinline__ bool single(const AttnTile& t, const AttnArgs& a, int i) {
+    return a.causal ? i == 0 : t.len == 1;
+}
+
 struct Block {
     AttnTile t;
     int head, row0, rows, tiles;
@@ -348,7 +354,7 @@ __device__ __forceinline__ void dq_block(const AttnArgs& a, unsigned index, floa
         const int i = ty + 16 * r;
         const bool in = i < b.rows;
         lse[r] = in ? a.lse[b.head * a.tokens + row + i] * kLog2e : 0.0f;
-        delta[r] = in && sizeof(E) == 4 ? a.delta[b.head * a.tokens + row + i] : 0.0f;
+        delta[r] = in && sizeof(E) == 4 && !single(b.t, a, b.row0 + i) ? a.delta[b.head * a.tokens + row + i] : 0.0f;
 #pragma unroll
         for (int k = 0; k < DP / 32; ++k) acc[r][k] = tc::both(0.0f);
     }
@@ -374,7 +380,7 @@ __device__ __forceinline__ void dq_block(const AttnArgs& a, unsigned index, floa
             for (int c = 0; c < 4; ++c) {
                 const bool in = tx + 16 * c < seen;
                 p[r][c] = in ? ex2(fmaf(p[r][c], a.scale_log2, -lse[r])) : 0.0f;
-                g[r][c] = in ? g[r][c] : 0.0f;
+                g[r][c] = in && !single(b.t, a, i) ? g[r][c] : 0.0f;
             }
         }
     };
@@ -470,7 +476,7 @@ __device__ __forceinline__ void dkv_block(const AttnArgs& a, unsigned index, flo
                 const bool seen = in && (!a.causal || b.row0 + j <= i0 + i);
                 const float p = seen ? ex2(fmaf(s[r][c], a.scale_log2, -lse)) : 0.0f;
                 P[j * LP + i] = p;
-                G[j * LP + i] = seen ? p * (g[r][c] - delta) : 0.0f;
+                G[j * LP + i] = seen && !single(b.t, a, i0 + i) ? p * (g[r][c] - delta) : 0.0f;
             }
         }
         __syncwarp();

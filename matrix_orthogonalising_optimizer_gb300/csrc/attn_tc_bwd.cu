@@ -580,6 +580,8 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
         const uint32_t lanes = (static_cast<uint32_t>(quarter * 32) << 16) + tmem;
         const bool in = r < t.len;
         const int seen = (!in ? 0 : a.causal ? r + 1 : t.len) - 64 * half;  // columns of this half that row r sees
+        // a row that sees one key only has ds = 0 exactly
+        const int varied = (a.causal ? r : t.len - 1) == 0 ? 0 : seen;
         const float2 c2 = both(a.scale_log2);
         bool ok = wait_warp(S, &S.own_full, 0);
         if (ok && t.len < kRows) clear_rows<DP>(S.own[0], t.len, thread, 256);  // K: the rows of ds k
@@ -599,8 +601,10 @@ __device__ __forceinline__ void short_side(const AttnArgs& a, Smem<DP>& S, const
             }
             if (t.len < kRows || a.causal) {
 #pragma unroll
-                for (int k = 0; k < 64; ++k)
-                    if (k >= seen) p[k] = g[k] = 0.0f;
+                for (int k = 0; k < 64; ++k) {
+                    if (k >= seen) p[k] = 0.0f;
+                    if (k >= varied) g[k] = 0.0f;
+                }
             }
             float2 sum2 = both(0.0f);
 #pragma unroll

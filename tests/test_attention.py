@@ -396,6 +396,18 @@ def test_attention_batch_of_equal_sequences(batch, n, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 33, 128])
+def test_attention_of_single_tokens(d, causal, dtype):
+    # one key: o is v, dv is do, and dq and dk are exactly 0
+    offsets = [0, 1, 1, 2, 3]
+    q, k, v, do, out = inputs(offsets, 3, 4, 4, d, dtype, False, d)
+    got = check(q, k, v, do, offsets, causal, out)
+    assert torch.equal(got["o"], v) and not got["dq"].any() and not got["dk"].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_large_logits_and_growing_maxima(d, dtype):
     # logits up to several hundred whose row maxima grow from tile to tile
