@@ -302,6 +302,8 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
             // columns of this half that see key r: [lo, hi)
             const bool masked = queries < kRows || (a.causal && row == row0);
             const int lo = (a.causal ? row0 + r - row : 0) - 64 * half, hi = queries - 64 * half;
+            // the same for ds: 0 exactly for a query that sees one key only (the sequence's first one)
+            const int lo_ds = row == 0 && (a.causal || t.len == 1) ? max(lo, 1 - 64 * half) : lo;
             ok = wait_warp(S, &S.stat_full[st], (i >> 1) & 1) && wait_warp(S, &S.s_full, i & 1);
             if (!ok) break;
             float p[64], g[C::kApart ? 64 : 32];
@@ -367,7 +369,7 @@ __device__ __forceinline__ void keys_side(const AttnArgs& a, Smem<DP>& S, const 
                 // not 0 times what the columns behind the sequence hold
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
-                    if (k < lo || k >= hi) p[k] = 0.0f;
+                    if (k < lo_ds || k >= hi) p[k] = 0.0f;
             }
             store_cols64(td, p);
             arrive_warp(&S.ds_ready, lane);
@@ -479,7 +481,9 @@ __device__ __forceinline__ void queries_side(const AttnArgs& a, Smem<DP>& S, con
             tmem_ld64(lanes + kQg + 64 * half, g);
             release_warp(&S.taken, lane);
             const bool masked = keys < kRows || (a.causal && i + 1 == steps);
-            const int seen = (a.causal ? min(row + 1 - i * kRows, keys) : keys) - 64 * half;
+            // ds = 0 exactly for a row that sees one key only
+            const int seen = ((a.causal ? row : t.len - 1) == 0 ? 0 : a.causal ? min(row + 1 - i * kRows, keys) : keys) -
+                             64 * half;
 #pragma unroll
             for (int k = 0; k < 64; k += 2) {
                 float2 x = fma2(make_float2(p[k], p[k + 1]), c2, nl);

@@ -122,6 +122,34 @@ def test_each_sequence_off_16_bytes(offsets, n, h, kv, d, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128, 50])
+def test_rows_of_one_key_have_no_logit_gradient(d, dtype):
+    # whichever kernel a batch takes: single tokens, and every causal sequence's first row
+    for offsets in ([0, 1, 2, 90], [0, 1, 1601, 1602], [0, 2000], [3, 1203, 1204, 2600]):
+        n, h, kv = offsets[-1] + 5, 4, 2
+        q, k, v, do, _ = inputs(offsets, n, h, kv, d, dtype, False, n)
+        for causal in (True, False):
+            _, dq, dk, _ = kernels(q, k, v, do, offsets, causal)
+            for a, b in zip(offsets, offsets[1:]):
+                if b - a == 1:
+                    assert not dq[a].any() and not dk[a].any(), (offsets, a, causal)
+                elif causal:
+                    assert not dq[a].any() and dq[b - 1].any(), (offsets, a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128, 50])
+def test_short_sequences_beside_a_long_one(d, dtype, causal):
+    # an average of more than 512 tokens: bf16 runs all sequences in the kernel of the long ones
+    offsets, n, h, kv = [0, 1, 3, 11, 4011, 4012, 4052], 4060, 4, 2
+    q, k, v, do, _ = inputs(offsets, n, h, kv, d, dtype, False, d)
+    compare(kernels(q, k, v, do, offsets, causal), q, k, v, do, offsets, causal, d ** -0.5)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("d", [64, 128, 50])
 def test_short_sequences_take_delta_unrounded(d, causal):
