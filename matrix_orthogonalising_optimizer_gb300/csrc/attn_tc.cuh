@@ -78,6 +78,17 @@ __device__ __forceinline__ void load_tile(uint32_t e, uint32_t dst, const CUtens
     for (int b = 0; b < DP / 64; ++b) tma_load_3d(e, dst + b * kBox, map, bar, 64 * b, head, token);
 }
 
+// Until an item's copies have landed -- those of `first`, outside the ring, and the last of
+// `issued` into `slots` -- by the warp that issued them, which is idle then: none is under way
+// when the CTA leaves, also after a wait of any warp that gave up (these are waited for once more,
+// with the same limit).
+__device__ __forceinline__ void await_copies(uint64_t* first, uint64_t* full, int issued, int slots, int32_t* bad) {
+    mbar_wait<false>(first, 0, bad);
+#pragma unroll 1
+    for (int i = max(issued - slots, 0); i < issued; ++i) mbar_wait<false>(&full[i % slots], (i / slots) & 1, bad);
+    __syncwarp();
+}
+
 // Rows [first, 128) of a tile, which belong to another sequence or to none, become
 // zero: their weight in a product over the rows is 0, but 0 times an infinity or NaN
 // is not.  By `threads` threads; visible to the tensor cores after a barrier.
@@ -106,6 +117,7 @@ __device__ __forceinline__ bool claim_block(uint4* claim, uint64_t* claimed, uin
     }
     __syncwarp();
     const bool there = __all_sync(kFullMask, mbar_wait<false>(claimed, asked & 1, bad));
+    if (!there) mbar_wait<false>(claimed, asked & 1, bad);  // once more: no answer after the CTA has left
     ++asked;
     uint32_t got = 0, index = 0;
     if (there)

@@ -123,8 +123,9 @@ __device__ __forceinline__ void release_warp(uint64_t* bar, int lane) {
 template <int DP, int kSlots, typename F>
 __device__ __forceinline__ void produce(Smem<DP>& S, uint32_t e, const uint8_t* slots, int count, F what) {
     Ring<kSlots> r;
-    for (int i = 0; i < count; ++i) {
-        if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[r.stage], r.phase ^ 1, &S.bad))) return;
+    int i = 0;
+    for (; i < count; ++i) {
+        if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[r.stage], r.phase ^ 1, &S.bad))) break;
         const CUtensorMap* map;
         int head, token;
         what(i, map, head, token);
@@ -132,6 +133,7 @@ __device__ __forceinline__ void produce(Smem<DP>& S, uint32_t e, const uint8_t* 
         load_tile<DP>(e, saddr(slots) + r.stage * kTile<DP>, map, saddr(&S.full[r.stage]), head, token);
         r.next();
     }
+    await_copies(&S.own_full, S.full, i, kSlots, &S.bad);
 }
 
 // 64 columns, packed, into TMEM columns t .. t + 31.

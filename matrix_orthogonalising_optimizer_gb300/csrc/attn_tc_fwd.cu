@@ -176,12 +176,9 @@ __device__ __forceinline__ void run_tile(const AttnArgs& a, Smem<DP, NT>& S, con
                     load_tile<DP>(e, saddr(S.q[i]), mq, saddr(&S.q_full), head, token0 + row0 + i * kRows);
             int stage = 0;
             uint32_t phase = 0;
-            bool ok = true;
-            for (int i = 0; i < 2 * steps && ok; ++i) {
-                if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[stage], phase ^ 1, &S.bad))) {
-                    ok = false;
-                    break;
-                }
+            int i = 0;
+            for (; i < 2 * steps; ++i) {
+                if (!__all_sync(kFullMask, mbar_wait<false>(&S.empty[stage], phase ^ 1, &S.bad))) break;
                 bool v = (i & 1) != 0;
                 int tile = i / 2;
                 if (NB == 3 && i > 0) {  // K0 K1 V0 K2 V1 .. V_last
@@ -196,6 +193,7 @@ __device__ __forceinline__ void run_tile(const AttnArgs& a, Smem<DP, NT>& S, con
                     phase ^= 1;
                 }
             }
+            await_copies(&S.q_full, S.full, i, NS, &S.bad);
         } else if (warp == 1) {
             // ------------------------------------------------ MMAs
             const uint32_t e = elect_one();
