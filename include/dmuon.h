@@ -554,12 +554,12 @@ int dmuon_qk_norm_rotary_backward(const dmuon_heads_t* dq_out, const dmuon_heads
  * No logits are stored.  bf16 on the tensor cores: exp(s - lse) and the gradient ds are
  * rounded to bf16 once, as operands of the next product (dim no multiple of 8: from padded
  * copies of q, k, v and d_o in the workspace); fp32, and bf16 rows that begin off 16-byte
- * boundaries though dim is a multiple of 8, run as fp32 FMAs, much slower.  Equal calls give equal bits; which kernels run goes by the
- * type, alignment and sizes, the number of tokens and sequences among them, so that a
- * sequence in another batch may differ in its roundings.  tokens in [0, 2^24], sequences in
- * [1, 2^20], heads in [1, 1024], (tokens / 32 + sequences) * (heads + kv_heads) below
- * 2^31 - 256, dim in [1, 128], scale finite and > 0 (usually 1 / sqrt(dim)).  Status codes
- * as for the gated block. */
+ * boundaries though dim is a multiple of 8, run as fp32 FMAs, much slower.  Equal calls give
+ * equal bits; which kernels run goes by the type, alignment and sizes, the number of tokens and
+ * sequences among them, so that a sequence in another batch may differ in its roundings.
+ * tokens in [0, 2^24], sequences in [1, 2^20], heads in [1, 1024],
+ * (tokens / 32 + sequences) * (heads + kv_heads) below 2^31 - 256, dim in [1, 128], scale finite
+ * and > 0 (usually 1 / sqrt(dim)).  Status codes as for the gated block. */
 size_t dmuon_attention_workspace_bytes(int64_t sequences, int64_t tokens, int32_t heads, int32_t kv_heads,
                                        int32_t dim, int32_t dtype, int32_t backward);
 int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, const dmuon_heads_t* v,
@@ -570,9 +570,10 @@ int dmuon_attention_forward(const dmuon_heads_t* q, const dmuon_heads_t* k, cons
  *   delta_i = d_o_i o_i,  ds_ij = exp(s_ij - lse_i) (d_o_i v_j - delta_i)
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i exp(s_ij - lse_i) d_o_i
  * dk and dv are summed over the query heads that share the key head, in a fixed order.
- * (In bf16 delta is taken from o as it was rounded; for sequences of up to 128 tokens in
- * batches of short ones, and in FMAs, it is the sum of p d_o v instead, and o
- * is not read.)
+ * (In bf16 delta is taken from o as it was rounded; in FMAs, and for sequences of up to 128
+ * tokens in batches whose average (tokens / sequences) is at most 512, it is the sum of p d_o v
+ * instead: o's values have no part in the result, though they may be read.)  A row that sees
+ * one key only adds nothing to dq and dk.
  * dq, dk, dv: contiguous. */
 int dmuon_attention_backward(const dmuon_heads_t* d_o, const dmuon_heads_t* q, const dmuon_heads_t* k,
                              const dmuon_heads_t* v, const void* o, const float* lse, const int64_t* offsets,

@@ -62,6 +62,9 @@ int common(AttnArgs& a, const dmuon_heads_t* q, const dmuon_heads_t* k, const dm
     a.group = heads / kv_heads;
     a.dim = dim;
     a.causal = causal != 0;
+    // Blocks that clear the rows of no sequence: one per SM where there are 128 rows for each.  Measured, 38 |
+    // 152 | 608 blocks, backward, 32/8 heads of 128: 1384 of 16384 tokens in sequences 158 | 119 | 111 us, half
+    // of 8192 326 | 318 | 313; without such rows they cost nothing that shows.
     a.fill = offsets ? static_cast<int32_t>(std::min<int64_t>(ceil_div(tokens, 128), 152)) : 0;
     a.scale = scale;
     a.scale_log2 = scale * kLog2e;
@@ -130,8 +133,8 @@ int set_packed_maps(AttnMaps& m, const AttnArgs& a, __nv_bfloat16* space, cudaSt
 // of the launch: about group * tiles steps, against the whole backward pass's steps over
 // all SMs (a query tile's step costs 0.8 of a key tile's).  With sequences of the average
 // length.  Measured, one part -> as chosen: 2048 tokens, 32 / 1 heads of 128: 640 -> 110 us;
-// 1024 tokens, 16 / 2 heads of 128: 96 -> 38 us; fp32, 777 tokens, 6 / 2 heads of 80: 367 ->
-// 136 us (with the kernels of then; 70 now).
+// 1024 tokens, 16 / 2 heads of 128: 96 -> 38 us; fp32, 777 tokens, 6 / 2 heads of 80: 238 ->
+// 72 us; 4096 tokens, 8 / 1 heads of 64: 3583 -> 1406 us.
 constexpr int kMaxParts = 16;
 
 int parts_of(int64_t sequences, int64_t tokens, int64_t heads, int64_t kv_heads, bool causal, bool tc) {
@@ -139,7 +142,8 @@ int parts_of(int64_t sequences, int64_t tokens, int64_t heads, int64_t kv_heads,
     const double length = static_cast<double>(tokens) / static_cast<double>(sequences);
     const double tiles = std::max(1.0, std::ceil(length / static_cast<double>(tile)));
     const double pairs = causal ? tiles * (tiles + 1.0) / 2.0 : tiles * tiles;
-    // the FFMA kernels' two sides are separate launches, two blocks per SM
+    // FFMA: the factor that does best over all sizes (0.5 | 1.0 | 2.0, fp32: 2048 tokens, 32 / 4 heads of 64
+    // 1414 | 1816 | 1815 us; 4096, 8 / 1 of 64 1406 | 1393 | 3584; 1024, 8 / 8 of 128 233 | 222 | 222)
     const double share = (tc ? 1.8 : 0.5) * static_cast<double>(heads * sequences) * pairs / sms;
     const double longest = static_cast<double>(heads / kv_heads) * tiles;
     // below 2.5 the partial sums cost more than the wait (2048 tokens, 8 heads of 128: 37 -> 60 us)

@@ -19,13 +19,17 @@
 // the key head follow one another.  (Heads of up to 64: as the queries.)
 // Queries: s, dp, ds, Q and dq; s and dp are taken into registers first, so that
 // s_{i+1} and dp_{i+1} run while ds_i is made, then dq_i.
-// Sequences of one tile: a CTA makes all three gradients (short_side).
+// Sequences of one tile, in batches of short ones: a CTA makes all three gradients (short_side).
 //
 // Bound: the tensor cores.  Per pair of 128-token tiles 7 * 512 cycles at dim = 128;
 // measured about 2300 a step of the keys (2048 of MMAs) and 1850 of the queries (1536), and 3
 // to 6 us a tile besides.  8192 tokens, 32/8 heads of 128, causal: 1.07 ms with delta,
 // 1.28 PFLOP/s of the five products, 1.80 of the seven; five documents packed into 8192
-// tokens 0.38 ms; 12 heads of 64 0.32 ms (element-wise work and hand-overs).
+// tokens 0.39 ms; 12 heads of 64 0.31 ms (element-wise work and hand-overs).
+//
+// delta = do . o is taken from o as it was rounded to bf16 (short_side: from p dp): errors of dq and
+// dk of 2.8e-3 of their norm, where the roundings of ds and of the results alone make 2.4e-3; the
+// exact delta would take two products more.  A row that sees one key only has ds = 0 exactly.
 //
 // Warp 0 loads and looks for the next item, warp 1 issues the MMAs, warp 2 fetches lse and
 // delta of the query tiles (side of the keys), warps 4 to 11 do the element-wise work, half of
@@ -863,8 +867,13 @@ cudaError_t launch(const AttnArgs& a, const AttnMaps& m, int64_t items, cudaStre
     return cudaLaunchKernelEx(&cfg, backward_kernel<DP, kWhole>, a, m.q, m.k, m.v, m.d_o);
 }
 
-// Sequences of one tile have their launch where the average one is no longer than
-// this; a few among longer ones are left to the other (their launch alone costs 3 us).
+// Sequences of one tile have a launch of their own where the average one is no longer than this.  It is
+// for delta's sake, not for time.  Measured, without -> with, by the average length (8192 tokens, 32/8
+// heads of 128 | 12 of 64): 102 tokens 223 -> 222 us | 92 -> 95; 256: 210 -> 226 | 84 -> 95; 512: 242
+// -> 247 | 91 -> 97; 683: 263 -> 267 | 96 -> 101; 1024: 347 -> 351 | 119 -> 124; 4096: 758 -> 762 | 231
+// -> 238; four texts in 4096 tokens 61 -> 66 us with heads of 64.  Among longer sequences a short one takes
+// delta from o like the others (two tokens: error of dq 4.6e-3 of its norm instead of 2.5e-3, more
+// where one key has nearly all the weight), as the first rows of every causal sequence do.
 constexpr int kShortAverage = 512;
 
 template <int DP>

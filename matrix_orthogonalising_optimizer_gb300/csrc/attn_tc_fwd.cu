@@ -23,8 +23,11 @@
 // Bound: the tensor cores, 4 * 128 * 128 * dim operations per pair of tiles -- at dim =
 // 128 1024 cycles, against 512 of exponentials (32 a cycle and SM) and about 670 of all the
 // softmax's pipes.  Measured: 16384 tokens, 32/8 heads of 128, causal: 1.22 ms, 1.80 PFLOP/s,
-// 92 % of cuBLAS's burst rate (1.37 ms = 1.61 in a loop, under the power cap).  Heads of 64: the
-// softmax (12 heads, 8192 tokens: 107 us, 0.97 PFLOP/s).  Short sequences: start and end of a
+// 92 % of cuBLAS's burst rate (1.33 ms = 1.65 in a loop, under the power cap).  Heads of 64: the
+// chain of waits of a tile (s, TMEM load, maximum, exponentials, store, arrival) with two warpgroups:
+// 12 heads, 8192 tokens: 104 us, 1.0 PFLOP/s, about 1250 cycles a pair of tiles where the MMAs and
+// the exponentials take 512 each and all of the softmax's pipes 670; tensor cores and exponentials are
+// 48 % busy, issue slots 46 %, and 13 % of the time SMs have run out of tiles.  Short sequences: start and end of a
 // tile, about 3 us (23 ragged ones of 356 tokens, 12 heads of 64: 32 us).
 #include <cstddef>
 
@@ -47,7 +50,8 @@ struct Cfg {
     static constexpr bool kHalves = kBuffers == 2;                   // p is handed over in two halves
     static constexpr int kStages = NT == 2 ? (DP == 128 ? 5 : 8) : (DP == 128 ? 2 : 4);
     static constexpr uint32_t kCols = NT == 2 ? 512 : 256;
-    static constexpr int kRegsLow = 56, kRegsSoft = NT == 2 ? 224 : 200;  // shares of 168 x 3 or 128 x 2
+    // shares of 168 x 3 or 128 x 2 (NT = 1: ptxas spills 40 bytes at DP = 64 and 48 at 128)
+    static constexpr int kRegsLow = 56, kRegsSoft = NT == 2 ? 224 : 200;
 };
 
 // What a CTA does next.
